@@ -317,6 +317,28 @@ __global__ void probe_kernel(const uint4* __restrict__ src, uint64_t nvec, uint6
 
 namespace kvo {
 
+kvo_status usable_status(kvo_ctx* ctx, uint32_t** status) {
+  if (!ctx) return KVO_EINVAL;
+  if (ctx->unusable) return KVO_ECUDA;
+  *status = ctx->status;
+  return KVO_OK;
+}
+
+int device_sms() {
+  static int known[64] = {};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  if (known[dev & 63]) return known[dev & 63];
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  return known[dev & 63] = sms;
+}
+
 cudaError_t launch_append(const void* src_dev, uint8_t* hist_dev_dst, uint64_t bytes,
                           uint32_t* counters, uint32_t new_len, cudaStream_t stream) {
   const uint64_t nvec = bytes / 16;

@@ -461,6 +461,14 @@ kvo_status kvo_pool_sync(kvo_pool* p, void* stream) {
   return KVO_OK;
 }
 
+kvo_status kvo_pool_rows(kvo_pool* pool, void** rows, int64_t* blocks, int32_t* block_rows) {
+  if (!pool || !rows || !blocks || !block_rows) return KVO_EINVAL;
+  *rows = pool->pool;
+  *blocks = pool->pool_blocks;
+  *block_rows = pool->block_tokens;
+  return KVO_OK;
+}
+
 kvo_status kvo_pool_get_stats(kvo_pool* p, kvo_pool_stats* out) {
   if (!p || !out) return KVO_EINVAL;
   reap(p, false);

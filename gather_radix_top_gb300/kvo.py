@@ -22,6 +22,11 @@ GATHER_LOADS, GATHER_STAGED, GATHER_AUTO = 0, 1, 2
 MISS_ZEROCOPY, MISS_BATCHED, MISS_AUTO = 0, 1, 2
 MAX_HOT_ROWS = 131072
 NOALLOC_MAX_PAIRS = 65536
+BF16, FP16, FP32, E4M3 = 0, 1, 2, 3
+LATENT_VALUES, ROPE_VALUES, KEY_VALUES = 512, 64, 128
+MAX_HEADS = 128
+MAX_SCORE_BLOCK = 128
+MAX_QUERIES = 65535
 
 KVO_OK, KVO_EINVAL, KVO_ENOMEM, KVO_ECUDA, KVO_ERANGE, KVO_EBUSY, KVO_ETIMEDOUT, KVO_ECAPACITY = (
     0, -1, -2, -3, -4, -5, -6, -7)
@@ -39,7 +44,8 @@ EXPORTED = [
     "kvo_pool_sync", "kvo_pool_block_table", "kvo_pool_get_stats", "kvo_pool_debug_fail_after",
     "kvo_pool_debug_free_queue", "kvo_copy_blocks_noalloc", "kvo_set_phase_timing", "kvo_layers_phase_times",
     "kvo_layers_counters", "kvo_probe_host_touch", "kvo_debug_history_host", "kvo_set_miss_fetch",
-    "kvo_touch_history",
+    "kvo_touch_history", "kvo_append_tokens", "kvo_index_scores", "kvo_attend", "kvo_attend_work_bytes",
+    "kvo_pool_rows",
 ]
 
 
@@ -61,6 +67,38 @@ class kvo_layer_task(ctypes.Structure):
     _fields_ = [("layer", ctypes.c_int32), ("reserved", ctypes.c_int32), ("new_rows", ctypes.c_void_p),
                 ("r", ctypes.c_int64), ("scores", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("idx", ctypes.c_void_p), ("out_rows", ctypes.c_void_p), ("out_bf16", ctypes.c_void_p)]
+
+
+class kvo_cache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("keys", ctypes.c_void_p), ("key_scales", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64), ("blocks", ctypes.c_int64),
+                ("block_rows", ctypes.c_int32), ("table_blocks", ctypes.c_int32), ("sequences", ctypes.c_int32),
+                ("key_type", ctypes.c_int32)]
+
+
+class kvo_tokens(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_void_p), ("rope", ctypes.c_void_p), ("key", ctypes.c_void_p),
+                ("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("out_bf16", ctypes.c_void_p), ("latent_ld", ctypes.c_int64), ("rope_ld", ctypes.c_int64),
+                ("key_ld", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class kvo_score_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("scores", ctypes.c_void_p), ("q_ld", ctypes.c_int64), ("q_head_ld", ctypes.c_int64),
+                ("weights_ld", ctypes.c_int64), ("ld", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("per_seq", ctypes.c_int32), ("heads", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kvo_attend_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("sel", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("work", ctypes.c_void_p),
+                ("work_bytes", ctypes.c_int64), ("q_ld", ctypes.c_int64), ("q_head_ld", ctypes.c_int64),
+                ("sel_ld", ctypes.c_int64), ("rows", ctypes.c_int64), ("picked", ctypes.c_int64),
+                ("sel_block", ctypes.c_int32), ("per_seq", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class kvo_pool_stats(ctypes.Structure):
@@ -138,6 +176,11 @@ def lib() -> ctypes.CDLL:
         "kvo_debug_history_host": (ctypes.c_int, [_vp, _i32, _vp]),
         "kvo_set_miss_fetch": (ctypes.c_int, [_vp, _i32, _i32]),
         "kvo_touch_history": (ctypes.c_int, [_vp, _i32, _vp]),
+        "kvo_append_tokens": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+        "kvo_index_scores": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+        "kvo_attend": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+        "kvo_attend_work_bytes": (_i64, [_i64, _i32, _i64]),
+        "kvo_pool_rows": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_i64), ctypes.POINTER(_i32)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -432,6 +475,213 @@ def kvo_probe_host_touch(addr: int, nbytes: int, stride: int, sink, stream=None)
            "kvo_probe_host_touch")
 
 
+# --------------------------------------------- sparse decode on cached rows
+class Cache:
+    """A kvo_cache: rows and index keys in blocks that a table maps.
+
+    rows: uint8 CUDA tensor of whole 656-byte rows, or a Pool (its blocks);
+    keys: bfloat16 or float8_e4m3fn CUDA tensor of whole 128-value keys, one
+    per row, with key_scales (float32, one per key) for float8.  block_rows
+    rows make a block (a Pool brings its own).  table: int32 CUDA tensor
+    [sequences, blocks of a sequence] (rows may be strided), or None: sequence
+    s is block s.  Holds the tensors; they stay where they are."""
+
+    def __init__(self, rows=None, keys=None, key_scales=None, block_rows=None, table=None, sequences=None):
+        c = self.c = kvo_cache()
+        self.tensors = (rows, keys, key_scales, table)
+        counts = []
+        if isinstance(rows, Pool):
+            ptr, blocks, pool_rows = kvo_pool_rows(rows.handle)
+            if block_rows is not None and block_rows != pool_rows:
+                raise ValueError("block_rows is not the pool's")
+            block_rows, c.rows = pool_rows, ptr
+            counts.append(blocks * pool_rows)
+        elif rows is not None:
+            c.rows = _dev_ptr(rows, "torch.uint8")
+            if rows.numel() % ROW_BYTES:
+                raise ValueError("rows must be whole 656-byte rows")
+            counts.append(rows.numel() // ROW_BYTES)
+        if block_rows is None or block_rows < 1:
+            raise ValueError("block_rows must be at least 1")
+        if keys is not None:
+            c.key_type = _key_type(keys)
+            c.keys = _dev_ptr(keys)
+            if keys.numel() % KEY_VALUES:
+                raise ValueError("keys must be whole keys of 128 values")
+            counts.append(keys.numel() // KEY_VALUES)
+            if c.key_type == E4M3:
+                if key_scales is None:
+                    raise ValueError("float8 keys need key_scales")
+                c.key_scales = _dev_ptr(key_scales, "torch.float32")
+                counts.append(key_scales.numel())
+        if not counts:
+            raise ValueError("a cache needs rows or keys")
+        if len(set(counts)) != 1 or counts[0] % block_rows:
+            raise ValueError("rows, keys and key_scales must hold the same whole number of blocks")
+        c.block_rows, c.blocks = block_rows, counts[0] // block_rows
+        if table is None:
+            c.sequences = c.blocks if sequences is None else sequences
+        else:
+            if table.dim() != 2 or not table.is_cuda or str(table.dtype) != "torch.int32":
+                raise ValueError("table must be an int32 CUDA tensor [sequences, blocks]")
+            if table.shape[1] > 1 and table.stride(1) != 1:
+                raise ValueError("table rows must be contiguous")
+            if sequences is not None and sequences != table.shape[0]:
+                raise ValueError("sequences is not the table's")
+            c.table = table.data_ptr()
+            c.sequences, c.table_blocks = table.shape
+            c.table_ld = max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else table.stride(0)
+        self.sequences, self.block_rows, self.blocks = c.sequences, c.block_rows, c.blocks
+        self.ref = ctypes.addressof(c)
+
+
+_ELEMENT = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+
+
+def _key_type(t) -> int:
+    kind = {"torch.bfloat16": BF16, "torch.float8_e4m3fn": E4M3}.get(str(t.dtype))
+    if kind is None:
+        raise ValueError(f"keys must be bfloat16 or float8_e4m3fn, got {t.dtype}")
+    return kind
+
+
+def _cuda(t, what: str, dtype: str, shape=None):
+    """data_ptr of a CUDA tensor of that type (and shape), its last dimension contiguous."""
+    if not t.is_cuda or str(t.dtype) != dtype:
+        raise ValueError(f"{what} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def _whole(t, what: str):
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=None, key=None,
+                      interleaved: bool = True, out_bf16=None, stream=None) -> None:
+    """latent [n, 512], rope [n, 64] and key [n, 128] (optional): bfloat16,
+    float16 or float32 CUDA tensors of one type, tokens strided as they are;
+    pos and seq (optional): int32 CUDA [n]; inv_freq: 32 floats; out_bf16:
+    bfloat16 (or int16) CUDA [n, 576] (optional)."""
+    n, dt = latent.shape[0], str(latent.dtype)
+    if dt not in _ELEMENT:
+        raise ValueError(f"latent must be bfloat16, float16 or float32, got {dt}")
+    t = kvo_tokens()
+    t.latent, t.latent_ld = _cuda(latent, "latent", dt, (n, LATENT_VALUES)), latent.stride(0)
+    t.rope, t.rope_ld = _cuda(rope, "rope", dt, (n, ROPE_VALUES)), rope.stride(0)
+    if key is not None:
+        t.key, t.key_ld = _cuda(key, "key", dt, (n, KEY_VALUES)), key.stride(0)
+    if n <= 1:                       # a lone token has no next one: its stride says nothing
+        t.latent_ld, t.rope_ld, t.key_ld = LATENT_VALUES, ROPE_VALUES, KEY_VALUES
+    t.pos = _cuda(pos, "pos", "torch.int32", (n,))
+    if seq is not None:
+        t.seq = _cuda(seq, "seq", "torch.int32", (n,))
+    if len(inv_freq) != ROPE_VALUES // 2:
+        raise ValueError("inv_freq must hold 32 values")
+    freq = (ctypes.c_double * 32)(*(inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq))
+    t.inv_freq = ctypes.addressof(freq)
+    if out_bf16 is not None:
+        if str(out_bf16.dtype) not in ("torch.bfloat16", "torch.int16") or out_bf16.numel() != n * DEQUANT_VALUES:
+            raise ValueError("out_bf16 must be bfloat16 or int16 [n, 576]")
+        t.out_bf16 = _dev_ptr(out_bf16)
+    t.n, t.dtype, t.interleaved = n, _ELEMENT[dt], 1 if interleaved else 0
+    _check(lib().kvo_append_tokens(ctx, cache.ref, ctypes.addressof(t), _stream_ptr(stream)), "kvo_append_tokens")
+
+
+def _queries(cache: Cache, q, values: int) -> tuple:
+    if q.dim() != 3 or q.shape[2] != values:
+        raise ValueError(f"q must be [queries, heads, {values}]")
+    nq = q.shape[0]
+    if nq < 1 or nq % cache.sequences:
+        raise ValueError("the number of queries must be a multiple of the cache's sequences")
+    heads = q.shape[1]
+    # a dimension of one has no next element: its stride says nothing
+    strides = (q.stride(0) if nq > 1 else heads * values, q.stride(1) if heads > 1 else values)
+    return nq, heads, nq // cache.sequences, strides
+
+
+def kvo_index_scores(ctx: int, cache: Cache, q, weights, lens, n: int, block: int = 1, out=None, stream=None):
+    """q: CUDA [nq, heads, 128] of the keys' type; weights: float32 [nq,
+    heads]; lens: int32 [nq].  Returns float32 [nq, ceil(n / block)] (`out`
+    if given; its rows may be strided)."""
+    import torch
+    nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, KEY_VALUES)
+    s = kvo_score_query()
+    keys = cache.tensors[1]
+    if keys is None:
+        raise ValueError("the cache has no keys")
+    s.q = _cuda(q, "q", str(keys.dtype))
+    s.q_ld, s.q_head_ld = q_ld, q_head_ld
+    s.weights, s.weights_ld = _cuda(weights, "weights", "torch.float32", (nq, heads)), weights.stride(0)
+    s.lens = _cuda(lens, "lens", "torch.int32", (nq,))
+    cols = -(-n // block) if block > 0 else 0
+    if out is None:
+        out = _empty((nq, cols), torch.float32, q.device, stream)
+    s.scores = _cuda(out, "out", "torch.float32", (nq, cols))
+    s.ld = out.stride(0) if nq > 1 else cols
+    s.n, s.per_seq, s.heads, s.block = n, per_seq, heads, block
+    _check(lib().kvo_index_scores(ctx, cache.ref, ctypes.addressof(s), _stream_ptr(stream)), "kvo_index_scores")
+    return out
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor that belongs to `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def kvo_attend_work_bytes(nq: int, heads: int, positions: int) -> int:
+    return int(lib().kvo_attend_work_bytes(nq, heads, positions))
+
+
+def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None = None, sel=None, sel_block: int = 1,
+               out=None, lse=None, work=None, stream=None):
+    """q: bfloat16 CUDA [nq, heads, 576]; lens: int32 [nq]; rows: the largest
+    lens value, needed without sel; sel: int32 [nq, picked] (rows may be
+    strided) of positions, or of blocks of sel_block positions.  Returns (out
+    bfloat16 [nq, heads, 512], lse float32 [nq, heads])."""
+    import torch
+    nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, DEQUANT_VALUES)
+    s = kvo_attend_query()
+    s.q = _cuda(q, "q", "torch.bfloat16")
+    s.q_ld, s.q_head_ld = q_ld, q_head_ld
+    s.lens = _cuda(lens, "lens", "torch.int32", (nq,))
+    if sel is None:
+        if rows is None:
+            raise ValueError("attending to whole sequences needs rows, the largest length")
+        s.rows = positions = rows
+    else:
+        if sel.dim() != 2:
+            raise ValueError("sel must be [queries, picked]")
+        s.sel = _cuda(sel, "sel", "torch.int32", (nq, sel.shape[1]))
+        s.picked = sel.shape[1]
+        s.sel_ld = sel.stride(0) if nq > 1 else s.picked
+        positions = s.picked * sel_block
+    if out is None:
+        out = _empty((nq, heads, LATENT_VALUES), torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _empty((nq, heads), torch.float32, q.device, stream)
+    s.out = _cuda(out, "out", "torch.bfloat16", (nq, heads, LATENT_VALUES))
+    s.lse = _cuda(lse, "lse", "torch.float32", (nq, heads))
+    _whole(out, "out")
+    _whole(lse, "lse")
+    need = kvo_attend_work_bytes(nq, heads, positions)
+    if need > 0:
+        if work is None:
+            work = _empty((need,), torch.uint8, q.device, stream)
+        s.work, s.work_bytes = _dev_ptr(work, "torch.uint8"), work.numel()
+    s.sel_block, s.per_seq, s.heads, s.scale = sel_block, per_seq, heads, scale
+    _check(lib().kvo_attend(ctx, cache.ref, ctypes.addressof(s), _stream_ptr(stream)), "kvo_attend")
+    return out, lse
+
+
 class Context:
     """Owns one kvo context; methods forward to the kvo_* calls above."""
 
@@ -508,6 +758,17 @@ class Context:
         calls = ctypes.c_int64()
         _check(lib().kvo_layers_phase_times(self.handle, ms, ctypes.byref(calls)), "kvo_layers_phase_times")
         return (ms[0], ms[1], ms[2]), calls.value
+
+    def append_tokens(self, cache, latent, rope, pos, inv_freq, seq=None, key=None, interleaved=True, out_bf16=None,
+                      stream=None):
+        kvo_append_tokens(self.handle, cache, latent, rope, pos, inv_freq, seq, key, interleaved, out_bf16, stream)
+
+    def index_scores(self, cache, q, weights, lens, n, block=1, out=None, stream=None):
+        return kvo_index_scores(self.handle, cache, q, weights, lens, n, block, out, stream)
+
+    def attend(self, cache, q, lens, scale, rows=None, sel=None, sel_block=1, out=None, lse=None, work=None,
+               stream=None):
+        return kvo_attend(self.handle, cache, q, lens, scale, rows, sel, sel_block, out, lse, work, stream)
 
     def sync(self, stream=None) -> int:
         return kvo_sync(self.handle, stream)
@@ -641,6 +902,13 @@ def kvo_pool_get_stats(pool: int) -> dict:
     s = kvo_pool_stats()
     _check(lib().kvo_pool_get_stats(pool, ctypes.byref(s)), "kvo_pool_get_stats")
     return s.as_dict()
+
+
+def kvo_pool_rows(pool: int) -> tuple:
+    """(address of the pool's first row, blocks, rows per block)."""
+    p, b, r = _vp(), _i64(), _i32()
+    _check(lib().kvo_pool_rows(pool, ctypes.byref(p), ctypes.byref(b), ctypes.byref(r)), "kvo_pool_rows")
+    return p.value, b.value, r.value
 
 
 def kvo_pool_debug_fail_after(pool: int, which: int, n: int) -> None:

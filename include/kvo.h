@@ -465,6 +465,197 @@ kvo_status kvo_touch_history(kvo_ctx* ctx, int32_t layer, void* stream);
 kvo_status kvo_debug_history_host(kvo_ctx* ctx, int32_t layer, void** out);
 
 /* ------------------------------------------------------------------------
+ * Sparse decode on cached rows: what makes a row, what scores it for the
+ * selection, and the attention that reads it.
+ *
+ * A kvo_cache describes device memory that the caller owns (or a session
+ * pool's blocks, kvo_pool_rows): rows in blocks of block_rows, and next to
+ * them, row for row, the index keys that the selection scores read.
+ * Position p of sequence s is row p % block_rows of block
+ * table[s * table_ld + p / block_rows]; without a table, row p of block s
+ * (one contiguous run of block_rows rows per sequence, such as the gathered
+ * rows of kvo_decode_layers).
+ *
+ * A table entry outside [0, blocks) - or a position past table_blocks
+ * entries, or past block_rows without a table - that a call has to read is
+ * no row: the call treats the position as masked (kvo_append_tokens writes
+ * nothing for it) and latches KVO_ERANGE for kvo_sync.  Entries that no
+ * visible position needs are not read, so they may hold anything.
+ *
+ * The calls keep nothing between them.  Every tensor has to be ready on
+ * `stream`; calls on several streams may overlap as long as they do not
+ * share `work` or an output.  All of them can be captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+
+/* Element types. */
+#define KVO_BF16 0
+#define KVO_FP16 1
+#define KVO_FP32 2
+#define KVO_E4M3 3
+
+#define KVO_KEY_VALUES 128          /* values of one index key */
+#define KVO_MAX_HEADS 128           /* query heads per call */
+#define KVO_MAX_QUERIES 65535       /* queries per call */
+#define KVO_MAX_SCORE_BLOCK 128     /* positions per score or per selected block */
+
+typedef struct kvo_cache {
+  void* rows;              /* blocks * block_rows Q8G64 rows (16-byte aligned), or NULL if a call needs none */
+  void* keys;              /* blocks * block_rows keys of 128 values (16-byte aligned), or NULL */
+  float* key_scales;       /* KVO_E4M3 keys: one fp32 factor per key; else NULL */
+  const int32_t* table;    /* device int32[sequences][table_ld], or NULL */
+  int64_t table_ld;        /* entries from one table row to the next */
+  int64_t blocks;          /* blocks behind rows and keys */
+  int32_t block_rows;      /* rows per block, >= 1 */
+  int32_t table_blocks;    /* entries of a table row that may be read */
+  int32_t sequences;       /* table rows; without a table at most `blocks` */
+  int32_t key_type;        /* KVO_BF16 or KVO_E4M3 */
+} kvo_cache;
+
+/*
+ * kvo_append_tokens - write the cache rows (and index keys) of n tokens in
+ * one launch, each from the model's outputs for that token.  Token i belongs
+ * to position pos[i] of sequence seq[i]:
+ *   - latent: 512 values, quantised in 8 groups of 64.  A group's scale is
+ *     the smallest fp16 s with 127 * s >= max|x| (at most 65504), its values
+ *     round(x / s), ties to even, within [-127, 127]: no value of a finite
+ *     group saturates below that limit.  A group that holds an infinity or a
+ *     NaN gets a NaN scale and zero values: all of it reads back as NaN.
+ *   - rope: 64 values in 32 pairs, (2i, 2i+1) if interleaved, else
+ *     (i, i+32); pair i is rotated by pos * inv_freq[i] radians (the turn is
+ *     formed exactly in integers, so far positions lose nothing) and stored
+ *     as bf16, in the order it came in.
+ *   - key (optional): 128 values, stored as bf16, or as e4m3 of key / s with
+ *     the factor s in key_scales: the smallest power of two (at least
+ *     2^-100) with 448 * s >= max|key|, so the only rounding is to e4m3.  A
+ *     key that holds an infinity or a NaN gets a NaN factor.
+ *   latent, rope, key   device, elements of `dtype` (KVO_BF16, KVO_FP16 or
+ *             KVO_FP32); a token's values are contiguous, tokens latent_ld,
+ *             rope_ld and key_ld elements apart.  Every token's values start
+ *             on a 16-byte boundary.
+ *   seq       device int32[n] or NULL (token i is sequence i); a negative
+ *             entry skips its token: nothing is written for it.
+ *   pos       device int32[n].
+ *   inv_freq  host double[32], each within [-2^20, 2^20], read before the
+ *             call returns.
+ *   out_bf16  device uint16[n][576] (16-byte aligned) or NULL: the values
+ *             the rows stand for, as kvo_resolve_gather's out_bf16.
+ * A sequence outside [0, sequences), a negative position or a position
+ * without a row latches KVO_ERANGE; that token's out_bf16 row is zero.  Two
+ * tokens of one call must not name the same position.
+ * KVO_EINVAL: n < 0, a NULL or misaligned argument that n > 0 needs, an
+ * unknown type, an inv_freq out of range or NaN, cache->rows NULL, or `key` given
+ * without cache->keys (or without key_scales for e4m3).
+ */
+typedef struct kvo_tokens {
+  const void* latent;
+  const void* rope;
+  const void* key;
+  const int32_t* seq;
+  const int32_t* pos;
+  const double* inv_freq;
+  uint16_t* out_bf16;
+  int64_t latent_ld;
+  int64_t rope_ld;
+  int64_t key_ld;
+  int64_t n;
+  int32_t dtype;
+  int32_t interleaved;
+} kvo_tokens;
+kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, const kvo_tokens* tokens, void* stream);
+
+/*
+ * kvo_index_scores - the scores that kvo_select_topk(_batch) selects from:
+ * for query t (of sequence t / per_seq) and cached position j < lens[t]
+ *     score[t][j] = s_j * sum_h weights[t][h] * max(0, q[t][h] . key_j)
+ * with s_j the key's factor (1 for bf16 keys); -inf for j >= lens[t].  With
+ * block > 1, column b is the largest score of positions
+ * [b * block, (b + 1) * block), a NaN counting as -inf.
+ *   q        device [nq][heads][128] of the keys' type; heads q_head_ld
+ *            elements apart, queries q_ld; every head 16-byte aligned.
+ *   weights  device fp32, query t's at weights + t * weights_ld.
+ *   lens     device int32[nq], the positions each query sees (<= 0: none).
+ *   n        positions to score: ceil(n / block) columns are written for
+ *            every query.  A query sees at most n positions.
+ *   block    a power of two, 1 .. KVO_MAX_SCORE_BLOCK.
+ *   scores   device fp32, query t's row at scores + t * ld.
+ * The products and the sum over heads are accumulated in fp32.
+ * nq = cache->sequences * per_seq, at most KVO_MAX_QUERIES.  KVO_EINVAL for a NULL or misaligned
+ * argument, heads outside 1 .. KVO_MAX_HEADS, per_seq < 1, n < 1, n > 2^31 - 256, ld <
+ * ceil(n / block), a bad block or key type, or a cache without keys.
+ */
+typedef struct kvo_score_query {
+  const void* q;
+  const float* weights;
+  const int32_t* lens;
+  float* scores;
+  int64_t q_ld;
+  int64_t q_head_ld;
+  int64_t weights_ld;
+  int64_t ld;
+  int64_t n;
+  int32_t per_seq;
+  int32_t heads;
+  int32_t block;
+  int32_t reserved;
+} kvo_score_query;
+kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, const kvo_score_query* query, void* stream);
+
+/*
+ * kvo_attend - softmax attention of absorbed MLA queries over cached rows:
+ *     z_j = scale * (q[0..512) . latent_j + q[512..576) . rope_j)
+ *     out = sum_j softmax(z)_j * latent_j,  lse = log sum_j exp(z_j)
+ * where latent_j and rope_j are the bf16 values a row stands for (the
+ * out_bf16 of kvo_resolve_gather).  Query t (of sequence t / per_seq)
+ * attends to positions below lens[t]:
+ *   sel NULL   all of them, positions [0, min(lens[t], rows));
+ *   sel        device int32, query t's list of `picked` entries at
+ *              sel + t * sel_ld: entry u names positions
+ *              [u * sel_block, (u + 1) * sel_block).  Entries below 0, and
+ *              positions at or past lens[t], are masked; a position listed
+ *              twice counts twice.  kvo_select_topk(_batch)'s idx is such a
+ *              list, over positions or over the blocks of kvo_index_scores.
+ * A query that sees no position gets out = 0 and lse = -inf.  A masked
+ * row's bytes never reach the output, whatever they hold.
+ *   q       device bf16 [nq][heads][576]; heads q_head_ld elements apart,
+ *           queries q_ld; every head 16-byte aligned.
+ *   out     device bf16 [nq][heads][512], contiguous, 16-byte aligned.
+ *   lse     device fp32 [nq][heads], or NULL.
+ *   work    device scratch of kvo_attend_work_bytes' size (16-byte aligned),
+ *           or NULL when that is 0; free again once the call's work is done.
+ * The products are exact (bf16 times bf16), summed in fp32; the weights are
+ * rounded to bf16 (at most 2^-8 of each weight) for the second product.
+ * nq = cache->sequences * per_seq, at most KVO_MAX_QUERIES.  KVO_EINVAL for a NULL or misaligned
+ * argument, heads outside 1 .. KVO_MAX_HEADS, per_seq < 1, rows < 0 or
+ * > 2^31 - 256, picked < 0, picked * sel_block > 2^31 - 256, a sel_block that is not a
+ * power of two in 1 .. KVO_MAX_SCORE_BLOCK, a scale that is not finite, too
+ * little work space, or a cache without rows.
+ */
+typedef struct kvo_attend_query {
+  const void* q;
+  const int32_t* lens;
+  const int32_t* sel;
+  uint16_t* out;
+  float* lse;
+  void* work;
+  int64_t work_bytes;
+  int64_t q_ld;
+  int64_t q_head_ld;
+  int64_t sel_ld;
+  int64_t rows;            /* without sel: the largest lens value (positions past it are not read) */
+  int64_t picked;          /* with sel: entries per query */
+  int32_t sel_block;
+  int32_t per_seq;
+  int32_t heads;
+  float scale;
+} kvo_attend_query;
+kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo_attend_query* query, void* stream);
+
+/* kvo_attend_work_bytes - the scratch bytes a kvo_attend of nq queries of
+ * `heads` heads over at most `positions` positions each (rows, or picked *
+ * sel_block) needs on the current device; -1 for arguments it would refuse. */
+int64_t kvo_attend_work_bytes(int64_t nq, int32_t heads, int64_t positions);
+
+/* ------------------------------------------------------------------------
  * Session block store/restore.
  *
  * Sources (page title, section):
@@ -591,6 +782,13 @@ kvo_status kvo_pool_block_table(kvo_pool* pool, int32_t session, int32_t layer, 
                                 int64_t max, int64_t* count);
 
 kvo_status kvo_pool_get_stats(kvo_pool* pool, kvo_pool_stats* out);
+
+/* kvo_pool_rows - the pool's blocks as a kvo_cache takes them: *rows = the
+ * first block's first row, *blocks = pool_blocks, *block_rows =
+ * block_tokens.  A session's table of a layer is kvo_pool_block_table with
+ * which = 0.  The memory stays the pool's; blocks that a store or restore
+ * still copies (KVO_EBUSY) must not be written.  Host only. */
+kvo_status kvo_pool_rows(kvo_pool* pool, void** rows, int64_t* blocks, int32_t* block_rows);
 
 /* Test hook: the n-th next single-block allocation (0 = the next one) from
  * the pool (which = 0) or tier (which = 1) queue fails; n < 0 disarms. */

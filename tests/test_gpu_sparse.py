@@ -1,0 +1,716 @@
+"""kvo_append_tokens, kvo_index_scores and kvo_attend against the 64-bit oracle.
+
+Tolerances, from the number formats alone (u = 2^-24, half a step of fp32;
+2^-8, half a step of bf16):
+  rotated values   2^-8 |x| for the one rounding, and 8 u (|a| + |b|) for the
+                   reduced angle, the sine and cosine and the three products;
+  scores           every product of the keys' types is exact in fp32; a sum of
+                   128 + 64 terms, each step off by at most 2 u of the sum of
+                   magnitudes (an accumulator may truncate), the factors
+                   2 steps more;
+  lse              the logits' error (576 steps of 2 u of the magnitudes), the
+                   exponentials and the logarithm 16 u, a blocked sum 2 u for
+                   each of n / 128 + 32 steps, and 2 u of its size;
+  out              2^-8 |out| for its rounding, and for the sum of p |v| the
+                   weights' rounding 2^-8, twice the logits' error and the
+                   steps of the sum as above.
+Quantised values, their scales and factors have to be equal.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kvo_sparse_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+INV_FREQ = 10_000.0 ** (-np.arange(0, 64, 2) / 64)
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from gather_radix_top_gb300 import build, kvo
+    build.build()
+    c = kvo.Context(1, 64, 64)
+    yield c
+    c.close()
+
+
+@pytest.fixture(scope="module")
+def kvo():
+    from gather_radix_top_gb300 import kvo as K
+    return K
+
+
+def dev(x, dtype=None):
+    t = torch.as_tensor(x)
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def block_table(rng, sequences, blocks, spare=2):
+    total = sequences * blocks + spare
+    return rng.permutation(total)[:sequences * blocks].reshape(sequences, blocks).astype(np.int32), total
+
+
+def random_rows(rng, n, scale=(1e-3, 1e-2)):
+    rows = rng.integers(0, 256, (n, 656), dtype=np.uint8)
+    rows[:, :512][rows[:, :512] == 128] = 0
+    rows[:, 512:528] = rng.uniform(*scale, (n, 8)).astype(np.float16).view(np.uint8)
+    rows[:, 528:] = np.ascontiguousarray(O.bf16_bits(rng.standard_normal((n, 64)))).view(np.uint8)
+    return rows
+
+
+# -------------------------------------------------------------------- append
+def append_case(kvo, ctx, rng, dtype, n, interleaved, key, block_rows, seqs=None, pos=None, sequences=None, spread=3.0,
+                x=None, ld=None):
+    sequences = sequences or max(1, n)
+    seqs = np.arange(n, dtype=np.int32) if seqs is None else np.asarray(seqs, np.int32)
+    pos = rng.integers(0, 3 * block_rows, n).astype(np.int32) if pos is None else np.asarray(pos, np.int32)
+    table, blocks = block_table(rng, sequences, 3)
+    wide = ld or 576
+    kv = rng.standard_normal((max(n, 1), wide)) * np.exp(rng.normal(0, spread, (max(n, 1), wide)))
+    if x is not None:
+        kv[:x.shape[0], :x.shape[1]] = x
+    kv = dev(kv, TYPES[dtype])[:n]
+    kk = dev(rng.standard_normal((n, 128)) * np.exp(rng.normal(0, spread, (n, 128))), TYPES[dtype])
+    R = blocks * block_rows
+    rows = torch.full((R, 656), 0x5A, dtype=torch.uint8, device="cuda")
+    keys = scales = None
+    if key == "bf16":
+        keys = torch.full((R, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    elif key == "e4m3":
+        keys = torch.full((R, 128), 0x22, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        scales = torch.full((R,), 5.0, device="cuda")
+    cache = kvo.Cache(rows=rows, keys=keys, key_scales=scales, block_rows=block_rows, table=dev(table))
+    values = torch.full((n, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:576], dev(pos), INV_FREQ, seq=dev(seqs),
+                      key=kk if key != "none" else None, interleaved=interleaved, out_bf16=values)
+    status = ctx.sync()
+    return dict(kv=f64(kv), kk=f64(kk), rows=rows.cpu().numpy(), keys=keys, scales=scales, table=table, blocks=blocks,
+                seqs=seqs, pos=pos, values=values, status=status, sequences=sequences)
+
+
+def check_append(kvo, r, dtype, interleaved, key, block_rows):
+    want_rows = np.full_like(r["rows"], 0x5A)
+    touched, bad = set(), False
+    got_values = f64(r["values"])
+    for i, (s, p) in enumerate(zip(r["seqs"], r["pos"])):
+        if s < 0:
+            assert (got_values[i] == 7.0).all()
+            continue
+        at = None
+        if s < r["sequences"] and p >= 0:
+            at = O.row_of(r["table"], r["blocks"], block_rows, r["sequences"], int(s), int(p))
+        if at is None:
+            bad = True
+            assert not got_values[i].any()
+            continue
+        touched.add(at)
+        row = r["rows"][at]
+        for g in range(8):
+            q, bits = O.latent_group(r["kv"][i, 64 * g:64 * g + 64])
+            assert int(row[512 + 2 * g:514 + 2 * g].view(np.uint16)[0]) == bits
+            assert np.array_equal(row[64 * g:64 * g + 64].view(np.int8), q), (i, g)
+        latent, rope = O.row_values(row)
+        assert np.array_equal(latent, got_values[i, :512], equal_nan=True)
+        assert np.array_equal(rope, got_values[i, 512:], equal_nan=True)
+        x = r["kv"][i, 512:576]
+        exact = O.rotate(x, int(p), INV_FREQ, interleaved)
+        pair = np.abs(x[0::2]) + np.abs(x[1::2]) if interleaved else np.abs(x[:32]) + np.abs(x[32:])
+        pair = np.repeat(pair, 2) if interleaved else np.tile(pair, 2)
+        assert (np.abs(rope - exact) <= 2.0 ** -8 * np.abs(exact) + 8 * U * pair + 2.0 ** -133).all(), i
+        if key == "bf16":
+            got = r["keys"][at].view(torch.int16).cpu().numpy().view(np.uint16)
+            assert np.array_equal(got, O.bf16_bits(r["kk"][i]))
+        elif key == "e4m3":
+            want, factor = O.key_e4m3(r["kk"][i])
+            assert float(r["scales"][at]) == factor
+            assert np.array_equal(r["keys"][at].view(torch.uint8).cpu().numpy(), want)
+        want_rows[at] = row
+    assert np.array_equal(r["rows"], want_rows)              # nothing else was written
+    rest = [i for i in range(len(r["rows"])) if i not in touched]
+    if key == "e4m3":
+        assert (r["keys"].view(torch.uint8)[rest] == 0x22).all() and (r["scales"][rest] == 5.0).all()
+    elif key == "bf16":
+        assert (r["keys"][rest] == 3.0).all()
+    assert r["status"] == (kvo.KVO_ERANGE if bad else kvo.KVO_OK)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("key", ["none", "bf16", "e4m3"])
+@pytest.mark.parametrize("n,block_rows,interleaved", [(1, 16, True), (7, 5, False), (33, 16, True), (65, 1, False)])
+def test_append(kvo, ctx, dtype, key, n, block_rows, interleaved):
+    rng = np.random.default_rng([n, block_rows, len(dtype), ord(key[0])])
+    spread = 1.0 if dtype == "fp16" else 3.0
+    r = append_case(kvo, ctx, rng, dtype, n, interleaved, key, block_rows, spread=spread, ld=640 if n == 7 else None)
+    check_append(kvo, r, dtype, interleaved, key, block_rows)
+
+
+def test_append_nothing(kvo, ctx):
+    r = append_case(kvo, ctx, np.random.default_rng(1), "bf16", 0, True, "e4m3", 16)
+    assert (r["rows"] == 0x5A).all() and r["status"] == kvo.KVO_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_edge_values(kvo, ctx, dtype):
+    """Groups of zeros, of values that no scale holds, next to rounding borders, infinite and NaN."""
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((8, 512))
+    x[0] = 0.0
+    x[1, 64:128] = 0.0
+    x[1, 70] = 2.0 ** -60
+    x[2, 0] = 1e30
+    x[3, 5], x[3, 200], x[3, 400] = np.inf, np.nan, -np.inf
+    x[4] = np.tile(np.arange(64) - 32 + 0.5, 8) * 2.0 ** -7   # ties of a power-of-two scale
+    x[4, ::64] = 127 * 2.0 ** -7
+    s = float(np.float16(0.0037))
+    x[5] = (np.arange(512) % 127 + 0.5) * s                   # as near to ties as the type gets
+    x[5, ::64] = 127 * s
+    x[6] = np.nextafter(np.float32((np.arange(512) % 127 + 0.5)) * np.float32(s), np.float32(0))
+    x[6, ::64] = 127 * s
+    x[7] *= 2.0 ** -22                                        # subnormal scales
+    r = append_case(kvo, ctx, rng, dtype, 8, True, "e4m3", 16, x=x)
+    check_append(kvo, r, dtype, True, "e4m3", 16)
+
+
+def test_append_key_edges(kvo, ctx):
+    rng = np.random.default_rng(10)
+    kk = rng.standard_normal((6, 128)).astype(np.float32)
+    kk[0] = 0.0
+    kk[1] = 0.0
+    kk[1, 3] = 448 * 2.0 ** -5                                # exactly the largest e4m3 at its factor
+    kk[2] = 0.0
+    kk[2, 3] = np.nextafter(np.float32(448 * 2.0 ** -5), np.float32(1e9))
+    kk[3, 7] = np.inf
+    kk[4, 0] = np.nan
+    kk[5] = np.float32(2.0 ** -140)
+    rows = torch.zeros(6, 656, dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(6, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.zeros(6, device="cuda")
+    cache = kvo.Cache(rows=rows, keys=keys, key_scales=scales, block_rows=1)
+    kv = torch.randn(6, 576, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], torch.zeros(6, dtype=torch.int32, device="cuda"), INV_FREQ,
+                      key=dev(kk))
+    assert ctx.sync() == kvo.KVO_OK
+    for i in range(6):
+        want, factor = O.key_e4m3(kk[i])
+        assert np.array_equal(float(scales[i]), factor, equal_nan=True)
+        assert np.array_equal(keys[i].view(torch.uint8).cpu().numpy(), want), i
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_append_far_positions(kvo, ctx, interleaved):
+    """Angles of positions up to 2^31 - 1 (a table whose last entry alone is used)."""
+    rng = np.random.default_rng(11)
+    pos = np.array([0, 1, 65_535, 1_048_575, 16_777_217, 2 ** 31 - 1], np.int32)
+    rows = torch.zeros(6, 656, dtype=torch.uint8, device="cuda")
+    kv = rng.standard_normal((6, 576)).astype(np.float32)
+    for i, p in enumerate(pos):
+        block = 2 ** 30
+        table = torch.full((1, 2), -1, dtype=torch.int32, device="cuda")
+        big = kvo.Cache(rows=rows[i:i + 1], block_rows=1, table=table)
+        # one block of 2^30 rows a table entry, of which only the addressed row exists: shift the base
+        big.c.block_rows, big.c.blocks = block, 1
+        table[0, int(p) // block] = 0
+        big.c.rows = rows.data_ptr() + i * 656 - (int(p) % block) * 656
+        ctx.append_tokens(big, dev(kv[i:i + 1, :512]), dev(kv[i:i + 1, 512:]), dev(pos[i:i + 1]), INV_FREQ,
+                          interleaved=interleaved)
+    assert ctx.sync() == kvo.KVO_OK
+    out = rows.cpu().numpy()
+    for i, p in enumerate(pos):
+        x = kv[i, 512:].astype(np.float64)
+        exact = O.rotate(x, int(p), INV_FREQ, interleaved)
+        pair = np.abs(x[0::2]) + np.abs(x[1::2]) if interleaved else np.abs(x[:32]) + np.abs(x[32:])
+        pair = np.repeat(pair, 2) if interleaved else np.tile(pair, 2)
+        rope = O.row_values(out[i])[1]
+        assert (np.abs(rope - exact) <= 2.0 ** -8 * np.abs(exact) + 8 * U * pair).all(), p
+
+
+def test_append_skips_padding_and_refuses_bad_places(kvo, ctx):
+    rng = np.random.default_rng(12)
+    r = append_case(kvo, ctx, rng, "bf16", 6, True, "e4m3", 4, seqs=[0, -1, 2, 3, 1, 0], pos=[0, 1, 11, 2, 7, 5],
+                    sequences=4)
+    check_append(kvo, r, "bf16", True, "e4m3", 4)
+    assert r["status"] == kvo.KVO_OK
+    r = append_case(kvo, ctx, rng, "bf16", 6, True, "e4m3", 4, seqs=[0, 4, 2, 3, 1, 0], pos=[0, 1, 12, -2, 7, 5],
+                    sequences=4)
+    check_append(kvo, r, "bf16", True, "e4m3", 4)
+    assert r["status"] == kvo.KVO_ERANGE
+
+
+def test_append_bad_table_entries(kvo, ctx):
+    rows = torch.full((8, 656), 0x5A, dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[-1, 2 ** 31 - 1], [2, 0]], dtype=torch.int32, device="cuda")
+    cache = kvo.Cache(rows=rows, block_rows=4, table=table)
+    kv = torch.randn(3, 576, device="cuda")
+    seq = torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([1, 5, 2], dtype=torch.int32, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], pos, INV_FREQ, seq=seq)
+    assert ctx.sync() == kvo.KVO_ERANGE
+    assert (rows == 0x5A).all()
+
+
+# --------------------------------------------------------------------- score
+def score_inputs(rng, nq, heads, keys_n, dtype):
+    q = dev(rng.standard_normal((nq, heads, 128)), torch.float32)
+    k = dev(rng.standard_normal((keys_n, 128)), torch.float32)
+    if dtype == "e4m3":
+        q, k = q.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn)
+        scales = torch.exp2(dev(rng.integers(-6, 2, keys_n), torch.float32))
+    else:
+        q, k, scales = q.bfloat16(), k.bfloat16(), None
+    w = dev(rng.standard_normal((nq, heads)), torch.float32)
+    return q, k, scales, w
+
+
+def check_scores(got, q, k, scales, w, rows, lens, n, block):
+    factors = np.ones(k.shape[0]) if scales is None else f64(scales)
+    heads = q.shape[1]
+    padded = [list(r) + [None] * (n - len(r)) for r in rows]
+    want, size = O.index_scores(f64(q), f64(w), f64(k), factors, padded, lens, block)
+    got = f64(got)
+    assert got.shape == want.shape
+    fin = np.isfinite(want)
+    assert np.array_equal(np.isneginf(got), np.isneginf(want)) and np.array_equal(np.isnan(got), np.isnan(want))
+    tol = (128 + heads + 2) * 2 * U * size
+    assert (np.abs(got - want)[fin] <= tol[fin]).all(), float((np.abs(got - want)[fin] - tol[fin]).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("sequences,per_seq,heads,n,block,block_rows", [
+    (1, 1, 1, 1, 1, 1), (1, 1, 64, 130, 1, 16), (2, 4, 64, 257, 1, 16), (3, 2, 24, 300, 16, 48), (1, 1, 128, 129, 64, 7),
+    (2, 3, 100, 200, 128, 16), (1, 7, 40, 140, 32, 64), (1, 1, 8, 1000, 2, 16), (5, 1, 17, 128, 4, 128)])
+def test_scores(kvo, ctx, dtype, sequences, per_seq, heads, n, block, block_rows):
+    rng = np.random.default_rng([sequences, per_seq, heads, n, len(dtype)])
+    nq, blocks = sequences * per_seq, -(-n // block_rows)
+    table, total = block_table(rng, sequences, blocks)
+    q, k, scales, w = score_inputs(rng, nq, heads, total * block_rows, dtype)
+    lens = rng.integers(0, n + 1, nq)
+    lens[0] = n
+    if nq > 2:
+        lens[1] = 0
+    if nq > 3:
+        lens[2] = -3
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=block_rows, table=dev(table))
+    got = ctx.index_scores(cache, q, w, dev(lens, torch.int32), n, block=block)
+    assert ctx.sync() == kvo.KVO_OK
+    rows = [[O.row_of(table, total, block_rows, sequences, t // per_seq, p) for p in range(n)] for t in range(nq)]
+    check_scores(got, q, k, scales, w, rows, lens, n, block)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_scores_strides_and_contiguous_cache(kvo, ctx, dtype):
+    rng = np.random.default_rng(21)
+    nq, heads, n = 3, 20, 150
+    wide, k, scales, w = score_inputs(rng, nq, 2 * heads, nq * n, dtype)
+    q = wide[:, ::2]
+    weights = torch.zeros(nq, 99, device="cuda")[:, 5:5 + heads]
+    weights.copy_(w[:, :heads])
+    out = torch.full((nq, 200), 3.0, device="cuda")
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=n)
+    lens = np.array([150, 1, 77])
+    ctx.index_scores(cache, q, weights, dev(lens, torch.int32), n, out=out[:, :n])
+    assert ctx.sync() == kvo.KVO_OK
+    assert (out[:, n:] == 3.0).all()
+    rows = [list(range(t * n, (t + 1) * n)) for t in range(nq)]
+    check_scores(out[:, :n], q, k, scales, weights, rows, lens, n, 1)
+
+
+def test_scores_bad_pages(kvo, ctx):
+    """Bad entries mask what they would hold; beyond a query's length they are not read."""
+    rng = np.random.default_rng(22)
+    q, k, scales, w = score_inputs(rng, 2, 16, 64, "e4m3")
+    table = np.array([[1, -1, 3, 0], [2, 0, 77, 9999]], np.int32)
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=16, table=dev(table))
+    for lens, want in (([64, 64], kvo.KVO_ERANGE), ([16, 32], kvo.KVO_OK)):
+        got = ctx.index_scores(cache, q, w, dev(lens, torch.int32), 64)
+        assert ctx.sync() == want
+        rows = [[O.row_of(table, 4, 16, 2, t, p) for p in range(64)] for t in range(2)]
+        check_scores(got, q, k, scales, w, rows, lens, 64, 1)
+    # a table shorter than n
+    short = kvo.Cache(keys=k, key_scales=scales, block_rows=16, table=dev(table[:1, :1]))
+    got = ctx.index_scores(short, q[:1], w[:1], dev([40], torch.int32), 64)
+    assert ctx.sync() == kvo.KVO_ERANGE
+    assert torch.isneginf(got[0, 16:]).all() and torch.isfinite(got[0, :16]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_scores_nan_keys(kvo, ctx, dtype):
+    """A NaN stays in its own column, ranks lowest in a block, and masked keys are never looked at."""
+    rng = np.random.default_rng(23)
+    n, heads = 140, 16
+    q, k, scales, w = score_inputs(rng, 1, heads, 256, dtype)
+    if dtype == "bf16":
+        k[5], k[130], k[150:] = math.nan, math.inf, math.nan
+        k[130] *= q[0, 0].sign()
+    else:
+        scales[5], scales[150:] = math.nan, math.nan
+        k.view(torch.uint8)[150:] = 0x7F
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=256)
+    rows = [list(range(n))]
+    for block in (1, 16):
+        got = ctx.index_scores(cache, q, w, dev([n - 1], torch.int32), n, block=block)
+        assert ctx.sync() == kvo.KVO_OK
+        clean = f64(k).copy()
+        if dtype == "e4m3" or block == 1:
+            assert torch.isnan(got[0, 5]) if block == 1 else torch.isfinite(got[0, 0])
+        assert torch.isneginf(got[0, n - 1]) if block == 1 else True
+        keep = np.array([c for c in range(got.shape[1]) if c not in ((130,) if block == 1 else (8,))])
+        if dtype == "bf16":
+            clean[130] = 0.0
+        factors = np.ones(256) if scales is None else f64(scales)
+        want, size = O.index_scores(f64(q), f64(w), clean, factors, rows, [n - 1], block)
+        g = f64(got)[:, keep]
+        want, size = want[:, keep], size[:, keep]
+        fin = np.isfinite(want)
+        assert np.array_equal(np.isnan(g), np.isnan(want))
+        assert (np.abs(g - want)[fin] <= ((128 + heads + 2) * 2 * U * size)[fin]).all()
+
+
+def test_scores_feed_the_selection(kvo, ctx):
+    """Scores of a short context select every visible position first, lower positions on ties."""
+    rng = np.random.default_rng(24)
+    q, k, scales, w = score_inputs(rng, 2, 32, 2 * 500, "e4m3")
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=500)
+    lens = dev([500, 40], torch.int32)
+    scores = ctx.index_scores(cache, q, w.abs(), lens, 500)
+    idx = ctx.select_topk_batch(scores, 64)
+    assert ctx.sync() == kvo.KVO_OK
+    assert idx[1].tolist() == list(range(64))
+    want = np.sort(np.argsort(-f64(scores[0]), kind="stable")[:64])
+    assert np.array_equal(idx[0].cpu().numpy(), want)
+
+
+# -------------------------------------------------------------------- attend
+def check_attend(out, lse, q, scale, lists, heads):
+    out, lse = f64(out), lse.cpu().numpy().astype(np.float64)
+    for t, rows in enumerate(lists):
+        want, want_lse, spread, size = O.attend(f64(q[t]), scale, rows)
+        if not rows:
+            assert not out[t].any() and np.isneginf(lse[t]).all(), t
+            continue
+        steps = len(rows) / 128 + 32
+        logit = 2 * U * 576 * size
+        tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 2 * logit + 16 * U + 2 * U * steps)[:, None]
+        assert (np.abs(out[t] - want) <= tol).all(), (t, float((np.abs(out[t] - want) / tol).max()))
+        tol = logit + 16 * U + 2 * U * steps + 2 * U * np.abs(want_lse)
+        assert (np.abs(lse[t] - want_lse) <= tol).all(), (t, float((np.abs(lse[t] - want_lse) / tol).max()))
+
+
+def attend_case(kvo, ctx, rng, sequences, per_seq, heads, n, sel_block, picked, block_rows, lens=None, scale=192 ** -0.5,
+                sel=None, rows_scale=(1e-3, 1e-2)):
+    nq = sequences * per_seq
+    blocks = -(-n // block_rows) if n else 1
+    table, total = block_table(rng, sequences, blocks)
+    rows = random_rows(rng, total * block_rows, rows_scale)
+    q = dev(rng.standard_normal((nq, heads, 576)), torch.bfloat16)
+    if lens is None:
+        lens = rng.integers(0, n + 1, nq)
+        lens[0] = n
+        if nq > 2:
+            lens[1] = 0
+    if sel is None and picked is not None:
+        units = -(-n // sel_block)
+        sel = np.stack([np.sort(rng.choice(units, picked, replace=False)) for _ in range(nq)]).astype(np.int32)
+    cache = kvo.Cache(rows=dev(rows), block_rows=block_rows, table=dev(table))
+    out, lse = ctx.attend(cache, q, dev(lens, torch.int32), scale, rows=n, sel=None if sel is None else dev(sel),
+                          sel_block=sel_block)
+    assert ctx.sync() == kvo.KVO_OK
+    lists = []
+    for t in range(nq):
+        pos = O.positions_of(None if sel is None else sel[t], sel_block, int(lens[t]), n)
+        lists.append([rows[O.row_of(table, total, block_rows, sequences, t // per_seq, p)] for p in pos])
+    check_attend(out, lse, q, scale, lists, heads)
+
+
+@pytest.mark.parametrize("sequences,per_seq,heads,n,block_rows", [
+    (1, 1, 1, 1, 1), (1, 1, 64, 128, 16), (1, 1, 16, 127, 16), (1, 1, 128, 129, 48), (3, 2, 20, 300, 16),
+    (2, 1, 100, 513, 64), (1, 4, 33, 260, 7), (1, 1, 64, 5000, 16), (40, 1, 8, 70, 16)])
+def test_attend_whole_sequences(kvo, ctx, sequences, per_seq, heads, n, block_rows):
+    rng = np.random.default_rng([sequences, per_seq, heads, n])
+    attend_case(kvo, ctx, rng, sequences, per_seq, heads, n, 1, None, block_rows)
+
+
+@pytest.mark.parametrize("sequences,per_seq,heads,n,sel_block,picked,block_rows", [
+    (1, 1, 64, 4000, 1, 2048, 16), (2, 2, 20, 1000, 1, 129, 48), (1, 1, 7, 50, 1, 1, 16), (3, 1, 64, 700, 16, 23, 16),
+    (1, 3, 128, 1000, 64, 9, 16), (2, 1, 32, 900, 128, 5, 7), (1, 1, 48, 333, 2, 100, 64)])
+def test_attend_selected(kvo, ctx, sequences, per_seq, heads, n, sel_block, picked, block_rows):
+    rng = np.random.default_rng([sequences, per_seq, heads, n, sel_block])
+    attend_case(kvo, ctx, rng, sequences, per_seq, heads, n, sel_block, picked, block_rows)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_attend_odd_lists(kvo, ctx, heads):
+    """Padding entries, repeated ones, entries past the length, in no order; a list with nothing visible."""
+    rng = np.random.default_rng(31)
+    sel = rng.integers(-3, 400, (4, 200)).astype(np.int32)
+    sel[1] = -1
+    sel[2] = 7
+    sel[3, :] = 2 ** 31 - 1
+    sel[3, 150] = 0
+    attend_case(kvo, ctx, rng, 4, 1, heads, 300, 1, None, 16, lens=np.array([250, 300, 300, 1]), sel=sel)
+    sel[3, :] = (2 ** 31 - 1) // 16
+    attend_case(kvo, ctx, rng, 4, 1, heads, 300, 16, None, 16, lens=np.array([250, 300, 113, 0]), sel=sel)
+
+
+def test_attend_wide_logits(kvo, ctx):
+    """Logits of hundreds, growing and falling along the list: the running maximum has to move."""
+    rng = np.random.default_rng(32)
+    for order in (1, -1):
+        n, heads = 1500, 16
+        rows = random_rows(rng, n)
+        for j in range(n):                                   # rope part grows with the position
+            x = np.zeros(64)
+            x[:8] = (j if order > 0 else n - j) / 20
+            rows[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+        q = rng.standard_normal((1, heads, 576))
+        q[..., 512:520] = np.linspace(-1, 4, heads)[None, :, None]
+        q = dev(q, torch.bfloat16)
+        cache = kvo.Cache(rows=dev(rows), block_rows=n)
+        out, lse = ctx.attend(cache, q, dev([n], torch.int32), 0.5, rows=n)
+        assert ctx.sync() == kvo.KVO_OK
+        check_attend(out, lse, q, 0.5, [list(rows)], heads)
+
+
+def test_attend_extreme_scales(kvo, ctx):
+    rng = np.random.default_rng(33)
+    for scale in (0.0, -0.07, 1e-30):
+        attend_case(kvo, ctx, rng, 1, 1, 16, 200, 1, None, 16, scale=scale)
+    attend_case(kvo, ctx, rng, 1, 1, 16, 200, 1, None, 16, rows_scale=(6e-8, 6e-7))
+
+
+@pytest.mark.parametrize("heads", [5, 64])
+def test_attend_masked_rows_never_reach_the_output(kvo, ctx, heads):
+    """NaN and infinite rows past the length, in unlisted blocks and beside them."""
+    rng = np.random.default_rng(34)
+    n, br = 400, 16
+    table, total = block_table(rng, 1, n // br)
+    rows = random_rows(rng, total * br)
+    poison = rows.copy()
+    lens = 333
+    sel = np.sort(rng.choice(n // br, 17, replace=False)).astype(np.int32)[None]
+    sel[0, 3] = lens // br
+    sel = np.unique(sel)[None]
+    seen = set(O.positions_of(sel[0], br, lens, n))
+    bad = [O.row_of(table, total, br, 1, 0, p) for p in range(n) if p not in seen]
+    bad += [r for r in range(total * br) if r // br not in table]
+    poison[bad, 512:] = 0xFF                                  # NaN scales and position parts
+    poison[bad[::2], 512:528] = np.array([0x7C00] * 8, np.uint16).view(np.uint8)
+    q = dev(rng.standard_normal((1, heads, 576)), torch.bfloat16)
+    res = []
+    for r in (rows, poison):
+        cache = kvo.Cache(rows=dev(r), block_rows=br, table=dev(table))
+        res.append(ctx.attend(cache, q, dev([lens], torch.int32), 0.07, sel=dev(sel), sel_block=br))
+        assert ctx.sync() == kvo.KVO_OK
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    lists = [[rows[O.row_of(table, total, br, 1, 0, p)] for p in sorted(seen)]]
+    check_attend(*res[1], q, 0.07, lists, heads)
+
+
+def test_attend_visible_nan_shows(kvo, ctx):
+    rng = np.random.default_rng(35)
+    rows = random_rows(rng, 300)
+    rows[200, 512:514] = 0xFF
+    cache = kvo.Cache(rows=dev(rows), block_rows=300)
+    q = dev(rng.standard_normal((1, 4, 576)), torch.bfloat16)
+    out, lse = ctx.attend(cache, q, dev([300], torch.int32), 0.07, rows=300)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.isnan(lse).all() and torch.isnan(out[..., :64]).all()
+
+
+def test_attend_bad_pages(kvo, ctx):
+    rng = np.random.default_rng(36)
+    rows = random_rows(rng, 64)
+    table = np.array([[1, -1, 3, 0], [2, 0, 77, 9999]], np.int32)
+    cache = kvo.Cache(rows=dev(rows), block_rows=16, table=dev(table))
+    q = dev(rng.standard_normal((2, 12, 576)), torch.bfloat16)
+    for lens, want in (([64, 60], kvo.KVO_ERANGE), ([16, 32], kvo.KVO_OK), ([0, 0], kvo.KVO_OK)):
+        out, lse = ctx.attend(cache, q, dev(lens, torch.int32), 0.07, rows=64)
+        assert ctx.sync() == want
+        lists = []
+        for t in range(2):
+            at = [O.row_of(table, 4, 16, 2, t, p) for p in range(lens[t])]
+            lists.append([rows[r] for r in at if r is not None])
+        check_attend(out, lse, q, 0.07, lists, 12)
+
+
+def test_attend_strided_queries_and_contiguous_rows(kvo, ctx):
+    rng = np.random.default_rng(37)
+    n, heads = 150, 24
+    rows = random_rows(rng, 3 * n)
+    wide = dev(rng.standard_normal((3, 2 * heads, 584)), torch.bfloat16)
+    q = wide[:, 1::2, 8:]
+    cache = kvo.Cache(rows=dev(rows), block_rows=n)
+    lens = [150, 149, 3]
+    out, lse = ctx.attend(cache, q, dev(lens, torch.int32), 0.07, rows=n)
+    assert ctx.sync() == kvo.KVO_OK
+    check_attend(out, lse, q, 0.07, [list(rows[t * n:t * n + lens[t]]) for t in range(3)], heads)
+
+
+def test_attend_no_positions_at_all(kvo, ctx):
+    rows = torch.zeros(16, 656, dtype=torch.uint8, device="cuda")
+    cache = kvo.Cache(rows=rows, block_rows=16)
+    q = torch.randn(2, 20, 576, device="cuda").bfloat16()[:1]
+    lens = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    empty = torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+    for kw in (dict(rows=0), dict(sel=torch.full((1, 5), -1, dtype=torch.int32, device="cuda")), dict(sel=empty)):
+        out, lse = ctx.attend(cache, q, lens, 0.07, **kw)
+        assert ctx.sync() == kvo.KVO_OK
+        assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_repeated_calls_give_the_same_bits(kvo, ctx):
+    rng = np.random.default_rng(38)
+    rows = dev(random_rows(rng, 6000))
+    cache = kvo.Cache(rows=rows, block_rows=6000)
+    q = dev(rng.standard_normal((1, 64, 576)), torch.bfloat16)
+    lens = dev([6000], torch.int32)
+    first = ctx.attend(cache, q, lens, 0.07, rows=6000)
+    for _ in range(3):
+        again = ctx.attend(cache, q, lens, 0.07, rows=6000)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ------------------------------------------------------------- streams, graphs
+def decode_step(kvo, ctx, st, stream=None):
+    ctx.append_tokens(st["cache"], st["kv"][:, :512], st["kv"][:, 512:], st["pos"], INV_FREQ, key=st["key"],
+                      stream=stream)
+    ctx.index_scores(st["cache"], st["qi"], st["w"], st["lens"], st["n"], out=st["scores"], stream=stream)
+    ctx.select_topk_batch(st["scores"], st["k"], idx=st["idx"], stream=stream)
+    return ctx.attend(st["cache"], st["q"], st["lens"], 0.07, sel=st["idx"], out=st["out"], lse=st["lse"],
+                      work=st["work"], stream=stream)
+
+
+def decode_state(kvo, seed, S=3, n=400, k=96, heads=20):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    blocks = -(-n // 16)
+    table = torch.randperm(S * blocks, generator=g, device="cuda").int().view(S, blocks)
+    rows = torch.zeros(S * blocks * 16, 656, dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(S * blocks * 16, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    st = dict(cache=kvo.Cache(rows=rows, keys=keys, key_scales=torch.zeros(S * blocks * 16, device="cuda"),
+                              block_rows=16, table=table),
+              kv=rand(S, 576).bfloat16(), key=rand(S, 128).bfloat16(),
+              qi=rand(S, 32, 128).to(torch.float8_e4m3fn), w=rand(S, 32), q=rand(S, heads, 576).bfloat16(),
+              pos=torch.full((S,), n - 1, dtype=torch.int32, device="cuda"),
+              lens=torch.full((S,), n, dtype=torch.int32, device="cuda"), n=n, k=k,
+              scores=torch.empty(S, n, device="cuda"), idx=torch.empty(S, k, dtype=torch.int32, device="cuda"),
+              out=torch.empty(S, heads, 512, dtype=torch.bfloat16, device="cuda"),
+              lse=torch.empty(S, heads, device="cuda"), rows=rows)
+    need = kvo.kvo_attend_work_bytes(S, heads, k)
+    st["work"] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    return st, rand
+
+
+def prefill(kvo, ctx, st, rand):
+    S, n = st["lens"].numel(), st["n"]
+    kv, key = rand(S * n, 576).bfloat16(), rand(S * n, 128).bfloat16()
+    seq = torch.arange(S, device="cuda").repeat_interleave(n).int()
+    pos = torch.arange(n, device="cuda").repeat(S).int()
+    ctx.append_tokens(st["cache"], kv[:, :512], kv[:, 512:], pos, INV_FREQ, seq=seq, key=key)
+
+
+def test_side_stream_and_graph_give_the_same_bits(kvo, ctx):
+    st, rand = decode_state(kvo, 41)
+    prefill(kvo, ctx, st, rand)
+    decode_step(kvo, ctx, st)
+    assert ctx.sync() == kvo.KVO_OK
+    want = [st[k].clone() for k in ("rows", "scores", "idx", "out", "lse")]
+    side = torch.cuda.Stream()
+
+    def same():
+        return all(torch.equal(a, st[k]) for a, k in zip(want, ("rows", "scores", "idx", "out", "lse")))
+
+    def spoil():
+        for k in ("scores", "idx", "out", "lse"):
+            st[k].zero_()
+        st["work"].fill_(0xFF)
+        torch.cuda.synchronize()
+
+    spoil()
+    decode_step(kvo, ctx, st, stream=side)
+    side.synchronize()
+    assert same()
+    spoil()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode_step(kvo, ctx, st)
+    for _ in range(2):
+        spoil()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same()
+    assert ctx.sync() == kvo.KVO_OK
+
+
+def test_outputs_made_on_a_given_stream(kvo, ctx):
+    """Outputs and scratch that a call makes itself belong to the stream it is given."""
+    st, rand = decode_state(kvo, 42, n=3000, k=2048)
+    prefill(kvo, ctx, st, rand)
+    decode_step(kvo, ctx, st)
+    assert ctx.sync() == kvo.KVO_OK
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(8):
+        out, lse = ctx.attend(st["cache"], st["q"], st["lens"], 0.07, sel=st["idx"], stream=side)
+        scores = ctx.index_scores(st["cache"], st["qi"], st["w"], st["lens"], st["n"], stream=side)
+    side.synchronize()
+    assert torch.equal(out, st["out"]) and torch.equal(lse, st["lse"]) and torch.equal(scores, st["scores"])
+
+
+# ----------------------------------------------------------- with the rest
+def test_gathered_rows_attend_like_the_pool(kvo):
+    """append -> history -> one decode step's gathered rows -> attend gives what attending in place gives."""
+    n, k, heads = 600, 128, 16
+    c = kvo.Context(1, n, 256)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    kv = torch.randn(n, 576, generator=g, device="cuda").bfloat16()
+    rows = torch.zeros(n, 656, dtype=torch.uint8, device="cuda")
+    flat = kvo.Cache(rows=rows, block_rows=n)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    values = torch.empty(n, 576, dtype=torch.bfloat16, device="cuda")
+    c.append_tokens(flat, kv[:, :512], kv[:, 512:], pos, INV_FREQ, seq=torch.zeros_like(pos), out_bf16=values)
+    c.append_rows(0, rows)
+    scores = torch.randn(n, generator=g, device="cuda")
+    idx = torch.empty(k, dtype=torch.int32, device="cuda")
+    got = torch.empty(k, 656, dtype=torch.uint8, device="cuda")
+    deq = torch.empty(k, 576, dtype=torch.bfloat16, device="cuda")
+    c.decode_layers([dict(layer=0, scores=scores, idx=idx, out_rows=got, out_bf16=deq)], k)
+    q = torch.randn(1, heads, 576, generator=g, device="cuda").bfloat16()
+    a = c.attend(kvo.Cache(rows=got, block_rows=k), q, torch.full((1,), k, dtype=torch.int32, device="cuda"), 0.07, rows=k)
+    b = c.attend(flat, q, torch.full((1,), n, dtype=torch.int32, device="cuda"), 0.07, sel=idx[None])
+    assert c.sync() == kvo.KVO_OK
+    assert torch.equal(deq, values[idx.long()])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_attend(*a, q, 0.07, [list(got.cpu().numpy())], heads)
+    c.close()
+
+
+def test_pool_session_rows(kvo, ctx):
+    """Rows appended into a session's pool blocks are what the pool's own calls read back."""
+    pool = kvo.Pool(layers=2, pool_blocks=20, block_tokens=16, tier_blocks=0)
+    assert pool.alloc(5, 50) == kvo.KVO_OK
+    table = torch.tensor([kvo.kvo_pool_block_table(pool.handle, 5, 1)], dtype=torch.int32, device="cuda")
+    cache = kvo.Cache(rows=pool, table=table)
+    assert cache.block_rows == 16 and cache.blocks == 20
+    kv = torch.randn(50, 576, device="cuda").bfloat16()
+    pos = torch.arange(50, dtype=torch.int32, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], pos, INV_FREQ, seq=torch.zeros_like(pos))
+    flat = torch.zeros(50, 656, dtype=torch.uint8, device="cuda")
+    ctx.append_tokens(kvo.Cache(rows=flat, block_rows=50), kv[:, :512], kv[:, 512:], pos, INV_FREQ,
+                      seq=torch.zeros_like(pos))
+    back = torch.empty(50, 656, dtype=torch.uint8, device="cuda")
+    pool.read(5, 1, 0, back)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.equal(back, flat)
+    pool.close()

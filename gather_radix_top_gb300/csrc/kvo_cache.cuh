@@ -13,6 +13,23 @@
 
 namespace kvo {
 
+// Division of n < 2^31 by a fixed d >= 1 as a product: with s = ceil(log2 d)
+// and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + (n m >> 32)) >> s, and
+// the sum stays below 2^32.
+struct Divider {
+  uint32_t mul, shift;
+};
+
+inline Divider divider(uint32_t d) {
+  uint32_t s = 0;
+  while (((uint64_t)1 << s) < d) ++s;
+  return Divider{(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1), s};
+}
+
+__host__ __device__ __forceinline__ uint32_t divide(uint32_t n, Divider by) {
+  return (n + (uint32_t)((uint64_t)n * by.mul >> 32)) >> by.shift;
+}
+
 // kvo_cache as kernels take it (by value, in the parameter space).
 struct CacheView {
   uint8_t* rows;
@@ -24,12 +41,14 @@ struct CacheView {
   uint32_t block_rows;
   uint32_t table_blocks;
   uint32_t sequences;
+  Divider by_block;          // division by block_rows
 };
 
 inline CacheView cache_view(const kvo_cache& c) {
   return CacheView{static_cast<uint8_t*>(c.rows),  static_cast<uint8_t*>(c.keys), c.key_scales,
                    c.table,                        c.table_ld,                    c.blocks,
-                   (uint32_t)c.block_rows,         (uint32_t)c.table_blocks,      (uint32_t)c.sequences};
+                   (uint32_t)c.block_rows,         (uint32_t)c.table_blocks,      (uint32_t)c.sequences,
+                   divider((uint32_t)c.block_rows)};
 }
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -50,17 +69,26 @@ inline bool cache_keys_ok(const kvo_cache* c) {
   return c->key_type == KVO_E4M3 && c->key_scales && aligned(c->key_scales, 4);
 }
 
-// The cache row of position p (>= 0) of sequence s (< sequences), or -1 where
-// there is none.  Rows are counted in 64 bits: a cache may hold more than
-// 2^31 of them.
-__host__ __device__ __forceinline__ int64_t cache_row(const CacheView& c, uint32_t s, uint32_t p) {
-  const uint32_t b = p / c.block_rows;
-  const uint32_t r = p - b * c.block_rows;
-  if (!c.table) return b == 0 ? (int64_t)s * c.block_rows + r : -1;
-  if (b >= c.table_blocks) return -1;
-  const int32_t id = c.table[(int64_t)s * c.table_ld + b];
+// The block that position p (below 2^31) of sequence s (< sequences) lies in,
+// as the table has it, unchecked; -1 where the table does not reach.  Apart
+// from cache_row_in, so that a loop can ask for the entries of later
+// positions and look at them only when they have come.
+__host__ __device__ __forceinline__ int32_t cache_block(const CacheView& c, uint32_t s, uint32_t p) {
+  const uint32_t b = divide(p, c.by_block);
+  if (!c.table) return b == 0 ? (int32_t)s : -1;
+  return b < c.table_blocks ? c.table[(int64_t)s * c.table_ld + b] : -1;
+}
+
+// The cache row of position p in block `id`, or -1 where there is no such
+// block.  Rows are counted in 64 bits: a cache may hold more than 2^31.
+__host__ __device__ __forceinline__ int64_t cache_row_in(const CacheView& c, int32_t id, uint32_t p) {
   if (id < 0 || id >= c.blocks) return -1;
-  return (int64_t)id * c.block_rows + r;
+  return (int64_t)id * c.block_rows + (p - divide(p, c.by_block) * c.block_rows);
+}
+
+// The cache row of position p of sequence s, or -1 where there is none.
+__host__ __device__ __forceinline__ int64_t cache_row(const CacheView& c, uint32_t s, uint32_t p) {
+  return cache_row_in(c, cache_block(c, s, p), p);
 }
 
 }  // namespace kvo

@@ -581,7 +581,7 @@ kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, const kvo_tok
  * The products and the sum over heads are accumulated in fp32.
  * nq = cache->sequences * per_seq, at most KVO_MAX_QUERIES.  KVO_EINVAL for a NULL or misaligned
  * argument, heads outside 1 .. KVO_MAX_HEADS, per_seq < 1, n < 1, n > 2^31 - 256, ld <
- * ceil(n / block), a bad block or key type, or a cache without keys.
+ * ceil(n / block), a bad block or key type, or a cache without keys or with 2^31 or more.
  */
 typedef struct kvo_score_query {
   const void* q;

@@ -182,11 +182,26 @@ def test_bad_pages_have_no_row(tmp_path):
 #include "kvo_cache.cuh"
 int main() {
   int32_t table[2][4] = {{3, -1, 0, 2147483647}, {99, 7, 100, 5}};
-  kvo::CacheView c = {nullptr, nullptr, nullptr, &table[0][0], 4, 100, 16, 3, 2};
+  kvo::CacheView c = {nullptr, nullptr, nullptr, &table[0][0], 4, 100, 16, 3, 2, kvo::divider(16)};
   for (uint32_t s = 0; s < 2; ++s)
     for (uint32_t p = 0; p < 80; ++p) std::printf("%lld\\n", (long long)kvo::cache_row(c, s, p));
   std::printf("%lld\\n", (long long)kvo::cache_row(c, 1, 2147483647u));
-  kvo::CacheView d = {nullptr, nullptr, nullptr, nullptr, 0, 4000000, 1000, 0, 4000000};
+  kvo::CacheView d = {nullptr, nullptr, nullptr, nullptr, 0, 4000000, 1000, 0, 4000000,
+                      kvo::divider(1000)};
+  uint64_t wrong = 0;
+  const uint32_t around[] = {1, 2, 3, 5, 7, 16, 48, 1000, 12345, 65535, 65536, 99999, 2147483647u};
+  for (uint32_t x : around) {
+    const kvo::Divider by = kvo::divider(x);
+    for (uint64_t k = 0; k < 200000; ++k) {
+      const uint64_t base = k * 10737ull / x * x;
+      for (int64_t e = -1; e <= 1; ++e) {
+        const int64_t n = (int64_t)base + e;
+        if (n >= 0 && n < 2147483648ll) wrong += kvo::divide((uint32_t)n, by) != (uint32_t)n / x;
+      }
+    }
+    wrong += kvo::divide(2147483647u, by) != 2147483647u / x;
+  }
+  std::printf("%llu\\n", (unsigned long long)wrong);
   std::printf("%lld %lld\\n", (long long)kvo::cache_row(d, 3999999, 999), (long long)kvo::cache_row(d, 5, 1000));
 }
 """)
@@ -197,4 +212,4 @@ int main() {
     table = np.array([[3, -1, 0], [99, 7, 100]])
     want = [O.row_of(table, 100, 16, 2, s, p) for s in range(2) for p in range(80)]
     assert got[:160] == [-1 if w is None else w for w in want]
-    assert got[160:] == [-1, 3999999999, -1]
+    assert got[160:] == [-1, 0, 3999999999, -1]

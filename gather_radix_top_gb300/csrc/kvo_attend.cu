@@ -1,15 +1,43 @@
 // kvo_attend: softmax attention of absorbed MLA queries over cached rows.
+//
+// One CTA holds up to 64 heads of one query and walks over tiles of 128 rows
+// of its list.  A tile's 656-byte rows come through registers, are
+// dequantised once to bf16 and written to shared memory; both products then
+// run on the tensor cores with the rows' operand as A:
+//     S^T [128 rows x heads]   = K [128 x 576] Q^T          (K contiguous)
+//     O^T [512 values x heads] += V^T [512 x 128] P^T       (the same bytes, read
+//                                along the other dimension, as 4 x 128 values)
+// With the heads as columns M is full whatever the number of heads, and the
+// accumulators fit: O^T needs 4 x 64 of the 512 columns of tensor memory, which
+// 128 heads by 512 values as rows would fill.  Shared memory holds one tile
+// (144 KB) and the queries (72 KB); P^T takes the place of the position part,
+// which the second product does not read.  Parts of the tile are refilled as
+// the second product releases them, and the next tile's bytes are on their
+// way meanwhile.
+//
+// The softmax is over the lanes of S^T: a maximum per column over the warp's
+// lanes, then over the four warps of a column.  The running maximum moves only
+// when it is exceeded by more than 8 (in powers of two; weights stay below
+// 256), so the accumulators are rarely rescaled.  The sum of the weights stays
+// in registers, per lane, and is reduced once at the end.
+//
+// Long lists with few queries are split over CTAs, whose normalised partial
+// results a second launch joins by their log-sum-exps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "kvo_cache.cuh"
+#include "kvo_tc.cuh"
 
 namespace kvo {
 namespace {
 
-constexpr int kAttendThreads = 256;
-constexpr int kAttendTile = 64;      // rows whose logits are held at a time
-constexpr int kQueryValues = KVO_DEQUANT_VALUES;
+constexpr uint32_t kWorkers = 256;                       // warps 0-7; warp 8 issues the MMAs
+constexpr uint32_t kAttendThreads = kWorkers + 32;
+constexpr uint32_t kRowTile = 128;
+constexpr uint32_t kChunkBytes = kRowTile * 128;         // 64 values of every row of a tile
+constexpr uint32_t kTileBytes = 9 * kChunkBytes;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
   CacheView cache;
@@ -18,85 +46,476 @@ struct AttendArgs {
   const int32_t* sel;
   uint16_t* out;
   float* lse;
+  float* part;               // [splits][queries * heads][512], with several splits
+  float* part_lse;           // [splits][queries * heads], base 2
   uint32_t* status;
   int64_t q_ld, q_head_ld;   // bytes
   int64_t sel_ld;
   uint32_t rows, picked, sel_shift;
-  uint32_t per_seq, heads;
-  float scale;
+  uint32_t per_seq, heads, nq;
+  uint32_t head_tiles, splits;
+  float scale;               // times log2(e)
 };
 
-// The position that entry j of query t's list names, or -1 (masked).
-__device__ __forceinline__ int64_t listed_position(const AttendArgs& a, uint32_t t, uint32_t j, int32_t len) {
-  int64_t p = j;
-  if (a.sel) {
-    const int32_t u = a.sel[t * a.sel_ld + (j >> a.sel_shift)];
-    if (u < 0) return -1;
-    p = ((int64_t)u << a.sel_shift) + (j & ((1u << a.sel_shift) - 1));
+struct AttendShared {
+  uint64_t k_full[5], s_full, p_full, pv_done[4], drained;
+  uint32_t tmem;
+  uint32_t gave_up;
+  int64_t row[2][kRowTile];          // a tile's cache rows, -1: masked
+  float top[2][4][32];               // per half of the columns and warp
+  float column[8][32];               // per warp: one value per column
+};
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Four int8 times a scale as bf16, rounded once.  A byte (plus 128) put into
+// bits 8-15 of the float 32768 makes 32768 + byte; times the scale, minus
+// (32768 + 128) * scale, is the exact product: both have at most 20 bits.
+__device__ __forceinline__ void dequant4(uint32_t bytes, float scale, float bias, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = bytes ^ 0x80808080u;
+  float v[4];
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    v[k] = fmaf(__uint_as_float(__byte_perm(u, 0x47000000u, 0x7504u | k << 4)), scale, bias);
+  lo = bf16_pair(v[0], v[1]);
+  hi = bf16_pair(v[2], v[3]);
+}
+
+// Barrier of the workers that also says whether any of them brings `flag`.
+__device__ __forceinline__ bool workers_any(bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 3, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)flag), "r"(kWorkers)
+      : "memory");
+  return r != 0;
+}
+
+// Sums of kN columns over the warp's lanes: a step with `kBit` halves the
+// columns that a lane keeps, and once one is left adds the lanes' shares.
+// v[0] is then column lane / (32 / kN)'s sum.
+template <uint32_t kN, uint32_t kBit>
+__device__ __forceinline__ void lane_sums(float* v, uint32_t lane) {
+  if constexpr (kN > 1) {
+    const bool up = lane & kBit;
+#pragma unroll
+    for (uint32_t c = 0; c < kN / 2; ++c) {
+      const float keep = up ? v[c + kN / 2] : v[c], give = up ? v[c] : v[c + kN / 2];
+      v[c] = keep + __shfl_xor_sync(0xffffffffu, give, kBit);
+    }
+  } else {
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], kBit);
   }
-  return p < len ? p : -1;
+  if constexpr (kBit > 1) lane_sums<(kN > 1 ? kN / 2 : 1), kBit / 2>(v, lane);
 }
 
-__device__ __forceinline__ float row_value(const uint8_t* row, uint32_t d) {
-  if (d >= KVO_LATENT_BYTES)
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row + KVO_LATENT_BYTES + 16)[d - KVO_LATENT_BYTES]);
-  const float s = __half2float(reinterpret_cast<const __half*>(row + KVO_LATENT_BYTES)[d >> 6]);
-  return __bfloat162float(__float2bfloat16_rn((float)(int8_t)row[d] * s));
+template <uint32_t kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
+  if constexpr (kCols == 32)
+    tmem_ld32(addr, v);
+  else if constexpr (kCols == 16)
+    tmem_ld16(addr, v);
+  else
+    tmem_ld8(addr, v);
 }
 
-// One CTA per (query, head): a running maximum and sum over tiles of rows; a
-// warp per row for the logits, two output values per thread.
-__global__ void __launch_bounds__(kAttendThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float q[kQueryValues];
-  __shared__ float z[kAttendTile];
-  __shared__ int64_t row[kAttendTile];
-  const uint32_t t = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q + t * a.q_ld + h * a.q_head_ld);
-  for (uint32_t d = tid; d < kQueryValues; d += kAttendThreads) q[d] = __bfloat162float(src[d]);
+// kHeads: columns of the CTA, 16, 32 or 64.
+template <uint32_t kHeads>
+__global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr uint32_t kCols = kHeads / 2;                 // of a worker warp
+  constexpr uint32_t kTmemCols = kHeads == 64 ? 512 : kHeads == 32 ? 256 : 128;
+  constexpr uint32_t kScores = 4 * kHeads;               // S^T's first column
+  extern __shared__ uint8_t raw[];
+  __shared__ AttendShared sh;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t t = blockIdx.y, seq = t / a.per_seq;
+  const uint32_t h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
+  const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + kTileBytes;
+  uint8_t* const smem = raw + (tile_at - smem_u32(raw));
+
   const int32_t len = a.lens[t];
-  const uint32_t all = a.sel ? a.picked << a.sel_shift : (uint32_t)(len <= 0 ? 0 : min((uint32_t)len, a.rows));
-  float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-  for (uint32_t j0 = 0; j0 < all; j0 += kAttendTile) {
-    __syncthreads();
-    if (tid < kAttendTile) {
-      const int64_t p = j0 + tid < all ? listed_position(a, t, j0 + tid, len) : -1;
-      const int64_t r = p >= 0 ? cache_row(a.cache, t / a.per_seq, (uint32_t)p) : -1;
-      if (p >= 0 && r < 0) atomicOr(a.status, kFlagRange);
-      row[tid] = r;
+  const uint32_t all = a.sel ? (len > 0 ? a.picked << a.sel_shift : 0u) : len <= 0 ? 0u : min((uint32_t)len, a.rows);
+  const uint32_t tiles_all = (all + kRowTile - 1) / kRowTile, per = (tiles_all + a.splits - 1) / a.splits;
+  const uint32_t first = min(split * per, tiles_all), tiles = min(per, tiles_all - first);
+
+  // this warp's columns: heads h0 + half * kCols + c; its lanes: rows (or
+  // values of O^T) quad * 32 + lane
+  const uint32_t quad = warp & 3, half = (warp >> 2) & 1;
+  const int64_t out_row = (int64_t)t * a.heads + h0 + half * kCols;
+  const uint32_t mine = a.heads > h0 + half * kCols ? min(kCols, a.heads - h0 - half * kCols) : 0;   // real columns
+  float* const part = a.part + ((int64_t)split * a.nq * a.heads + out_row) * KVO_LATENT_BYTES;
+  float* const part_lse = a.part_lse + (int64_t)split * a.nq * a.heads + out_row;
+
+  if (tiles == 0) {
+    if (warp >= 8) return;
+    if (a.splits > 1) {                                  // the join skips it
+      if (quad == 0 && lane < mine) part_lse[lane] = -INFINITY;
+      return;
     }
-    __syncthreads();
-    for (uint32_t j = warp; j < kAttendTile; j += kAttendThreads / 32) {
-      float sum = 0.0f;
-      if (row[j] >= 0) {
-        const uint8_t* r = a.cache.rows + row[j] * KVO_ROW_BYTES;
-        for (uint32_t d = lane; d < kQueryValues; d += 32) sum = fmaf(q[d], row_value(r, d), sum);
+    for (uint32_t c = 0; c < mine; ++c)
+      for (uint32_t d = quad * 32 + lane; d < KVO_LATENT_BYTES; d += 128) a.out[(out_row + c) * KVO_LATENT_BYTES + d] = 0;
+    if (a.lse && quad == 0 && lane < mine) a.lse[out_row + lane] = -INFINITY;
+    return;
+  }
+
+  if (tid == 0) {
+    for (uint32_t i = 0; i < 5; ++i) mbar_init(&sh.k_full[i], kWorkers);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.pv_done[i], 1);
+    mbar_init(&sh.s_full, 1);
+    mbar_init(&sh.p_full, kWorkers);
+    mbar_init(&sh.drained, 1);
+    sh.gave_up = 0;
+  }
+  if (warp == 8) tmem_alloc(&sh.tmem, kTmemCols);
+
+  // Where a tile's rows are: thread r < 128 looks up row r in three steps, one
+  // tile apart, so that no step waits for the one before: the list's entry
+  // (tile i + 3), the table's (i + 2), the row (i + 1).
+  const uint32_t sub = (1u << a.sel_shift) - 1;
+  auto listed = [&](uint32_t i) -> int32_t {             // the list's entry, unchecked
+    const uint32_t j = (first + i) * kRowTile + tid;
+    if (i >= tiles || j >= all) return -1;
+    return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
+  };
+  auto position = [&](uint32_t i, int32_t unit) -> int32_t {   // or -1: masked
+    const int64_t p = ((int64_t)unit << (a.sel ? a.sel_shift : 0u)) + (a.sel ? ((first + i) * kRowTile + tid) & sub : 0u);
+    return unit >= 0 && p < len ? (int32_t)p : -1;
+  };
+  auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
+  auto row_of = [&](int32_t p, int32_t block) -> int64_t {
+    if (p < 0) return -1;
+    const int64_t r = cache_row_in(a.cache, block, (uint32_t)p);
+    if (r < 0) atomicOr(a.status, kFlagRange);
+    return r;
+  };
+  int32_t unit_after = -1, pos_next = -1, block_next = -1;
+  if (tid < kRowTile) {
+    const int32_t u0 = listed(0), u1 = listed(1);
+    unit_after = listed(2);
+    const int32_t p0 = position(0, u0);
+    const int32_t b0 = block_of(p0);
+    pos_next = position(1, u1);
+    block_next = block_of(pos_next);
+    sh.row[0][tid] = row_of(p0, b0);
+  }
+
+  // the queries: heads past the last are zeros
+  for (uint32_t i = tid; i < kHeads * 72; i += kAttendThreads) {
+    const uint32_t r = i / 72, c = i - r * 72;
+    const bool real = h0 + r < a.heads;
+    copy16_async(queries + (c >> 3) * (kHeads * 128) + swizzled(r, c & 7),
+                 real ? a.q + t * a.q_ld + (h0 + r) * a.q_head_ld + c * 16 : a.q, real);
+  }
+  copy_async_commit();
+  copy_async_wait<0>();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp < 8) {
+    // A thread's part of a tile: 16-byte piece `piece` (of each 128 latent
+    // bytes) of rows slot + 32 u.  A warp reads 128 consecutive bytes of four
+    // rows at a time; the eight lanes of a store phase hold an even and an odd
+    // row, whose swizzled pieces fall into different banks.
+    const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3);
+    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1);
+    // rows 32 apart have the same swizzle: everything else is a fixed offset
+    uint8_t* const to = smem + (piece >> 2) * kChunkBytes;
+    uint8_t* const to_lo = to + swizzled(slot, 2 * (piece & 3));
+    uint8_t* const to_hi = to + swizzled(slot, 2 * (piece & 3) + 1);
+    uint8_t* const to_rope = smem + 8 * kChunkBytes + swizzled(slot, piece);
+    uint4 lat[4][4], rope[4], scales[4];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load_latent = [&](uint32_t b) {
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        const int64_t r = sh.row[b][slot + 32 * u];
+        const uint8_t* p = a.cache.rows + (r < 0 ? 0 : r) * KVO_ROW_BYTES + 16 * piece;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) lat[j][u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + 128 * j)) : zero;
       }
-      for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      if (lane == 0) z[j] = row[j] >= 0 ? sum * a.scale : -INFINITY;
+    };
+    auto load_rest = [&](uint32_t b) {
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        const int64_t r = sh.row[b][slot + 32 * u];
+        const uint8_t* p = a.cache.rows + (r < 0 ? 0 : r) * KVO_ROW_BYTES + KVO_LATENT_BYTES;
+        scales[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : zero;
+        rope[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + 16 + 16 * piece)) : zero;
+      }
+    };
+    load_latent(0);
+    load_rest(0);
+
+    float top = -INFINITY;                               // lane c < kCols: the running maximum of column c
+    float sum[kCols];
+#pragma unroll
+    for (uint32_t c = 0; c < kCols; ++c) sum[c] = 0.0f;
+    const uint32_t lanes = tmem + (quad << 21);          // (quad * 32) << 16
+
+    for (uint32_t i = 0; i < tiles; ++i) {
+      const uint32_t turn = i & 1;
+      // the tile, part by part, as the products of the last tile release it
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+          const uint32_t two = j == 0 ? scales[u].x : j == 1 ? scales[u].y : j == 2 ? scales[u].z : scales[u].w;
+          const float s = __half2float(__ushort_as_half((uint16_t)(piece >= 4 ? two >> 16 : two & 0xffffu)));
+          const float bias = -32896.0f * s;
+          uint4 x, y;
+          dequant4(lat[j][u].x, s, bias, x.x, x.y);
+          dequant4(lat[j][u].y, s, bias, x.z, x.w);
+          dequant4(lat[j][u].z, s, bias, y.x, y.y);
+          dequant4(lat[j][u].w, s, bias, y.z, y.w);
+          *reinterpret_cast<uint4*>(to_lo + 2 * j * kChunkBytes + u * 4096) = x;
+          *reinterpret_cast<uint4*>(to_hi + 2 * j * kChunkBytes + u * 4096) = y;
+        }
+        mbar_arrive(&sh.k_full[j]);
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(to_rope + u * 4096) = rope[u];
+      mbar_arrive(&sh.k_full[4]);
+
+      // the next tile's rows, and its bytes on their way
+      if (tid < kRowTile) {
+        sh.row[turn ^ 1][tid] = row_of(pos_next, block_next);
+        pos_next = position(i + 2, unit_after);
+        block_next = block_of(pos_next);
+        unit_after = listed(i + 3);
+      }
+      if (workers_any(*(volatile uint32_t*)&sh.gave_up != 0)) break;
+      if (i + 1 < tiles) load_latent(turn ^ 1);
+
+      // softmax: this thread has row quad * 32 + lane against kCols heads
+      wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
+      __syncwarp();
+      tc_fence_after();
+      float s[kCols];
+      tmem_ld_cols<kCols>(lanes + kScores + half * kCols, s);
+      const bool there = sh.row[turn][quad * 32 + lane] >= 0;
+      tmem_ld_wait();
+      float best = -INFINITY;
+#pragma unroll
+      for (uint32_t c = 0; c < kCols; ++c) {
+        s[c] = there ? s[c] * a.scale : -INFINITY;
+        float m;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(s[c]));
+        if (lane == c) best = m;
+      }
+      if (lane < kCols) sh.top[half][quad][lane] = best;
+      named_sync(1 + half, 128);
+      float alpha = 1.0f;
+      if (lane < kCols) {
+        best = fmaxf(fmaxf(sh.top[half][0][lane], sh.top[half][1][lane]),
+                     fmaxf(sh.top[half][2][lane], sh.top[half][3][lane]));
+        if (best > top + 8.0f || (top == -INFINITY && best > top)) {
+          alpha = exp2_approx(top - best);               // 0 from -inf
+          top = best;
+        }
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.0f) && i > 0) {
+        sh.column[warp][lane] = alpha;
+        __syncwarp();
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll
+          for (uint32_t c = 0; c < kCols; c += 8) {
+            float o[8];
+            tmem_ld8(lanes + j * kHeads + half * kCols + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) o[e] *= sh.column[warp][c + e];
+            tmem_st8(lanes + j * kHeads + half * kCols + c, o);
+          }
+#pragma unroll
+        for (uint32_t c = 0; c < kCols; ++c) sum[c] *= sh.column[warp][c];
+        tmem_st_wait();
+        __syncwarp();
+      }
+      sh.column[warp][lane] = top == -INFINITY ? 0.0f : top;
+      __syncwarp();
+      uint32_t p[kCols / 2];
+#pragma unroll
+      for (uint32_t c = 0; c < kCols; c += 2) {
+        const float p0 = exp2_approx(s[c] - sh.column[warp][c]), p1 = exp2_approx(s[c + 1] - sh.column[warp][c + 1]);
+        sum[c] += p0;
+        sum[c + 1] += p1;
+        p[c / 2] = bf16_pair(p0, p1);
+      }
+#pragma unroll
+      for (uint32_t c = 0; c < kCols / 8; ++c)
+        *reinterpret_cast<uint4*>(smem + 8 * kChunkBytes + swizzled(quad * 32 + lane, half * (kCols / 8) + c)) =
+            make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+      tc_fence_before();
+      mbar_arrive(&sh.p_full);
+      // (later than the latent: registers are free again)
+      if (i + 1 < tiles) load_rest(turn ^ 1);
     }
-    __syncthreads();
-    float top = m;
-    for (uint32_t j = 0; j < kAttendTile; ++j) top = fmaxf(top, z[j]);
-    if (top == -INFINITY) continue;
-    const float keep = expf(m - top);
-    m = top;
-    l *= keep;
-    o0 *= keep;
-    o1 *= keep;
-    for (uint32_t j = 0; j < kAttendTile; ++j) {
-      if (row[j] < 0) continue;
-      const uint8_t* r = a.cache.rows + row[j] * KVO_ROW_BYTES;
-      const float p = expf(z[j] - m);
-      l += p;
-      o0 = fmaf(p, row_value(r, tid), o0);
-      o1 = fmaf(p, row_value(r, tid + kAttendThreads), o1);
+
+    lane_sums<kCols, 16>(sum, lane);
+    named_sync(1 + half, 128);                           // sh.top is free again
+    if (lane % (32 / kCols) == 0) sh.top[half][quad][lane / (32 / kCols)] = sum[0];
+    named_sync(1 + half, 128);
+    float total = 0.0f;
+    if (lane < kCols)
+      total = (sh.top[half][0][lane] + sh.top[half][1][lane]) + (sh.top[half][2][lane] + sh.top[half][3][lane]);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float lse2 = total == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) + log2f(total);
+    if (quad == 0 && lane < mine) {
+      if (a.splits > 1)
+        part_lse[lane] = lse2;
+      else if (a.lse)
+        a.lse[out_row + lane] = lse2 * 0.6931471805599453f;
+    }
+    __syncwarp();
+    sh.column[warp][lane] = inv;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+      wait_or_give_up(&sh.pv_done[j], (tiles - 1) & 1, &sh.gave_up);
+      __syncwarp();
+      tc_fence_after();
+      float o[kCols];
+      tmem_ld_cols<kCols>(lanes + j * kHeads + half * kCols, o);
+      tmem_ld_wait();
+      const uint32_t d = j * 128 + quad * 32 + lane;
+      if (a.splits > 1) {
+#pragma unroll
+        for (uint32_t c = 0; c < kCols; ++c)
+          if (c < mine) part[c * KVO_LATENT_BYTES + d] = o[c] * sh.column[warp][c];
+      } else {
+#pragma unroll
+        for (uint32_t c = 0; c < kCols; ++c)
+          if (c < mine)
+            reinterpret_cast<__nv_bfloat16*>(a.out)[(out_row + c) * KVO_LATENT_BYTES + d] =
+                __float2bfloat16_rn(o[c] * sh.column[warp][c]);
+      }
+    }
+  } else if (lane == 0) {
+    constexpr uint32_t kQk = mma_desc(1, kHeads, false, false), kPv = mma_desc(1, kHeads, true, true);
+    const uint64_t keys = tile_desc(tile_at, 16), heads = tile_desc(queries, 16);
+    const uint64_t values = tile_desc(tile_at, kChunkBytes), weights = tile_desc(tile_at + 8 * kChunkBytes, kChunkBytes);
+    bool ok = true;
+    for (uint32_t i = 0; i < tiles && ok; ++i) {
+      const uint32_t turn = i & 1;
+      // S^T: 64 values of K and Q at a time, four steps of 16
+#pragma unroll
+      for (uint32_t c = 0; c < 9 && ok; ++c) {
+        if (c % 2 == 0) {
+          ok = wait_or_give_up(&sh.k_full[c / 2], turn, &sh.gave_up);
+          if (!ok) break;
+          fence_proxy_async_smem();                      // the workers' stores, before the MMAs read them
+          tc_fence_after();
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          mma_bf16(tmem + kScores, keys + c * (kChunkBytes >> 4) + 2 * k, heads + c * (kHeads * 128 >> 4) + 2 * k, kQk,
+                   c + k > 0);
+      }
+      if (!ok) break;
+      mma_commit(&sh.s_full);
+      ok = wait_or_give_up(&sh.p_full, turn, &sh.gave_up);
+      if (!ok) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      // O^T: 128 values at a time, eight steps of 16 rows (2,048 bytes)
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+          mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
+                   i + k > 0);
+        mma_commit(&sh.pv_done[j]);
+      }
+    }
+    if (!ok) {
+      // let the MMAs in flight finish before their memory is given back
+      mma_commit(&sh.drained);
+      atomicOr(a.status, kFlagTimeout);
+      if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
     }
   }
-  const float inv = l > 0.0f || isnan(l) ? 1.0f / l : 0.0f;
-  uint16_t* out = a.out + ((int64_t)t * a.heads + h) * KVO_LATENT_BYTES;
-  reinterpret_cast<__nv_bfloat16*>(out)[tid] = __float2bfloat16_rn(o0 * inv);
-  reinterpret_cast<__nv_bfloat16*>(out)[tid + kAttendThreads] = __float2bfloat16_rn(o1 * inv);
-  if (a.lse && tid == 0) a.lse[(int64_t)t * a.heads + h] = l == 0.0f ? -INFINITY : m + logf(l);
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
+  __syncwarp();
+  if (warp == 8) tmem_free(tmem, kTmemCols);
+}
+
+// Joins the splits of one (query, head): their results weighted by
+// exp2(lse - the joint lse).  128 threads, four values each.
+__global__ void __launch_bounds__(128) join_kernel(const float* part, const float* part_lse, uint32_t splits,
+                                                   int64_t rows, uint16_t* out, float* lse) {
+  const int64_t r = blockIdx.x;
+  const uint32_t tid = threadIdx.x;
+  float top = -INFINITY;
+  for (uint32_t s = 0; s < splits; ++s) top = fmaxf(top, part_lse[s * rows + r]);
+  float total = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float base = top == -INFINITY ? 0.0f : top;
+  for (uint32_t s = 0; s < splits; ++s) {
+    const float l = part_lse[s * rows + r];
+    if (l == -INFINITY) continue;                        // nothing there, and nothing was written
+    const float w = exp2f(l - base);
+    const float4 v = *reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * tid);
+    total += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[tid] =
+      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+  if (lse && tid == 0) lse[r] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+}
+
+// How a call is cut: columns per CTA and splits of every list.
+struct Cut {
+  uint32_t heads, head_tiles, splits;
+};
+
+Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
+  Cut c;
+  c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
+  c.head_tiles = (heads + c.heads - 1) / c.heads;
+  const int64_t tiles = (positions + kRowTile - 1) / kRowTile, ctas = nq * c.head_tiles, sms = device_sms();
+  int64_t splits = ctas >= sms ? 1 : sms / ctas;
+  if (splits > tiles) splits = tiles;
+  c.splits = (uint32_t)(splits < 1 ? 1 : splits);
+  return c;
+}
+
+template <uint32_t kHeads>
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
+  constexpr size_t smem = 1024 + kTileBytes + 9 * kHeads * 128;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!ready[dev & 63]) {
+    e = cudaFuncSetAttribute(attend_kernel<kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready[dev & 63] = true;
+  }
+  attend_kernel<kHeads><<<dim3(a.head_tiles * a.splits, a.nq), kAttendThreads, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -105,7 +524,8 @@ __global__ void __launch_bounds__(kAttendThreads) attend_kernel(const __grid_con
 extern "C" int64_t kvo_attend_work_bytes(int64_t nq, int32_t heads, int64_t positions) {
   if (nq < 1 || nq > KVO_MAX_QUERIES || heads < 1 || heads > KVO_MAX_HEADS || positions < 0 || positions > INT32_MAX - 255)
     return -1;
-  return 0;
+  const kvo::Cut c = kvo::cut_of(nq, (uint32_t)heads, positions);
+  return c.splits == 1 ? 0 : (int64_t)c.splits * nq * heads * (KVO_LATENT_BYTES + 1) * 4;
 }
 
 extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo_attend_query* s, void* stream) {
@@ -141,8 +561,20 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
   while ((1 << a.sel_shift) < s->sel_block) ++a.sel_shift;
   a.per_seq = (uint32_t)s->per_seq;
   a.heads = (uint32_t)s->heads;
-  a.scale = s->scale;
-  const dim3 grid((unsigned)s->heads, (unsigned)nq);
-  attend_kernel<<<grid, kAttendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KVO_OK : KVO_ECUDA;
+  a.nq = (uint32_t)nq;
+  a.scale = s->scale * kLog2e;
+  const Cut cut = cut_of(nq, a.heads, positions);
+  a.head_tiles = cut.head_tiles;
+  a.splits = cut.splits;
+  a.part = static_cast<float*>(s->work);
+  a.part_lse = a.part + (int64_t)a.splits * nq * a.heads * KVO_LATENT_BYTES;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cut.heads == 16   ? launch_attend<16>(a, on)
+                  : cut.heads == 32 ? launch_attend<32>(a, on)
+                                    : launch_attend<64>(a, on);
+  if (e == cudaSuccess && a.splits > 1) {
+    join_kernel<<<(unsigned)(nq * a.heads), 128, 0, on>>>(a.part, a.part_lse, a.splits, nq * a.heads, a.out, a.lse);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -78,15 +78,6 @@ struct ScoreShared {
   float w[kScoreMaxCols];
 };
 
-// Waits for a phase that work in flight completes, whether or not other
-// waits have given up; false after the same bounded time.
-__device__ __forceinline__ bool landed(uint64_t* bar, uint32_t parity) {
-  const long long start = clock64();
-  while (!mbar_test(bar, parity))
-    if (clock64() - start > kWaitClocks) return false;
-  return true;
-}
-
 template <bool kF8>
 __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __grid_constant__ ScoreArgs a,
                                                                         const __grid_constant__ CUtensorMap map) {

@@ -142,6 +142,15 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, 
   }
 }
 
+// Waits for a phase that work in flight completes, whether or not other
+// waits have given up; false after the same bounded time.
+__device__ __forceinline__ bool landed(uint64_t* bar, uint32_t parity) {
+  const long long start = clock64();
+  while (!mbar_test(bar, parity))
+    if (clock64() - start > kWaitClocks) return false;
+  return true;
+}
+
 // 16 bytes from global to shared memory without a register; zeros if !take.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool take) {
   const uint32_t bytes = take ? 16u : 0u;

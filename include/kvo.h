@@ -605,7 +605,7 @@ kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, const kvo_scor
  *     z_j = scale * (q[0..512) . latent_j + q[512..576) . rope_j)
  *     out = sum_j softmax(z)_j * latent_j,  lse = log sum_j exp(z_j)
  * where latent_j and rope_j are the bf16 values a row stands for (the
- * out_bf16 of kvo_resolve_gather).  Query t (of sequence t / per_seq)
+ * out_bf16 of kvo_resolve_gather; an infinite scale reads as NaN).  Query t (of sequence t / per_seq)
  * attends to positions below lens[t]:
  *   sel NULL   all of them, positions [0, min(lens[t], rows));
  *   sel        device int32, query t's list of `picked` entries at

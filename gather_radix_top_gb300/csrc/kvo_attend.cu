@@ -32,11 +32,23 @@
 namespace kvo {
 namespace {
 
-constexpr uint32_t kWorkers = 256;                       // warps 0-7; warp 8 issues the MMAs
-constexpr uint32_t kAttendThreads = kWorkers + 32;
-constexpr uint32_t kRowTile = 128;
-constexpr uint32_t kChunkBytes = kRowTile * 128;         // 64 values of every row of a tile
-constexpr uint32_t kTileBytes = 9 * kChunkBytes;
+constexpr uint32_t kWorkers = 256;                       // warps 0-7; warp 8 issues the MMAs, warp 9 loads
+constexpr uint32_t kAttendThreads = kWorkers + 64;
+constexpr uint32_t kPitch = 704;                         // of a raw row: an even and an odd row's halves of a store
+                                                         // phase fall into different banks
+
+// kHeads: columns of a CTA, 16, 32 or 64.
+template <uint32_t kHeads>
+struct AttendShape {
+  // rows of a tile: what the queries leave room for, raw and dequantised
+  static constexpr uint32_t kRows = kHeads == 64 ? 80 : kHeads == 32 ? 96 : 112;
+  static constexpr uint32_t kGroups = (kRows + 31) / 32;           // of 32 rows, the last one maybe half
+  static constexpr uint32_t kChunkBytes = kRows * 128;             // 64 values of every row
+  static constexpr uint32_t kTileBytes = 9 * kChunkBytes;
+  static constexpr uint32_t kQueryBytes = 9 * kHeads * 128;
+  static constexpr uint32_t kSmem = 1024 + kTileBytes + kQueryBytes + kRows * kPitch;
+  static constexpr uint32_t kTmemCols = kHeads == 64 ? 512 : kHeads == 32 ? 256 : 128;
+};
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -59,9 +71,10 @@ struct AttendArgs {
 
 struct AttendShared {
   uint64_t k_full[5], s_full, p_full, pv_done[4], drained;
+  uint64_t raw_full[4], raw_empty[4];
   uint32_t tmem;
   uint32_t gave_up;
-  int64_t row[2][kRowTile];          // a tile's cache rows, -1: masked
+  uint32_t there[2][4];              // tile i's rows that are not masked, in i % 2: a bit per row of a group
   float top[2][4][32];               // per half of the columns and warp
   float column[8][32];               // per warp: one value per column
 };
@@ -91,13 +104,14 @@ __device__ __forceinline__ void dequant4(uint32_t bytes, float scale, float bias
   hi = bf16_pair(v[2], v[3]);
 }
 
-// Barrier of the workers that also says whether any of them brings `flag`.
-__device__ __forceinline__ bool workers_any(bool flag) {
+// Barrier of the 128 threads of a half that also says whether any of them
+// brings `flag`.
+__device__ __forceinline__ bool half_sync_any(uint32_t half, bool flag) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 3, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)flag), "r"(kWorkers)
+      : "r"((uint32_t)flag), "r"(1 + half)
       : "memory");
   return r != 0;
 }
@@ -130,23 +144,23 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
     tmem_ld8(addr, v);
 }
 
-// kHeads: columns of the CTA, 16, 32 or 64.
 template <uint32_t kHeads>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
   constexpr uint32_t kCols = kHeads / 2;                 // of a worker warp
-  constexpr uint32_t kTmemCols = kHeads == 64 ? 512 : kHeads == 32 ? 256 : 128;
+  using S = AttendShape<kHeads>;
+  constexpr uint32_t kRows = S::kRows, kChunkBytes = S::kChunkBytes;
   constexpr uint32_t kScores = 4 * kHeads;               // S^T's first column
   extern __shared__ uint8_t raw[];
   __shared__ AttendShared sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t t = blockIdx.y, seq = t / a.per_seq;
   const uint32_t h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
-  const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + kTileBytes;
+  const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes, stage = queries + S::kQueryBytes;
   uint8_t* const smem = raw + (tile_at - smem_u32(raw));
 
   const int32_t len = a.lens[t];
   const uint32_t all = a.sel ? (len > 0 ? a.picked << a.sel_shift : 0u) : len <= 0 ? 0u : min((uint32_t)len, a.rows);
-  const uint32_t tiles_all = (all + kRowTile - 1) / kRowTile, per = (tiles_all + a.splits - 1) / a.splits;
+  const uint32_t tiles_all = (all + kRows - 1) / kRows, per = (tiles_all + a.splits - 1) / a.splits;
   const uint32_t first = min(split * per, tiles_all), tiles = min(per, tiles_all - first);
 
   // this warp's columns: heads h0 + half * kCols + c; its lanes: rows (or
@@ -175,40 +189,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     mbar_init(&sh.s_full, 1);
     mbar_init(&sh.p_full, kWorkers);
     mbar_init(&sh.drained, 1);
+    for (uint32_t u = 0; u < S::kGroups; ++u) {
+      mbar_init(&sh.raw_full[u], 1);
+      mbar_init(&sh.raw_empty[u], kWorkers);
+    }
     sh.gave_up = 0;
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, kTmemCols);
-
-  // Where a tile's rows are: thread r < 128 looks up row r in three steps, one
-  // tile apart, so that no step waits for the one before: the list's entry
-  // (tile i + 3), the table's (i + 2), the row (i + 1).
-  const uint32_t sub = (1u << a.sel_shift) - 1;
-  auto listed = [&](uint32_t i) -> int32_t {             // the list's entry, unchecked
-    const uint32_t j = (first + i) * kRowTile + tid;
-    if (i >= tiles || j >= all) return -1;
-    return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
-  };
-  auto position = [&](uint32_t i, int32_t unit) -> int32_t {   // or -1: masked
-    const int64_t p = ((int64_t)unit << (a.sel ? a.sel_shift : 0u)) + (a.sel ? ((first + i) * kRowTile + tid) & sub : 0u);
-    return unit >= 0 && p < len ? (int32_t)p : -1;
-  };
-  auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
-  auto row_of = [&](int32_t p, int32_t block) -> int64_t {
-    if (p < 0) return -1;
-    const int64_t r = cache_row_in(a.cache, block, (uint32_t)p);
-    if (r < 0) atomicOr(a.status, kFlagRange);
-    return r;
-  };
-  int32_t unit_after = -1, pos_next = -1, block_next = -1;
-  if (tid < kRowTile) {
-    const int32_t u0 = listed(0), u1 = listed(1);
-    unit_after = listed(2);
-    const int32_t p0 = position(0, u0);
-    const int32_t b0 = block_of(p0);
-    pos_next = position(1, u1);
-    block_next = block_of(pos_next);
-    sh.row[0][tid] = row_of(p0, b0);
-  }
+  if (warp == 8) tmem_alloc(&sh.tmem, S::kTmemCols);
 
   // the queries: heads past the last are zeros
   for (uint32_t i = tid; i < kHeads * 72; i += kAttendThreads) {
@@ -237,28 +224,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     uint8_t* const to_lo = to + swizzled(slot, 2 * (piece & 3));
     uint8_t* const to_hi = to + swizzled(slot, 2 * (piece & 3) + 1);
     uint8_t* const to_rope = smem + 8 * kChunkBytes + swizzled(slot, piece);
-    uint4 lat[4][4], rope[4], scales[4];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto load_latent = [&](uint32_t b) {
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u) {
-        const int64_t r = sh.row[b][slot + 32 * u];
-        const uint8_t* p = a.cache.rows + (r < 0 ? 0 : r) * KVO_ROW_BYTES + 16 * piece;
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) lat[j][u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + 128 * j)) : zero;
-      }
-    };
-    auto load_rest = [&](uint32_t b) {
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u) {
-        const int64_t r = sh.row[b][slot + 32 * u];
-        const uint8_t* p = a.cache.rows + (r < 0 ? 0 : r) * KVO_ROW_BYTES + KVO_LATENT_BYTES;
-        scales[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : zero;
-        rope[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + 16 + 16 * piece)) : zero;
-      }
-    };
-    load_latent(0);
-    load_rest(0);
+    const uint8_t* const from = smem + (stage - tile_at) + slot * kPitch + 16 * piece;
+    uint4 lat[4][S::kGroups], rope[S::kGroups], scales[S::kGroups];
 
     float top = -INFINITY;                               // lane c < kCols: the running maximum of column c
     float sum[kCols];
@@ -268,12 +235,33 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     for (uint32_t i = 0; i < tiles; ++i) {
       const uint32_t turn = i & 1;
-      // the tile, part by part, as the products of the last tile release it
+      // the raw rows, while the second product of the last tile runs; a masked
+      // row becomes zeros
+#pragma unroll
+      for (uint32_t u = 0; u < S::kGroups; ++u) {
+        wait_or_give_up(&sh.raw_full[u], turn, &sh.gave_up);
+        if (slot + 32 * u < kRows) {
+          const uint8_t* p = from + u * (32 * kPitch);
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) lat[j][u] = *reinterpret_cast<const uint4*>(p + 128 * j);
+          scales[u] = *reinterpret_cast<const uint4*>(p - 16 * piece + KVO_LATENT_BYTES);
+          rope[u] = *reinterpret_cast<const uint4*>(p + KVO_LATENT_BYTES + 16);
+          if (!(sh.there[turn][u] >> slot & 1)) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) lat[j][u] = zero;
+            scales[u] = rope[u] = zero;
+          }
+        }
+        mbar_arrive(&sh.raw_empty[u]);
+      }
+      // dequantised, part by part, as the products of the last tile release it
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
         if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
 #pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {
+        for (uint32_t u = 0; u < S::kGroups; ++u) {
+          if (slot + 32 * u >= kRows) break;
           const uint32_t two = j == 0 ? scales[u].x : j == 1 ? scales[u].y : j == 2 ? scales[u].z : scales[u].w;
           const float s = __half2float(__ushort_as_half((uint16_t)(piece >= 4 ? two >> 16 : two & 0xffffu)));
           const float bias = -32896.0f * s;
@@ -288,19 +276,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         mbar_arrive(&sh.k_full[j]);
       }
 #pragma unroll
-      for (uint32_t u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4*>(to_rope + u * 4096) = rope[u];
+      for (uint32_t u = 0; u < S::kGroups; ++u)
+        if (slot + 32 * u < kRows) *reinterpret_cast<uint4*>(to_rope + u * 4096) = rope[u];
       mbar_arrive(&sh.k_full[4]);
-
-      // the next tile's rows, and its bytes on their way
-      if (tid < kRowTile) {
-        sh.row[turn ^ 1][tid] = row_of(pos_next, block_next);
-        pos_next = position(i + 2, unit_after);
-        block_next = block_of(pos_next);
-        unit_after = listed(i + 3);
-      }
-      if (workers_any(*(volatile uint32_t*)&sh.gave_up != 0)) break;
-      if (i + 1 < tiles) load_latent(turn ^ 1);
 
       // softmax: this thread has row quad * 32 + lane against kCols heads
       wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
@@ -308,7 +286,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       tc_fence_after();
       float s[kCols];
       tmem_ld_cols<kCols>(lanes + kScores + half * kCols, s);
-      const bool there = sh.row[turn][quad * 32 + lane] >= 0;
+      const bool there = quad * 32 + lane < kRows && (sh.there[turn][quad] >> lane & 1);
       tmem_ld_wait();
       float best = -INFINITY;
 #pragma unroll
@@ -319,7 +297,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (lane == c) best = m;
       }
       if (lane < kCols) sh.top[half][quad][lane] = best;
-      named_sync(1 + half, 128);
+      if (half_sync_any(half, *(volatile uint32_t*)&sh.gave_up != 0)) break;
       float alpha = 1.0f;
       if (lane < kCols) {
         best = fmaxf(fmaxf(sh.top[half][0][lane], sh.top[half][1][lane]),
@@ -358,14 +336,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         sum[c + 1] += p1;
         p[c / 2] = bf16_pair(p0, p1);
       }
+      if (quad * 32 + lane < kRows)
 #pragma unroll
       for (uint32_t c = 0; c < kCols / 8; ++c)
         *reinterpret_cast<uint4*>(smem + 8 * kChunkBytes + swizzled(quad * 32 + lane, half * (kCols / 8) + c)) =
             make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
       tc_fence_before();
       mbar_arrive(&sh.p_full);
-      // (later than the latent: registers are free again)
-      if (i + 1 < tiles) load_rest(turn ^ 1);
     }
 
     lane_sums<kCols, 16>(sum, lane);
@@ -407,6 +384,74 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 __float2bfloat16_rn(o[c] * sh.column[warp][c]);
       }
     }
+  } else if (warp == 9) {
+    // Lane l brings row l of every group of 32.  Where it is, is looked up in
+    // three steps, one tile apart, so that none waits for the one before: the
+    // list's entry (tile i + 3), the table's (i + 2), the row (i + 1).
+    const uint32_t sub = (1u << a.sel_shift) - 1;
+    auto entry = [&](uint32_t i, uint32_t u) -> uint32_t { return (first + i) * kRows + 32 * u + lane; };
+    auto listed = [&](uint32_t i, uint32_t u) -> int32_t {       // the list's entry, unchecked
+      const uint32_t j = entry(i, u);
+      if (i >= tiles || j >= all || 32 * u + lane >= kRows) return -1;
+      return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
+    };
+    auto position = [&](uint32_t i, uint32_t u, int32_t unit) -> int32_t {   // or -1: masked
+      const int64_t p = a.sel ? ((int64_t)unit << a.sel_shift) + (entry(i, u) & sub) : (int64_t)unit;
+      return unit >= 0 && p < len ? (int32_t)p : -1;
+    };
+    auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
+    auto row_of = [&](int32_t p, int32_t block) -> int64_t {
+      if (p < 0) return -1;
+      const int64_t r = cache_row_in(a.cache, block, (uint32_t)p);
+      if (r < 0) atomicOr(a.status, kFlagRange);
+      return r;
+    };
+    int32_t unit[S::kGroups], pos[S::kGroups], block[S::kGroups];
+    int64_t row[S::kGroups];
+#pragma unroll
+    for (uint32_t u = 0; u < S::kGroups; ++u) {
+      unit[u] = listed(0, u);
+      pos[u] = listed(1, u);
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < S::kGroups; ++u) {
+      const int32_t p0 = position(0, u, unit[u]);
+      pos[u] = position(1, u, pos[u]);
+      block[u] = block_of(pos[u]);
+      row[u] = row_of(p0, block_of(p0));
+      unit[u] = listed(2, u);
+    }
+    bool ok = true;
+    uint32_t i = 0;
+    for (; i < tiles; ++i) {
+#pragma unroll
+      for (uint32_t u = 0; u < S::kGroups; ++u) {
+        ok = ok && (i == 0 || wait_or_give_up(&sh.raw_empty[u], (i - 1) & 1, &sh.gave_up));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t there = __ballot_sync(0xffffffffu, row[u] >= 0);
+        if (lane == 0) {
+          sh.there[i & 1][u] = there;
+          mbar_arrive_expect_tx(&sh.raw_full[u], __popc(there) * KVO_ROW_BYTES);
+        }
+        __syncwarp();
+        if (row[u] >= 0)
+          bulk_copy_g2s(smem + (stage - tile_at) + (32 * u + lane) * kPitch, a.cache.rows + row[u] * KVO_ROW_BYTES,
+                        KVO_ROW_BYTES, &sh.raw_full[u]);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (uint32_t u = 0; u < S::kGroups; ++u) {
+        row[u] = row_of(pos[u], block[u]);
+        pos[u] = position(i + 2, u, unit[u]);
+        block[u] = block_of(pos[u]);
+        unit[u] = listed(i + 3, u);
+      }
+    }
+    // where the CTA gives up, the copies in flight finish before it ends
+    if (!ok && i > 0)
+      for (uint32_t u = 0; u < S::kGroups; ++u)
+        if (!landed(&sh.raw_full[u], (i - 1) & 1) && !mbar_test(&sh.raw_full[u], i & 1)) atomicOr(a.status, kFlagInflight);
   } else if (lane == 0) {
     constexpr uint32_t kQk = mma_desc(1, kHeads, false, false), kPv = mma_desc(1, kHeads, true, true);
     const uint64_t keys = tile_desc(tile_at, 16), heads = tile_desc(queries, 16);
@@ -434,11 +479,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       if (!ok) break;
       fence_proxy_async_smem();
       tc_fence_after();
-      // O^T: 128 values at a time, eight steps of 16 rows (2,048 bytes)
+      // O^T: 128 values at a time, in steps of 16 rows (2,048 bytes)
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k)
+        for (uint32_t k = 0; k < kRows / 16; ++k)
           mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
                    i + k > 0);
         mma_commit(&sh.pv_done[j]);
@@ -455,7 +500,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   __syncthreads();
   if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
   __syncwarp();
-  if (warp == 8) tmem_free(tmem, kTmemCols);
+  if (warp == 8) tmem_free(tmem, S::kTmemCols);
 }
 
 // Joins the splits of one (query, head): their results weighted by
@@ -495,7 +540,8 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
   c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   c.head_tiles = (heads + c.heads - 1) / c.heads;
-  const int64_t tiles = (positions + kRowTile - 1) / kRowTile, ctas = nq * c.head_tiles, sms = device_sms();
+  const int64_t rows = c.heads == 64 ? AttendShape<64>::kRows : c.heads == 32 ? AttendShape<32>::kRows : AttendShape<16>::kRows;
+  const int64_t tiles = (positions + rows - 1) / rows, ctas = nq * c.head_tiles, sms = device_sms();
   int64_t splits = ctas >= sms ? 1 : sms / ctas;
   if (splits > tiles) splits = tiles;
   c.splits = (uint32_t)(splits < 1 ? 1 : splits);
@@ -504,7 +550,7 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
 
 template <uint32_t kHeads>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  constexpr size_t smem = 1024 + kTileBytes + 9 * kHeads * 128;
+  constexpr size_t smem = AttendShape<kHeads>::kSmem;
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

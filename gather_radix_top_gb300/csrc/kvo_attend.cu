@@ -1,7 +1,7 @@
 // kvo_attend: softmax attention of absorbed MLA queries over cached rows.
 //
-// One CTA holds up to 64 heads of one query and walks over tiles of 128 rows
-// of its list.  A tile's 656-byte rows come through registers, are
+// One CTA holds up to 64 heads of one query and walks over tiles of 80 or 96
+// rows of its list.  A tile's 656-byte rows come through registers, are
 // dequantised once to bf16 and written to shared memory; both products then
 // run on the tensor cores with the rows' operand as A:
 //     S^T [128 rows x heads]   = K [128 x 576] Q^T          (K contiguous)
@@ -32,8 +32,10 @@
 namespace kvo {
 namespace {
 
-constexpr uint32_t kWorkers = 256;                       // warps 0-7; warp 8 issues the MMAs, warp 9 loads
-constexpr uint32_t kAttendThreads = kWorkers + 64;
+constexpr uint32_t kWorkerWarps = 16;                    // four for each quarter of the columns
+constexpr uint32_t kMmaWarp = kWorkerWarps;
+constexpr uint32_t kLoadWarp = kMmaWarp + 1, kLoadWarps = 3;   // a warp issues a row's copy every 60 clocks
+constexpr uint32_t kAttendThreads = (kLoadWarp + kLoadWarps) * 32;
 constexpr uint32_t kPitch = 704;                         // of a raw row: an even and an odd row's halves of a store
                                                          // phase fall into different banks
 
@@ -41,8 +43,8 @@ constexpr uint32_t kPitch = 704;                         // of a raw row: an eve
 template <uint32_t kHeads>
 struct AttendShape {
   // rows of a tile: what the queries leave room for, raw and dequantised
-  static constexpr uint32_t kRows = kHeads == 64 ? 80 : kHeads == 32 ? 96 : 112;
-  static constexpr uint32_t kGroups = (kRows + 31) / 32;           // of 32 rows, the last one maybe half
+  static constexpr uint32_t kRows = kHeads == 64 ? 80 : 96;
+  static constexpr uint32_t kPasses = (kRows + 63) / 64;           // of 64 rows, the last one maybe part
   static constexpr uint32_t kChunkBytes = kRows * 128;             // 64 values of every row
   static constexpr uint32_t kTileBytes = 9 * kChunkBytes;
   static constexpr uint32_t kQueryBytes = 9 * kHeads * 128;
@@ -70,13 +72,12 @@ struct AttendArgs {
 };
 
 struct AttendShared {
-  uint64_t k_full[5], s_full, p_full, pv_done[4], drained;
-  uint64_t raw_full[4], raw_empty[4];
+  uint64_t k_full[5], s_full, p_full, pv_done[4], raw_full, raw_empty, drained;
   uint32_t tmem;
   uint32_t gave_up;
-  uint32_t there[2][4];              // tile i's rows that are not masked, in i % 2: a bit per row of a group
-  float top[2][4][32];               // per half of the columns and warp
-  float column[8][32];               // per warp: one value per column
+  uint32_t there[2][kLoadWarps];     // tile i's rows that are not masked, in i % 2: row r is bit r / 3 of word r % 3
+  float top[4][4][16];               // per quarter of the columns and warp
+  float column[kWorkerWarps][16];    // per warp: one value per column
 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -104,16 +105,22 @@ __device__ __forceinline__ void dequant4(uint32_t bytes, float scale, float bias
   hi = bf16_pair(v[2], v[3]);
 }
 
-// Barrier of the 128 threads of a half that also says whether any of them
+// Barrier of the 128 threads of a quarter that also says whether any of them
 // brings `flag`.
-__device__ __forceinline__ bool half_sync_any(uint32_t half, bool flag) {
+__device__ __forceinline__ bool quarter_sync_any(uint32_t quarter, bool flag) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)flag), "r"(1 + half)
+      : "r"((uint32_t)flag), "r"(1 + quarter)
       : "memory");
   return r != 0;
+}
+
+// One arrival for the whole warp, after all its lanes' accesses.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, uint32_t lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 // Sums of kN columns over the warp's lanes: a step with `kBit` halves the
@@ -136,43 +143,45 @@ __device__ __forceinline__ void lane_sums(float* v, uint32_t lane) {
 
 template <uint32_t kCols>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
-  if constexpr (kCols == 32)
-    tmem_ld32(addr, v);
-  else if constexpr (kCols == 16)
+  if constexpr (kCols == 16)
     tmem_ld16(addr, v);
-  else
+  else if constexpr (kCols == 8)
     tmem_ld8(addr, v);
+  else
+    tmem_ld4(addr, v);
 }
 
 template <uint32_t kHeads>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr uint32_t kCols = kHeads / 2;                 // of a worker warp
   using S = AttendShape<kHeads>;
   constexpr uint32_t kRows = S::kRows, kChunkBytes = S::kChunkBytes;
+  constexpr uint32_t kCols = kHeads / 4;                 // of a worker warp
   constexpr uint32_t kScores = 4 * kHeads;               // S^T's first column
   extern __shared__ uint8_t raw[];
   __shared__ AttendShared sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t t = blockIdx.y, seq = t / a.per_seq;
   const uint32_t h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
-  const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes, stage = queries + S::kQueryBytes;
+  const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes;
   uint8_t* const smem = raw + (tile_at - smem_u32(raw));
+  uint8_t* const stage = smem + S::kTileBytes + S::kQueryBytes;
 
   const int32_t len = a.lens[t];
   const uint32_t all = a.sel ? (len > 0 ? a.picked << a.sel_shift : 0u) : len <= 0 ? 0u : min((uint32_t)len, a.rows);
   const uint32_t tiles_all = (all + kRows - 1) / kRows, per = (tiles_all + a.splits - 1) / a.splits;
   const uint32_t first = min(split * per, tiles_all), tiles = min(per, tiles_all - first);
 
-  // this warp's columns: heads h0 + half * kCols + c; its lanes: rows (or
+  // a worker warp's columns: heads h0 + quarter * kCols + c; its lanes: rows (or
   // values of O^T) quad * 32 + lane
-  const uint32_t quad = warp & 3, half = (warp >> 2) & 1;
-  const int64_t out_row = (int64_t)t * a.heads + h0 + half * kCols;
-  const uint32_t mine = a.heads > h0 + half * kCols ? min(kCols, a.heads - h0 - half * kCols) : 0;   // real columns
+  const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3;
+  const uint32_t head = h0 + quarter * kCols;
+  const int64_t out_row = (int64_t)t * a.heads + head;
+  const uint32_t mine = a.heads > head ? min(kCols, a.heads - head) : 0;   // real columns
   float* const part = a.part + ((int64_t)split * a.nq * a.heads + out_row) * KVO_LATENT_BYTES;
   float* const part_lse = a.part_lse + (int64_t)split * a.nq * a.heads + out_row;
 
   if (tiles == 0) {
-    if (warp >= 8) return;
+    if (warp >= kWorkerWarps) return;
     if (a.splits > 1) {                                  // the join skips it
       if (quad == 0 && lane < mine) part_lse[lane] = -INFINITY;
       return;
@@ -184,49 +193,103 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   }
 
   if (tid == 0) {
-    for (uint32_t i = 0; i < 5; ++i) mbar_init(&sh.k_full[i], kWorkers);
+    for (uint32_t i = 0; i < 5; ++i) mbar_init(&sh.k_full[i], kWorkerWarps);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.pv_done[i], 1);
     mbar_init(&sh.s_full, 1);
-    mbar_init(&sh.p_full, kWorkers);
+    mbar_init(&sh.p_full, kWorkerWarps);
+    mbar_init(&sh.raw_full, kLoadWarps);
+    mbar_init(&sh.raw_empty, kWorkerWarps);
     mbar_init(&sh.drained, 1);
-    for (uint32_t u = 0; u < S::kGroups; ++u) {
-      mbar_init(&sh.raw_full[u], 1);
-      mbar_init(&sh.raw_empty[u], kWorkers);
-    }
     sh.gave_up = 0;
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, S::kTmemCols);
-
-  // the queries: heads past the last are zeros
-  for (uint32_t i = tid; i < kHeads * 72; i += kAttendThreads) {
-    const uint32_t r = i / 72, c = i - r * 72;
-    const bool real = h0 + r < a.heads;
-    copy16_async(queries + (c >> 3) * (kHeads * 128) + swizzled(r, c & 7),
-                 real ? a.q + t * a.q_ld + (h0 + r) * a.q_head_ld + c * 16 : a.q, real);
-  }
-  copy_async_commit();
-  copy_async_wait<0>();
-  fence_proxy_async_smem();
-  tc_fence_before();
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, S::kTmemCols);
   __syncthreads();
-  tc_fence_after();
+
+  if (warp >= kLoadWarp) {
+    // Lane l of loading warp w brings row 3 l + w of a tile.  Where it is, is
+    // looked up in three steps, one tile apart, so that none waits for the one
+    // before: the list's entry (tile i + 3), the table's (i + 2), the row
+    // (i + 1).  A masked row becomes zeros.
+    const uint32_t load = warp - kLoadWarp, r = kLoadWarps * lane + load;
+    const uint32_t sub = (1u << a.sel_shift) - 1;
+    auto listed = [&](uint32_t i) -> int32_t {           // the list's entry, unchecked
+      const uint32_t j = (first + i) * kRows + r;
+      if (i >= tiles || j >= all || r >= kRows) return -1;
+      return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
+    };
+    auto position = [&](uint32_t i, int32_t unit) -> int32_t {   // or -1: masked
+      const int64_t p = a.sel ? ((int64_t)unit << a.sel_shift) + (((first + i) * kRows + r) & sub) : (int64_t)unit;
+      return unit >= 0 && p < len ? (int32_t)p : -1;
+    };
+    auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
+    auto row_of = [&](int32_t p, int32_t block) -> int64_t {
+      if (p < 0) return -1;
+      const int64_t found = cache_row_in(a.cache, block, (uint32_t)p);
+      if (found < 0) atomicOr(a.status, kFlagRange);
+      return found;
+    };
+    int32_t unit = listed(0), pos = listed(1);
+    const int32_t unit2 = listed(2), pos0 = position(0, unit);
+    pos = position(1, pos);
+    int32_t block = block_of(pos);
+    int64_t row = row_of(pos0, block_of(pos0));
+    unit = unit2;
+    uint8_t* const dst = stage + r * kPitch;
+    uint32_t i = 0;
+    for (; i < tiles; ++i) {
+      const bool ok = i == 0 || wait_or_give_up(&sh.raw_empty, (i - 1) & 1, &sh.gave_up);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+      if (row < 0 && r < kRows) {
+        for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();                        // before a later tile's copy to the same place
+      }
+      __syncwarp();
+      if (lane == 0) {
+        sh.there[i & 1][load] = there;
+        mbar_arrive_expect_tx(&sh.raw_full, __popc(there) * KVO_ROW_BYTES);
+      }
+      __syncwarp();
+      if (row >= 0) bulk_copy_g2s(dst, a.cache.rows + row * KVO_ROW_BYTES, KVO_ROW_BYTES, &sh.raw_full);
+      row = row_of(pos, block);
+      pos = position(i + 2, unit);
+      block = block_of(pos);
+      unit = listed(i + 3);
+    }
+    // where the CTA gives up, the last copies finish before it ends
+    if (i < tiles && i > 0 && !landed(&sh.raw_full, (i - 1) & 1)) atomicOr(a.status, kFlagInflight);
+  } else {
+    // the queries: heads past the last are zeros
+    for (uint32_t i = tid; i < kHeads * 72; i += kLoadWarp * 32) {
+      const uint32_t r = i / 72, c = i - r * 72;
+      const bool real = h0 + r < a.heads;
+      copy16_async(queries + (c >> 3) * (kHeads * 128) + swizzled(r, c & 7),
+                   real ? a.q + t * a.q_ld + (h0 + r) * a.q_head_ld + c * 16 : a.q, real);
+    }
+    copy_async_commit();
+    copy_async_wait<0>();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    named_sync(5, kLoadWarp * 32);
+    tc_fence_after();
+  }
   const uint32_t tmem = sh.tmem;
 
-  if (warp < 8) {
+  if (warp < kWorkerWarps) {
     // A thread's part of a tile: 16-byte piece `piece` (of each 128 latent
-    // bytes) of rows slot + 32 u.  A warp reads 128 consecutive bytes of four
+    // bytes) of rows slot + 64 u.  A warp takes 128 consecutive bytes of four
     // rows at a time; the eight lanes of a store phase hold an even and an odd
     // row, whose swizzled pieces fall into different banks.
     const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3);
     const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1);
-    // rows 32 apart have the same swizzle: everything else is a fixed offset
+    // rows 64 apart have the same swizzle: everything else is a fixed offset
     uint8_t* const to = smem + (piece >> 2) * kChunkBytes;
     uint8_t* const to_lo = to + swizzled(slot, 2 * (piece & 3));
     uint8_t* const to_hi = to + swizzled(slot, 2 * (piece & 3) + 1);
     uint8_t* const to_rope = smem + 8 * kChunkBytes + swizzled(slot, piece);
-    const uint8_t* const from = smem + (stage - tile_at) + slot * kPitch + 16 * piece;
-    uint4 lat[4][S::kGroups], rope[S::kGroups], scales[S::kGroups];
+    const uint8_t* const from = stage + slot * kPitch;
 
+    const uint32_t mine_row = quad * 32 + lane;          // of S^T
     float top = -INFINITY;                               // lane c < kCols: the running maximum of column c
     float sum[kCols];
 #pragma unroll
@@ -235,58 +298,53 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     for (uint32_t i = 0; i < tiles; ++i) {
       const uint32_t turn = i & 1;
-      // the raw rows, while the second product of the last tile runs; a masked
-      // row becomes zeros
+      // the raw rows to bf16, part by part, as the products of the last tile
+      // release their places
+      wait_or_give_up(&sh.raw_full, turn, &sh.gave_up);
+      uint4 scales[S::kPasses];
 #pragma unroll
-      for (uint32_t u = 0; u < S::kGroups; ++u) {
-        wait_or_give_up(&sh.raw_full[u], turn, &sh.gave_up);
-        if (slot + 32 * u < kRows) {
-          const uint8_t* p = from + u * (32 * kPitch);
-#pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) lat[j][u] = *reinterpret_cast<const uint4*>(p + 128 * j);
-          scales[u] = *reinterpret_cast<const uint4*>(p - 16 * piece + KVO_LATENT_BYTES);
-          rope[u] = *reinterpret_cast<const uint4*>(p + KVO_LATENT_BYTES + 16);
-          if (!(sh.there[turn][u] >> slot & 1)) {
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) lat[j][u] = zero;
-            scales[u] = rope[u] = zero;
-          }
-        }
-        mbar_arrive(&sh.raw_empty[u]);
-      }
-      // dequantised, part by part, as the products of the last tile release it
+      for (uint32_t u = 0; u < S::kPasses; ++u)
+        if (slot + 64 * u < kRows)
+          scales[u] = *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + KVO_LATENT_BYTES);
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
+        uint4 lat[S::kPasses];
+#pragma unroll
+        for (uint32_t u = 0; u < S::kPasses; ++u)
+          if (slot + 64 * u < kRows)
+            lat[u] = *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + 128 * j + 16 * piece);
         if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
 #pragma unroll
-        for (uint32_t u = 0; u < S::kGroups; ++u) {
-          if (slot + 32 * u >= kRows) break;
+        for (uint32_t u = 0; u < S::kPasses; ++u) {
+          if (slot + 64 * u >= kRows) break;
           const uint32_t two = j == 0 ? scales[u].x : j == 1 ? scales[u].y : j == 2 ? scales[u].z : scales[u].w;
           const float s = __half2float(__ushort_as_half((uint16_t)(piece >= 4 ? two >> 16 : two & 0xffffu)));
           const float bias = -32896.0f * s;
           uint4 x, y;
-          dequant4(lat[j][u].x, s, bias, x.x, x.y);
-          dequant4(lat[j][u].y, s, bias, x.z, x.w);
-          dequant4(lat[j][u].z, s, bias, y.x, y.y);
-          dequant4(lat[j][u].w, s, bias, y.z, y.w);
-          *reinterpret_cast<uint4*>(to_lo + 2 * j * kChunkBytes + u * 4096) = x;
-          *reinterpret_cast<uint4*>(to_hi + 2 * j * kChunkBytes + u * 4096) = y;
+          dequant4(lat[u].x, s, bias, x.x, x.y);
+          dequant4(lat[u].y, s, bias, x.z, x.w);
+          dequant4(lat[u].z, s, bias, y.x, y.y);
+          dequant4(lat[u].w, s, bias, y.z, y.w);
+          *reinterpret_cast<uint4*>(to_lo + 2 * j * kChunkBytes + u * 8192) = x;
+          *reinterpret_cast<uint4*>(to_hi + 2 * j * kChunkBytes + u * 8192) = y;
         }
-        mbar_arrive(&sh.k_full[j]);
+        warp_arrive(&sh.k_full[j], lane);
       }
 #pragma unroll
-      for (uint32_t u = 0; u < S::kGroups; ++u)
-        if (slot + 32 * u < kRows) *reinterpret_cast<uint4*>(to_rope + u * 4096) = rope[u];
-      mbar_arrive(&sh.k_full[4]);
+      for (uint32_t u = 0; u < S::kPasses; ++u)
+        if (slot + 64 * u < kRows)
+          *reinterpret_cast<uint4*>(to_rope + u * 8192) =
+              *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + KVO_LATENT_BYTES + 16 + 16 * piece);
+      warp_arrive(&sh.k_full[4], lane);
+      const bool there = mine_row < kRows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
+      warp_arrive(&sh.raw_empty, lane);
 
-      // softmax: this thread has row quad * 32 + lane against kCols heads
+      // softmax: this thread has row mine_row against kCols heads
       wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
       __syncwarp();
       tc_fence_after();
       float s[kCols];
-      tmem_ld_cols<kCols>(lanes + kScores + half * kCols, s);
-      const bool there = quad * 32 + lane < kRows && (sh.there[turn][quad] >> lane & 1);
+      tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, s);
       tmem_ld_wait();
       float best = -INFINITY;
 #pragma unroll
@@ -296,37 +354,40 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(s[c]));
         if (lane == c) best = m;
       }
-      if (lane < kCols) sh.top[half][quad][lane] = best;
-      if (half_sync_any(half, *(volatile uint32_t*)&sh.gave_up != 0)) break;
+      if (lane < kCols) sh.top[quarter][quad][lane] = best;
+      if (quarter_sync_any(quarter, *(volatile uint32_t*)&sh.gave_up != 0)) break;
       float alpha = 1.0f;
       if (lane < kCols) {
-        best = fmaxf(fmaxf(sh.top[half][0][lane], sh.top[half][1][lane]),
-                     fmaxf(sh.top[half][2][lane], sh.top[half][3][lane]));
+        best = fmaxf(fmaxf(sh.top[quarter][0][lane], sh.top[quarter][1][lane]),
+                     fmaxf(sh.top[quarter][2][lane], sh.top[quarter][3][lane]));
         if (best > top + 8.0f || (top == -INFINITY && best > top)) {
           alpha = exp2_approx(top - best);               // 0 from -inf
           top = best;
         }
       }
       if (__any_sync(0xffffffffu, alpha != 1.0f) && i > 0) {
-        sh.column[warp][lane] = alpha;
+        if (lane < kCols) sh.column[warp][lane] = alpha;
         __syncwarp();
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
+        for (uint32_t j = 0; j < 4; ++j) {
+          float o[kCols];
+          tmem_ld_cols<kCols>(lanes + j * kHeads + quarter * kCols, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (uint32_t c = 0; c < kCols; c += 8) {
-            float o[8];
-            tmem_ld8(lanes + j * kHeads + half * kCols + c, o);
-            tmem_ld_wait();
+          for (uint32_t c = 0; c < kCols; ++c) o[c] *= sh.column[warp][c];
+          if constexpr (kCols == 4) {
+            tmem_st4(lanes + j * kHeads + quarter * kCols, o);
+          } else {
 #pragma unroll
-            for (uint32_t e = 0; e < 8; ++e) o[e] *= sh.column[warp][c + e];
-            tmem_st8(lanes + j * kHeads + half * kCols + c, o);
+            for (uint32_t c = 0; c < kCols; c += 8) tmem_st8(lanes + j * kHeads + quarter * kCols + c, o + c);
           }
+        }
 #pragma unroll
         for (uint32_t c = 0; c < kCols; ++c) sum[c] *= sh.column[warp][c];
         tmem_st_wait();
         __syncwarp();
       }
-      sh.column[warp][lane] = top == -INFINITY ? 0.0f : top;
+      if (lane < kCols) sh.column[warp][lane] = top == -INFINITY ? 0.0f : top;
       __syncwarp();
       uint32_t p[kCols / 2];
 #pragma unroll
@@ -336,22 +397,29 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         sum[c + 1] += p1;
         p[c / 2] = bf16_pair(p0, p1);
       }
-      if (quad * 32 + lane < kRows)
+      if (mine_row < kRows) {
+        uint8_t* const weights = smem + 8 * kChunkBytes;
+        if constexpr (kCols == 4) {                      // half a piece
+          *reinterpret_cast<uint2*>(weights + swizzled(mine_row, quarter >> 1) + (quarter & 1) * 8) =
+              make_uint2(p[0], p[1]);
+        } else {
 #pragma unroll
-      for (uint32_t c = 0; c < kCols / 8; ++c)
-        *reinterpret_cast<uint4*>(smem + 8 * kChunkBytes + swizzled(quad * 32 + lane, half * (kCols / 8) + c)) =
-            make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+          for (uint32_t c = 0; c < kCols / 8; ++c)
+            *reinterpret_cast<uint4*>(weights + swizzled(mine_row, quarter * (kCols / 8) + c)) =
+                make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+        }
+      }
       tc_fence_before();
-      mbar_arrive(&sh.p_full);
+      warp_arrive(&sh.p_full, lane);
     }
 
     lane_sums<kCols, 16>(sum, lane);
-    named_sync(1 + half, 128);                           // sh.top is free again
-    if (lane % (32 / kCols) == 0) sh.top[half][quad][lane / (32 / kCols)] = sum[0];
-    named_sync(1 + half, 128);
+    named_sync(1 + quarter, 128);                        // sh.top is free again
+    if (lane % (32 / kCols) == 0) sh.top[quarter][quad][lane / (32 / kCols)] = sum[0];
+    named_sync(1 + quarter, 128);
     float total = 0.0f;
     if (lane < kCols)
-      total = (sh.top[half][0][lane] + sh.top[half][1][lane]) + (sh.top[half][2][lane] + sh.top[half][3][lane]);
+      total = (sh.top[quarter][0][lane] + sh.top[quarter][1][lane]) + (sh.top[quarter][2][lane] + sh.top[quarter][3][lane]);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const float lse2 = total == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) + log2f(total);
     if (quad == 0 && lane < mine) {
@@ -361,7 +429,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         a.lse[out_row + lane] = lse2 * 0.6931471805599453f;
     }
     __syncwarp();
-    sh.column[warp][lane] = inv;
+    if (lane < kCols) sh.column[warp][lane] = inv;
     __syncwarp();
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
@@ -369,7 +437,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       __syncwarp();
       tc_fence_after();
       float o[kCols];
-      tmem_ld_cols<kCols>(lanes + j * kHeads + half * kCols, o);
+      tmem_ld_cols<kCols>(lanes + j * kHeads + quarter * kCols, o);
       tmem_ld_wait();
       const uint32_t d = j * 128 + quad * 32 + lane;
       if (a.splits > 1) {
@@ -384,86 +452,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 __float2bfloat16_rn(o[c] * sh.column[warp][c]);
       }
     }
-  } else if (warp == 9) {
-    // Lane l brings row l of every group of 32.  Where it is, is looked up in
-    // three steps, one tile apart, so that none waits for the one before: the
-    // list's entry (tile i + 3), the table's (i + 2), the row (i + 1).
-    const uint32_t sub = (1u << a.sel_shift) - 1;
-    auto entry = [&](uint32_t i, uint32_t u) -> uint32_t { return (first + i) * kRows + 32 * u + lane; };
-    auto listed = [&](uint32_t i, uint32_t u) -> int32_t {       // the list's entry, unchecked
-      const uint32_t j = entry(i, u);
-      if (i >= tiles || j >= all || 32 * u + lane >= kRows) return -1;
-      return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
-    };
-    auto position = [&](uint32_t i, uint32_t u, int32_t unit) -> int32_t {   // or -1: masked
-      const int64_t p = a.sel ? ((int64_t)unit << a.sel_shift) + (entry(i, u) & sub) : (int64_t)unit;
-      return unit >= 0 && p < len ? (int32_t)p : -1;
-    };
-    auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
-    auto row_of = [&](int32_t p, int32_t block) -> int64_t {
-      if (p < 0) return -1;
-      const int64_t r = cache_row_in(a.cache, block, (uint32_t)p);
-      if (r < 0) atomicOr(a.status, kFlagRange);
-      return r;
-    };
-    int32_t unit[S::kGroups], pos[S::kGroups], block[S::kGroups];
-    int64_t row[S::kGroups];
-#pragma unroll
-    for (uint32_t u = 0; u < S::kGroups; ++u) {
-      unit[u] = listed(0, u);
-      pos[u] = listed(1, u);
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < S::kGroups; ++u) {
-      const int32_t p0 = position(0, u, unit[u]);
-      pos[u] = position(1, u, pos[u]);
-      block[u] = block_of(pos[u]);
-      row[u] = row_of(p0, block_of(p0));
-      unit[u] = listed(2, u);
-    }
-    bool ok = true;
-    uint32_t i = 0;
-    for (; i < tiles; ++i) {
-#pragma unroll
-      for (uint32_t u = 0; u < S::kGroups; ++u) {
-        ok = ok && (i == 0 || wait_or_give_up(&sh.raw_empty[u], (i - 1) & 1, &sh.gave_up));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t there = __ballot_sync(0xffffffffu, row[u] >= 0);
-        if (lane == 0) {
-          sh.there[i & 1][u] = there;
-          mbar_arrive_expect_tx(&sh.raw_full[u], __popc(there) * KVO_ROW_BYTES);
-        }
-        __syncwarp();
-        if (row[u] >= 0)
-          bulk_copy_g2s(smem + (stage - tile_at) + (32 * u + lane) * kPitch, a.cache.rows + row[u] * KVO_ROW_BYTES,
-                        KVO_ROW_BYTES, &sh.raw_full[u]);
-      }
-      if (!ok) break;
-#pragma unroll
-      for (uint32_t u = 0; u < S::kGroups; ++u) {
-        row[u] = row_of(pos[u], block[u]);
-        pos[u] = position(i + 2, u, unit[u]);
-        block[u] = block_of(pos[u]);
-        unit[u] = listed(i + 3, u);
-      }
-    }
-    // where the CTA gives up, the copies in flight finish before it ends
-    if (!ok && i > 0)
-      for (uint32_t u = 0; u < S::kGroups; ++u)
-        if (!landed(&sh.raw_full[u], (i - 1) & 1) && !mbar_test(&sh.raw_full[u], i & 1)) atomicOr(a.status, kFlagInflight);
-  } else if (lane == 0) {
+  } else if (warp == kMmaWarp && lane == 0) {
     constexpr uint32_t kQk = mma_desc(1, kHeads, false, false), kPv = mma_desc(1, kHeads, true, true);
     const uint64_t keys = tile_desc(tile_at, 16), heads = tile_desc(queries, 16);
     const uint64_t values = tile_desc(tile_at, kChunkBytes), weights = tile_desc(tile_at + 8 * kChunkBytes, kChunkBytes);
     bool ok = true;
     for (uint32_t i = 0; i < tiles && ok; ++i) {
       const uint32_t turn = i & 1;
-      // S^T: 64 values of K and Q at a time, four steps of 16
+      // S^T: 64 values of K and Q at a time, four steps of 16.  (M is 128 and a
+      // tile has fewer rows: the others are whatever lies behind, and masked.)
 #pragma unroll
-      for (uint32_t c = 0; c < 9 && ok; ++c) {
+      for (uint32_t c = 0; c < 9; ++c) {
         if (c % 2 == 0) {
-          ok = wait_or_give_up(&sh.k_full[c / 2], turn, &sh.gave_up);
+          ok = ok && wait_or_give_up(&sh.k_full[c / 2], turn, &sh.gave_up);
           if (!ok) break;
           fence_proxy_async_smem();                      // the workers' stores, before the MMAs read them
           tc_fence_after();
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   __syncthreads();
   if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
   __syncwarp();
-  if (warp == 8) tmem_free(tmem, S::kTmemCols);
+  if (warp == kMmaWarp) tmem_free(tmem, S::kTmemCols);
 }
 
 // Joins the splits of one (query, head): their results weighted by
@@ -540,7 +541,7 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
   c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   c.head_tiles = (heads + c.heads - 1) / c.heads;
-  const int64_t rows = c.heads == 64 ? AttendShape<64>::kRows : c.heads == 32 ? AttendShape<32>::kRows : AttendShape<16>::kRows;
+  const int64_t rows = c.heads == 64 ? AttendShape<64>::kRows : AttendShape<32>::kRows;
   const int64_t tiles = (positions + rows - 1) / rows, ctas = nq * c.head_tiles, sms = device_sms();
   int64_t splits = ctas >= sms ? 1 : sms / ctas;
   if (splits > tiles) splits = tiles;

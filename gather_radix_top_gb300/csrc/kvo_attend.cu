@@ -15,16 +15,19 @@
 // the second product releases them, and the next tile's bytes are on their
 // way meanwhile.
 //
-// The softmax is over the lanes of S^T: a maximum per column over the warp's
-// lanes, then over the four warps of a column.  The running maximum moves only
-// when it is exceeded by more than 8 (in powers of two; weights stay below
-// 256), so the accumulators are rarely rescaled.  The sum of the weights stays
-// in registers, per lane, and is reduced once at the end.
+// The softmax is over the lanes of S^T.  Its reference is not the running
+// maximum but the maximum at some earlier tile: weights of up to 2^64 lose
+// nothing in fp32 and bf16 (sums of 2^31 of them times the largest latent stay
+// below 2^119), so a column's maximum over four warps is formed for the first
+// tile and again only when a logit lies 2^64 above the reference.  The sum of
+// the weights stays in registers, per lane, and is reduced once at the end.
 //
 // Long lists with few queries are split over CTAs, whose normalised partial
 // results a second launch joins by their log-sum-exps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kvo_cache.cuh"
 #include "kvo_tc.cuh"
@@ -51,6 +54,8 @@ struct AttendShape {
   static constexpr uint32_t kSmem = 1024 + kTileBytes + kQueryBytes + kRows * kPitch;
   static constexpr uint32_t kTmemCols = kHeads == 64 ? 512 : kHeads == 32 ? 256 : 128;
 };
+constexpr float kFar = 64.0f;                            // in powers of two
+constexpr int64_t kLeastRows = 32;                       // of a split
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -72,10 +77,11 @@ struct AttendArgs {
 };
 
 struct AttendShared {
-  uint64_t k_full[5], s_full, p_full, pv_done[4], raw_full, raw_empty, drained;
+  uint64_t k_full[5], s_full, p_full, pv_done[4], voted[4], raw_full, raw_empty, drained;
   uint32_t tmem;
   uint32_t gave_up;
   uint32_t there[2][kLoadWarps];     // tile i's rows that are not masked, in i % 2: row r is bit r / 3 of word r % 3
+  uint32_t far[2][4];                // per quarter of the columns, in i % 2: tile i needs new references
   float top[4][4][16];               // per quarter of the columns and warp
   float column[kWorkerWarps][16];    // per warp: one value per column
 };
@@ -141,6 +147,15 @@ __device__ __forceinline__ void lane_sums(float* v, uint32_t lane) {
   if constexpr (kBit > 1) lane_sums<(kN > 1 ? kN / 2 : 1), kBit / 2>(v, lane);
 }
 
+// f(0), f(1), .. f(kN - 1), each with its index as a constant.
+template <uint32_t kN, uint32_t kI = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (kI < kN) {
+    f(std::integral_constant<uint32_t, kI>{});
+    static_for<kN, kI + 1>(f);
+  }
+}
+
 template <uint32_t kCols>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
   if constexpr (kCols == 16)
@@ -163,27 +178,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   const uint32_t t = blockIdx.y, seq = t / a.per_seq;
   const uint32_t h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
   const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes;
-  uint8_t* const smem = raw + (tile_at - smem_u32(raw));
-  uint8_t* const stage = smem + S::kTileBytes + S::kQueryBytes;
+  const uint32_t stage = queries + S::kQueryBytes;
 
   const int32_t len = a.lens[t];
-  const uint32_t all = a.sel ? (len > 0 ? a.picked << a.sel_shift : 0u) : len <= 0 ? 0u : min((uint32_t)len, a.rows);
-  const uint32_t tiles_all = (all + kRows - 1) / kRows, per = (tiles_all + a.splits - 1) / a.splits;
-  const uint32_t first = min(split * per, tiles_all), tiles = min(per, tiles_all - first);
+  // this CTA's entries of the list: from `first` on, `count` of them.  (With a
+  // list nothing here waits for len: an empty query finds all of it masked.)
+  const uint32_t all = a.sel ? a.picked << a.sel_shift : len <= 0 ? 0u : min((uint32_t)len, a.rows);
+  const uint32_t share = (all + a.splits - 1) / a.splits;
+  const uint32_t per = share > kRows ? (share + kRows - 1) / kRows * kRows : (share + 15u) & ~15u;
+  const uint32_t first = (uint32_t)min((uint64_t)split * per, (uint64_t)all), count = min(per, all - first);
+  const uint32_t tiles = (count + kRows - 1) / kRows;
+  // rows of tile i that may be there, rounded up to a step of the second
+  // product; a tile's other rows are not touched
+  auto rows_of = [&](uint32_t i) -> uint32_t { return (min(kRows, count - i * kRows) + 15u) & ~15u; };
 
   // a worker warp's columns: heads h0 + quarter * kCols + c; its lanes: rows (or
   // values of O^T) quad * 32 + lane
   const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3;
   const uint32_t head = h0 + quarter * kCols;
-  const int64_t out_row = (int64_t)t * a.heads + head;
   const uint32_t mine = a.heads > head ? min(kCols, a.heads - head) : 0;   // real columns
-  float* const part = a.part + ((int64_t)split * a.nq * a.heads + out_row) * KVO_LATENT_BYTES;
-  float* const part_lse = a.part_lse + (int64_t)split * a.nq * a.heads + out_row;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tiles == 0) {
     if (warp >= kWorkerWarps) return;
+    const int64_t out_row = (int64_t)t * a.heads + head;
     if (a.splits > 1) {                                  // the join skips it
-      if (quad == 0 && lane < mine) part_lse[lane] = -INFINITY;
+      if (quad == 0 && lane < mine) a.part_lse[(int64_t)split * a.nq * a.heads + out_row + lane] = -INFINITY;
       return;
     }
     for (uint32_t c = 0; c < mine; ++c)
@@ -194,12 +214,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
   if (tid == 0) {
     for (uint32_t i = 0; i < 5; ++i) mbar_init(&sh.k_full[i], kWorkerWarps);
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.pv_done[i], 1);
+    for (uint32_t i = 0; i < 4; ++i) {
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.voted[i], 4);
+    }
     mbar_init(&sh.s_full, 1);
     mbar_init(&sh.p_full, kWorkerWarps);
     mbar_init(&sh.raw_full, kLoadWarps);
     mbar_init(&sh.raw_empty, kWorkerWarps);
     mbar_init(&sh.drained, 1);
+    for (uint32_t i = 0; i < 8; ++i) sh.far[i >> 2][i & 3] = 0;
     sh.gave_up = 0;
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, S::kTmemCols);
@@ -213,12 +237,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const uint32_t load = warp - kLoadWarp, r = kLoadWarps * lane + load;
     const uint32_t sub = (1u << a.sel_shift) - 1;
     auto listed = [&](uint32_t i) -> int32_t {           // the list's entry, unchecked
-      const uint32_t j = (first + i) * kRows + r;
-      if (i >= tiles || j >= all || r >= kRows) return -1;
+      const uint32_t j = first + i * kRows + r;
+      if (i >= tiles || i * kRows + r >= count || r >= kRows) return -1;
       return a.sel ? a.sel[t * a.sel_ld + (j >> a.sel_shift)] : (int32_t)j;
     };
     auto position = [&](uint32_t i, int32_t unit) -> int32_t {   // or -1: masked
-      const int64_t p = a.sel ? ((int64_t)unit << a.sel_shift) + (((first + i) * kRows + r) & sub) : (int64_t)unit;
+      const int64_t p = a.sel ? ((int64_t)unit << a.sel_shift) + ((first + i * kRows + r) & sub) : (int64_t)unit;
       return unit >= 0 && p < len ? (int32_t)p : -1;
     };
     auto block_of = [&](int32_t p) -> int32_t { return p >= 0 ? cache_block(a.cache, seq, (uint32_t)p) : -1; };
@@ -234,14 +258,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     int32_t block = block_of(pos);
     int64_t row = row_of(pos0, block_of(pos0));
     unit = unit2;
-    uint8_t* const dst = stage + r * kPitch;
+    const uint32_t dst = stage + r * kPitch;
     uint32_t i = 0;
     for (; i < tiles; ++i) {
       const bool ok = i == 0 || wait_or_give_up(&sh.raw_empty, (i - 1) & 1, &sh.gave_up);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
-      if (row < 0 && r < kRows) {
-        for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+      if (row < 0 && r < rows_of(i)) {
+        for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
         fence_proxy_async_smem();                        // before a later tile's copy to the same place
       }
       __syncwarp();
@@ -250,7 +274,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         mbar_arrive_expect_tx(&sh.raw_full, __popc(there) * KVO_ROW_BYTES);
       }
       __syncwarp();
-      if (row >= 0) bulk_copy_g2s(dst, a.cache.rows + row * KVO_ROW_BYTES, KVO_ROW_BYTES, &sh.raw_full);
+      if (row >= 0) bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row * KVO_ROW_BYTES, KVO_ROW_BYTES, &sh.raw_full);
       row = row_of(pos, block);
       pos = position(i + 2, unit);
       block = block_of(pos);
@@ -283,14 +307,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3);
     const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1);
     // rows 64 apart have the same swizzle: everything else is a fixed offset
-    uint8_t* const to = smem + (piece >> 2) * kChunkBytes;
-    uint8_t* const to_lo = to + swizzled(slot, 2 * (piece & 3));
-    uint8_t* const to_hi = to + swizzled(slot, 2 * (piece & 3) + 1);
-    uint8_t* const to_rope = smem + 8 * kChunkBytes + swizzled(slot, piece);
-    const uint8_t* const from = stage + slot * kPitch;
+    const uint32_t to_lo = tile_at + (piece >> 2) * kChunkBytes + swizzled(slot, 2 * (piece & 3));
+    const uint32_t to_hi = tile_at + (piece >> 2) * kChunkBytes + swizzled(slot, 2 * (piece & 3) + 1);
+    const uint32_t to_rope = tile_at + 8 * kChunkBytes + swizzled(slot, piece);
+    const uint32_t from = stage + slot * kPitch;
 
     const uint32_t mine_row = quad * 32 + lane;          // of S^T
-    float top = -INFINITY;                               // lane c < kCols: the running maximum of column c
+    if (lane < kCols) sh.column[warp][lane] = 0.0f;
+    __syncwarp();
+    bool unset = true;                                   // some column has no reference yet
+    float top = -INFINITY;                               // lane c < kCols: column c's reference
     float sum[kCols];
 #pragma unroll
     for (uint32_t c = 0; c < kCols; ++c) sum[c] = 0.0f;
@@ -298,121 +324,163 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     for (uint32_t i = 0; i < tiles; ++i) {
       const uint32_t turn = i & 1;
+      const uint32_t rows = rows_of(i);
       // the raw rows to bf16, part by part, as the products of the last tile
-      // release their places
+      // release their places; the second half of them is in registers, and the
+      // next rows may come, before its places are free
       wait_or_give_up(&sh.raw_full, turn, &sh.gave_up);
-      uint4 scales[S::kPasses];
+      const bool there =
+          mine_row < rows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
+      uint32_t scales[S::kPasses][2];                    // this piece's scale of each part, as fp16 pairs
 #pragma unroll
       for (uint32_t u = 0; u < S::kPasses; ++u)
-        if (slot + 64 * u < kRows)
-          scales[u] = *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + KVO_LATENT_BYTES);
+        if (slot + 64 * u < rows) {
+          const uint4 eight = lds16(from + u * (64 * kPitch) + KVO_LATENT_BYTES);
+          scales[u][0] = __byte_perm(eight.x, eight.y, piece >= 4 ? 0x7632u : 0x5410u);
+          scales[u][1] = __byte_perm(eight.z, eight.w, piece >= 4 ? 0x7632u : 0x5410u);
+        }
+      uint4 rope[S::kPasses];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        uint4 lat[S::kPasses];
+      for (uint32_t j2 = 0; j2 < 4; j2 += 2) {
+        uint4 lat[2][S::kPasses];
 #pragma unroll
         for (uint32_t u = 0; u < S::kPasses; ++u)
-          if (slot + 64 * u < kRows)
-            lat[u] = *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + 128 * j + 16 * piece);
-        if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
+          if (slot + 64 * u < rows) {
+            const uint32_t p = from + u * (64 * kPitch) + 16 * piece;
+            lat[0][u] = lds16(p + 128 * j2);
+            lat[1][u] = lds16(p + 128 * j2 + 128);
+            if (j2) rope[u] = lds16(p + KVO_LATENT_BYTES + 16);
+          }
+        if (j2) warp_arrive(&sh.raw_empty, lane);
 #pragma unroll
-        for (uint32_t u = 0; u < S::kPasses; ++u) {
-          if (slot + 64 * u >= kRows) break;
-          const uint32_t two = j == 0 ? scales[u].x : j == 1 ? scales[u].y : j == 2 ? scales[u].z : scales[u].w;
-          const float s = __half2float(__ushort_as_half((uint16_t)(piece >= 4 ? two >> 16 : two & 0xffffu)));
-          const float bias = -32896.0f * s;
-          uint4 x, y;
-          dequant4(lat[u].x, s, bias, x.x, x.y);
-          dequant4(lat[u].y, s, bias, x.z, x.w);
-          dequant4(lat[u].z, s, bias, y.x, y.y);
-          dequant4(lat[u].w, s, bias, y.z, y.w);
-          *reinterpret_cast<uint4*>(to_lo + 2 * j * kChunkBytes + u * 8192) = x;
-          *reinterpret_cast<uint4*>(to_hi + 2 * j * kChunkBytes + u * 8192) = y;
+        for (uint32_t k = 0; k < 2; ++k) {
+          const uint32_t j = j2 + k;
+          if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
+#pragma unroll
+          for (uint32_t u = 0; u < S::kPasses; ++u) {
+            if (slot + 64 * u >= rows) break;
+            const float s = __half2float(__ushort_as_half((uint16_t)(scales[u][j >> 1] >> (j & 1) * 16)));
+            const float bias = -32896.0f * s;
+            uint4 x, y;
+            dequant4(lat[k][u].x, s, bias, x.x, x.y);
+            dequant4(lat[k][u].y, s, bias, x.z, x.w);
+            dequant4(lat[k][u].z, s, bias, y.x, y.y);
+            dequant4(lat[k][u].w, s, bias, y.z, y.w);
+            sts16(to_lo + 2 * j * kChunkBytes + u * 8192, x);
+            sts16(to_hi + 2 * j * kChunkBytes + u * 8192, y);
+          }
+          warp_arrive(&sh.k_full[j], lane);
         }
-        warp_arrive(&sh.k_full[j], lane);
       }
 #pragma unroll
       for (uint32_t u = 0; u < S::kPasses; ++u)
-        if (slot + 64 * u < kRows)
-          *reinterpret_cast<uint4*>(to_rope + u * 8192) =
-              *reinterpret_cast<const uint4*>(from + u * (64 * kPitch) + KVO_LATENT_BYTES + 16 + 16 * piece);
+        if (slot + 64 * u < rows) sts16(to_rope + u * 8192, rope[u]);
       warp_arrive(&sh.k_full[4], lane);
-      const bool there = mine_row < kRows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
-      warp_arrive(&sh.raw_empty, lane);
 
       // softmax: this thread has row mine_row against kCols heads
       wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
       __syncwarp();
       tc_fence_after();
-      float s[kCols];
-      tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, s);
+      float x[kCols];
+      tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, x);
       tmem_ld_wait();
-      float best = -INFINITY;
+      float most = -INFINITY;
 #pragma unroll
       for (uint32_t c = 0; c < kCols; ++c) {
-        s[c] = there ? s[c] * a.scale : -INFINITY;
-        float m;
-        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(s[c]));
-        if (lane == c) best = m;
+        x[c] = fmaf(x[c], a.scale, -sh.column[warp][c]);
+        most = fmaxf(most, x[c]);
       }
-      if (lane < kCols) sh.top[quarter][quad][lane] = best;
-      if (quarter_sync_any(quarter, *(volatile uint32_t*)&sh.gave_up != 0)) break;
-      float alpha = 1.0f;
-      if (lane < kCols) {
-        best = fmaxf(fmaxf(sh.top[quarter][0][lane], sh.top[quarter][1][lane]),
-                     fmaxf(sh.top[quarter][2][lane], sh.top[quarter][3][lane]));
-        if (best > top + 8.0f || (top == -INFINITY && best > top)) {
-          alpha = exp2_approx(top - best);               // 0 from -inf
-          top = best;
-        }
-      }
-      if (__any_sync(0xffffffffu, alpha != 1.0f) && i > 0) {
-        if (lane < kCols) sh.column[warp][lane] = alpha;
-        __syncwarp();
+      // whether a row of the four warps lies too far above the references: said
+      // through a flag and a barrier that is waited for behind the exponentials
+      const bool quit = *(volatile uint32_t*)&sh.gave_up != 0;
+      if (__any_sync(0xffffffffu, quit || (there && most > kFar)) && lane == 0) sh.far[turn][quarter] = 1;
+      warp_arrive(&sh.voted[quarter], lane);
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-          float o[kCols];
-          tmem_ld_cols<kCols>(lanes + j * kHeads + quarter * kCols, o);
+      for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(x[c]);
+      wait_or_give_up(&sh.voted[quarter], turn, &sh.gave_up);
+      const bool far = *(volatile uint32_t*)&sh.far[turn][quarter] != 0;
+      if (quad == 0 && lane == 0) sh.far[turn ^ 1][quarter] = 0;
+      if (unset || far) {                                // the same in all four warps
+        // new references: the columns' largest logits so far.  (Four columns at
+        // a time: this is rare, and registers for more would be taken from the
+        // rest.)
+        float best = -INFINITY;
+#pragma unroll
+        for (uint32_t c = 0; c < kCols; c += 4) {
+          float z[4];
+          tmem_ld4(lanes + kScores + quarter * kCols + c, z);
           tmem_ld_wait();
 #pragma unroll
-          for (uint32_t c = 0; c < kCols; ++c) o[c] *= sh.column[warp][c];
-          if constexpr (kCols == 4) {
-            tmem_st4(lanes + j * kHeads + quarter * kCols, o);
-          } else {
-#pragma unroll
-            for (uint32_t c = 0; c < kCols; c += 8) tmem_st8(lanes + j * kHeads + quarter * kCols + c, o + c);
+          for (uint32_t e = 0; e < 4; ++e) {
+            float m;
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(there ? z[e] * a.scale : -INFINITY));
+            if (lane == c + e) best = m;
           }
         }
+        if (lane < kCols) sh.top[quarter][quad][lane] = best;
+        if (quarter_sync_any(quarter, quit)) break;
+        float alpha = 1.0f;
+        if (lane < kCols) {
+          best = fmaxf(fmaxf(sh.top[quarter][0][lane], sh.top[quarter][1][lane]),
+                       fmaxf(sh.top[quarter][2][lane], sh.top[quarter][3][lane]));
+          if (best > top) {
+            alpha = exp2_approx(top - best);             // 0 from -inf
+            top = best;
+          }
+        }
+        unset = __any_sync(0xffffffffu, lane < kCols && top == -INFINITY);
+        if (__any_sync(0xffffffffu, alpha != 1.0f) && i > 0) {
+          if (lane < kCols) sh.column[warp][lane] = alpha;
+          __syncwarp();
+#pragma unroll 1
+          for (uint32_t j = 0; j < 4; ++j)
+#pragma unroll 1
+            for (uint32_t c = 0; c < kCols; c += 4) {
+              float o[4];
+              tmem_ld4(lanes + j * kHeads + quarter * kCols + c, o);
+              tmem_ld_wait();
 #pragma unroll
-        for (uint32_t c = 0; c < kCols; ++c) sum[c] *= sh.column[warp][c];
-        tmem_st_wait();
+              for (uint32_t e = 0; e < 4; ++e) o[e] *= sh.column[warp][c + e];
+              tmem_st4(lanes + j * kHeads + quarter * kCols + c, o);
+            }
+#pragma unroll
+          for (uint32_t c = 0; c < kCols; ++c) sum[c] *= sh.column[warp][c];
+          tmem_st_wait();
+          __syncwarp();
+        }
+        if (lane < kCols) sh.column[warp][lane] = top == -INFINITY ? 0.0f : top;
         __syncwarp();
+        tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(fmaf(x[c], a.scale, -sh.column[warp][c]));
       }
-      if (lane < kCols) sh.column[warp][lane] = top == -INFINITY ? 0.0f : top;
-      __syncwarp();
       uint32_t p[kCols / 2];
 #pragma unroll
       for (uint32_t c = 0; c < kCols; c += 2) {
-        const float p0 = exp2_approx(s[c] - sh.column[warp][c]), p1 = exp2_approx(s[c + 1] - sh.column[warp][c + 1]);
-        sum[c] += p0;
-        sum[c + 1] += p1;
-        p[c / 2] = bf16_pair(p0, p1);
+        if (there) {                                     // (a row that is not may hold anything)
+          sum[c] += x[c];
+          sum[c + 1] += x[c + 1];
+        }
+        p[c / 2] = there ? bf16_pair(x[c], x[c + 1]) : 0u;
       }
-      if (mine_row < kRows) {
-        uint8_t* const weights = smem + 8 * kChunkBytes;
+      if (mine_row < rows) {
+        const uint32_t weights = tile_at + 8 * kChunkBytes;
         if constexpr (kCols == 4) {                      // half a piece
-          *reinterpret_cast<uint2*>(weights + swizzled(mine_row, quarter >> 1) + (quarter & 1) * 8) =
-              make_uint2(p[0], p[1]);
+          sts8(weights + swizzled(mine_row, quarter >> 1) + (quarter & 1) * 8, p[0], p[1]);
         } else {
 #pragma unroll
           for (uint32_t c = 0; c < kCols / 8; ++c)
-            *reinterpret_cast<uint4*>(weights + swizzled(mine_row, quarter * (kCols / 8) + c)) =
-                make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+            sts16(weights + swizzled(mine_row, quarter * (kCols / 8) + c),
+                  make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
         }
       }
       tc_fence_before();
       warp_arrive(&sh.p_full, lane);
     }
 
+    const int64_t out_row = (int64_t)t * a.heads + head;
+    float* const part = a.part + ((int64_t)split * a.nq * a.heads + out_row) * KVO_LATENT_BYTES;
     lane_sums<kCols, 16>(sum, lane);
     named_sync(1 + quarter, 128);                        // sh.top is free again
     if (lane % (32 / kCols) == 0) sh.top[quarter][quad][lane / (32 / kCols)] = sum[0];
@@ -424,7 +492,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const float lse2 = total == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) + log2f(total);
     if (quad == 0 && lane < mine) {
       if (a.splits > 1)
-        part_lse[lane] = lse2;
+        a.part_lse[(int64_t)split * a.nq * a.heads + out_row + lane] = lse2;
       else if (a.lse)
         a.lse[out_row + lane] = lse2 * 0.6931471805599453f;
     }
@@ -452,50 +520,65 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 __float2bfloat16_rn(o[c] * sh.column[warp][c]);
       }
     }
-  } else if (warp == kMmaWarp && lane == 0) {
+  } else if (warp == kMmaWarp) {
     constexpr uint32_t kQk = mma_desc(1, kHeads, false, false), kPv = mma_desc(1, kHeads, true, true);
     const uint64_t keys = tile_desc(tile_at, 16), heads = tile_desc(queries, 16);
     const uint64_t values = tile_desc(tile_at, kChunkBytes), weights = tile_desc(tile_at + 8 * kChunkBytes, kChunkBytes);
     bool ok = true;
-    for (uint32_t i = 0; i < tiles && ok; ++i) {
-      const uint32_t turn = i & 1;
+    for (uint32_t i = 0; i < tiles; ++i) {
+      const uint32_t turn = i & 1, steps = rows_of(i) / 16;
       // S^T: 64 values of K and Q at a time, four steps of 16.  (M is 128 and a
       // tile has fewer rows: the others are whatever lies behind, and masked.)
 #pragma unroll
-      for (uint32_t c = 0; c < 9; ++c) {
-        if (c % 2 == 0) {
-          ok = ok && wait_or_give_up(&sh.k_full[c / 2], turn, &sh.gave_up);
-          if (!ok) break;
-          fence_proxy_async_smem();                      // the workers' stores, before the MMAs read them
-          tc_fence_after();
-        }
+      for (uint32_t part = 0; part < 5; ++part) {
+        ok = ok && wait_or_give_up(&sh.k_full[part], turn, &sh.gave_up);
+        __syncwarp();
+        fence_proxy_async_smem();                        // the workers' stores, before the MMAs read them
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-          mma_bf16(tmem + kScores, keys + c * (kChunkBytes >> 4) + 2 * k, heads + c * (kHeads * 128 >> 4) + 2 * k, kQk,
-                   c + k > 0);
+          for (uint32_t m = 0; m < (part < 4 ? 8 : 4); ++m) {
+            const uint32_t c = 2 * part + m / 4, k = m % 4;
+            mma_bf16(tmem + kScores, keys + c * (kChunkBytes >> 4) + 2 * k, heads + c * (kHeads * 128 >> 4) + 2 * k,
+                     kQk, c + k > 0);
+          }
+          if (part == 4) mma_commit(&sh.s_full);
+        }
+        __syncwarp();
       }
-      if (!ok) break;
-      mma_commit(&sh.s_full);
-      ok = wait_or_give_up(&sh.p_full, turn, &sh.gave_up);
-      if (!ok) break;
+      ok = ok && wait_or_give_up(&sh.p_full, turn, &sh.gave_up);
+      if (!__all_sync(0xffffffffu, ok)) break;
       fence_proxy_async_smem();
       tc_fence_after();
       // O^T: 128 values at a time, in steps of 16 rows (2,048 bytes)
+      if (elect_one()) {
+        if (steps == kRows / 16) {
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
+          for (uint32_t j = 0; j < 4; ++j) {
 #pragma unroll
-        for (uint32_t k = 0; k < kRows / 16; ++k)
-          mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
-                   i + k > 0);
-        mma_commit(&sh.pv_done[j]);
+            for (uint32_t k = 0; k < kRows / 16; ++k)
+              mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
+                       k > 0 || i > 0);
+            mma_commit(&sh.pv_done[j]);
+          }
+        } else {
+          for (uint32_t j = 0; j < 4; ++j) {
+            for (uint32_t k = 0; k < steps; ++k)
+              mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
+                       k > 0 || i > 0);
+            mma_commit(&sh.pv_done[j]);
+          }
+        }
       }
+      __syncwarp();
     }
-    if (!ok) {
+    if (!__all_sync(0xffffffffu, ok) && lane == 0) {
       // let the MMAs in flight finish before their memory is given back
       mma_commit(&sh.drained);
       atomicOr(a.status, kFlagTimeout);
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -505,31 +588,57 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 }
 
 // Joins the splits of one (query, head): their results weighted by
-// exp2(lse - the joint lse).  128 threads, four values each.
-__global__ void __launch_bounds__(128) join_kernel(const float* part, const float* part_lse, uint32_t splits,
+// exp2(lse - the joint lse).  Four groups of 128 threads take every fourth
+// split, four values a thread.
+constexpr uint32_t kMaxSplits = 1024;
+__global__ void __launch_bounds__(512) join_kernel(const float* part, const float* part_lse, uint32_t splits,
                                                    int64_t rows, uint16_t* out, float* lse) {
+  __shared__ float weight[kMaxSplits];
+  __shared__ float red[16];
+  __shared__ float4 sums[3][128];
   const int64_t r = blockIdx.x;
-  const uint32_t tid = threadIdx.x;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial results are there
   float top = -INFINITY;
-  for (uint32_t s = 0; s < splits; ++s) top = fmaxf(top, part_lse[s * rows + r]);
-  float total = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (uint32_t s = tid; s < splits; s += 512) {
+    weight[s] = part_lse[s * rows + r];
+    top = fmaxf(top, weight[s]);
+  }
+  for (uint32_t d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+  for (uint32_t w = 0; w < 16; ++w) top = fmaxf(top, red[w]);
   const float base = top == -INFINITY ? 0.0f : top;
-  for (uint32_t s = 0; s < splits; ++s) {
-    const float l = part_lse[s * rows + r];
-    if (l == -INFINITY) continue;                        // nothing there, and nothing was written
-    const float w = exp2f(l - base);
-    const float4 v = *reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * tid);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float total = 0.0f;
+#pragma unroll 8
+  for (uint32_t s = group; s < splits; s += 4) {
+    const float l = weight[s], w = exp2f(l - base);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (l != -INFINITY)                                    // else nothing is there, and nothing was written
+      v = *reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * at);
     total += w;
     o.x = fmaf(w, v.x, o.x);
     o.y = fmaf(w, v.y, o.y);
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   }
+  __syncthreads();
+  if (group) sums[group - 1][at] = o;
+  if (at == 0) red[group] = total;
+  __syncthreads();
+  if (group) return;
+  total = (red[0] + red[1]) + (red[2] + red[3]);
+  for (uint32_t g = 0; g < 3; ++g) {
+    o.x += sums[g][at].x;
+    o.y += sums[g][at].y;
+    o.z += sums[g][at].z;
+    o.w += sums[g][at].w;
+  }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[tid] =
+  reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[at] =
       make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-  if (lse && tid == 0) lse[r] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+  if (lse && at == 0) lse[r] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
 }
 
 // How a call is cut: columns per CTA and splits of every list.
@@ -541,10 +650,10 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
   c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   c.head_tiles = (heads + c.heads - 1) / c.heads;
-  const int64_t rows = c.heads == 64 ? AttendShape<64>::kRows : AttendShape<32>::kRows;
-  const int64_t tiles = (positions + rows - 1) / rows, ctas = nq * c.head_tiles, sms = device_sms();
+  const int64_t ctas = nq * c.head_tiles, sms = device_sms(), most = (positions + kLeastRows - 1) / kLeastRows;
   int64_t splits = ctas >= sms ? 1 : sms / ctas;
-  if (splits > tiles) splits = tiles;
+  if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   c.splits = (uint32_t)(splits < 1 ? 1 : splits);
   return c;
 }
@@ -620,8 +729,18 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
                   : cut.heads == 32 ? launch_attend<32>(a, on)
                                     : launch_attend<64>(a, on);
   if (e == cudaSuccess && a.splits > 1) {
-    join_kernel<<<(unsigned)(nq * a.heads), 128, 0, on>>>(a.part, a.part_lse, a.splits, nq * a.heads, a.out, a.lse);
-    e = cudaGetLastError();
+    // launched while the attention runs, it waits on the GPU for its end
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = dim3((unsigned)(nq * a.heads));
+    lc.blockDim = dim3(512);
+    lc.stream = on;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelEx(&lc, join_kernel, (const float*)a.part, (const float*)a.part_lse, a.splits,
+                           nq * (int64_t)a.heads, a.out, a.lse);
   }
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

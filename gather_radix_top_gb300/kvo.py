@@ -535,23 +535,47 @@ class Cache:
         self.ref = ctypes.addressof(c)
 
 
-_ELEMENT = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+class _Torch:
+    """torch and its types, looked up once: these calls are short enough for that to show."""
+
+    def __init__(self):
+        import torch
+        self.torch, self.int32, self.float32 = torch, torch.int32, torch.float32
+        self.bfloat16, self.int16, self.uint8, self.float64 = torch.bfloat16, torch.int16, torch.uint8, torch.float64
+        self.element = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+        self.key = {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_torch_types = None
+
+
+def _T() -> _Torch:
+    global _torch_types
+    if _torch_types is None:
+        _torch_types = _Torch()
+    return _torch_types
+
+
+def _raw_stream(T, device, stream) -> int:
+    """The address of `stream`, or of the device's current one."""
+    return T.raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _key_type(t) -> int:
-    kind = {"torch.bfloat16": BF16, "torch.float8_e4m3fn": E4M3}.get(str(t.dtype))
+    kind = _T().key.get(t.dtype)
     if kind is None:
         raise ValueError(f"keys must be bfloat16 or float8_e4m3fn, got {t.dtype}")
     return kind
 
 
-def _cuda(t, what: str, dtype: str, shape=None):
+def _cuda(t, what: str, dtype, shape=None):
     """data_ptr of a CUDA tensor of that type (and shape), its last dimension contiguous."""
-    if not t.is_cuda or str(t.dtype) != dtype:
+    if not t.is_cuda or t.dtype is not dtype:
         raise ValueError(f"{what} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{what} must be contiguous in its last dimension")
     return t.data_ptr()
 
@@ -567,29 +591,36 @@ def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=N
     float16 or float32 CUDA tensors of one type, tokens strided as they are;
     pos and seq (optional): int32 CUDA [n]; inv_freq: 32 floats; out_bf16:
     bfloat16 (or int16) CUDA [n, 576] (optional)."""
-    n, dt = latent.shape[0], str(latent.dtype)
-    if dt not in _ELEMENT:
+    T = _T()
+    n, dt = latent.shape[0], latent.dtype
+    kind = T.element.get(dt)
+    if kind is None:
         raise ValueError(f"latent must be bfloat16, float16 or float32, got {dt}")
-    t = kvo_tokens()
-    t.latent, t.latent_ld = _cuda(latent, "latent", dt, (n, LATENT_VALUES)), latent.stride(0)
-    t.rope, t.rope_ld = _cuda(rope, "rope", dt, (n, ROPE_VALUES)), rope.stride(0)
+    lone = n <= 1                    # a lone token has no next one: its stride says nothing
+    key_ptr, key_ld = None, 0
     if key is not None:
-        t.key, t.key_ld = _cuda(key, "key", dt, (n, KEY_VALUES)), key.stride(0)
-    if n <= 1:                       # a lone token has no next one: its stride says nothing
-        t.latent_ld, t.rope_ld, t.key_ld = LATENT_VALUES, ROPE_VALUES, KEY_VALUES
-    t.pos = _cuda(pos, "pos", "torch.int32", (n,))
-    if seq is not None:
-        t.seq = _cuda(seq, "seq", "torch.int32", (n,))
+        key_ptr, key_ld = _cuda(key, "key", dt, (n, KEY_VALUES)), KEY_VALUES if lone else key.stride(0)
     if len(inv_freq) != ROPE_VALUES // 2:
         raise ValueError("inv_freq must hold 32 values")
-    freq = (ctypes.c_double * 32)(*(inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq))
-    t.inv_freq = ctypes.addressof(freq)
+    if getattr(inv_freq, "dtype", None) is T.float64 and not inv_freq.is_cuda and inv_freq.is_contiguous():
+        freq, freq_ptr = inv_freq, inv_freq.data_ptr()
+    else:
+        freq = (ctypes.c_double * 32)(*(inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq))
+        freq_ptr = ctypes.addressof(freq)
+    out_ptr = None
     if out_bf16 is not None:
-        if str(out_bf16.dtype) not in ("torch.bfloat16", "torch.int16") or out_bf16.numel() != n * DEQUANT_VALUES:
+        if out_bf16.dtype not in (T.bfloat16, T.int16) or out_bf16.numel() != n * DEQUANT_VALUES:
             raise ValueError("out_bf16 must be bfloat16 or int16 [n, 576]")
-        t.out_bf16 = _dev_ptr(out_bf16)
-    t.n, t.dtype, t.interleaved = n, _ELEMENT[dt], 1 if interleaved else 0
-    _check(lib().kvo_append_tokens(ctx, cache.ref, ctypes.addressof(t), _stream_ptr(stream)), "kvo_append_tokens")
+        if not out_bf16.is_cuda or not out_bf16.is_contiguous():
+            raise ValueError("out_bf16 must be a contiguous CUDA tensor")
+        out_ptr = out_bf16.data_ptr()
+    t = kvo_tokens(_cuda(latent, "latent", dt, (n, LATENT_VALUES)), _cuda(rope, "rope", dt, (n, ROPE_VALUES)), key_ptr,
+                   None if seq is None else _cuda(seq, "seq", T.int32, (n,)), _cuda(pos, "pos", T.int32, (n,)), freq_ptr,
+                   out_ptr, LATENT_VALUES if lone else latent.stride(0), ROPE_VALUES if lone else rope.stride(0), key_ld,
+                   n, kind, 1 if interleaved else 0)
+    _check(lib().kvo_append_tokens(ctx, cache.ref, ctypes.addressof(t), _raw_stream(T, latent.device, stream)),
+           "kvo_append_tokens")
+    del freq
 
 
 def _queries(cache: Cache, q, values: int) -> tuple:
@@ -608,23 +639,19 @@ def kvo_index_scores(ctx: int, cache: Cache, q, weights, lens, n: int, block: in
     """q: CUDA [nq, heads, 128] of the keys' type; weights: float32 [nq,
     heads]; lens: int32 [nq].  Returns float32 [nq, ceil(n / block)] (`out`
     if given; its rows may be strided)."""
-    import torch
+    T = _T()
     nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, KEY_VALUES)
-    s = kvo_score_query()
     keys = cache.tensors[1]
     if keys is None:
         raise ValueError("the cache has no keys")
-    s.q = _cuda(q, "q", str(keys.dtype))
-    s.q_ld, s.q_head_ld = q_ld, q_head_ld
-    s.weights, s.weights_ld = _cuda(weights, "weights", "torch.float32", (nq, heads)), weights.stride(0)
-    s.lens = _cuda(lens, "lens", "torch.int32", (nq,))
     cols = -(-n // block) if block > 0 else 0
     if out is None:
-        out = _empty((nq, cols), torch.float32, q.device, stream)
-    s.scores = _cuda(out, "out", "torch.float32", (nq, cols))
-    s.ld = out.stride(0) if nq > 1 else cols
-    s.n, s.per_seq, s.heads, s.block = n, per_seq, heads, block
-    _check(lib().kvo_index_scores(ctx, cache.ref, ctypes.addressof(s), _stream_ptr(stream)), "kvo_index_scores")
+        out = _empty((nq, cols), T.float32, q.device, stream)
+    s = kvo_score_query(_cuda(q, "q", keys.dtype), _cuda(weights, "weights", T.float32, (nq, heads)),
+                        _cuda(lens, "lens", T.int32, (nq,)), _cuda(out, "out", T.float32, (nq, cols)), q_ld, q_head_ld,
+                        weights.stride(0), out.stride(0) if nq > 1 else cols, n, per_seq, heads, block)
+    _check(lib().kvo_index_scores(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)),
+           "kvo_index_scores")
     return out
 
 
@@ -647,38 +674,38 @@ def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None =
     lens value, needed without sel; sel: int32 [nq, picked] (rows may be
     strided) of positions, or of blocks of sel_block positions.  Returns (out
     bfloat16 [nq, heads, 512], lse float32 [nq, heads])."""
-    import torch
+    T = _T()
     nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, DEQUANT_VALUES)
-    s = kvo_attend_query()
-    s.q = _cuda(q, "q", "torch.bfloat16")
-    s.q_ld, s.q_head_ld = q_ld, q_head_ld
-    s.lens = _cuda(lens, "lens", "torch.int32", (nq,))
+    sel_ptr, sel_ld, picked = None, 0, 0
     if sel is None:
         if rows is None:
             raise ValueError("attending to whole sequences needs rows, the largest length")
-        s.rows = positions = rows
+        positions = rows
     else:
         if sel.dim() != 2:
             raise ValueError("sel must be [queries, picked]")
-        s.sel = _cuda(sel, "sel", "torch.int32", (nq, sel.shape[1]))
-        s.picked = sel.shape[1]
-        s.sel_ld = sel.stride(0) if nq > 1 else s.picked
-        positions = s.picked * sel_block
+        rows, picked = 0, sel.shape[1]
+        sel_ptr = _cuda(sel, "sel", T.int32, (nq, picked))
+        sel_ld = sel.stride(0) if nq > 1 else picked
+        positions = picked * sel_block
     if out is None:
-        out = _empty((nq, heads, LATENT_VALUES), torch.bfloat16, q.device, stream)
+        out = _empty((nq, heads, LATENT_VALUES), T.bfloat16, q.device, stream)
     if lse is None:
-        lse = _empty((nq, heads), torch.float32, q.device, stream)
-    s.out = _cuda(out, "out", "torch.bfloat16", (nq, heads, LATENT_VALUES))
-    s.lse = _cuda(lse, "lse", "torch.float32", (nq, heads))
+        lse = _empty((nq, heads), T.float32, q.device, stream)
     _whole(out, "out")
     _whole(lse, "lse")
-    need = kvo_attend_work_bytes(nq, heads, positions)
+    work_ptr, need = None, lib().kvo_attend_work_bytes(nq, heads, positions)
     if need > 0:
         if work is None:
-            work = _empty((need,), torch.uint8, q.device, stream)
-        s.work, s.work_bytes = _dev_ptr(work, "torch.uint8"), work.numel()
-    s.sel_block, s.per_seq, s.heads, s.scale = sel_block, per_seq, heads, scale
-    _check(lib().kvo_attend(ctx, cache.ref, ctypes.addressof(s), _stream_ptr(stream)), "kvo_attend")
+            work = _empty((need,), T.uint8, q.device, stream)
+        else:
+            need = work.numel()
+        work_ptr = _cuda(work, "work", T.uint8)
+    s = kvo_attend_query(_cuda(q, "q", T.bfloat16), _cuda(lens, "lens", T.int32, (nq,)), sel_ptr,
+                         _cuda(out, "out", T.bfloat16, (nq, heads, LATENT_VALUES)),
+                         _cuda(lse, "lse", T.float32, (nq, heads)), work_ptr, max(need, 0), q_ld, q_head_ld, sel_ld, rows,
+                         picked, sel_block, per_seq, heads, scale)
+    _check(lib().kvo_attend(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)), "kvo_attend")
     return out, lse
 
 

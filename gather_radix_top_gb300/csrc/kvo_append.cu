@@ -64,7 +64,12 @@ __device__ __forceinline__ void load_floats(const T* p, float* v) {
   }
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The larger value; a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // The smallest fp16 s with 127 * s >= amax, at most 65504.  127 * s has 18
 // significant bits, so the comparisons in fp32 are exact.
@@ -76,14 +81,25 @@ __device__ __forceinline__ __half group_scale(float amax) {
   return __ushort_as_half(h);
 }
 
-// x / s rounded to the nearest integer, ties to even, within [-127, 127]:
-// the quotient through the reciprocal may be a unit off next to a tie, and
-// the remainder x - q * s (exact: both products fit) says which way.
-__device__ __forceinline__ int quantise(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x), half = 0.5f * s;
-  if (fabsf(r) > half || (fabsf(r) == half && ((int)q & 1))) q += r > 0.0f ? 1.0f : -1.0f;
-  return (int)fminf(fmaxf(q, -127.0f), 127.0f);
+constexpr float kToInteger = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, in the low bits
+
+// x / s rounded to the nearest integer, ties to even, as kToInteger + q
+// (|x| <= 127 s).  The quotient through the reciprocal and one correction
+// (x - q s is exact) is exact where the quotient is a tie.  For 16-bit x
+// every other quotient is at least 2^-12 from a tie (x has at most 11 bits, s
+// 11), so its rounding does not matter.  An fp32 x can be nearer than the
+// quotient's last bit: there the remainder decides.
+template <bool kWide>
+__device__ __forceinline__ float quantise(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);
+  float t = q + kToInteger;
+  if (kWide) {
+    q = t - kToInteger;
+    const float r = fmaf(-q, s, x), half = 0.5f * s;
+    if (fabsf(r) > half || (fabsf(r) == half && ((int)q & 1))) t += r > 0.0f ? 1.0f : -1.0f;
+  }
+  return t;
 }
 
 template <typename T>
@@ -91,9 +107,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_tokens_kernel(const __g
   const uint32_t lane = threadIdx.x & 31;
   const int64_t i = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
   if (i >= a.n) return;
+
+  // the token's values are asked for before its place is looked up, so that
+  // the two chains of loads overlap
   const int32_t s = a.seq ? a.seq[i] : (int32_t)(i < INT32_MAX ? i : INT32_MAX);
-  if (s < 0) return;
   const int32_t p = a.pos[i];
+  float x[16], k[4];
+  load_floats<T, 16>(reinterpret_cast<const T*>(a.latent) + i * a.latent_ld + 16 * lane, x);
+  const T* rope = reinterpret_cast<const T*>(a.rope) + i * a.rope_ld;
+  const uint32_t i0 = a.interleaved ? 2 * lane : lane, i1 = a.interleaved ? 2 * lane + 1 : lane + 32;
+  const float r0 = to_float(rope[i0]), r1 = to_float(rope[i1]);
+  if (a.key) load_floats<T, 4>(reinterpret_cast<const T*>(a.key) + i * a.key_ld + 4 * lane, k);
+
+  if (s < 0) return;
   const int64_t row = p >= 0 && (uint32_t)s < a.cache.sequences ? cache_row(a.cache, (uint32_t)s, (uint32_t)p) : -1;
   uint16_t* values = a.out_bf16 ? a.out_bf16 + i * KVO_DEQUANT_VALUES : nullptr;
   if (row < 0) {
@@ -106,42 +132,40 @@ __global__ void __launch_bounds__(kAppendThreads) append_tokens_kernel(const __g
   }
   uint8_t* dst = a.cache.rows + row * KVO_ROW_BYTES;
 
-  // loads first, so that they overlap
-  float x[16], r0, r1, k[4];
-  load_floats<T, 16>(reinterpret_cast<const T*>(a.latent) + i * a.latent_ld + 16 * lane, x);
-  const T* rope = reinterpret_cast<const T*>(a.rope) + i * a.rope_ld;
-  const uint32_t i0 = a.interleaved ? 2 * lane : lane, i1 = a.interleaved ? 2 * lane + 1 : lane + 32;
-  r0 = to_float(rope[i0]);
-  r1 = to_float(rope[i1]);
-  if (a.key) load_floats<T, 4>(reinterpret_cast<const T*>(a.key) + i * a.key_ld + 4 * lane, k);
-
-  // latent: lanes 4g .. 4g+3 hold group g.  As integers, magnitudes order
-  // like the floats, and an infinity or a NaN is above every finite value.
-  uint32_t top = 0;
+  // latent: lanes 4g .. 4g+3 hold group g; a NaN or an infinity shows in its maximum
+  float top = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) top = max(top, abs_bits(x[e]));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const bool finite = top < 0x7f800000u;
-  const __half scale = finite ? group_scale(__uint_as_float(top)) : __ushort_as_half(0x7e00);
+  for (int e = 0; e < 16; ++e) top = max_nan(top, fabsf(x[e]));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool finite = top < INFINITY;
+  const __half scale = finite ? group_scale(top) : __ushort_as_half(0x7e00);
   const float sf = __half2float(scale);
-  const bool some = finite && sf > 0.0f;
-  const float inv = some ? 1.0f / sf : 0.0f;
-  int q[16];
+  if (!(finite && sf > 0.0f)) {                           // all 64 values are zeros
 #pragma unroll
-  for (int e = 0; e < 16; ++e) q[e] = some ? quantise(x[e], sf, inv) : 0;
+    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+  } else if (top > 127.0f * 65504.0f) {                   // beyond the largest scale
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = fminf(fmaxf(x[e], -127.0f * 65504.0f), 127.0f * 65504.0f);
+  }
+  const float by = finite && sf > 0.0f ? sf : 1.0f, inv = 1.0f / by;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = quantise<sizeof(T) == 4>(x[e], by, inv);
   uint32_t packed[4];
 #pragma unroll
-  for (int w = 0; w < 4; ++w)
-    packed[w] = (uint32_t)(q[4 * w] & 255) | (uint32_t)(q[4 * w + 1] & 255) << 8 |
-                (uint32_t)(q[4 * w + 2] & 255) << 16 | (uint32_t)(q[4 * w + 3] & 255) << 24;
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t lo = __byte_perm(__float_as_uint(x[4 * w]), __float_as_uint(x[4 * w + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(x[4 * w + 2]), __float_as_uint(x[4 * w + 3]), 0x0040);
+    packed[w] = __byte_perm(lo, hi, 0x5410);
+  }
   reinterpret_cast<uint4*>(dst)[lane] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
   if ((lane & 3) == 0) reinterpret_cast<__half*>(dst + KVO_LATENT_BYTES)[lane >> 2] = scale;
   if (values) {
     uint32_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const __nv_bfloat162 two = __floats2bfloat162_rn((float)q[2 * e] * sf, (float)q[2 * e + 1] * sf);
+      const __nv_bfloat162 two =
+          __floats2bfloat162_rn((x[2 * e] - kToInteger) * sf, (x[2 * e + 1] - kToInteger) * sf);
       v[e] = *reinterpret_cast<const uint32_t*>(&two);
     }
     uint4* o = reinterpret_cast<uint4*>(values + 16 * lane);
@@ -157,12 +181,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_tokens_kernel(const __g
   sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn, &cs);
   const __nv_bfloat16 o0 = __float2bfloat16_rn(r0 * cs - r1 * sn), o1 = __float2bfloat16_rn(r1 * cs + r0 * sn);
   __nv_bfloat16* rd = reinterpret_cast<__nv_bfloat16*>(dst + KVO_LATENT_BYTES + 16);
-  rd[i0] = o0;
-  rd[i1] = o1;
-  if (values) {
-    __nv_bfloat16* vd = reinterpret_cast<__nv_bfloat16*>(values) + KVO_LATENT_BYTES;
-    vd[i0] = o0;
-    vd[i1] = o1;
+  __nv_bfloat16* vd = reinterpret_cast<__nv_bfloat16*>(values) + KVO_LATENT_BYTES;
+  if (a.interleaved) {
+    const __nv_bfloat162 two = __halves2bfloat162(o0, o1);
+    reinterpret_cast<__nv_bfloat162*>(rd)[lane] = two;
+    if (values) reinterpret_cast<__nv_bfloat162*>(vd)[lane] = two;
+  } else {
+    rd[i0] = o0;
+    rd[i1] = o1;
+    if (values) {
+      vd[i0] = o0;
+      vd[i1] = o1;
+    }
   }
 
   if (!a.key) return;
@@ -172,8 +202,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_tokens_kernel(const __g
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     return;
   }
-  const uint32_t big =
-      __reduce_max_sync(0xffffffffu, max(max(abs_bits(k[0]), abs_bits(k[1])), max(abs_bits(k[2]), abs_bits(k[3]))));
+  // magnitudes as integers order like the floats, infinities and NaNs above all
+  uint32_t big = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) big = max(big, __float_as_uint(k[e]) & 0x7fffffffu);
+  big = __reduce_max_sync(0xffffffffu, big);
   // 448 = 1.75 * 2^8: the smallest 2^e with 448 * 2^e >= amax, from amax's bits
   int e = (int)(big >> 23) - 127 - 8 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = max(e, -100);

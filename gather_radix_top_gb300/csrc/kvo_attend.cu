@@ -77,7 +77,7 @@ struct AttendArgs {
 };
 
 struct AttendShared {
-  uint64_t k_full[5], s_full, p_full, pv_done[4], voted[4], raw_full, raw_empty, drained;
+  uint64_t k_full[2], s_full, p_full, pv_done[2], voted[4], raw_full, raw_empty, drained;
   uint32_t tmem;
   uint32_t gave_up;
   uint32_t there[2][kLoadWarps];     // tile i's rows that are not masked, in i % 2: row r is bit r / 3 of word r % 3
@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   }
 
   if (tid == 0) {
-    for (uint32_t i = 0; i < 5; ++i) mbar_init(&sh.k_full[i], kWorkerWarps);
-    for (uint32_t i = 0; i < 4; ++i) {
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], kWorkerWarps);
       mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.voted[i], 4);
     }
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.voted[i], 4);
     mbar_init(&sh.s_full, 1);
     mbar_init(&sh.p_full, kWorkerWarps);
     mbar_init(&sh.raw_full, kLoadWarps);
@@ -339,43 +339,42 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           scales[u][0] = __byte_perm(eight.x, eight.y, piece >= 4 ? 0x7632u : 0x5410u);
           scales[u][1] = __byte_perm(eight.z, eight.w, piece >= 4 ? 0x7632u : 0x5410u);
         }
-      uint4 rope[S::kPasses];
 #pragma unroll
-      for (uint32_t j2 = 0; j2 < 4; j2 += 2) {
-        uint4 lat[2][S::kPasses];
+      for (uint32_t part = 0; part < 2; ++part) {
+        uint4 lat[2][S::kPasses], rope[S::kPasses];
 #pragma unroll
         for (uint32_t u = 0; u < S::kPasses; ++u)
           if (slot + 64 * u < rows) {
-            const uint32_t p = from + u * (64 * kPitch) + 16 * piece;
-            lat[0][u] = lds16(p + 128 * j2);
-            lat[1][u] = lds16(p + 128 * j2 + 128);
-            if (j2) rope[u] = lds16(p + KVO_LATENT_BYTES + 16);
+            const uint32_t p = from + u * (64 * kPitch) + 16 * piece + 256 * part;
+            lat[0][u] = lds16(p);
+            lat[1][u] = lds16(p + 128);
+            if (part) rope[u] = lds16(p - 256 + KVO_LATENT_BYTES + 16);
           }
-        if (j2) warp_arrive(&sh.raw_empty, lane);
+        if (part) warp_arrive(&sh.raw_empty, lane);
+        if (i > 0) wait_or_give_up(&sh.pv_done[part], turn ^ 1, &sh.gave_up);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k) {
-          const uint32_t j = j2 + k;
-          if (i > 0) wait_or_give_up(&sh.pv_done[j], turn ^ 1, &sh.gave_up);
 #pragma unroll
           for (uint32_t u = 0; u < S::kPasses; ++u) {
             if (slot + 64 * u >= rows) break;
-            const float s = __half2float(__ushort_as_half((uint16_t)(scales[u][j >> 1] >> (j & 1) * 16)));
+            const float s = __half2float(__ushort_as_half((uint16_t)(scales[u][part] >> k * 16)));
             const float bias = -32896.0f * s;
             uint4 x, y;
             dequant4(lat[k][u].x, s, bias, x.x, x.y);
             dequant4(lat[k][u].y, s, bias, x.z, x.w);
             dequant4(lat[k][u].z, s, bias, y.x, y.y);
             dequant4(lat[k][u].w, s, bias, y.z, y.w);
-            sts16(to_lo + 2 * j * kChunkBytes + u * 8192, x);
-            sts16(to_hi + 2 * j * kChunkBytes + u * 8192, y);
+            sts16(to_lo + (4 * part + 2 * k) * kChunkBytes + u * 8192, x);
+            sts16(to_hi + (4 * part + 2 * k) * kChunkBytes + u * 8192, y);
           }
-          warp_arrive(&sh.k_full[j], lane);
         }
-      }
+        if (part) {
 #pragma unroll
-      for (uint32_t u = 0; u < S::kPasses; ++u)
-        if (slot + 64 * u < rows) sts16(to_rope + u * 8192, rope[u]);
-      warp_arrive(&sh.k_full[4], lane);
+          for (uint32_t u = 0; u < S::kPasses; ++u)
+            if (slot + 64 * u < rows) sts16(to_rope + u * 8192, rope[u]);
+        }
+        warp_arrive(&sh.k_full[part], lane);
+      }
 
       // softmax: this thread has row mine_row against kCols heads
       wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     __syncwarp();
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
-      wait_or_give_up(&sh.pv_done[j], (tiles - 1) & 1, &sh.gave_up);
+      if (j % 2 == 0) wait_or_give_up(&sh.pv_done[j / 2], (tiles - 1) & 1, &sh.gave_up);
       __syncwarp();
       tc_fence_after();
       float o[kCols];
@@ -530,19 +529,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       // S^T: 64 values of K and Q at a time, four steps of 16.  (M is 128 and a
       // tile has fewer rows: the others are whatever lies behind, and masked.)
 #pragma unroll
-      for (uint32_t part = 0; part < 5; ++part) {
+      for (uint32_t part = 0; part < 2; ++part) {
         ok = ok && wait_or_give_up(&sh.k_full[part], turn, &sh.gave_up);
         __syncwarp();
         fence_proxy_async_smem();                        // the workers' stores, before the MMAs read them
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (uint32_t m = 0; m < (part < 4 ? 8 : 4); ++m) {
-            const uint32_t c = 2 * part + m / 4, k = m % 4;
+          for (uint32_t m = 0; m < (part ? 20 : 16); ++m) {
+            const uint32_t c = 4 * part + m / 4, k = m % 4;
             mma_bf16(tmem + kScores, keys + c * (kChunkBytes >> 4) + 2 * k, heads + c * (kHeads * 128 >> 4) + 2 * k,
                      kQk, c + k > 0);
           }
-          if (part == 4) mma_commit(&sh.s_full);
+          if (part) mma_commit(&sh.s_full);
         }
         __syncwarp();
       }
@@ -559,14 +558,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             for (uint32_t k = 0; k < kRows / 16; ++k)
               mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
                        k > 0 || i > 0);
-            mma_commit(&sh.pv_done[j]);
+            if (j % 2) mma_commit(&sh.pv_done[j / 2]);
           }
         } else {
           for (uint32_t j = 0; j < 4; ++j) {
             for (uint32_t k = 0; k < steps; ++k)
               mma_bf16(tmem + j * kHeads, values + (2 * j) * (kChunkBytes >> 4) + k * 128, weights + k * 128, kPv,
                        k > 0 || i > 0);
-            mma_commit(&sh.pv_done[j]);
+            if (j % 2) mma_commit(&sh.pv_done[j / 2]);
           }
         }
       }
@@ -588,31 +587,33 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 }
 
 // Joins the splits of one (query, head): their results weighted by
-// exp2(lse - the joint lse).  Four groups of 128 threads take every fourth
-// split, four values a thread.
-constexpr uint32_t kMaxSplits = 1024;
-__global__ void __launch_bounds__(512) join_kernel(const float* part, const float* part_lse, uint32_t splits,
-                                                   int64_t rows, uint16_t* out, float* lse) {
-  __shared__ float weight[kMaxSplits];
-  __shared__ float red[16];
-  __shared__ float4 sums[3][128];
+// exp2(lse - the joint lse).  kGroups groups of 128 threads take every
+// kGroups-th split, four values a thread.
+constexpr uint32_t kMaxSplits = 1024, kFewSplits = 8;
+template <uint32_t kGroups>
+__global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, const float* part_lse, uint32_t splits,
+                                                             int64_t rows, uint16_t* out, float* lse) {
+  constexpr uint32_t kThreads = 128 * kGroups;
+  __shared__ float weight[kGroups > 1 ? kMaxSplits : kFewSplits];
+  __shared__ float red[4 * kGroups];
+  __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][128];
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial results are there
   float top = -INFINITY;
-  for (uint32_t s = tid; s < splits; s += 512) {
+  for (uint32_t s = tid; s < splits; s += kThreads) {
     weight[s] = part_lse[s * rows + r];
     top = fmaxf(top, weight[s]);
   }
   for (uint32_t d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) red[warp] = top;
   __syncthreads();
-  for (uint32_t w = 0; w < 16; ++w) top = fmaxf(top, red[w]);
+  for (uint32_t w = 0; w < 4 * kGroups; ++w) top = fmaxf(top, red[w]);
   const float base = top == -INFINITY ? 0.0f : top;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
 #pragma unroll 8
-  for (uint32_t s = group; s < splits; s += 4) {
+  for (uint32_t s = group; s < splits; s += kGroups) {
     const float l = weight[s], w = exp2f(l - base);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (l != -INFINITY)                                    // else nothing is there, and nothing was written
@@ -623,17 +624,20 @@ __global__ void __launch_bounds__(512) join_kernel(const float* part, const floa
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   }
-  __syncthreads();
-  if (group) sums[group - 1][at] = o;
-  if (at == 0) red[group] = total;
-  __syncthreads();
-  if (group) return;
-  total = (red[0] + red[1]) + (red[2] + red[3]);
-  for (uint32_t g = 0; g < 3; ++g) {
-    o.x += sums[g][at].x;
-    o.y += sums[g][at].y;
-    o.z += sums[g][at].z;
-    o.w += sums[g][at].w;
+  if constexpr (kGroups > 1) {
+    __syncthreads();
+    if (group) sums[group - 1][at] = o;
+    if (at == 0) red[group] = total;
+    __syncthreads();
+    if (group) return;
+    total = 0.0f;
+    for (uint32_t g = 0; g < kGroups; ++g) total += red[g];
+    for (uint32_t g = 0; g + 1 < kGroups; ++g) {
+      o.x += sums[g][at].x;
+      o.y += sums[g][at].y;
+      o.z += sums[g][at].z;
+      o.w += sums[g][at].w;
+    }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[at] =
@@ -735,11 +739,12 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.gridDim = dim3((unsigned)(nq * a.heads));
-    lc.blockDim = dim3(512);
+    const bool few = a.splits <= kFewSplits;
+    lc.blockDim = dim3(few ? 128 : 512);
     lc.stream = on;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    e = cudaLaunchKernelEx(&lc, join_kernel, (const float*)a.part, (const float*)a.part_lse, a.splits,
+    e = cudaLaunchKernelEx(&lc, few ? join_kernel<1> : join_kernel<4>, (const float*)a.part, (const float*)a.part_lse, a.splits,
                            nq * (int64_t)a.heads, a.out, a.lse);
   }
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;

@@ -55,7 +55,7 @@ struct AttendShape {
   static constexpr uint32_t kTmemCols = kHeads == 64 ? 512 : kHeads == 32 ? 256 : 128;
 };
 constexpr float kFar = 64.0f;                            // in powers of two
-constexpr int64_t kLeastRows = 32;                       // of a split
+constexpr int64_t kLeastRows = 64;                       // of a split
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -77,7 +77,7 @@ struct AttendArgs {
 };
 
 struct AttendShared {
-  uint64_t k_full[2], s_full, p_full, pv_done[2], voted[4], raw_full, raw_empty, drained;
+  uint64_t k_full[2], s_full, p_full, pv_done[2], voted[4], met[4], raw_full, raw_empty, drained;
   uint32_t tmem;
   uint32_t gave_up;
   uint32_t there[2][kLoadWarps];     // tile i's rows that are not masked, in i % 2: row r is bit r / 3 of word r % 3
@@ -109,18 +109,6 @@ __device__ __forceinline__ void dequant4(uint32_t bytes, float scale, float bias
     v[k] = fmaf(__uint_as_float(__byte_perm(u, 0x47000000u, 0x7504u | k << 4)), scale, bias);
   lo = bf16_pair(v[0], v[1]);
   hi = bf16_pair(v[2], v[3]);
-}
-
-// Barrier of the 128 threads of a quarter that also says whether any of them
-// brings `flag`.
-__device__ __forceinline__ bool quarter_sync_any(uint32_t quarter, bool flag) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)flag), "r"(1 + quarter)
-      : "memory");
-  return r != 0;
 }
 
 // One arrival for the whole warp, after all its lanes' accesses.
@@ -217,7 +205,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       mbar_init(&sh.k_full[i], kWorkerWarps);
       mbar_init(&sh.pv_done[i], 1);
     }
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.voted[i], 4);
+    for (uint32_t i = 0; i < 4; ++i) {
+      mbar_init(&sh.voted[i], 4);
+      mbar_init(&sh.met[i], 4);
+    }
     mbar_init(&sh.s_full, 1);
     mbar_init(&sh.p_full, kWorkerWarps);
     mbar_init(&sh.raw_full, kLoadWarps);
@@ -315,6 +306,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const uint32_t mine_row = quad * 32 + lane;          // of S^T
     if (lane < kCols) sh.column[warp][lane] = 0.0f;
     __syncwarp();
+    uint32_t meets = 0;                                  // times the references have moved
     bool unset = true;                                   // some column has no reference yet
     float top = -INFINITY;                               // lane c < kCols: column c's reference
     float sum[kCols];
@@ -417,7 +409,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
           }
         }
         if (lane < kCols) sh.top[quarter][quad][lane] = best;
-        if (quarter_sync_any(quarter, quit)) break;
+        warp_arrive(&sh.met[quarter], lane);
+        const bool all = wait_or_give_up(&sh.met[quarter], meets & 1, &sh.gave_up);
+        if (!__all_sync(0xffffffffu, all)) break;
+        ++meets;
         float alpha = 1.0f;
         if (lane < kCols) {
           best = fmaxf(fmaxf(sh.top[quarter][0][lane], sh.top[quarter][1][lane]),
@@ -652,7 +647,15 @@ struct Cut {
 
 Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
+  // Units of 64 heads by 64 rows: where they do not fill the GPU, fewer heads
+  // a CTA leave it less to store and give the rows to more of them.  2,048
+  // rows of 64 heads, with 16, 32 and 64 heads a CTA: one query 11.6, 11.4,
+  // 12.9 us, two 13.6, 13.3, 13.3, four 16.3, 15.8, 15.5, sixteen 34.7, 25.4,
+  // 22.5; 512 rows of one query 10.0, 11.1, 12.5.
+  const int64_t units = nq * ((heads + 63) / 64) * ((positions + 63) / 64);
+  const uint32_t most_heads = 4 * units <= device_sms() ? 16 : units <= device_sms() ? 32 : 64;
   c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
+  if (c.heads > most_heads) c.heads = most_heads;
   c.head_tiles = (heads + c.heads - 1) / c.heads;
   const int64_t ctas = nq * c.head_tiles, sms = device_sms(), most = (positions + kLeastRows - 1) / kLeastRows;
   int64_t splits = ctas >= sms ? 1 : sms / ctas;

@@ -190,6 +190,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ void sts4(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+// The value rounded to bf16.
+__device__ __forceinline__ void sts2(uint32_t addr, float x) {
+  asm volatile("{\n .reg .b16 h;\n cvt.rn.bf16.f32 h, %1;\n st.shared.b16 [%0], h;\n}" ::"r"(addr), "f"(x) : "memory");
+}
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }

@@ -98,17 +98,27 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Four int8 times a scale as bf16, rounded once.  A byte (plus 128) put into
-// bits 8-15 of the float 32768 makes 32768 + byte; times the scale, minus
-// (32768 + 128) * scale, is the exact product: both have at most 20 bits.
-__device__ __forceinline__ void dequant4(uint32_t bytes, float scale, float bias, uint32_t& lo, uint32_t& hi) {
+// The fp16 value of a half of `two`, times an fp16, plus an fp32: exact before
+// the one rounding to fp32.
+__device__ __forceinline__ float fma_low(uint32_t two, uint16_t b, float c) {
+  float r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n fma.rn.f32.f16 %0, l, %2, %3;\n}" : "=f"(r) : "r"(two), "h"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float fma_high(uint32_t two, uint16_t b, float c) {
+  float r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n fma.rn.f32.f16 %0, h, %2, %3;\n}" : "=f"(r) : "r"(two), "h"(b), "f"(c));
+  return r;
+}
+
+// Four int8 times a scale as bf16, rounded once.  A byte (plus 128) under the
+// byte 0x64 is the fp16 1024 + byte; times the scale, minus (1024 + 128) *
+// scale (exact: 4 and 11 bits), that is the exact product.
+__device__ __forceinline__ void dequant4(uint32_t bytes, uint16_t scale, float bias, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = bytes ^ 0x80808080u;
-  float v[4];
-#pragma unroll
-  for (uint32_t k = 0; k < 4; ++k)
-    v[k] = fmaf(__uint_as_float(__byte_perm(u, 0x47000000u, 0x7504u | k << 4)), scale, bias);
-  lo = bf16_pair(v[0], v[1]);
-  hi = bf16_pair(v[2], v[3]);
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140u), b = __byte_perm(u, 0x64646464u, 0x4342u);
+  lo = bf16_pair(fma_low(a, scale, bias), fma_high(a, scale, bias));
+  hi = bf16_pair(fma_low(b, scale, bias), fma_high(b, scale, bias));
 }
 
 // One arrival for the whole warp, after all its lanes' accesses.
@@ -349,8 +359,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
           for (uint32_t u = 0; u < S::kPasses; ++u) {
             if (slot + 64 * u >= rows) break;
-            const float s = __half2float(__ushort_as_half((uint16_t)(scales[u][part] >> k * 16)));
-            const float bias = -32896.0f * s;
+            const uint16_t s = (uint16_t)(scales[u][part] >> k * 16);
+            const float bias = -1152.0f * __half2float(__ushort_as_half(s));
             uint4 x, y;
             dequant4(lat[k][u].x, s, bias, x.x, x.y);
             dequant4(lat[k][u].y, s, bias, x.z, x.w);

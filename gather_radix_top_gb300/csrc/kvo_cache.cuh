@@ -13,6 +13,14 @@
 
 namespace kvo {
 
+// From the context (kvo_api.cu).  Its device status word, for calls that keep
+// no other state in it; KVO_EINVAL without a context, KVO_ECUDA for one that
+// must not launch.
+kvo_status usable_status(kvo_ctx* ctx, uint32_t** status);
+
+// Streaming multiprocessors of the current device (152 where none can be asked).
+int device_sms();
+
 // Division of n < 2^31 by a fixed d >= 1 as a product: with s = ceil(log2 d)
 // and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + (n m >> 32)) >> s, and
 // the sum stays below 2^32.

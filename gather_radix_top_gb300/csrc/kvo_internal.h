@@ -136,13 +136,6 @@ cudaError_t launch_ring_append(const void* src_dev, uint8_t* ring, uint32_t r, u
                                uint32_t* counters, uint32_t new_len, cudaStream_t stream);
 cudaError_t launch_probe(const void* src, uint64_t bytes, void* sink, cudaStream_t stream, uint64_t stride = 16);
 
-// The context's device status word, for calls that keep no other state in it;
-// KVO_EINVAL without a context, KVO_ECUDA for one that must not launch.
-kvo_status usable_status(kvo_ctx* ctx, uint32_t** status);
-
-// Streaming multiprocessors of the current device (152 where none can be asked).
-int device_sms();
-
 // Largest cluster size (16 non-portable, else 8, 4, 2) that can run with the
 // given kernel's resources; 0 if none.
 int best_cluster(const void* kernel, size_t smem, int want);

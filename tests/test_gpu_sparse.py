@@ -714,3 +714,21 @@ def test_pool_session_rows(kvo, ctx):
     assert ctx.sync() == kvo.KVO_OK
     assert torch.equal(back, flat)
     pool.close()
+
+
+@pytest.mark.parametrize("block", [1, 16])
+def test_example(block):
+    """The example's decode: with k past the context the selection is everything, and holds the whole softmax."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sparse_decode.py")
+    spec = importlib.util.spec_from_file_location("sparse_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    r = example.decode(sessions=2, prompt=300, steps=3, k=4_096 if block > 1 else 303, block=block)
+    # log-sum-exps of the same rows in another order: within the bound of their sums
+    assert (r["lse"] - r["all_lse"]).abs().max() < 1e-4 and abs(r["share"] - 1) < 1e-4
+    assert torch.isfinite(r["out"].float()).all()
+    some = example.decode(sessions=2, prompt=300, steps=2, k=64, block=block)
+    assert 0 < some["share"] < 1 and (some["lse"] < some["all_lse"]).all()
+    assert some["idx"].shape == (2, 64 // block) and (some["idx"].diff(dim=1) > 0).all()

@@ -569,20 +569,30 @@ def _key_type(t) -> int:
     return kind
 
 
-def _cuda(t, what: str, dtype, shape=None):
-    """data_ptr of a CUDA tensor of that type (and shape), its last dimension contiguous."""
-    if not t.is_cuda or t.dtype is not dtype:
+def _refuse(t, what: str, dtype, shape) -> None:
+    """The reason why _cuda or _flat does not take t."""
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{what} must be a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError(f"{what} must be contiguous in its last dimension")
+    raise ValueError(f"{what} must be contiguous in its last dimension")
+
+
+def _cuda(t, what: str, dtype, shape) -> int:
+    """data_ptr of a CUDA tensor of that type and shape, its last dimension contiguous."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape or (
+            not t.is_contiguous() and t.stride(-1) != 1 and shape[-1] > 1):
+        _refuse(t, what, dtype, shape)
     return t.data_ptr()
 
 
-def _whole(t, what: str):
+def _flat(t, what: str, dtype, shape) -> int:
+    """data_ptr of a contiguous CUDA tensor of that type and shape."""
+    if t.dtype is not dtype or not t.is_cuda or t.shape != shape:
+        _refuse(t, what, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=None, key=None,
@@ -623,16 +633,17 @@ def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=N
     del freq
 
 
-def _queries(cache: Cache, q, values: int) -> tuple:
+def _queries(cache: Cache, q, values: int, dtype) -> tuple:
+    """(address, queries, heads, queries of a sequence, strides of query and head) of q [queries, heads, values]."""
     if q.dim() != 3 or q.shape[2] != values:
         raise ValueError(f"q must be [queries, heads, {values}]")
-    nq = q.shape[0]
+    nq, heads, _ = shape = q.shape
     if nq < 1 or nq % cache.sequences:
         raise ValueError("the number of queries must be a multiple of the cache's sequences")
-    heads = q.shape[1]
+    ptr = _cuda(q, "q", dtype, shape)
+    q_ld, head_ld, _ = q.stride()
     # a dimension of one has no next element: its stride says nothing
-    strides = (q.stride(0) if nq > 1 else heads * values, q.stride(1) if heads > 1 else values)
-    return nq, heads, nq // cache.sequences, strides
+    return (ptr, nq, heads, nq // cache.sequences, q_ld if nq > 1 else heads * values, head_ld if heads > 1 else values)
 
 
 def kvo_index_scores(ctx: int, cache: Cache, q, weights, lens, n: int, block: int = 1, out=None, stream=None):
@@ -640,16 +651,16 @@ def kvo_index_scores(ctx: int, cache: Cache, q, weights, lens, n: int, block: in
     heads]; lens: int32 [nq].  Returns float32 [nq, ceil(n / block)] (`out`
     if given; its rows may be strided)."""
     T = _T()
-    nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, KEY_VALUES)
     keys = cache.tensors[1]
     if keys is None:
         raise ValueError("the cache has no keys")
+    q_ptr, nq, heads, per_seq, q_ld, q_head_ld = _queries(cache, q, KEY_VALUES, keys.dtype)
     cols = -(-n // block) if block > 0 else 0
     if out is None:
         out = _empty((nq, cols), T.float32, q.device, stream)
-    s = kvo_score_query(_cuda(q, "q", keys.dtype), _cuda(weights, "weights", T.float32, (nq, heads)),
-                        _cuda(lens, "lens", T.int32, (nq,)), _cuda(out, "out", T.float32, (nq, cols)), q_ld, q_head_ld,
-                        weights.stride(0), out.stride(0) if nq > 1 else cols, n, per_seq, heads, block)
+    s = kvo_score_query(q_ptr, _cuda(weights, "weights", T.float32, (nq, heads)), _cuda(lens, "lens", T.int32, (nq,)),
+                        _cuda(out, "out", T.float32, (nq, cols)), q_ld, q_head_ld, weights.stride(0),
+                        out.stride(0) if nq > 1 else cols, n, per_seq, heads, block)
     _check(lib().kvo_index_scores(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)),
            "kvo_index_scores")
     return out
@@ -675,7 +686,7 @@ def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None =
     strided) of positions, or of blocks of sel_block positions.  Returns (out
     bfloat16 [nq, heads, 512], lse float32 [nq, heads])."""
     T = _T()
-    nq, heads, per_seq, (q_ld, q_head_ld) = _queries(cache, q, DEQUANT_VALUES)
+    q_ptr, nq, heads, per_seq, q_ld, q_head_ld = _queries(cache, q, DEQUANT_VALUES, T.bfloat16)
     sel_ptr, sel_ld, picked = None, 0, 0
     if sel is None:
         if rows is None:
@@ -692,20 +703,21 @@ def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None =
         out = _empty((nq, heads, LATENT_VALUES), T.bfloat16, q.device, stream)
     if lse is None:
         lse = _empty((nq, heads), T.float32, q.device, stream)
-    _whole(out, "out")
-    _whole(lse, "lse")
-    work_ptr, need = None, lib().kvo_attend_work_bytes(nq, heads, positions)
+    L = lib()
+    work_ptr, need = None, L.kvo_attend_work_bytes(nq, heads, positions)
     if need > 0:
         if work is None:
-            work = _empty((need,), T.uint8, q.device, stream)
+            work = _empty(need, T.uint8, q.device, stream)
+        elif work.dtype is not T.uint8 or not work.is_cuda or not work.is_contiguous():
+            raise ValueError("work must be a contiguous uint8 CUDA tensor")
         else:
             need = work.numel()
-        work_ptr = _cuda(work, "work", T.uint8)
-    s = kvo_attend_query(_cuda(q, "q", T.bfloat16), _cuda(lens, "lens", T.int32, (nq,)), sel_ptr,
-                         _cuda(out, "out", T.bfloat16, (nq, heads, LATENT_VALUES)),
-                         _cuda(lse, "lse", T.float32, (nq, heads)), work_ptr, max(need, 0), q_ld, q_head_ld, sel_ld, rows,
+        work_ptr = work.data_ptr()
+    s = kvo_attend_query(q_ptr, _cuda(lens, "lens", T.int32, (nq,)), sel_ptr,
+                         _flat(out, "out", T.bfloat16, (nq, heads, LATENT_VALUES)),
+                         _flat(lse, "lse", T.float32, (nq, heads)), work_ptr, max(need, 0), q_ld, q_head_ld, sel_ld, rows,
                          picked, sel_block, per_seq, heads, scale)
-    _check(lib().kvo_attend(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)), "kvo_attend")
+    _check(L.kvo_attend(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)), "kvo_attend")
     return out, lse
 
 

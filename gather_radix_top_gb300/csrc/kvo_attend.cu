@@ -605,29 +605,45 @@ __global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, 
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial results are there
+  // the first partial results are asked for before their weights (past the
+  // first-level cache: this grid may have begun before they were written)
+  constexpr uint32_t kAhead = kGroups > 1 ? 8 : 2;
+  float4 v[kAhead];
+  auto load = [&](uint32_t from) {
+#pragma unroll
+    for (uint32_t k = 0; k < kAhead; ++k) {
+      const uint32_t s = from + k * kGroups;
+      if (s < splits) v[k] = __ldcg(reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * at));
+    }
+  };
+  load(group);
   float top = -INFINITY;
   for (uint32_t s = tid; s < splits; s += kThreads) {
-    weight[s] = part_lse[s * rows + r];
+    weight[s] = __ldcg(part_lse + s * rows + r);
     top = fmaxf(top, weight[s]);
   }
+#pragma unroll
   for (uint32_t d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) red[warp] = top;
   __syncthreads();
+#pragma unroll
   for (uint32_t w = 0; w < 4 * kGroups; ++w) top = fmaxf(top, red[w]);
   const float base = top == -INFINITY ? 0.0f : top;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
-#pragma unroll 8
-  for (uint32_t s = group; s < splits; s += kGroups) {
-    const float l = weight[s], w = exp2f(l - base);
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (l != -INFINITY)                                    // else nothing is there, and nothing was written
-      v = *reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * at);
-    total += w;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  for (uint32_t from = group; from < splits; from += kAhead * kGroups) {
+#pragma unroll
+    for (uint32_t k = 0; k < kAhead; ++k) {
+      const uint32_t s = from + k * kGroups;
+      const float w = s < splits ? exp2f(weight[s] - base) : 0.0f;
+      if (!(w > 0.0f) && !isnan(w)) continue;              // an empty split has written nothing
+      total += w;
+      o.x = fmaf(w, v[k].x, o.x);
+      o.y = fmaf(w, v[k].y, o.y);
+      o.z = fmaf(w, v[k].z, o.z);
+      o.w = fmaf(w, v[k].w, o.w);
+    }
+    load(from + kAhead * kGroups);
   }
   if constexpr (kGroups > 1) {
     __syncthreads();

@@ -579,6 +579,130 @@ def test_repeated_calls_give_the_same_bits(kvo, ctx):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("heads", [16, 32, 64])
+@pytest.mark.parametrize("order", ["rising", "falling", "jumps"])
+def test_attend_many_tiles_a_query(kvo, ctx, heads, order):
+    """Enough queries that each list stays with one CTA, and logits (in powers of two, up to +-700) that rise, fall or
+    jump along it: references move, accumulators are rescaled, early weights vanish."""
+    rng = np.random.default_rng([39, heads, len(order)])
+    n, nq = 700, 170
+    rows = random_rows(rng, n)
+    level = {"rising": np.linspace(-40, 40, n), "falling": np.linspace(40, -40, n),
+             "jumps": np.where(np.arange(n) // 90 % 3 == 1, 40.0, -40.0) * (np.arange(n) > 200)}[order]
+    for j in range(n):
+        x = np.zeros(64)
+        x[0] = level[j]
+        rows[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+    q = rng.standard_normal((nq, heads, 576))
+    q[..., 512] = np.linspace(-12, 12, heads)
+    q = dev(q, torch.bfloat16)
+    lens = rng.integers(1, n + 1, nq)
+    lens[3], lens[77], lens[160] = n, 81, 80
+    cache = kvo.Cache(rows=dev(rows), block_rows=n)
+    out, lse = ctx.attend(cache, q, dev(lens, torch.int32), 1.0, rows=n)
+    assert ctx.sync() == kvo.KVO_OK
+    for t in (0, 3, 77, 160, 169):
+        check_attend(out[t:t + 1], lse[t:t + 1], q[t:t + 1], 1.0, [list(rows[:lens[t]])], heads)
+
+
+def test_attend_far_into_a_large_cache(kvo, ctx):
+    """Rows whose byte offsets pass 2^31 and 2^32, and whose row numbers differ only there."""
+    rng = np.random.default_rng(40)
+    total = 7_000_000                                        # 4.6 GB
+    rows = torch.zeros(total, 656, dtype=torch.uint8, device="cuda")
+    small = random_rows(rng, 64)
+    at = np.array([5, 3_300_000, 6_600_000, 6_999_984 // 16 * 16]) // 16
+    for b, i in enumerate(at):
+        rows[i * 16:(i + 1) * 16] = dev(small[16 * b:16 * b + 16])
+    table = torch.tensor(at[None], dtype=torch.int32, device="cuda")
+    cache = kvo.Cache(rows=rows, block_rows=16, table=table)
+    q = dev(rng.standard_normal((1, 20, 576)), torch.bfloat16)
+    out, lse = ctx.attend(cache, q, dev([64], torch.int32), 0.07, rows=64)
+    assert ctx.sync() == kvo.KVO_OK
+    check_attend(out, lse, q, 0.07, [list(small)], 20)
+    kv = dev(rng.standard_normal((1, 576)), torch.bfloat16)
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], dev([63], torch.int32), INV_FREQ)
+    assert ctx.sync() == kvo.KVO_OK
+    got = rows[int(at[3]) * 16 + 15].cpu().numpy()
+    for group in range(8):
+        want, bits = O.latent_group(f64(kv)[0, 64 * group:64 * group + 64])
+        assert np.array_equal(got[64 * group:64 * group + 64].view(np.int8), want)
+        assert int(got[512 + 2 * group:514 + 2 * group].view(np.uint16)[0]) == bits
+
+
+def test_scores_far_into_a_large_cache(kvo, ctx):
+    rng = np.random.default_rng(41)
+    total = 36_000_000                                       # 4.6 GB of e4m3 keys
+    keys = torch.zeros(total, 128, dtype=torch.uint8, device="cuda")
+    q, k, scales, w = score_inputs(rng, 1, 16, 64, "e4m3")
+    every = torch.zeros(total, device="cuda")
+    at = np.array([7, 17_000_000, 34_000_000, total - 16]) // 16
+    for b, i in enumerate(at):
+        keys[i * 16:(i + 1) * 16] = k.view(torch.uint8)[16 * b:16 * b + 16]
+        every[i * 16:(i + 1) * 16] = scales[16 * b:16 * b + 16]
+    cache = kvo.Cache(keys=keys.view(torch.float8_e4m3fn), key_scales=every, block_rows=16,
+                      table=torch.tensor(at[None], dtype=torch.int32, device="cuda"))
+    got = ctx.index_scores(cache, q, w, dev([64], torch.int32), 64)
+    assert ctx.sync() == kvo.KVO_OK
+    check_scores(got, q, k, scales, w, [list(range(64))], [64], 64, 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 100])
+def test_scores_tiny_contiguous_caches(kvo, ctx, dtype, n):
+    """Caches with fewer keys than a tile, without a table: what lies past them is never looked at."""
+    rng = np.random.default_rng([42, n])
+    q, k, scales, w = score_inputs(rng, 2, 33, 2 * n, dtype)
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=n)
+    got = ctx.index_scores(cache, q, w, dev([n, n], torch.int32), n)
+    assert ctx.sync() == kvo.KVO_OK
+    check_scores(got, q, k, scales, w, [list(range(n)), list(range(n, 2 * n))], [n, n], n, 1)
+
+
+def test_strided_tables(kvo, ctx):
+    """A table that is a part of a wider one."""
+    rng = np.random.default_rng(43)
+    wide = torch.full((3, 9), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    table = wide[:, 2:5]
+    ids, total = block_table(rng, 3, 3)
+    table.copy_(dev(ids))
+    rows = random_rows(rng, total * 16)
+    q, k, scales, w = score_inputs(rng, 3, 8, total * 16, "e4m3")
+    cache = kvo.Cache(rows=dev(rows), keys=k, key_scales=scales, block_rows=16, table=table)
+    lens = [48, 20, 33]
+    qa = dev(rng.standard_normal((3, 9, 576)), torch.bfloat16)
+    out, lse = ctx.attend(cache, qa, dev(lens, torch.int32), 0.07, rows=48)
+    got = ctx.index_scores(cache, q, w, dev(lens, torch.int32), 48)
+    assert ctx.sync() == kvo.KVO_OK
+    where = [[O.row_of(ids, total, 16, 3, s, p) for p in range(48)] for s in range(3)]
+    check_attend(out, lse, qa, 0.07, [[rows[r] for r in where[s][:lens[s]]] for s in range(3)], 9)
+    check_scores(got, q, k, scales, w, where, lens, 48, 1)
+
+
+def test_binding_refuses_wrong_shapes(kvo, ctx):
+    rows = torch.zeros(32, 656, dtype=torch.uint8, device="cuda")
+    cache = kvo.Cache(rows=rows, block_rows=16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.zeros(2, 4, 576, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:, :, :512]), dict(q=q[:1]), dict(q=q.transpose(1, 2)), dict(lens=i32(3)),
+                dict(lens=i32(2).long()), dict(rows=None), dict(sel=i32(2)), dict(sel=i32(3, 4)),
+                dict(out=torch.zeros(2, 4, 512, device="cuda")), dict(lse=torch.zeros(2, 5, device="cuda")),
+                dict(out=torch.zeros(2, 512, 4, dtype=torch.bfloat16, device="cuda").transpose(1, 2))):
+        with pytest.raises(ValueError):
+            ctx.attend(cache, **{**dict(q=q, lens=i32(2), scale=0.1, rows=16), **bad})
+    with pytest.raises(ValueError):
+        ctx.index_scores(cache, q[..., :128], torch.zeros(2, 4, device="cuda"), i32(2), 16)
+    kv = torch.zeros(2, 576, device="cuda")
+    for bad in (dict(latent=kv[:, :500]), dict(latent=kv[:, :512].double()), dict(rope=kv[:, 512:].bfloat16()),
+                dict(pos=i32(3)), dict(inv_freq=INV_FREQ[:8]), dict(seq=i32(2).long()), dict(latent=kv[:, :512].cpu())):
+        with pytest.raises(ValueError):
+            ctx.append_tokens(cache, **{**dict(latent=kv[:, :512], rope=kv[:, 512:], pos=i32(2), inv_freq=INV_FREQ),
+                                        **bad})
+    with pytest.raises(kvo.KvoError):                        # no keys in the cache
+        ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], i32(2), INV_FREQ, key=torch.zeros(2, 128, device="cuda"))
+    assert ctx.sync() == kvo.KVO_OK
+
+
 # ------------------------------------------------------------- streams, graphs
 def decode_step(kvo, ctx, st, stream=None):
     ctx.append_tokens(st["cache"], st["kv"][:, :512], st["kv"][:, 512:], st["pos"], INV_FREQ, key=st["key"],

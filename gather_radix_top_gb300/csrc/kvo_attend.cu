@@ -1,19 +1,23 @@
 // kvo_attend: softmax attention of absorbed MLA queries over cached rows.
 //
 // One CTA holds up to 64 heads of one query and walks over tiles of 80 or 96
-// rows of its list.  A tile's 656-byte rows come through registers, are
-// dequantised once to bf16 and written to shared memory; both products then
-// run on the tensor cores with the rows' operand as A:
-//     S^T [128 rows x heads]   = K [128 x 576] Q^T          (K contiguous)
-//     O^T [512 values x heads] += V^T [512 x 128] P^T       (the same bytes, read
+// rows of its list.  Whole 656-byte rows come into shared memory by bulk
+// copies, are dequantised once to bf16 in the tensor cores' layout, and both
+// products take the rows' operand as A:
+//     S^T [rows x heads]       = K [rows x 576] Q^T         (K contiguous)
+//     O^T [512 values x heads] += V^T [512 x rows] P^T      (the same bytes, read
 //                                along the other dimension, as 4 x 128 values)
-// With the heads as columns M is full whatever the number of heads, and the
-// accumulators fit: O^T needs 4 x 64 of the 512 columns of tensor memory, which
-// 128 heads by 512 values as rows would fill.  Shared memory holds one tile
-// (144 KB) and the queries (72 KB); P^T takes the place of the position part,
-// which the second product does not read.  Parts of the tile are refilled as
-// the second product releases them, and the next tile's bytes are on their
-// way meanwhile.
+// With the heads as columns the accumulators fit: O^T needs 4 x 64 of the 512
+// columns of tensor memory, which 128 heads by 512 values as rows would fill,
+// and M is full for few heads too.  Shared memory holds the queries (72 KB for
+// 64 heads), one dequantised tile (90 KB for 80 rows) and the next tile's raw
+// rows (55 KB).  P^T takes the place of the position part, which the second
+// product does not read.
+//
+// Sixteen worker warps dequantise and do the softmax, three warps bring rows,
+// one issues the MMAs.  A tile goes through in two parts of 256 values: a part
+// is dequantised as soon as the second product of the last tile has released
+// its place, and multiplied while the other part is dequantised.
 //
 // The softmax is over the lanes of S^T.  Its reference is not the running
 // maximum but the maximum at some earlier tile: weights of up to 2^64 lose
@@ -24,6 +28,22 @@
 //
 // Long lists with few queries are split over CTAs, whose normalised partial
 // results a second launch joins by their log-sum-exps.
+//
+// What bounds it.  A tile of 80 rows and 64 heads takes 2.85 us (5,700 clocks),
+// of which the MMAs are 2,700: with 64 columns they are bound by shared memory
+// (48 clocks each, 65 with 128 columns), which the dequantised tile's stores
+// (720), the raw rows (820) and the queries share.  The softmax (about 1,450
+// from scores to weights) and the hand-overs are the rest: with one tile in
+// shared memory nothing else of the tensor cores' work can run beside it.
+//     1,048,576 rows of one query with 128 heads    490 us, 597 TFLOP/s
+//     64 queries of 64 heads and 2,048 positions     52 us, 1.8 TB/s
+//     2,048 rows of one query with 64 heads         11.1 us
+// Measured on the way, the first of them in us: rows through registers 942
+// (next to this much shared memory the SM keeps about 28 KB of loads in
+// flight), eight worker warps and one loading warp 672, three loading warps
+// 647, references that move seldom and MMAs issued by one elected lane of a
+// converged warp 525 (by a divergent thread 664), two parts instead of five
+// 501, multiply-adds on fp16 operands in the dequantisation 491.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

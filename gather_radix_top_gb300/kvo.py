@@ -532,7 +532,14 @@ class Cache:
             c.sequences, c.table_blocks = table.shape
             c.table_ld = max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else table.stride(0)
         self.sequences, self.block_rows, self.blocks = c.sequences, c.block_rows, c.blocks
-        self.ref = ctypes.addressof(c)
+        self.pool = rows if isinstance(rows, Pool) else None
+
+    @property
+    def ref(self) -> int:
+        """The address of the kvo_cache."""
+        if self.pool is not None and not self.pool.handle:
+            raise ValueError("the cache's pool is closed")
+        return ctypes.addressof(self.c)
 
 
 class _Torch:

@@ -484,7 +484,9 @@ kvo_status kvo_debug_history_host(kvo_ctx* ctx, int32_t layer, void** out);
  *
  * The calls keep nothing between them.  Every tensor has to be ready on
  * `stream`; calls on several streams may overlap as long as they do not
- * share `work` or an output.  All of them can be captured into a CUDA graph.
+ * share `work` or an output.  All of them can be captured into a CUDA graph,
+ * after a first call of the same kind outside a capture, which loads the
+ * kernels.
  * ---------------------------------------------------------------------- */
 
 /* Element types. */

@@ -856,3 +856,33 @@ def test_example(block):
     some = example.decode(sessions=2, prompt=300, steps=2, k=64, block=block)
     assert 0 < some["share"] < 1 and (some["lse"] < some["all_lse"]).all()
     assert some["idx"].shape == (2, 64 // block) and (some["idx"].diff(dim=1) > 0).all()
+
+
+def test_an_unusable_context_refuses(kvo):
+    """After a wait whose copies may still land, nothing more is launched."""
+    c = kvo.Context(1, 64, 64)
+    c.raise_status(4 | 8)
+    assert c.sync() == kvo.KVO_ETIMEDOUT
+    rows = torch.zeros(16, 656, dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
+    cache = kvo.Cache(rows=rows, keys=keys, block_rows=16)
+    lens = torch.full((1,), 16, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(1, 576, device="cuda").bfloat16()
+    for call in (lambda: c.append_tokens(cache, kv[:, :512], kv[:, 512:], lens - 1, INV_FREQ),
+                 lambda: c.index_scores(cache, kv[None, :, :128], torch.zeros(1, 1, device="cuda"), lens, 16),
+                 lambda: c.attend(cache, kv[None], lens, 0.1, rows=16)):
+        with pytest.raises(kvo.KvoError) as e:
+            call()
+        assert e.value.status == kvo.KVO_ECUDA
+    torch.cuda.synchronize()
+    assert not rows.any()
+    c.close()
+
+
+def test_a_closed_pool_is_refused(kvo, ctx):
+    pool = kvo.Pool(layers=1, pool_blocks=2, block_tokens=16, tier_blocks=0)
+    cache = kvo.Cache(rows=pool)
+    pool.close()
+    with pytest.raises(ValueError):
+        ctx.attend(cache, torch.zeros(2, 1, 576, dtype=torch.bfloat16, device="cuda"),
+                   torch.ones(2, dtype=torch.int32, device="cuda"), 0.1, rows=16)

@@ -791,6 +791,30 @@ def test_outputs_made_on_a_given_stream(kvo, ctx):
     assert torch.equal(out, st["out"]) and torch.equal(lse, st["lse"]) and torch.equal(scores, st["scores"])
 
 
+def test_two_streams_at_once(kvo, ctx):
+    """Steps of two independent states on two streams, interleaved: neither changes the other's bits."""
+    states, want, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed, (n, k, heads) in enumerate([(3000, 2048, 64), (700, 96, 20)]):
+        st, rand = decode_state(kvo, 60 + seed, S=2 + seed, n=n, k=k, heads=heads)
+        prefill(kvo, ctx, st, rand)
+        decode_step(kvo, ctx, st)
+        states.append(st)
+    assert ctx.sync() == kvo.KVO_OK
+    names = ("rows", "scores", "idx", "out", "lse")
+    for st in states:
+        want.append([st[k].clone() for k in names])
+        for k in names[1:]:
+            st[k].zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, stream in zip(states, streams):
+            decode_step(kvo, ctx, st, stream=stream)
+    torch.cuda.synchronize()
+    for st, w in zip(states, want):
+        assert all(torch.equal(a, st[k]) for a, k in zip(w, names))
+    assert ctx.sync() == kvo.KVO_OK
+
+
 # ----------------------------------------------------------- with the rest
 def test_gathered_rows_attend_like_the_pool(kvo):
     """append -> history -> one decode step's gathered rows -> attend gives what attending in place gives."""

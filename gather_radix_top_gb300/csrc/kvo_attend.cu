@@ -596,8 +596,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
       __syncwarp();
     }
-    if (!__all_sync(0xffffffffu, ok) && lane == 0) {
+    if (!__all_sync(0xffffffffu, ok) && elect_one()) {
       // let the MMAs in flight finish before their memory is given back
+      // (the lane that issued them commits)
       mma_commit(&sh.drained);
       atomicOr(a.status, kFlagTimeout);
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);

@@ -44,18 +44,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// The same with the operands' descriptors advanced by kA and kB (in units of
-// 16 bytes): formed at the MMA, for a long unrolled sequence would otherwise
-// keep every one of them in registers of its own.
-template <uint32_t kA, uint32_t kB>
-__device__ __forceinline__ void mma_bf16_at(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n add.s64 x, %1, %5;\n add.s64 y, %2, %6;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kA), "n"(kB)
-      : "memory");
-}
-
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
@@ -133,12 +121,6 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, const float* v) {
                "r"(r[3]), "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -189,13 +171,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void sts4(uint32_t addr, float x) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
-// The value rounded to bf16.
-__device__ __forceinline__ void sts2(uint32_t addr, float x) {
-  asm volatile("{\n .reg .b16 h;\n cvt.rn.bf16.f32 h, %1;\n st.shared.b16 [%0], h;\n}" ::"r"(addr), "f"(x) : "memory");
 }
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");

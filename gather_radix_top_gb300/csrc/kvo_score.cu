@@ -9,19 +9,20 @@
 //
 // One CTA per SM, each over every gridDim.x-th key tile of one group of
 // query tokens: a warp brings key tiles into a ring in shared memory
-// (a TMA box per run of keys of one block, looked up in the table), one
-// thread issues the MMAs into accumulators in tensor memory, and four
+// (a TMA box per run of keys of one block, looked up in the table), another
+// issues the MMAs into accumulators in tensor memory, and four
 // teams of four warps reduce them in turn.  Nothing but the queries and the
 // scores passes through global memory twice.
 //
 // What bounds it: up to 128 columns, reading the keys (132 bytes a key as e4m3,
-// 256 as bf16) after about 5 us of launch, queries and first keys: a million
-// keys take 28.8 us as one run of e4m3 (4.8 TB/s), 30.1 in shuffled blocks of
-// 16 and 43.0 as bf16 (6.2 TB/s), whether for 16 or 64 heads.  For 256
+// 256 as bf16) after about 4.5 us of launch, queries and first keys: a million
+// keys take 25.6 us as one run of e4m3 (5.4 TB/s), 28.4 in shuffled blocks of
+// 16 and 42.4 as bf16 (6.3 TB/s), whether for 16 or 64 heads.  For 256
 // columns (four tokens of 64 heads), the epilogue's two operations per
-// product: 262,144 keys take 19.3 us against 10.5 for one token.  One loading warp
-// alone was 45.2 us for the million (it issues a box every 60 clocks), and
-// table entries that are used as soon as they are asked for 48.2.
+// product: 262,144 keys take 18.9 us against 9.7 for one token.  Slower ones, for
+// the million in blocks: MMAs from one thread of a diverged warp 30.3 us, one
+// loading warp alone 45.2 (it issues a box every 60 clocks), table entries
+// that are used as soon as they are asked for 48.2.
 #include <cuda.h>
 
 #include "kvo_cache.cuh"
@@ -278,7 +279,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         for (uint32_t i = next < S::kStages + kLoadWarps ? turn0 : next - S::kStages; i < next; ++i)
           if ((i - turn0) % kLoadWarps == 0 && !landed(&sh.full[i % S::kStages], (i / S::kStages) & 1))
             atomicOr(a.status, kFlagInflight);
-    } else if (lane == 0) {
+    } else {
+      // the whole warp walks along, one elected lane issues: what a converged
+      // warp computes stays in the uniform registers that the MMAs read
       const uint32_t idesc = mma_desc(kF8 ? 0u : 1u, cols, false, false);
       const uint64_t keys = tile_desc(ring, 16), heads = tile_desc(queries, 16);
       const uint64_t next_half = (cols * 128) >> 4;
@@ -286,30 +289,35 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       for (uint32_t i = 0, slot = 0, slot_turn = 0, acc = 0, acc_turn = 0; i < mine; ++i) {
         ok = wait_or_give_up(&sh.full[slot], slot_turn & 1, &sh.gave_up) &&
              (acc_turn == 0 || wait_or_give_up(&sh.acc_empty[acc], (acc_turn - 1) & 1, &sh.gave_up));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t tile = keys + slot * (S::kTileBytes >> 4);
         const uint32_t d = tmem + acc * cols;
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t k = 0; k < S::kKeyBytes / 32; ++k) {      // 32 bytes of K per MMA
-          const uint64_t da = tile + (k >> 2) * (kKeyTile * 128 >> 4) + (k & 3) * 2;
-          const uint64_t db = heads + (k >> 2) * next_half + (k & 3) * 2;
-          if (kF8)
-            mma_f8(d, da, db, idesc, k > 0);
-          else
-            mma_bf16(d, da, db, idesc, k > 0);
+          for (uint32_t k = 0; k < S::kKeyBytes / 32; ++k) {    // 32 bytes of K per MMA
+            const uint64_t da = tile + (k >> 2) * (kKeyTile * 128 >> 4) + (k & 3) * 2;
+            const uint64_t db = heads + (k >> 2) * next_half + (k & 3) * 2;
+            if (kF8)
+              mma_f8(d, da, db, idesc, k > 0);
+            else
+              mma_bf16(d, da, db, idesc, k > 0);
+          }
+          mma_commit(&sh.empty[slot]);
+          mma_commit(&sh.acc_full[acc]);
         }
-        mma_commit(&sh.empty[slot]);
-        mma_commit(&sh.acc_full[acc]);
+        __syncwarp();
         if (++slot == S::kStages) slot = 0, ++slot_turn;
         if (++acc == a.accs) acc = 0, ++acc_turn;
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         // let the MMAs in flight finish before their memory is given back
         mma_commit(&sh.drained);
         atomicOr(a.status, kFlagTimeout);
         if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
       }
+      __syncwarp();
     }
     tc_fence_before();
     __syncthreads();

@@ -7,10 +7,10 @@
 // key four values a lane, and nothing needs shared memory or a barrier.
 //
 // What bounds it: 60,000 bf16 tokens with e4m3 keys and the dequantised copy
-// (201 MB) take 40.0 us, 5.0 TB/s, where a copy of the bytes would take 30:
+// (201 MB) take 39.9 us, 5.0 TB/s, where a copy of the bytes would take 30:
 // about 450 instructions a token fill the schedulers to 60 % while the loads'
 // latency is covered by 40 warps an SM.  16,381 fp32 tokens (78 MB) take 12.4
-// us, 6.3 TB/s.  One token takes 2.5 us, most of it launch.  Measured against
+// us, 6.3 TB/s.  One token takes 2.3 us, most of it launch.  Measured against
 // it for the 60,000: lookups before the loads 53 us, CTAs of 256 threads 45.6,
 // 64 registers (32 warps an SM) 42.6, half a warp per token (120 registers)
 // 56, a persistent loop that loads one token ahead 46.6.
@@ -120,6 +120,8 @@ template <typename T>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) append_tokens_kernel(const __grid_constant__ AppendArgs a) {
   const uint32_t lane = threadIdx.x & 31;
   const int64_t i = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
+  wait_previous_grid();
+  allow_next_grid();
   if (i >= a.n) return;
 
   // the token's values are asked for before its place is looked up, so that
@@ -297,13 +299,10 @@ extern "C" kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, co
   for (int i = 0; i < 32; ++i) a.turn[i] = turns_of(t->inv_freq[i]);
   a.interleaved = t->interleaved ? 1u : 0u;
   a.key_type = (uint32_t)cache->key_type;
-  const unsigned grid = (unsigned)((t->n + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+  const dim3 grid((unsigned)((t->n + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (t->dtype == KVO_BF16)
-    append_tokens_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, s>>>(a);
-  else if (t->dtype == KVO_FP16)
-    append_tokens_kernel<__half><<<grid, kAppendThreads, 0, s>>>(a);
-  else
-    append_tokens_kernel<float><<<grid, kAppendThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KVO_OK : KVO_ECUDA;
+  const auto kernel = t->dtype == KVO_BF16   ? append_tokens_kernel<__nv_bfloat16>
+                      : t->dtype == KVO_FP16 ? append_tokens_kernel<__half>
+                                             : append_tokens_kernel<float>;
+  return launch_early(kernel, grid, kAppendThreads, 0, s, a) == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -35,9 +35,9 @@
 // (720), the raw rows (820) and the queries share.  The softmax (about 1,450
 // from scores to weights) and the hand-overs are the rest: with one tile in
 // shared memory nothing else of the tensor cores' work can run beside it.
-//     1,048,576 rows of one query with 128 heads    490 us, 597 TFLOP/s
+//     1,048,576 rows of one query with 128 heads    486 us, 602 TFLOP/s
 //     64 queries of 64 heads and 2,048 positions     52 us, 1.8 TB/s
-//     2,048 rows of one query with 64 heads         11.1 us
+//     2,048 rows of one query with 64 heads         10.9 us
 // Measured on the way, the first of them in us: rows through registers 942
 // (next to this much shared memory the SM keeps about 28 KB of loads in
 // flight), eight worker warps and one loading warp 672, three loading warps
@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes;
   const uint32_t stage = queries + S::kQueryBytes;
 
+  wait_previous_grid();
+  allow_next_grid();
   const int32_t len = a.lens[t];
   // this CTA's entries of the list: from `first` on, `count` of them.  (With a
   // list nothing here waits for len: an empty query finds all of it masked.)
@@ -216,7 +218,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   const uint32_t head = h0 + quarter * kCols;
   const uint32_t mine = a.heads > head ? min(kCols, a.heads - head) : 0;   // real columns
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tiles == 0) {
     if (warp >= kWorkerWarps) return;
     const int64_t out_row = (int64_t)t * a.heads + head;
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, 
   __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][128];
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial results are there
+  wait_previous_grid();                                    // the partial results are there
   // the first partial results are asked for before their weights (past the
   // first-level cache: this grid may have begun before they were written)
   constexpr uint32_t kAhead = kGroups > 1 ? 8 : 2;
@@ -724,8 +725,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
-  attend_kernel<kHeads><<<dim3(a.head_tiles * a.splits, a.nq), kAttendThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(attend_kernel<kHeads>, dim3(a.head_tiles * a.splits, a.nq), kAttendThreads, smem, stream, a);
 }
 
 }  // namespace
@@ -783,19 +783,9 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
                   : cut.heads == 32 ? launch_attend<32>(a, on)
                                     : launch_attend<64>(a, on);
   if (e == cudaSuccess && a.splits > 1) {
-    // launched while the attention runs, it waits on the GPU for its end
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.gridDim = dim3((unsigned)(nq * a.heads));
     const bool few = a.splits <= kFewSplits;
-    lc.blockDim = dim3(few ? 128 : 512);
-    lc.stream = on;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    e = cudaLaunchKernelEx(&lc, few ? join_kernel<1> : join_kernel<4>, (const float*)a.part, (const float*)a.part_lse, a.splits,
-                           nq * (int64_t)a.heads, a.out, a.lse);
+    e = launch_early(few ? join_kernel<1> : join_kernel<4>, dim3((unsigned)(nq * a.heads)), few ? 128 : 512, 0, on, a.part,
+                     a.part_lse, a.splits, nq * (int64_t)a.heads, a.out, a.lse);
   }
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

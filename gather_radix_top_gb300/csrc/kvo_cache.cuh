@@ -21,6 +21,31 @@ kvo_status usable_status(kvo_ctx* ctx, uint32_t** status);
 // Streaming multiprocessors of the current device (152 where none can be asked).
 int device_sms();
 
+// The operators' launches may be scheduled while the work before them on the
+// stream still ends, and every thread waits here, before its first access to
+// memory, until that has completed and is visible.  The launch after them may
+// be scheduled once all their CTAs run.  Replayed from a graph that takes 0.2
+// to 0.9 us off a call (one appended token 2.5 to 2.3, 50,023 scores 5.2 to
+// 4.85, those of four tokens 8.25 to 7.7).
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t stream,
+                                const A&... args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
+}
+
 // Division of n < 2^31 by a fixed d >= 1 as a product: with s = ceil(log2 d)
 // and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + (n m >> 32)) >> s, and
 // the sum stays below 2^32.

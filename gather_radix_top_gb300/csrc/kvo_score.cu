@@ -15,14 +15,14 @@
 // scores passes through global memory twice.
 //
 // What bounds it: up to 128 columns, reading the keys (132 bytes a key as e4m3,
-// 256 as bf16) after about 4.5 us of launch, queries and first keys: a million
-// keys take 25.6 us as one run of e4m3 (5.4 TB/s), 28.4 in shuffled blocks of
-// 16 and 42.4 as bf16 (6.3 TB/s), whether for 16 or 64 heads.  For 256
+// 256 as bf16) after about 4 us of launch, queries and first keys: a million
+// keys take 25.5 us as one run of e4m3 (5.4 TB/s), 27.5 in shuffled blocks of
+// 16 and 42.1 as bf16 (6.4 TB/s), whether for 16 or 64 heads.  For 256
 // columns (four tokens of 64 heads), the epilogue's two operations per
-// product: 262,144 keys take 18.9 us against 9.7 for one token.  Slower ones, for
-// the million in blocks: MMAs from one thread of a diverged warp 30.3 us, one
-// loading warp alone 45.2 (it issues a box every 60 clocks), table entries
-// that are used as soon as they are asked for 48.2.
+// product: 262,144 keys take 18.3 us against 9.3 for one token.  Slower ones, for
+// the million in blocks: MMAs from one thread of a diverged warp 30.3 us (28.4
+// by then), one loading warp alone 45.2 (it issues a box every 60 clocks), table
+// entries that are used as soon as they are asked for 48.2.
 #include <cuda.h>
 
 #include "kvo_cache.cuh"
@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
   const uint32_t cols = a.group * a.head_cols;
   const uint32_t ring = smem_u32(smem), queries = ring + S::kStages * S::kTileBytes;
 
+  wait_previous_grid();
+  allow_next_grid();
   int32_t most = 0;                                             // positions that any of the tokens sees
   for (uint32_t g = 0; g < tokens; ++g) most = max(most, min(a.lens[t0 + g], (int32_t)a.n));
   const uint32_t tiles = ((uint32_t)most + kKeyTile - 1) / kKeyTile;
@@ -376,8 +378,7 @@ cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, uint32_t seque
   const uint32_t rows = sequences * a.groups, sms = (uint32_t)device_sms(), tiles = (a.n + kKeyTile - 1) / kKeyTile;
   uint32_t x = rows <= sms ? sms / rows : (4 * sms + rows - 1) / rows;
   if (x > tiles) x = tiles;
-  index_scores_kernel<kF8><<<dim3(x, rows), kScoreThreads, smem, stream>>>(a, map);
-  return cudaGetLastError();
+  return launch_early(index_scores_kernel<kF8>, dim3(x, rows), kScoreThreads, smem, stream, a, map);
 }
 
 }  // namespace
@@ -423,8 +424,8 @@ extern "C" kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, con
   a.tmem_cols = 128;
   while (a.tmem_cols < a.accs * a.group * a.head_cols) a.tmem_cols *= 2;
   // the largest power of two that divides both a tile and a block; without a
-  // table a sequence is one block.  A million e4m3 keys take 30.1 us in runs of
-  // 16, 42.2 as gathered rows (blocks of 5).
+  // table a sequence is one block.  A million e4m3 keys take 27.5 us in runs of
+  // 16, 41.3 as gathered rows (blocks of 5).
   a.run = kKeyTile;
   while (cache->table && a.run > 1 && cache->block_rows % a.run) a.run /= 2;
   if (a.run < 4) a.run = 1;

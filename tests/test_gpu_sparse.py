@@ -447,6 +447,35 @@ def test_attend_selected(kvo, ctx, sequences, per_seq, heads, n, sel_block, pick
     attend_case(kvo, ctx, rng, sequences, per_seq, heads, n, sel_block, picked, block_rows)
 
 
+@pytest.mark.parametrize("sequences,heads", [(18, 64), (20, 64), (24, 50), (28, 64), (18, 128), (45, 64), (70, 33), (40, 20),
+                                             (60, 16)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_attend_a_few_splits_a_query(kvo, ctx, sequences, heads, listed):
+    """Between 18 and 76 queries share the SMs, so that two to eight CTAs join their parts of each; some parts are
+    empty (whole sequences of a few rows) or see nothing (listed positions past the length)."""
+    rng = np.random.default_rng([sequences, heads, listed])
+    n = 640
+    lens = rng.integers(0, n + 1, sequences)
+    lens[:6] = n, 0, 1, 17, 81, 320
+    attend_case(kvo, ctx, rng, sequences, 1, heads, n, 1, 600 if listed else None, 16, lens=lens)
+
+
+def test_attend_nan_in_one_split(kvo, ctx):
+    """A NaN that one of three CTAs sees reaches the whole result of its query, and no other query's."""
+    rng = np.random.default_rng(39)
+    n, nq = 400, 45
+    rows = random_rows(rng, nq * n)
+    rows[3 * n + 350, 512:514] = 0xFF
+    cache = kvo.Cache(rows=dev(rows), block_rows=n)
+    q = dev(rng.standard_normal((nq, 64, 576)), torch.bfloat16)
+    lens = [n] * nq
+    out, lse = ctx.attend(cache, q, dev(lens, torch.int32), 0.07, rows=n)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.isnan(lse[3]).all() and torch.isnan(out[3][:, :64]).all()
+    keep = [t for t in range(nq) if t != 3][:8]
+    check_attend(out[keep], lse[keep], q[keep], 0.07, [list(rows[t * n:(t + 1) * n]) for t in keep], 64)
+
+
 @pytest.mark.parametrize("heads", [16, 64])
 def test_attend_odd_lists(kvo, ctx, heads):
     """Padding entries, repeated ones, entries past the length, in no order; a list with nothing visible."""
@@ -789,6 +818,71 @@ def test_outputs_made_on_a_given_stream(kvo, ctx):
         scores = ctx.index_scores(st["cache"], st["qi"], st["w"], st["lens"], st["n"], stream=side)
     side.synchronize()
     assert torch.equal(out, st["out"]) and torch.equal(lse, st["lse"]) and torch.equal(scores, st["scores"])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_written_just_before_and_spoilt_just_after(kvo, ctx, captured):
+    """Every call's launch may be scheduled while the work before it runs: it reads nothing that slow kernels on its
+    own stream and on another that it waits for have yet to write, and kernels behind it change nothing for it."""
+    st, rand = decode_state(kvo, 43, n=1000, k=512, heads=64)
+    prefill(kvo, ctx, st, rand)
+    decode_step(kvo, ctx, st)
+    assert ctx.sync() == kvo.KVO_OK
+    results = ("rows", "scores", "idx", "out", "lse")
+    want = {k: st[k].clone() for k in results}
+    inputs = {"append": (("kv", "key"), ("pos",)), "score": (("qi", "w"), ("lens",)), "attend": (("q",), ("lens",))}
+    good = {k: st[k].clone() for own, other in inputs.values() for k in own + other}
+    bad = {k: torch.full_like(v.float(), -5.0 if k in ("pos", "lens") else float("nan")).to(v.dtype) for k, v in good.items()}
+    load = torch.randn(32 << 20, device="cuda")
+    side = torch.cuda.Stream()
+
+    def spoil(names):
+        for k in names:
+            st[k].copy_(bad[k])
+
+    def step(main):
+        def call(name):
+            own, other = inputs[name]
+            side.wait_stream(main)
+            for stream, names in ((side, other), (main, own)):
+                with torch.cuda.stream(stream):
+                    load.mul_(1.0)
+                    for k in names:
+                        st[k].copy_(good[k])
+            main.wait_stream(side)
+            with torch.cuda.stream(main):
+                if name == "append":
+                    ctx.append_tokens(st["cache"], st["kv"][:, :512], st["kv"][:, 512:], st["pos"], INV_FREQ,
+                                      key=st["key"])
+                elif name == "score":
+                    ctx.index_scores(st["cache"], st["qi"], st["w"], st["lens"], st["n"], out=st["scores"])
+                    ctx.select_topk_batch(st["scores"], st["k"], idx=st["idx"])
+                else:
+                    ctx.attend(st["cache"], st["q"], st["lens"], 0.07, sel=st["idx"], out=st["out"], lse=st["lse"],
+                               work=st["work"])
+                spoil(own + other)
+
+        for name in inputs:
+            call(name)
+
+    main = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    spoil(good)
+    torch.cuda.synchronize()
+    if captured:
+        with torch.cuda.graph(graph, stream=main):
+            step(torch.cuda.current_stream())
+    for _ in range(3):
+        for k in results[1:]:
+            st[k].zero_()
+        torch.cuda.synchronize()
+        if captured:
+            graph.replay()
+        else:
+            step(main)
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[k], st[k]) for k in results)
+    assert ctx.sync() == kvo.KVO_OK
 
 
 def test_two_streams_at_once(kvo, ctx):

@@ -26,7 +26,7 @@ int device_sms();
 // memory, until that has completed and is visible.  The launch after them may
 // be scheduled once all their CTAs run.  Replayed from a graph that takes 0.2
 // to 0.9 us off a call (one appended token 2.5 to 2.3, 50,023 scores 5.2 to
-// 4.85, those of four tokens 8.25 to 7.7).
+// 4.85, those of four tokens 8.25 to 7.7, in the form they had).
 __device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

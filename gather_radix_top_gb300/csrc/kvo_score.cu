@@ -7,22 +7,27 @@
 // weighted sum over heads needs no exchange between threads, and the keys
 // are read once for all query tokens of their sequence.
 //
-// One CTA per SM, each over every gridDim.x-th key tile of one group of
-// query tokens: a warp brings key tiles into a ring in shared memory
+// One CTA per SM: a warp brings key tiles into a ring in shared memory
 // (a TMA box per run of keys of one block, looked up in the table), another
 // issues the MMAs into accumulators in tensor memory, and four
 // teams of four warps reduce them in turn.  Nothing but the queries and the
-// scores passes through global memory twice.
+// scores passes through global memory twice.  A sequence's query tokens (a
+// task) have a row of the grid, whose CTAs take their tiles in turn; of many
+// tasks, whose lengths may differ, the tiles are shared out end to end, and a
+// CTA goes from one task to the next while its ring fills on.
 //
 // What bounds it: up to 128 columns, reading the keys (132 bytes a key as e4m3,
 // 256 as bf16) after about 4 us of launch, queries and first keys: a million
-// keys take 25.5 us as one run of e4m3 (5.4 TB/s), 27.5 in shuffled blocks of
-// 16 and 42.1 as bf16 (6.4 TB/s), whether for 16 or 64 heads.  For 256
+// keys take 25.4 us as one run of e4m3 (5.5 TB/s), 26.7 in shuffled blocks of
+// 16 and 42.2 as bf16 (6.4 TB/s), whether for 16 or 64 heads.  For 256
 // columns (four tokens of 64 heads), the epilogue's two operations per
-// product: 262,144 keys take 18.3 us against 9.3 for one token.  Slower ones, for
-// the million in blocks: MMAs from one thread of a diverged warp 30.3 us (28.4
-// by then), one loading warp alone 45.2 (it issues a box every 60 clocks), table
-// entries that are used as soon as they are asked for 48.2.
+// product: 262,144 keys take 17.9 us against 9.0 for one token.  Slower ones, for
+// the million in blocks: a barrier of all warps before the first keys instead of
+// one for the queries alone 27.5 us, MMAs from one thread of a diverged warp 30.3
+// (28.4 by then), one loading warp alone 45.2 (it issues a box every 60 clocks),
+// table entries that are used as soon as they are asked for 48.2.
+#include <algorithm>
+
 #include <cuda.h>
 
 #include "kvo_cache.cuh"
@@ -39,6 +44,8 @@ constexpr uint32_t kScoreThreads = (kMmaWarp + 1) * 32;
 constexpr uint32_t kKeyTile = 128;
 constexpr uint32_t kScoreMaxCols = 256;
 constexpr uint32_t kScoreMaxTokens = kScoreMaxCols / 32;
+constexpr uint32_t kMostTasks = 512;                            // of a grid's row
+constexpr uint32_t kTaskCost = 4;                               // of going to another task, in tiles
 
 struct ScoreArgs {
   CacheView cache;
@@ -55,6 +62,8 @@ struct ScoreArgs {
   uint32_t head_cols;        // columns of a query token: heads rounded up to 32
   uint32_t group;            // query tokens of a CTA
   uint32_t groups;           // groups of a sequence
+  Divider by_groups;
+  uint32_t tasks, slice;     // groups of all sequences, and how many of them a row of the grid shares out
   uint32_t accs;             // accumulators in tensor memory: 4, or 2 of more than 128 columns
   uint32_t tmem_cols;
   uint32_t run;              // consecutive keys that never leave their block (>= 4), or 1
@@ -71,15 +80,21 @@ struct ScoreShape {
 };
 
 struct ScoreShared {
-  uint64_t full[8], empty[8], acc_full[4], acc_empty[4], drained;
+  uint64_t full[8], empty[8], acc_full[4], acc_empty[4], q_full, task_done, drained;
   uint32_t tmem;
   uint32_t gave_up;
-  int32_t len[kScoreMaxTokens];
+  uint32_t first, last, first_task;                             // this CTA's tiles
+  uint32_t warp_tiles[kScoreThreads / 32], warp_cost[kScoreThreads / 32];
+  uint32_t start[kMostTasks + 1];                               // tiles before each task's
+  uint32_t most[kMostTasks];                                    // positions that any of a task's tokens sees
+  int32_t len[2][kScoreMaxTokens];                              // of the task at hand and the next
+  float w[2][kScoreMaxCols];
   float best[kScoreTeams][4];
-  float w[kScoreMaxCols];
 };
 
-template <bool kF8>
+// kShared: the CTAs of a row of the grid share the tiles of many tasks out;
+// else a row is one task, whose tiles go to its CTAs in turn.
+template <bool kF8, bool kShared>
 __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __grid_constant__ ScoreArgs a,
                                                                         const __grid_constant__ CUtensorMap map) {
   using S = ScoreShape<kF8>;
@@ -87,34 +102,103 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
   __shared__ ScoreShared sh;
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t seq = blockIdx.y / a.groups, g0 = (blockIdx.y % a.groups) * a.group;
-  const uint32_t tokens = min(a.group, a.per_seq - g0);         // of this CTA
-  const uint32_t t0 = seq * a.per_seq + g0;
   const uint32_t cols = a.group * a.head_cols;
   const uint32_t ring = smem_u32(smem), queries = ring + S::kStages * S::kTileBytes;
 
+  // a task is a group of query tokens of one sequence: here task0 .. task0 + tasks - 1
+  const uint32_t task0 = kShared ? blockIdx.y * a.slice : blockIdx.y;
+  const uint32_t tasks = kShared ? min(a.slice, a.tasks - task0) : 1;
+  auto seq_of = [&](uint32_t r) -> uint32_t { return divide(task0 + r, a.by_groups); };
+  auto token_of = [&](uint32_t r) -> uint32_t {                 // the first token of task r
+    const uint32_t s = seq_of(r);
+    return s * a.per_seq + (task0 + r - s * a.groups) * a.group;
+  };
+  auto tokens_of = [&](uint32_t r) -> uint32_t {
+    return min(a.group, a.per_seq - (task0 + r - seq_of(r) * a.groups) * a.group);
+  };
+  auto longest = [&](uint32_t r) -> uint32_t {                  // positions that any of its tokens sees
+    const uint32_t t0 = token_of(r), tokens = tokens_of(r);
+    int32_t most = 0;
+    for (uint32_t g = 0; g < tokens; ++g) most = max(most, min(a.lens[t0 + g], (int32_t)a.n));
+    return (uint32_t)most;
+  };
+
   wait_previous_grid();
   allow_next_grid();
-  int32_t most = 0;                                             // positions that any of the tokens sees
-  for (uint32_t g = 0; g < tokens; ++g) most = max(most, min(a.lens[t0 + g], (int32_t)a.n));
-  const uint32_t tiles = ((uint32_t)most + kKeyTile - 1) / kKeyTile;
-  const uint32_t step = gridDim.x, first = blockIdx.x;
-  const uint32_t mine = tiles > first ? (tiles - first + step - 1) / step : 0;
+  if (tid == 0) {
+    for (uint32_t i = 0; i < S::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (uint32_t i = 0; i < a.accs; ++i) {
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], kScoreEpilogue / a.accs);
+    }
+    mbar_init(&sh.q_full, kLoadWarp);
+    mbar_init(&sh.task_done, 1);
+    mbar_init(&sh.drained, 1);
+    sh.gave_up = 0;
+    sh.first = sh.last = sh.first_task = 0;
+  }
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, a.tmem_cols);
+  // this CTA's tiles are number first, first + step, .. below last of all tasks' tiles end to end
+  uint32_t first, last, first_task = 0, only = 0;
+  const uint32_t step = kShared ? 1 : gridDim.x;
+  if constexpr (kShared) {
+    // a part of about the same cost for every CTA, from running sums over the tasks
+    const uint32_t most = tid < tasks ? longest(tid) : 0;
+    const uint32_t here = (most + kKeyTile - 1) / kKeyTile, cost = here ? here + kTaskCost : 0;
+    uint32_t tiles_to = here, cost_to = cost;                   // up to and with task tid
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d *= 2) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, tiles_to, d), c = __shfl_up_sync(0xffffffffu, cost_to, d);
+      if (lane >= d) tiles_to += t, cost_to += c;
+    }
+    if (lane == 31) sh.warp_tiles[warp] = tiles_to, sh.warp_cost[warp] = cost_to;
+    __syncthreads();
+    const uint32_t wt = lane < kScoreThreads / 32 ? sh.warp_tiles[lane] : 0;
+    const uint32_t wc = lane < kScoreThreads / 32 ? sh.warp_cost[lane] : 0;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, wc);
+    tiles_to += __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
+    cost_to += __reduce_add_sync(0xffffffffu, lane < warp ? wc : 0);
+    if (tid < tasks) {
+      const uint32_t from = cost_to - cost, tiles_from = tiles_to - here;
+      sh.most[tid] = most;
+      sh.start[tid] = tiles_from;
+      if (tid == tasks - 1) sh.start[tasks] = tiles_to;
+      const uint32_t lo = (uint32_t)((uint64_t)all * blockIdx.x / gridDim.x);
+      const uint32_t hi = (uint32_t)((uint64_t)all * (blockIdx.x + 1) / gridDim.x);
+      auto tile_at = [&](uint32_t x) { return tiles_from + (x - from > kTaskCost ? x - from - kTaskCost : 0); };
+      if (lo >= from && lo < cost_to) sh.first = tile_at(lo), sh.first_task = tid;
+      if (hi > from && hi <= cost_to) sh.last = tile_at(hi);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    first = sh.first, last = sh.last, first_task = sh.first_task;
+  } else {
+    only = longest(0);
+    first = blockIdx.x, last = (only + kKeyTile - 1) / kKeyTile;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t mine = last > first ? (last - first + step - 1) / step : 0;
+  const uint32_t tmem = sh.tmem;
 
   if (mine) {
-    if (tid == 0) {
-      for (uint32_t i = 0; i < S::kStages; ++i) {
-        mbar_init(&sh.full[i], 1);
-        mbar_init(&sh.empty[i], 1);
-      }
-      for (uint32_t i = 0; i < a.accs; ++i) {
-        mbar_init(&sh.acc_full[i], 1);
-        mbar_init(&sh.acc_empty[i], kScoreEpilogue / a.accs);
-      }
-      mbar_init(&sh.drained, 1);
-      sh.gave_up = 0;
-    }
-    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, a.tmem_cols);
+    // whether tile i is behind task r, the task of tile i from one before, and
+    // its first position there
+    auto behind = [&](uint32_t i, uint32_t r) -> bool { return kShared && first + i >= sh.start[r + 1]; };
+    auto walk = [&](uint32_t i, uint32_t& r) {
+      while (behind(i, r)) ++r;
+    };
+    auto position = [&](uint32_t i, uint32_t r) -> uint32_t {
+      return (kShared ? first + i - sh.start[r] : first + i * step) * kKeyTile;
+    };
+    const uint32_t only_seq = kShared ? 0 : seq_of(0);
+    auto task_seq = [&](uint32_t r) -> uint32_t { return kShared ? seq_of(r) : only_seq; };
+    auto most_of = [&](uint32_t r) -> uint32_t { return kShared ? sh.most[r] : only; };
 
     // Lane l of the loading warp brings the l-th run of a.run keys of a tile
     // (all in one block), or keys 4l .. 4l+3 where a block holds no such run;
@@ -127,21 +211,24 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
     const bool runs = a.run > 1;
     const uint32_t width = runs ? a.run : 4;
     int4 block[kLookup];
+    uint32_t ahead_task = first_task, bring_task = ahead_task;
     auto look_ahead = [&](uint32_t i) -> int4 {
-      const uint32_t p = (first + i * step) * kKeyTile + width * lane;
       int32_t b[4] = {0, 0, 0, 0};
+      if (i < mine) walk(i, ahead_task);
       if (i < mine && width * lane < kKeyTile) {
+        const uint32_t p = position(i, ahead_task) + width * lane, seq = task_seq(ahead_task), most = most_of(ahead_task);
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k)
-          if ((k == 0 || !runs) && p + k < (uint32_t)most) b[k] = cache_block(a.cache, seq, p + k);
+          if ((k == 0 || !runs) && p + k < most) b[k] = cache_block(a.cache, seq, p + k);
       }
       return make_int4(b[0], b[1], b[2], b[3]);
     };
     auto bring = [&](uint32_t j) {
       const uint32_t slot = j % S::kStages, dst = ring + slot * S::kTileBytes + lane * width * 128;
-      const uint32_t p = (first + j * step) * kKeyTile + width * lane;
+      walk(j, bring_task);
+      const uint32_t p = position(j, bring_task) + width * lane, most = most_of(bring_task);
       auto row = [&](int32_t id, uint32_t k) -> int32_t {
-        return p + k < (uint32_t)most ? max(0, (int32_t)cache_row_in(a.cache, id, p + k)) : 0;
+        return p + k < most ? max(0, (int32_t)cache_row_in(a.cache, id, p + k)) : 0;
       };
       if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], S::kTileBytes);
       __syncwarp();
@@ -166,47 +253,58 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
 #pragma unroll
       for (uint32_t i = 0; i < kLookup; ++i) block[i] = look_ahead(turn0 + i * kLoadWarps);
     }
-    // the barriers are ready, and so are the first tiles' places
-    __syncthreads();
-    uint32_t next = turn0;                                      // a loading warp's next tile
-    if (loads) {
-      for (; next < S::kStages && next < mine; next += kLoadWarps) bring(next);
-    } else {
-      const uint32_t at = warp < kLoadWarp ? tid : tid - 32 * kLoadWarps;
-      for (uint32_t i = at; i < cols * S::kPieces; i += kScoreThreads - 32 * kLoadWarps) {
-        const uint32_t r = i / S::kPieces, c = i % S::kPieces, g = r / a.head_cols, h = r - g * a.head_cols;
-        const bool real = g < tokens && h < a.heads;
-        copy16_async(queries + (c >> 3) * (cols * 128) + swizzled(r, c & 7),
-                     real ? a.q + (t0 + g) * a.q_ld + h * a.q_head_ld + c * 16 : a.q, real);
-      }
-      copy_async_commit();
-      for (uint32_t i = at; i < cols; i += kScoreThreads - 32 * kLoadWarps) {
-        const uint32_t g = i / a.head_cols, h = i - g * a.head_cols;
-        sh.w[i] = g < tokens && h < a.heads ? a.w[(t0 + g) * a.w_ld + h] : 0.0f;
-      }
-      if (at < tokens) sh.len[at] = min(a.lens[t0 + at], (int32_t)a.n);
-      copy_async_wait<0>();
-      fence_proxy_async_smem();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-
     if (warp < kLoadWarp) {
       // team w takes the tiles of accumulator w % accs, and of their query
       // tokens every parts-th
       const uint32_t team = warp >> 2, acc = team % a.accs, part = team / a.accs, parts = kScoreTeams / a.accs;
       const uint32_t lane_base = (warp & 3) * 32, key = lane_base + lane;
       const uint32_t from = tmem + (lane_base << 16) + acc * cols;
+      // The queries of a task, their weights and lengths.  The workers bring
+      // those of the next one when the last product of this one is done.
+      uint32_t task = first_task, nth = 0, tokens = 0, t0 = 0;
+      auto bring_queries = [&] {
+        tokens = tokens_of(task), t0 = token_of(task);
+        for (uint32_t i = tid; i < cols * S::kPieces; i += kScoreEpilogue) {
+          const uint32_t r = i / S::kPieces, c = i % S::kPieces, g = r / a.head_cols, h = r - g * a.head_cols;
+          const bool real = g < tokens && h < a.heads;
+          copy16_async(queries + (c >> 3) * (cols * 128) + swizzled(r, c & 7),
+                       real ? a.q + (t0 + g) * a.q_ld + h * a.q_head_ld + c * 16 : a.q, real);
+        }
+        copy_async_commit();
+        for (uint32_t i = tid; i < cols; i += kScoreEpilogue) {
+          const uint32_t g = i / a.head_cols, h = i - g * a.head_cols;
+          sh.w[nth & 1][i] = g < tokens && h < a.heads ? a.w[(t0 + g) * a.w_ld + h] : 0.0f;
+        }
+        if (tid < tokens) sh.len[nth & 1][tid] = min(a.lens[t0 + tid], (int32_t)a.n);
+        copy_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+      };
+      auto next_task = [&] {
+        wait_or_give_up(&sh.task_done, nth & 1, &sh.gave_up);
+        __syncwarp();
+        do ++task;
+        while (sh.start[task + 1] == sh.start[task]);
+        ++nth;
+        bring_queries();
+      };
+      bring_queries();
+      wait_or_give_up(&sh.q_full, 0, &sh.gave_up);
+
       // table entries are asked for two of this team's tiles ahead, the keys'
       // factors one
+      uint32_t block_task = task, row_task = task;
       auto look_up = [&](uint32_t i) -> int32_t {
-        const uint32_t p = (first + i * step) * kKeyTile + key;
-        return i < mine && p < (uint32_t)most ? cache_block(a.cache, seq, p) : -1;
+        if (i >= mine) return -1;
+        walk(i, block_task);
+        const uint32_t p = position(i, block_task) + key;
+        return p < most_of(block_task) ? cache_block(a.cache, task_seq(block_task), p) : -1;
       };
       auto row_in = [&](uint32_t i, int32_t id) -> int64_t {
-        return cache_row_in(a.cache, id, (first + i * step) * kKeyTile + key);
+        if (i >= mine) return -1;
+        walk(i, row_task);
+        return cache_row_in(a.cache, id, position(i, row_task) + key);
       };
       auto factor_of = [&](int64_t r) -> float { return kF8 && r >= 0 ? a.cache.key_scales[r] : 1.0f; };
       bool next_there;
@@ -218,10 +316,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       }
       int32_t block_after = look_up(acc + a.accs);
       for (uint32_t i = acc, turn = 0; i < mine; i += a.accs, turn ^= 1) {
-        const uint32_t p = (first + i * step) * kKeyTile + key;
+        if (behind(i, task)) {
+          while (behind(i, task)) next_task();
+          wait_or_give_up(&sh.q_full, nth & 1, &sh.gave_up);
+        }
+        const float* weights = sh.w[nth & 1];
+        const int32_t* lens = sh.len[nth & 1];
+        const uint32_t p = position(i, task) + key;
         const bool there = next_there;
         const float factor = next_factor;
-        if (!there && p < (uint32_t)most) atomicOr(a.status, kFlagRange);
+        if (!there && p < most_of(task)) atomicOr(a.status, kFlagRange);
         const int64_t r = row_in(i + a.accs, block_after);
         next_there = r >= 0;
         next_factor = factor_of(r);
@@ -236,7 +340,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
           for (uint32_t c = 0; c < a.head_cols; c += 32) {
             float v[32];
             tmem_ld32(from + g * a.head_cols + c, v);
-            const float4* w4 = reinterpret_cast<const float4*>(&sh.w[g * a.head_cols + c]);
+            const float4* w4 = reinterpret_cast<const float4*>(&weights[g * a.head_cols + c]);
             tmem_ld_wait();
 #pragma unroll
             for (uint32_t e = 0; e < 8; ++e) {
@@ -247,7 +351,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
               s1 = fmaf(w.w, max_nan(v[4 * e + 3], 0.0f), s1);
             }
           }
-          float score = there && (int32_t)p < sh.len[g] ? (s0 + s1) * factor : -INFINITY;
+          float score = there && (int32_t)p < lens[g] ? (s0 + s1) * factor : -INFINITY;
           float* out = a.scores + (t0 + g) * a.ld;
           if (a.block_shift == 0) {
             if (p < a.n) out[p] = score;
@@ -269,7 +373,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         tc_fence_before();
         mbar_arrive(&sh.acc_empty[acc]);                        // the accumulator has been read
       }
+      while (kShared && sh.start[task + 1] < last) next_task();  // those that other teams have tiles of
     } else if (warp < kMmaWarp) {
+      uint32_t next = turn0;                                    // this warp's next tile
+      for (; next < S::kStages && next < mine; next += kLoadWarps) bring(next);
       for (; next < mine; next += kLoadWarps) {                 // the slot held tile next - kStages
         const bool ok = wait_or_give_up(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1, &sh.gave_up);
         if (__any_sync(0xffffffffu, !ok)) break;
@@ -287,9 +394,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       const uint32_t idesc = mma_desc(kF8 ? 0u : 1u, cols, false, false);
       const uint64_t keys = tile_desc(ring, 16), heads = tile_desc(queries, 16);
       const uint64_t next_half = (cols * 128) >> 4;
-      bool ok = true;
+      uint32_t task = first_task, nth = 0;
+      bool ok = wait_or_give_up(&sh.q_full, 0, &sh.gave_up);
       for (uint32_t i = 0, slot = 0, slot_turn = 0, acc = 0, acc_turn = 0; i < mine; ++i) {
-        ok = wait_or_give_up(&sh.full[slot], slot_turn & 1, &sh.gave_up) &&
+        if (behind(i, task)) {                                  // the next task: its queries replace these
+          if (elect_one()) mma_commit(&sh.task_done);
+          __syncwarp();
+          walk(i, task);
+          ok = ok && wait_or_give_up(&sh.q_full, ++nth & 1, &sh.gave_up);
+        }
+        ok = ok && wait_or_give_up(&sh.full[slot], slot_turn & 1, &sh.gave_up) &&
              (acc_turn == 0 || wait_or_give_up(&sh.acc_empty[acc], (acc_turn - 1) & 1, &sh.gave_up));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -324,17 +438,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
-    __syncwarp();
-    if (warp == kMmaWarp) tmem_free(tmem, a.tmem_cols);
   }
+  __syncwarp();
+  if (warp == kMmaWarp) tmem_free(tmem, a.tmem_cols);
 
-  // columns that no token sees
-  const uint32_t per_tile = kKeyTile >> a.block_shift;
-  for (uint32_t t = first + mine * step; (uint64_t)t * kKeyTile < a.n; t += step)
-    for (uint32_t i = tid; i < per_tile * tokens; i += kScoreThreads) {
-      const uint32_t g = i / per_tile, c = t * per_tile + i % per_tile;
-      if ((uint64_t)c << a.block_shift < a.n) a.scores[(t0 + g) * a.ld + c] = -INFINITY;
-    }
+  // columns that no token sees, in pieces of 64 tiles of a task, or of one tile, to the CTAs in turn
+  constexpr uint32_t kPiece = kShared ? 64 : 1;
+  const uint32_t per_tile = kKeyTile >> a.block_shift, tiles = (a.n + kKeyTile - 1) / kKeyTile;
+  const uint32_t pieces = (tiles + kPiece - 1) / kPiece;
+  for (uint64_t i = kShared ? blockIdx.x : first + mine * step; i < (uint64_t)tasks * pieces; i += gridDim.x) {
+    const uint32_t r = kShared ? (uint32_t)(i / pieces) : 0, piece = (uint32_t)(i - (uint64_t)r * pieces);
+    const uint32_t from = max(piece * kPiece, kShared ? sh.start[r + 1] - sh.start[r] : 0), to = min(tiles, (piece + 1) * kPiece);
+    if (from >= to) continue;
+    const uint32_t t0 = token_of(r), tokens = tokens_of(r);
+    for (uint32_t g = 0; g < tokens; ++g)
+      for (uint32_t c = from * per_tile + tid; c < to * per_tile; c += kScoreThreads)
+        if ((uint64_t)c << a.block_shift < a.n) a.scores[(t0 + g) * a.ld + c] = -INFINITY;
+  }
 }
 
 // The keys as a matrix of rows, in boxes of `run` rows of 128 bytes.
@@ -358,8 +478,8 @@ bool key_map(CUtensorMap* map, const void* keys, int64_t rows, uint32_t run, boo
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kF8>
-cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, uint32_t sequences, cudaStream_t stream) {
+template <bool kF8, bool kShared>
+cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, cudaStream_t stream) {
   using S = ScoreShape<kF8>;
   CUtensorMap map;
   if (!key_map(&map, a.cache.keys, cache_rows, a.run, kF8)) return cudaErrorInvalidValue;
@@ -369,16 +489,18 @@ cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, uint32_t seque
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(index_scores_kernel<kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(index_scores_kernel<kF8, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
-  // one CTA per SM where the groups allow it in one wave, else several waves
-  // of shorter ones, so that uneven lengths even out
-  const uint32_t rows = sequences * a.groups, sms = (uint32_t)device_sms(), tiles = (a.n + kKeyTile - 1) / kKeyTile;
-  uint32_t x = rows <= sms ? sms / rows : (4 * sms + rows - 1) / rows;
-  if (x > tiles) x = tiles;
-  return launch_early(index_scores_kernel<kF8>, dim3(x, rows), kScoreThreads, smem, stream, a, map);
+  // one CTA per SM; where shared tasks are cut into several rows of the grid,
+  // two waves, for these may differ
+  const uint32_t sms = (uint32_t)device_sms(), tiles = (a.n + kKeyTile - 1) / kKeyTile;
+  const uint32_t rows = kShared ? (a.tasks + a.slice - 1) / a.slice : a.tasks;
+  const uint64_t most = kShared ? (uint64_t)std::min(a.slice, a.tasks) * tiles : tiles;
+  uint32_t x = kShared && rows > 1 ? (2 * sms + rows - 1) / rows : rows <= sms ? sms / rows : 1;
+  if (x > most) x = (uint32_t)most;
+  return launch_early(index_scores_kernel<kF8, kShared>, dim3(x, rows), kScoreThreads, smem, stream, a, map);
 }
 
 }  // namespace
@@ -420,17 +542,31 @@ extern "C" kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, con
   a.group = kScoreMaxCols / a.head_cols;
   if (a.group > a.per_seq) a.group = a.per_seq;
   a.groups = (a.per_seq + a.group - 1) / a.group;
+  a.by_groups = divider(a.groups);
+  a.tasks = (uint32_t)cache->sequences * a.groups;
+  // a row of the grid counts its tiles in 31 bits
+  a.slice = (uint32_t)std::min<uint64_t>(kMostTasks, 0x7fffffffu / ((uint64_t)(a.n + kKeyTile - 1) / kKeyTile + kTaskCost));
   a.accs = a.group * a.head_cols > 128 ? 2 : 4;
   a.tmem_cols = 128;
   while (a.tmem_cols < a.accs * a.group * a.head_cols) a.tmem_cols *= 2;
   // the largest power of two that divides both a tile and a block; without a
-  // table a sequence is one block.  A million e4m3 keys take 27.5 us in runs of
-  // 16, 41.3 as gathered rows (blocks of 5).
+  // table a sequence is one block.  A million e4m3 keys take 26.7 us in runs of
+  // 16, 39.7 as gathered rows (blocks of 5).
   a.run = kKeyTile;
   while (cache->table && a.run > 1 && cache->block_rows % a.run) a.run /= 2;
   if (a.run < 4) a.run = 1;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->key_type == KVO_BF16 ? launch_scores<false>(a, rows, (uint32_t)cache->sequences, on)
-                                                    : launch_scores<true>(a, rows, (uint32_t)cache->sequences, on);
+  // With one task to a row of the grid uneven lengths leave SMs idle, and more
+  // than half as many tasks as SMs one CTA a task; tiles shared out cost a
+  // lookup of their task at every step.  e4m3 keys of 64 heads, 8,192 a
+  // sequence, a row each against shared, us: 48 sequences of uneven length 11.3,
+  // 11.6, of equal length 11.6, 13.6; 100 uneven 25.7, 18.2, equal 26.6, 25.1;
+  // 128 26.3, 22.5 and 28.8, 31.5; 200 47.5, 35.3 and 54.2, 46.5; 700 116, 114
+  // and 142, 155.  2,000 of up to 300 keys 52.8, 41.8 and 57.5, 46.5.
+  const uint32_t sms = (uint32_t)device_sms();
+  const bool shared = 2 * a.tasks > sms && (a.tasks <= 2 * sms || a.n <= 16 * kKeyTile);
+  const auto launch = cache->key_type == KVO_BF16 ? shared ? launch_scores<false, true> : launch_scores<false, false>
+                                                  : shared ? launch_scores<true, true> : launch_scores<true, false>;
+  const cudaError_t e = launch(a, rows, on);
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

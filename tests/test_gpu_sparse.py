@@ -307,6 +307,40 @@ def test_scores(kvo, ctx, dtype, sequences, per_seq, heads, n, block, block_rows
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lengths", ["uneven", "one long", "none"])
+@pytest.mark.parametrize("sequences,per_seq,heads,n,block,block_rows", [
+    (90, 1, 16, 700, 1, 16), (40, 5, 64, 300, 1, 16), (100, 1, 64, 1000, 16, 16), (65, 4, 24, 500, 64, 48),
+    (1100, 1, 8, 150, 1, 16), (160, 1, 128, 129, 128, 7), (310, 1, 5, 2100, 2, 48), (600, 3, 100, 40, 1, 5)])
+def test_scores_many_sequences(kvo, ctx, dtype, lengths, sequences, per_seq, heads, n, block, block_rows):
+    """More tasks than half the SMs: CTAs go from one sequence to the next, past empty ones; blocks are shared."""
+    rng = np.random.default_rng([sequences, per_seq, heads, n, len(dtype), len(lengths)])
+    nq, blocks, total = sequences * per_seq, -(-n // block_rows), 60
+    table = rng.integers(0, total, (sequences, blocks)).astype(np.int32)
+    q, k, scales, w = score_inputs(rng, nq, heads, total * block_rows, dtype)
+    if lengths == "uneven":
+        lens = rng.integers(0, n + 1, nq)
+        lens[rng.random(nq) < 0.2] = 0
+        lens[:2 * per_seq] = 0
+        lens[-1] = n
+    elif lengths == "one long":
+        lens = rng.integers(-1, 2, nq)
+        lens[nq // 3] = n
+        lens[-per_seq:] = 0
+    else:
+        lens = np.zeros(nq, np.int64)
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=block_rows, table=dev(table))
+    out = torch.full((nq, -(-n // block) + 3), 3.0, device="cuda")[:, :-(-n // block)]
+    got = ctx.index_scores(cache, q, w, dev(lens, torch.int32), n, block=block, out=out)
+    assert ctx.sync() == kvo.KVO_OK
+    at = np.arange(n)
+    whole = table[:, at // block_rows].astype(np.int64) * block_rows + at % block_rows
+    some = np.unique(np.concatenate([rng.choice(nq, min(nq, 60), replace=False), [0, nq // 3, nq - 1]]))
+    check_scores(got[some], q[some], k, scales, w[some], [list(whole[t // per_seq]) for t in some], lens[some], n, block)
+    columns = np.arange(-(-n // block))[None] * block                # every query: what is seen and what is not
+    assert np.array_equal(np.isneginf(f64(got)), columns >= np.maximum(lens, 0)[:, None])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_scores_strides_and_contiguous_cache(kvo, ctx, dtype):
     rng = np.random.default_rng(21)
     nq, heads, n = 3, 20, 150

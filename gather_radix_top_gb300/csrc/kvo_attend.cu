@@ -36,8 +36,8 @@
 // from scores to weights) and the hand-overs are the rest: with one tile in
 // shared memory nothing else of the tensor cores' work can run beside it.
 //     1,048,576 rows of one query with 128 heads    486 us, 602 TFLOP/s
-//     64 queries of 64 heads and 2,048 positions     52 us, 1.8 TB/s
-//     2,048 rows of one query with 64 heads         10.9 us
+//     64 queries of 64 heads and 2,048 positions     50.5 us, 1.9 TB/s
+//     2,048 rows of one query with 64 heads          9.9 us
 // Measured on the way, the first of them in us: rows through registers 942
 // (next to this much shared memory the SM keeps about 28 KB of loads in
 // flight), eight worker warps and one loading warp 672, three loading warps
@@ -613,29 +613,112 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   if (warp == kMmaWarp) tmem_free(tmem, S::kTmemCols);
 }
 
-// Joins the splits of one (query, head): their results weighted by
-// exp2(lse - the joint lse).  kGroups groups of 128 threads take every
-// kGroups-th split, four values a thread.
-constexpr uint32_t kMaxSplits = 1024, kFewSplits = 8;
-template <uint32_t kGroups>
-__global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, const float* part_lse, uint32_t splits,
-                                                             int64_t rows, uint16_t* out, float* lse) {
-  constexpr uint32_t kThreads = 128 * kGroups;
-  __shared__ float weight[kGroups > 1 ? kMaxSplits : kFewSplits];
-  __shared__ float red[4 * kGroups];
+// The weights exp2(lse - the joint lse) join the splits of one (query, head).
+// Partial results are asked for before their weights, and past the first-level
+// cache: these grids may have begun before they were written.  A split without
+// rows has written nothing but its -inf.
+constexpr uint32_t kMaxSplits = 1024;
+
+__device__ __forceinline__ float4 partial(const float* part, int64_t row, uint32_t at) {
+  return __ldcg(reinterpret_cast<const float4*>(part + row * KVO_LATENT_BYTES + 4 * at));
+}
+
+struct Joined {
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float total = 0.0f;
+  __device__ __forceinline__ void add(float w, const float4& v) {
+    if (!(w > 0.0f) && !isnan(w)) return;
+    total += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  __device__ __forceinline__ void write(float base, int64_t r, uint32_t at, uint16_t* out, float* lse) const {
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[at] =
+        make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+    if (lse && at == 0) lse[r] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+  }
+};
+
+// Up to 32 splits: group g of 128 threads has every kGroups-th one's values
+// from g on, kMost at most.  The weights are formed by every thread for up to
+// 8 splits and by every warp, one a lane, for more, so that nothing waits at a
+// barrier before the sum: 64 queries of 64 heads with 2 splits 48.4 us in all,
+// 49.4 with a barrier, 12 with 12 splits 19.8 and 24.1, one with 32 10.0 and 10.7.
+template <uint32_t kMost, uint32_t kGroups>
+__global__ void __launch_bounds__(128 * kGroups) join_few_kernel(const float* part, const float* part_lse, uint32_t splits,
+                                                                 int64_t rows, uint16_t* out, float* lse) {
+  static_assert(kMost * kGroups <= 32);
   __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][128];
+  __shared__ float totals[kGroups];
+  const int64_t r = blockIdx.x;
+  const uint32_t at = threadIdx.x & 127, group = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  wait_previous_grid();
+  float4 v[kMost];
+  constexpr bool kEach = kMost * kGroups <= 8;
+  float l[kEach ? kMost : 1], top = -INFINITY;             // of split k, or of split `lane`
+#pragma unroll
+  for (uint32_t k = 0; k < (kEach ? kMost : 1); ++k) {
+    const uint32_t s = kEach ? k : lane;
+    l[k] = s < splits ? __ldcg(part_lse + s * rows + r) : -INFINITY;
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kMost; ++k)
+    if (group + k * kGroups < splits) v[k] = partial(part, (group + k * kGroups) * rows + r, at);
+#pragma unroll
+  for (uint32_t k = 0; k < (kEach ? kMost : 1); ++k) top = fmaxf(top, l[k]);
+  if constexpr (!kEach) {
+#pragma unroll
+    for (uint32_t d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  const float base = top == -INFINITY ? 0.0f : top;
+  float w[kEach ? kMost : 1];
+#pragma unroll
+  for (uint32_t k = 0; k < (kEach ? kMost : 1); ++k) w[k] = exp2f(l[k] - base);
+  Joined j;
+#pragma unroll
+  for (uint32_t k = 0; k < kMost; ++k) {
+    if constexpr (kEach)
+      j.add(w[k], v[k]);
+    else
+      j.add(__shfl_sync(0xffffffffu, w[0], group + k * kGroups), v[k]);
+  }
+  if constexpr (kGroups > 1) {
+    if (group) sums[group - 1][at] = j.o;
+    if (at == 0) totals[group] = j.total;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (uint32_t g = 1; g < kGroups; ++g) {
+      j.total += totals[g];
+      j.o.x += sums[g - 1][at].x;
+      j.o.y += sums[g - 1][at].y;
+      j.o.z += sums[g - 1][at].z;
+      j.o.w += sums[g - 1][at].w;
+    }
+  }
+  j.write(base, r, at, out, lse);
+}
+
+// More: kGroups groups of 128 threads take every kGroups-th split.
+__global__ void __launch_bounds__(512) join_kernel(const float* part, const float* part_lse, uint32_t splits, int64_t rows,
+                                                   uint16_t* out, float* lse) {
+  constexpr uint32_t kGroups = 4, kThreads = 128 * kGroups;
+  __shared__ float weight[kMaxSplits];
+  __shared__ float red[4 * kGroups];
+  __shared__ float4 sums[kGroups - 1][128];
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
-  wait_previous_grid();                                    // the partial results are there
-  // the first partial results are asked for before their weights (past the
-  // first-level cache: this grid may have begun before they were written)
-  constexpr uint32_t kAhead = kGroups > 1 ? 8 : 2;
+  wait_previous_grid();
+  constexpr uint32_t kAhead = 8;
   float4 v[kAhead];
   auto load = [&](uint32_t from) {
 #pragma unroll
     for (uint32_t k = 0; k < kAhead; ++k) {
       const uint32_t s = from + k * kGroups;
-      if (s < splits) v[k] = __ldcg(reinterpret_cast<const float4*>(part + (s * rows + r) * KVO_LATENT_BYTES + 4 * at));
+      if (s < splits) v[k] = partial(part, s * rows + r, at);
     }
   };
   load(group);
@@ -651,41 +734,29 @@ __global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, 
 #pragma unroll
   for (uint32_t w = 0; w < 4 * kGroups; ++w) top = fmaxf(top, red[w]);
   const float base = top == -INFINITY ? 0.0f : top;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float total = 0.0f;
+  Joined j;
   for (uint32_t from = group; from < splits; from += kAhead * kGroups) {
 #pragma unroll
     for (uint32_t k = 0; k < kAhead; ++k) {
       const uint32_t s = from + k * kGroups;
-      const float w = s < splits ? exp2f(weight[s] - base) : 0.0f;
-      if (!(w > 0.0f) && !isnan(w)) continue;              // an empty split has written nothing
-      total += w;
-      o.x = fmaf(w, v[k].x, o.x);
-      o.y = fmaf(w, v[k].y, o.y);
-      o.z = fmaf(w, v[k].z, o.z);
-      o.w = fmaf(w, v[k].w, o.w);
+      j.add(s < splits ? exp2f(weight[s] - base) : 0.0f, v[k]);
     }
     load(from + kAhead * kGroups);
   }
-  if constexpr (kGroups > 1) {
-    __syncthreads();
-    if (group) sums[group - 1][at] = o;
-    if (at == 0) red[group] = total;
-    __syncthreads();
-    if (group) return;
-    total = 0.0f;
-    for (uint32_t g = 0; g < kGroups; ++g) total += red[g];
-    for (uint32_t g = 0; g + 1 < kGroups; ++g) {
-      o.x += sums[g][at].x;
-      o.y += sums[g][at].y;
-      o.z += sums[g][at].z;
-      o.w += sums[g][at].w;
-    }
+  __syncthreads();
+  if (group) sums[group - 1][at] = j.o;
+  if (at == 0) red[group] = j.total;
+  __syncthreads();
+  if (group) return;
+  j.total = 0.0f;
+  for (uint32_t g = 0; g < kGroups; ++g) j.total += red[g];
+  for (uint32_t g = 0; g + 1 < kGroups; ++g) {
+    j.o.x += sums[g][at].x;
+    j.o.y += sums[g][at].y;
+    j.o.z += sums[g][at].z;
+    j.o.w += sums[g][at].w;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  reinterpret_cast<uint2*>(out + r * KVO_LATENT_BYTES)[at] =
-      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-  if (lse && at == 0) lse[r] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+  j.write(base, r, at, out, lse);
 }
 
 // How a call is cut: columns per CTA and splits of every list.
@@ -697,9 +768,9 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
   // Units of 64 heads by 64 rows: where they do not fill the GPU, fewer heads
   // a CTA leave it less to store and give the rows to more of them.  2,048
-  // rows of 64 heads, with 16, 32 and 64 heads a CTA: one query 11.6, 11.4,
-  // 12.9 us, two 13.6, 13.3, 13.3, four 16.3, 15.8, 15.5, sixteen 34.7, 25.4,
-  // 22.5; 512 rows of one query 10.0, 11.1, 12.5.
+  // rows of 64 heads, with 16, 32 and 64 heads a CTA: one query 9.9, 10.2,
+  // 11.9 us, two 12.8, 11.4, 12.4, four 15.2, 14.2, 13.5, sixteen 32.8, 24.6,
+  // 19.7; 512 rows of one query 8.7, 9.5, 11.2.
   const int64_t units = nq * ((heads + 63) / 64) * ((positions + 63) / 64);
   const uint32_t most_heads = 4 * units <= device_sms() ? 16 : units <= device_sms() ? 32 : 64;
   c.heads = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
@@ -783,8 +854,13 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
                   : cut.heads == 32 ? launch_attend<32>(a, on)
                                     : launch_attend<64>(a, on);
   if (e == cudaSuccess && a.splits > 1) {
-    const bool few = a.splits <= kFewSplits;
-    e = launch_early(few ? join_kernel<1> : join_kernel<4>, dim3((unsigned)(nq * a.heads)), few ? 128 : 512, 0, on, a.part,
+    const auto join = a.splits <= 2    ? join_few_kernel<2, 1>
+                      : a.splits <= 4  ? join_few_kernel<4, 1>
+                      : a.splits <= 8  ? join_few_kernel<8, 1>
+                      : a.splits <= 16 ? join_few_kernel<16, 1>
+                      : a.splits <= 32 ? join_few_kernel<16, 2>
+                                       : join_kernel;
+    e = launch_early(join, dim3((unsigned)(nq * a.heads)), a.splits <= 16 ? 128 : a.splits <= 32 ? 256 : 512, 0, on, a.part,
                      a.part_lse, a.splits, nq * (int64_t)a.heads, a.out, a.lse);
   }
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;

@@ -35,9 +35,9 @@
 // (720), the raw rows (820) and the queries share.  The softmax (about 1,450
 // from scores to weights) and the hand-overs are the rest: with one tile in
 // shared memory nothing else of the tensor cores' work can run beside it.
-//     1,048,576 rows of one query with 128 heads    486 us, 602 TFLOP/s
+//     1,048,576 rows of one query with 128 heads    483 us, 605 TFLOP/s
 //     64 queries of 64 heads and 2,048 positions     50.5 us, 1.9 TB/s
-//     2,048 rows of one query with 64 heads          9.9 us
+//     2,048 rows of one query with 64 heads          9.8 us
 // Measured on the way, the first of them in us: rows through registers 942
 // (next to this much shared memory the SM keeps about 28 KB of loads in
 // flight), eight worker warps and one loading warp 672, three loading warps
@@ -702,17 +702,17 @@ __global__ void __launch_bounds__(128 * kGroups) join_few_kernel(const float* pa
   j.write(base, r, at, out, lse);
 }
 
-// More: kGroups groups of 128 threads take every kGroups-th split.
-__global__ void __launch_bounds__(512) join_kernel(const float* part, const float* part_lse, uint32_t splits, int64_t rows,
-                                                   uint16_t* out, float* lse) {
-  constexpr uint32_t kGroups = 4, kThreads = 128 * kGroups;
+// More: kGroups groups of 128 threads take every kGroups-th split, kAhead at a time.
+template <uint32_t kGroups, uint32_t kAhead>
+__global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, const float* part_lse, uint32_t splits,
+                                                             int64_t rows, uint16_t* out, float* lse) {
+  constexpr uint32_t kThreads = 128 * kGroups;
   __shared__ float weight[kMaxSplits];
   __shared__ float red[4 * kGroups];
   __shared__ float4 sums[kGroups - 1][128];
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
   wait_previous_grid();
-  constexpr uint32_t kAhead = 8;
   float4 v[kAhead];
   auto load = [&](uint32_t from) {
 #pragma unroll
@@ -854,14 +854,20 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
                   : cut.heads == 32 ? launch_attend<32>(a, on)
                                     : launch_attend<64>(a, on);
   if (e == cudaSuccess && a.splits > 1) {
+    // Past 32 splits, 1,024 threads for as many outputs as SMs and 512 for more.
+    // 64 heads, us: one query of 8,192 rows 15.6 and 17.9, of 65,536 29.5 and
+    // 33.6, four of 8,192 22.7 and 21.4.
+    const int64_t joins = nq * a.heads;
+    const bool wide = joins <= device_sms();
     const auto join = a.splits <= 2    ? join_few_kernel<2, 1>
                       : a.splits <= 4  ? join_few_kernel<4, 1>
                       : a.splits <= 8  ? join_few_kernel<8, 1>
                       : a.splits <= 16 ? join_few_kernel<16, 1>
                       : a.splits <= 32 ? join_few_kernel<16, 2>
-                                       : join_kernel;
-    e = launch_early(join, dim3((unsigned)(nq * a.heads)), a.splits <= 16 ? 128 : a.splits <= 32 ? 256 : 512, 0, on, a.part,
-                     a.part_lse, a.splits, nq * (int64_t)a.heads, a.out, a.lse);
+                      : wide           ? join_kernel<8, 4>
+                                       : join_kernel<4, 8>;
+    const uint32_t threads = a.splits <= 16 ? 128 : a.splits <= 32 ? 256 : wide ? 1024 : 512;
+    e = launch_early(join, dim3((unsigned)joins), threads, 0, on, a.part, a.part_lse, a.splits, joins, a.out, a.lse);
   }
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

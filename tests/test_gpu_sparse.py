@@ -494,6 +494,18 @@ def test_attend_a_few_splits_a_query(kvo, ctx, sequences, heads, listed):
     attend_case(kvo, ctx, rng, sequences, 1, heads, n, 1, 600 if listed else None, 16, lens=lens)
 
 
+@pytest.mark.parametrize("sequences,heads,n", [(10, 64, 1100), (6, 64, 2048), (4, 64, 3000), (1, 64, 9000), (1, 128, 6000),
+                                               (3, 128, 1700)])
+def test_attend_many_splits_a_query(kvo, ctx, sequences, heads, n):
+    """About 15, 25, 38 and 76 to 140 splits; a query of one row leaves most of its splits empty."""
+    rng = np.random.default_rng([sequences, heads, n, 7])
+    lens = rng.integers(n // 2, n + 1, sequences)
+    lens[0] = n
+    if sequences > 2:
+        lens[1:3] = 1, 0
+    attend_case(kvo, ctx, rng, sequences, 1, heads, n, 1, None, 16, lens=lens)
+
+
 def test_attend_nan_in_one_split(kvo, ctx):
     """A NaN that one of three CTAs sees reaches the whole result of its query, and no other query's."""
     rng = np.random.default_rng(39)

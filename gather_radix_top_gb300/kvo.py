@@ -528,11 +528,18 @@ class Cache:
                 raise ValueError("table rows must be contiguous")
             if sequences is not None and sequences != table.shape[0]:
                 raise ValueError("sequences is not the table's")
-            c.table = table.data_ptr()
+            # an empty tensor's address is 0, which says "no table": one without
+            # columns gets an entry that no call reads
+            c.table = table.data_ptr() or self._unread_entry(table)
             c.sequences, c.table_blocks = table.shape
             c.table_ld = max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else table.stride(0)
         self.sequences, self.block_rows, self.blocks = c.sequences, c.block_rows, c.blocks
         self.pool = rows if isinstance(rows, Pool) else None
+
+    def _unread_entry(self, table) -> int:
+        entry = table.new_empty(1)
+        self.tensors += (entry,)
+        return entry.data_ptr()
 
     @property
     def ref(self) -> int:

@@ -1050,3 +1050,25 @@ def test_a_closed_pool_is_refused(kvo, ctx):
     with pytest.raises(ValueError):
         ctx.attend(cache, torch.zeros(2, 1, 576, dtype=torch.bfloat16, device="cuda"),
                    torch.ones(2, dtype=torch.int32, device="cuda"), 0.1, rows=16)
+
+
+@pytest.mark.parametrize("block_rows", [1, 16])
+def test_a_table_without_columns_has_no_rows(kvo, ctx, block_rows):
+    """Every position is masked and says so: nothing is written to, or read from, the block of the sequence's number."""
+    rng = np.random.default_rng(51)
+    held = dev(random_rows(rng, 4 * block_rows))
+    keys = dev(rng.standard_normal((4 * block_rows, 128)), torch.bfloat16)
+    rows_before, keys_before = held.clone(), keys.clone()
+    cache = kvo.Cache(rows=held, keys=keys, block_rows=block_rows, table=torch.empty(2, 0, dtype=torch.int32, device="cuda"))
+    kv = dev(rng.standard_normal((2, 576)), torch.bfloat16)
+    values = torch.full((2, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    lens = torch.ones(2, dtype=torch.int32, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], lens - 1, INV_FREQ, key=kv[:, :128], out_bf16=values)
+    assert ctx.sync() == kvo.KVO_ERANGE
+    assert torch.equal(held, rows_before) and torch.equal(keys, keys_before) and not values.any()
+    scores = ctx.index_scores(cache, kv[:, None, :128], torch.ones(2, 1, device="cuda"), lens, 3)
+    assert ctx.sync() == kvo.KVO_ERANGE and torch.isneginf(scores).all()
+    out, lse = ctx.attend(cache, kv[:, None], lens, 0.1, rows=1)
+    assert ctx.sync() == kvo.KVO_ERANGE and not out.any() and torch.isneginf(lse).all()
+    scores = ctx.index_scores(cache, kv[:, None, :128], torch.ones(2, 1, device="cuda"), lens - 1, 3)
+    assert ctx.sync() == kvo.KVO_OK and torch.isneginf(scores).all()      # nothing visible: no entry is needed

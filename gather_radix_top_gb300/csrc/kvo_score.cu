@@ -27,6 +27,7 @@
 // (28.4 by then), one loading warp alone 45.2 (it issues a box every 60 clocks),
 // table entries that are used as soon as they are asked for 48.2.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -93,8 +94,9 @@ struct ScoreShared {
 };
 
 // kShared: the CTAs of a row of the grid share the tiles of many tasks out;
-// else a row is one task, whose tiles go to its CTAs in turn.
-template <bool kF8, bool kShared>
+// else a row is one task, whose tiles go to its CTAs in turn.  kPadded: there
+// are fewer heads than columns of a token.
+template <bool kF8, bool kShared, bool kPadded>
 __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __grid_constant__ ScoreArgs a,
                                                                         const __grid_constant__ CUtensorMap map) {
   using S = ScoreShape<kF8>;
@@ -351,6 +353,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
               s1 = fmaf(w.w, max_nan(v[4 * e + 3], 0.0f), s1);
             }
           }
+          // Columns past the last head are no part of the sum, but an infinite
+          // key's products with their zeros are NaN, and so is the sum then:
+          // it is formed again without them.  Asked of the sum, as that is
+          // rare: 13 contexts of 24 heads take 9.2 us, with a bound or a choice
+          // at the last columns' products 9.8 to 10.1, with neither 8.9.
+          if (kPadded && __any_sync(0xffffffffu, isnan(s0 + s1))) {
+            s0 = s1 = 0.0f;
+#pragma unroll 1
+            for (uint32_t c = 0; c < a.heads; c += 4) {
+              float v[4];
+              tmem_ld4(from + g * a.head_cols + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (uint32_t e = 0; e < 4; ++e)
+                if (c + e < a.heads) s0 = fmaf(weights[g * a.head_cols + c + e], max_nan(v[e], 0.0f), s0);
+            }
+          }
           float score = there && (int32_t)p < lens[g] ? (s0 + s1) * factor : -INFINITY;
           float* out = a.scores + (t0 + g) * a.ld;
           if (a.block_shift == 0) {
@@ -478,7 +497,7 @@ bool key_map(CUtensorMap* map, const void* keys, int64_t rows, uint32_t run, boo
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kF8, bool kShared>
+template <bool kF8, bool kShared, bool kPadded>
 cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, cudaStream_t stream) {
   using S = ScoreShape<kF8>;
   CUtensorMap map;
@@ -489,7 +508,7 @@ cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, cudaStream_t s
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(index_scores_kernel<kF8, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(index_scores_kernel<kF8, kShared, kPadded>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
@@ -500,7 +519,7 @@ cudaError_t launch_scores(const ScoreArgs& a, int64_t cache_rows, cudaStream_t s
   const uint64_t most = kShared ? (uint64_t)std::min(a.slice, a.tasks) * tiles : tiles;
   uint32_t x = kShared && rows > 1 ? (2 * sms + rows - 1) / rows : rows <= sms ? sms / rows : 1;
   if (x > most) x = (uint32_t)most;
-  return launch_early(index_scores_kernel<kF8, kShared>, dim3(x, rows), kScoreThreads, smem, stream, a, map);
+  return launch_early(index_scores_kernel<kF8, kShared, kPadded>, dim3(x, rows), kScoreThreads, smem, stream, a, map);
 }
 
 }  // namespace
@@ -565,8 +584,13 @@ extern "C" kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, con
   // and 142, 155.  2,000 of up to 300 keys 52.8, 41.8 and 57.5, 46.5.
   const uint32_t sms = (uint32_t)device_sms();
   const bool shared = 2 * a.tasks > sms && (a.tasks <= 2 * sms || a.n <= 16 * kKeyTile);
-  const auto launch = cache->key_type == KVO_BF16 ? shared ? launch_scores<false, true> : launch_scores<false, false>
-                                                  : shared ? launch_scores<true, true> : launch_scores<true, false>;
+  const auto choose = [&](auto f8, auto is_shared) {
+    return a.heads == a.head_cols ? launch_scores<f8.value, is_shared.value, false> : launch_scores<f8.value, is_shared.value, true>;
+  };
+  using No = std::false_type;
+  using Yes = std::true_type;
+  const auto launch = cache->key_type == KVO_BF16 ? shared ? choose(No{}, Yes{}) : choose(No{}, No{})
+                                                  : shared ? choose(Yes{}, Yes{}) : choose(Yes{}, No{});
   const cudaError_t e = launch(a, rows, on);
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -1072,3 +1072,35 @@ def test_a_table_without_columns_has_no_rows(kvo, ctx, block_rows):
     assert ctx.sync() == kvo.KVO_ERANGE and not out.any() and torch.isneginf(lse).all()
     scores = ctx.index_scores(cache, kv[:, None, :128], torch.ones(2, 1, device="cuda"), lens - 1, 3)
     assert ctx.sync() == kvo.KVO_OK and torch.isneginf(scores).all()      # nothing visible: no entry is needed
+
+
+@pytest.mark.parametrize("heads", [1, 8, 24, 32, 40, 64, 100, 128])
+@pytest.mark.parametrize("per_seq,block", [(1, 1), (1, 16), (3, 1), (2, 4)])
+def test_scores_infinite_keys(kvo, ctx, heads, per_seq, block):
+    """An infinite key scores the sum over the heads there are, whatever they are rounded up to: 0 where every
+    product is -inf, +inf where one is +inf, NaN where infinities of both signs meet."""
+    rng = np.random.default_rng([52, heads, per_seq, block])
+    n = 400
+    q, k, _, w = score_inputs(rng, per_seq, heads, n, "bf16")
+    signs = dev(rng.choice([-1.0, 1.0], (per_seq, heads)), torch.bfloat16)
+    q[:, :, 3], q[:, :, 4], q[:, :, 5] = 1.5, -0.75, signs          # the dimensions that infinite keys have
+    w = w.abs() + 0.125
+    w[-1] *= dev(rng.choice([-1.0, 1.0], heads), torch.float32)     # the last token's weights of both signs
+    infinite = {5: (3, math.inf), 70: (4, math.inf), 131: (5, math.inf), 140: (3, -math.inf), 290: (4, -math.inf),
+                399: (5, -math.inf)}
+    for at, (d, x) in infinite.items():
+        k[at, d] = x
+    cache = kvo.Cache(keys=k, block_rows=n)
+    got = f64(ctx.index_scores(cache, q, w, torch.full((per_seq,), n, dtype=torch.int32, device="cuda"), n, block=block))
+    assert ctx.sync() == kvo.KVO_OK
+    rows, lens = [list(range(n))] * per_seq, [n] * per_seq
+    want, _ = O.index_scores(f64(q), f64(w), f64(k), np.ones(n), rows, lens, block)
+    clean = f64(k)
+    clean[~np.isfinite(clean)] = 0.0                                # what is finite at an infinite key is exactly 0
+    _, size = O.index_scores(f64(q), f64(w), clean, np.ones(n), rows, lens, block)
+    fin = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[~fin & ~np.isnan(want)], want[~fin & ~np.isnan(want)])
+    assert (np.abs(got[fin] - want[fin]) <= ((128 + heads + 2) * 2 * U * size)[fin]).all()
+    assert per_seq == 1 or np.isposinf(want[0]).any()
+    assert block > 1 or (want[:, 70] == 0).all()

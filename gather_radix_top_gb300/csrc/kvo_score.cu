@@ -27,6 +27,7 @@
 // (28.4 by then), one loading warp alone 45.2 (it issues a box every 60 clocks),
 // table entries that are used as soon as they are asked for 48.2.
 #include <algorithm>
+#include <cstddef>
 #include <type_traits>
 
 #include <cuda.h>
@@ -89,9 +90,10 @@ struct ScoreShared {
   uint32_t start[kMostTasks + 1];                               // tiles before each task's
   uint32_t most[kMostTasks];                                    // positions that any of a task's tokens sees
   int32_t len[2][kScoreMaxTokens];                              // of the task at hand and the next
-  float w[2][kScoreMaxCols];
+  alignas(16) float w[2][kScoreMaxCols];                        // read four at a time
   float best[kScoreTeams][4];
 };
+static_assert(alignof(ScoreShared) >= 16 && offsetof(ScoreShared, w) % 16 == 0);
 
 // kShared: the CTAs of a row of the grid share the tiles of many tasks out;
 // else a row is one task, whose tiles go to its CTAs in turn.  kPadded: there

@@ -32,6 +32,7 @@ struct kvo_ctx {
   int32_t* evlog = nullptr;              // device [layers][1 + 3*KVO_MAX_ROUND] when recording
   uint32_t* status = nullptr;            // device status word
   bool resolved = false;                 // a resolve has been enqueued (the policy is fixed from then on)
+  int64_t wait_clocks = KVO_WAIT_CLOCKS; // after which a wait of the operators on a kvo_cache gives up
   bool unusable = false;                 // a bulk copy may still land in freed shared memory: no more launches
   uint32_t ring_rows = 0;                // recent ring rows per layer (0: appends go straight to RAM)
   std::vector<int64_t> ram_len;          // per layer: rows the host history (RAM) holds
@@ -317,10 +318,11 @@ __global__ void probe_kernel(const uint4* __restrict__ src, uint64_t nvec, uint6
 
 namespace kvo {
 
-kvo_status usable_status(kvo_ctx* ctx, uint32_t** status) {
+kvo_status usable_status(kvo_ctx* ctx, uint32_t** status, int64_t* wait_clocks) {
   if (!ctx) return KVO_EINVAL;
   if (ctx->unusable) return KVO_ECUDA;
   *status = ctx->status;
+  if (wait_clocks) *wait_clocks = ctx->wait_clocks;
   return KVO_OK;
 }
 
@@ -687,6 +689,12 @@ kvo_status kvo_set_policy(kvo_ctx* ctx, int32_t policy) {
   if (!ctx || (policy != KVO_POLICY_LRU && policy != KVO_POLICY_CIRCULAR)) return KVO_EINVAL;
   if (ctx->resolved) return KVO_EBUSY;
   for (kvo::LayerView& v : ctx->views) v.policy = (uint32_t)policy;
+  return KVO_OK;
+}
+
+kvo_status kvo_debug_set_wait_clocks(kvo_ctx* ctx, int64_t clocks) {
+  if (!ctx || clocks < 0) return KVO_EINVAL;
+  ctx->wait_clocks = clocks;
   return KVO_OK;
 }
 

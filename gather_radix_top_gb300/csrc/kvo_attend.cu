@@ -94,6 +94,7 @@ struct AttendArgs {
   uint32_t per_seq, heads, nq;
   uint32_t head_tiles, splits;
   float scale;               // times log2(e)
+  int64_t wait_clocks;       // after which a wait gives up
 };
 
 struct AttendShared {
@@ -198,6 +199,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes;
   const uint32_t stage = queries + S::kQueryBytes;
 
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+  };
+
   wait_previous_grid();
   allow_next_grid();
   const int32_t len = a.lens[t];
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     const uint32_t dst = stage + r * kPitch;
     uint32_t i = 0;
     for (; i < tiles; ++i) {
-      const bool ok = i == 0 || wait_or_give_up(&sh.raw_empty, (i - 1) & 1, &sh.gave_up);
+      const bool ok = i == 0 || wait(&sh.raw_empty, (i - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
       if (row < 0 && r < rows_of(i)) {
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       // the raw rows to bf16, part by part, as the products of the last tile
       // release their places; the second half of them is in registers, and the
       // next rows may come, before its places are free
-      wait_or_give_up(&sh.raw_full, turn, &sh.gave_up);
+      wait(&sh.raw_full, turn);
       const bool there =
           mine_row < rows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
       uint32_t scales[S::kPasses][2];                    // this piece's scale of each part, as fp16 pairs
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (part) rope[u] = lds16(p - 256 + KVO_LATENT_BYTES + 16);
           }
         if (part) warp_arrive(&sh.raw_empty, lane);
-        if (i > 0) wait_or_give_up(&sh.pv_done[part], turn ^ 1, &sh.gave_up);
+        if (i > 0) wait(&sh.pv_done[part], turn ^ 1);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k) {
 #pragma unroll
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
 
       // softmax: this thread has row mine_row against kCols heads
-      wait_or_give_up(&sh.s_full, turn, &sh.gave_up);
+      wait(&sh.s_full, turn);
       __syncwarp();
       tc_fence_after();
       float x[kCols];
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       warp_arrive(&sh.voted[quarter], lane);
 #pragma unroll
       for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(x[c]);
-      wait_or_give_up(&sh.voted[quarter], turn, &sh.gave_up);
+      wait(&sh.voted[quarter], turn);
       const bool far = *(volatile uint32_t*)&sh.far[turn][quarter] != 0;
       if (quad == 0 && lane == 0) sh.far[turn ^ 1][quarter] = 0;
       if (unset || far) {                                // the same in all four warps
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
         if (lane < kCols) sh.top[quarter][quad][lane] = best;
         warp_arrive(&sh.met[quarter], lane);
-        const bool all = wait_or_give_up(&sh.met[quarter], meets & 1, &sh.gave_up);
+        const bool all = wait(&sh.met[quarter], meets & 1);
         if (!__all_sync(0xffffffffu, all)) break;
         ++meets;
         float alpha = 1.0f;
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     __syncwarp();
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
-      if (j % 2 == 0) wait_or_give_up(&sh.pv_done[j / 2], (tiles - 1) & 1, &sh.gave_up);
+      if (j % 2 == 0) wait(&sh.pv_done[j / 2], (tiles - 1) & 1);
       __syncwarp();
       tc_fence_after();
       float o[kCols];
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       // tile has fewer rows: the others are whatever lies behind, and masked.)
 #pragma unroll
       for (uint32_t part = 0; part < 2; ++part) {
-        ok = ok && wait_or_give_up(&sh.k_full[part], turn, &sh.gave_up);
+        ok = ok && wait(&sh.k_full[part], turn);
         __syncwarp();
         fence_proxy_async_smem();                        // the workers' stores, before the MMAs read them
         tc_fence_after();
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
         __syncwarp();
       }
-      ok = ok && wait_or_give_up(&sh.p_full, turn, &sh.gave_up);
+      ok = ok && wait(&sh.p_full, turn);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_proxy_async_smem();
       tc_fence_after();
@@ -823,10 +828,12 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
   if (need < 0 || s->work_bytes < need || (need && !s->work)) return KVO_EINVAL;
   if (!aligned(s->q, 16) || s->q_ld % 8 || s->q_head_ld % 8 || !aligned(s->out, 16)) return KVO_EINVAL;
   if (!aligned(s->lens, 4) || !aligned(s->sel, 4) || !aligned(s->lse, 4) || !aligned(s->work, 16)) return KVO_EINVAL;
-  const kvo_status st = usable_status(ctx, &status);
+  int64_t wait_clocks = 0;
+  const kvo_status st = usable_status(ctx, &status, &wait_clocks);
   if (st != KVO_OK) return st;
 
   AttendArgs a = {};
+  a.wait_clocks = wait_clocks;
   a.cache = cache_view(*cache);
   a.q = static_cast<const uint8_t*>(s->q);
   a.lens = s->lens;

@@ -13,10 +13,10 @@
 
 namespace kvo {
 
-// From the context (kvo_api.cu).  Its device status word, for calls that keep
-// no other state in it; KVO_EINVAL without a context, KVO_ECUDA for one that
-// must not launch.
-kvo_status usable_status(kvo_ctx* ctx, uint32_t** status);
+// From the context (kvo_api.cu).  Its device status word and the clocks after
+// which a wait gives up, for calls that keep no other state in it; KVO_EINVAL
+// without a context, KVO_ECUDA for one that must not launch.
+kvo_status usable_status(kvo_ctx* ctx, uint32_t** status, int64_t* wait_clocks = nullptr);
 
 // Streaming multiprocessors of the current device (152 where none can be asked).
 int device_sms();

@@ -68,6 +68,7 @@ struct ScoreArgs {
   uint32_t tasks, slice;     // groups of all sequences, and how many of them a row of the grid shares out
   uint32_t accs;             // accumulators in tensor memory: 4, or 2 of more than 128 columns
   uint32_t tmem_cols;
+  int64_t wait_clocks;       // after which a wait gives up
   uint32_t run;              // consecutive keys that never leave their block (>= 4), or 1
 };
 
@@ -85,6 +86,7 @@ struct ScoreShared {
   uint64_t full[8], empty[8], acc_full[4], acc_empty[4], q_full, task_done, drained;
   uint32_t tmem;
   uint32_t gave_up;
+  uint32_t brought[kLoadWarps];                                 // per loading warp: its first tile that it has not brought
   uint32_t first, last, first_task;                             // this CTA's tiles
   uint32_t warp_tiles[kScoreThreads / 32], warp_cost[kScoreThreads / 32];
   uint32_t start[kMostTasks + 1];                               // tiles before each task's
@@ -127,6 +129,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
     return (uint32_t)most;
   };
 
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+  };
+
   wait_previous_grid();
   allow_next_grid();
   if (tid == 0) {
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
     mbar_init(&sh.q_full, kLoadWarp);
     mbar_init(&sh.task_done, 1);
     mbar_init(&sh.drained, 1);
-    sh.gave_up = 0;
+    sh.gave_up = a.wait_clocks == 0;
     sh.first = sh.last = sh.first_task = 0;
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, a.tmem_cols);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         if (lane == 0) mbar_arrive(&sh.q_full);
       };
       auto next_task = [&] {
-        wait_or_give_up(&sh.task_done, nth & 1, &sh.gave_up);
+        wait(&sh.task_done, nth & 1);
         __syncwarp();
         do ++task;
         while (sh.start[task + 1] == sh.start[task]);
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         bring_queries();
       };
       bring_queries();
-      wait_or_give_up(&sh.q_full, 0, &sh.gave_up);
+      wait(&sh.q_full, 0);
 
       // table entries are asked for two of this team's tiles ahead, the keys'
       // factors one
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       for (uint32_t i = acc, turn = 0; i < mine; i += a.accs, turn ^= 1) {
         if (behind(i, task)) {
           while (behind(i, task)) next_task();
-          wait_or_give_up(&sh.q_full, nth & 1, &sh.gave_up);
+          wait(&sh.q_full, nth & 1);
         }
         const float* weights = sh.w[nth & 1];
         const int32_t* lens = sh.len[nth & 1];
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         block_after = look_up(i + 2 * a.accs);
         // after a wait that gave up the team goes on through what it finds
         // (its warps meet at barriers below); the status says so
-        wait_or_give_up(&sh.acc_full[acc], turn, &sh.gave_up);
+        wait(&sh.acc_full[acc], turn);
         __syncwarp();
         tc_fence_after();
         for (uint32_t g = part; g < tokens; g += parts) {
@@ -399,16 +405,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       uint32_t next = turn0;                                    // this warp's next tile
       for (; next < S::kStages && next < mine; next += kLoadWarps) bring(next);
       for (; next < mine; next += kLoadWarps) {                 // the slot held tile next - kStages
-        const bool ok = wait_or_give_up(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1, &sh.gave_up);
+        const bool ok = wait(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1);
         if (__any_sync(0xffffffffu, !ok)) break;
         bring(next);
       }
-      // where the CTA gives up, the copies in flight finish before it ends
-      // (the last tile of each slot that this warp has brought)
-      if (next < mine)
-        for (uint32_t i = next < S::kStages + kLoadWarps ? turn0 : next - S::kStages; i < next; ++i)
-          if ((i - turn0) % kLoadWarps == 0 && !landed(&sh.full[i % S::kStages], (i / S::kStages) & 1))
-            atomicOr(a.status, kFlagInflight);
+      if (lane == 0) sh.brought[turn0] = next;
     } else {
       // the whole warp walks along, one elected lane issues: what a converged
       // warp computes stays in the uniform registers that the MMAs read
@@ -416,16 +417,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
       const uint64_t keys = tile_desc(ring, 16), heads = tile_desc(queries, 16);
       const uint64_t next_half = (cols * 128) >> 4;
       uint32_t task = first_task, nth = 0;
-      bool ok = wait_or_give_up(&sh.q_full, 0, &sh.gave_up);
+      bool ok = wait(&sh.q_full, 0);
       for (uint32_t i = 0, slot = 0, slot_turn = 0, acc = 0, acc_turn = 0; i < mine; ++i) {
         if (behind(i, task)) {                                  // the next task: its queries replace these
           if (elect_one()) mma_commit(&sh.task_done);
           __syncwarp();
           walk(i, task);
-          ok = ok && wait_or_give_up(&sh.q_full, ++nth & 1, &sh.gave_up);
+          ok = ok && wait(&sh.q_full, ++nth & 1);
         }
-        ok = ok && wait_or_give_up(&sh.full[slot], slot_turn & 1, &sh.gave_up) &&
-             (acc_turn == 0 || wait_or_give_up(&sh.acc_empty[acc], (acc_turn - 1) & 1, &sh.gave_up));
+        ok = ok && wait(&sh.full[slot], slot_turn & 1) &&
+             (acc_turn == 0 || wait(&sh.acc_empty[acc], (acc_turn - 1) & 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -448,17 +449,31 @@ __global__ void __launch_bounds__(kScoreThreads, 1) index_scores_kernel(const __
         if (++slot == S::kStages) slot = 0, ++slot_turn;
         if (++acc == a.accs) acc = 0, ++acc_turn;
       }
-      if (!ok && elect_one()) {
-        // let the MMAs in flight finish before their memory is given back
-        mma_commit(&sh.drained);
-        atomicOr(a.status, kFlagTimeout);
-        if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
-      }
-      __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
+    // Where any wait gave up, whoever it was, what is in flight finishes before
+    // the CTA ends and its memory is given back: the MMAs (the lane that issued
+    // them commits), and the last tile that was brought to each slot.  (One
+    // before it has landed: its product released the slot.)
+    if (sh.gave_up) {
+      if (tid == 0) atomicOr(a.status, kFlagTimeout);
+      if (warp == kMmaWarp) {
+        if (elect_one()) {
+          mma_commit(&sh.drained);
+          if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
+        }
+      } else if (warp == kLoadWarp && lane < S::kStages) {
+        uint32_t to = 0;                                        // past the last tile that was brought
+        for (uint32_t w = 0; w < kLoadWarps; ++w) to = max(to, sh.brought[w]);
+        for (uint32_t i = to; i-- > 0;)
+          if (i % S::kStages == lane && i < sh.brought[i % kLoadWarps]) {
+            if (!landed(&sh.full[lane], (i / S::kStages) & 1)) atomicOr(a.status, kFlagInflight);
+            break;
+          }
+      }
+      __syncthreads();
+    }
   }
   __syncwarp();
   if (warp == kMmaWarp) tmem_free(tmem, a.tmem_cols);
@@ -540,10 +555,12 @@ extern "C" kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, con
   if (nq > KVO_MAX_QUERIES || s->ld < (s->n + s->block - 1) / s->block) return KVO_EINVAL;
   if (!aligned(s->q, 16) || (s->q_ld * size) % 16 || (s->q_head_ld * size) % 16) return KVO_EINVAL;
   if (!aligned(s->weights, 4) || !aligned(s->lens, 4) || !aligned(s->scores, 4)) return KVO_EINVAL;
-  const kvo_status st = usable_status(ctx, &status);
+  int64_t wait_clocks = 0;
+  const kvo_status st = usable_status(ctx, &status, &wait_clocks);
   if (st != KVO_OK) return st;
 
   ScoreArgs a = {};
+  a.wait_clocks = wait_clocks;
   a.cache = cache_view(*cache);
   if (cache->key_type == KVO_BF16) a.cache.key_scales = nullptr;
   a.q = static_cast<const uint8_t*>(s->q);

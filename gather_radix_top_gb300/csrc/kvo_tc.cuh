@@ -9,6 +9,7 @@
 
 #include <cstdint>
 
+#include "kvo.h"
 #include "kvo_device.cuh"
 
 namespace kvo {
@@ -128,11 +129,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// A CTA whose waits share `gave_up` (a shared-memory word, zero at start).
-// Waits for phase `parity` of `bar`; after about a second of clocks, or as
-// soon as another thread of the CTA has given up, it returns false.
-constexpr long long kWaitClocks = 2000000000ll;
-__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
+// A CTA whose waits share `gave_up` (a shared-memory word).  Waits for phase
+// `parity` of `bar`; after `clocks`, or as soon as another thread of the CTA
+// has given up, it returns false.  What is in flight then is waited for once
+// more before the CTA ends, with landed().
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up,
+                                                long long clocks) {
   const uint32_t a = smem_u32(bar);
   uint32_t done;
   long long start = 0;
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, 
       if (*gave_up) return false;
       const long long now = clock64();
       if (start == 0) start = now;
-      if (now - start > kWaitClocks) {
+      if (now - start > clocks) {
         *gave_up = 1;
         return false;
       }
@@ -156,11 +158,11 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, 
 }
 
 // Waits for a phase that work in flight completes, whether or not other
-// waits have given up; false after the same bounded time.
+// waits have given up; false after about a second.
 __device__ __forceinline__ bool landed(uint64_t* bar, uint32_t parity) {
   const long long start = clock64();
   while (!mbar_test(bar, parity))
-    if (clock64() - start > kWaitClocks) return false;
+    if (clock64() - start > KVO_WAIT_CLOCKS) return false;
   return true;
 }
 

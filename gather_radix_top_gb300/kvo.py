@@ -27,6 +27,7 @@ LATENT_VALUES, ROPE_VALUES, KEY_VALUES = 512, 64, 128
 MAX_HEADS = 128
 MAX_SCORE_BLOCK = 128
 MAX_QUERIES = 65535
+WAIT_CLOCKS = 2_000_000_000
 
 KVO_OK, KVO_EINVAL, KVO_ENOMEM, KVO_ECUDA, KVO_ERANGE, KVO_EBUSY, KVO_ETIMEDOUT, KVO_ECAPACITY = (
     0, -1, -2, -3, -4, -5, -6, -7)
@@ -45,7 +46,7 @@ EXPORTED = [
     "kvo_pool_debug_free_queue", "kvo_copy_blocks_noalloc", "kvo_set_phase_timing", "kvo_layers_phase_times",
     "kvo_layers_counters", "kvo_probe_host_touch", "kvo_debug_history_host", "kvo_set_miss_fetch",
     "kvo_touch_history", "kvo_append_tokens", "kvo_index_scores", "kvo_attend", "kvo_attend_work_bytes",
-    "kvo_pool_rows",
+    "kvo_pool_rows", "kvo_debug_set_wait_clocks",
 ]
 
 
@@ -153,6 +154,7 @@ def lib() -> ctypes.CDLL:
         "kvo_debug_read_history": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp]),
         "kvo_debug_layer_counters": (ctypes.c_int, [_vp, _i32, _vp]),
         "kvo_debug_raise_status": (ctypes.c_int, [_vp, ctypes.c_uint32]),
+        "kvo_debug_set_wait_clocks": (ctypes.c_int, [_vp, _i64]),
         "kvo_tier_blocks": (_i64, [_i64, _i64]),
         "kvo_pool_create": (ctypes.c_int, [_i32, _i64, _i32, _i32, _i64, ctypes.POINTER(_vp)]),
         "kvo_pool_destroy": (ctypes.c_int, [_vp]),
@@ -861,6 +863,9 @@ class Context:
 
     def raise_status(self, bits):
         _check(lib().kvo_debug_raise_status(self.handle, bits), "kvo_debug_raise_status")
+
+    def set_wait_clocks(self, clocks=WAIT_CLOCKS):
+        _check(lib().kvo_debug_set_wait_clocks(self.handle, clocks), "kvo_debug_set_wait_clocks")
 
     def record_evictions(self, on=True):
         kvo_debug_record_evictions(self.handle, on)

@@ -427,6 +427,17 @@ kvo_status kvo_debug_layer_counters(kvo_ctx* ctx, int32_t layer, uint32_t* out);
 kvo_status kvo_debug_raise_status(kvo_ctx* ctx, uint32_t bits);
 
 /*
+ * kvo_debug_set_wait_clocks - test hook: the GPU clocks after which a wait
+ * inside kvo_index_scores and kvo_attend gives up (KVO_WAIT_CLOCKS, about a
+ * second, unless set).  0: as if some wait had given up before the first: the
+ * call goes the way of a timeout from its start and ends in KVO_ETIMEDOUT.
+ * The outputs of a call that timed out are undefined.  Takes effect for later
+ * calls.  KVO_EINVAL: clocks < 0.
+ */
+#define KVO_WAIT_CLOCKS 2000000000ll
+kvo_status kvo_debug_set_wait_clocks(kvo_ctx* ctx, int64_t clocks);
+
+/*
  * kvo_debug_record_evictions - when enabled (on != 0), every resolve call
  * records its fills as (slot, evicted position or -1, new position) triples,
  * in the order the misses took them.  kvo_debug_evictions copies the last

@@ -1104,3 +1104,45 @@ def test_scores_infinite_keys(kvo, ctx, heads, per_seq, block):
     assert (np.abs(got[fin] - want[fin]) <= ((128 + heads + 2) * 2 * U * size)[fin]).all()
     assert per_seq == 1 or np.isposinf(want[0]).any()
     assert block > 1 or (want[:, 70] == 0).all()
+
+
+# Waits that run out.  Clocks of 0 say that a wait has given up before the first one; a few clocks end some waits or
+# none, as the GPU's work falls: a call then ends in KVO_ETIMEDOUT, or gives what it always gives.
+WAITS = (0, 0, 1, 100, 1_000, 4_000, 0, 20_000, 400)
+
+
+def check_waits(kvo, run):
+    """`run(context)` returns outputs; nothing of a call that timed out is in the next one's way."""
+    c = kvo.Context(1, 64, 64)
+    want = [t.clone() for t in run(c)]
+    assert c.sync() == kvo.KVO_OK
+    for clocks in WAITS:
+        c.set_wait_clocks(clocks)
+        got = run(c)
+        status = c.sync()
+        assert status in ((kvo.KVO_ETIMEDOUT,) if clocks == 0 else (kvo.KVO_OK, kvo.KVO_ETIMEDOUT))
+        assert c.sync() == kvo.KVO_OK                            # said once, and the context goes on
+        c.set_wait_clocks()
+        for again in (got if status == kvo.KVO_OK else None, run(c)):
+            for a, b in zip(again or (), want):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), clocks
+        assert c.sync() == kvo.KVO_OK
+    c.close()
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("sequences,per_seq,heads,n,block,block_rows", [
+    (1, 1, 16, 100, 1, 16), (1, 1, 64, 160_000, 1, 16), (1, 4, 64, 60_000, 128, 0), (1, 2, 20, 30_000, 4, 5),
+    (120, 1, 64, 1_500, 1, 16), (90, 5, 64, 700, 64, 48)])
+def test_scores_waits_that_run_out(kvo, dtype, sequences, per_seq, heads, n, block, block_rows):
+    rng = np.random.default_rng([53, sequences, per_seq, heads, n])
+    nq = sequences * per_seq
+    br = block_rows or n
+    blocks = -(-n // br)
+    total = sequences * blocks
+    q, k, scales, w = score_inputs(rng, nq, heads, total * br, dtype)
+    table = None if not block_rows else dev(rng.permutation(total).reshape(sequences, blocks).astype(np.int32))
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=br, table=table)
+    lens = dev(rng.integers(0, n + 1, nq), torch.int32)
+    lens[0] = n
+    check_waits(kvo, lambda c: [c.index_scores(cache, q, w, lens, n, block=block)])

@@ -213,3 +213,10 @@ int main() {
     want = [O.row_of(table, 100, 16, 2, s, p) for s in range(2) for p in range(80)]
     assert got[:160] == [-1 if w is None else w for w in want]
     assert got[160:] == [-1, 0, 3999999999, -1]
+
+
+def test_wait_clocks_refusals(kvo, ctx):
+    call = kvo.lib().kvo_debug_set_wait_clocks
+    assert call(None, 5) == kvo.KVO_EINVAL
+    assert call(ctypes.addressof(ctx), -1) == kvo.KVO_EINVAL
+    assert call(ctypes.addressof(ctx), 0) == kvo.KVO_OK

@@ -101,6 +101,7 @@ struct AttendShared {
   uint64_t k_full[2], s_full, p_full, pv_done[2], voted[4], met[4], raw_full, raw_empty, drained;
   uint32_t tmem;
   uint32_t gave_up;
+  uint32_t brought[kLoadWarps];      // per loading warp: tiles whose rows it has brought
   uint32_t there[2][kLoadWarps];     // tile i's rows that are not masked, in i % 2: row r is bit r / 3 of word r % 3
   uint32_t far[2][4];                // per quarter of the columns, in i % 2: tile i needs new references
   float top[4][4][16];               // per quarter of the columns and warp
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     mbar_init(&sh.raw_empty, kWorkerWarps);
     mbar_init(&sh.drained, 1);
     for (uint32_t i = 0; i < 8; ++i) sh.far[i >> 2][i & 3] = 0;
-    sh.gave_up = 0;
+    sh.gave_up = a.wait_clocks == 0;
   }
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, S::kTmemCols);
   __syncthreads();
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     unit = unit2;
     const uint32_t dst = stage + r * kPitch;
     uint32_t i = 0;
-    for (; i < tiles; ++i) {
+    for (; i < tiles; ++i) {                             // (the workers let go of a tile only once all of it has come)
       const bool ok = i == 0 || wait(&sh.raw_empty, (i - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
@@ -307,8 +308,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       block = block_of(pos);
       unit = listed(i + 3);
     }
-    // where the CTA gives up, the last copies finish before it ends
-    if (i < tiles && i > 0 && !landed(&sh.raw_full, (i - 1) & 1)) atomicOr(a.status, kFlagInflight);
+    if (lane == 0) sh.brought[load] = i;
   } else {
     // the queries: heads past the last are zeros
     for (uint32_t i = tid; i < kHeads * 72; i += kLoadWarp * 32) {
@@ -350,13 +350,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     for (uint32_t c = 0; c < kCols; ++c) sum[c] = 0.0f;
     const uint32_t lanes = tmem + (quad << 21);          // (quad * 32) << 16
 
+    bool come = true;                                    // every tile's rows so far
     for (uint32_t i = 0; i < tiles; ++i) {
       const uint32_t turn = i & 1;
       const uint32_t rows = rows_of(i);
       // the raw rows to bf16, part by part, as the products of the last tile
       // release their places; the second half of them is in registers, and the
       // next rows may come, before its places are free
-      wait(&sh.raw_full, turn);
+      come &= wait(&sh.raw_full, turn);
       const bool there =
           mine_row < rows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
       uint32_t scales[S::kPasses][2];                    // this piece's scale of each part, as fp16 pairs
@@ -378,7 +379,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             lat[1][u] = lds16(p + 128);
             if (part) rope[u] = lds16(p - 256 + KVO_LATENT_BYTES + 16);
           }
-        if (part) warp_arrive(&sh.raw_empty, lane);
+        if (part) {                                        // after a wait that gave up the next rows must not come
+          __syncwarp();
+          if (lane == 0 && come) mbar_arrive(&sh.raw_empty);
+        }
         if (i > 0) wait(&sh.pv_done[part], turn ^ 1);
 #pragma unroll
         for (uint32_t k = 0; k < 2; ++k) {
@@ -419,8 +423,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
       // whether a row of the four warps lies too far above the references: said
       // through a flag and a barrier that is waited for behind the exponentials
-      const bool quit = *(volatile uint32_t*)&sh.gave_up != 0;
-      if (__any_sync(0xffffffffu, quit || (there && most > kFar)) && lane == 0) sh.far[turn][quarter] = 1;
+      if (__any_sync(0xffffffffu, there && most > kFar) && lane == 0) sh.far[turn][quarter] = 1;
       warp_arrive(&sh.voted[quarter], lane);
 #pragma unroll
       for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(x[c]);
@@ -602,19 +605,29 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       }
       __syncwarp();
     }
-    if (!__all_sync(0xffffffffu, ok) && elect_one()) {
-      // let the MMAs in flight finish before their memory is given back
-      // (the lane that issued them commits)
-      mma_commit(&sh.drained);
-      atomicOr(a.status, kFlagTimeout);
-      if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && sh.gave_up) atomicOr(a.status, kFlagTimeout);
-  __syncwarp();
+  // Where any wait gave up, whoever it was, what is in flight finishes before
+  // the CTA ends and its memory is given back: the MMAs (the lane that issued
+  // them commits) and the last tile's copies.  A loading warp that had given up
+  // before that tile arrives for it, so that its phase can end; the tile before
+  // had come whole.
+  if (sh.gave_up) {
+    if (tid == 0) atomicOr(a.status, kFlagTimeout);
+    if (warp == kMmaWarp) {
+      if (elect_one()) {
+        mma_commit(&sh.drained);
+        if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
+      }
+    } else if (warp >= kLoadWarp && lane == 0) {
+      uint32_t most = 0;
+      for (uint32_t w = 0; w < kLoadWarps; ++w) most = max(most, sh.brought[w]);
+      if (sh.brought[warp - kLoadWarp] < most) mbar_arrive(&sh.raw_full);
+      if (most && !landed(&sh.raw_full, (most - 1) & 1)) atomicOr(a.status, kFlagInflight);
+    }
+    __syncthreads();
+  }
   if (warp == kMmaWarp) tmem_free(tmem, S::kTmemCols);
 }
 

@@ -1146,3 +1146,20 @@ def test_scores_waits_that_run_out(kvo, dtype, sequences, per_seq, heads, n, blo
     lens = dev(rng.integers(0, n + 1, nq), torch.int32)
     lens[0] = n
     check_waits(kvo, lambda c: [c.index_scores(cache, q, w, lens, n, block=block)])
+
+
+@pytest.mark.parametrize("sequences,heads,n,sel_block,picked,block_rows", [
+    (1, 64, 70, 1, None, 16), (1, 16, 40_000, 1, None, 16), (2, 64, 30_000, 1, None, 64), (1, 128, 20_000, 1, 2048, 16),
+    (160, 64, 600, 1, None, 16), (170, 20, 900, 16, 30, 16), (77, 40, 2_000, 1, 700, 48)])
+def test_attend_waits_that_run_out(kvo, sequences, heads, n, sel_block, picked, block_rows):
+    rng = np.random.default_rng([54, sequences, heads, n, sel_block])
+    blocks, total = -(-n // block_rows), max(4_000 // block_rows, 8)
+    table = dev(rng.integers(0, total, (sequences, blocks)).astype(np.int32))
+    cache = kvo.Cache(rows=dev(random_rows(rng, total * block_rows)), block_rows=block_rows, table=table)
+    q = dev(rng.standard_normal((sequences, heads, 576)), torch.bfloat16)
+    lens = dev(rng.integers(0, n + 1, sequences), torch.int32)
+    lens[0] = n
+    sel = None
+    if picked is not None:
+        sel = dev(np.sort(rng.integers(0, n // sel_block, (sequences, picked)), 1).astype(np.int32))
+    check_waits(kvo, lambda c: c.attend(cache, q, lens, 192 ** -0.5, rows=n, sel=sel, sel_block=sel_block))

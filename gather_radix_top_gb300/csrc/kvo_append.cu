@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) appen
   }
 
   // position part: the angle's turns modulo one are the low 64 bits of
-  // pos * turn, off by at most pos * 2^-64 turns; its top 32 bits as a signed
+  // pos * turn, off by at most 2 pos * 2^-64 turns; its top 32 bits as a signed
   // number are half turns in [-1, 1).
   const uint64_t turns = (uint64_t)(uint32_t)p * a.turn[lane];
   float sn, cs;
@@ -242,15 +242,15 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) appen
 
 // inv_freq / 2 pi modulo 1, times 2^64: the quotient in two doubles (1 / 2 pi
 // as the nearest double and what that leaves), so that no far position sees
-// the rounding of either.
+// the rounding of either.  A negative one's is the other's complement: as a
+// double, a whole turn less a small part would lose bits of the part.
 uint64_t turns_of(double inv_freq) {
   constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;
-  const double hi = inv_freq * kInv;
-  const double lo = std::fma(inv_freq, kInv, -hi) + inv_freq * kInvLow;
-  double f = hi - std::floor(hi);
-  if (f >= 1.0) f = 0.0;                // a tiny negative quotient, rounded up to a whole turn
-  const uint64_t u = (uint64_t)(f * 18446744073709551616.0);
-  return u + (uint64_t)(int64_t)(lo * 18446744073709551616.0);
+  const double x = std::fabs(inv_freq), hi = x * kInv;
+  const double lo = std::fma(x, kInv, -hi) + x * kInvLow;
+  const uint64_t u = (uint64_t)((hi - std::floor(hi)) * 18446744073709551616.0) +
+                     (uint64_t)(int64_t)(lo * 18446744073709551616.0);
+  return inv_freq < 0.0 ? 0 - u : u;
 }
 
 }  // namespace

@@ -1163,3 +1163,32 @@ def test_attend_waits_that_run_out(kvo, sequences, heads, n, sel_block, picked, 
     if picked is not None:
         sel = dev(np.sort(rng.integers(0, n // sel_block, (sequences, picked)), 1).astype(np.int32))
     check_waits(kvo, lambda c: c.attend(cache, q, lens, 192 ** -0.5, rows=n, sel=sel, sel_block=sel_block))
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_append_negative_frequencies(kvo, ctx, interleaved):
+    """Rotations backwards, of small frequencies among them, up to position 2^31 - 1."""
+    rng = np.random.default_rng(55)
+    freq = -INV_FREQ
+    freq[::3] = -np.exp(rng.uniform(np.log(1e-19), np.log(1e-7), len(freq[::3])))
+    pos = np.array([0, 1, 4_097, 1_048_575, 2 ** 31 - 1], np.int32)
+    n, block = len(pos), 2 ** 30
+    rows = torch.zeros(n, 656, dtype=torch.uint8, device="cuda")
+    kv = rng.standard_normal((n, 576)).astype(np.float32)
+    for i, p in enumerate(pos):
+        # one block of 2^30 rows, of which only the addressed row exists: its base is shifted
+        table = torch.full((1, 2), -1, dtype=torch.int32, device="cuda")
+        table[0, int(p) // block] = 0
+        big = kvo.Cache(rows=rows[i:i + 1], block_rows=1, table=table)
+        big.c.block_rows, big.c.blocks = block, 1
+        big.c.rows = rows.data_ptr() + i * 656 - (int(p) % block) * 656
+        ctx.append_tokens(big, dev(kv[i:i + 1, :512]), dev(kv[i:i + 1, 512:]), dev(pos[i:i + 1]), freq,
+                          interleaved=interleaved)
+    assert ctx.sync() == kvo.KVO_OK
+    out = rows.cpu().numpy()
+    for i, p in enumerate(pos):
+        x = kv[i, 512:].astype(np.float64)
+        exact = O.rotate(x, int(p), freq, interleaved)
+        pair = np.abs(x[0::2]) + np.abs(x[1::2]) if interleaved else np.abs(x[:32]) + np.abs(x[32:])
+        pair = np.repeat(pair, 2) if interleaved else np.tile(pair, 2)
+        assert (np.abs(O.row_values(out[i])[1] - exact) <= 2.0 ** -8 * np.abs(exact) + 8 * U * pair).all(), p

@@ -220,3 +220,36 @@ def test_wait_clocks_refusals(kvo, ctx):
     assert call(None, 5) == kvo.KVO_EINVAL
     assert call(ctypes.addressof(ctx), -1) == kvo.KVO_EINVAL
     assert call(ctypes.addressof(ctx), 0) == kvo.KVO_OK
+
+
+def test_turns_of_either_sign(tmp_path):
+    """inv_freq / 2 pi modulo one turn, in units of 2^-64: off by at most one unit for each of the two parts it is put
+    together from, whatever the sign (an angle at position 2^31 - 1 is off by 2^-32 turns at most)."""
+    from fractions import Fraction
+    from gather_radix_top_gb300 import build
+    src = tmp_path / "turns.cu"
+    src.write_text("""
+#include <cstdio>
+#include <cstdlib>
+#include "kvo_append.cu"
+kvo_status kvo::usable_status(kvo_ctx*, uint32_t**, int64_t*) { return KVO_ECUDA; }
+int kvo::device_sms() { return 1; }
+int main(int argc, char** argv) {
+  for (int i = 1; i < argc; ++i)
+    std::printf("%llu\\n", (unsigned long long)kvo::turns_of(std::strtod(argv[i], nullptr)));
+}
+""")
+    exe = tmp_path / "turns"
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-o", str(exe),
+                    str(src)], check=True)
+    rng = np.random.default_rng(3)
+    x = [0.0, 1.0, 1e-5, 3e-9, 1e-15, 2.0 ** -40, 0.7, 6.283185307179586, 1234.5, 2.0 ** 20, 1e-30, 5e-324]
+    x += list(np.exp(rng.uniform(np.log(1e-20), np.log(2.0 ** 20), 200)))
+    x = [s * v for v in x for s in (1.0, -1.0)]
+    got = subprocess.run([str(exe), *[float(v).hex() for v in x]], check=True, capture_output=True, text=True).stdout.split()
+    two_pi = Fraction(62831853071795864769252867665590057683943387987502116419498891846156328125724179972560696506842341359,
+                      10 ** 100)
+    for v, g in zip(x, got):
+        want = Fraction(v) / two_pi * 2 ** 64
+        off = (Fraction(int(g)) - want) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 2, (v, float(min(off, 2 ** 64 - off)))

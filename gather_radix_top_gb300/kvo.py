@@ -654,8 +654,8 @@ def _queries(cache: Cache, q, values: int, dtype) -> tuple:
     if q.dim() != 3 or q.shape[2] != values:
         raise ValueError(f"q must be [queries, heads, {values}]")
     nq, heads, _ = shape = q.shape
-    if nq < 1 or nq % cache.sequences:
-        raise ValueError("the number of queries must be a multiple of the cache's sequences")
+    if nq < 1 or cache.sequences < 1 or nq % cache.sequences:
+        raise ValueError("the number of queries must be a multiple of the cache's sequences, both at least 1")
     ptr = _cuda(q, "q", dtype, shape)
     q_ld, head_ld, _ = q.stride()
     # a dimension of one has no next element: its stride says nothing

@@ -34,3 +34,14 @@ def test_a_table_without_columns_is_a_table(kvo, table):
     full = kvo.Cache(rows=rows(), block_rows=4, table=on_gpu(torch.zeros(2, 9, dtype=torch.int32)[:, 5:6])).c
     assert full.table_blocks == 1 and full.table_ld == 9
     assert not kvo.Cache(rows=rows(), block_rows=4).c.table
+
+
+def test_a_cache_of_no_sequences_is_refused(kvo):
+    """A table without rows: the calls say what is wrong, before anything is launched."""
+    table = on_gpu(torch.empty(0, 4, dtype=torch.int32))
+    cache = kvo.Cache(rows=rows(), keys=on_gpu(torch.zeros(16, 128, dtype=torch.bfloat16)), block_rows=4, table=table)
+    lens = on_gpu(torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="sequences"):
+        kvo.kvo_attend(0, cache, on_gpu(torch.zeros(2, 1, 576, dtype=torch.bfloat16)), lens, 0.1, rows=4)
+    with pytest.raises(ValueError, match="sequences"):
+        kvo.kvo_index_scores(0, cache, on_gpu(torch.zeros(2, 1, 128, dtype=torch.bfloat16)), on_gpu(torch.zeros(2, 1)), lens, 4)

@@ -1192,3 +1192,105 @@ def test_append_negative_frequencies(kvo, ctx, interleaved):
         pair = np.abs(x[0::2]) + np.abs(x[1::2]) if interleaved else np.abs(x[:32]) + np.abs(x[32:])
         pair = np.repeat(pair, 2) if interleaved else np.tile(pair, 2)
         assert (np.abs(O.row_values(out[i])[1] - exact) <= 2.0 ** -8 * np.abs(exact) + 8 * U * pair).all(), p
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lengths", ["uneven", "one long", "none"])
+@pytest.mark.parametrize("sequences,per_seq,heads,n,block,block_rows", [
+    (80, 4, 24, 500, 64, 48), (310, 1, 5, 2_000, 2, 48), (100, 3, 32, 700, 128, 64), (90, 2, 128, 400, 8, 5)])
+def test_scores_tiles_shared_out(kvo, ctx, dtype, lengths, sequences, per_seq, heads, n, block, block_rows):
+    """More than half as many tasks as SMs, few tiles each: several tokens in 128 and 256 columns, blocks beyond a warp."""
+    test_scores_many_sequences(kvo, ctx, dtype, lengths, sequences, per_seq, heads, n, block, block_rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("per_seq,heads,n,block,block_rows", [
+    (1, 16, 170_003, 1, 16), (4, 64, 130_000, 1, 0), (2, 40, 150_001, 16, 5), (1, 64, 260_000, 64, 64)])
+def test_scores_of_long_contexts(kvo, ctx, dtype, per_seq, heads, n, block, block_rows):
+    """One row of the grid a sequence, and many more tiles a CTA than its ring has slots and its accumulators."""
+    rng = np.random.default_rng([56, per_seq, heads, n])
+    br = block_rows or n
+    blocks = -(-n // br)
+    q, k, scales, w = score_inputs(rng, per_seq, heads, blocks * br, dtype)
+    order = rng.permutation(blocks)
+    table = dev(order[None].astype(np.int32)) if block_rows else None
+    lens = np.array([n - 17 * g for g in range(per_seq)])
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=br, table=table)
+    got = f64(ctx.index_scores(cache, q, w, dev(lens, torch.int32), n, block=block))
+    assert ctx.sync() == kvo.KVO_OK
+    at = np.arange(n)
+    rows = order[at // br] * br + at % br if block_rows else at
+    keys, factors = f64(k)[rows], np.ones(n) if scales is None else f64(scales)[rows]
+    for g in range(per_seq):
+        qg, wg = f64(q[g]), f64(w[g])
+        want = factors * (np.maximum(keys @ qg.T, 0.0) @ wg)
+        size = factors * ((np.abs(keys) @ np.abs(qg).T) @ np.abs(wg))
+        want[lens[g]:], size[lens[g]:] = -np.inf, 0.0
+        pad = -n % block
+        want = np.pad(want, (0, pad), constant_values=-np.inf).reshape(-1, block).max(1)
+        size = np.pad(size, (0, pad)).reshape(-1, block).max(1)
+        fin = np.isfinite(want)
+        assert np.array_equal(np.isfinite(got[g]), fin)
+        assert (np.abs(got[g][fin] - want[fin]) <= ((128 + heads + 2) * 2 * U * size)[fin]).all()
+
+
+@pytest.mark.parametrize("dtype,sequences,per_seq,heads,n", [("e4m3", 1, 300, 32, 700), ("bf16", 2, 131, 64, 300),
+                                                             ("e4m3", 3, 65, 7, 200)])
+def test_scores_of_a_prompt(kvo, ctx, dtype, sequences, per_seq, heads, n):
+    """Every token of a prompt sees those up to its own."""
+    rng = np.random.default_rng([57, sequences, per_seq, heads, n])
+    nq, br = sequences * per_seq, 16
+    blocks = -(-n // br)
+    table, total = block_table(rng, sequences, blocks)
+    q, k, scales, w = score_inputs(rng, nq, heads, total * br, dtype)
+    lens = np.tile(n - per_seq + 1 + np.arange(per_seq), sequences)
+    cache = kvo.Cache(keys=k, key_scales=scales, block_rows=br, table=dev(table))
+    got = ctx.index_scores(cache, q, w, dev(lens, torch.int32), n)
+    assert ctx.sync() == kvo.KVO_OK
+    assert np.array_equal(np.isneginf(f64(got)), np.arange(n)[None] >= lens[:, None])
+    some = np.unique(np.concatenate([rng.choice(nq, 40, replace=False), [0, per_seq - 1, nq - 1]]))
+    rows = [[O.row_of(table, total, br, sequences, t // per_seq, p) for p in range(n)] for t in some]
+    check_scores(got[some], q[some], k, scales, w[some], rows, lens[some], n, 1)
+
+
+@pytest.mark.parametrize("sequences,per_seq,heads", [(1, 200, 8), (2, 90, 20), (1, 170, 64)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_attend_of_a_prompt(kvo, ctx, sequences, per_seq, heads, listed):
+    rng = np.random.default_rng([58, sequences, per_seq, heads, int(listed)])
+    n = per_seq + 40
+    lens = np.tile(41 + np.arange(per_seq), sequences)
+    attend_case(kvo, ctx, rng, sequences, per_seq, heads, n, 1, 50 if listed else None, 16, lens=lens)
+
+
+@pytest.mark.parametrize("sequences,heads", [(76, 64), (77, 64), (100, 33), (152, 16), (153, 64), (77, 128)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_attend_batches_about_the_number_of_sms(kvo, ctx, sequences, heads, listed):
+    """Batches on either side of half, of all, and of twice the SMs of this GPU."""
+    rng = np.random.default_rng([59, sequences, heads, int(listed)])
+    attend_case(kvo, ctx, rng, sequences, 1, heads, 260, 1, 150 if listed else None, 16)
+
+
+@pytest.mark.parametrize("dtype,key,interleaved", [("bf16", "e4m3", True), ("fp16", "bf16", False), ("fp32", "e4m3", False)])
+def test_append_prompt_pieces(kvo, ctx, dtype, key, interleaved):
+    """Runs of several sequences' next positions, over many CTAs and a partly filled last one."""
+    rng = np.random.default_rng([60, len(dtype), len(key)])
+    n, sequences, br = 603, 5, 64
+    seqs = np.sort(rng.integers(0, sequences, n)).astype(np.int32)
+    first = np.searchsorted(seqs, np.arange(sequences))
+    pos = (np.arange(n) - first[seqs] + 7 * seqs).astype(np.int32)
+    assert pos.max() < 3 * br
+    r = append_case(kvo, ctx, rng, dtype, n, interleaved, key, br, seqs=seqs, pos=pos, sequences=sequences)
+    assert r["status"] == kvo.KVO_OK
+    # pairs that hold an infinity (fp16 inputs overflow) are compared as what they are, and as zeros from there on
+    for i, j in zip(*np.nonzero(~np.isfinite(r["kv"][:, 512:576]))):
+        at = O.row_of(r["table"], r["blocks"], br, sequences, int(seqs[i]), int(pos[i]))
+        pair = [j // 2 * 2, j // 2 * 2 + 1] if interleaved else [j % 32, j % 32 + 32]
+        with np.errstate(invalid="ignore"):
+            exact = O.rotate(r["kv"][i, 512:576], int(pos[i]), INV_FREQ, interleaved)[pair]
+        bits = r["rows"][at, 528:].view(np.uint16)
+        assert not np.isfinite(exact).any() and np.array_equal(O.row_values(r["rows"][at])[1][pair], exact, equal_nan=True)
+        assert np.array_equal(f64(r["values"])[i, 512:][pair], exact, equal_nan=True)
+        bits[pair] = 0
+        r["values"][i, 512 + np.array(pair)] = 0
+        r["kv"][i, 512 + np.array(pair)] = 0.0
+    check_append(kvo, r, dtype, interleaved, key, br)

@@ -71,13 +71,6 @@ __device__ __forceinline__ void load_floats(const T* p, float* v) {
   }
 }
 
-// The larger value; a NaN if either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // The smallest fp16 s with 127 * s >= amax, at most 65504: the product with
 // 1 / 127 rounded up is at most one step off.  127 * s has 18 significant
 // bits, so the comparisons in fp32 are exact.

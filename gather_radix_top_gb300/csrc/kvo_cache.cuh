@@ -46,6 +46,13 @@ inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, uint32_t thread
   return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
 }
 
+// The larger value; a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Division of n < 2^31 by a fixed d >= 1 as a product: with s = ceil(log2 d)
 // and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n + (n m >> 32)) >> s, and
 // the sum stays below 2^32.

@@ -7,10 +7,10 @@
 // key four values a lane, and nothing needs shared memory or a barrier.
 //
 // What bounds it: 60,000 bf16 tokens with e4m3 keys and the dequantised copy
-// (201 MB) take 39.9 us, 5.0 TB/s, where a copy of the bytes would take 30:
-// about 450 instructions a token fill the schedulers to 60 % while the loads'
-// latency is covered by 40 warps an SM.  16,381 fp32 tokens (78 MB) take 12.4
-// us, 6.3 TB/s.  One token takes 2.3 us, most of it launch.  Measured against
+// (201 MB) take 39.4 us, 5.1 TB/s, where a copy of the bytes would take 30:
+// 481 warp instructions a token fill the schedulers to 64 % while the loads'
+// latency is covered by 35 warps an SM (of 40 that fit).  16,381 fp32 tokens
+// (78 MB) take 12.3 us, 6.3 TB/s.  One token takes 2.4 us, most of it launch.  Measured against
 // it for the 60,000: lookups before the loads 53 us, CTAs of 256 threads 45.6,
 // 64 registers (32 warps an SM) 42.6, half a warp per token (120 registers)
 // 56, a persistent loop that loads one token ahead 46.6.

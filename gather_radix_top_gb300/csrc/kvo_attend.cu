@@ -35,9 +35,9 @@
 // (720), the raw rows (820) and the queries share.  The softmax (about 1,450
 // from scores to weights) and the hand-overs are the rest: with one tile in
 // shared memory nothing else of the tensor cores' work can run beside it.
-//     1,048,576 rows of one query with 128 heads    483 us, 605 TFLOP/s
-//     64 queries of 64 heads and 2,048 positions     50.5 us, 1.9 TB/s
-//     2,048 rows of one query with 64 heads          9.8 us
+//     1,048,576 rows of one query with 128 heads                480 us, 608 TFLOP/s
+//     64 queries of 64 heads, each with 2,048 listed positions   50.6 us, 1.9 TB/s
+//     2,048 rows of one query with 64 heads                      9.8 us
 // Measured on the way, the first of them in us: rows through registers 942
 // (next to this much shared memory the SM keeps about 28 KB of loads in
 // flight), eight worker warps and one loading warp 672, three loading warps
@@ -488,6 +488,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
         for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(fmaf(x[c], a.scale, -sh.column[warp][c]));
       }
+      // The weights go into the second product as bf16, which its values are
+      // (the tensor cores take both operands in one type): half a step is 2^-8
+      // of a weight, and of the result no more than that share of sum p |v|.
+      // The sum of the weights takes them before the rounding, in fp32, so that
+      // the log-sum-exp and the joining of splits lose nothing.
       uint32_t p[kCols / 2];
 #pragma unroll
       for (uint32_t c = 0; c < kCols; c += 2) {
@@ -663,8 +668,9 @@ struct Joined {
 // Up to 32 splits: group g of 128 threads has every kGroups-th one's values
 // from g on, kMost at most.  The weights are formed by every thread for up to
 // 8 splits and by every warp, one a lane, for more, so that nothing waits at a
-// barrier before the sum: 64 queries of 64 heads with 2 splits 48.4 us in all,
-// 49.4 with a barrier, 12 with 12 splits 19.8 and 24.1, one with 32 10.0 and 10.7.
+// barrier before the sum: 64 queries of 64 heads over whole sequences of 2,048
+// rows, 2 splits, 48.4 us in all, 49.4 with a barrier, 12 with 12 splits 19.8
+// and 24.1, one with 32 10.0 and 10.7.
 template <uint32_t kMost, uint32_t kGroups>
 __global__ void __launch_bounds__(128 * kGroups) join_few_kernel(const float* part, const float* part_lse, uint32_t splits,
                                                                  int64_t rows, uint16_t* out, float* lse) {
@@ -784,6 +790,10 @@ struct Cut {
 
 Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   Cut c;
+  // Every query gets the same number of CTAs, from the largest number of
+  // positions: a batch just past half, or past all, of the SMs leaves up to half
+  // of them without work (2,048 listed positions of 64 heads: 76 queries 53.6
+  // us, 77 78.8, 152 86.8, 153 158), and so do uneven lengths.
   // Units of 64 heads by 64 rows: where they do not fill the GPU, fewer heads
   // a CTA leave it less to store and give the rows to more of them.  2,048
   // rows of 64 heads, with 16, 32 and 64 heads a CTA: one query 9.9, 10.2,

@@ -20,8 +20,12 @@
 // 256 as bf16) after about 4 us of launch, queries and first keys: a million
 // keys take 25.4 us as one run of e4m3 (5.5 TB/s), 26.7 in shuffled blocks of
 // 16 and 42.2 as bf16 (6.4 TB/s), whether for 16 or 64 heads.  For 256
-// columns (four tokens of 64 heads), the epilogue's two operations per
-// product: 262,144 keys take 17.9 us against 9.0 for one token.  Slower ones, for
+// columns (four tokens of 64 heads), the epilogue: 262,144 keys take 16.0 us
+// against 8.6 for one token.  Not its two operations per product, though: they
+// are under half of its 5 warp instructions per 32 products, the issue slots are
+// 54 % busy, and a copy without them took 14.7 us where all took 18.5.  The rest
+// is what goes with a tile (both teams of an accumulator look its rows up) and
+// waiting; the two have not been told apart.  Slower ones, for
 // the million in blocks: a barrier of all warps before the first keys instead of
 // one for the queries alone 27.5 us, MMAs from one thread of a diverged warp 30.3
 // (28.4 by then), one loading warp alone 45.2 (it issues a box every 60 clocks),

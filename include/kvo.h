@@ -491,7 +491,11 @@ kvo_status kvo_debug_history_host(kvo_ctx* ctx, int32_t layer, void** out);
  * entries, or past block_rows without a table - that a call has to read is
  * no row: the call treats the position as masked (kvo_append_tokens writes
  * nothing for it) and latches KVO_ERANGE for kvo_sync.  Entries that no
- * visible position needs are not read, so they may hold anything.
+ * visible position needs are not read, so they may hold anything.  A table
+ * of no entries (table_blocks = 0) has no rows; NULL alone says that there is
+ * no table.  KVO_EINVAL for a cache with blocks, block_rows or sequences below
+ * 1, more sequences than blocks without a table, or a table with table_ld <
+ * table_blocks.
  *
  * The calls keep nothing between them.  Every tensor has to be ready on
  * `stream`; calls on several streams may overlap as long as they do not
@@ -555,8 +559,8 @@ typedef struct kvo_cache {
  * A sequence outside [0, sequences), a negative position or a position
  * without a row latches KVO_ERANGE; that token's out_bf16 row is zero.  Two
  * tokens of one call must not name the same position.
- * KVO_EINVAL: n < 0, a NULL or misaligned argument that n > 0 needs, an
- * unknown type, an inv_freq out of range or NaN, cache->rows NULL, or `key` given
+ * KVO_EINVAL: n < 0, a NULL or misaligned argument that n > 0 needs, a
+ * stride below a token's values where n > 1 (0 among them), an unknown type, an inv_freq out of range or NaN, cache->rows NULL, or `key` given
  * without cache->keys (or without key_scales for e4m3).
  */
 typedef struct kvo_tokens {
@@ -640,8 +644,9 @@ kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, const kvo_scor
  * nq = cache->sequences * per_seq, at most KVO_MAX_QUERIES.  KVO_EINVAL for a NULL or misaligned
  * argument, heads outside 1 .. KVO_MAX_HEADS, per_seq < 1, rows < 0 or
  * > 2^31 - 256, picked < 0, picked * sel_block > 2^31 - 256, a sel_block that is not a
- * power of two in 1 .. KVO_MAX_SCORE_BLOCK, a scale that is not finite, too
- * little work space, or a cache without rows.
+ * power of two in 1 .. KVO_MAX_SCORE_BLOCK, sel_ld < picked (0 too: a list that
+ * queries share is given to each), a scale that is not finite, too little work
+ * space, or a cache without rows.
  */
 typedef struct kvo_attend_query {
   const void* q;

@@ -631,8 +631,9 @@ kvo_status kvo_index_scores(kvo_ctx* ctx, const kvo_cache* cache, const kvo_scor
  *              positions at or past lens[t], are masked; a position listed
  *              twice counts twice.  kvo_select_topk(_batch)'s idx is such a
  *              list, over positions or over the blocks of kvo_index_scores.
- * A query that sees no position gets out = 0 and lse = -inf.  A masked
- * row's bytes never reach the output, whatever they hold.
+ * A query that sees no position, or whose z_j are all -inf (infinite rope
+ * values), gets out = 0 and lse = -inf.  A masked row's bytes never reach the
+ * output, whatever they hold.
  *   q       device bf16 [nq][heads][576]; heads q_head_ld elements apart,
  *           queries q_ld; every head 16-byte aligned.
  *   out     device bf16 [nq][heads][512], contiguous, 16-byte aligned.

@@ -1294,3 +1294,26 @@ def test_append_prompt_pieces(kvo, ctx, dtype, key, interleaved):
         r["values"][i, 512 + np.array(pair)] = 0
         r["kv"][i, 512 + np.array(pair)] = 0.0
     check_append(kvo, r, dtype, interleaved, key, br)
+
+
+@pytest.mark.parametrize("heads,n", [(5, 40), (64, 300), (20, 9_000)])
+def test_attend_infinite_logits(kvo, ctx, heads, n):
+    """-inf weighs nothing, and all of them leave an empty query; +inf is a NaN, in its own heads alone."""
+    rng = np.random.default_rng([61, heads, n])
+    rows = random_rows(rng, 3 * n)
+    rope = rows[:, 528:].view(np.uint16)
+    rope[:n, 7] = O.bf16_bits([-math.inf])[0]                       # sequence 0: every row
+    rope[n:2 * n:3, 7] = O.bf16_bits([-math.inf])[0]                # 1: every third
+    rope[2 * n + n // 2, 7] = O.bf16_bits([math.inf])[0]            # 2: one, above
+    q = rng.standard_normal((3, heads, 576))
+    q[:, :, 519] = 1.0
+    q[2, 1::2, 519] = -1.0                                          # -inf there for every other head
+    q = dev(q, torch.bfloat16)
+    cache = kvo.Cache(rows=dev(rows), block_rows=n)
+    out, lse = ctx.attend(cache, q, torch.full((3,), n, dtype=torch.int32, device="cuda"), 192 ** -0.5, rows=n)
+    assert ctx.sync() == kvo.KVO_OK
+    assert not out[0].any() and torch.isneginf(lse[0]).all()
+    left = [[], [rows[n + i] for i in range(n) if i % 3], [rows[2 * n + i] for i in range(n) if i != n // 2]]
+    check_attend(out[1:2], lse[1:2], q[1:2], 192 ** -0.5, left[1:2], heads)
+    assert torch.isnan(out[2, 0::2]).all() and torch.isnan(lse[2, 0::2]).all()
+    check_attend(out[2:, 1::2], lse[2:, 1::2], q[2:, 1::2], 192 ** -0.5, left[2:], heads // 2)

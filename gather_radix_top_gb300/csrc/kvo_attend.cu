@@ -44,12 +44,11 @@
 // 647, references that move seldom and MMAs issued by one elected lane of a
 // converged warp 525 (by a divergent thread 664), two parts instead of five
 // 501, multiply-adds on fp16 operands in the dequantisation 491.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
 #include "kvo_cache.cuh"
+#include "kvo_chunk.cuh"
+#include "kvo_rows.cuh"
 #include "kvo_tc.cuh"
 
 namespace kvo {
@@ -76,7 +75,6 @@ struct AttendShape {
 };
 constexpr float kFar = 64.0f;                            // in powers of two
 constexpr int64_t kLeastRows = 64;                       // of a split
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
   CacheView cache;
@@ -95,6 +93,9 @@ struct AttendArgs {
   uint32_t head_tiles, splits;
   float scale;               // times log2(e)
   int64_t wait_clocks;       // after which a wait gives up
+  const int32_t* starts;     // chunks: first token of every sequence, and the last one's end
+  uint32_t tokens;
+  Divider by_heads;
 };
 
 struct AttendShared {
@@ -106,42 +107,8 @@ struct AttendShared {
   uint32_t far[2][4];                // per quarter of the columns, in i % 2: tile i needs new references
   float top[4][4][16];               // per quarter of the columns and warp
   float column[kWorkerWarps][16];    // per warp: one value per column
+  int32_t seen[64];                  // chunks: per column, the positions it sees
 };
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The fp16 value of a half of `two`, times an fp16, plus an fp32: exact before
-// the one rounding to fp32.
-__device__ __forceinline__ float fma_low(uint32_t two, uint16_t b, float c) {
-  float r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n fma.rn.f32.f16 %0, l, %2, %3;\n}" : "=f"(r) : "r"(two), "h"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float fma_high(uint32_t two, uint16_t b, float c) {
-  float r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n fma.rn.f32.f16 %0, h, %2, %3;\n}" : "=f"(r) : "r"(two), "h"(b), "f"(c));
-  return r;
-}
-
-// Four int8 times a scale as bf16, rounded once.  A byte (plus 128) under the
-// byte 0x64 is the fp16 1024 + byte; times the scale, minus (1024 + 128) *
-// scale (exact: 4 and 11 bits), that is the exact product.
-__device__ __forceinline__ void dequant4(uint32_t bytes, uint16_t scale, float bias, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = bytes ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140u), b = __byte_perm(u, 0x64646464u, 0x4342u);
-  lo = bf16_pair(fma_low(a, scale, bias), fma_high(a, scale, bias));
-  hi = bf16_pair(fma_low(b, scale, bias), fma_high(b, scale, bias));
-}
 
 // One arrival for the whole warp, after all its lanes' accesses.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, uint32_t lane) {
@@ -186,7 +153,10 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
     tmem_ld4(addr, v);
 }
 
-template <uint32_t kHeads>
+// kChunk: the columns are not the heads of one query but (token, head) pairs
+// of a chunk, the heads of a token next to each other, and see unequal numbers
+// of positions, the last column the most of them.
+template <uint32_t kHeads, bool kChunk>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttendShape<kHeads>;
   constexpr uint32_t kRows = S::kRows, kChunkBytes = S::kChunkBytes;
@@ -195,8 +165,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   extern __shared__ uint8_t raw[];
   __shared__ AttendShared sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t t = blockIdx.y, seq = t / a.per_seq;
-  const uint32_t h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
+  const uint32_t t = blockIdx.y;
+  uint32_t seq = t / a.per_seq, h0 = (blockIdx.x % a.head_tiles) * kHeads, split = blockIdx.x / a.head_tiles;
+  int64_t row0 = (int64_t)t * a.heads + h0;              // of out, of column 0
+  uint32_t columns = a.heads > h0 ? a.heads - h0 : 0;    // real ones, of this CTA and those behind it
   const uint32_t tile_at = (smem_u32(raw) + 1023u) & ~1023u, queries = tile_at + S::kTileBytes;
   const uint32_t stage = queries + S::kQueryBytes;
 
@@ -206,7 +178,24 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
   wait_previous_grid();
   allow_next_grid();
-  const int32_t len = a.lens[t];
+  int32_t len, least = 0;                                // chunks: the first column sees `least` positions
+  if constexpr (kChunk) {
+    split = blockIdx.x % a.splits;
+    const ChunkTile tile = chunk_tile(a.starts, a.cache.sequences, a.tokens, a.heads, kHeads, blockIdx.x / a.splits,
+                                      a.status);
+    if (tile.seq < 0) return;
+    seq = (uint32_t)tile.seq;
+    h0 = tile.index * kHeads;
+    columns = tile.tokens * a.heads - h0;
+    row0 = (int64_t)tile.first * a.heads + h0;
+    const int32_t before = min(max(a.lens[seq], 0), INT32_MAX - 1) - (int32_t)tile.tokens + 1;
+    auto sees = [&](uint32_t c) { return min(max(before + (int32_t)divide(h0 + c, a.by_heads), 0), (int32_t)a.rows); };
+    len = sees(min(columns, kHeads) - 1);
+    least = sees(0);
+    if (tid < kHeads) sh.seen[tid] = tid < columns ? sees(tid) : INT32_MAX;   // (zeros see all: they hold nothing up)
+  } else {
+    len = a.lens[t];
+  }
   // this CTA's entries of the list: from `first` on, `count` of them.  (With a
   // list nothing here waits for len: an empty query finds all of it masked.)
   const uint32_t all = a.sel ? a.picked << a.sel_shift : len <= 0 ? 0u : min((uint32_t)len, a.rows);
@@ -221,12 +210,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
   // a worker warp's columns: heads h0 + quarter * kCols + c; its lanes: rows (or
   // values of O^T) quad * 32 + lane
   const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3;
-  const uint32_t head = h0 + quarter * kCols;
-  const uint32_t mine = a.heads > head ? min(kCols, a.heads - head) : 0;   // real columns
+  const uint32_t mine = columns > quarter * kCols ? min(kCols, columns - quarter * kCols) : 0;   // real columns
 
   if (tiles == 0) {
     if (warp >= kWorkerWarps) return;
-    const int64_t out_row = (int64_t)t * a.heads + head;
+    const int64_t out_row = row0 + quarter * kCols;
     if (a.splits > 1) {                                  // the join skips it
       if (quad == 0 && lane < mine) a.part_lse[(int64_t)split * a.nq * a.heads + out_row + lane] = -INFINITY;
       return;
@@ -313,9 +301,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     // the queries: heads past the last are zeros
     for (uint32_t i = tid; i < kHeads * 72; i += kLoadWarp * 32) {
       const uint32_t r = i / 72, c = i - r * 72;
-      const bool real = h0 + r < a.heads;
-      copy16_async(queries + (c >> 3) * (kHeads * 128) + swizzled(r, c & 7),
-                   real ? a.q + t * a.q_ld + (h0 + r) * a.q_head_ld + c * 16 : a.q, real);
+      const bool real = r < columns;
+      const uint8_t* from;
+      if constexpr (kChunk) {
+        const uint32_t token = divide(h0 + r, a.by_heads);
+        from = a.q + (row0 - h0) / a.heads * a.q_ld + token * a.q_ld + (h0 + r - token * a.heads) * a.q_head_ld;
+      } else {
+        from = a.q + t * a.q_ld + (h0 + r) * a.q_head_ld;
+      }
+      copy16_async(queries + (c >> 3) * (kHeads * 128) + swizzled(r, c & 7), real ? from + c * 16 : a.q, real);
     }
     copy_async_commit();
     copy_async_wait<0>();
@@ -361,12 +355,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       const bool there =
           mine_row < rows && (sh.there[turn][mine_row % kLoadWarps] >> (mine_row / kLoadWarps) & 1);
       uint32_t scales[S::kPasses][2];                    // this piece's scale of each part, as fp16 pairs
+      bool bad[S::kPasses];                              // chunks: a row that reads as NaN somewhere
 #pragma unroll
       for (uint32_t u = 0; u < S::kPasses; ++u)
         if (slot + 64 * u < rows) {
           const uint4 eight = lds16(from + u * (64 * kPitch) + KVO_LATENT_BYTES);
           scales[u][0] = __byte_perm(eight.x, eight.y, piece >= 4 ? 0x7632u : 0x5410u);
           scales[u][1] = __byte_perm(eight.z, eight.w, piece >= 4 ? 0x7632u : 0x5410u);
+          // Not all columns may see it, and a weight of 0 would not keep it out
+          // of the second product: its latents become zeros and its position
+          // part NaN, so that its logits are NaN as they would have been, and
+          // with them all of the columns that do see it.
+          if constexpr (kChunk) {
+            bad[u] = any_not_finite(eight);
+            if (bad[u]) scales[u][0] = scales[u][1] = 0;
+          }
         }
 #pragma unroll
       for (uint32_t part = 0; part < 2; ++part) {
@@ -403,7 +406,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (part) {
 #pragma unroll
           for (uint32_t u = 0; u < S::kPasses; ++u)
-            if (slot + 64 * u < rows) sts16(to_rope + u * 8192, rope[u]);
+            if (slot + 64 * u < rows) {
+              if (kChunk && bad[u]) rope[u] = make_uint4(~0u, ~0u, ~0u, ~0u);
+              sts16(to_rope + u * 8192, rope[u]);
+            }
         }
         warp_arrive(&sh.k_full[part], lane);
       }
@@ -416,9 +422,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, x);
       tmem_ld_wait();
       float most = -INFINITY;
+      // chunks: positions that not all columns see (`there` holds for the last one)
+      const uint32_t at = first + i * kRows + mine_row;
+      const bool edge = kChunk && first + i * kRows + rows > (uint32_t)least;
 #pragma unroll
       for (uint32_t c = 0; c < kCols; ++c) {
         x[c] = fmaf(x[c], a.scale, -sh.column[warp][c]);
+        if (edge && at >= (uint32_t)sh.seen[quarter * kCols + c]) x[c] = -INFINITY;
         most = fmaxf(most, x[c]);
       }
       // whether a row of the four warps lies too far above the references: said
@@ -443,7 +453,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
             float m;
-            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(there ? z[e] * a.scale : -INFINITY));
+            const bool visible = there && !(edge && at >= (uint32_t)sh.seen[quarter * kCols + c + e]);
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(visible ? z[e] * a.scale : -INFINITY));
             if (lane == c + e) best = m;
           }
         }
@@ -486,7 +497,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         tmem_ld_cols<kCols>(lanes + kScores + quarter * kCols, x);
         tmem_ld_wait();
 #pragma unroll
-        for (uint32_t c = 0; c < kCols; ++c) x[c] = exp2_approx(fmaf(x[c], a.scale, -sh.column[warp][c]));
+        for (uint32_t c = 0; c < kCols; ++c) {
+          x[c] = exp2_approx(fmaf(x[c], a.scale, -sh.column[warp][c]));
+          if (edge && at >= (uint32_t)sh.seen[quarter * kCols + c]) x[c] = 0.0f;
+        }
       }
       // The weights go into the second product as bf16, which its values are
       // (the tensor cores take both operands in one type): half a step is 2^-8
@@ -517,7 +531,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
       warp_arrive(&sh.p_full, lane);
     }
 
-    const int64_t out_row = (int64_t)t * a.heads + head;
+    const int64_t out_row = row0 + quarter * kCols;
     float* const part = a.part + ((int64_t)split * a.nq * a.heads + out_row) * KVO_LATENT_BYTES;
     lane_sums<kCols, 16>(sum, lane);
     named_sync(1 + quarter, 128);                        // sh.top is free again
@@ -646,6 +660,15 @@ __device__ __forceinline__ float4 partial(const float* part, int64_t row, uint32
   return __ldcg(reinterpret_cast<const float4*>(part + row * KVO_LATENT_BYTES + 4 * at));
 }
 
+// Rows of a chunk call that belong to no sequence are left as they are.
+struct Covered {
+  const int32_t* starts;     // or NULL: all rows
+  uint32_t sequences, heads;
+  __device__ __forceinline__ bool has(int64_t r) const {
+    return !starts || (r >= (int64_t)starts[0] * heads && r < (int64_t)starts[sequences] * heads);
+  }
+};
+
 struct Joined {
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
@@ -673,13 +696,14 @@ struct Joined {
 // and 24.1, one with 32 10.0 and 10.7.
 template <uint32_t kMost, uint32_t kGroups>
 __global__ void __launch_bounds__(128 * kGroups) join_few_kernel(const float* part, const float* part_lse, uint32_t splits,
-                                                                 int64_t rows, uint16_t* out, float* lse) {
+                                                                 int64_t rows, uint16_t* out, float* lse, Covered covered) {
   static_assert(kMost * kGroups <= 32);
   __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][128];
   __shared__ float totals[kGroups];
   const int64_t r = blockIdx.x;
   const uint32_t at = threadIdx.x & 127, group = threadIdx.x >> 7, lane = threadIdx.x & 31;
   wait_previous_grid();
+  if (!covered.has(r)) return;
   float4 v[kMost];
   constexpr bool kEach = kMost * kGroups <= 8;
   float l[kEach ? kMost : 1], top = -INFINITY;             // of split k, or of split `lane`
@@ -729,7 +753,7 @@ __global__ void __launch_bounds__(128 * kGroups) join_few_kernel(const float* pa
 // More: kGroups groups of 128 threads take every kGroups-th split, kAhead at a time.
 template <uint32_t kGroups, uint32_t kAhead>
 __global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, const float* part_lse, uint32_t splits,
-                                                             int64_t rows, uint16_t* out, float* lse) {
+                                                             int64_t rows, uint16_t* out, float* lse, Covered covered) {
   constexpr uint32_t kThreads = 128 * kGroups;
   __shared__ float weight[kMaxSplits];
   __shared__ float red[4 * kGroups];
@@ -737,6 +761,7 @@ __global__ void __launch_bounds__(128 * kGroups) join_kernel(const float* part, 
   const int64_t r = blockIdx.x;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid >> 7, at = tid & 127;
   wait_previous_grid();
+  if (!covered.has(r)) return;
   float4 v[kAhead];
   auto load = [&](uint32_t from) {
 #pragma unroll
@@ -812,19 +837,50 @@ Cut cut_of(int64_t nq, uint32_t heads, int64_t positions) {
   return c;
 }
 
-template <uint32_t kHeads>
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
+// A chunk call: its columns are cut as one query's heads are.  The splits come
+// from as many tiles as there are when every sequence has the same tokens.
+Cut chunk_cut_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
+  Cut c = cut_of(1, (uint32_t)(tokens > 0 ? tokens * heads : 1), rows);
+  const int64_t busy = sequences < tokens ? sequences : tokens;
+  const int64_t ctas = c.head_tiles > busy ? c.head_tiles : busy, sms = device_sms();
+  const int64_t most = (rows + kLeastRows - 1) / kLeastRows;
+  int64_t splits = ctas >= sms ? 1 : sms / (ctas < 1 ? 1 : ctas);
+  if (splits > most) splits = most;
+  c.splits = (uint32_t)(splits < 1 ? 1 : splits);
+  return c;
+}
+
+template <uint32_t kHeads, bool kChunk>
+cudaError_t launch_attend(const AttendArgs& a, dim3 grid, cudaStream_t stream) {
   constexpr size_t smem = AttendShape<kHeads>::kSmem;
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(attend_kernel<kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(attend_kernel<kHeads, kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
-  return launch_early(attend_kernel<kHeads>, dim3(a.head_tiles * a.splits, a.nq), kAttendThreads, smem, stream, a);
+  return launch_early(attend_kernel<kHeads, kChunk>, grid, kAttendThreads, smem, stream, a);
+}
+
+// The splits' results of `rows` outputs joined.
+cudaError_t launch_join(const AttendArgs& a, int64_t rows, const Covered& covered, cudaStream_t stream) {
+  // Past 32 splits, 1,024 threads for as many outputs as SMs and 512 for more.
+  // 64 heads, us: one query of 8,192 rows 15.6 and 17.9, of 65,536 29.5 and
+  // 33.6, four of 8,192 22.7 and 21.4.
+  const bool wide = rows <= device_sms();
+  const auto join = a.splits <= 2    ? join_few_kernel<2, 1>
+                    : a.splits <= 4  ? join_few_kernel<4, 1>
+                    : a.splits <= 8  ? join_few_kernel<8, 1>
+                    : a.splits <= 16 ? join_few_kernel<16, 1>
+                    : a.splits <= 32 ? join_few_kernel<16, 2>
+                    : wide           ? join_kernel<8, 4>
+                                     : join_kernel<4, 8>;
+  const uint32_t threads = a.splits <= 16 ? 128 : a.splits <= 32 ? 256 : wide ? 1024 : 512;
+  return launch_early(join, dim3((unsigned)rows), threads, 0, stream, a.part, a.part_lse, a.splits, rows, a.out, a.lse,
+                      covered);
 }
 
 }  // namespace
@@ -880,24 +936,68 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
   a.part = static_cast<float*>(s->work);
   a.part_lse = a.part + (int64_t)a.splits * nq * a.heads * KVO_LATENT_BYTES;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cut.heads == 16   ? launch_attend<16>(a, on)
-                  : cut.heads == 32 ? launch_attend<32>(a, on)
-                                    : launch_attend<64>(a, on);
-  if (e == cudaSuccess && a.splits > 1) {
-    // Past 32 splits, 1,024 threads for as many outputs as SMs and 512 for more.
-    // 64 heads, us: one query of 8,192 rows 15.6 and 17.9, of 65,536 29.5 and
-    // 33.6, four of 8,192 22.7 and 21.4.
-    const int64_t joins = nq * a.heads;
-    const bool wide = joins <= device_sms();
-    const auto join = a.splits <= 2    ? join_few_kernel<2, 1>
-                      : a.splits <= 4  ? join_few_kernel<4, 1>
-                      : a.splits <= 8  ? join_few_kernel<8, 1>
-                      : a.splits <= 16 ? join_few_kernel<16, 1>
-                      : a.splits <= 32 ? join_few_kernel<16, 2>
-                      : wide           ? join_kernel<8, 4>
-                                       : join_kernel<4, 8>;
-    const uint32_t threads = a.splits <= 16 ? 128 : a.splits <= 32 ? 256 : wide ? 1024 : 512;
-    e = launch_early(join, dim3((unsigned)joins), threads, 0, on, a.part, a.part_lse, a.splits, joins, a.out, a.lse);
+  const dim3 grid(a.head_tiles * a.splits, a.nq);
+  cudaError_t e = cut.heads == 16   ? launch_attend<16, false>(a, grid, on)
+                  : cut.heads == 32 ? launch_attend<32, false>(a, grid, on)
+                                    : launch_attend<64, false>(a, grid, on);
+  if (e == cudaSuccess && a.splits > 1) e = launch_join(a, nq * a.heads, Covered{}, on);
+  return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
+}
+
+extern "C" int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows) {
+  if (tokens < 0 || tokens > KVO_MAX_QUERIES || sequences < 1 || sequences > KVO_MAX_QUERIES) return -1;
+  if (heads < 1 || heads > KVO_MAX_HEADS || rows < 0 || rows > INT32_MAX - 255) return -1;
+  const kvo::Cut c = kvo::chunk_cut_of(tokens, sequences, (uint32_t)heads, rows);
+  return c.splits == 1 ? 0 : (int64_t)c.splits * tokens * heads * (KVO_LATENT_BYTES + 1) * 4;
+}
+
+extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, const kvo_chunk_query* s, void* stream) {
+  using namespace kvo;
+  uint32_t* status = nullptr;
+  if (!ctx || !cache_ok(cache) || !s || !cache_rows_ok(cache)) return KVO_EINVAL;
+  const int64_t need = kvo_attend_chunk_work_bytes(s->tokens, cache->sequences, s->heads, s->rows);
+  if (need < 0 || !s->starts || !s->lens || !std::isfinite(s->scale)) return KVO_EINVAL;
+  if (!aligned(s->starts, 4) || !aligned(s->lens, 4)) return KVO_EINVAL;
+  if (s->tokens > 0) {
+    if (!s->q || !s->out || s->work_bytes < need || (need && !s->work)) return KVO_EINVAL;
+    if (!aligned(s->q, 16) || s->q_ld % 8 || s->q_head_ld % 8 || !aligned(s->out, 16)) return KVO_EINVAL;
+    if (!aligned(s->lse, 4) || !aligned(s->work, 16)) return KVO_EINVAL;
   }
+  int64_t wait_clocks = 0;
+  const kvo_status st = usable_status(ctx, &status, &wait_clocks);
+  if (st != KVO_OK) return st;
+  if (s->tokens == 0) return KVO_OK;
+
+  AttendArgs a = {};
+  a.wait_clocks = wait_clocks;
+  a.cache = cache_view(*cache);
+  a.q = static_cast<const uint8_t*>(s->q);
+  a.lens = s->lens;
+  a.starts = s->starts;
+  a.tokens = (uint32_t)s->tokens;
+  a.out = s->out;
+  a.lse = s->lse;
+  a.status = status;
+  a.q_ld = s->q_ld * 2;
+  a.q_head_ld = s->q_head_ld * 2;
+  a.rows = (uint32_t)s->rows;
+  a.per_seq = 1;
+  a.heads = (uint32_t)s->heads;
+  a.by_heads = divider(a.heads);
+  a.scale = s->scale * kLog2e;
+  const Cut cut = chunk_cut_of(s->tokens, cache->sequences, a.heads, s->rows);
+  const int64_t columns = s->tokens * a.heads;
+  a.nq = a.tokens;
+  a.head_tiles = cut.head_tiles;
+  a.splits = cut.splits;
+  a.part = static_cast<float*>(s->work);
+  a.part_lse = a.part + (int64_t)a.splits * columns * KVO_LATENT_BYTES;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  const dim3 grid(chunk_tiles(s->tokens, cache->sequences, a.heads, cut.heads) * a.splits);
+  cudaError_t e = cut.heads == 16   ? launch_attend<16, true>(a, grid, on)
+                  : cut.heads == 32 ? launch_attend<32, true>(a, grid, on)
+                                    : launch_attend<64, true>(a, grid, on);
+  if (e == cudaSuccess && a.splits > 1)
+    e = launch_join(a, columns, Covered{a.starts, a.cache.sequences, a.heads}, on);
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -125,6 +125,87 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, const float* v) {
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// ---- Two CTAs of a cluster (ranks 0 and 1) on one matrix product.  Rank 0
+// issues the MMAs; operands and accumulators are at the same addresses in both.
+// M is 256: a CTA holds 128 rows of A and of D (all N columns of them, in its
+// tensor memory), and N / 2 rows of B.
+
+__host__ __device__ constexpr uint32_t pair_desc(uint32_t operand, uint32_t n, bool a_mn_major, bool b_mn_major) {
+  return (mma_desc(operand, n, a_mn_major, b_mn_major) & ~(31u << 24)) | (256u >> 4) << 24;
+}
+
+__device__ __forceinline__ void pair_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// The barrier at this address in the CTAs of `mask` (bit r: rank r) gets one
+// arrival once every pair MMA this thread has issued is complete.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+
+// One warp of each CTA, at the same time.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+
+// An arrival at a barrier of another CTA of the cluster (or this one), given
+// its cluster address: after this thread's accesses to shared memory anywhere
+// in the cluster.
+__device__ __forceinline__ void cluster_mbar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// As wait_or_give_up, for a phase that threads of the other CTA complete.
+__device__ __forceinline__ bool cluster_wait_or_give_up(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up,
+                                                        long long clocks) {
+  const uint32_t a = smem_u32(bar);
+  uint32_t done;
+  long long start = 0;
+  for (uint32_t i = 0;; ++i) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 15u) == 15u) {
+      if (*gave_up) return false;
+      const long long now = clock64();
+      if (start == 0) start = now;
+      if (now - start > clocks) {
+        *gave_up = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// A box of a three-dimensional tensor map to this CTA's shared memory at
+// `dst`; completes on the barrier at cluster address `bar`, of either CTA.
+__device__ __forceinline__ void pair_load_box(uint32_t dst, const void* map, int32_t x, int32_t y, int32_t z,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }

@@ -46,7 +46,8 @@ EXPORTED = [
     "kvo_pool_debug_free_queue", "kvo_copy_blocks_noalloc", "kvo_set_phase_timing", "kvo_layers_phase_times",
     "kvo_layers_counters", "kvo_probe_host_touch", "kvo_debug_history_host", "kvo_set_miss_fetch",
     "kvo_touch_history", "kvo_append_tokens", "kvo_index_scores", "kvo_attend", "kvo_attend_work_bytes",
-    "kvo_pool_rows", "kvo_debug_set_wait_clocks",
+    "kvo_pool_rows", "kvo_debug_set_wait_clocks", "kvo_attend_chunk", "kvo_attend_chunk_work_bytes",
+    "kvo_shrink_cache", "kvo_attention_weights", "kvo_attention_weights_work_bytes",
 ]
 
 
@@ -100,6 +101,31 @@ class kvo_attend_query(ctypes.Structure):
                 ("sel_ld", ctypes.c_int64), ("rows", ctypes.c_int64), ("picked", ctypes.c_int64),
                 ("sel_block", ctypes.c_int32), ("per_seq", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class kvo_chunk_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("work", ctypes.c_void_p),
+                ("work_bytes", ctypes.c_int64), ("q_ld", ctypes.c_int64), ("q_head_ld", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class kvo_weight_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("carry", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_int64), ("q_ld", ctypes.c_int64),
+                ("q_head_ld", ctypes.c_int64), ("carry_ld", ctypes.c_int64), ("out_ld", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("scale", ctypes.c_float), ("keep", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class kvo_shrink(ctypes.Structure):
+    _fields_ = [("weights", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("to_weights", ctypes.c_void_p), ("weights_ld", ctypes.c_int64),
+                ("kept_ld", ctypes.c_int64), ("to_weights_ld", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("budget", ctypes.c_int64), ("first", ctypes.c_int32), ("last", ctypes.c_int32)]
 
 
 class kvo_pool_stats(ctypes.Structure):
@@ -182,6 +208,11 @@ def lib() -> ctypes.CDLL:
         "kvo_index_scores": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
         "kvo_attend": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
         "kvo_attend_work_bytes": (_i64, [_i64, _i32, _i64]),
+        "kvo_attend_chunk": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+        "kvo_attend_chunk_work_bytes": (_i64, [_i64, _i32, _i32, _i64]),
+        "kvo_attention_weights": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+        "kvo_attention_weights_work_bytes": (_i64, [_i64, _i32, _i32, _i64, _i64]),
+        "kvo_shrink_cache": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp]),
         "kvo_pool_rows": (ctypes.c_int, [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_i64), ctypes.POINTER(_i32)]),
     }
     for name, (res, args) in sig.items():
@@ -737,6 +768,110 @@ def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None =
     return out, lse
 
 
+def _tokens(cache: Cache, q, starts, lens) -> tuple:
+    """(address, tokens, heads, strides of token and head, starts, lens) of a chunk's q [tokens, heads, 576]."""
+    if q.dim() != 3 or q.shape[2] != DEQUANT_VALUES:
+        raise ValueError(f"q must be [tokens, heads, {DEQUANT_VALUES}]")
+    T = _T()
+    tokens, heads, _ = shape = q.shape
+    ptr = _cuda(q, "q", T.bfloat16, shape)
+    q_ld, head_ld, _ = q.stride()
+    # a dimension of one has no next element: its stride says nothing
+    return (ptr, tokens, heads, q_ld if tokens > 1 else heads * DEQUANT_VALUES, head_ld if heads > 1 else DEQUANT_VALUES,
+            _flat(starts, "starts", T.int32, (cache.sequences + 1,)), _flat(lens, "lens", T.int32, (cache.sequences,)))
+
+
+def _work(work, need: int, device, stream) -> tuple:
+    """(tensor, address, bytes) of the caller's scratch, or of some that holds `need` bytes."""
+    if need <= 0:
+        return work, None, 0
+    if work is None:
+        work = _empty(need, _T().uint8, device, stream)
+    elif work.dtype is not _T().uint8 or not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work must be a contiguous uint8 CUDA tensor")
+    return work, work.data_ptr(), work.numel()
+
+
+def kvo_attend_chunk_work_bytes(tokens: int, sequences: int, heads: int, rows: int) -> int:
+    return int(lib().kvo_attend_chunk_work_bytes(tokens, sequences, heads, rows))
+
+
+def kvo_attend_chunk(ctx: int, cache: Cache, q, starts, lens, scale: float, rows: int, out=None, lse=None, work=None,
+                     stream=None):
+    """q: bfloat16 CUDA [tokens, heads, 576], the new tokens of all sequences;
+    starts: int32 [sequences + 1]; lens: int32 [sequences]; rows: the largest
+    lens value.  Returns (out bfloat16 [tokens, heads, 512], lse float32
+    [tokens, heads])."""
+    T = _T()
+    q_ptr, tokens, heads, q_ld, q_head_ld, starts_ptr, lens_ptr = _tokens(cache, q, starts, lens)
+    if out is None:
+        out = _empty((tokens, heads, LATENT_VALUES), T.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _empty((tokens, heads), T.float32, q.device, stream)
+    L = lib()
+    work, work_ptr, size = _work(work, L.kvo_attend_chunk_work_bytes(tokens, cache.sequences, heads, rows), q.device, stream)
+    s = kvo_chunk_query(q_ptr, starts_ptr, lens_ptr, _flat(out, "out", T.bfloat16, (tokens, heads, LATENT_VALUES)),
+                        _flat(lse, "lse", T.float32, (tokens, heads)), work_ptr, size, q_ld, q_head_ld, tokens, rows, heads,
+                        scale)
+    _check(L.kvo_attend_chunk(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)), "kvo_attend_chunk")
+    return out, lse
+
+
+def kvo_attention_weights_work_bytes(tokens: int, sequences: int, heads: int, rows: int, window: int = 0) -> int:
+    return int(lib().kvo_attention_weights_work_bytes(tokens, sequences, heads, rows, window))
+
+
+def kvo_attention_weights(ctx: int, cache: Cache, q, starts, lens, lse, scale: float, rows: int, window: int = 0,
+                          carry=None, keep: float = 1.0, out=None, work=None, stream=None):
+    """q, starts, lens, scale and rows as for kvo_attend_chunk; lse: float32
+    CUDA [tokens, heads]; window: the last tokens of each sequence that count
+    (0: all); carry: float32 [sequences, rows] (rows may be strided).  Returns
+    float32 [sequences, rows] (`out` if given; it may be carry)."""
+    T = _T()
+    q_ptr, tokens, heads, q_ld, q_head_ld, starts_ptr, lens_ptr = _tokens(cache, q, starts, lens)
+    n = cache.sequences
+    if out is None:
+        out = _empty((n, rows), T.float32, q.device, stream)
+    carry_ptr, carry_ld = None, 0
+    if carry is not None:
+        carry_ptr, carry_ld = _cuda(carry, "carry", T.float32, (n, rows)), carry.stride(0) if n > 1 else rows
+    L = lib()
+    work, work_ptr, size = _work(work, L.kvo_attention_weights_work_bytes(tokens, n, heads, rows, window), q.device, stream)
+    s = kvo_weight_query(q_ptr, starts_ptr, lens_ptr, _flat(lse, "lse", T.float32, (tokens, heads)), carry_ptr,
+                         _cuda(out, "out", T.float32, (n, rows)), work_ptr, size, q_ld, q_head_ld, carry_ld,
+                         out.stride(0) if n > 1 else rows, tokens, rows, window, heads, scale, keep)
+    _check(L.kvo_attention_weights(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)),
+           "kvo_attention_weights")
+    return out
+
+
+def kvo_shrink_cache(ctx: int, cache: Cache, to: Cache, weights, lens, budget: int, first: int = 0, last: int = 0,
+                     kept=None, new_lens=None, to_weights=None, stream=None):
+    """weights: float32 CUDA [sequences, positions]; lens: int32 [sequences].
+    Copies what stays of `cache` to `to`.  Returns (kept int32 [sequences,
+    budget], new_lens int32 [sequences], to_weights float32 [sequences,
+    budget])."""
+    T = _T()
+    n, device = cache.sequences, weights.device
+    if weights.dim() != 2:
+        raise ValueError("weights must be [sequences, positions]")
+    rows = weights.shape[1]
+    w_ptr = _cuda(weights, "weights", T.float32, (n, rows))
+    if kept is None:
+        kept = _empty((n, budget), T.int32, device, stream)
+    if new_lens is None:
+        new_lens = _empty((n,), T.int32, device, stream)
+    if to_weights is None:
+        to_weights = _empty((n, budget), T.float32, device, stream)
+    s = kvo_shrink(w_ptr, _flat(lens, "lens", T.int32, (n,)), _cuda(kept, "kept", T.int32, (n, budget)),
+                   _flat(new_lens, "new_lens", T.int32, (n,)), _cuda(to_weights, "to_weights", T.float32, (n, budget)),
+                   weights.stride(0) if n > 1 else rows, kept.stride(0) if n > 1 else budget,
+                   to_weights.stride(0) if n > 1 else budget, rows, budget, first, last)
+    _check(lib().kvo_shrink_cache(ctx, cache.ref, to.ref, ctypes.addressof(s), _raw_stream(T, device, stream)),
+           "kvo_shrink_cache")
+    return kept, new_lens, to_weights
+
+
 class Context:
     """Owns one kvo context; methods forward to the kvo_* calls above."""
 
@@ -824,6 +959,19 @@ class Context:
     def attend(self, cache, q, lens, scale, rows=None, sel=None, sel_block=1, out=None, lse=None, work=None,
                stream=None):
         return kvo_attend(self.handle, cache, q, lens, scale, rows, sel, sel_block, out, lse, work, stream)
+
+    def attend_chunk(self, cache, q, starts, lens, scale, rows, out=None, lse=None, work=None, stream=None):
+        return kvo_attend_chunk(self.handle, cache, q, starts, lens, scale, rows, out, lse, work, stream)
+
+    def attention_weights(self, cache, q, starts, lens, lse, scale, rows, window=0, carry=None, keep=1.0, out=None,
+                          work=None, stream=None):
+        return kvo_attention_weights(self.handle, cache, q, starts, lens, lse, scale, rows, window, carry, keep, out,
+                                     work, stream)
+
+    def shrink_cache(self, cache, to, weights, lens, budget, first=0, last=0, kept=None, new_lens=None,
+                     to_weights=None, stream=None):
+        return kvo_shrink_cache(self.handle, cache, to, weights, lens, budget, first, last, kept, new_lens, to_weights,
+                                stream)
 
     def sync(self, stream=None) -> int:
         return kvo_sync(self.handle, stream)

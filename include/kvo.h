@@ -675,6 +675,161 @@ kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo_attend_que
 int64_t kvo_attend_work_bytes(int64_t nq, int32_t heads, int64_t positions);
 
 /* ------------------------------------------------------------------------
+ * Prompt chunks over a cache, and caches shrunk by what attention looked at.
+ *
+ * The new tokens of all the cache's sequences lie one after the other:
+ * sequence s's are tokens [starts[s], starts[s + 1]), and their rows are
+ * already the last ones of lens[s] positions (kvo_append_tokens wrote them).
+ * Token i of a sequence's n therefore sees its first lens[s] - n + 1 + i
+ * positions: everything before the chunk, the chunk's earlier tokens, itself.
+ *   starts  device int32[sequences + 1], never decreasing, within [0, tokens].
+ *           Others latch KVO_ERANGE (and leave unspecified what the calls
+ *           below write, within their outputs' bounds).
+ *   lens    device int32[sequences], the positions each sequence holds.  With
+ *           fewer than its tokens, the first tokens see none.
+ *   rows    the largest lens value: positions at or past it are not looked at.
+ * Tokens that belong to no sequence (before starts[0], or at and past the last
+ * entry) are not looked at, and their outputs are left as they are.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * kvo_attend_chunk - kvo_attend for such tokens: every (token, head) attends
+ * to the positions its token sees, with the same formulas and numerics; one
+ * that sees none gets out = 0 and lse = -inf.
+ *   q       device bf16 [tokens][heads][576]; heads q_head_ld elements apart,
+ *           tokens q_ld; every head 16-byte aligned.
+ *   out     device bf16 [tokens][heads][512], contiguous, 16-byte aligned.
+ *   lse     device fp32 [tokens][heads], or NULL.
+ *   work    device scratch of kvo_attend_chunk_work_bytes' size (16-byte
+ *           aligned), or NULL when that is 0; free again once the call's work
+ *           is done.
+ * KVO_EINVAL for a NULL or misaligned argument that tokens > 0 needs, tokens
+ * or sequences above KVO_MAX_QUERIES, heads outside 1 .. KVO_MAX_HEADS, rows
+ * < 0 or > 2^31 - 256, a scale that is not finite, too little work space, or
+ * a cache without rows.
+ */
+typedef struct kvo_chunk_query {
+  const void* q;
+  const int32_t* starts;
+  const int32_t* lens;
+  uint16_t* out;
+  float* lse;
+  void* work;
+  int64_t work_bytes;
+  int64_t q_ld;
+  int64_t q_head_ld;
+  int64_t tokens;
+  int64_t rows;
+  int32_t heads;
+  float scale;
+} kvo_chunk_query;
+kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, const kvo_chunk_query* query, void* stream);
+
+/* kvo_attend_chunk_work_bytes - the scratch bytes a kvo_attend_chunk of
+ * `tokens` tokens in all needs on the current device; -1 for arguments it
+ * would refuse. */
+int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows);
+
+/*
+ * kvo_attention_weights - the attention weight that every cached position
+ * receives from such tokens, all heads together: for p < lens[s]
+ *     out[s][p] = keep * carry[s][p] + sum_t sum_h exp(z_thp - lse[t][h])
+ * over the last `window` tokens t of sequence s (0: all of them) that see p,
+ * with kvo_attend's logits z; and 0 for lens[s] <= p < rows.  With the lse of
+ * kvo_attend_chunk (or kvo_attend) these are the softmax weights.  A (token,
+ * head) whose lse is -inf adds nothing, nor does a position without a row (it
+ * latches KVO_ERANGE); carry counts all the same.
+ *   q       device bf16 [tokens][heads][576], as for kvo_attend_chunk; where
+ *           there are several, heads are at least 576 and below 2^38 elements
+ *           apart, and so are tokens.
+ *   lse     device fp32 [tokens][heads].
+ *   carry   device fp32, sequence s's at carry + s * carry_ld, or NULL (0).
+ *   out     device fp32, sequence s's `rows` values at out + s * out_ld; may
+ *           be carry, with the same stride.
+ *   work    device scratch of kvo_attention_weights_work_bytes' size (4-byte
+ *           aligned), or NULL when that is 0; free again once the call's work
+ *           is done.
+ * Sums are held in fp32, in an order that does not change from call to call.
+ * KVO_EINVAL for a NULL or misaligned argument that tokens > 0 or rows > 0
+ * need, tokens or sequences above KVO_MAX_QUERIES, heads outside 1 ..
+ * KVO_MAX_HEADS, rows < 0 or > 2^31 - 256, window < 0, a scale or keep that is
+ * not finite, a bad stride, too little work space, or a cache without rows.
+ */
+typedef struct kvo_weight_query {
+  const void* q;
+  const int32_t* starts;
+  const int32_t* lens;
+  const float* lse;
+  const float* carry;
+  float* out;
+  void* work;
+  int64_t work_bytes;
+  int64_t q_ld;
+  int64_t q_head_ld;
+  int64_t carry_ld;
+  int64_t out_ld;
+  int64_t tokens;
+  int64_t rows;
+  int64_t window;
+  int32_t heads;
+  float scale;
+  float keep;
+  int32_t reserved;
+} kvo_weight_query;
+kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache, const kvo_weight_query* query, void* stream);
+
+/* kvo_attention_weights_work_bytes - the scratch bytes a kvo_attention_weights
+ * of `tokens` tokens in all needs on the current device; -1 for arguments it
+ * would refuse. */
+int64_t kvo_attention_weights_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows, int64_t window);
+
+/*
+ * kvo_shrink_cache - evict the least attended positions: of every sequence s
+ * at most `budget` positions stay - the first `first`, the last `last`, and of
+ * the others those with the largest weights (of equal ones the lower
+ * position, a NaN below every number) - and are copied, in their order, to
+ * positions 0, 1, .. of sequence s of the cache `to`, each with its row and,
+ * if `to` has keys, its key and factor.  A sequence of at most `budget`
+ * positions is copied whole.  Rows hold their position's rotation, so
+ * attention over the copy needs nothing else; later tokens keep counting
+ * their positions for kvo_append_tokens' rotation from the original ones.
+ *   weights     device fp32, sequence s's at weights + s * weights_ld:
+ *               kvo_attention_weights' output, or any other measure.
+ *   lens        device int32[sequences], at most `rows` of them counted.
+ *   kept        device int32, sequence s's at kept + s * kept_ld: `budget`
+ *               entries, the positions that stayed, ascending, then -1.
+ *   new_lens    device int32[sequences]: how many stayed.
+ *   to_weights  device fp32 like kept, the weights of those that stayed, then
+ *               0; or NULL.
+ * The outputs must not overlap the inputs, nor the blocks that `to` names
+ * those that `from` names (a cache cannot be shrunk in place; both may lie in
+ * one pool).  Source blocks may be shared between sequences, destination
+ * blocks may not.  Positions without a source row become zeros, those without
+ * a destination are dropped, and both latch KVO_ERANGE.
+ * KVO_EINVAL for a NULL or misaligned argument, caches with different numbers
+ * of sequences (or more than KVO_MAX_QUERIES), the same rows and table, `to`
+ * with keys that `from` lacks or has in another type, rows or budget outside
+ * 1 .. 2^31 - 256, first or last below 0 or together above budget, or, with
+ * more than one sequence, a stride below its row.
+ */
+typedef struct kvo_shrink {
+  const float* weights;
+  const int32_t* lens;
+  int32_t* kept;
+  int32_t* new_lens;
+  float* to_weights;
+  int64_t weights_ld;
+  int64_t kept_ld;
+  int64_t to_weights_ld;
+  int64_t rows;
+  int64_t budget;
+  int32_t first;
+  int32_t last;
+} kvo_shrink;
+kvo_status kvo_shrink_cache(kvo_ctx* ctx, const kvo_cache* from, const kvo_cache* to, const kvo_shrink* shrink,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
  * Session block store/restore.
  *
  * Sources (page title, section):

@@ -1,0 +1,689 @@
+"""kvo_attend_chunk, kvo_attention_weights and kvo_shrink_cache against the 64-bit oracle.
+
+Tolerances, from the number formats alone (u = 2^-24, half a step of fp32; 2^-8, half a step of bf16):
+  lse      the logits' error (576 steps of 2 u of the magnitudes: an accumulator may truncate), the exponentials and the
+           logarithm 16 u, a blocked sum 2 u for each of n / 128 + 32 steps, and 2 u of its size;
+  out      2^-8 |out| for its rounding, and for the sum of p |v| the weights' rounding 2^-8, twice the logits' error and
+           the steps of the sum as above.
+           A weight below 2^-126 of the largest is 0 in fp32, and takes at most 2^-126 |v| with it: 2^-112 for 2^13
+           positions of latents below 2;
+  weights  every term p = exp(z - lse) off by p times the error of its logit, 4 u of |lse| (its product with log2 e and
+           the difference, each rounded) and 16 u for the exponential; the sum of a tile's 128 terms and the carried
+           tiles 64 u of its size; and 2 u of keep * carry.
+What is chosen and copied has to be equal.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kvo_chunk_oracle as C
+from oracle import kvo_sparse_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SCALE = 192 ** -0.5
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from gather_radix_top_gb300 import build, kvo
+    build.build()
+    c = kvo.Context(1, 64, 64)
+    yield c
+    c.close()
+
+
+@pytest.fixture(scope="module")
+def kvo():
+    from gather_radix_top_gb300 import kvo as K
+    return K
+
+
+def dev(x, dtype=None):
+    t = torch.as_tensor(x)
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def block_table(rng, sequences, blocks, spare=2):
+    total = sequences * blocks + spare
+    return rng.permutation(total)[:sequences * blocks].reshape(sequences, blocks).astype(np.int32), total
+
+
+def random_rows(rng, n, scale=(1e-3, 1e-2)):
+    rows = rng.integers(0, 256, (n, 656), dtype=np.uint8)
+    rows[:, :512][rows[:, :512] == 128] = 0
+    rows[:, 512:528] = rng.uniform(*scale, (n, 8)).astype(np.float16).view(np.uint8)
+    rows[:, 528:] = np.ascontiguousarray(O.bf16_bits(rng.standard_normal((n, 64)))).view(np.uint8)
+    return rows
+
+
+class Chunk:
+    """Queries of a ragged batch over a paged cache, and what the calls on them have to give."""
+
+    def __init__(self, kvo, rng, counts, lens, heads, block_rows=16, rows=None, scale=SCALE, gain=1.0, q=None, raw=None,
+                 table=None, first=0, after=0):
+        self.kvo, self.counts, self.lens, self.heads, self.scale = kvo, counts, list(lens), heads, scale
+        self.n, self.rows = len(counts), max(max(lens), 0) if rows is None else rows
+        self.starts = first + np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        self.tokens = int(self.starts[-1]) + after
+        br = self.br = block_rows or max(self.rows, 1)
+        if block_rows:
+            self.table, self.total = block_table(rng, self.n, max(1, -(-self.rows // br)))
+        else:
+            self.table, self.total = None, self.n
+        if table is not None:
+            self.table, self.total = table
+        self.raw = random_rows(rng, self.total * br) if raw is None else raw
+        self.q = dev(rng.standard_normal((self.tokens, heads, 576)) * gain, torch.bfloat16) if q is None else q
+        self.cache = kvo.Cache(rows=dev(self.raw), block_rows=br, table=None if self.table is None else dev(self.table),
+                               sequences=self.n if self.table is None else None)
+        self.dev_starts, self.dev_lens = dev(self.starts), dev(self.lens, torch.int32)
+
+    def keys(self, s, n):
+        """Values of the sequence's first n positions that have a row, and their positions."""
+        at = [O.row_of(self.table, self.total, self.br, self.n, s, p) for p in range(n)]
+        have = [p for p, r in enumerate(at) if r is not None]
+        return C.values([self.raw[at[p]] for p in have]), np.array(have, int)
+
+    def attend(self, ctx, **kw):
+        return ctx.attend_chunk(self.cache, self.q, self.dev_starts, self.dev_lens, self.scale, self.rows, **kw)
+
+    def check_attend(self, out, lse):
+        out, lse, q = f64(out), f64(lse), f64(self.q)
+        for s in range(self.n):
+            keys, have = self.keys(s, min(max(self.lens[s], 0), self.rows))
+            for t in C.tokens_of(self.starts, s):
+                n = int((have < C.seen(self.starts, self.lens, s, t, self.rows)).sum())
+                want, want_lse, spread, size = C.attend(q[t], self.scale, keys[:n])
+                if n == 0:
+                    assert not out[t].any() and np.isneginf(lse[t]).all(), (s, t)
+                    continue
+                steps, logit = n / 128 + 32, 2 * U * 576 * size
+                tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 2 * logit + 16 * U + 2 * U * steps)[:, None]
+                tol += 2.0 ** -112
+                assert (np.abs(out[t] - want) <= tol).all(), (s, t, float((np.abs(out[t] - want) / tol).max()))
+                tol = logit + 16 * U + 2 * U * steps + 2 * U * np.abs(want_lse)
+                assert (np.abs(lse[t] - want_lse) <= tol).all(), (s, t, float((np.abs(lse[t] - want_lse) / tol).max()))
+
+    def lse(self):
+        """The log-sum-exps as attention returns them."""
+        q, out = f64(self.q), np.full((self.tokens, self.heads), -np.inf)
+        for s in range(self.n):
+            keys, have = self.keys(s, min(max(self.lens[s], 0), self.rows))
+            for t in C.tokens_of(self.starts, s):
+                n = int((have < C.seen(self.starts, self.lens, s, t, self.rows)).sum())
+                out[t] = C.attend(q[t], self.scale, keys[:n])[1]
+        return dev(out, torch.float32)
+
+    def weights(self, ctx, lse, **kw):
+        return ctx.attention_weights(self.cache, self.q, self.dev_starts, self.dev_lens, lse, self.scale, self.rows, **kw)
+
+    def check_weights(self, got, lse, window=0, carry=None, keep=1.0):
+        got, lse, q = f64(got), f64(lse), f64(self.q)
+        assert got.shape == (self.n, self.rows)
+        for s in range(self.n):
+            held = min(max(self.lens[s], 0), self.rows)
+            keys, have = self.keys(s, held)
+            want, tol = np.zeros(self.rows), np.full(self.rows, 2.0 ** -120)
+            if carry is not None:
+                want[:held] = keep * f64(carry)[s, :held]
+                tol += 4 * U * np.abs(want)
+            tokens = list(C.tokens_of(self.starts, s))
+            for t in tokens[-window:] if window else tokens:
+                n = int((have < C.seen(self.starts, self.lens, s, t, self.rows)).sum())
+                add, share = C.weights(q[t], self.scale, keys[:n], lse[t])
+                want[have[:n]] += add
+                tol[have[:n]] += (2 * 576 + 4) * U * share + (16 + 64) * U * add
+            assert (np.abs(got[s] - want) <= tol).all(), (s, float((np.abs(got[s] - want) / tol).max()))
+
+
+# ------------------------------------------------------------------ attention
+SHAPES = [
+    ([1], [1], 1, 1), ([1], [61], 16, 0), ([1], [300], 128, 16), ([4], [4], 16, 16), ([7], [500], 20, 48),
+    ([1, 4, 2], [70, 33, 129], 64, 16), ([33], [257], 5, 7), ([130], [130], 16, 16), ([5, 0, 40, 1], [900, 77, 41, 640], 24, 64),
+    ([64], [4000], 8, 16), ([3] * 40, list(range(3, 123, 3)), 16, 16), ([2], [1500], 100, 16)]
+
+
+@pytest.mark.parametrize("counts,lens,heads,block_rows", SHAPES)
+def test_chunk(kvo, ctx, counts, lens, heads, block_rows):
+    rng = np.random.default_rng([71, sum(counts), max(lens), heads])
+    c = Chunk(kvo, rng, counts, lens, heads, block_rows)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("heads", [3, 16, 64])
+def test_chunk_tokens_that_see_nothing(kvo, ctx, heads):
+    """Fewer positions than tokens, none, a negative length; `rows` below a length."""
+    rng = np.random.default_rng([72, heads])
+    c = Chunk(kvo, rng, [9, 20, 5, 6, 0], [4, 0, -7, 200, 90], heads, rows=150)
+    c.lens[0] = 4
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    c = Chunk(kvo, rng, [9, 20], [0, 0], heads, rows=0)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([6, 0, 3], [200, 10, 33], 20), ([40], [5000], 64), ([3], [40], 128)])
+def test_chunk_leaves_other_tokens_alone(kvo, ctx, counts, lens, heads):
+    """Tokens before the first sequence's and behind the last one's."""
+    rng = np.random.default_rng([73, heads])
+    c = Chunk(kvo, rng, counts, lens, heads, first=2, after=5)
+    out = torch.full((c.tokens, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.tokens, heads), 7.0, device="cuda")
+    c.attend(ctx, out=out, lse=lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    for x in (out, lse):
+        assert (x[:2] == 7).all() and (x[-5:] == 7).all()
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "one"])
+@pytest.mark.parametrize("tokens,heads", [(1, 16), (9, 20), (300, 16)])
+def test_chunk_wide_logits(kvo, ctx, order, tokens, heads):
+    """Logits of hundreds that rise or fall along the positions, or one position far above all others."""
+    rng = np.random.default_rng([74, tokens, heads, len(order)])
+    n = 1300
+    raw = random_rows(rng, n)
+    for j in range(n):
+        x = np.zeros(64)
+        x[:8] = {"rising": j / 20, "falling": (n - j) / 20, "one": 60.0 * (j == 777)}[order]
+        raw[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+    q = rng.standard_normal((tokens, heads, 576))
+    q[..., 512:520] = np.linspace(-1, 4, heads)[None, :, None]
+    c = Chunk(kvo, rng, [tokens], [n], heads, 0, scale=0.5, q=dev(q, torch.bfloat16), raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("heads,tokens", [(5, 12), (16, 40), (64, 40), (64, 300)])
+def test_chunk_values_that_are_not_seen(kvo, ctx, heads, tokens):
+    """A row that reads as NaN: the tokens before it give what they give without it, the others are NaN.  Rows past the
+    length, whatever they hold, change nothing."""
+    rng = np.random.default_rng([75, heads, tokens])
+    n, at = 333, 333 - tokens // 2
+    c = Chunk(kvo, rng, [tokens], [n], heads, rows=400)
+    clean = c.attend(ctx)
+    raw = c.raw.copy()
+    past = [O.row_of(c.table, c.total, 16, 1, 0, p) for p in range(n, 400)]
+    raw[past, 512:] = 0xFF
+    nan = O.row_of(c.table, c.total, 16, 1, 0, at)
+    for kind in range(3):
+        spoilt = raw.copy()
+        if kind == 0:
+            spoilt[nan, 518:520] = 0xFF                       # a NaN scale
+        elif kind == 1:
+            spoilt[nan, 512:514] = np.array([0x7C00], np.uint16).view(np.uint8)   # an infinite one
+        else:
+            spoilt[nan, 600:602] = 0xFF                       # a NaN in the position part
+        d = Chunk(kvo, rng, [tokens], [n], heads, rows=400, q=c.q, raw=spoilt, table=(c.table, c.total))
+        out, lse = d.attend(ctx)
+        assert ctx.sync() == kvo.KVO_OK
+        before = at - (n - tokens)                            # tokens that do not see it
+        assert torch.equal(out[:before], clean[0][:before]) and torch.equal(lse[:before], clean[1][:before])
+        assert torch.isnan(lse[before:]).all() and torch.isnan(out[before:, :, :64]).all()
+
+
+@pytest.mark.parametrize("tokens", [4, 200])
+def test_chunk_infinite_logits(kvo, ctx, tokens):
+    """Position parts that make logits -inf for some heads: nothing from them, and nothing at all from only such."""
+    rng = np.random.default_rng([76, tokens])
+    n, heads = 260, 20
+    raw = random_rows(rng, n)
+    raw[3::7, 528:530] = np.array([0x7F80], np.uint16).view(np.uint8)             # +inf
+    q = np.abs(rng.standard_normal((tokens, heads, 576)))
+    q[:, :, 512] = -np.abs(q[:, :, 512])
+    c = Chunk(kvo, rng, [tokens], [n], heads, 0, q=dev(q, torch.bfloat16), raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    gone = [p for p in range(n) if p % 7 == 3]
+    keys = C.values(raw)
+    for t in range(tokens):
+        seen = C.seen(c.starts, c.lens, 0, t, n)
+        have = [p for p in range(seen) if p not in gone]
+        want, want_lse, spread, size = C.attend(f64(c.q)[t], SCALE, keys[have])
+        tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 4 * U * 576 * size + 100 * U)[:, None]
+        assert (np.abs(f64(out)[t] - want) <= tol).all()
+        assert (np.abs(f64(lse)[t] - want_lse) <= 2 * U * 576 * size + 100 * U + 2 * U * np.abs(want_lse)).all()
+    raw[:, 528:530] = np.array([0x7F80], np.uint16).view(np.uint8)
+    c = Chunk(kvo, rng, [tokens], [n], heads, 0, q=c.q, raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("heads,tokens", [(12, 3), (64, 50), (128, 200)])
+def test_chunk_bad_pages(kvo, ctx, heads, tokens):
+    """Entries without a block mask what they would hold, at the front too, and say so only when they are needed."""
+    rng = np.random.default_rng([77, heads])
+    table = np.array([[-1, 1, -5, 3, 0, 77, 2 ** 31 - 1], [2, 0, 77, 9999, -1, -1, -1]], np.int32)
+    for lens, want in (([112, 60], kvo.KVO_ERANGE), ([80, 20], kvo.KVO_ERANGE), ([0, 32], kvo.KVO_OK)):
+        c = Chunk(kvo, rng, [tokens, min(tokens, 7)], lens, heads, 16, rows=112, table=(table, 4))
+        out, lse = c.attend(ctx)
+        assert ctx.sync() == want
+        c.check_attend(out, lse)
+
+
+def test_chunk_bad_starts(kvo, ctx):
+    """Starts outside the tokens, or that go back: an error is latched, and nothing behind the outputs is touched."""
+    rng = np.random.default_rng(78)
+    c = Chunk(kvo, rng, [4, 4, 4], [100, 90, 80], 20)
+    for starts in ([0, 4, 8, 13], [-1, 4, 8, 12], [0, 9, 4, 12], [0, 4, 2 ** 31 - 1, 12], [0, -2 ** 31, 8, 12]):
+        wide = torch.full((14, 20, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(12, 20, device="cuda")
+        bad = dev(starts, torch.int32)
+        ctx.attend_chunk(c.cache, c.q, bad, c.dev_lens, SCALE, 100, out=wide[1:13], lse=lse)
+        assert ctx.sync() == kvo.KVO_ERANGE, starts
+        assert (wide[0] == 7).all() and (wide[13] == 7).all()
+        ctx.attention_weights(c.cache, c.q, bad, c.dev_lens, lse, SCALE, 100)
+        assert ctx.sync() == kvo.KVO_ERANGE, starts
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([3, 2], [90, 41], 24), ([70], [300], 16), ([5], [200], 128), ([40, 41], [99, 200], 7)])
+def test_chunk_strides(kvo, ctx, counts, lens, heads):
+    """Queries as views of wider ones, and heads before tokens."""
+    rng = np.random.default_rng([79, heads])
+    c = Chunk(kvo, rng, counts, lens, heads)
+    want, want_lse = c.attend(ctx)
+    c.check_attend(want, want_lse)
+    weights = c.weights(ctx, want_lse)
+    wide = torch.full((c.tokens, 2 * heads, 592), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1::2, 8:584] = c.q
+    across = torch.empty(heads, c.tokens, 576, dtype=torch.bfloat16, device="cuda")
+    across.copy_(c.q.transpose(0, 1))
+    for q in (wide[:, 1::2, 8:584], across.transpose(0, 1)):
+        c.q = q
+        out, lse = c.attend(ctx)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        got = c.weights(ctx, want_lse)
+        assert ctx.sync() == kvo.KVO_OK
+        c.check_weights(got, want_lse)
+    del weights
+
+
+def test_chunk_of_one_token_is_attend(kvo, ctx):
+    """The decode form: a token a sequence gives what kvo_attend gives, to the rounding of both."""
+    rng = np.random.default_rng(80)
+    c = Chunk(kvo, rng, [1] * 5, [300, 1, 0, 77, 160], 20)
+    out, lse = c.attend(ctx)
+    one, one_lse = ctx.attend(c.cache, c.q, c.dev_lens, SCALE, rows=300)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    c.check_attend(one, one_lse)
+
+
+# -------------------------------------------------------------------- weights
+@pytest.mark.parametrize("counts,lens,heads,block_rows", SHAPES)
+@pytest.mark.parametrize("window", [0, 1, 3])
+def test_weights(kvo, ctx, counts, lens, heads, block_rows, window):
+    rng = np.random.default_rng([81, sum(counts), max(lens), heads])
+    c = Chunk(kvo, rng, counts, lens, heads, block_rows)
+    lse = c.lse()
+    carry = dev(rng.exponential(1.0, (c.n, c.rows)), torch.float32)
+    got = c.weights(ctx, lse, window=window, carry=carry, keep=0.875)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_weights(got, lse, window, carry, 0.875)
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([700], [900], 16), ([300], [300], 64), ([64, 1, 200], [2500, 513, 255], 20)])
+def test_weights_of_many_tokens(kvo, ctx, counts, lens, heads):
+    """Several tiles of columns, in one pair of CTAs and split; what a token gives adds up to one a head."""
+    rng = np.random.default_rng([82, sum(counts), heads])
+    c = Chunk(kvo, rng, counts, lens, heads)
+    out, lse = c.attend(ctx)
+    got = c.weights(ctx, lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    c.check_weights(got, lse)
+    total = got.double().sum(1).cpu().numpy()
+    assert np.allclose(total, np.array(counts) * heads, rtol=1e-4)
+
+
+def test_weights_edges(kvo, ctx):
+    """Tokens that see nothing, sequences without tokens or positions, strides, in place, and -inf from a masked lse."""
+    rng = np.random.default_rng(83)
+    c = Chunk(kvo, rng, [9, 20, 0, 6, 2], [4, 0, 40, 200, -5], 24, rows=170)
+    lse = c.lse()
+    wide = dev(rng.exponential(1.0, (5, 400)), torch.float32)
+    carry = wide[:, 7:177].clone()
+    got = c.weights(ctx, lse, carry=wide[:, 7:177], keep=0.5, out=wide[:, 7:177])
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_weights(got, lse, 0, carry, 0.5)
+    lse[29:33, 3:9] = -float("inf")
+    got = c.weights(ctx, lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_weights(got, lse)
+    none = Chunk(kvo, rng, [0, 0], [50, 3], 8)
+    carry = dev(rng.exponential(1.0, (2, 50)), torch.float32)
+    got = none.weights(ctx, torch.empty(0, 8, device="cuda"), carry=carry)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.equal(got[0], carry[0]) and torch.equal(got[1, :3], carry[1, :3]) and not got[1, 3:].any()
+
+
+def test_weights_are_not_reached_by_hidden_values(kvo, ctx):
+    """NaN rows past the length, NaN queries of a neighbouring sequence, a NaN row that only later tokens see."""
+    rng = np.random.default_rng(84)
+    c = Chunk(kvo, rng, [3, 5, 4], [150, 90, 33], 20, rows=160)
+    lse = c.lse()
+    clean = c.weights(ctx, lse)
+    c.check_weights(clean, lse)
+    raw = c.raw.copy()
+    for s in range(3):
+        for p in range(c.lens[s], 160):
+            raw[O.row_of(c.table, c.total, 16, 3, s, p), 512:] = 0xFF
+    q = c.q.clone()
+    q[8:] = float("nan")
+    d = Chunk(kvo, rng, [3, 5, 4], [150, 90, 33], 20, rows=160, q=q, raw=raw, table=(c.table, c.total))
+    got = d.weights(ctx, lse)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.equal(got[:2], clean[:2]) and torch.isnan(got[2, :30]).all()
+    raw = c.raw.copy()
+    raw[O.row_of(c.table, c.total, 16, 3, 1, 87), 528:530] = 0xFF
+    d = Chunk(kvo, rng, [3, 5, 4], [150, 90, 33], 20, rows=160, q=c.q, raw=raw, table=(c.table, c.total))
+    got = d.weights(ctx, lse)
+    assert torch.isnan(got[1, 87])
+    got[1, 87] = clean[1, 87]
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("counts,lens", [([3, 2], [112, 60]), ([30, 30], [80, 64])])
+def test_weights_bad_pages(kvo, ctx, counts, lens):
+    rng = np.random.default_rng(85)
+    table = np.array([[-1, 1, -5, 3, 0, 77, 2 ** 31 - 1], [2, 0, 77, 9999, -1, -1, -1]], np.int32)
+    c = Chunk(kvo, rng, counts, lens, 12, 16, rows=112, table=(table, 4))
+    lse = c.lse()
+    carry = dev(rng.exponential(1.0, (2, 112)), torch.float32)
+    got = c.weights(ctx, lse, carry=carry)
+    assert ctx.sync() == kvo.KVO_ERANGE
+    c.check_weights(got, lse, 0, carry)
+
+
+# --------------------------------------------------------------------- shrink
+def shrink_case(kvo, ctx, rng, lens, n, budget, first, last, key, block_rows, to_rows=None, weights=None, strided=False):
+    sequences = len(lens)
+    br, to_br = block_rows or n, to_rows or block_rows or budget
+    table, total = block_table(rng, sequences, -(-n // br)) if block_rows else (None, sequences)
+    to_table, to_total = block_table(rng, sequences, -(-budget // to_br)) if block_rows or to_rows else (None, sequences)
+    raw = random_rows(rng, total * br)
+    src, dst = dict(rows=dev(raw)), dict(rows=torch.full((to_total * to_br, 656), 0x5A, dtype=torch.uint8, device="cuda"))
+    if key != "none":
+        keys = dev(rng.integers(0, 255, (total * br, 128 if key == "e4m3" else 256), dtype=np.uint8))
+        kind = torch.float8_e4m3fn if key == "e4m3" else torch.bfloat16
+        src["keys"] = keys.view(kind)
+        dst["keys"] = torch.full((to_total * to_br, keys.shape[1]), 0x22, dtype=torch.uint8, device="cuda").view(kind)
+        if key == "e4m3":
+            src["key_scales"] = dev(rng.exponential(1.0, total * br), torch.float32)
+            dst["key_scales"] = torch.full((to_total * to_br,), 5.0, device="cuda")
+    if weights is None:
+        weights = rng.exponential(1.0, (sequences, n)).astype(np.float32)
+        weights[rng.random((sequences, n)) < 0.3] = 0.0
+    a = kvo.Cache(**src, block_rows=br, table=None if table is None else dev(table))
+    b = kvo.Cache(**dst, block_rows=to_br, table=None if to_table is None else dev(to_table))
+    w, kw = dev(weights), {}
+    if strided:
+        wide = torch.full((sequences, n + 9), float("nan"), device="cuda")
+        wide[:, 4:n + 4] = w
+        w = wide[:, 4:n + 4]
+        kw = dict(kept=torch.full((sequences, budget + 3), 77, dtype=torch.int32, device="cuda")[:, 1:budget + 1],
+                  to_weights=torch.full((sequences, budget + 5), 77.0, device="cuda")[:, 2:budget + 2])
+    kept, new_lens, to_weights = ctx.shrink_cache(a, b, w, dev(lens, torch.int32), budget, first, last, **kw)
+    assert ctx.sync() == kvo.KVO_OK
+    want_rows = np.full((to_total * to_br, 656), 0x5A, np.uint8)
+    want_keys = None if key == "none" else np.full((to_total * to_br, src["keys"].view(torch.uint8).shape[1]), 0x22, np.uint8)
+    want_scales = np.full(to_total * to_br, 5.0, np.float32)
+    for s, have in enumerate(lens):
+        have = min(max(have, 0), n)
+        stay = C.keep(weights[s], have, budget, first, last)
+        assert int(new_lens[s]) == len(stay)
+        assert kept[s].tolist() == stay + [-1] * (budget - len(stay)), s
+        got = to_weights[s].cpu().numpy()
+        assert np.array_equal(got[:len(stay)], weights[s, stay], equal_nan=True) and not got[len(stay):].any()
+        for j, p in enumerate(stay):
+            x = O.row_of(table, total, br, sequences, s, p)
+            y = O.row_of(to_table, to_total, to_br, sequences, s, j)
+            want_rows[y] = raw[x]
+            if key != "none":
+                want_keys[y] = src["keys"][x].view(torch.uint8).cpu().numpy()
+            if key == "e4m3":
+                want_scales[y] = float(src["key_scales"][x])
+    assert np.array_equal(dst["rows"].cpu().numpy(), want_rows)
+    if key != "none":
+        assert np.array_equal(dst["keys"].view(torch.uint8).cpu().numpy(), want_keys)
+    if key == "e4m3":
+        assert np.array_equal(dst["key_scales"].cpu().numpy(), want_scales)
+    if strided:
+        assert (kw["kept"]._base[:, 0] == 77).all() and (kw["kept"]._base[:, budget + 1:] == 77).all()
+        assert (kw["to_weights"]._base[:, :2] == 77).all() and (kw["to_weights"]._base[:, budget + 2:] == 77).all()
+
+
+@pytest.mark.parametrize("key", ["none", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens,n,budget,first,last,block_rows", [
+    ([1], 1, 1, 0, 0, 1), ([50], 50, 1, 0, 1, 16), ([300], 300, 77, 4, 10, 16), ([300, 0, 77, 78, -3, 500], 300, 77, 0, 77, 48),
+    ([90, 41, 64], 90, 64, 64, 0, 7), ([700], 700, 699, 1, 1, 0), ([64] * 20, 64, 33, 1, 2, 16)])
+def test_shrink(kvo, ctx, key, lens, n, budget, first, last, block_rows):
+    rng = np.random.default_rng([91, n, budget, len(lens)])
+    shrink_case(kvo, ctx, rng, lens, n, budget, first, last, key, block_rows)
+    shrink_case(kvo, ctx, rng, lens, n, budget, first, last, key, block_rows, to_rows=5, strided=True)
+
+
+@pytest.mark.parametrize("kind", ["ties", "specials", "falling", "negative"])
+@pytest.mark.parametrize("n,budget", [(100, 37), (9000, 4100), (9000, 8999)])
+def test_shrink_orders(kvo, ctx, kind, n, budget):
+    """Equal weights, infinities, NaN and zeros of both signs at the border."""
+    rng = np.random.default_rng([92, n, budget, len(kind)])
+    w = {"ties": rng.integers(0, 3, (2, n)).astype(np.float32),
+         "specials": rng.choice(np.array([0.0, -0.0, np.nan, -np.nan, np.inf, -np.inf, 1e-45, -1e-45, 1.0], np.float32), (2, n)),
+         "falling": np.tile(np.linspace(1, 0, n, dtype=np.float32), (2, 1)),
+         "negative": -rng.exponential(1.0, (2, n)).astype(np.float32)}[kind]
+    shrink_case(kvo, ctx, rng, [n, n - 50], n, budget, 2, 3, "none", 16, weights=w)
+
+
+@pytest.mark.parametrize("n,budget,sequences", [(70_001, 20_000, 1), (30_000, 1_000, 9), (900_000, 450_001, 1), (2_500, 300, 200)])
+def test_shrink_large(kvo, ctx, n, budget, sequences):
+    """Clusters of every width, keys in shared memory and not; compared on the GPU with a stable sort."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    lens = torch.full((sequences,), n, dtype=torch.int32, device="cuda")
+    lens[sequences // 2:] -= 7
+    w = torch.rand(sequences, n, generator=g, device="cuda")
+    w = torch.where(w < 0.6, (w * 50).round(), w)            # many equal ones
+    rows = torch.randint(0, 256, (sequences * n, 656), generator=g, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(sequences * budget, 656, dtype=torch.uint8, device="cuda")
+    a, b = kvo.Cache(rows=rows, block_rows=n), kvo.Cache(rows=out, block_rows=budget)
+    kept, new_lens, to_weights = ctx.shrink_cache(a, b, w, lens, budget, first=5, last=100)
+    assert ctx.sync() == kvo.KVO_OK
+    assert (new_lens == budget).all()
+    for s in range(sequences):
+        have = int(lens[s])
+        order = w[s, :have].clone()
+        order[:5] = order[have - 100:] = 1e9
+        want = order.sort(descending=True, stable=True).indices[:budget].sort().values
+        assert torch.equal(kept[s].long(), want)
+        assert torch.equal(to_weights[s], w[s, want])
+        assert torch.equal(out[s * budget:(s + 1) * budget], rows[s * n + want])
+
+
+def test_shrink_bad_pages(kvo, ctx):
+    """A source without a row becomes zeros, a destination without one is dropped; both are said."""
+    rng = np.random.default_rng(94)
+    raw = random_rows(rng, 64)
+    table = np.array([[1, -1, 3, 0], [2, 0, 77, 9999]], np.int32)
+    to_table = np.array([[0, 1], [-1, 2]], np.int32)
+    w = rng.exponential(1.0, (2, 64)).astype(np.float32)
+    out = torch.full((48, 656), 0x5A, dtype=torch.uint8, device="cuda")
+    keys = dev(rng.integers(0, 255, (64, 256), dtype=np.uint8)).view(torch.bfloat16)
+    to_keys = torch.full((48, 256), 0x5A, dtype=torch.uint8, device="cuda").view(torch.bfloat16)
+    a = kvo.Cache(rows=dev(raw), keys=keys, block_rows=16, table=dev(table))
+    b = kvo.Cache(rows=out, keys=to_keys, block_rows=16, table=dev(to_table))
+    kept, new_lens, _ = ctx.shrink_cache(a, b, dev(w), dev([64, 60], torch.int32), 30, 0, 5)
+    assert ctx.sync() == kvo.KVO_ERANGE
+    want, want_keys = np.full((48, 656), 0x5A, np.uint8), np.full((48, 256), 0x5A, np.uint8)
+    for s in range(2):
+        stay = C.keep(w[s], (64, 60)[s], 30, 0, 5)
+        assert kept[s].tolist() == stay
+        for j, p in enumerate(stay):
+            x, y = O.row_of(table, 4, 16, 2, s, p), O.row_of(to_table, 3, 16, 2, s, j)
+            if y is not None:
+                want[y] = 0 if x is None else raw[x]
+                want_keys[y] = 0 if x is None else keys[x].view(torch.uint8).cpu().numpy()
+    assert np.array_equal(out.cpu().numpy(), want)
+    assert np.array_equal(to_keys.view(torch.uint8).cpu().numpy(), want_keys)
+
+
+# ------------------------------------------------------------------- together
+def session(kvo, ctx, seed, stream=None, sizes=((120, 90), (60, 61)), heads=20, budget=70):
+    """Two chunks of two sessions, their attention and weights, then the shrunk cache and a decode step on it."""
+    rng = np.random.default_rng(seed)
+    n = max(sum(s[i] for s in sizes) for i in range(2))
+    br = 16
+    table, total = block_table(rng, 2, -(-n // br))
+    to_table, to_total = block_table(rng, 2, -(-(budget + 1) // br))
+    st = dict(rng=rng, raw=torch.zeros(total * br, 656, dtype=torch.uint8, device="cuda"), table=table, to_table=to_table,
+              to=torch.zeros(to_total * br, 656, dtype=torch.uint8, device="cuda"), n=n, heads=heads, budget=budget, br=br)
+    st["cache"] = kvo.Cache(rows=st["raw"], block_rows=br, table=dev(table))
+    st["small"] = kvo.Cache(rows=st["to"], block_rows=br, table=dev(to_table))
+    st["total"], st["to_total"] = total, to_total
+    held = np.zeros(2, int)
+    st["pieces"] = []
+    for piece in sizes:
+        seq = np.repeat([0, 1], piece).astype(np.int32)
+        pos = np.concatenate([held[s] + np.arange(piece[s]) for s in range(2)]).astype(np.int32)
+        held = held + piece
+        st["pieces"].append(dict(seq=dev(seq), pos=dev(pos), starts=dev(np.array([0, piece[0], sum(piece)], np.int32)),
+                                 lens=dev(held.astype(np.int32)), host=held.copy(),
+                                 kv=dev(rng.standard_normal((sum(piece), 576)), torch.bfloat16),
+                                 q=dev(rng.standard_normal((sum(piece), heads, 576)), torch.bfloat16)))
+    st["weights"] = torch.zeros(2, n, device="cuda")
+    st["one"] = dev(rng.standard_normal((2, heads, 576)), torch.bfloat16)
+    st["one_kv"] = dev(rng.standard_normal((2, 576)), torch.bfloat16)
+    st["one_starts"] = dev(np.arange(3), torch.int32)
+    return st
+
+
+FREQ = 10_000.0 ** (-np.arange(0, 64, 2) / 64)
+
+
+def run_session(ctx, st, stream=None):
+    outs = []
+    st["weights"].zero_()
+    for p in st["pieces"]:
+        ctx.append_tokens(st["cache"], p["kv"][:, :512], p["kv"][:, 512:], p["pos"], FREQ, seq=p["seq"], stream=stream)
+        out, lse = ctx.attend_chunk(st["cache"], p["q"], p["starts"], p["lens"], SCALE, st["n"], stream=stream)
+        ctx.attention_weights(st["cache"], p["q"], p["starts"], p["lens"], lse, SCALE, st["n"], window=16,
+                              carry=st["weights"], keep=0.75, out=st["weights"], stream=stream)
+        outs += [out, lse]
+    kept, lens, w = ctx.shrink_cache(st["cache"], st["small"], st["weights"], st["pieces"][-1]["lens"], st["budget"], 2, 8,
+                                     stream=stream)
+    # the next token goes behind what stayed, turned by its own position
+    pos = st["pieces"][-1]["lens"]
+    at = st["one_kv"]
+    ctx.append_tokens(st["small"], at[:, :512], at[:, 512:], lens, FREQ, stream=stream)
+    more = lens + 1
+    out, lse = ctx.attend_chunk(st["small"], st["one"], st["one_starts"], more, SCALE, st["budget"] + 1, stream=stream)
+    del pos
+    return outs + [kept, lens, w, st["weights"], out, lse, st["to"], st["raw"]]
+
+
+def test_a_session_together(kvo, ctx):
+    st = session(kvo, ctx, 95)
+    outs = run_session(ctx, st)
+    assert ctx.sync() == kvo.KVO_OK
+    rng = np.random.default_rng(1)
+    raw = st["raw"].cpu().numpy()
+    mass = None
+    for i, p in enumerate(st["pieces"]):
+        counts = np.diff(p["starts"].cpu().numpy()).tolist()
+        c = Chunk(kvo, rng, counts, p["host"].tolist(), st["heads"], st["br"], rows=st["n"], q=p["q"], raw=raw,
+                  table=(st["table"], st["total"]))
+        c.check_attend(outs[2 * i], outs[2 * i + 1])
+        got = c.weights(ctx, outs[2 * i + 1], window=16, carry=mass, keep=0.75)
+        c.check_weights(got, outs[2 * i + 1], 16, mass, 0.75)
+        mass = got
+    kept, lens, w, total, out, lse = outs[4:10]
+    assert torch.equal(mass, total)
+    for s in range(2):
+        stay = C.keep(total[s].cpu().numpy(), int(st["pieces"][-1]["host"][s]), st["budget"], 2, 8)
+        assert kept[s].tolist() == stay and torch.equal(w[s], total[s, stay])
+    small = Chunk(kvo, rng, [1, 1], (lens.cpu().numpy() + 1).tolist(), st["heads"], st["br"], rows=st["budget"] + 1,
+                  q=st["one"], raw=st["to"].cpu().numpy(), table=(st["to_table"], st["to_total"]))
+    small.check_attend(out, lse)
+
+
+def test_side_stream_graph_and_two_streams(kvo, ctx):
+    """The same bits on another stream, captured and replayed on new inputs, and from two sessions at once."""
+    a, b = session(kvo, ctx, 96), session(kvo, ctx, 97, sizes=((33, 200), (10, 7)), heads=64, budget=90)
+    want = [[t.clone() for t in run_session(ctx, x)] for x in (a, b)]
+    assert ctx.sync() == kvo.KVO_OK
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x in (a, b):
+            x["raw"].zero_()
+            x["to"].zero_()
+        torch.cuda.synchronize()
+        got = [None, None]
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i] = run_session(ctx, x)
+        torch.cuda.synchronize()
+        for x, y in zip(want[0] + want[1], got[0] + got[1]):
+            assert torch.equal(x, y)
+    graphs = []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = run_session(ctx, x)
+        graphs.append((g, res))
+    for p in a["pieces"]:
+        p["q"].copy_(p["q"].roll(1, 0))
+        p["kv"].copy_(p["kv"].roll(1, 0))
+    want[0] = [t.clone() for t in run_session(ctx, a)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for i, (g, _) in enumerate(graphs):
+            with torch.cuda.stream(streams[i]):
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (_, res) in enumerate(graphs):
+            for x, y in zip(want[i], res):
+                assert torch.equal(x, y)
+    assert ctx.sync() == kvo.KVO_OK
+
+
+WAITS = (0, 0, 1, 100, 1_000, 4_000, 0, 20_000, 400)
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([3, 2], [300, 40], 20), ([512], [600], 16), ([90, 300], [4000, 900], 64)])
+def test_waits_that_run_out(kvo, counts, lens, heads):
+    rng = np.random.default_rng([98, sum(counts)])
+    c = kvo.Context(1, 64, 64)
+    chunk = Chunk(kvo, rng, counts, lens, heads)
+
+    def run(lse=None):
+        out, l = chunk.attend(c)
+        return out, l, chunk.weights(c, l if lse is None else lse)
+
+    want = [t.clone() for t in run()]
+    assert c.sync() == kvo.KVO_OK
+    for clocks in WAITS:
+        c.set_wait_clocks(clocks)
+        got = run(want[1])
+        status = c.sync()
+        assert status in ((kvo.KVO_ETIMEDOUT,) if clocks == 0 else (kvo.KVO_OK, kvo.KVO_ETIMEDOUT))
+        assert c.sync() == kvo.KVO_OK                            # said once, and the context goes on
+        c.set_wait_clocks()
+        for again in (got if status == kvo.KVO_OK else None, run()):
+            for a, b in zip(again or (), want):
+                assert torch.equal(a, b), clocks
+        assert c.sync() == kvo.KVO_OK
+    c.close()

@@ -944,60 +944,47 @@ extern "C" kvo_status kvo_attend(kvo_ctx* ctx, const kvo_cache* cache, const kvo
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }
 
-extern "C" int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows) {
-  if (tokens < 0 || tokens > KVO_MAX_QUERIES || sequences < 1 || sequences > KVO_MAX_QUERIES) return -1;
-  if (heads < 1 || heads > KVO_MAX_HEADS || rows < 0 || rows > INT32_MAX - 255) return -1;
-  const kvo::Cut c = kvo::chunk_cut_of(tokens, sequences, (uint32_t)heads, rows);
+namespace kvo {
+
+// kvo_attend_chunk for chunks with few columns (kvo_chunk.cu chooses).
+int64_t few_columns_work(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
+  const Cut c = chunk_cut_of(tokens, sequences, heads, rows);
   return c.splits == 1 ? 0 : (int64_t)c.splits * tokens * heads * (KVO_LATENT_BYTES + 1) * 4;
 }
 
-extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, const kvo_chunk_query* s, void* stream) {
-  using namespace kvo;
-  uint32_t* status = nullptr;
-  if (!ctx || !cache_ok(cache) || !s || !cache_rows_ok(cache)) return KVO_EINVAL;
-  const int64_t need = kvo_attend_chunk_work_bytes(s->tokens, cache->sequences, s->heads, s->rows);
-  if (need < 0 || !s->starts || !s->lens || !std::isfinite(s->scale)) return KVO_EINVAL;
-  if (!aligned(s->starts, 4) || !aligned(s->lens, 4)) return KVO_EINVAL;
-  if (s->tokens > 0) {
-    if (!s->q || !s->out || s->work_bytes < need || (need && !s->work)) return KVO_EINVAL;
-    if (!aligned(s->q, 16) || s->q_ld % 8 || s->q_head_ld % 8 || !aligned(s->out, 16)) return KVO_EINVAL;
-    if (!aligned(s->lse, 4) || !aligned(s->work, 16)) return KVO_EINVAL;
-  }
-  int64_t wait_clocks = 0;
-  const kvo_status st = usable_status(ctx, &status, &wait_clocks);
-  if (st != KVO_OK) return st;
-  if (s->tokens == 0) return KVO_OK;
-
+cudaError_t launch_few_columns(const kvo_cache& cache, const kvo_chunk_query& s, uint32_t* status, int64_t wait_clocks,
+                               cudaStream_t stream) {
   AttendArgs a = {};
   a.wait_clocks = wait_clocks;
-  a.cache = cache_view(*cache);
-  a.q = static_cast<const uint8_t*>(s->q);
-  a.lens = s->lens;
-  a.starts = s->starts;
-  a.tokens = (uint32_t)s->tokens;
-  a.out = s->out;
-  a.lse = s->lse;
+  a.cache = cache_view(cache);
+  a.q = static_cast<const uint8_t*>(s.q);
+  a.lens = s.lens;
+  a.starts = s.starts;
+  a.tokens = (uint32_t)s.tokens;
+  a.out = s.out;
+  a.lse = s.lse;
   a.status = status;
-  a.q_ld = s->q_ld * 2;
-  a.q_head_ld = s->q_head_ld * 2;
-  a.rows = (uint32_t)s->rows;
+  a.q_ld = s.q_ld * 2;
+  a.q_head_ld = s.q_head_ld * 2;
+  a.rows = (uint32_t)s.rows;
   a.per_seq = 1;
-  a.heads = (uint32_t)s->heads;
+  a.heads = (uint32_t)s.heads;
   a.by_heads = divider(a.heads);
-  a.scale = s->scale * kLog2e;
-  const Cut cut = chunk_cut_of(s->tokens, cache->sequences, a.heads, s->rows);
-  const int64_t columns = s->tokens * a.heads;
+  a.scale = s.scale * kLog2e;
+  const Cut cut = chunk_cut_of(s.tokens, cache.sequences, a.heads, s.rows);
+  const int64_t columns = s.tokens * a.heads;
   a.nq = a.tokens;
   a.head_tiles = cut.head_tiles;
   a.splits = cut.splits;
-  a.part = static_cast<float*>(s->work);
+  a.part = static_cast<float*>(s.work);
   a.part_lse = a.part + (int64_t)a.splits * columns * KVO_LATENT_BYTES;
-  const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  const dim3 grid(chunk_tiles(s->tokens, cache->sequences, a.heads, cut.heads) * a.splits);
-  cudaError_t e = cut.heads == 16   ? launch_attend<16, true>(a, grid, on)
-                  : cut.heads == 32 ? launch_attend<32, true>(a, grid, on)
-                                    : launch_attend<64, true>(a, grid, on);
+  const dim3 grid(chunk_tiles(s.tokens, cache.sequences, a.heads, cut.heads) * a.splits);
+  cudaError_t e = cut.heads == 16   ? launch_attend<16, true>(a, grid, stream)
+                  : cut.heads == 32 ? launch_attend<32, true>(a, grid, stream)
+                                    : launch_attend<64, true>(a, grid, stream);
   if (e == cudaSuccess && a.splits > 1)
-    e = launch_join(a, columns, Covered{a.starts, a.cache.sequences, a.heads}, on);
-  return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
+    e = launch_join(a, columns, Covered{a.starts, a.cache.sequences, a.heads}, stream);
+  return e;
 }
+
+}  // namespace kvo

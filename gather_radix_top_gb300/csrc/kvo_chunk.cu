@@ -1,0 +1,934 @@
+// kvo_attend_chunk: causal attention of prompt chunks over a paged cache.
+//
+// Chunks with few columns ((token, head) pairs) go through the kernel of
+// kvo_attend, which dequantises rows for 64 columns at a time.  With many, the
+// rows are first unpacked to bf16 in the caller's scratch, once, and two CTAs
+// of a cluster work on 128 columns and 256 positions at a time:
+//     S^T [256 positions x 128 columns]      = K [256 x 576] Q^T
+//     O^T [512 values x 128 columns]        += V^T [512 x 256] P^T
+// as pair MMAs with M = 256: a CTA holds 128 of the positions for the first
+// product and 256 of the values for the second, so that O^T takes 256 of its
+// 512 columns of tensor memory and S^T, twice, the rest.  The columns' operand
+// is halved between them: 64 columns of queries (72 KB) and of weights (32 KB
+// for 256 positions) lie in each CTA's shared memory; the positions' operands
+// stream through a ring of seven pieces of 16 KB (128 positions of 64 values
+// for the first product, 64 positions of 128 values for the second).
+//
+// Sixteen worker warps do the softmax: a lane of S^T is a position.  A CTA
+// writes the weights of the other's 64 columns to the other's shared memory.
+// The softmax's reference is the column's maximum in the first tile of
+// positions.  Weights of up to 2^64 lose nothing in fp32 and bf16; where a
+// later logit lies further above, or the first tile shows a column nothing and
+// a later one does, the tile is done again at the end, with the true maximum
+// from a pass over its logits.  So no tile waits for a maximum.
+//
+// Tiles of columns times tiles of positions, end to end, are shared out evenly
+// over the pairs.  Where a share begins or ends inside a tile of columns, the
+// parts are joined by their log-sum-exps in a second launch.
+#include "kvo_cache.cuh"
+#include "kvo_chunk.cuh"
+#include "kvo_rows.cuh"
+#include "kvo_tc.cuh"
+
+namespace kvo {
+
+// The kernel for few columns (kvo_attend.cu).
+int64_t few_columns_work(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows);
+cudaError_t launch_few_columns(const kvo_cache& cache, const kvo_chunk_query& s, uint32_t* status, int64_t wait_clocks,
+                               cudaStream_t stream);
+
+namespace {
+
+constexpr uint32_t kSpan = 256;                          // positions of a tile
+constexpr uint32_t kTileColumns = 2 * kColumns;
+constexpr uint32_t kWorkers = 16;
+constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
+constexpr uint32_t kChunkThreads = (kLoader + 1) * 32;
+constexpr uint32_t kQueryBytes = 9 * kColumns * 128;
+constexpr uint32_t kWeightBytes = kSpan * 128;
+constexpr uint32_t kSlotBytes = 16384, kSlots = 7;
+constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + kWeightBytes + kSlots * kSlotBytes;
+constexpr uint32_t kValueBytes = KVO_DEQUANT_VALUES * 2;
+constexpr float kFar = 64.0f;                            // in powers of two
+
+// One tile of columns, as the plan lists it.
+struct __align__(16) PlanTile {
+  uint64_t units;            // tiles of positions of all tiles before it
+  int32_t seq;
+  uint32_t index;            // of its sequence's tiles
+  uint32_t first, tokens;    // its sequence's tokens
+  int32_t before;            // token i sees the first before + i positions
+  uint32_t pad;
+};
+
+struct ChunkArgs {
+  CacheView cache;
+  const int32_t* starts;
+  const int32_t* lens;
+  uint16_t* out;
+  float* lse;
+  uint8_t* values;           // [sequences][span][576] bf16
+  float* off;                // [sequences][span]: 0, or -inf where there is no row
+  PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
+  uint8_t* again;            // [most_tiles] whole tiles, [2 * pairs] parts that need another pass
+  float* part;               // [2 * pairs][128][512]
+  float* part_lse;           // [2 * pairs][128], base 2
+  uint32_t* status;
+  uint32_t rows, span, tokens, heads, most_tiles, pairs;
+  uint32_t unpack_blocks;    // of a sequence
+  Divider by_heads;
+  Columns columns;
+  float scale;               // times log2(e)
+  int64_t wait_clocks;
+};
+
+// ------------------------------------------------------------ rows and plan
+constexpr uint32_t kUnpackThreads = 256, kUnpackRows = 64;   // of a CTA, 8 of a warp
+
+__device__ __forceinline__ uint32_t visible(const ChunkArgs& a, int32_t before, uint32_t token) {
+  return (uint32_t)min(max(before + (int32_t)token, 0), (int32_t)a.rows);
+}
+
+// The token of column `in_half` of half tile `half`; >= tokens where there is none.
+__device__ __forceinline__ uint32_t column_at(const ChunkArgs& a, const PlanTile& t, uint32_t half, uint32_t in_half,
+                                              uint32_t* at) {
+  const Columns& c = a.columns;
+  const uint32_t deep = divide(in_half, c.by_wide), wide = in_half - deep * c.wide;
+  const uint32_t row = half / c.across * c.deep + deep, head = half % c.across * c.wide + wide;
+  *at = c.flat ? row : row * a.heads + head;
+  if (deep >= c.deep || (!c.flat && head >= a.heads)) return UINT32_MAX;
+  return divide(*at, a.by_heads);
+}
+
+// The last token of a tile.
+__device__ __forceinline__ uint32_t last_token(const ChunkArgs& a, uint32_t index, uint32_t tokens) {
+  const Columns& c = a.columns;
+  const uint32_t rows = (2 * index + 1) / c.across * c.deep + c.deep;   // up to the tile's end
+  return min(c.flat ? divide(min(rows, tokens * a.heads) - 1, a.by_heads) : rows - 1, tokens - 1);
+}
+
+// One CTA lists the tiles: 256 sequences at a time, then their tiles.
+__device__ void make_plan(const ChunkArgs& a) {
+  __shared__ uint32_t upto[kUnpackThreads], first[kUnpackThreads], count[kUnpackThreads];
+  __shared__ uint64_t sums[kUnpackThreads / 32];
+  __shared__ uint32_t tile_sums[kUnpackThreads / 32];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Columns& c = a.columns;
+  uint32_t tiles = 0;
+  uint64_t units = 0;
+  for (uint32_t i = tid; i < a.most_tiles + 2 * a.pairs; i += kUnpackThreads) a.again[i] = 0;
+  for (uint32_t s0 = 0; s0 < a.cache.sequences; s0 += kUnpackThreads) {
+    const uint32_t s = s0 + tid;
+    uint32_t mine = 0;
+    if (s < a.cache.sequences) {
+      const int32_t b = a.starts[s], e = a.starts[s + 1], T = (int32_t)a.tokens;
+      if (b < 0 || b > T || e < b || e > T) atomicOr(a.status, kFlagRange);
+      first[tid] = (uint32_t)min(max(b, 0), T);
+      count[tid] = (uint32_t)min(max(e, (int32_t)first[tid]), T) - first[tid];
+      const uint32_t rows = c.flat ? count[tid] * a.heads : count[tid];
+      mine = ((rows + c.deep - 1) / c.deep * c.across + 1) / 2;
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) tile_sums[warp] = incl;
+    __syncthreads();
+    for (uint32_t w = 0; w < warp; ++w) incl += tile_sums[w];
+    upto[tid] = incl;
+    __syncthreads();
+    // (starts that go back could list more tiles than there is room for)
+    const uint32_t all = min(upto[kUnpackThreads - 1], a.most_tiles - tiles);
+    for (uint32_t j0 = 0; j0 < all; j0 += kUnpackThreads) {
+      const uint32_t j = j0 + tid;
+      PlanTile t = {};
+      uint64_t n = 0;
+      if (j < all) {
+        uint32_t lo = 0, hi = kUnpackThreads - 1;        // the first with upto > j
+        while (lo < hi) {
+          const uint32_t mid = (lo + hi) / 2;
+          if (upto[mid] > j) hi = mid; else lo = mid + 1;
+        }
+        t.seq = (int32_t)(s0 + lo);
+        t.index = j - (lo ? upto[lo - 1] : 0);
+        t.first = first[lo];
+        t.tokens = count[lo];
+        t.before = min(max(a.lens[t.seq], 0), INT32_MAX - 1) - (int32_t)t.tokens + 1;
+        n = max((visible(a, t.before, last_token(a, t.index, t.tokens)) + kSpan - 1) / kSpan, 1u);
+      }
+      uint64_t sum = n;
+#pragma unroll
+      for (uint32_t d = 1; d < 32; d <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (lane == 31) sums[warp] = sum;
+      __syncthreads();
+      uint64_t total = 0;
+      for (uint32_t w = 0; w < kUnpackThreads / 32; ++w) {
+        if (w < warp) sum += sums[w];
+        total += sums[w];
+      }
+      if (j < all) {
+        t.units = units + sum - n;
+        a.plan[tiles + j] = t;
+      }
+      units += total;
+      __syncthreads();
+    }
+    tiles += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    // the end's units, and the number of tiles in its index
+    PlanTile end = {};
+    end.units = units;
+    a.plan[tiles] = end;
+    PlanTile head = {};
+    head.units = units;
+    head.index = tiles;
+    a.plan[a.most_tiles + 1] = head;
+  }
+}
+
+// The rows that a tile of positions may hold as bf16.  A row that reads as NaN
+// somewhere gets zero latents and a NaN position part: its logits are NaN, as
+// they would have been, and a weight of 0 keeps it out of the second product.
+__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_constant__ ChunkArgs a) {
+  wait_previous_grid();
+  allow_next_grid();
+  if (blockIdx.x == 0) {
+    make_plan(a);
+    return;
+  }
+  const uint32_t s = (blockIdx.x - 1) / a.unpack_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t p0 = ((blockIdx.x - 1) % a.unpack_blocks) * kUnpackRows + warp * 8;
+  const uint32_t len = (uint32_t)min(max(a.lens[s], 0), (int32_t)a.rows);
+  if (p0 >= (max(len, 1u) + kSpan - 1) / kSpan * kSpan) return;
+  int64_t row = -1;
+  if (lane < 8) {
+    const uint32_t p = p0 + lane;
+    if (p < len) {
+      row = cache_row(a.cache, s, p);
+      if (row < 0) atomicOr(a.status, kFlagRange);
+    }
+    a.off[(int64_t)s * a.span + p] = row < 0 ? -INFINITY : 0.0f;
+  }
+  uint4 lat[8], eight[8], rope[8];
+  const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (uint32_t r = 0; r < 8; ++r) {
+    const int64_t at = __shfl_sync(0xffffffffu, row, r);
+    const uint4* from = reinterpret_cast<const uint4*>(a.cache.rows) + at * (KVO_ROW_BYTES / 16);
+    lat[r] = at >= 0 ? __ldg(from + lane) : none;
+    eight[r] = at >= 0 ? __ldg(from + KVO_LATENT_BYTES / 16) : none;
+    rope[r] = at >= 0 && lane < 8 ? __ldg(from + KVO_LATENT_BYTES / 16 + 1 + lane) : none;
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < 8; ++r) {
+    const bool bad = any_not_finite(eight[r]);
+    const uint32_t g = lane >> 2;                        // the lane's group of 64 values
+    const uint32_t two = g < 4 ? (g < 2 ? eight[r].x : eight[r].y) : (g < 6 ? eight[r].z : eight[r].w);
+    const uint16_t scale = bad ? 0 : (uint16_t)(two >> (g & 1) * 16);
+    const float bias = -1152.0f * __half2float(__ushort_as_half(scale));
+    uint4 x, y;
+    dequant4(lat[r].x, scale, bias, x.x, x.y);
+    dequant4(lat[r].y, scale, bias, x.z, x.w);
+    dequant4(lat[r].z, scale, bias, y.x, y.y);
+    dequant4(lat[r].w, scale, bias, y.z, y.w);
+    uint4* const to = reinterpret_cast<uint4*>(a.values + ((int64_t)s * a.span + p0 + r) * kValueBytes);
+    to[2 * lane] = x;
+    to[2 * lane + 1] = y;
+    if (lane < 8) to[64 + lane] = bad ? make_uint4(~0u, ~0u, ~0u, ~0u) : rope[r];
+  }
+}
+
+// ---------------------------------------------------------------- the shares
+// Pair g's share of the units: [share(g), share(g + 1)).
+struct Shares {
+  uint64_t units;
+  uint32_t pairs;
+  __device__ __forceinline__ Shares(const ChunkArgs& a) {
+    units = __ldcg(&a.plan[a.most_tiles + 1].units);
+    pairs = (uint32_t)min((uint64_t)a.pairs, max(units / 2, (uint64_t)1));
+  }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * units / pairs : units; }
+};
+
+// The tile that unit u lies in; a whole warp.
+__device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
+  uint32_t lo = 0, hi = __ldcg(&a.plan[a.most_tiles + 1].index);   // in [lo, hi)
+  const uint32_t lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool before = at < hi && __ldcg(&a.plan[at].units) <= u;
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, before));   // lane 0's always is
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ PlanTile plan_tile(const ChunkArgs& a, uint32_t i) {
+  PlanTile t;
+  const uint4* from = reinterpret_cast<const uint4*>(a.plan + i);
+  reinterpret_cast<uint4*>(&t)[0] = __ldcg(from);
+  reinterpret_cast<uint4*>(&t)[1] = __ldcg(from + 1);
+  return t;
+}
+
+// A share's part of one tile of columns: tiles of positions [from, to).
+struct Segment {
+  PlanTile tile;
+  uint32_t number, from, to;
+  bool whole;
+  // where a segment notes that it needs another pass, and its result if it is
+  // part of a tile: a share has one that begins inside a tile and one that
+  // ends inside one at most
+  __device__ __forceinline__ uint32_t slot(uint32_t pair) const { return 2 * pair + (from == 0); }
+  __device__ __forceinline__ uint32_t note(const ChunkArgs& a, uint32_t pair) const {
+    return whole ? number : a.most_tiles + slot(pair);
+  }
+};
+
+// f(segment) for every segment of a pair's share, in order, in every warp.
+template <typename F>
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, F f) {
+  if (begin >= end) return;
+  PlanTile next = plan_tile(a, tile);
+  for (uint64_t u = begin; u < end; ++tile) {
+    Segment g;
+    g.tile = next;
+    next = plan_tile(a, tile + 1);
+    g.number = tile;
+    g.from = (uint32_t)(u - g.tile.units);
+    g.to = (uint32_t)(min(next.units, end) - g.tile.units);
+    g.whole = g.from == 0 && next.units <= end;
+    u = g.tile.units + g.to;
+    if (!f(g)) return;
+  }
+}
+
+struct ChunkShared {
+  uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_empty, o_empty, met[4], agreed,
+      drained;
+  uint32_t tmem, gave_up;
+  uint32_t issued[2], q_issued[2];   // copies that each CTA's loader has started
+  uint32_t redo;                     // some segment needs another pass
+  uint32_t flag[2][kWorkers];        // per warp of both CTAs: this segment does
+  float top[2][4][4][32];            // per CTA, quarter of the columns and warp: maxima
+  float sums[2][4][4][32];
+  // per column: the softmax's reference and the positions it sees.  The four
+  // warps of a quarter write the same values, after all of them have agreed on
+  // the segment before.
+  float ref[4][32];
+  uint32_t seen[4][32];
+};
+
+template <uint32_t kN, uint32_t kBit>
+__device__ __forceinline__ void add_lanes(float* v, uint32_t lane) {
+  // a step halves the columns that a lane keeps: v[0] is column lane's sum at last
+  const bool up = lane & kBit;
+#pragma unroll
+  for (uint32_t c = 0; c < kN / 2; ++c) {
+    const float stay = up ? v[c + kN / 2] : v[c], give = up ? v[c] : v[c + kN / 2];
+    v[c] = stay + __shfl_xor_sync(0xffffffffu, give, kBit);
+  }
+  if constexpr (kBit > 1) add_lanes<kN / 2, kBit / 2>(v, lane);
+}
+
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t raw[];
+  __shared__ ChunkShared sh;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
+  const uint32_t pair = blockIdx.x >> 1;
+  const uint32_t queries = (smem_u32(raw) + 1023u) & ~1023u, probs = queries + kQueryBytes, ring = probs + kWeightBytes;
+
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], 2 * kWorkers);
+      sh.issued[i] = sh.q_issued[i] = 0;
+    }
+    mbar_init(&sh.p_full, 2 * kWorkers);
+    mbar_init(&sh.p_empty, 1);
+    mbar_init(&sh.o_empty, 2 * kWorkers);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.met[i], 8);
+    mbar_init(&sh.agreed, 2 * kWorkers);
+    mbar_init(&sh.drained, 1);
+    sh.gave_up = a.wait_clocks == 0;
+    sh.redo = 0;
+  }
+  if (warp == kMma) pair_tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  wait_previous_grid();
+  allow_next_grid();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return cluster_wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+  };
+  const Shares shares(a);
+  const uint64_t begin = shares.from(pair), end = pair < shares.pairs ? shares.from(pair + 1) : begin;
+  const uint32_t tile0 = begin < end ? tile_of(a, begin) : 0;
+  const uint32_t box = a.columns.wide * a.columns.deep * 128;
+
+  // The roles' counters run on over segments and passes.
+  uint32_t n = 0, q_n = 0;                               // copies; segments' queries
+  uint32_t it = 0, pv = 0;                               // tiles of S; second products
+  uint32_t full_n = 0, met_n = 0;                        // whole passes; exchanges of maxima
+  bool ok = true;
+
+  // One segment's work for each role; max_only: only the columns' maxima.
+  auto load = [&](const Segment& g, bool max_only) -> bool {
+    if (lane == 0) {
+      if (q_n > 0) ok = ok && wait(&sh.q_empty, (q_n - 1) & 1);
+      if (ok) {
+        const uint32_t half = 2 * g.tile.index + rank, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, 0);
+        if (rank == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
+        for (uint32_t i = 0; i < 9; ++i)
+          pair_load_box(queries + i * (kColumns * 128), &qmap, (int32_t)(i * 64),
+                        (int32_t)(half % a.columns.across * a.columns.wide),
+                        (int32_t)((a.columns.flat ? g.tile.first * a.heads : g.tile.first) + row * a.columns.deep), bar);
+        ++q_n;
+      }
+      const uint32_t base = (uint32_t)g.tile.seq * a.span, tiles = g.to - g.from;
+      auto copy = [&](int32_t x0, int32_t y0, int32_t x1, int32_t y1) {
+        const uint32_t slot = n % kSlots, bar = dsmem_addr(&sh.full[slot], 0);
+        if (n >= kSlots) ok = ok && wait(&sh.empty[slot], (n / kSlots - 1) & 1);
+        if (!ok) return;
+        if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kSlotBytes);
+        pair_load_box(ring + slot * kSlotBytes, &vmap, x0, y0, bar);
+        pair_load_box(ring + slot * kSlotBytes + kSlotBytes / 2, &vmap, x1, y1, bar);
+        ++n;
+      };
+      for (uint32_t i = 0; i <= tiles && ok; ++i) {
+        const int32_t row = (int32_t)(base + (g.from + i) * kSpan), mine = row + (int32_t)rank * 128;
+        if (i < tiles)
+          for (int32_t k = 0; k < 9; ++k) copy(64 * k, mine, 64 * k, mine + 64);
+        if (i > 0 && !max_only)
+          for (int32_t k = 0; k < 8; ++k) {
+            const int32_t x = (k / 4) * 256 + (int32_t)rank * 128, y = row - (int32_t)kSpan + (k % 4) * 64;
+            copy(x, y, x + 64, y);
+          }
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    return ok;
+  };
+
+  auto multiply = [&](const Segment& g, bool max_only) -> bool {
+    constexpr uint32_t kQk = pair_desc(1, kTileColumns, false, false), kPv = pair_desc(1, kTileColumns, true, true);
+    const uint64_t q_desc = tile_desc(queries, 16), k_desc = tile_desc(ring, 16);
+    const uint64_t p_desc = tile_desc(probs, 16), v_desc = tile_desc(ring, kSlotBytes / 2);
+    const uint32_t tiles = g.to - g.from;
+    ok = ok && wait(&sh.q_full, q_n & 1);
+    ++q_n;
+    for (uint32_t i = 0; i <= tiles && __all_sync(0xffffffffu, ok); ++i) {
+      if (i < tiles) {
+        const uint32_t buf = it & 1, d = tmem + 256 + buf * kTileColumns;
+        if (it >= 2) ok = wait(&sh.s_empty[buf], ((it >> 1) - 1) & 1);
+        for (uint32_t k = 0; k < 9; ++k, ++n) {
+          const uint32_t slot = n % kSlots;
+          ok = ok && wait(&sh.full[slot], n / kSlots & 1);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+              pair_mma_bf16(d, k_desc + slot * (kSlotBytes >> 4) + 2 * e, q_desc + k * (kColumns * 128 >> 4) + 2 * e, kQk,
+                            k + e > 0);
+            pair_commit(&sh.empty[slot], 3);
+            if (k == 8) {
+              pair_commit(&sh.s_full[buf], 3);
+              if (i + 1 == tiles) pair_commit(&sh.q_empty, 3);
+            }
+          }
+          __syncwarp();
+        }
+        ++it;
+      }
+      if (i > 0 && !max_only) {
+        ok = wait(&sh.p_full, pv & 1);
+        if (i == 1 && full_n > 0) ok = ok && wait(&sh.o_empty, (full_n - 1) & 1);
+        fence_proxy_async();
+        for (uint32_t k = 0; k < 8; ++k, ++n) {
+          const uint32_t slot = n % kSlots;
+          ok = ok && wait(&sh.full[slot], n / kSlots & 1);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+              pair_mma_bf16(tmem + (k / 4) * kTileColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
+                            p_desc + (k % 4) * 512 + 128 * e, kPv, i > 1 || k % 4 + e > 0);
+            pair_commit(&sh.empty[slot], 3);
+            if (k == 7) pair_commit(&sh.p_empty, 3);
+          }
+          __syncwarp();
+        }
+        ++pv;
+      }
+    }
+    if (!max_only) ++full_n;
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  // A worker's position of a tile: rank * 128 + quad * 32 + lane; its columns: quarter * 32 + c.
+  const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3, mine = rank * 128 + quad * 32 + lane;
+  const uint32_t lanes = tmem + (quad << 21);
+  auto arrive0 = [&](uint64_t* bar) {                    // at rank 0's barrier, for the warp
+    __syncwarp();
+    if (lane == 0) cluster_mbar_arrive(dsmem_addr(bar, 0));
+  };
+  // the maxima of this warp's columns (lane c: column c's) to both CTAs, and back the whole tile's
+  auto meet = [&](float best) -> float {
+    sh.top[rank][quarter][quad][lane] = best;
+    dsmem_st_u32(dsmem_addr(&sh.top[rank][quarter][quad][lane], rank ^ 1), __float_as_uint(best));
+    __syncwarp();
+    if (lane == 0) {
+      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 0));
+      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 1));
+    }
+    ok = ok && wait(&sh.met[quarter], met_n & 1);
+    ++met_n;
+    float m = -INFINITY;
+    for (uint32_t r = 0; r < 2; ++r)
+      for (uint32_t w = 0; w < 4; ++w) m = fmaxf(m, ((volatile float*)sh.top[r][quarter][w])[lane]);
+    return m;
+  };
+
+  // first: the references are still to be found
+  auto soften = [&](const Segment& g, bool max_only, bool first) -> bool {
+    uint32_t at;
+    const uint32_t token = column_at(a, g.tile, 2 * g.tile.index + quarter / 2, quarter % 2 * 32 + lane, &at);
+    const bool real = token < g.tile.tokens;
+    const uint32_t sees = real ? visible(a, g.tile.before, token) : UINT32_MAX;   // (others hold nothing up)
+    const uint32_t least = __reduce_min_sync(0xffffffffu, sees);
+    __syncwarp();
+    sh.seen[quarter][lane] = sees;
+    __syncwarp();
+    // (what a column that is none multiplies may be anything: its weights are zeros, or NaN for itself alone)
+    auto reference = [&](float best) { return !real ? INFINITY : fabsf(best) < INFINITY ? best : 0.0f; };
+    float sum[32];                                       // or maxima
+#pragma unroll
+    for (uint32_t c = 0; c < 32; ++c) sum[c] = max_only ? -INFINITY : 0.0f;
+    uint32_t flagged = 0;
+    const float* const off = a.off + (int64_t)g.tile.seq * a.span;
+    for (uint32_t i = g.from; i < g.to; ++i, ++it) {
+      const uint32_t p = i * kSpan + mine;
+      const bool gone = __ldcg(off + p) != 0.0f;
+      ok = ok && wait(&sh.s_full[it & 1], it >> 1 & 1);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      tc_fence_after();
+      float x[32];
+      tmem_ld32(lanes + 256 + (it & 1) * kTileColumns + quarter * 32, x);
+      tmem_ld_wait();
+      tc_fence_before();
+      arrive0(&sh.s_empty[it & 1]);
+      const bool edge = __any_sync(0xffffffffu, gone) || (i + 1) * kSpan > least;
+      float scale = a.scale;
+      if (edge) {
+        scale = 1.0f;
+#pragma unroll
+        for (uint32_t c = 0; c < 32; ++c) x[c] = gone || p >= sh.seen[quarter][c] ? -INFINITY : x[c] * a.scale;
+      }
+      if (max_only) {
+#pragma unroll
+        for (uint32_t c = 0; c < 32; ++c) sum[c] = fmaxf(sum[c], x[c] * scale);
+        continue;
+      }
+      if (first && i == g.from) {
+        float best = -INFINITY;
+#pragma unroll
+        for (uint32_t c = 0; c < 32; ++c) {
+          float m;
+          asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c] * scale));
+          if (lane == c) best = m;
+        }
+        best = meet(best);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const bool unset = !(fabsf(best) < INFINITY);
+        sh.ref[quarter][lane] = reference(best);
+        flagged = __any_sync(0xffffffffu, unset && real && sees > (i + 1) * kSpan);
+        __syncwarp();
+      }
+      float most = -INFINITY;
+#pragma unroll
+      for (uint32_t c = 0; c < 32; ++c) {
+        x[c] = fmaf(x[c], scale, -sh.ref[quarter][c]);
+        most = fmaxf(most, x[c]);
+      }
+      flagged |= most > kFar;
+      // The weights are rounded to bf16 for the second product (half a step is
+      // 2^-8 of a weight); their sum takes them before that, in fp32.
+      uint32_t w[16];
+#pragma unroll
+      for (uint32_t c = 0; c < 32; c += 2) {
+        const float u = exp2_approx(x[c]), v = exp2_approx(x[c + 1]);
+        sum[c] += u;
+        sum[c + 1] += v;
+        w[c / 2] = bf16_pair(u, v);
+      }
+      if (pv > 0) ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      const uint32_t to = quarter >> 1;                  // the CTA whose columns they are
+#pragma unroll
+      for (uint32_t c = 0; c < 4; ++c) {
+        const uint32_t dst = probs + swizzled(mine, (quarter & 1) * 4 + c);
+        const uint4 v = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        if (to == rank) {
+          sts16(dst, v);
+        } else {
+          uint32_t remote;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(dst), "r"(to));
+          dsmem_st_v4(remote, v);
+        }
+      }
+      fence_proxy_async();
+      arrive0(&sh.p_full);
+      ++pv;
+    }
+    if (max_only) {
+      float best = -INFINITY;
+#pragma unroll
+      for (uint32_t c = 0; c < 32; ++c) {
+        float m;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(sum[c]));
+        if (lane == c) best = m;
+      }
+      best = meet(best);
+      sh.ref[quarter][lane] = reference(best);
+      __syncwarp();
+      return __all_sync(0xffffffffu, ok);
+    }
+
+    // the sums of both CTAs' positions, and whether the segment stands
+    add_lanes<32, 16>(sum, lane);
+    flagged = first && __any_sync(0xffffffffu, flagged);
+    sh.sums[rank][quarter][quad][lane] = sum[0];
+    dsmem_st_u32(dsmem_addr(&sh.sums[rank][quarter][quad][lane], rank ^ 1), __float_as_uint(sum[0]));
+    if (lane == 0) {
+      sh.flag[rank][warp] = flagged;
+      dsmem_st_u32(dsmem_addr(&sh.flag[rank][warp], rank ^ 1), flagged);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      cluster_mbar_arrive(dsmem_addr(&sh.agreed, 0));
+      cluster_mbar_arrive(dsmem_addr(&sh.agreed, 1));
+    }
+    const float ref = sh.ref[quarter][lane];
+    ok = ok && wait(&sh.agreed, full_n & 1);
+    ++full_n;
+    ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    const bool again = __any_sync(0xffffffffu, ((volatile uint32_t*)&sh.flag[0][0])[lane] != 0);
+    float total = 0.0f;
+    for (uint32_t r = 0; r < 2; ++r)
+      for (uint32_t q = 0; q < 4; ++q) total += ((volatile float*)sh.sums[r][quarter][q])[lane];
+    const uint32_t slot = g.slot(pair);
+    if (again) {
+      if (tid == 0) {
+        a.again[g.note(a, pair)] = 1;                    // (both CTAs write it)
+        sh.redo = 1;
+      }
+    } else {
+      const float lse2 = total == 0.0f ? -INFINITY : ref + log2f(total);
+      if (quad == 0 && rank == 0) {
+        if (!g.whole)
+          a.part_lse[slot * kTileColumns + quarter * 32 + lane] = lse2;
+        else if (real && a.lse)
+          a.lse[(int64_t)g.tile.first * a.heads + at] = lse2 * 0.6931471805599453f;
+      }
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      const uint32_t place = real ? at : UINT32_MAX;     // where the column's result goes
+#pragma unroll
+      for (uint32_t half = 0; half < 2; ++half) {
+        float o[32];
+        tmem_ld32(lanes + half * kTileColumns + quarter * 32, o);
+        tmem_ld_wait();
+        const uint32_t d = half * 256 + rank * 128 + quad * 32 + lane;
+        if (g.whole) {
+          __nv_bfloat16* const out =
+              reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)g.tile.first * a.heads * KVO_LATENT_BYTES + d;
+#pragma unroll
+          for (uint32_t c = 0; c < 32; ++c) {
+            const uint32_t to = __shfl_sync(0xffffffffu, place, c);
+            const float by = __shfl_sync(0xffffffffu, inv, c);
+            if (to != UINT32_MAX) out[(int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+          }
+        } else {
+          float* const out = a.part + ((int64_t)slot * kTileColumns + quarter * 32) * KVO_LATENT_BYTES + d;
+#pragma unroll
+          for (uint32_t c = 0; c < 32; ++c) out[c * KVO_LATENT_BYTES] = o[c] * __shfl_sync(0xffffffffu, inv, c);
+        }
+      }
+    }
+    tc_fence_before();
+    arrive0(&sh.o_empty);
+    return true;
+  };
+
+  // All segments, then those that need another pass: their columns' maxima,
+  // and the whole of it with them.
+  for (uint32_t round = 0; round < 2; ++round) {
+    for_segments(a, begin, end, tile0, [&](const Segment& g) -> bool {
+      if (round && !__ldcg(a.again + g.note(a, pair))) return true;
+      for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
+        const bool max_only = pass == 0;
+        if (!(warp < kWorkers    ? soften(g, max_only, !round)
+              : warp == kLoader  ? load(g, max_only)
+              : rank == 0        ? multiply(g, max_only)
+                                 : true))
+          return false;
+      }
+      return true;
+    });
+    ok = __all_sync(0xffffffffu, ok);
+    __threadfence();
+    __syncthreads();
+    cluster_sync();
+    // the same answer in both CTAs: nothing changes between the barriers
+    const uint32_t redo = sh.redo | dsmem_ld_u32(dsmem_addr(&sh.redo, rank ^ 1));
+    const uint32_t gave_up = sh.gave_up | dsmem_ld_u32(dsmem_addr(&sh.gave_up, rank ^ 1));
+    __syncthreads();
+    cluster_sync();
+    if (!redo || gave_up) break;
+  }
+
+  // no slot's release may still be on its way when the CTA ends
+  if (warp == kLoader && lane == 0) {
+    for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
+    if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
+    for (uint32_t r = 0; r < 2; ++r) {
+      dsmem_st_u32(dsmem_addr(&sh.issued[rank], r), n);
+      dsmem_st_u32(dsmem_addr(&sh.q_issued[rank], r), q_n);
+    }
+  }
+  // Both CTAs end together.  Where a wait gave up in either, what is in flight
+  // finishes first: the MMAs, then the copies; a copy that only one CTA has
+  // started counts as come for the other.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  const uint32_t other_gave_up = dsmem_ld_u32(dsmem_addr(&sh.gave_up, rank ^ 1));
+  if (sh.gave_up | other_gave_up) {
+    if (tid == 0) atomicOr(a.status, kFlagTimeout);
+    if (rank == 0 && warp == kMma && elect_one()) {
+      pair_commit(&sh.drained, 1);
+      if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
+    }
+    if (rank == 0 && warp == kLoader && lane == 0) {
+      auto even = [&](uint64_t* bar, bool here, bool there, uint32_t bytes) {
+        if (!here) mbar_arrive_expect_tx(bar, 2 * bytes);
+        if (!here || !there) mbar_complete_tx(bar, bytes);
+      };
+      const uint32_t most = max(sh.issued[0], sh.issued[1]), least = min(sh.issued[0], sh.issued[1]);
+      for (uint32_t m = least; m < most; ++m) even(&sh.full[m % kSlots], m < sh.issued[0], m < sh.issued[1], kSlotBytes);
+      for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
+        if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
+      const uint32_t queried = max(sh.q_issued[0], sh.q_issued[1]);
+      if (sh.q_issued[0] != sh.q_issued[1])
+        even(&sh.q_full, sh.q_issued[0] == queried, sh.q_issued[1] == queried, 9 * box);
+      if (queried && !landed(&sh.q_full, (queried - 1) & 1)) atomicOr(a.status, kFlagInflight);
+    }
+    __syncthreads();
+  }
+  cluster_sync();
+  if (warp == kMma) pair_tmem_free(tmem, 512);
+}
+
+// A tile that shares' ends cut: block (g - 1, column) joins its parts if share
+// g is the first to begin inside it.
+__global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
+  const uint32_t g = blockIdx.x + 1, column = blockIdx.y, d = threadIdx.x;
+  wait_previous_grid();
+  const Shares shares(a);
+  if (g >= shares.pairs) return;
+  const uint64_t at = shares.from(g);
+  if (at >= shares.units) return;
+  const uint32_t tile = tile_of(a, at);
+  const PlanTile t = plan_tile(a, tile);
+  const uint64_t end = __ldcg(&a.plan[tile + 1].units);
+  if (at == t.units || shares.from(g - 1) > t.units) return;
+  uint32_t where;
+  const uint32_t token = column_at(a, t, 2 * t.index + column / kColumns, column % kColumns, &where);
+  if (token >= t.tokens) return;
+  uint32_t last = g;                                     // the last share that begins inside the tile
+  while (last + 1 < shares.pairs && shares.from(last + 1) < end) ++last;
+  // parts: of share g - 1 the one that ends inside, of the others the one that begins there
+  auto slot = [&](uint32_t p) { return 2 * p + (p == g - 1); };
+  float top = -INFINITY;
+  for (uint32_t p = g - 1; p <= last; ++p) top = fmaxf(top, __ldcg(a.part_lse + slot(p) * kTileColumns + column));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (uint32_t p = g - 1; p <= last; ++p) {
+    const uint32_t from = slot(p) * kTileColumns + column;
+    const float w = exp2f(__ldcg(a.part_lse + from) - base);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)from * KVO_LATENT_BYTES) + d);
+    if (!(w > 0.0f) && !isnan(w)) continue;
+    total += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t row = (int64_t)t.first * a.heads + where;
+  reinterpret_cast<uint2*>(a.out + row * KVO_LATENT_BYTES)[d] =
+      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+  if (a.lse && d == 0) a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ the host
+// Whether a call has enough columns a sequence.
+bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
+  const int64_t busy = sequences < tokens ? sequences : tokens;
+  const int64_t span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
+  return tokens * heads >= 256 * busy && sequences * span <= INT32_MAX;
+}
+
+struct Layout {              // of the scratch
+  int64_t span, tiles, pairs;
+  int64_t values, off, plan, again, part, part_lse, bytes;
+};
+
+Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
+  Layout l;
+  l.span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
+  l.pairs = device_sms() / 2;
+  // Tiles of either way to fill them: at worst 33 heads of one token a half.
+  const int64_t busy = sequences < tokens ? sequences : tokens;
+  const int64_t deep = heads < kColumns ? kColumns / heads : 1, across = heads > kColumns ? 2 : 1;
+  const int64_t halves = (tokens + busy * (deep - 1)) / deep * across;
+  const int64_t flat = (tokens * heads + busy * (kColumns - 1)) / kColumns;
+  l.tiles = ((halves > flat ? halves : flat) + busy + 1) / 2;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t from = at;
+    at += (bytes + 255) / 256 * 256;
+    return from;
+  };
+  l.values = take(sequences * l.span * kValueBytes);
+  l.off = take(sequences * l.span * 4);
+  l.plan = take((l.tiles + 2) * (int64_t)sizeof(PlanTile));
+  l.again = take(l.tiles + 2 * l.pairs);
+  l.part = take(2 * l.pairs * kTileColumns * KVO_LATENT_BYTES * 4);
+  l.part_lse = take(2 * l.pairs * kTileColumns * 4);
+  l.bytes = at;
+  return l;
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& qmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!ready[dev & 63]) {
+    e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev & 63] = true;
+  }
+  e = launch_early(unpack_kernel, dim3(1 + a.unpack_blocks * a.cache.sequences), kUnpackThreads, 0, stream, a);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3(2 * a.pairs);
+  lc.blockDim = dim3(kChunkThreads);
+  lc.dynamicSmemBytes = kChunkSmem;
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, vmap);
+  if (e != cudaSuccess || a.pairs < 2) return e;
+  return launch_early(join_parts_kernel, dim3(a.pairs - 1, kTileColumns), 128, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace kvo
+
+extern "C" int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows) {
+  using namespace kvo;
+  if (tokens < 0 || tokens > KVO_MAX_QUERIES || sequences < 1 || sequences > KVO_MAX_QUERIES) return -1;
+  if (heads < 1 || heads > KVO_MAX_HEADS || rows < 0 || rows > INT32_MAX - 255) return -1;
+  if (tokens == 0) return 0;
+  return many_columns(tokens, sequences, (uint32_t)heads, rows) ? layout_of(tokens, sequences, (uint32_t)heads, rows).bytes
+                                                                : few_columns_work(tokens, sequences, (uint32_t)heads, rows);
+}
+
+extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, const kvo_chunk_query* s, void* stream) {
+  using namespace kvo;
+  uint32_t* status = nullptr;
+  if (!ctx || !cache_ok(cache) || !s || !cache_rows_ok(cache)) return KVO_EINVAL;
+  const int64_t need = kvo_attend_chunk_work_bytes(s->tokens, cache->sequences, s->heads, s->rows);
+  if (need < 0 || !s->starts || !s->lens || !std::isfinite(s->scale)) return KVO_EINVAL;
+  if (!aligned(s->starts, 4) || !aligned(s->lens, 4)) return KVO_EINVAL;
+  if (s->tokens > 0) {
+    if (!s->q || !s->out || s->work_bytes < need || (need && !s->work)) return KVO_EINVAL;
+    if (!query_ok(s->q, s->q_ld, s->q_head_ld, s->tokens, s->heads) || !aligned(s->out, 16)) return KVO_EINVAL;
+    if (!aligned(s->lse, 4) || !aligned(s->work, 16)) return KVO_EINVAL;
+  }
+  int64_t wait_clocks = 0;
+  const kvo_status st = usable_status(ctx, &status, &wait_clocks);
+  if (st != KVO_OK) return st;
+  if (s->tokens == 0) return KVO_OK;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (!many_columns(s->tokens, cache->sequences, (uint32_t)s->heads, s->rows))
+    return launch_few_columns(*cache, *s, status, wait_clocks, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
+
+  const Layout l = layout_of(s->tokens, cache->sequences, (uint32_t)s->heads, s->rows);
+  uint8_t* const work = static_cast<uint8_t*>(s->work);
+  ChunkArgs a = {};
+  a.cache = cache_view(*cache);
+  a.starts = s->starts;
+  a.lens = s->lens;
+  a.out = s->out;
+  a.lse = s->lse;
+  a.values = work + l.values;
+  a.off = reinterpret_cast<float*>(work + l.off);
+  a.plan = reinterpret_cast<PlanTile*>(work + l.plan);
+  a.again = work + l.again;
+  a.part = reinterpret_cast<float*>(work + l.part);
+  a.part_lse = reinterpret_cast<float*>(work + l.part_lse);
+  a.status = status;
+  a.rows = (uint32_t)s->rows;
+  a.span = (uint32_t)l.span;
+  a.tokens = (uint32_t)s->tokens;
+  a.heads = (uint32_t)s->heads;
+  a.most_tiles = (uint32_t)l.tiles;
+  a.pairs = (uint32_t)l.pairs;
+  a.unpack_blocks = (uint32_t)(l.span / kUnpackRows);
+  a.by_heads = divider(a.heads);
+  a.scale = s->scale * kLog2e;
+  a.wait_clocks = wait_clocks;
+  // a dimension of one has no next element: its stride says nothing
+  const int64_t head_ld = a.heads > 1 ? s->q_head_ld : KVO_DEQUANT_VALUES;
+  const int64_t q_ld = s->tokens > 1 ? s->q_ld : a.heads * head_ld;
+  a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens);
+  CUtensorMap qmap, vmap;
+  if (!query_map(&qmap, s->q, a.heads, s->tokens, q_ld * 2, head_ld * 2, a.columns) ||
+      !value_map(&vmap, a.values, cache->sequences * l.span))
+    return KVO_ECUDA;
+  return launch_chunk(a, qmap, vmap, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
+}

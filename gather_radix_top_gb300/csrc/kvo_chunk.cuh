@@ -81,9 +81,7 @@ inline Columns columns_of(uint32_t heads, int64_t q_ld, int64_t q_head_ld, int64
   return c;
 }
 
-// The queries as boxes of 64 values of a tile's columns; strides in bytes.
-inline bool query_map(CUtensorMap* map, const void* q, uint32_t heads, int64_t tokens, int64_t q_ld, int64_t q_head_ld,
-                      const Columns& c) {
+inline decltype(&cuTensorMapEncodeTiled) map_encoder() {
   static const auto encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
@@ -94,6 +92,13 @@ inline bool query_map(CUtensorMap* map, const void* q, uint32_t heads, int64_t t
     }
     return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
   }();
+  return encode;
+}
+
+// The queries as boxes of 64 values of a tile's columns; strides in bytes.
+inline bool query_map(CUtensorMap* map, const void* q, uint32_t heads, int64_t tokens, int64_t q_ld, int64_t q_head_ld,
+                      const Columns& c) {
+  const auto encode = map_encoder();
   if (!encode) return false;
   const cuuint64_t size[3] = {KVO_DEQUANT_VALUES, c.flat ? 1 : (cuuint64_t)heads,
                               (cuuint64_t)(c.flat ? tokens * heads : tokens)};
@@ -102,6 +107,24 @@ inline bool query_map(CUtensorMap* map, const void* q, uint32_t heads, int64_t t
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), size, pitch, box, every,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Unpacked rows as boxes of 64 values of 64 rows.
+inline bool value_map(CUtensorMap* map, const void* values, int64_t rows) {
+  const auto encode = map_encoder();
+  if (!encode) return false;
+  const cuuint64_t size[2] = {KVO_DEQUANT_VALUES, (cuuint64_t)rows}, pitch[1] = {KVO_DEQUANT_VALUES * 2};
+  const cuuint32_t box[2] = {64, 64}, every[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(values), size, pitch, box, every,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries that query_map can describe; strides in elements.
+inline bool query_ok(const void* q, int64_t q_ld, int64_t q_head_ld, int64_t tokens, int64_t heads) {
+  if (!q || !aligned(q, 16) || q_ld % 8 || q_head_ld % 8) return false;
+  if (tokens > 1 && (q_ld < KVO_DEQUANT_VALUES || q_ld >= kMaxQueryLd)) return false;
+  return heads <= 1 || (q_head_ld >= KVO_DEQUANT_VALUES && q_head_ld < kMaxQueryLd);
 }
 
 }  // namespace kvo

@@ -397,9 +397,7 @@ extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache
   if (need < 0 || !s->starts || !s->lens || !std::isfinite(s->scale) || !std::isfinite(s->keep)) return KVO_EINVAL;
   if (!aligned(s->starts, 4) || !aligned(s->lens, 4) || !aligned(s->lse, 4)) return KVO_EINVAL;
   if (s->tokens > 0) {
-    if (!s->q || !s->lse || !aligned(s->q, 16) || s->q_ld % 8 || s->q_head_ld % 8) return KVO_EINVAL;
-    if (s->tokens > 1 && (s->q_ld < KVO_DEQUANT_VALUES || s->q_ld >= kMaxQueryLd)) return KVO_EINVAL;
-    if (s->heads > 1 && (s->q_head_ld < KVO_DEQUANT_VALUES || s->q_head_ld >= kMaxQueryLd)) return KVO_EINVAL;
+    if (!s->lse || !query_ok(s->q, s->q_ld, s->q_head_ld, s->tokens, s->heads)) return KVO_EINVAL;
   }
   if (s->rows > 0) {
     if (!s->out || !aligned(s->out, 4) || !aligned(s->carry, 4)) return KVO_EINVAL;

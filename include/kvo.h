@@ -697,14 +697,15 @@ int64_t kvo_attend_work_bytes(int64_t nq, int32_t heads, int64_t positions);
  * to the positions its token sees, with the same formulas and numerics; one
  * that sees none gets out = 0 and lse = -inf.
  *   q       device bf16 [tokens][heads][576]; heads q_head_ld elements apart,
- *           tokens q_ld; every head 16-byte aligned.
+ *           tokens q_ld, every head 16-byte aligned; where there are several,
+ *           each at least 576 and below 2^38 elements apart.
  *   out     device bf16 [tokens][heads][512], contiguous, 16-byte aligned.
  *   lse     device fp32 [tokens][heads], or NULL.
  *   work    device scratch of kvo_attend_chunk_work_bytes' size (16-byte
  *           aligned), or NULL when that is 0; free again once the call's work
  *           is done.
- * KVO_EINVAL for a NULL or misaligned argument that tokens > 0 needs, tokens
- * or sequences above KVO_MAX_QUERIES, heads outside 1 .. KVO_MAX_HEADS, rows
+ * KVO_EINVAL for a NULL or misaligned argument that tokens > 0 needs, a bad
+ * stride, tokens or sequences above KVO_MAX_QUERIES, heads outside 1 .. KVO_MAX_HEADS, rows
  * < 0 or > 2^31 - 256, a scale that is not finite, too little work space, or
  * a cache without rows.
  */
@@ -739,9 +740,7 @@ int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t h
  * kvo_attend_chunk (or kvo_attend) these are the softmax weights.  A (token,
  * head) whose lse is -inf adds nothing, nor does a position without a row (it
  * latches KVO_ERANGE); carry counts all the same.
- *   q       device bf16 [tokens][heads][576], as for kvo_attend_chunk; where
- *           there are several, heads are at least 576 and below 2^38 elements
- *           apart, and so are tokens.
+ *   q       device bf16 [tokens][heads][576], as for kvo_attend_chunk.
  *   lse     device fp32 [tokens][heads].
  *   carry   device fp32, sequence s's at carry + s * carry_ld, or NULL (0).
  *   out     device fp32, sequence s's `rows` values at out + s * out_ld; may

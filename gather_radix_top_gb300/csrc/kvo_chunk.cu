@@ -11,11 +11,13 @@
 // 512 columns of tensor memory and S^T, twice, the rest.  The columns' operand
 // is halved between them: 64 columns of queries (72 KB) and of weights (32 KB
 // for 256 positions) lie in each CTA's shared memory; the positions' operands
-// stream through a ring of seven pieces of 16 KB (128 positions of 64 values
+// stream through a ring of six pieces of 16 KB (128 positions of 64 values
 // for the first product, 64 positions of 128 values for the second).
 //
-// Sixteen worker warps do the softmax: a lane of S^T is a position.  A CTA
-// writes the weights of the other's 64 columns to the other's shared memory.
+// Sixteen worker warps do the softmax: a lane of S^T is a position.  The
+// weights of the other CTA's 64 columns go to it as one bulk copy (16 KB);
+// stored there directly they took 3,700 clocks a tile, most of them in the
+// fence before the MMAs.
 // The softmax's reference is the column's maximum in the first tile of
 // positions.  Weights of up to 2^64 lose nothing in fp32 and bf16; where a
 // later logit lies further above, or the first tile shows a column nothing and
@@ -45,9 +47,9 @@ constexpr uint32_t kWorkers = 16;
 constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
 constexpr uint32_t kChunkThreads = (kLoader + 1) * 32;
 constexpr uint32_t kQueryBytes = 9 * kColumns * 128;
-constexpr uint32_t kWeightBytes = kSpan * 128;
-constexpr uint32_t kSlotBytes = 16384, kSlots = 7;
-constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + kWeightBytes + kSlots * kSlotBytes;
+constexpr uint32_t kHalfBytes = kSpan / 2 * 128;         // a CTA's positions' weights of 64 columns
+constexpr uint32_t kSlotBytes = 16384, kSlots = 6;
+constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + 3 * kHalfBytes + kSlots * kSlotBytes;
 constexpr uint32_t kValueBytes = KVO_DEQUANT_VALUES * 2;
 constexpr float kFar = 64.0f;                            // in powers of two
 
@@ -312,10 +314,11 @@ __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin,
 }
 
 struct ChunkShared {
-  uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_empty, o_empty, met[4], agreed,
-      drained;
+  uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_come, p_empty, o_empty, given,
+      met[4], agreed, drained;
   uint32_t tmem, gave_up;
   uint32_t issued[2], q_issued[2];   // copies that each CTA's loader has started
+  uint32_t gifts, armed;             // weights that the other CTA has sent, and that this one has been ready for
   uint32_t redo;                     // some segment needs another pass
   uint32_t flag[2][kWorkers];        // per warp of both CTAs: this segment does
   float top[2][4][4][32];            // per CTA, quarter of the columns and warp: maxima
@@ -346,7 +349,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __shared__ ChunkShared sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
   const uint32_t pair = blockIdx.x >> 1;
-  const uint32_t queries = (smem_u32(raw) + 1023u) & ~1023u, probs = queries + kQueryBytes, ring = probs + kWeightBytes;
+  const uint32_t queries = (smem_u32(raw) + 1023u) & ~1023u, probs = queries + kQueryBytes;
+  const uint32_t gift = probs + 2 * kHalfBytes, ring = gift + kHalfBytes;
 
   if (tid == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
@@ -360,7 +364,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.s_empty[i], 2 * kWorkers);
       sh.issued[i] = sh.q_issued[i] = 0;
     }
-    mbar_init(&sh.p_full, 2 * kWorkers);
+    mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns; rank 1 has the others of its own
+    mbar_init(&sh.p_come, 1);
+    mbar_init(&sh.given, kWorkers / 2);
+    sh.gifts = sh.armed = 0;
     mbar_init(&sh.p_empty, 1);
     mbar_init(&sh.o_empty, 2 * kWorkers);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.met[i], 8);
@@ -379,6 +386,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   allow_next_grid();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+  };
+  auto cluster_wait = [&](uint64_t* bar, uint32_t parity) -> bool {   // where the other CTA has written
     return cluster_wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
   const Shares shares(a);
@@ -390,6 +400,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t n = 0, q_n = 0;                               // copies; segments' queries
   uint32_t it = 0, pv = 0;                               // tiles of S; second products
   uint32_t full_n = 0, met_n = 0;                        // whole passes; exchanges of maxima
+  uint32_t gifts = 0;
   bool ok = true;
 
   // One segment's work for each role; max_only: only the columns' maxima.
@@ -430,69 +441,100 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return ok;
   };
 
+  // the weights that the other CTA sends, the p-th of them; one thread
+  auto come = [&](uint32_t p) -> bool {
+    mbar_arrive_expect_tx(&sh.p_come, kHalfBytes);
+    sh.armed = p + 1;
+    return wait(&sh.p_come, p & 1);
+  };
+
+  // One thread issues all of a segment's MMAs: what it does between them has
+  // to fit into the 256 clocks that four take, beside the workers' instructions.
+  // (Waits of the whole warp, with a vote, a fence and an election for every
+  // four: 430 clocks.)
   auto multiply = [&](const Segment& g, bool max_only) -> bool {
     constexpr uint32_t kQk = pair_desc(1, kTileColumns, false, false), kPv = pair_desc(1, kTileColumns, true, true);
-    const uint64_t q_desc = tile_desc(queries, 16), k_desc = tile_desc(ring, 16);
-    const uint64_t p_desc = tile_desc(probs, 16), v_desc = tile_desc(ring, kSlotBytes / 2);
     const uint32_t tiles = g.to - g.from;
-    ok = ok && wait(&sh.q_full, q_n & 1);
-    ++q_n;
-    for (uint32_t i = 0; i <= tiles && __all_sync(0xffffffffu, ok); ++i) {
-      if (i < tiles) {
-        const uint32_t buf = it & 1, d = tmem + 256 + buf * kTileColumns;
-        if (it >= 2) ok = wait(&sh.s_empty[buf], ((it >> 1) - 1) & 1);
-        for (uint32_t k = 0; k < 9; ++k, ++n) {
-          const uint32_t slot = n % kSlots;
-          ok = ok && wait(&sh.full[slot], n / kSlots & 1);
-          if (!__all_sync(0xffffffffu, ok)) return false;
+    if (ok && elect_one()) {
+      const uint64_t q_desc = tile_desc(queries, 16), k_desc = tile_desc(ring, 16);
+      const uint64_t p_desc = tile_desc(probs, 16), v_desc = tile_desc(ring, kSlotBytes / 2);
+      uint32_t slot = n % kSlots, turn = n / kSlots & 1;
+      auto next = [&] {
+        if (++slot == kSlots) {
+          slot = 0;
+          turn ^= 1;
+        }
+      };
+      ok = wait(&sh.q_full, q_n & 1);
+      for (uint32_t i = 0, t = it, p = pv; i <= tiles && ok; ++i) {
+        if (i < tiles) {
+          const uint32_t buf = t & 1, d = tmem + 256 + buf * kTileColumns;
+          if (t >= 2) ok = wait(&sh.s_empty[buf], ((t >> 1) - 1) & 1);
           tc_fence_after();
-          if (elect_one()) {
+#pragma unroll 3
+          for (uint32_t k = 0; k < 9 && ok; ++k, next()) {
+            ok = wait(&sh.full[slot], turn);
+            if (!ok) break;
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e)
               pair_mma_bf16(d, k_desc + slot * (kSlotBytes >> 4) + 2 * e, q_desc + k * (kColumns * 128 >> 4) + 2 * e, kQk,
                             k + e > 0);
             pair_commit(&sh.empty[slot], 3);
-            if (k == 8) {
-              pair_commit(&sh.s_full[buf], 3);
-              if (i + 1 == tiles) pair_commit(&sh.q_empty, 3);
-            }
           }
-          __syncwarp();
+          if (!ok) break;
+          pair_commit(&sh.s_full[buf], 3);
+          if (i + 1 == tiles) pair_commit(&sh.q_empty, 3);
+          ++t;
         }
-        ++it;
-      }
-      if (i > 0 && !max_only) {
-        ok = wait(&sh.p_full, pv & 1);
-        if (i == 1 && full_n > 0) ok = ok && wait(&sh.o_empty, (full_n - 1) & 1);
-        fence_proxy_async();
-        for (uint32_t k = 0; k < 8; ++k, ++n) {
-          const uint32_t slot = n % kSlots;
-          ok = ok && wait(&sh.full[slot], n / kSlots & 1);
-          if (!__all_sync(0xffffffffu, ok)) return false;
+        if (i > 0 && !max_only) {
+          ok = come(p) && cluster_wait(&sh.p_full, p & 1);
+          if (i == 1 && full_n > 0) ok = ok && wait(&sh.o_empty, (full_n - 1) & 1);
           tc_fence_after();
-          if (elect_one()) {
+#pragma unroll 4
+          for (uint32_t k = 0; k < 8 && ok; ++k, next()) {
+            ok = wait(&sh.full[slot], turn);
+            if (!ok) break;
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e)
               pair_mma_bf16(tmem + (k / 4) * kTileColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
                             p_desc + (k % 4) * 512 + 128 * e, kPv, i > 1 || k % 4 + e > 0);
             pair_commit(&sh.empty[slot], 3);
-            if (k == 7) pair_commit(&sh.p_empty, 3);
           }
-          __syncwarp();
+          if (!ok) break;
+          pair_commit(&sh.p_empty, 3);
+          ++p;
         }
-        ++pv;
       }
     }
-    if (!max_only) ++full_n;
-    return __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
+    ++q_n;
+    n += tiles * (max_only ? 9 : 17);
+    it += tiles;
+    if (!max_only) {
+      pv += tiles;
+      ++full_n;
+    }
+    return ok;
+  };
+
+  // rank 1's warp without MMAs tells rank 0 when its weights have come
+  auto pass_on = [&](const Segment& g, bool max_only) -> bool {
+    for (uint32_t i = g.from; i < g.to && !max_only; ++i, ++pv) {
+      if (lane == 0) {
+        ok = come(pv);
+        if (ok) cluster_mbar_arrive(dsmem_addr(&sh.p_full, 0));
+      }
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+    return true;
   };
 
   // A worker's position of a tile: rank * 128 + quad * 32 + lane; its columns: quarter * 32 + c.
   const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3, mine = rank * 128 + quad * 32 + lane;
   const uint32_t lanes = tmem + (quad << 21);
-  auto arrive0 = [&](uint64_t* bar) {                    // at rank 0's barrier, for the warp
+  auto arrive0 = [&](uint64_t* bar) {                    // at rank 0's barrier, for the warp's loads from tensor memory
     __syncwarp();
-    if (lane == 0) cluster_mbar_arrive(dsmem_addr(bar, 0));
+    if (lane == 0) cluster_mbar_arrive_relaxed(dsmem_addr(bar, 0));
   };
   // the maxima of this warp's columns (lane c: column c's) to both CTAs, and back the whole tile's
   auto meet = [&](float best) -> float {
@@ -503,7 +545,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 0));
       cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 1));
     }
-    ok = ok && wait(&sh.met[quarter], met_n & 1);
+    ok = ok && cluster_wait(&sh.met[quarter], met_n & 1);
     ++met_n;
     float m = -INFINITY;
     for (uint32_t r = 0; r < 2; ++r)
@@ -585,21 +627,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       if (pv > 0) ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      const uint32_t to = quarter >> 1;                  // the CTA whose columns they are
+      const bool own = quarter >> 1 == rank;             // this CTA's columns, or the other's
+      const uint32_t dst = own ? probs + rank * kHalfBytes : gift;
 #pragma unroll
-      for (uint32_t c = 0; c < 4; ++c) {
-        const uint32_t dst = probs + swizzled(mine, (quarter & 1) * 4 + c);
-        const uint4 v = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        if (to == rank) {
-          sts16(dst, v);
-        } else {
-          uint32_t remote;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(dst), "r"(to));
-          dsmem_st_v4(remote, v);
+      for (uint32_t c = 0; c < 4; ++c)
+        sts16(dst + swizzled(quad * 32 + lane, (quarter & 1) * 4 + c),
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (own) {
+        if (lane == 0) cluster_mbar_arrive(dsmem_addr(&sh.p_full, 0));
+      } else {
+        if (lane == 0) mbar_arrive(&sh.given);
+        if (warp % 8 == 0) {                             // the first of the eight warps with the other's columns
+          ok = ok && wait(&sh.given, pv & 1);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          if (lane == 0) {
+            uint32_t there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(probs + rank * kHalfBytes), "r"(rank ^ 1));
+            bulk_copy_s2peer(there, gift, kHalfBytes, dsmem_addr(&sh.p_come, rank ^ 1));
+            ++gifts;
+          }
         }
       }
-      fence_proxy_async();
-      arrive0(&sh.p_full);
       ++pv;
     }
     if (max_only) {
@@ -631,7 +681,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       cluster_mbar_arrive(dsmem_addr(&sh.agreed, 1));
     }
     const float ref = sh.ref[quarter][lane];
-    ok = ok && wait(&sh.agreed, full_n & 1);
+    ok = ok && cluster_wait(&sh.agreed, full_n & 1);
     ++full_n;
     ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -693,7 +743,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!(warp < kWorkers    ? soften(g, max_only, !round)
               : warp == kLoader  ? load(g, max_only)
               : rank == 0        ? multiply(g, max_only)
-                                 : true))
+                                 : pass_on(g, max_only)))
           return false;
       }
       return true;
@@ -719,6 +769,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       dsmem_st_u32(dsmem_addr(&sh.q_issued[rank], r), q_n);
     }
   }
+  if (warp < kWorkers && warp % 8 == 0 && (warp >> 3) != rank && lane == 0) dsmem_st_u32(dsmem_addr(&sh.gifts, rank ^ 1), gifts);
   // Both CTAs end together.  Where a wait gave up in either, what is in flight
   // finishes first: the MMAs, then the copies; a copy that only one CTA has
   // started counts as come for the other.
@@ -731,6 +782,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (rank == 0 && warp == kMma && elect_one()) {
       pair_commit(&sh.drained, 1);
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
+    }
+    if (warp == 0 && lane == 0) {
+      for (uint32_t m = sh.armed; m < sh.gifts; ++m) mbar_arrive_expect_tx(&sh.p_come, kHalfBytes);
+      if (sh.gifts && !landed(&sh.p_come, (sh.gifts - 1) & 1)) atomicOr(a.status, kFlagInflight);
     }
     if (rank == 0 && warp == kLoader && lane == 0) {
       auto even = [&](uint64_t* bar, bool here, bool there, uint32_t bytes) {

@@ -169,6 +169,20 @@ __device__ __forceinline__ void cluster_mbar_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// The same without an order: for accesses that are complete by themselves, as
+// loads from tensor memory are once they have been waited for.
+__device__ __forceinline__ void cluster_mbar_arrive_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// `bytes` of this CTA's shared memory to another CTA's, given the cluster
+// addresses of the destination and of a barrier there that it completes on.
+__device__ __forceinline__ void bulk_copy_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // As wait_or_give_up, for a phase that threads of the other CTA complete.
 __device__ __forceinline__ bool cluster_wait_or_give_up(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up,
                                                         long long clocks) {

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   }
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return cluster_wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
   if (tid == 0) {
     mbar_init(&sh.k_full, 2 * kWorkers);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     if (rank == 0) {
       constexpr uint32_t kDesc = pair_desc(1, kTileColumns, false, false);
       const uint64_t k_tile = tile_desc(keys, 16), q_ring = tile_desc(ring, 16);
-      bool ok = wait(&sh.k_full, 0);
+      bool ok = cluster_wait_or_give_up(&sh.k_full, 0, &sh.gave_up, a.wait_clocks);
       uint32_t n = 0;
       for (uint32_t t = 0; t < run.end - run.begin && __all_sync(0xffffffffu, ok); ++t) {
         const uint32_t buf = t % kAhead;
@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const uint32_t slot = n % kSlots;
           ok = ok && wait(&sh.full[slot], n / kSlots & 1);
           if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_mbar_arrive(s_empty + buf * 8);
+      if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (uint32_t c = 0; c < 32; ++c) {

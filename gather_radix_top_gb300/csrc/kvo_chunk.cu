@@ -42,7 +42,9 @@ cudaError_t launch_few_columns(const kvo_cache& cache, const kvo_chunk_query& s,
 namespace {
 
 constexpr uint32_t kSpan = 256;                          // positions of a tile
-constexpr uint32_t kTileColumns = 2 * kColumns;
+constexpr uint32_t kPairColumns = 2 * kColumns;
+constexpr uint32_t kTileColumns = 4 * kColumns;          // of a cluster
+constexpr uint32_t kTileCost = 1;                        // of a tile of columns, in tiles of positions
 constexpr uint32_t kWorkers = 16;
 constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
 constexpr uint32_t kChunkThreads = (kLoader + 1) * 32;
@@ -51,16 +53,16 @@ constexpr uint32_t kHalfBytes = kSpan / 2 * 128;         // a CTA's positions' w
 constexpr uint32_t kSlotBytes = 16384, kSlots = 6;
 constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + 3 * kHalfBytes + kSlots * kSlotBytes;
 constexpr uint32_t kValueBytes = KVO_DEQUANT_VALUES * 2;
-constexpr float kFar = 64.0f;                            // in powers of two
+constexpr float kRoom = 32.0f;                           // of a reference above the first tile's maximum, in powers of two
 
 // One tile of columns, as the plan lists it.
 struct __align__(16) PlanTile {
-  uint64_t units;            // tiles of positions of all tiles before it
+  uint64_t units;            // work of all tiles before it: their tiles of positions and kTileCost each
   int32_t seq;
   uint32_t index;            // of its sequence's tiles
   uint32_t first, tokens;    // its sequence's tokens
   int32_t before;            // token i sees the first before + i positions
-  uint32_t pad;
+  uint32_t spans;            // its tiles of positions
 };
 
 struct ChunkArgs {
@@ -72,15 +74,16 @@ struct ChunkArgs {
   uint8_t* values;           // [sequences][span][576] bf16
   float* off;                // [sequences][span]: 0, or -inf where there is no row
   PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
-  uint8_t* again;            // [most_tiles] whole tiles, [2 * pairs] parts that need another pass
-  float* part;               // [2 * pairs][128][512]
-  float* part_lse;           // [2 * pairs][128], base 2
+  uint8_t* again;            // [most_tiles] whole tiles, [2 * clusters] parts that need another pass
+  float* part;               // [2 * clusters][256][512]
+  float* part_lse;           // [2 * clusters][256], base 2
   uint32_t* status;
-  uint32_t rows, span, tokens, heads, most_tiles, pairs;
+  uint32_t rows, span, tokens, heads, most_tiles, clusters;
   uint32_t unpack_blocks;    // of a sequence
   Divider by_heads;
   Columns columns;
   float scale;               // times log2(e)
+  float far;                 // a logit this far above its reference wants another pass
   int64_t wait_clocks;
 };
 
@@ -105,7 +108,7 @@ __device__ __forceinline__ uint32_t column_at(const ChunkArgs& a, const PlanTile
 // The last token of a tile.
 __device__ __forceinline__ uint32_t last_token(const ChunkArgs& a, uint32_t index, uint32_t tokens) {
   const Columns& c = a.columns;
-  const uint32_t rows = (2 * index + 1) / c.across * c.deep + c.deep;   // up to the tile's end
+  const uint32_t rows = (4 * index + 3) / c.across * c.deep + c.deep;   // up to the tile's end
   return min(c.flat ? divide(min(rows, tokens * a.heads) - 1, a.by_heads) : rows - 1, tokens - 1);
 }
 
@@ -118,7 +121,7 @@ __device__ void make_plan(const ChunkArgs& a) {
   const Columns& c = a.columns;
   uint32_t tiles = 0;
   uint64_t units = 0;
-  for (uint32_t i = tid; i < a.most_tiles + 2 * a.pairs; i += kUnpackThreads) a.again[i] = 0;
+  for (uint32_t i = tid; i < a.most_tiles + 2 * a.clusters; i += kUnpackThreads) a.again[i] = 0;
   for (uint32_t s0 = 0; s0 < a.cache.sequences; s0 += kUnpackThreads) {
     const uint32_t s = s0 + tid;
     uint32_t mine = 0;
@@ -128,7 +131,7 @@ __device__ void make_plan(const ChunkArgs& a) {
       first[tid] = (uint32_t)min(max(b, 0), T);
       count[tid] = (uint32_t)min(max(e, (int32_t)first[tid]), T) - first[tid];
       const uint32_t rows = c.flat ? count[tid] * a.heads : count[tid];
-      mine = ((rows + c.deep - 1) / c.deep * c.across + 1) / 2;
+      mine = ((rows + c.deep - 1) / c.deep * c.across + 3) / 4;
     }
     uint32_t incl = mine;
 #pragma unroll
@@ -158,7 +161,8 @@ __device__ void make_plan(const ChunkArgs& a) {
         t.first = first[lo];
         t.tokens = count[lo];
         t.before = min(max(a.lens[t.seq], 0), INT32_MAX - 1) - (int32_t)t.tokens + 1;
-        n = max((visible(a, t.before, last_token(a, t.index, t.tokens)) + kSpan - 1) / kSpan, 1u);
+        t.spans = max((visible(a, t.before, last_token(a, t.index, t.tokens)) + kSpan - 1) / kSpan, 1u);
+        n = t.spans + kTileCost;
       }
       uint64_t sum = n;
 #pragma unroll
@@ -248,15 +252,15 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- the shares
-// Pair g's share of the units: [share(g), share(g + 1)).
+// Cluster g's share of the work: [from(g), from(g + 1)).
 struct Shares {
   uint64_t units;
-  uint32_t pairs;
+  uint32_t clusters;
   __device__ __forceinline__ Shares(const ChunkArgs& a) {
     units = __ldcg(&a.plan[a.most_tiles + 1].units);
-    pairs = (uint32_t)min((uint64_t)a.pairs, max(units / 2, (uint64_t)1));
+    clusters = (uint32_t)min((uint64_t)a.clusters, max(units / 2, (uint64_t)1));
   }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * units / pairs : units; }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * units / clusters : units; }
 };
 
 // The tile that unit u lies in; a whole warp.
@@ -289,13 +293,13 @@ struct Segment {
   // where a segment notes that it needs another pass, and its result if it is
   // part of a tile: a share has one that begins inside a tile and one that
   // ends inside one at most
-  __device__ __forceinline__ uint32_t slot(uint32_t pair) const { return 2 * pair + (from == 0); }
-  __device__ __forceinline__ uint32_t note(const ChunkArgs& a, uint32_t pair) const {
-    return whole ? number : a.most_tiles + slot(pair);
+  __device__ __forceinline__ uint32_t slot(uint32_t cluster) const { return 2 * cluster + (from == 0); }
+  __device__ __forceinline__ uint32_t note(const ChunkArgs& a, uint32_t cluster) const {
+    return whole ? number : a.most_tiles + slot(cluster);
   }
 };
 
-// f(segment) for every segment of a pair's share, in order, in every warp.
+// f(segment) for every segment of a cluster's share, in order, in every warp.
 template <typename F>
 __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, F f) {
   if (begin >= end) return;
@@ -305,11 +309,11 @@ __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin,
     g.tile = next;
     next = plan_tile(a, tile + 1);
     g.number = tile;
-    g.from = (uint32_t)(u - g.tile.units);
-    g.to = (uint32_t)(min(next.units, end) - g.tile.units);
-    g.whole = g.from == 0 && next.units <= end;
-    u = g.tile.units + g.to;
-    if (!f(g)) return;
+    g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
+    g.to = min((uint32_t)(min(next.units, end) - g.tile.units), g.tile.spans);
+    g.whole = g.to - g.from == g.tile.spans;
+    u = next.units;
+    if (g.from < g.to && !f(g)) return;
   }
 }
 
@@ -317,10 +321,10 @@ struct ChunkShared {
   uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_come, p_empty, o_empty, given,
       met[4], agreed, drained;
   uint32_t tmem, gave_up;
-  uint32_t issued[2], q_issued[2];   // copies that each CTA's loader has started
+  uint32_t issued[4], q_issued[4];   // copies that each CTA's loader has started
   uint32_t gifts, armed;             // weights that the other CTA has sent, and that this one has been ready for
   uint32_t redo;                     // some segment needs another pass
-  uint32_t flag[2][kWorkers];        // per warp of both CTAs: this segment does
+  uint32_t flag[2][kWorkers];        // per warp of the pair: this segment does
   float top[2][4][4][32];            // per CTA, quarter of the columns and warp: maxima
   float sums[2][4][4][32];
   // per column: the softmax's reference and the positions it sees.  The four
@@ -347,24 +351,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                  const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ uint8_t raw[];
   __shared__ ChunkShared sh;
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
-  const uint32_t pair = blockIdx.x >> 1;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // ranks 2 p and 2 p + 1 are pair p: its leader, and the other
+  const uint32_t place = cluster_rank(), rank = place & 1, leader = place & 2, other = place ^ 1;
+  const uint32_t cluster = blockIdx.x >> 2;
+  const uint16_t both = (uint16_t)(3u << leader);
   const uint32_t queries = (smem_u32(raw) + 1023u) & ~1023u, probs = queries + kQueryBytes;
   const uint32_t gift = probs + 2 * kHalfBytes, ring = gift + kHalfBytes;
 
   if (tid == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], 2);                        // both pairs
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 2 * kWorkers);
-      sh.issued[i] = sh.q_issued[i] = 0;
     }
-    mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns; rank 1 has the others of its own
+    for (uint32_t i = 0; i < 4; ++i) sh.issued[i] = sh.q_issued[i] = 0;
+    mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns, and that rank 1 has all of its
     mbar_init(&sh.p_come, 1);
     mbar_init(&sh.given, kWorkers / 2);
     sh.gifts = sh.armed = 0;
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return cluster_wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
   const Shares shares(a);
-  const uint64_t begin = shares.from(pair), end = pair < shares.pairs ? shares.from(pair + 1) : begin;
+  const uint64_t begin = shares.from(cluster), end = cluster < shares.clusters ? shares.from(cluster + 1) : begin;
   const uint32_t tile0 = begin < end ? tile_of(a, begin) : 0;
   const uint32_t box = a.columns.wide * a.columns.deep * 128;
 
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (lane == 0) {
       if (q_n > 0) ok = ok && wait(&sh.q_empty, (q_n - 1) & 1);
       if (ok) {
-        const uint32_t half = 2 * g.tile.index + rank, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, 0);
+        const uint32_t half = 4 * g.tile.index + place, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, leader);
         if (rank == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
         for (uint32_t i = 0; i < 9; ++i)
           pair_load_box(queries + i * (kColumns * 128), &qmap, (int32_t)(i * 64),
@@ -416,25 +423,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         (int32_t)((a.columns.flat ? g.tile.first * a.heads : g.tile.first) + row * a.columns.deep), bar);
         ++q_n;
       }
-      const uint32_t base = (uint32_t)g.tile.seq * a.span, tiles = g.to - g.from;
-      auto copy = [&](int32_t x0, int32_t y0, int32_t x1, int32_t y1) {
-        const uint32_t slot = n % kSlots, bar = dsmem_addr(&sh.full[slot], 0);
+      // Both pairs take the same pieces: this CTA brings half of each, for itself
+      // and the CTA of its rank in the other pair.
+      const uint32_t base = (uint32_t)g.tile.seq * a.span, tiles = g.to - g.from, half = place >> 1;
+      const uint16_t mask = (uint16_t)(5u << rank);
+      auto copy = [&](uint32_t x, uint32_t y) {
+        const uint32_t slot = n % kSlots;
         if (n >= kSlots) ok = ok && wait(&sh.empty[slot], (n / kSlots - 1) & 1);
         if (!ok) return;
         if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kSlotBytes);
-        pair_load_box(ring + slot * kSlotBytes, &vmap, x0, y0, bar);
-        pair_load_box(ring + slot * kSlotBytes + kSlotBytes / 2, &vmap, x1, y1, bar);
+        pair_load_box_multicast(ring + slot * kSlotBytes + half * (kSlotBytes / 2), &vmap, (int32_t)x, (int32_t)y,
+                                dsmem_addr(&sh.full[slot], leader), mask);
         ++n;
       };
       for (uint32_t i = 0; i <= tiles && ok; ++i) {
-        const int32_t row = (int32_t)(base + (g.from + i) * kSpan), mine = row + (int32_t)rank * 128;
+        const uint32_t row = base + (g.from + i) * kSpan;
         if (i < tiles)
-          for (int32_t k = 0; k < 9; ++k) copy(64 * k, mine, 64 * k, mine + 64);
+          for (uint32_t k = 0; k < 9; ++k) copy(64 * k, row + rank * 128 + half * 64);
         if (i > 0 && !max_only)
-          for (int32_t k = 0; k < 8; ++k) {
-            const int32_t x = (k / 4) * 256 + (int32_t)rank * 128, y = row - (int32_t)kSpan + (k % 4) * 64;
-            copy(x, y, x + 64, y);
-          }
+          for (uint32_t k = 0; k < 8; ++k)
+            copy((k / 4) * 256 + rank * 128 + half * 64, row - kSpan + (k % 4) * 64);
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -453,7 +461,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // (Waits of the whole warp, with a vote, a fence and an election for every
   // four: 430 clocks.)
   auto multiply = [&](const Segment& g, bool max_only) -> bool {
-    constexpr uint32_t kQk = pair_desc(1, kTileColumns, false, false), kPv = pair_desc(1, kTileColumns, true, true);
+    constexpr uint32_t kQk = pair_desc(1, kPairColumns, false, false), kPv = pair_desc(1, kPairColumns, true, true);
     const uint32_t tiles = g.to - g.from;
     if (ok && elect_one()) {
       const uint64_t q_desc = tile_desc(queries, 16), k_desc = tile_desc(ring, 16);
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ok = wait(&sh.q_full, q_n & 1);
       for (uint32_t i = 0, t = it, p = pv; i <= tiles && ok; ++i) {
         if (i < tiles) {
-          const uint32_t buf = t & 1, d = tmem + 256 + buf * kTileColumns;
+          const uint32_t buf = t & 1, d = tmem + 256 + buf * kPairColumns;
           if (t >= 2) ok = wait(&sh.s_empty[buf], ((t >> 1) - 1) & 1);
           tc_fence_after();
 #pragma unroll 3
@@ -479,11 +487,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (uint32_t e = 0; e < 4; ++e)
               pair_mma_bf16(d, k_desc + slot * (kSlotBytes >> 4) + 2 * e, q_desc + k * (kColumns * 128 >> 4) + 2 * e, kQk,
                             k + e > 0);
-            pair_commit(&sh.empty[slot], 3);
+            pair_commit(&sh.empty[slot], 15);
           }
           if (!ok) break;
-          pair_commit(&sh.s_full[buf], 3);
-          if (i + 1 == tiles) pair_commit(&sh.q_empty, 3);
+          pair_commit(&sh.s_full[buf], both);
+          if (i + 1 == tiles) pair_commit(&sh.q_empty, both);
           ++t;
         }
         if (i > 0 && !max_only) {
@@ -496,12 +504,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!ok) break;
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e)
-              pair_mma_bf16(tmem + (k / 4) * kTileColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
+              pair_mma_bf16(tmem + (k / 4) * kPairColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
                             p_desc + (k % 4) * 512 + 128 * e, kPv, i > 1 || k % 4 + e > 0);
-            pair_commit(&sh.empty[slot], 3);
+            pair_commit(&sh.empty[slot], 15);
           }
           if (!ok) break;
-          pair_commit(&sh.p_empty, 3);
+          pair_commit(&sh.p_empty, both);
           ++p;
         }
       }
@@ -522,7 +530,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t i = g.from; i < g.to && !max_only; ++i, ++pv) {
       if (lane == 0) {
         ok = come(pv);
-        if (ok) cluster_mbar_arrive(dsmem_addr(&sh.p_full, 0));
+        if (ok) cluster_mbar_arrive(dsmem_addr(&sh.p_full, leader));
       }
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
@@ -532,18 +540,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // A worker's position of a tile: rank * 128 + quad * 32 + lane; its columns: quarter * 32 + c.
   const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3, mine = rank * 128 + quad * 32 + lane;
   const uint32_t lanes = tmem + (quad << 21);
-  auto arrive0 = [&](uint64_t* bar) {                    // at rank 0's barrier, for the warp's loads from tensor memory
+  auto arrive0 = [&](uint64_t* bar) {                    // at the leader's, for the warp's loads from tensor memory
     __syncwarp();
-    if (lane == 0) cluster_mbar_arrive_relaxed(dsmem_addr(bar, 0));
+    if (lane == 0) cluster_mbar_arrive_relaxed(dsmem_addr(bar, leader));
   };
   // the maxima of this warp's columns (lane c: column c's) to both CTAs, and back the whole tile's
   auto meet = [&](float best) -> float {
     sh.top[rank][quarter][quad][lane] = best;
-    dsmem_st_u32(dsmem_addr(&sh.top[rank][quarter][quad][lane], rank ^ 1), __float_as_uint(best));
+    dsmem_st_u32(dsmem_addr(&sh.top[rank][quarter][quad][lane], other), __float_as_uint(best));
     __syncwarp();
     if (lane == 0) {
-      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 0));
-      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], 1));
+      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], place));
+      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], other));
     }
     ok = ok && cluster_wait(&sh.met[quarter], met_n & 1);
     ++met_n;
@@ -556,7 +564,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // first: the references are still to be found
   auto soften = [&](const Segment& g, bool max_only, bool first) -> bool {
     uint32_t at;
-    const uint32_t token = column_at(a, g.tile, 2 * g.tile.index + quarter / 2, quarter % 2 * 32 + lane, &at);
+    const uint32_t token = column_at(a, g.tile, 4 * g.tile.index + leader + quarter / 2, quarter % 2 * 32 + lane, &at);
     const bool real = token < g.tile.tokens;
     const uint32_t sees = real ? visible(a, g.tile.before, token) : UINT32_MAX;   // (others hold nothing up)
     const uint32_t least = __reduce_min_sync(0xffffffffu, sees);
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
       float x[32];
-      tmem_ld32(lanes + 256 + (it & 1) * kTileColumns + quarter * 32, x);
+      tmem_ld32(lanes + 256 + (it & 1) * kPairColumns + quarter * 32, x);
       tmem_ld_wait();
       tc_fence_before();
       arrive0(&sh.s_empty[it & 1]);
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         best = meet(best);
         if (!__all_sync(0xffffffffu, ok)) return false;
         const bool unset = !(fabsf(best) < INFINITY);
-        sh.ref[quarter][lane] = reference(best);
+        sh.ref[quarter][lane] = reference(best) + kRoom;
         flagged = __any_sync(0xffffffffu, unset && real && sees > (i + 1) * kSpan);
         __syncwarp();
       }
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         x[c] = fmaf(x[c], scale, -sh.ref[quarter][c]);
         most = fmaxf(most, x[c]);
       }
-      flagged |= most > kFar;
+      flagged |= most > a.far;
       // The weights are rounded to bf16 for the second product (half a step is
       // 2^-8 of a weight); their sum takes them before that, in fp32.
       uint32_t w[16];
@@ -636,7 +644,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (own) {
-        if (lane == 0) cluster_mbar_arrive(dsmem_addr(&sh.p_full, 0));
+        if (lane == 0) cluster_mbar_arrive(dsmem_addr(&sh.p_full, leader));
       } else {
         if (lane == 0) mbar_arrive(&sh.given);
         if (warp % 8 == 0) {                             // the first of the eight warps with the other's columns
@@ -644,8 +652,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!__all_sync(0xffffffffu, ok)) return false;
           if (lane == 0) {
             uint32_t there;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(probs + rank * kHalfBytes), "r"(rank ^ 1));
-            bulk_copy_s2peer(there, gift, kHalfBytes, dsmem_addr(&sh.p_come, rank ^ 1));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(probs + rank * kHalfBytes), "r"(other));
+            bulk_copy_s2peer(there, gift, kHalfBytes, dsmem_addr(&sh.p_come, other));
             ++gifts;
           }
         }
@@ -670,15 +678,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     add_lanes<32, 16>(sum, lane);
     flagged = first && __any_sync(0xffffffffu, flagged);
     sh.sums[rank][quarter][quad][lane] = sum[0];
-    dsmem_st_u32(dsmem_addr(&sh.sums[rank][quarter][quad][lane], rank ^ 1), __float_as_uint(sum[0]));
+    dsmem_st_u32(dsmem_addr(&sh.sums[rank][quarter][quad][lane], other), __float_as_uint(sum[0]));
     if (lane == 0) {
       sh.flag[rank][warp] = flagged;
-      dsmem_st_u32(dsmem_addr(&sh.flag[rank][warp], rank ^ 1), flagged);
+      dsmem_st_u32(dsmem_addr(&sh.flag[rank][warp], other), flagged);
     }
     __syncwarp();
     if (lane == 0) {
-      cluster_mbar_arrive(dsmem_addr(&sh.agreed, 0));
-      cluster_mbar_arrive(dsmem_addr(&sh.agreed, 1));
+      cluster_mbar_arrive(dsmem_addr(&sh.agreed, place));
+      cluster_mbar_arrive(dsmem_addr(&sh.agreed, other));
     }
     const float ref = sh.ref[quarter][lane];
     ok = ok && cluster_wait(&sh.agreed, full_n & 1);
@@ -690,39 +698,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float total = 0.0f;
     for (uint32_t r = 0; r < 2; ++r)
       for (uint32_t q = 0; q < 4; ++q) total += ((volatile float*)sh.sums[r][quarter][q])[lane];
-    const uint32_t slot = g.slot(pair);
+    const uint32_t slot = g.slot(cluster);
     if (again) {
       if (tid == 0) {
-        a.again[g.note(a, pair)] = 1;                    // (both CTAs write it)
+        a.again[g.note(a, cluster)] = 1;                 // (both CTAs write it)
         sh.redo = 1;
       }
     } else {
-      const float lse2 = total == 0.0f ? -INFINITY : ref + log2f(total);
+      // (the room taken off the sum again before its logarithm)
+      const float up = total < 1.0f ? kRoom : 0.0f;
+      const float lse2 = total == 0.0f ? -INFINITY : ref - up + log2f(total * (up ? 0x1p32f : 1.0f));
       if (quad == 0 && rank == 0) {
         if (!g.whole)
-          a.part_lse[slot * kTileColumns + quarter * 32 + lane] = lse2;
+          a.part_lse[slot * kTileColumns + leader * kColumns + quarter * 32 + lane] = lse2;
         else if (real && a.lse)
           a.lse[(int64_t)g.tile.first * a.heads + at] = lse2 * 0.6931471805599453f;
       }
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      const uint32_t place = real ? at : UINT32_MAX;     // where the column's result goes
+      const uint32_t there = __ballot_sync(0xffffffffu, real), columns = __popc(there);
+      const uint32_t first_at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
       for (uint32_t half = 0; half < 2; ++half) {
         float o[32];
-        tmem_ld32(lanes + half * kTileColumns + quarter * 32, o);
+        tmem_ld32(lanes + half * kPairColumns + quarter * 32, o);
         tmem_ld_wait();
         const uint32_t d = half * 256 + rank * 128 + quad * 32 + lane;
         if (g.whole) {
-          __nv_bfloat16* const out =
-              reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)g.tile.first * a.heads * KVO_LATENT_BYTES + d;
+          // (in one run the columns' results follow each other)
+          __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                     ((int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)) * KVO_LATENT_BYTES + d;
+          if (a.columns.flat) {
 #pragma unroll
-          for (uint32_t c = 0; c < 32; ++c) {
-            const uint32_t to = __shfl_sync(0xffffffffu, place, c);
-            const float by = __shfl_sync(0xffffffffu, inv, c);
-            if (to != UINT32_MAX) out[(int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+            for (uint32_t c = 0; c < 32; ++c) {
+              const float by = __shfl_sync(0xffffffffu, inv, c);
+              if (c < columns) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+            }
+          } else {
+#pragma unroll
+            for (uint32_t c = 0; c < 32; ++c) {
+              const uint32_t to = __shfl_sync(0xffffffffu, at, c);
+              const float by = __shfl_sync(0xffffffffu, inv, c);
+              if (there >> c & 1) out[(int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+            }
           }
         } else {
-          float* const out = a.part + ((int64_t)slot * kTileColumns + quarter * 32) * KVO_LATENT_BYTES + d;
+          float* const out = a.part + ((int64_t)slot * kTileColumns + leader * kColumns + quarter * 32) * KVO_LATENT_BYTES + d;
 #pragma unroll
           for (uint32_t c = 0; c < 32; ++c) out[c * KVO_LATENT_BYTES] = o[c] * __shfl_sync(0xffffffffu, inv, c);
         }
@@ -737,7 +757,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // and the whole of it with them.
   for (uint32_t round = 0; round < 2; ++round) {
     for_segments(a, begin, end, tile0, [&](const Segment& g) -> bool {
-      if (round && !__ldcg(a.again + g.note(a, pair))) return true;
+      if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
       for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
         const bool max_only = pass == 0;
         if (!(warp < kWorkers    ? soften(g, max_only, !round)
@@ -752,9 +772,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __threadfence();
     __syncthreads();
     cluster_sync();
-    // the same answer in both CTAs: nothing changes between the barriers
-    const uint32_t redo = sh.redo | dsmem_ld_u32(dsmem_addr(&sh.redo, rank ^ 1));
-    const uint32_t gave_up = sh.gave_up | dsmem_ld_u32(dsmem_addr(&sh.gave_up, rank ^ 1));
+    // the same answer in all CTAs: nothing changes between the barriers
+    uint32_t redo = 0, gave_up = 0;
+    for (uint32_t r = 0; r < 4; ++r) {
+      redo |= dsmem_ld_u32(dsmem_addr(&sh.redo, r));
+      gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
+    }
     __syncthreads();
     cluster_sync();
     if (!redo || gave_up) break;
@@ -764,23 +787,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == kLoader && lane == 0) {
     for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
     if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
-    for (uint32_t r = 0; r < 2; ++r) {
-      dsmem_st_u32(dsmem_addr(&sh.issued[rank], r), n);
-      dsmem_st_u32(dsmem_addr(&sh.q_issued[rank], r), q_n);
+    for (uint32_t r = 0; r < 4; ++r) {
+      dsmem_st_u32(dsmem_addr(&sh.issued[place], r), n);
+      dsmem_st_u32(dsmem_addr(&sh.q_issued[place], r), q_n);
     }
   }
-  if (warp < kWorkers && warp % 8 == 0 && (warp >> 3) != rank && lane == 0) dsmem_st_u32(dsmem_addr(&sh.gifts, rank ^ 1), gifts);
-  // Both CTAs end together.  Where a wait gave up in either, what is in flight
-  // finishes first: the MMAs, then the copies; a copy that only one CTA has
-  // started counts as come for the other.
+  if (warp < kWorkers && warp % 8 == 0 && (warp >> 3) != rank && lane == 0) dsmem_st_u32(dsmem_addr(&sh.gifts, other), gifts);
+  // All CTAs end together.  Where a wait gave up in any, what is in flight
+  // finishes first: the MMAs, then the copies; those that a CTA has not started
+  // count as come.
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  const uint32_t other_gave_up = dsmem_ld_u32(dsmem_addr(&sh.gave_up, rank ^ 1));
-  if (sh.gave_up | other_gave_up) {
+  uint32_t any_gave_up = 0;
+  for (uint32_t r = 0; r < 4; ++r) any_gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
+  if (any_gave_up) {
     if (tid == 0) atomicOr(a.status, kFlagTimeout);
     if (rank == 0 && warp == kMma && elect_one()) {
-      pair_commit(&sh.drained, 1);
+      pair_commit(&sh.drained, (uint16_t)(1u << place));
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
     }
     if (warp == 0 && lane == 0) {
@@ -788,17 +812,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (sh.gifts && !landed(&sh.p_come, (sh.gifts - 1) & 1)) atomicOr(a.status, kFlagInflight);
     }
     if (rank == 0 && warp == kLoader && lane == 0) {
-      auto even = [&](uint64_t* bar, bool here, bool there, uint32_t bytes) {
-        if (!here) mbar_arrive_expect_tx(bar, 2 * bytes);
-        if (!here || !there) mbar_complete_tx(bar, bytes);
-      };
-      const uint32_t most = max(sh.issued[0], sh.issued[1]), least = min(sh.issued[0], sh.issued[1]);
-      for (uint32_t m = least; m < most; ++m) even(&sh.full[m % kSlots], m < sh.issued[0], m < sh.issued[1], kSlotBytes);
+      uint32_t most = 0, least = UINT32_MAX;
+      for (uint32_t r = 0; r < 4; ++r) {
+        most = max(most, sh.issued[r]);
+        least = min(least, sh.issued[r]);
+      }
+      for (uint32_t m = least; m < most; ++m) {
+        uint64_t* const bar = &sh.full[m % kSlots];
+        if (m >= sh.issued[place]) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
+        for (uint32_t r = 0; r < 4; ++r)
+          if (m >= sh.issued[r]) mbar_complete_tx(bar, kSlotBytes / 2);
+      }
       for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
         if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
-      const uint32_t queried = max(sh.q_issued[0], sh.q_issued[1]);
-      if (sh.q_issued[0] != sh.q_issued[1])
-        even(&sh.q_full, sh.q_issued[0] == queried, sh.q_issued[1] == queried, 9 * box);
+      const uint32_t q0 = sh.q_issued[place], q1 = sh.q_issued[other], queried = max(q0, q1);
+      if (q0 != q1) {
+        if (q0 < queried) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
+        mbar_complete_tx(&sh.q_full, 9 * box);
+      }
       if (queried && !landed(&sh.q_full, (queried - 1) & 1)) atomicOr(a.status, kFlagInflight);
     }
     __syncthreads();
@@ -807,47 +838,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == kMma) pair_tmem_free(tmem, 512);
 }
 
-// A tile that shares' ends cut: block (g - 1, column) joins its parts if share
-// g is the first to begin inside it.
-__global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
-  const uint32_t g = blockIdx.x + 1, column = blockIdx.y, d = threadIdx.x;
+// A tile that shares' ends cut: blocks (g - 1, ..) join its parts if share g is
+// the first to begin inside it.  Two columns at a time, 128 threads each.
+constexpr uint32_t kJoinColumns = 16;                    // of a block
+
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
+  const uint32_t g = blockIdx.x + 1, d = threadIdx.x & 127;
   wait_previous_grid();
   const Shares shares(a);
-  if (g >= shares.pairs) return;
+  if (g >= shares.clusters) return;
   const uint64_t at = shares.from(g);
-  if (at >= shares.units) return;
   const uint32_t tile = tile_of(a, at);
   const PlanTile t = plan_tile(a, tile);
-  const uint64_t end = __ldcg(&a.plan[tile + 1].units);
-  if (at == t.units || shares.from(g - 1) > t.units) return;
-  uint32_t where;
-  const uint32_t token = column_at(a, t, 2 * t.index + column / kColumns, column % kColumns, &where);
-  if (token >= t.tokens) return;
+  const uint64_t end = t.units + t.spans;
+  if (at == t.units || at >= end || shares.from(g - 1) > t.units) return;
   uint32_t last = g;                                     // the last share that begins inside the tile
-  while (last + 1 < shares.pairs && shares.from(last + 1) < end) ++last;
+  while (last + 1 < shares.clusters && shares.from(last + 1) < end) ++last;
   // parts: of share g - 1 the one that ends inside, of the others the one that begins there
   auto slot = [&](uint32_t p) { return 2 * p + (p == g - 1); };
-  float top = -INFINITY;
-  for (uint32_t p = g - 1; p <= last; ++p) top = fmaxf(top, __ldcg(a.part_lse + slot(p) * kTileColumns + column));
-  const float base = top == -INFINITY ? 0.0f : top;
-  float total = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (uint32_t p = g - 1; p <= last; ++p) {
-    const uint32_t from = slot(p) * kTileColumns + column;
-    const float w = exp2f(__ldcg(a.part_lse + from) - base);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)from * KVO_LATENT_BYTES) + d);
-    if (!(w > 0.0f) && !isnan(w)) continue;
-    total += w;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  for (uint32_t i = 0; i < kJoinColumns; i += 2) {
+    const uint32_t column = blockIdx.y * kJoinColumns + i + (threadIdx.x >> 7);
+    uint32_t where;
+    const uint32_t token = column_at(a, t, 4 * t.index + column / kColumns, column % kColumns, &where);
+    if (token >= t.tokens) continue;
+    float top = -INFINITY;
+    for (uint32_t p = g - 1; p <= last; ++p) top = fmaxf(top, __ldcg(a.part_lse + slot(p) * kTileColumns + column));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float total = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (uint32_t p = g - 1; p <= last; ++p) {
+      const uint32_t from = slot(p) * kTileColumns + column;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)from * KVO_LATENT_BYTES) + d);
+      const float w = exp2f(__ldcg(a.part_lse + from) - base);
+      if (!(w > 0.0f) && !isnan(w)) continue;
+      total += w;
+      o.x = fmaf(w, v.x, o.x);
+      o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z);
+      o.w = fmaf(w, v.w, o.w);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const int64_t row = (int64_t)t.first * a.heads + where;
+    reinterpret_cast<uint2*>(a.out + row * KVO_LATENT_BYTES)[d] =
+        make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+    if (a.lse && d == 0) a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  const int64_t row = (int64_t)t.first * a.heads + where;
-  reinterpret_cast<uint2*>(a.out + row * KVO_LATENT_BYTES)[d] =
-      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-  if (a.lse && d == 0) a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ the host
@@ -859,20 +895,20 @@ bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t row
 }
 
 struct Layout {              // of the scratch
-  int64_t span, tiles, pairs;
+  int64_t span, tiles, clusters;
   int64_t values, off, plan, again, part, part_lse, bytes;
 };
 
 Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   Layout l;
   l.span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
-  l.pairs = device_sms() / 2;
+  l.clusters = device_sms() / 4;
   // Tiles of either way to fill them: at worst 33 heads of one token a half.
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t deep = heads < kColumns ? kColumns / heads : 1, across = heads > kColumns ? 2 : 1;
   const int64_t halves = (tokens + busy * (deep - 1)) / deep * across;
   const int64_t flat = (tokens * heads + busy * (kColumns - 1)) / kColumns;
-  l.tiles = ((halves > flat ? halves : flat) + busy + 1) / 2;
+  l.tiles = ((halves > flat ? halves : flat) + 3 * busy + 3) / 4;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -882,42 +918,49 @@ Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows
   l.values = take(sequences * l.span * kValueBytes);
   l.off = take(sequences * l.span * 4);
   l.plan = take((l.tiles + 2) * (int64_t)sizeof(PlanTile));
-  l.again = take(l.tiles + 2 * l.pairs);
-  l.part = take(2 * l.pairs * kTileColumns * KVO_LATENT_BYTES * 4);
-  l.part_lse = take(2 * l.pairs * kTileColumns * 4);
+  l.again = take(l.tiles + 2 * l.clusters);
+  l.part = take(2 * l.clusters * kTileColumns * KVO_LATENT_BYTES * 4);
+  l.part_lse = take(2 * l.clusters * kTileColumns * 4);
   l.bytes = at;
   return l;
 }
 
-cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& qmap, const CUtensorMap& vmap, cudaStream_t stream) {
-  static bool ready[64] = {};
+cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  static int room[64] = {};                              // clusters that run at the same time
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkSmem);
-    if (e != cudaSuccess) return e;
-    ready[dev & 63] = true;
-  }
-  e = launch_early(unpack_kernel, dim3(1 + a.unpack_blocks * a.cache.sequences), kUnpackThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 4;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3(2 * a.pairs);
+  lc.gridDim = dim3(4);
   lc.blockDim = dim3(kChunkThreads);
   lc.dynamicSmemBytes = kChunkSmem;
   lc.stream = stream;
   lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (!room[dev & 63]) {
+    e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkSmem);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, chunk_kernel, &lc);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    room[dev & 63] = n;
+  }
+  if (a.clusters > (uint32_t)room[dev & 63]) a.clusters = (uint32_t)room[dev & 63];
+  e = launch_early(unpack_kernel, dim3(1 + a.unpack_blocks * a.cache.sequences), kUnpackThreads, 0, stream, a);
+  if (e != cudaSuccess) return e;
+  lc.gridDim = dim3(4 * a.clusters);
   lc.numAttrs = 2;
   e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, vmap);
-  if (e != cudaSuccess || a.pairs < 2) return e;
-  return launch_early(join_parts_kernel, dim3(a.pairs - 1, kTileColumns), 128, 0, stream, a);
+  if (e != cudaSuccess || a.clusters < 2) return e;
+  return launch_early(join_parts_kernel, dim3(a.clusters - 1, kTileColumns / kJoinColumns), 256, 0, stream, a);
 }
 
 }  // namespace
@@ -972,10 +1015,12 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.tokens = (uint32_t)s->tokens;
   a.heads = (uint32_t)s->heads;
   a.most_tiles = (uint32_t)l.tiles;
-  a.pairs = (uint32_t)l.pairs;
+  a.clusters = (uint32_t)l.clusters;
   a.unpack_blocks = (uint32_t)(l.span / kUnpackRows);
   a.by_heads = divider(a.heads);
   a.scale = s->scale * kLog2e;
+  // sums of weights up to 2^far over all rows, times latents below 2^23, stay below 2^126
+  a.far = 103.0f - std::ceil(std::log2((float)(s->rows > 1 ? s->rows : 1)));
   a.wait_clocks = wait_clocks;
   // a dimension of one has no next element: its stride says nothing
   const int64_t head_ld = a.heads > 1 ? s->q_head_ld : KVO_DEQUANT_VALUES;

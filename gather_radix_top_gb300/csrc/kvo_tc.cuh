@@ -220,12 +220,14 @@ __device__ __forceinline__ void pair_load_box(uint32_t dst, const void* map, int
       : "memory");
 }
 
-// The same of a two-dimensional one.
-__device__ __forceinline__ void pair_load_box(uint32_t dst, const void* map, int32_t x, int32_t y, uint32_t bar) {
+// A box of a two-dimensional one to that place in the CTAs of `mask`; each completes on the barrier
+// at `bar`'s place in the CTA of its pair that has the parity of `bar`'s.
+__device__ __forceinline__ void pair_load_box_multicast(uint32_t dst, const void* map, int32_t x, int32_t y, uint32_t bar,
+                                                        uint16_t mask) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "h"(mask)
       : "memory");
 }
 
@@ -233,10 +235,6 @@ __device__ __forceinline__ void pair_load_box(uint32_t dst, const void* map, int
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-
-// Between this thread's plain accesses, anywhere, and the asynchronous ones of
-// whoever it synchronises with.
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");

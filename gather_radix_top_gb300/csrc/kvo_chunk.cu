@@ -47,12 +47,14 @@ constexpr uint32_t kTileColumns = 4 * kColumns;          // of a cluster
 constexpr uint32_t kTileCost = 1;                        // of a tile of columns, in tiles of positions
 constexpr uint32_t kWorkers = 16;
 constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
-constexpr uint32_t kChunkThreads = (kLoader + 1) * 32;
+constexpr uint32_t kLoaders = 3;                         // warps: one takes 500 clocks a copy beside the workers
+constexpr uint32_t kChunkThreads = (kLoader + kLoaders) * 32;
 constexpr uint32_t kQueryBytes = 9 * kColumns * 128;
 constexpr uint32_t kHalfBytes = kSpan / 2 * 128;         // a CTA's positions' weights of 64 columns
 constexpr uint32_t kSlotBytes = 16384, kSlots = 6;
 constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + 3 * kHalfBytes + kSlots * kSlotBytes;
 constexpr uint32_t kValueBytes = KVO_DEQUANT_VALUES * 2;
+static_assert(9 % kLoaders == 0 && kSlots % kLoaders == 0, "even shares of the queries, and a warp its own slots");
 constexpr float kRoom = 32.0f;                           // of a reference above the first tile's maximum, in powers of two
 
 // One tile of columns, as the plan lists it.
@@ -321,7 +323,8 @@ struct ChunkShared {
   uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_come, p_empty, o_empty, given,
       met[4], agreed, drained;
   uint32_t tmem, gave_up;
-  uint32_t issued[4], q_issued[4];   // copies that each CTA's loader has started
+  // per CTA and loading warp: copies of its own and before them that it has started, and queries
+  uint32_t issued[4][kLoaders], q_issued[4][kLoaders];
   uint32_t gifts, armed;             // weights that the other CTA has sent, and that this one has been ready for
   uint32_t redo;                     // some segment needs another pass
   uint32_t flag[2][kWorkers];        // per warp of the pair: this segment does
@@ -370,7 +373,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 2 * kWorkers);
     }
-    for (uint32_t i = 0; i < 4; ++i) sh.issued[i] = sh.q_issued[i] = 0;
+    for (uint32_t i = 0; i < 4; ++i)
+      for (uint32_t w = 0; w < kLoaders; ++w) sh.issued[i][w] = sh.q_issued[i][w] = 0;
     mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns, and that rank 1 has all of its
     mbar_init(&sh.p_come, 1);
     mbar_init(&sh.given, kWorkers / 2);
@@ -411,13 +415,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   bool ok = true;
 
   // One segment's work for each role; max_only: only the columns' maxima.
+  //
+  // Loading warp w takes every kLoaders-th copy from copy w on, and as many of
+  // the queries' nine.
+  const uint32_t load_warp = warp - kLoader, full0 = dsmem_addr(&sh.full[0], leader);
   auto load = [&](const Segment& g, bool max_only) -> bool {
+    const uint32_t tiles = g.to - g.from;
     if (lane == 0) {
       if (q_n > 0) ok = ok && wait(&sh.q_empty, (q_n - 1) & 1);
       if (ok) {
         const uint32_t half = 4 * g.tile.index + place, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, leader);
-        if (rank == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
-        for (uint32_t i = 0; i < 9; ++i)
+        if (rank == 0 && load_warp == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
+        for (uint32_t i = load_warp; i < 9; i += kLoaders)
           pair_load_box(queries + i * (kColumns * 128), &qmap, (int32_t)(i * 64),
                         (int32_t)(half % a.columns.across * a.columns.wide),
                         (int32_t)((a.columns.flat ? g.tile.first * a.heads : g.tile.first) + row * a.columns.deep), bar);
@@ -425,25 +434,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       // Both pairs take the same pieces: this CTA brings half of each, for itself
       // and the CTA of its rank in the other pair.
-      const uint32_t base = (uint32_t)g.tile.seq * a.span, tiles = g.to - g.from, half = place >> 1;
+      const uint32_t half = place >> 1;
       const uint16_t mask = (uint16_t)(5u << rank);
-      auto copy = [&](uint32_t x, uint32_t y) {
-        const uint32_t slot = n % kSlots;
-        if (n >= kSlots) ok = ok && wait(&sh.empty[slot], (n / kSlots - 1) & 1);
-        if (!ok) return;
-        if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kSlotBytes);
-        pair_load_box_multicast(ring + slot * kSlotBytes + half * (kSlotBytes / 2), &vmap, (int32_t)x, (int32_t)y,
-                                dsmem_addr(&sh.full[slot], leader), mask);
-        ++n;
+      uint32_t at = n;                                   // the copy that a run of them begins with
+      // the next `count` copies, the k-th from place_of(k) on
+      auto copies = [&](uint32_t count, auto&& place_of) {
+        for (uint32_t k = (load_warp + kLoaders - at % kLoaders) % kLoaders; k < count && ok; k += kLoaders) {
+          const uint32_t m = at + k, slot = m % kSlots;
+          if (m >= kSlots) ok = wait(&sh.empty[slot], (m / kSlots - 1) & 1);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kSlotBytes);
+          const uint2 xy = place_of(k);
+          pair_load_box_multicast(ring + slot * kSlotBytes + half * (kSlotBytes / 2), &vmap, (int32_t)xy.x, (int32_t)xy.y,
+                                  full0 + slot * 8, mask);
+          n = m + 1;
+        }
+        at += count;
       };
+      const uint32_t k_row = (uint32_t)g.tile.seq * a.span + rank * 128 + half * 64, v_row = (uint32_t)g.tile.seq * a.span;
+      const uint32_t v_col = rank * 128 + half * 64;
       for (uint32_t i = 0; i <= tiles && ok; ++i) {
-        const uint32_t row = base + (g.from + i) * kSpan;
-        if (i < tiles)
-          for (uint32_t k = 0; k < 9; ++k) copy(64 * k, row + rank * 128 + half * 64);
+        const uint32_t row = (g.from + i) * kSpan;
+        if (i < tiles) copies(9, [&](uint32_t k) { return make_uint2(64 * k, k_row + row); });
         if (i > 0 && !max_only)
-          for (uint32_t k = 0; k < 8; ++k)
-            copy((k / 4) * 256 + rank * 128 + half * 64, row - kSpan + (k % 4) * 64);
+          copies(8, [&](uint32_t k) { return make_uint2((k >> 2) * 256 + v_col, v_row + row - kSpan + (k & 3) * 64); });
       }
+      if (ok) n = at;
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
     return ok;
@@ -761,7 +777,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
         const bool max_only = pass == 0;
         if (!(warp < kWorkers    ? soften(g, max_only, !round)
-              : warp == kLoader  ? load(g, max_only)
+              : warp >= kLoader  ? load(g, max_only)
               : rank == 0        ? multiply(g, max_only)
                                  : pass_on(g, max_only)))
           return false;
@@ -784,12 +800,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
 
   // no slot's release may still be on its way when the CTA ends
-  if (warp == kLoader && lane == 0) {
+  if (warp >= kLoader && lane == 0) {
     for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
     if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
     for (uint32_t r = 0; r < 4; ++r) {
-      dsmem_st_u32(dsmem_addr(&sh.issued[place], r), n);
-      dsmem_st_u32(dsmem_addr(&sh.q_issued[place], r), q_n);
+      dsmem_st_u32(dsmem_addr(&sh.issued[place][load_warp], r), n);
+      dsmem_st_u32(dsmem_addr(&sh.q_issued[place][load_warp], r), q_n);
     }
   }
   if (warp < kWorkers && warp % 8 == 0 && (warp >> 3) != rank && lane == 0) dsmem_st_u32(dsmem_addr(&sh.gifts, other), gifts);
@@ -812,25 +828,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (sh.gifts && !landed(&sh.p_come, (sh.gifts - 1) & 1)) atomicOr(a.status, kFlagInflight);
     }
     if (rank == 0 && warp == kLoader && lane == 0) {
-      uint32_t most = 0, least = UINT32_MAX;
-      for (uint32_t r = 0; r < 4; ++r) {
-        most = max(most, sh.issued[r]);
-        least = min(least, sh.issued[r]);
-      }
+      uint32_t most = 0, least = UINT32_MAX, queried = 0;
+      for (uint32_t r = 0; r < 4; ++r)
+        for (uint32_t w = 0; w < kLoaders; ++w) {
+          most = max(most, sh.issued[r][w]);
+          least = min(least, sh.issued[r][w]);
+          if ((r & 2) == leader) queried = max(queried, sh.q_issued[r][w]);
+        }
+      // (whoever starts a copy has seen the one before it in its slot used up)
+      auto started = [&](uint32_t m) {
+        for (uint32_t r = 0; r < 4; ++r)
+          if (m < sh.issued[r][m % kLoaders]) return true;
+        return false;
+      };
       for (uint32_t m = least; m < most; ++m) {
         uint64_t* const bar = &sh.full[m % kSlots];
-        if (m >= sh.issued[place]) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
+        if (!started(m)) continue;
+        if (m >= sh.issued[place][m % kLoaders]) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
         for (uint32_t r = 0; r < 4; ++r)
-          if (m >= sh.issued[r]) mbar_complete_tx(bar, kSlotBytes / 2);
+          if (m >= sh.issued[r][m % kLoaders]) mbar_complete_tx(bar, kSlotBytes / 2);
       }
       for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
-        if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
-      const uint32_t q0 = sh.q_issued[place], q1 = sh.q_issued[other], queried = max(q0, q1);
-      if (q0 != q1) {
-        if (q0 < queried) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
-        mbar_complete_tx(&sh.q_full, 9 * box);
+        if (started(m) && !landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
+      if (queried) {
+        if (sh.q_issued[place][0] < queried) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
+        for (uint32_t r = leader; r < leader + 2; ++r)
+          for (uint32_t w = 0; w < kLoaders; ++w)
+            if (sh.q_issued[r][w] < queried) mbar_complete_tx(&sh.q_full, 9 / kLoaders * box);
+        if (!landed(&sh.q_full, (queried - 1) & 1)) atomicOr(a.status, kFlagInflight);
       }
-      if (queried && !landed(&sh.q_full, (queried - 1) & 1)) atomicOr(a.status, kFlagInflight);
     }
     __syncthreads();
   }

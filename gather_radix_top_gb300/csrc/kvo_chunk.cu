@@ -305,11 +305,14 @@ struct Segment {
 template <typename F>
 __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, F f) {
   if (begin >= end) return;
-  PlanTile next = plan_tile(a, tile);
+  // (asked for a segment ahead)
+  const uint32_t last = __ldcg(&a.plan[a.most_tiles + 1].index);
+  PlanTile next = plan_tile(a, tile), after = plan_tile(a, min(tile + 1, last));
   for (uint64_t u = begin; u < end; ++tile) {
     Segment g;
     g.tile = next;
-    next = plan_tile(a, tile + 1);
+    next = after;
+    after = plan_tile(a, min(tile + 2, last));
     g.number = tile;
     g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
     g.to = min((uint32_t)(min(next.units, end) - g.tile.units), g.tile.spans);
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           ++t;
         }
         if (i > 0 && !max_only) {
-          ok = come(p) && cluster_wait(&sh.p_full, p & 1);
+          ok = come(p) && wait(&sh.p_full, p & 1);
           if (i == 1 && full_n > 0) ok = ok && wait(&sh.o_empty, (full_n - 1) & 1);
           tc_fence_after();
 #pragma unroll 4
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t i = g.from; i < g.to && !max_only; ++i, ++pv) {
       if (lane == 0) {
         ok = come(pv);
-        if (ok) cluster_mbar_arrive(dsmem_addr(&sh.p_full, leader));
+        if (ok) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, leader));
       }
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (own) {
-        if (lane == 0) cluster_mbar_arrive(dsmem_addr(&sh.p_full, leader));
+        if (lane == 0) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, leader));
       } else {
         if (lane == 0) mbar_arrive(&sh.given);
         if (warp % 8 == 0) {                             // the first of the eight warps with the other's columns

@@ -280,11 +280,9 @@ __device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
 }
 
 __device__ __forceinline__ PlanTile plan_tile(const ChunkArgs& a, uint32_t i) {
-  PlanTile t;
-  const uint4* from = reinterpret_cast<const uint4*>(a.plan + i);
-  reinterpret_cast<uint4*>(&t)[0] = __ldcg(from);
-  reinterpret_cast<uint4*>(&t)[1] = __ldcg(from + 1);
-  return t;
+  const uint4* const from = reinterpret_cast<const uint4*>(a.plan + i);
+  const uint4 x = __ldcg(from), y = __ldcg(from + 1);
+  return PlanTile{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
 }
 
 // A share's part of one tile of columns: tiles of positions [from, to).
@@ -302,22 +300,23 @@ struct Segment {
 };
 
 // f(segment) for every segment of a cluster's share, in order, in every warp.
+// The next tile is asked for a segment ahead, but not by the workers: they have
+// no registers for it, and time, while the MMAs of two tiles of positions run.
 template <typename F>
-__device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, F f) {
-  if (begin >= end) return;
-  // (asked for a segment ahead)
-  const uint32_t last = __ldcg(&a.plan[a.most_tiles + 1].index);
-  PlanTile next = plan_tile(a, tile), after = plan_tile(a, min(tile + 1, last));
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, bool ahead,
+                                             F f) {
+  PlanTile next;
+  if (ahead && begin < end) next = plan_tile(a, tile);
   for (uint64_t u = begin; u < end; ++tile) {
     Segment g;
-    g.tile = next;
-    next = after;
-    after = plan_tile(a, min(tile + 2, last));
+    g.tile = ahead ? next : plan_tile(a, tile);
+    const uint64_t past = g.tile.units + g.tile.spans + kTileCost;
+    if (ahead && past < end) next = plan_tile(a, tile + 1);
     g.number = tile;
     g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
-    g.to = min((uint32_t)(min(next.units, end) - g.tile.units), g.tile.spans);
+    g.to = min((uint32_t)(min(past, end) - g.tile.units), g.tile.spans);
     g.whole = g.to - g.from == g.tile.spans;
-    u = next.units;
+    u = past;
     if (g.from < g.to && !f(g)) return;
   }
 }
@@ -336,9 +335,27 @@ struct ChunkShared {
   // per column: the softmax's reference and the positions it sees.  The four
   // warps of a quarter write the same values, after all of them have agreed on
   // the segment before.
-  float ref[4][32];
-  uint32_t seen[4][32];
+  alignas(16) float ref[4][32];
+  alignas(16) uint32_t seen[4][32];
 };
+
+// x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
+__device__ __forceinline__ void fma_two(float& x, float& y, float scale, float a, float b) {
+  asm("{\n .reg .b64 v, s, t;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mov.b64 t, {%3, %4};\n"
+      " fma.rn.f32x2 v, v, s, t;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(scale), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_two(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 v, t;\n mov.b64 v, {%0, %1};\n mov.b64 t, {%2, %3};\n add.rn.f32x2 v, v, t;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max_three(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 template <uint32_t kN, uint32_t kBit>
 __device__ __forceinline__ void add_lanes(float* v, uint32_t lane) {
@@ -603,30 +620,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ok = ok && wait(&sh.s_full[it & 1], it >> 1 & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
-      float x[32];
-      tmem_ld32(lanes + 256 + (it & 1) * kPairColumns + quarter * 32, x);
-      tmem_ld_wait();
-      tc_fence_before();
-      arrive0(&sh.s_empty[it & 1]);
+      const uint32_t scores = lanes + 256 + (it & 1) * kPairColumns + quarter * 32;
       const bool edge = __any_sync(0xffffffffu, gone) || (i + 1) * kSpan > least;
-      float scale = a.scale;
-      if (edge) {
-        scale = 1.0f;
+      // sixteen columns at a time, `x` times `scale` their logits
+      auto logits = [&](uint32_t h, float* x) -> float {
+        tmem_ld16(scores + 16 * h, x);
+        tmem_ld_wait();
+        if (!edge) return a.scale;
 #pragma unroll
-        for (uint32_t c = 0; c < 32; ++c) x[c] = gone || p >= sh.seen[quarter][c] ? -INFINITY : x[c] * a.scale;
-      }
+        for (uint32_t c = 0; c < 16; c += 4) {
+          const uint4 see = *reinterpret_cast<const uint4*>(&sh.seen[quarter][16 * h + c]);
+          x[c] = p < see.x ? x[c] * a.scale : -INFINITY;
+          x[c + 1] = p < see.y ? x[c + 1] * a.scale : -INFINITY;
+          x[c + 2] = p < see.z ? x[c + 2] * a.scale : -INFINITY;
+          x[c + 3] = p < see.w ? x[c + 3] * a.scale : -INFINITY;
+        }
+        if (gone) {
+#pragma unroll
+          for (uint32_t c = 0; c < 16; ++c) x[c] = -INFINITY;
+        }
+        return 1.0f;
+      };
       if (max_only) {
 #pragma unroll
-        for (uint32_t c = 0; c < 32; ++c) sum[c] = fmaxf(sum[c], x[c] * scale);
+        for (uint32_t h = 0; h < 2; ++h) {
+          float x[16];
+          const float scale = logits(h, x);
+#pragma unroll
+          for (uint32_t c = 0; c < 16; ++c) sum[16 * h + c] = fmaxf(sum[16 * h + c], x[c] * scale);
+        }
+        tc_fence_before();
+        arrive0(&sh.s_empty[it & 1]);
         continue;
       }
       if (first && i == g.from) {
         float best = -INFINITY;
 #pragma unroll
-        for (uint32_t c = 0; c < 32; ++c) {
-          float m;
-          asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c] * scale));
-          if (lane == c) best = m;
+        for (uint32_t h = 0; h < 2; ++h) {
+          float x[16];
+          const float scale = logits(h, x);
+#pragma unroll
+          for (uint32_t c = 0; c < 16; ++c) {
+            float m;
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x[c] * scale));
+            if (lane == 16 * h + c) best = m;
+          }
         }
         best = meet(best);
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -635,23 +673,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         flagged = __any_sync(0xffffffffu, unset && real && sees > (i + 1) * kSpan);
         __syncwarp();
       }
+      // The weights are rounded to bf16 for the second product (half a step is
+      // 2^-8 of a weight); their sum takes them before that, in fp32.  Two
+      // values an instruction: the MMAs' and the copies' threads have to find
+      // room between the workers' instructions.
+      uint32_t w[16];
       float most = -INFINITY;
 #pragma unroll
-      for (uint32_t c = 0; c < 32; ++c) {
-        x[c] = fmaf(x[c], scale, -sh.ref[quarter][c]);
-        most = fmaxf(most, x[c]);
+      for (uint32_t h = 0; h < 2; ++h) {
+        float x[16];
+        const float scale = logits(h, x);
+        if (h == 1) {
+          tc_fence_before();
+          arrive0(&sh.s_empty[it & 1]);
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < 16; c += 4) {
+          const float4 ref = *reinterpret_cast<const float4*>(&sh.ref[quarter][16 * h + c]);
+          fma_two(x[c], x[c + 1], scale, -ref.x, -ref.y);
+          fma_two(x[c + 2], x[c + 3], scale, -ref.z, -ref.w);
+          most = max_three(max_three(most, x[c], x[c + 1]), x[c + 2], x[c + 3]);
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < 16; c += 2) {
+          const float u = exp2_approx(x[c]), v = exp2_approx(x[c + 1]);
+          add_two(sum[16 * h + c], sum[16 * h + c + 1], u, v);
+          w[8 * h + c / 2] = bf16_pair(u, v);
+        }
       }
       flagged |= most > a.far;
-      // The weights are rounded to bf16 for the second product (half a step is
-      // 2^-8 of a weight); their sum takes them before that, in fp32.
-      uint32_t w[16];
-#pragma unroll
-      for (uint32_t c = 0; c < 32; c += 2) {
-        const float u = exp2_approx(x[c]), v = exp2_approx(x[c + 1]);
-        sum[c] += u;
-        sum[c + 1] += v;
-        w[c / 2] = bf16_pair(u, v);
-      }
       if (pv > 0) ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
       const bool own = quarter >> 1 == rank;             // this CTA's columns, or the other's
@@ -736,34 +786,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
       const uint32_t there = __ballot_sync(0xffffffffu, real), columns = __popc(there);
       const uint32_t first_at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-      for (uint32_t half = 0; half < 2; ++half) {
-        float o[32];
-        tmem_ld32(lanes + half * kPairColumns + quarter * 32, o);
+      // sixteen columns of 128 values at a time (in one run the columns' results follow each other)
+      const int64_t row0 = g.whole ? (int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)
+                                   : (int64_t)slot * kTileColumns + leader * kColumns + quarter * 32;
+#pragma unroll 1
+      for (uint32_t part = 0; part < 4; ++part) {
+        const uint32_t c0 = part % 2 * 16, half = part / 2;
+        float o[16];
+        tmem_ld16(lanes + half * kPairColumns + quarter * 32 + c0, o);
         tmem_ld_wait();
-        const uint32_t d = half * 256 + rank * 128 + quad * 32 + lane;
-        if (g.whole) {
-          // (in one run the columns' results follow each other)
-          __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                     ((int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)) * KVO_LATENT_BYTES + d;
-          if (a.columns.flat) {
+        const int64_t d = row0 * KVO_LATENT_BYTES + half * 256 + rank * 128 + quad * 32 + lane;
+        if (!g.whole) {
+          float* const out = a.part + d + c0 * KVO_LATENT_BYTES;
 #pragma unroll
-            for (uint32_t c = 0; c < 32; ++c) {
-              const float by = __shfl_sync(0xffffffffu, inv, c);
-              if (c < columns) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
-            }
-          } else {
+          for (uint32_t c = 0; c < 16; ++c) out[c * KVO_LATENT_BYTES] = o[c] * __shfl_sync(0xffffffffu, inv, c0 + c);
+        } else if (a.columns.flat) {
+          __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(a.out) + d + c0 * KVO_LATENT_BYTES;
 #pragma unroll
-            for (uint32_t c = 0; c < 32; ++c) {
-              const uint32_t to = __shfl_sync(0xffffffffu, at, c);
-              const float by = __shfl_sync(0xffffffffu, inv, c);
-              if (there >> c & 1) out[(int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
-            }
+          for (uint32_t c = 0; c < 16; ++c) {
+            const float by = __shfl_sync(0xffffffffu, inv, c0 + c);
+            if (c0 + c < columns) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
           }
         } else {
-          float* const out = a.part + ((int64_t)slot * kTileColumns + leader * kColumns + quarter * 32) * KVO_LATENT_BYTES + d;
 #pragma unroll
-          for (uint32_t c = 0; c < 32; ++c) out[c * KVO_LATENT_BYTES] = o[c] * __shfl_sync(0xffffffffu, inv, c);
+          for (uint32_t c = 0; c < 16; ++c) {
+            const uint32_t to = __shfl_sync(0xffffffffu, at, c0 + c);
+            const float by = __shfl_sync(0xffffffffu, inv, c0 + c);
+            if (there >> (c0 + c) & 1)
+              reinterpret_cast<__nv_bfloat16*>(a.out)[d + (int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+          }
         }
       }
     }
@@ -775,7 +826,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // All segments, then those that need another pass: their columns' maxima,
   // and the whole of it with them.
   for (uint32_t round = 0; round < 2; ++round) {
-    for_segments(a, begin, end, tile0, [&](const Segment& g) -> bool {
+    for_segments(a, begin, end, tile0, warp >= kWorkers, [&](const Segment& g) -> bool {
       if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
       for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
         const bool max_only = pass == 0;

@@ -300,18 +300,19 @@ struct Segment {
 };
 
 // f(segment) for every segment of a cluster's share, in order, in every warp.
-// The next tile is asked for a segment ahead, but not by the workers: they have
-// no registers for it, and time, while the MMAs of two tiles of positions run.
+// `next` is tile `number`, if that has been asked for ahead: by most warps here,
+// but the workers do it at a segment's end, when they have registers for it.
 template <typename F>
 __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, bool ahead,
-                                             F f) {
-  PlanTile next;
-  if (ahead && begin < end) next = plan_tile(a, tile);
+                                             PlanTile& next, uint32_t& number, F f) {
   for (uint64_t u = begin; u < end; ++tile) {
     Segment g;
-    g.tile = ahead ? next : plan_tile(a, tile);
+    g.tile = number == tile ? next : plan_tile(a, tile);
     const uint64_t past = g.tile.units + g.tile.spans + kTileCost;
-    if (ahead && past < end) next = plan_tile(a, tile + 1);
+    if (ahead) {
+      next = plan_tile(a, tile + 1);
+      number = tile + 1;
+    }
     g.number = tile;
     g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
     g.to = min((uint32_t)(min(past, end) - g.tile.units), g.tile.spans);
@@ -321,22 +322,31 @@ __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin,
   }
 }
 
+// What a pair's CTAs send each other: weights of the other's columns, maxima of
+// the columns, sums of their weights.
+enum Letter : uint32_t { kGift, kTop, kSum, kLetters };
+
+struct Sums {
+  float of[4][4][32];                // per quarter of the columns and warp
+  uint32_t again[kWorkers];          // per warp: this segment needs another pass
+};
+
 struct ChunkShared {
-  uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_come, p_empty, o_empty, given,
-      met[4], agreed, drained;
+  uint64_t full[kSlots], empty[kSlots], q_full, q_empty, s_full[2], s_empty[2], p_full, p_empty, o_empty;
+  uint64_t ready[kLetters], come[kLetters], drained;
   uint32_t tmem, gave_up;
   // per CTA and loading warp: copies of its own and before them that it has started, and queries
   uint32_t issued[4][kLoaders], q_issued[4][kLoaders];
-  uint32_t gifts, armed;             // weights that the other CTA has sent, and that this one has been ready for
+  uint32_t sent[kLetters], armed[kLetters];   // letters that the other CTA has sent, and that this one has been ready for
   uint32_t redo;                     // some segment needs another pass
-  uint32_t flag[2][kWorkers];        // per warp of the pair: this segment does
-  float top[2][4][4][32];            // per CTA, quarter of the columns and warp: maxima
-  float sums[2][4][4][32];
-  // per column: the softmax's reference and the positions it sees.  The four
-  // warps of a quarter write the same values, after all of them have agreed on
-  // the segment before.
+  alignas(16) float top[2][4][4][32];         // per CTA, quarter of the columns and warp: maxima
+  alignas(16) Sums sums[2];
+  // per column: the softmax's reference, the positions it sees, 1 / the sum of
+  // its weights.  The four warps of a quarter write the same values, after all
+  // of them have agreed on the segment before.
   alignas(16) float ref[4][32];
   alignas(16) uint32_t seen[4][32];
+  alignas(16) float inv[4][32];
 };
 
 // x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
@@ -396,13 +406,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t i = 0; i < 4; ++i)
       for (uint32_t w = 0; w < kLoaders; ++w) sh.issued[i][w] = sh.q_issued[i][w] = 0;
     mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns, and that rank 1 has all of its
-    mbar_init(&sh.p_come, 1);
-    mbar_init(&sh.given, kWorkers / 2);
-    sh.gifts = sh.armed = 0;
+    for (uint32_t i = 0; i < kLetters; ++i) {
+      mbar_init(&sh.ready[i], i == kGift ? kWorkers / 2 : kWorkers);
+      mbar_init(&sh.come[i], 1);
+      sh.sent[i] = sh.armed[i] = 0;
+    }
     mbar_init(&sh.p_empty, 1);
     mbar_init(&sh.o_empty, 2 * kWorkers);
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(&sh.met[i], 8);
-    mbar_init(&sh.agreed, 2 * kWorkers);
     mbar_init(&sh.drained, 1);
     sh.gave_up = a.wait_clocks == 0;
     sh.redo = 0;
@@ -419,9 +429,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
-  auto cluster_wait = [&](uint64_t* bar, uint32_t parity) -> bool {   // where the other CTA has written
-    return cluster_wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
-  };
   const Shares shares(a);
   const uint64_t begin = shares.from(cluster), end = cluster < shares.clusters ? shares.from(cluster + 1) : begin;
   const uint32_t tile0 = begin < end ? tile_of(a, begin) : 0;
@@ -431,7 +438,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t n = 0, q_n = 0;                               // copies; segments' queries
   uint32_t it = 0, pv = 0;                               // tiles of S; second products
   uint32_t full_n = 0, met_n = 0;                        // whole passes; exchanges of maxima
-  uint32_t gifts = 0;
+  uint32_t sent[kLetters] = {};                          // by this thread
+  PlanTile upcoming;                                     // a worker's next tile
+  uint32_t upcoming_number = UINT32_MAX;
   bool ok = true;
 
   // One segment's work for each role; max_only: only the columns' maxima.
@@ -485,11 +494,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return ok;
   };
 
+  // Letters go as bulk copies: what a warp stores to the other CTA's memory
+  // itself, and the order over the cluster behind it, takes 2,000 to 4,000 clocks.
+  // arm: one thread of the receiver, for the n-th letter of its kind; send: one
+  // thread, after everyone who wrote it has passed a proxy fence and arrived.
+  auto arm = [&](Letter kind, uint32_t n, uint32_t bytes) {
+    mbar_arrive_expect_tx(&sh.come[kind], bytes);
+    sh.armed[kind] = n + 1;
+  };
+  auto send = [&](Letter kind, uint32_t dst, uint32_t src, uint32_t bytes) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(dst), "r"(other));
+    bulk_copy_s2peer(there, src, bytes, dsmem_addr(&sh.come[kind], other));
+    ++sent[kind];
+  };
   // the weights that the other CTA sends, the p-th of them; one thread
   auto come = [&](uint32_t p) -> bool {
-    mbar_arrive_expect_tx(&sh.p_come, kHalfBytes);
-    sh.armed = p + 1;
-    return wait(&sh.p_come, p & 1);
+    arm(kGift, p, kHalfBytes);
+    return wait(&sh.come[kGift], p & 1);
+  };
+  // every worker warp has written its part of this CTA's letter, the n-th of its kind: both CTAs' are there afterwards
+  auto trade = [&](Letter kind, uint32_t n, const void* mine, uint32_t bytes) -> bool {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.ready[kind]);
+    bool there = wait(&sh.ready[kind], n & 1);
+    if (tid == 0 && there) {
+      arm(kind, n, bytes);
+      send(kind, smem_u32(mine), smem_u32(mine), bytes);
+    }
+    __syncwarp();
+    there = there && wait(&sh.come[kind], n & 1);
+    return __all_sync(0xffffffffu, there);
   };
 
   // One thread issues all of a segment's MMAs: what it does between them has
@@ -583,13 +619,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // the maxima of this warp's columns (lane c: column c's) to both CTAs, and back the whole tile's
   auto meet = [&](float best) -> float {
     sh.top[rank][quarter][quad][lane] = best;
-    dsmem_st_u32(dsmem_addr(&sh.top[rank][quarter][quad][lane], other), __float_as_uint(best));
-    __syncwarp();
-    if (lane == 0) {
-      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], place));
-      cluster_mbar_arrive(dsmem_addr(&sh.met[quarter], other));
-    }
-    ok = ok && cluster_wait(&sh.met[quarter], met_n & 1);
+    ok = ok && trade(kTop, met_n, &sh.top[rank], sizeof(sh.top[0]));
     ++met_n;
     float m = -INFINITY;
     for (uint32_t r = 0; r < 2; ++r)
@@ -715,16 +745,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (own) {
         if (lane == 0) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, leader));
       } else {
-        if (lane == 0) mbar_arrive(&sh.given);
+        if (lane == 0) mbar_arrive(&sh.ready[kGift]);
         if (warp % 8 == 0) {                             // the first of the eight warps with the other's columns
-          ok = ok && wait(&sh.given, pv & 1);
+          ok = ok && wait(&sh.ready[kGift], pv & 1);
           if (!__all_sync(0xffffffffu, ok)) return false;
-          if (lane == 0) {
-            uint32_t there;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(probs + rank * kHalfBytes), "r"(other));
-            bulk_copy_s2peer(there, gift, kHalfBytes, dsmem_addr(&sh.p_come, other));
-            ++gifts;
-          }
+          if (lane == 0) send(kGift, probs + rank * kHalfBytes, gift, kHalfBytes);
         }
       }
       ++pv;
@@ -746,28 +771,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // the sums of both CTAs' positions, and whether the segment stands
     add_lanes<32, 16>(sum, lane);
     flagged = first && __any_sync(0xffffffffu, flagged);
-    sh.sums[rank][quarter][quad][lane] = sum[0];
-    dsmem_st_u32(dsmem_addr(&sh.sums[rank][quarter][quad][lane], other), __float_as_uint(sum[0]));
-    if (lane == 0) {
-      sh.flag[rank][warp] = flagged;
-      dsmem_st_u32(dsmem_addr(&sh.flag[rank][warp], other), flagged);
-    }
-    __syncwarp();
-    if (lane == 0) {
-      cluster_mbar_arrive(dsmem_addr(&sh.agreed, place));
-      cluster_mbar_arrive(dsmem_addr(&sh.agreed, other));
-    }
+    sh.sums[rank].of[quarter][quad][lane] = sum[0];
+    if (lane == 0) sh.sums[rank].again[warp] = flagged;
     const float ref = sh.ref[quarter][lane];
-    ok = ok && cluster_wait(&sh.agreed, full_n & 1);
+    ok = ok && trade(kSum, full_n, &sh.sums[rank], sizeof(Sums));
     ++full_n;
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    // (the next tile is asked for before the results are written)
+    upcoming = plan_tile(a, g.number + 1);
+    upcoming_number = g.number + 1;
+    const bool again = __any_sync(0xffffffffu, ((volatile uint32_t*)sh.sums[lane >> 4].again)[lane & 15] != 0);
+    float total = 0.0f;
+    for (uint32_t r = 0; r < 2; ++r)
+      for (uint32_t q = 0; q < 4; ++q) total += ((volatile float*)sh.sums[r].of[quarter][q])[lane];
+    const uint32_t slot = g.slot(cluster);
     ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
-    const bool again = __any_sync(0xffffffffu, ((volatile uint32_t*)&sh.flag[0][0])[lane] != 0);
-    float total = 0.0f;
-    for (uint32_t r = 0; r < 2; ++r)
-      for (uint32_t q = 0; q < 4; ++q) total += ((volatile float*)sh.sums[r][quarter][q])[lane];
-    const uint32_t slot = g.slot(cluster);
     if (again) {
       if (tid == 0) {
         a.again[g.note(a, cluster)] = 1;                 // (both CTAs write it)
@@ -789,31 +809,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // sixteen columns of 128 values at a time (in one run the columns' results follow each other)
       const int64_t row0 = g.whole ? (int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)
                                    : (int64_t)slot * kTileColumns + leader * kColumns + quarter * 32;
+      sh.inv[quarter][lane] = inv;
+      __syncwarp();
 #pragma unroll 1
       for (uint32_t part = 0; part < 4; ++part) {
         const uint32_t c0 = part % 2 * 16, half = part / 2;
         float o[16];
         tmem_ld16(lanes + half * kPairColumns + quarter * 32 + c0, o);
         tmem_ld_wait();
+#pragma unroll
+        for (uint32_t c = 0; c < 16; c += 4) {
+          const float4 by = *reinterpret_cast<const float4*>(&sh.inv[quarter][c0 + c]);
+          o[c] *= by.x;
+          o[c + 1] *= by.y;
+          o[c + 2] *= by.z;
+          o[c + 3] *= by.w;
+        }
         const int64_t d = row0 * KVO_LATENT_BYTES + half * 256 + rank * 128 + quad * 32 + lane;
         if (!g.whole) {
           float* const out = a.part + d + c0 * KVO_LATENT_BYTES;
 #pragma unroll
-          for (uint32_t c = 0; c < 16; ++c) out[c * KVO_LATENT_BYTES] = o[c] * __shfl_sync(0xffffffffu, inv, c0 + c);
+          for (uint32_t c = 0; c < 16; ++c) out[c * KVO_LATENT_BYTES] = o[c];
         } else if (a.columns.flat) {
           __nv_bfloat16* const out = reinterpret_cast<__nv_bfloat16*>(a.out) + d + c0 * KVO_LATENT_BYTES;
+          if (columns == 32) {
 #pragma unroll
-          for (uint32_t c = 0; c < 16; ++c) {
-            const float by = __shfl_sync(0xffffffffu, inv, c0 + c);
-            if (c0 + c < columns) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+            for (uint32_t c = 0; c < 16; ++c) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c]);
+          } else {
+#pragma unroll
+            for (uint32_t c = 0; c < 16; ++c)
+              if (c0 + c < columns) out[c * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c]);
           }
         } else {
 #pragma unroll
           for (uint32_t c = 0; c < 16; ++c) {
             const uint32_t to = __shfl_sync(0xffffffffu, at, c0 + c);
-            const float by = __shfl_sync(0xffffffffu, inv, c0 + c);
             if (there >> (c0 + c) & 1)
-              reinterpret_cast<__nv_bfloat16*>(a.out)[d + (int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c] * by);
+              reinterpret_cast<__nv_bfloat16*>(a.out)[d + (int64_t)to * KVO_LATENT_BYTES] = __float2bfloat16_rn(o[c]);
           }
         }
       }
@@ -826,7 +858,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // All segments, then those that need another pass: their columns' maxima,
   // and the whole of it with them.
   for (uint32_t round = 0; round < 2; ++round) {
-    for_segments(a, begin, end, tile0, warp >= kWorkers, [&](const Segment& g) -> bool {
+    for_segments(a, begin, end, tile0, warp >= kWorkers, upcoming, upcoming_number, [&](const Segment& g) -> bool {
       if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
       for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
         const bool max_only = pass == 0;
@@ -862,7 +894,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       dsmem_st_u32(dsmem_addr(&sh.q_issued[place][load_warp], r), q_n);
     }
   }
-  if (warp < kWorkers && warp % 8 == 0 && (warp >> 3) != rank && lane == 0) dsmem_st_u32(dsmem_addr(&sh.gifts, other), gifts);
+  if (warp < kWorkers && lane == 0) {
+    if (warp % 8 == 0 && (warp >> 3) != rank) dsmem_st_u32(dsmem_addr(&sh.sent[kGift], other), sent[kGift]);
+    if (warp == 0) {
+      dsmem_st_u32(dsmem_addr(&sh.sent[kTop], other), sent[kTop]);
+      dsmem_st_u32(dsmem_addr(&sh.sent[kSum], other), sent[kSum]);
+    }
+  }
   // All CTAs end together.  Where a wait gave up in any, what is in flight
   // finishes first: the MMAs, then the copies; those that a CTA has not started
   // count as come.
@@ -877,9 +915,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       pair_commit(&sh.drained, (uint16_t)(1u << place));
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
     }
-    if (warp == 0 && lane == 0) {
-      for (uint32_t m = sh.armed; m < sh.gifts; ++m) mbar_arrive_expect_tx(&sh.p_come, kHalfBytes);
-      if (sh.gifts && !landed(&sh.p_come, (sh.gifts - 1) & 1)) atomicOr(a.status, kFlagInflight);
+    if (tid == 0) {
+      const uint32_t bytes[kLetters] = {kHalfBytes, sizeof(sh.top[0]), sizeof(Sums)};
+      for (uint32_t i = 0; i < kLetters; ++i) {
+        if (sh.armed[i] < sh.sent[i]) mbar_arrive_expect_tx(&sh.come[i], bytes[i]);   // one at most
+        if (sh.sent[i] && !landed(&sh.come[i], (sh.sent[i] - 1) & 1)) atomicOr(a.status, kFlagInflight);
+      }
     }
     if (rank == 0 && warp == kLoader && lane == 0) {
       uint32_t most = 0, least = UINT32_MAX, queried = 0;

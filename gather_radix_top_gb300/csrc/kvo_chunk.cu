@@ -300,19 +300,13 @@ struct Segment {
 };
 
 // f(segment) for every segment of a cluster's share, in order, in every warp.
-// `next` is tile `number`, if that has been asked for ahead: by most warps here,
-// but the workers do it at a segment's end, when they have registers for it.
-template <typename F>
-__device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, bool ahead,
-                                             PlanTile& next, uint32_t& number, F f) {
+// tile_at(i): tile i of the plan.
+template <typename T, typename F>
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, T tile_at, F f) {
   for (uint64_t u = begin; u < end; ++tile) {
     Segment g;
-    g.tile = number == tile ? next : plan_tile(a, tile);
+    g.tile = tile_at(tile);
     const uint64_t past = g.tile.units + g.tile.spans + kTileCost;
-    if (ahead) {
-      next = plan_tile(a, tile + 1);
-      number = tile + 1;
-    }
     g.number = tile;
     g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
     g.to = min((uint32_t)(min(past, end) - g.tile.units), g.tile.spans);
@@ -341,12 +335,12 @@ struct ChunkShared {
   uint32_t redo;                     // some segment needs another pass
   alignas(16) float top[2][4][4][32];         // per CTA, quarter of the columns and warp: maxima
   alignas(16) Sums sums[2];
-  // per column: the softmax's reference, the positions it sees, 1 / the sum of
-  // its weights.  The four warps of a quarter write the same values, after all
-  // of them have agreed on the segment before.
+  // per column: the softmax's reference, and after a segment 1 / the sum of its
+  // weights; the positions it sees.  The four warps of a quarter write the same
+  // values, when all of them have done with the ones before.
   alignas(16) float ref[4][32];
   alignas(16) uint32_t seen[4][32];
-  alignas(16) float inv[4][32];
+  PlanTile upcoming[2];              // the workers' next tile, in turns
 };
 
 // x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
@@ -439,8 +433,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t it = 0, pv = 0;                               // tiles of S; second products
   uint32_t full_n = 0, met_n = 0;                        // whole passes; exchanges of maxima
   uint32_t sent[kLetters] = {};                          // by this thread
-  PlanTile upcoming;                                     // a worker's next tile
-  uint32_t upcoming_number = UINT32_MAX;
+  uint32_t upcoming_number = UINT32_MAX;                 // the tile that the workers have asked for
   bool ok = true;
 
   // One segment's work for each role; max_only: only the columns' maxima.
@@ -644,6 +637,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t c = 0; c < 32; ++c) sum[c] = max_only ? -INFINITY : 0.0f;
     uint32_t flagged = 0;
     const float* const off = a.off + (int64_t)g.tile.seq * a.span;
+    if (warp == 0 && !max_only) {                        // the next segment's tile, there once the sums have been traded
+      if (lane < 2)
+        copy16_async(smem_u32(&sh.upcoming[full_n & 1]) + 16 * lane, reinterpret_cast<const uint4*>(a.plan + g.number + 1) + lane,
+                     true);
+      copy_async_commit();
+    }
     for (uint32_t i = g.from; i < g.to; ++i, ++it) {
       const uint32_t p = i * kSpan + mine;
       const bool gone = __ldcg(off + p) != 0.0f;
@@ -774,12 +773,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     sh.sums[rank].of[quarter][quad][lane] = sum[0];
     if (lane == 0) sh.sums[rank].again[warp] = flagged;
     const float ref = sh.ref[quarter][lane];
+    if (warp == 0) copy_async_wait<0>();
     ok = ok && trade(kSum, full_n, &sh.sums[rank], sizeof(Sums));
+    upcoming_number = g.number + 1;
     ++full_n;
     if (!__all_sync(0xffffffffu, ok)) return false;
-    // (the next tile is asked for before the results are written)
-    upcoming = plan_tile(a, g.number + 1);
-    upcoming_number = g.number + 1;
     const bool again = __any_sync(0xffffffffu, ((volatile uint32_t*)sh.sums[lane >> 4].again)[lane & 15] != 0);
     float total = 0.0f;
     for (uint32_t r = 0; r < 2; ++r)
@@ -809,7 +807,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // sixteen columns of 128 values at a time (in one run the columns' results follow each other)
       const int64_t row0 = g.whole ? (int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)
                                    : (int64_t)slot * kTileColumns + leader * kColumns + quarter * 32;
-      sh.inv[quarter][lane] = inv;
+      sh.ref[quarter][lane] = inv;
       __syncwarp();
 #pragma unroll 1
       for (uint32_t part = 0; part < 4; ++part) {
@@ -819,7 +817,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (uint32_t c = 0; c < 16; c += 4) {
-          const float4 by = *reinterpret_cast<const float4*>(&sh.inv[quarter][c0 + c]);
+          const float4 by = *reinterpret_cast<const float4*>(&sh.ref[quarter][c0 + c]);
           o[c] *= by.x;
           o[c + 1] *= by.y;
           o[c + 2] *= by.z;
@@ -856,50 +854,65 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   };
 
   // All segments, then those that need another pass: their columns' maxima,
-  // and the whole of it with them.
-  for (uint32_t round = 0; round < 2; ++round) {
-    for_segments(a, begin, end, tile0, warp >= kWorkers, upcoming, upcoming_number, [&](const Segment& g) -> bool {
-      if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
-      for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass) {
-        const bool max_only = pass == 0;
-        if (!(warp < kWorkers    ? soften(g, max_only, !round)
-              : warp >= kLoader  ? load(g, max_only)
-              : rank == 0        ? multiply(g, max_only)
-                                 : pass_on(g, max_only)))
-          return false;
+  // and the whole of it with them.  (A loop for each role, so that none keeps
+  // the others' values.)
+  auto rounds = [&](auto&& tile_at, auto&& work) {
+    for (uint32_t round = 0; round < 2; ++round) {
+      for_segments(a, begin, end, tile0, tile_at, [&](const Segment& g) -> bool {
+        if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
+        for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass)
+          if (!work(g, pass == 0, !round)) return false;
+        return true;
+      });
+      ok = __all_sync(0xffffffffu, ok);
+      __threadfence();
+      __syncthreads();
+      cluster_sync();
+      // the same answer in all CTAs: nothing changes between the barriers
+      uint32_t redo = 0, gave_up = 0;
+      for (uint32_t r = 0; r < 4; ++r) {
+        redo |= dsmem_ld_u32(dsmem_addr(&sh.redo, r));
+        gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
       }
-      return true;
-    });
-    ok = __all_sync(0xffffffffu, ok);
-    __threadfence();
-    __syncthreads();
-    cluster_sync();
-    // the same answer in all CTAs: nothing changes between the barriers
-    uint32_t redo = 0, gave_up = 0;
-    for (uint32_t r = 0; r < 4; ++r) {
-      redo |= dsmem_ld_u32(dsmem_addr(&sh.redo, r));
-      gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
+      __syncthreads();
+      cluster_sync();
+      if (!redo || gave_up) break;
     }
-    __syncthreads();
-    cluster_sync();
-    if (!redo || gave_up) break;
-  }
-
-  // no slot's release may still be on its way when the CTA ends
-  if (warp >= kLoader && lane == 0) {
-    for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
-    if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
-    for (uint32_t r = 0; r < 4; ++r) {
-      dsmem_st_u32(dsmem_addr(&sh.issued[place][load_warp], r), n);
-      dsmem_st_u32(dsmem_addr(&sh.q_issued[place][load_warp], r), q_n);
+  };
+  // most warps ask for a tile of the plan while they work on the one before
+  PlanTile next;
+  uint32_t next_number = UINT32_MAX;
+  auto ahead = [&](uint32_t i) {
+    const PlanTile t = i == next_number ? next : plan_tile(a, i);
+    next = plan_tile(a, i + 1);
+    next_number = i + 1;
+    return t;
+  };
+  if (warp < kWorkers) {
+    rounds([&](uint32_t i) { return i == upcoming_number ? sh.upcoming[(full_n - 1) & 1] : plan_tile(a, i); }, soften);
+    copy_async_wait<0>();
+    if (lane == 0) {
+      if (warp % 8 == 0 && (warp >> 3) != rank) dsmem_st_u32(dsmem_addr(&sh.sent[kGift], other), sent[kGift]);
+      if (warp == 0) {
+        dsmem_st_u32(dsmem_addr(&sh.sent[kTop], other), sent[kTop]);
+        dsmem_st_u32(dsmem_addr(&sh.sent[kSum], other), sent[kSum]);
+      }
     }
-  }
-  if (warp < kWorkers && lane == 0) {
-    if (warp % 8 == 0 && (warp >> 3) != rank) dsmem_st_u32(dsmem_addr(&sh.sent[kGift], other), sent[kGift]);
-    if (warp == 0) {
-      dsmem_st_u32(dsmem_addr(&sh.sent[kTop], other), sent[kTop]);
-      dsmem_st_u32(dsmem_addr(&sh.sent[kSum], other), sent[kSum]);
+  } else if (warp >= kLoader) {
+    rounds(ahead, [&](const Segment& g, bool max_only, bool) { return load(g, max_only); });
+    if (lane == 0) {
+      // no slot's release may still be on its way when the CTA ends
+      for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
+      if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
+      for (uint32_t r = 0; r < 4; ++r) {
+        dsmem_st_u32(dsmem_addr(&sh.issued[place][load_warp], r), n);
+        dsmem_st_u32(dsmem_addr(&sh.q_issued[place][load_warp], r), q_n);
+      }
     }
+  } else if (rank == 0) {
+    rounds(ahead, [&](const Segment& g, bool max_only, bool) { return multiply(g, max_only); });
+  } else {
+    rounds(ahead, [&](const Segment& g, bool max_only, bool) { return pass_on(g, max_only); });
   }
   // All CTAs end together.  Where a wait gave up in any, what is in flight
   // finishes first: the MMAs, then the copies; those that a CTA has not started

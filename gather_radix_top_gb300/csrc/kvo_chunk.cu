@@ -27,6 +27,8 @@
 // Tiles of columns times tiles of positions, end to end, are shared out evenly
 // over the pairs.  Where a share begins or ends inside a tile of columns, the
 // parts are joined by their log-sum-exps in a second launch.
+#include <algorithm>
+
 #include "kvo_cache.cuh"
 #include "kvo_chunk.cuh"
 #include "kvo_rows.cuh"
@@ -44,7 +46,7 @@ namespace {
 constexpr uint32_t kSpan = 256;                          // positions of a tile
 constexpr uint32_t kPairColumns = 2 * kColumns;
 constexpr uint32_t kTileColumns = 4 * kColumns;          // of a cluster
-constexpr uint32_t kTileCost = 1;                        // of a tile of columns, in tiles of positions
+constexpr uint32_t kTileCost = 2;                        // of a tile of columns, in tiles of positions
 constexpr uint32_t kWorkers = 16;
 constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
 constexpr uint32_t kLoaders = 3;                         // warps: one takes 500 clocks a copy beside the workers
@@ -67,6 +69,14 @@ struct __align__(16) PlanTile {
   uint32_t spans;            // its tiles of positions
 };
 
+// A tile that ends of shares cut, as the join takes it: of share g - 1 the part
+// that ends inside it, of g .. last those that begin there.
+struct __align__(16) Cut {
+  PlanTile tile;
+  uint32_t last;             // 0: share g is not the first to begin inside a tile
+  uint32_t pad[3];
+};
+
 struct ChunkArgs {
   CacheView cache;
   const int32_t* starts;
@@ -76,6 +86,7 @@ struct ChunkArgs {
   uint8_t* values;           // [sequences][span][576] bf16
   float* off;                // [sequences][span]: 0, or -inf where there is no row
   PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
+  Cut* cuts;                 // [clusters], from share 1 on
   uint8_t* again;            // [most_tiles] whole tiles, [2 * clusters] parts that need another pass
   float* part;               // [2 * clusters][256][512]
   float* part_lse;           // [2 * clusters][256], base 2
@@ -88,6 +99,38 @@ struct ChunkArgs {
   float far;                 // a logit this far above its reference wants another pass
   int64_t wait_clocks;
 };
+
+// ---------------------------------------------------------------- the shares
+// Cluster g's share of the work: [from(g), from(g + 1)).
+struct Shares {
+  uint64_t units;
+  uint32_t clusters;
+  __device__ __forceinline__ Shares(const ChunkArgs& a) {
+    units = __ldcg(&a.plan[a.most_tiles + 1].units);
+    clusters = (uint32_t)min((uint64_t)a.clusters, max(units / 2, (uint64_t)1));
+  }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * units / clusters : units; }
+};
+
+// The tile that unit u lies in; a whole warp.
+__device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
+  uint32_t lo = 0, hi = __ldcg(&a.plan[a.most_tiles + 1].index);   // in [lo, hi)
+  const uint32_t lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool before = at < hi && __ldcg(&a.plan[at].units) <= u;
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, before));   // lane 0's always is
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ PlanTile plan_tile(const ChunkArgs& a, uint32_t i) {
+  const uint4* const from = reinterpret_cast<const uint4*>(a.plan + i);
+  const uint4 x = __ldcg(from), y = __ldcg(from + 1);
+  return PlanTile{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
+}
 
 // ------------------------------------------------------------ rows and plan
 constexpr uint32_t kUnpackThreads = 256, kUnpackRows = 64;   // of a CTA, 8 of a warp
@@ -199,6 +242,22 @@ __device__ void make_plan(const ChunkArgs& a) {
     head.index = tiles;
     a.plan[a.most_tiles + 1] = head;
   }
+  __threadfence_block();
+  __syncthreads();
+  const Shares shares(a);
+  for (uint32_t g = 1 + warp; g < shares.clusters; g += kUnpackThreads / 32) {
+    const uint64_t at = shares.from(g);
+    const uint32_t tile = tile_of(a, at);
+    Cut cut;
+    cut.tile = plan_tile(a, tile);
+    const uint64_t from = cut.tile.units, end = from + cut.tile.spans;
+    cut.last = 0;
+    if (at > from && at < end && shares.from(g - 1) <= from) {
+      cut.last = g;
+      while (cut.last + 1 < shares.clusters && shares.from(cut.last + 1) < end) ++cut.last;
+    }
+    if (lane == 0) a.cuts[g] = cut;
+  }
 }
 
 // The rows that a tile of positions may hold as bf16.  A row that reads as NaN
@@ -253,38 +312,7 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
   }
 }
 
-// ---------------------------------------------------------------- the shares
-// Cluster g's share of the work: [from(g), from(g + 1)).
-struct Shares {
-  uint64_t units;
-  uint32_t clusters;
-  __device__ __forceinline__ Shares(const ChunkArgs& a) {
-    units = __ldcg(&a.plan[a.most_tiles + 1].units);
-    clusters = (uint32_t)min((uint64_t)a.clusters, max(units / 2, (uint64_t)1));
-  }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * units / clusters : units; }
-};
-
-// The tile that unit u lies in; a whole warp.
-__device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
-  uint32_t lo = 0, hi = __ldcg(&a.plan[a.most_tiles + 1].index);   // in [lo, hi)
-  const uint32_t lane = threadIdx.x & 31;
-  while (hi - lo > 1) {
-    const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const bool before = at < hi && __ldcg(&a.plan[at].units) <= u;
-    const uint32_t n = __popc(__ballot_sync(0xffffffffu, before));   // lane 0's always is
-    lo += (n - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-__device__ __forceinline__ PlanTile plan_tile(const ChunkArgs& a, uint32_t i) {
-  const uint4* const from = reinterpret_cast<const uint4*>(a.plan + i);
-  const uint4 x = __ldcg(from), y = __ldcg(from + 1);
-  return PlanTile{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
-}
-
+// ---------------------------------------------------------------- the segments
 // A share's part of one tile of columns: tiles of positions [from, to).
 struct Segment {
   PlanTile tile;
@@ -972,71 +1000,79 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == kMma) pair_tmem_free(tmem, 512);
 }
 
-// A tile that shares' ends cut: blocks (g - 1, ..) join its parts if share g is
-// the first to begin inside it.  Two columns at a time, 128 threads each.
-constexpr uint32_t kJoinColumns = 16;                    // of a block
+// Joins the parts of a cut tile by their log-sum-exps: blocks (g - 1, ..) those
+// that share g is the first to cut, four columns of 128 threads each.
+constexpr uint32_t kJoinColumns = 4, kMostParts = 64;
 
-__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
-  const uint32_t g = blockIdx.x + 1, d = threadIdx.x & 127;
+__global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
+  const uint32_t g = blockIdx.x + 1, d = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t column = blockIdx.y * kJoinColumns + (threadIdx.x >> 7);
   wait_previous_grid();
-  const Shares shares(a);
-  if (g >= shares.clusters) return;
-  const uint64_t at = shares.from(g);
-  const uint32_t tile = tile_of(a, at);
-  const PlanTile t = plan_tile(a, tile);
-  const uint64_t end = t.units + t.spans;
-  if (at == t.units || at >= end || shares.from(g - 1) > t.units) return;
-  uint32_t last = g;                                     // the last share that begins inside the tile
-  while (last + 1 < shares.clusters && shares.from(last + 1) < end) ++last;
-  // parts: of share g - 1 the one that ends inside, of the others the one that begins there
-  auto slot = [&](uint32_t p) { return 2 * p + (p == g - 1); };
-  for (uint32_t i = 0; i < kJoinColumns; i += 2) {
-    const uint32_t column = blockIdx.y * kJoinColumns + i + (threadIdx.x >> 7);
-    uint32_t where;
-    const uint32_t token = column_at(a, t, 4 * t.index + column / kColumns, column % kColumns, &where);
-    if (token >= t.tokens) continue;
-    float top = -INFINITY;
-    for (uint32_t p = g - 1; p <= last; ++p) top = fmaxf(top, __ldcg(a.part_lse + slot(p) * kTileColumns + column));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float total = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (g >= Shares(a).clusters) return;
+  const uint32_t last = __ldcg(&a.cuts[g].last);
+  if (last == 0) return;
+  const uint4 *const cut = reinterpret_cast<const uint4*>(a.cuts + g), x = __ldcg(cut), y = __ldcg(cut + 1);
+  const PlanTile t{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
+  uint32_t where;
+  const uint32_t token = column_at(a, t, 4 * t.index + column / kColumns, column % kColumns, &where);
+  if (token >= t.tokens) return;                         // (the same for a column's warps)
+  const uint32_t parts = last - g + 2;
+  auto row_of = [&](uint32_t i) { return (2 * (g - 1 + i) + (i == 0)) * kTileColumns + column; };
+  // lane l has the weights of parts l and l + 32
+  float l0 = lane < parts ? __ldcg(a.part_lse + row_of(lane)) : -INFINITY;
+  float l1 = lane + 32 < parts ? __ldcg(a.part_lse + row_of(lane + 32)) : -INFINITY;
+  float top = fmaxf(l0, l1);
+#pragma unroll
+  for (uint32_t e = 16; e; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+  const float base = top == -INFINITY ? 0.0f : top;
+  l0 = exp2f(l0 - base);
+  l1 = exp2f(l1 - base);
+  float total = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (uint32_t p = g - 1; p <= last; ++p) {
-      const uint32_t from = slot(p) * kTileColumns + column;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)from * KVO_LATENT_BYTES) + d);
-      const float w = exp2f(__ldcg(a.part_lse + from) - base);
-      if (!(w > 0.0f) && !isnan(w)) continue;
-      total += w;
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
-    }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const int64_t row = (int64_t)t.first * a.heads + where;
-    reinterpret_cast<uint2*>(a.out + row * KVO_LATENT_BYTES)[d] =
-        make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-    if (a.lse && d == 0) a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
+  for (uint32_t i = 0; i < parts; ++i) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)row_of(i) * KVO_LATENT_BYTES) + d);
+    const float w = __shfl_sync(0xffffffffu, i < 32 ? l0 : l1, i & 31);
+    if (!(w > 0.0f) && !isnan(w)) continue;
+    total += w;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
   }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t row = (int64_t)t.first * a.heads + where;
+  reinterpret_cast<uint2*>(a.out + row * KVO_LATENT_BYTES)[d] =
+      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+  if (a.lse && d == 0) a.lse[row] = total == 0.0f ? -INFINITY : (base + log2f(total)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ the host
-// Whether a call has enough columns a sequence.
+// Whether unpacking the rows pays.  Per 1,000 rows of a sequence the kernel for
+// few columns takes about 0.29 us for every 64 columns, this one 0.36 us for
+// every 256 and 0.40 us to unpack them, and about 20 us more a call.  Both
+// ways, us: 16 sequences of 8,192 rows with 128 columns each 89 and 131, with
+// 256 165 and 134; one of 50,000 rows with 256 64 and 70, with 512 110 and 86;
+// 1,024 columns over 4,000 rows 31 and 40, over 50,000 216 and 121.
 bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
-  return tokens * heads >= 256 * busy && sequences * span <= INT32_MAX;
+  if (sequences * span > INT32_MAX) return false;
+  const int64_t columns = (tokens * heads + busy - 1) / busy, each = (tokens + busy - 1) / busy;
+  const int64_t seen = rows - std::min(each, rows) / 2;  // of the middle token
+  const int64_t gain = 29 * ((columns + 63) / 64) - 36 * ((columns + 255) / 256) - 40;
+  return gain > 0 && (double)busy * (double)seen * (double)gain > 2e6;
 }
 
 struct Layout {              // of the scratch
   int64_t span, tiles, clusters;
-  int64_t values, off, plan, again, part, part_lse, bytes;
+  int64_t values, off, plan, cuts, again, part, part_lse, bytes;
 };
 
 Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   Layout l;
   l.span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
-  l.clusters = device_sms() / 4;
+  l.clusters = std::min(device_sms() / 4, (int)kMostParts);
   // Tiles of either way to fill them: at worst 33 heads of one token a half.
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t deep = heads < kColumns ? kColumns / heads : 1, across = heads > kColumns ? 2 : 1;
@@ -1052,6 +1088,7 @@ Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows
   l.values = take(sequences * l.span * kValueBytes);
   l.off = take(sequences * l.span * 4);
   l.plan = take((l.tiles + 2) * (int64_t)sizeof(PlanTile));
+  l.cuts = take(l.clusters * (int64_t)sizeof(Cut));
   l.again = take(l.tiles + 2 * l.clusters);
   l.part = take(2 * l.clusters * kTileColumns * KVO_LATENT_BYTES * 4);
   l.part_lse = take(2 * l.clusters * kTileColumns * 4);
@@ -1094,7 +1131,8 @@ cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap
   lc.numAttrs = 2;
   e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, vmap);
   if (e != cudaSuccess || a.clusters < 2) return e;
-  return launch_early(join_parts_kernel, dim3(a.clusters - 1, kTileColumns / kJoinColumns), 256, 0, stream, a);
+  return launch_early(join_parts_kernel, dim3(a.clusters - 1, kTileColumns / kJoinColumns), 128 * kJoinColumns, 0,
+                      stream, a);
 }
 
 }  // namespace
@@ -1140,6 +1178,7 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.values = work + l.values;
   a.off = reinterpret_cast<float*>(work + l.off);
   a.plan = reinterpret_cast<PlanTile*>(work + l.plan);
+  a.cuts = reinterpret_cast<Cut*>(work + l.cuts);
   a.again = work + l.again;
   a.part = reinterpret_cast<float*>(work + l.part);
   a.part_lse = reinterpret_cast<float*>(work + l.part_lse);

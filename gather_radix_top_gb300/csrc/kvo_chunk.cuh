@@ -59,23 +59,23 @@ __device__ __forceinline__ ChunkTile chunk_tile(const int32_t* starts, uint32_t 
   return ChunkTile{-1, 0, 0, 0};
 }
 
-// How a chunk's columns fill tiles of 64.  Where a token's heads and the
+// How a chunk's columns fill tiles of `size`.  Where a token's heads and the
 // tokens themselves are evenly spaced, all (token, head) pairs are one run; else a
 // tile is `wide` heads of `deep` tokens.
 struct Columns {
   uint32_t flat;             // 1: one run
-  uint32_t wide, deep;       // wide * deep <= 64 columns
+  uint32_t wide, deep;       // wide * deep <= size columns
   uint32_t across;           // tiles across the heads
   Divider by_wide;
 };
 constexpr uint32_t kColumns = 64;
 constexpr int64_t kMaxQueryLd = (int64_t)1 << 38;         // elements: strides of a tensor map end at 2^40 bytes
 
-inline Columns columns_of(uint32_t heads, int64_t q_ld, int64_t q_head_ld, int64_t tokens) {
+inline Columns columns_of(uint32_t heads, int64_t q_ld, int64_t q_head_ld, int64_t tokens, uint32_t size = kColumns) {
   Columns c = {};
   c.flat = tokens == 1 || q_ld == heads * q_head_ld;
-  c.wide = c.flat ? 1 : heads < kColumns ? heads : kColumns;
-  c.deep = kColumns / c.wide;
+  c.wide = c.flat ? 1 : heads < size ? heads : size;
+  c.deep = size / c.wide;
   c.across = c.flat ? 1 : (heads + c.wide - 1) / c.wide;
   c.by_wide = divider(c.wide);
   return c;

@@ -163,14 +163,8 @@ __device__ __forceinline__ void pair_tmem_free(uint32_t base, uint32_t cols) {
 }
 
 // An arrival at a barrier of another CTA of the cluster (or this one), given
-// its cluster address: after this thread's accesses to shared memory anywhere
-// in the cluster.
-__device__ __forceinline__ void cluster_mbar_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// The same after this thread's accesses to its own CTA's memory only: for
-// operands there, which its own tensor core reads.  (The order over the whole
+// its cluster address, after this thread's accesses to its own CTA's memory: for
+// operands there, which its own tensor core reads.  (An order over the whole
 // cluster takes about 2,200 clocks.)
 __device__ __forceinline__ void cluster_mbar_arrive_own(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -188,32 +182,6 @@ __device__ __forceinline__ void bulk_copy_s2peer(uint32_t dst, uint32_t src, uin
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "r"(src), "r"(bytes), "r"(bar)
                : "memory");
-}
-
-// As wait_or_give_up, for a phase that threads of the other CTA complete.
-__device__ __forceinline__ bool cluster_wait_or_give_up(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up,
-                                                        long long clocks) {
-  const uint32_t a = smem_u32(bar);
-  uint32_t done;
-  long long start = 0;
-  for (uint32_t i = 0;; ++i) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((i & 15u) == 15u) {
-      if (*gave_up) return false;
-      const long long now = clock64();
-      if (start == 0) start = now;
-      if (now - start > clocks) {
-        *gave_up = 1;
-        return false;
-      }
-    }
-  }
 }
 
 // A box of a three-dimensional tensor map to this CTA's shared memory at

@@ -4,17 +4,22 @@
 // over the (token, head) columns c whose token sees position p.
 //
 // Two CTAs of a cluster hold 128 positions each, dequantised once, and walk
-// over the columns in tiles of 128: S [256 positions x 128 columns] = K Q^T as
+// over the columns in tiles of 64 or 128: S [256 positions x columns] = K Q^T as
 // pair MMAs, for which each CTA brings half of a tile's queries.  A position is
 // a lane of S, so its sum over the columns stays in one thread's register.
-// Shared memory holds the positions (144 KB) and a ring of nine pieces of 64
-// columns by 64 values; tensor memory four tiles of S.
+// Shared memory holds the positions (144 KB), a ring of 32 KB for the queries'
+// pieces (64 values of a CTA's columns), and the next 64 raw rows, which come by
+// bulk copies in four groups of 16, each with its own four warps: they take
+// them to registers, let the next ones come, and store the dequantised ones
+// when the MMAs of the positions before have ended.  Tensor memory holds four
+// tiles of S.
 //
 // A thread's sum over a tile is added to its running sum with the rounding
 // error carried along, so that many tokens lose nothing.
 //
-// Where a call's positions do not fill the GPU, the columns are split over
-// several pairs, whose sums a second launch adds in their order.
+// Tiles of positions times tiles of columns, end to end, are shared out evenly
+// over the pairs.  Where a share begins or ends inside a tile of positions, a
+// second launch adds the parts in their order.
 #include "kvo_cache.cuh"
 #include "kvo_chunk.cuh"
 #include "kvo_rows.cuh"
@@ -24,15 +29,16 @@ namespace kvo {
 namespace {
 
 constexpr uint32_t kTile = 128;                          // positions of a CTA
-constexpr uint32_t kTileColumns = 2 * kColumns;          // of a pair
+constexpr uint32_t kSpan = 2 * kTile;                    // of a pair
+constexpr uint32_t kHalf = 64;                           // rows that come together
 constexpr uint32_t kWorkers = 16;                        // warps: four for each quarter of the columns
-constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
-constexpr uint32_t kWeightThreads = (kLoader + 1) * 32;
+constexpr uint32_t kMma = kWorkers, kQuery = kWorkers + 1, kLoader = kWorkers + 2, kLoaders = 2;
+constexpr uint32_t kWeightThreads = (kLoader + kLoaders) * 32;
 constexpr uint32_t kPieceBytes = kTile * 128;            // 64 values of every position
-constexpr uint32_t kSlotBytes = kColumns * 128;          // 64 values of a CTA's columns
-constexpr uint32_t kSlots = 9, kAhead = 4;               // ring of slots, tiles of S
-constexpr uint32_t kWeightSmem = 1024 + 9 * kPieceBytes + kSlots * kSlotBytes;
-constexpr uint32_t kPairGrid = 2 * kTile;                // positions of a pair
+constexpr uint32_t kRingBytes = 32768, kAhead = 4;       // queries; tiles of S
+constexpr uint32_t kPitch = KVO_ROW_BYTES + 16;          // of a raw row
+constexpr uint32_t kWeightSmem = 1024 + 9 * kPieceBytes + kRingBytes + kHalf * kPitch;
+constexpr uint32_t kTileCost = 3;                        // of a tile of positions, in tiles of columns
 
 struct WeightArgs {
   CacheView cache;
@@ -41,84 +47,140 @@ struct WeightArgs {
   const float* lse;
   const float* carry;        // or NULL
   float* out;
-  float* part;               // [splits][sequences][rows], with several splits
+  float* part;               // [2 * pairs][256]: of shares that begin, or end, inside a tile of positions
   uint32_t* status;
   int64_t carry_ld, out_ld;
-  uint32_t rows, tokens, heads, window, splits;
+  uint32_t rows, tokens, heads, window, pairs;
   Divider by_heads;
-  Columns columns;
+  Columns columns;           // of a CTA's half of a tile
   float scale;               // times log2(e)
   float keep;
   int64_t wait_clocks;
 };
 
+template <uint32_t kSlots>
 struct WeightShared {
-  uint64_t k_full, full[kSlots], empty[kSlots], s_full[kAhead], s_empty[kAhead], drained;
+  uint64_t k_full, k_empty, full[kSlots], empty[kSlots], s_full[kAhead], s_empty[kAhead], raw_full[4], raw_empty[4], summed, drained;
   uint32_t tmem, gave_up;
-  uint32_t issued[2];                // slots that each CTA's loader has filled
-  float lse[kWorkers][32];           // per warp and column, base 2
-  int32_t seen[kWorkers][32];        // and the positions it sees
-  float sums[4][kTile];
+  uint32_t issued[2];                // queries' pieces that each CTA has asked for
+  uint32_t brought[4];               // halves that each group's rows have come for
+  uint32_t there[3][4];              // per job in turns: rows that are not masked, row r is bit r % 32 of word r / 32
+  alignas(16) float lse[kWorkers][32];   // per warp and column, base 2
+  alignas(16) int32_t seen[kWorkers][32];    // and the positions it sees
+  float sums[2][3][kTile];           // per job in turns: of the quarters 1 to 3
 };
 
-// The columns of one sequence and the tiles of them that a CTA pair takes.
+// A sequence's columns.
 struct Run {
   uint32_t first, tokens;            // of the sequence
   int32_t before;                    // token i sees the first before + i positions
   uint32_t from;                     // the first token that counts
-  uint32_t begin, end;               // tiles of 128 columns
+  uint32_t len;                      // positions held
+  uint32_t begin, end;               // tiles of columns that count, for position 0
+
+  __device__ __forceinline__ Run(const WeightArgs& a, uint32_t s) {
+    const int32_t b = a.starts[s], e = a.starts[s + 1], T = (int32_t)a.tokens, held = max(a.lens[s], 0);
+    if (b < 0 || b > T || e < b || e > T) atomicOr(a.status, kFlagRange);
+    first = (uint32_t)min(max(b, 0), T);
+    tokens = (uint32_t)min(max(e, (int32_t)first), T) - first;
+    len = (uint32_t)min(held, (int32_t)a.rows);
+    before = min(held, INT32_MAX - 1) - (int32_t)tokens + 1;
+    from = max(a.window && a.window < tokens ? tokens - a.window : 0, sees(0));
+    const Columns& c = a.columns;
+    const uint32_t units = c.flat ? tokens * a.heads : tokens;
+    begin = tile_of(a, from);
+    end = len && from < tokens ? ((units + c.deep - 1) / c.deep * c.across + 1) / 2 : begin;
+  }
+  // The first token that sees position p.
+  __device__ __forceinline__ uint32_t sees(uint32_t p) const { return (uint32_t)max((int32_t)p - before + 1, 0); }
+  __device__ __forceinline__ uint32_t tile_of(const WeightArgs& a, uint32_t token) const {
+    const Columns& c = a.columns;
+    return (c.flat ? token * a.heads : token) / c.deep * c.across / 2;
+  }
+  __device__ __forceinline__ uint32_t tiles() const { return end - begin; }
+  __device__ __forceinline__ uint32_t spans() const { return tiles() ? (len + kSpan - 1) / kSpan : 0; }
+  __device__ __forceinline__ uint64_t work() const { return (uint64_t)spans() * (tiles() + kTileCost); }
 };
 
-__device__ __forceinline__ void run_of(const WeightArgs& a, uint32_t s, uint32_t p0, uint32_t split, Run* r) {
-  const int32_t b = a.starts[s], e = a.starts[s + 1], T = (int32_t)a.tokens;
-  if (b < 0 || b > T || e < b || e > T) atomicOr(a.status, kFlagRange);
-  r->first = (uint32_t)min(max(b, 0), T);
-  r->tokens = (uint32_t)min(max(e, (int32_t)r->first), T) - r->first;
-  const int32_t n = (int32_t)r->tokens;
-  r->before = min(max(a.lens[s], 0), INT32_MAX - 1) - n + 1;
-  const int32_t sees = max((int32_t)p0 - r->before + 1, 0);   // the first token that sees position p0
-  r->from = (uint32_t)max(a.window && a.window < r->tokens ? n - (int32_t)a.window : 0, sees);
-  const Columns& c = a.columns;
-  const uint32_t units = c.flat ? r->tokens * a.heads : r->tokens, skip = c.flat ? r->from * a.heads : r->from;
-  const uint32_t halves = (units + c.deep - 1) / c.deep * c.across;
-  const uint32_t t0 = r->from < r->tokens ? skip / c.deep * c.across / 2 : 0;
-  const uint32_t t1 = r->from < r->tokens ? (halves + 1) / 2 : 0;
-  const uint32_t share = (t1 - t0 + a.splits - 1) / a.splits;
-  r->begin = min(t0 + split * share, t1);
-  r->end = min(r->begin + share, t1);
+// Part of the columns of one tile of positions.
+struct Job {
+  uint32_t seq, p0;                  // the pair's first position
+  uint32_t begin, end;               // tiles of columns
+  uint32_t slot;                     // of part, or UINT32_MAX: all of its columns
+};
+
+// All sequences' work, 32 of them at a time: f(first sequence, work before it and the lanes' after it).
+template <typename F>
+__device__ __forceinline__ uint64_t for_work(const WeightArgs& a, F f) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint64_t before = 0;
+  for (uint32_t s0 = 0; s0 < a.cache.sequences; s0 += 32) {
+    uint64_t upto = s0 + lane < a.cache.sequences ? Run(a, s0 + lane).work() : 0;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d <<= 1) {
+      const uint64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (!f(s0, before, upto)) break;
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return before;
 }
 
+struct Shares {
+  uint64_t work;
+  uint32_t pairs;
+  __device__ __forceinline__ Shares(const WeightArgs& a) {
+    work = for_work(a, [](uint32_t, uint64_t, uint64_t) { return true; });
+    pairs = (uint32_t)min((uint64_t)a.pairs, max(work / (kTileCost + 1), (uint64_t)1));
+  }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * work / pairs : work; }
+};
+
+// f(job, run) for every job of the pair's share [lo, hi), in order, in every warp.
+template <typename F>
+__device__ __forceinline__ void for_jobs(const WeightArgs& a, uint32_t pair, uint64_t lo, uint64_t hi, F f) {
+  if (lo >= hi) return;
+  bool go = true;
+  for_work(a, [&](uint32_t s0, uint64_t before, uint64_t upto) {
+    for (uint32_t i = 0; i < 32 && s0 + i < a.cache.sequences && go; ++i) {
+      const uint64_t end = before + __shfl_sync(0xffffffffu, upto, i);
+      const uint64_t from = i ? before + __shfl_sync(0xffffffffu, upto, i - 1) : before;
+      if (end <= lo || from == end) continue;
+      if (from >= hi) return false;
+      const Run run(a, s0 + i);
+      const uint32_t tiles = run.tiles();
+      const uint64_t cost = tiles + kTileCost, stop = min(hi, end) - from;
+      uint64_t u = lo > from ? lo - from : 0;
+      for (uint32_t j = (uint32_t)(u / cost); u < stop && go; ++j) {
+        const uint64_t start = j * cost;
+        const uint32_t x = (uint32_t)min(u - start, (uint64_t)tiles), y = (uint32_t)min(stop - start, (uint64_t)tiles);
+        u = start + cost;
+        if (x == y) continue;
+        Job job{s0 + i, j * kSpan, run.begin + x, run.begin + y, UINT32_MAX};
+        if (y - x < tiles) job.slot = 2 * pair + (x == 0);
+        job.begin = max(job.begin, run.tile_of(a, max(run.from, run.sees(job.p0))));   // columns that see none of them
+        go = f(job, run);
+      }
+    }
+    return go;
+  });
+}
+
+// kC: a CTA's columns of a tile, 32 or 64.
+template <uint32_t kC>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weights_kernel(const __grid_constant__ WeightArgs a, const __grid_constant__ CUtensorMap qmap) {
+  constexpr uint32_t kSlotBytes = kC * 128, kSlots = kRingBytes / kSlotBytes;
+  constexpr uint32_t kMine = kC / 2;                     // columns of a worker warp
   extern __shared__ uint8_t raw[];
-  __shared__ WeightShared sh;
-  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
-  const uint32_t s = blockIdx.y, split = (blockIdx.x >> 1) % a.splits;
-  const uint32_t pair0 = (blockIdx.x >> 1) / a.splits * kPairGrid, p0 = pair0 + rank * kTile;
-  const uint32_t keys = (smem_u32(raw) + 1023u) & ~1023u, ring = keys + 9 * kPieceBytes;
+  __shared__ WeightShared<kSlots> sh;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank(), pair = blockIdx.x >> 1;
+  const uint32_t keys = (smem_u32(raw) + 1023u) & ~1023u, ring = keys + 9 * kPieceBytes, stage = ring + kRingBytes;
 
-  wait_previous_grid();
-  allow_next_grid();
-  const uint32_t len = (uint32_t)min(max(a.lens[s], 0), (int32_t)a.rows);
-  float* const part = a.part + ((int64_t)split * a.cache.sequences + s) * a.rows;
-  Run run;
-  run_of(a, s, pair0, split, &run);
-  if (pair0 >= len || run.begin == run.end) {            // the same in both CTAs
-    const uint32_t p = p0 + tid;
-    if (tid < kTile && p < a.rows) {
-      if (a.splits > 1)
-        part[p] = 0.0f;
-      else
-        a.out[s * a.out_ld + p] = p < len && a.carry ? a.keep * a.carry[s * a.carry_ld + p] : 0.0f;
-    }
-    return;
-  }
-
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
-  };
   if (tid == 0) {
     mbar_init(&sh.k_full, 2 * kWorkers);
+    mbar_init(&sh.k_empty, 1);
     for (uint32_t i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
@@ -127,6 +189,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 2 * kWorkers);
     }
+    for (uint32_t i = 0; i < 4; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 4);
+      sh.brought[i] = 0;
+    }
+    mbar_init(&sh.summed, kWorkers);
     mbar_init(&sh.drained, 1);
     sh.gave_up = a.wait_clocks == 0;
     sh.issued[0] = sh.issued[1] = 0;
@@ -137,166 +205,250 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  wait_previous_grid();
+  allow_next_grid();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
+  };
+  const Shares shares(a);
+  const uint64_t lo = shares.from(pair), hi = pair < shares.pairs ? shares.from(pair + 1) : lo;
   const Columns& cols = a.columns;
   const uint32_t box = cols.wide * cols.deep * 128;      // bytes of a slot that a copy fills
+  uint32_t n = 0, t = 0, jobs = 0;                       // pieces, tiles of S, jobs so far
+  bool ok = true;
 
-  // Piece k of tile t's queries to their slot: the n-th of this CTA's copies.
-  auto bring = [&](uint32_t n) {
-    const uint32_t tile = run.begin + n / 9, piece = n % 9, slot = n % kSlots, half = 2 * tile + rank;
-    if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
-    const uint32_t row = half / cols.across, head = half % cols.across * cols.wide;
-    pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)(piece * 64), (int32_t)head,
-                  (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep), dsmem_addr(&sh.full[slot], 0));
-  };
-
-  if (warp == kLoader) {
-    if (lane == 0) {
-      const uint32_t all = (run.end - run.begin) * 9;
-      uint32_t n = 0;
-      for (; n < all; ++n) {
-        if (n >= kSlots && !wait(&sh.empty[n % kSlots], (n / kSlots - 1) & 1)) break;
-        bring(n);
+  if (warp >= kLoader) {
+    // Rows: lane l of warp w brings row 32 w + l of a half; 16 lanes are a group.
+    const uint32_t r = (warp - kLoader) * 32 + lane, group = r / 16, dst = stage + r * kPitch;
+    uint32_t halves = 0;
+    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
+      int64_t row[2];
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) {
+        const uint32_t p = job.p0 + rank * kTile + h * kHalf + r;
+        row[h] = p < run.len ? cache_row(a.cache, job.seq, p) : -1;
+        if (p < run.len && row[h] < 0) atomicOr(a.status, kFlagRange);
       }
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h, ++halves) {
+        if (halves) ok = ok && wait(&sh.raw_empty[group], (halves - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const uint32_t there = __ballot_sync(0xffffffffu, row[h] >= 0);
+        if (row[h] < 0) {
+          for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
+          fence_proxy_async_smem();                      // before a later half's copy to the same place
+        }
+        __syncwarp();
+        if (lane == 0) sh.there[jobs % 3][2 * h + r / 32] = there;   // (a slow warp may be two jobs behind)
+        __syncwarp();
+        if (lane % 16 == 0) {
+          mbar_arrive_expect_tx(&sh.raw_full[group], __popc(there >> lane & 0xffffu) * KVO_ROW_BYTES);
+          sh.brought[group] = halves + 1;
+        }
+        __syncwarp();
+        if (row[h] >= 0)
+          bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row[h] * KVO_ROW_BYTES, KVO_ROW_BYTES, &sh.raw_full[group]);
+      }
+      ++jobs;
+      return true;
+    });
+  } else if (warp == kQuery) {
+    // the queries' pieces
+    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
+      if (lane == 0) {
+        for (uint32_t tile = job.begin; tile < job.end && ok; ++tile) {
+          const uint32_t half = 2 * tile + rank, row = half / cols.across, head = half % cols.across * cols.wide;
+          const int32_t z = (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep);
+          for (uint32_t piece = 0; piece < 9; ++piece, ++n) {
+            const uint32_t slot = n % kSlots;
+            if (n >= kSlots) ok = wait(&sh.empty[slot], (n / kSlots - 1) & 1);
+            if (!ok) break;
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
+            pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)(piece * 64), (int32_t)head, z, dsmem_addr(&sh.full[slot], 0));
+          }
+        }
+      }
+      return (bool)__shfl_sync(0xffffffffu, ok, 0);
+    });
+    if (lane == 0) {
       // no slot's release may still be on its way when the CTA ends
-      for (uint32_t m = all > kSlots ? all - kSlots : 0; n == all && m < all; ++m)
-        if (!wait(&sh.empty[m % kSlots], m / kSlots & 1)) break;
-      dsmem_st_u32(dsmem_addr(&sh.issued[rank], 0), n);  // both counts are looked at by both CTAs
+      for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
+      dsmem_st_u32(dsmem_addr(&sh.issued[rank], 0), n);  // both counts are looked at by rank 0
       dsmem_st_u32(dsmem_addr(&sh.issued[rank], 1), n);
     }
   } else if (warp == kMma) {
-    if (rank == 0) {
-      constexpr uint32_t kDesc = pair_desc(1, kTileColumns, false, false);
-      const uint64_t k_tile = tile_desc(keys, 16), q_ring = tile_desc(ring, 16);
-      bool ok = cluster_wait_or_give_up(&sh.k_full, 0, &sh.gave_up, a.wait_clocks);
-      uint32_t n = 0;
-      for (uint32_t t = 0; t < run.end - run.begin && __all_sync(0xffffffffu, ok); ++t) {
-        const uint32_t buf = t % kAhead;
-        if (t >= kAhead) ok = wait(&sh.s_empty[buf], (t / kAhead - 1) & 1);
-        tc_fence_after();
-        for (uint32_t piece = 0; piece < 9; ++piece, ++n) {
-          const uint32_t slot = n % kSlots;
-          ok = ok && wait(&sh.full[slot], n / kSlots & 1);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          if (elect_one()) {
+    if (rank == 0)
+      for_jobs(a, pair, lo, hi, [&](const Job& job, const Run&) {
+        constexpr uint32_t kDesc = pair_desc(1, 2 * kC, false, false);
+        const uint64_t k_tile = tile_desc(keys, 16), q_ring = tile_desc(ring, 16);
+        const uint32_t tiles = job.end > job.begin ? job.end - job.begin : 0;
+        if (elect_one()) {
+          ok = wait(&sh.k_full, jobs & 1);
+          uint32_t slot = n % kSlots, turn = n / kSlots & 1;
+          for (uint32_t i = 0, at = t; i < tiles && ok; ++i, ++at) {
+            const uint32_t buf = at % kAhead;
+            if (at >= kAhead) ok = wait(&sh.s_empty[buf], (at / kAhead - 1) & 1);
+            tc_fence_after();
+#pragma unroll 3
+            for (uint32_t piece = 0; piece < 9 && ok; ++piece) {
+              ok = wait(&sh.full[slot], turn);
+              if (!ok) break;
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k)
-              pair_mma_bf16(tmem + buf * kTileColumns, k_tile + piece * (kPieceBytes >> 4) + 2 * k,
-                            q_ring + slot * (kSlotBytes >> 4) + 2 * k, kDesc, piece + k > 0);
-            pair_commit(&sh.empty[slot], 3);
-            if (piece == 8) pair_commit(&sh.s_full[buf], 3);
+              for (uint32_t k = 0; k < 4; ++k)
+                pair_mma_bf16(tmem + buf * (2 * kC), k_tile + piece * (kPieceBytes >> 4) + 2 * k,
+                              q_ring + slot * (kSlotBytes >> 4) + 2 * k, kDesc, piece + k > 0);
+              pair_commit(&sh.empty[slot], 3);
+              if (++slot == kSlots) {
+                slot = 0;
+                turn ^= 1;
+              }
+            }
+            if (ok) pair_commit(&sh.s_full[buf], 3);
           }
-          __syncwarp();
+          if (ok) pair_commit(&sh.k_empty, 3);
         }
-      }
-    }
+        ok = __all_sync(0xffffffffu, ok);
+        n += 9 * tiles;
+        t += tiles;
+        ++jobs;
+        return ok;
+      });
   } else {
     // positions: piece `piece` of each 128 latent bytes of rows slot and slot + 64
-    const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3);
-    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1);
+    const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3), group = warp / 4;
+    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), from = stage + slot * kPitch;
     const uint32_t to_lo = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3));
     const uint32_t to_hi = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + 1);
     const uint32_t to_rope = keys + 8 * kPieceBytes + swizzled(slot, piece);
-    uint4 lat[2][4], rope[2], eight[2];
-#pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) {
-      const uint32_t p = p0 + slot + 64 * u;
-      const int64_t row = p < len ? cache_row(a.cache, s, p) : -1;
-      const uint4* from = reinterpret_cast<const uint4*>(a.cache.rows) + row * (KVO_ROW_BYTES / 16);
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      for (uint32_t k = 0; k < 4; ++k) lat[u][k] = row >= 0 ? __ldg(from + 8 * k + piece) : none;
-      eight[u] = row >= 0 ? __ldg(from + KVO_LATENT_BYTES / 16) : none;
-      rope[u] = row >= 0 ? __ldg(from + KVO_LATENT_BYTES / 16 + 1 + piece) : none;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) {
-      const uint32_t pick = piece >= 4 ? 0x7632u : 0x5410u;
-      const uint32_t scales[2] = {__byte_perm(eight[u].x, eight[u].y, pick), __byte_perm(eight[u].z, eight[u].w, pick)};
-#pragma unroll
-      for (uint32_t k = 0; k < 4; ++k) {
-        const uint16_t scale = (uint16_t)(scales[k >> 1] >> (k & 1) * 16);
-        const float bias = -1152.0f * __half2float(__ushort_as_half(scale));
-        uint4 x, y;
-        dequant4(lat[u][k].x, scale, bias, x.x, x.y);
-        dequant4(lat[u][k].y, scale, bias, x.z, x.w);
-        dequant4(lat[u][k].z, scale, bias, y.x, y.y);
-        dequant4(lat[u][k].w, scale, bias, y.z, y.w);
-        sts16(to_lo + 2 * k * kPieceBytes + u * 8192, x);
-        sts16(to_hi + 2 * k * kPieceBytes + u * 8192, y);
-      }
-      sts16(to_rope + u * 8192, rope[u]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) cluster_mbar_arrive(dsmem_addr(&sh.k_full, 0));
-
-    // this thread: position p0 + quad * 32 + lane against 32 columns of a tile
-    const uint32_t quad = warp & 3, quarter = warp >> 2, mine = p0 + quad * 32 + lane;
-    const bool there = mine < len && cache_row(a.cache, s, mine) >= 0;
-    if (quarter == 0 && mine < len && !there) atomicOr(a.status, kFlagRange);
-    // lane l looks up column 32 * quarter + l: its half of a tile, and where it lies in it
-    const uint32_t in_half = quarter % 2 * 32 + lane, deep = divide(in_half, cols.by_wide);
+    // scores: position quad * 32 + lane against the columns quarter * kMine + c of a tile
+    const uint32_t quad = warp & 3, quarter = warp >> 2;
+    const uint32_t in_half = quarter % 2 * kMine + lane % kMine, deep = divide(in_half, cols.by_wide);
     const uint32_t wide = in_half - deep * cols.wide;
-    auto column = [&](uint32_t t, float* lse, int32_t* seen) {
-      *lse = 0.0f;
-      *seen = 0;
-      if (t >= run.end || deep >= cols.deep) return;
-      const uint32_t half = 2 * t + quarter / 2, row = half / cols.across * cols.deep + deep;
-      const uint32_t head = half % cols.across * cols.wide + wide;
-      const uint32_t at = cols.flat ? row : row * a.heads + head, token = divide(at, a.by_heads);
-      if (token < run.from || token >= run.tokens || (!cols.flat && head >= a.heads)) return;
-      const float l = __ldg(a.lse + (int64_t)run.first * a.heads + at);
-      if (l == -INFINITY) return;
-      *lse = l * kLog2e;
-      *seen = min(run.before + (int32_t)token, (int32_t)len);
-    };
-    float total = 0.0f, lost = 0.0f, next_lse;
-    int32_t next_seen;
-    column(run.begin, &next_lse, &next_seen);
-    const uint32_t lanes = tmem + (quad << 21) + quarter * 32, s_empty = dsmem_addr(&sh.s_empty[0], 0);
-    for (uint32_t t = 0; t < run.end - run.begin; ++t) {
-      const uint32_t buf = t % kAhead;
-      sh.lse[warp][lane] = next_lse;
-      sh.seen[warp][lane] = next_seen;
-      const bool edge = __any_sync(0xffffffffu, next_seen < (int32_t)(p0 + kTile));
-      column(run.begin + t + 1, &next_lse, &next_seen);
-      const bool ok = wait(&sh.s_full[buf], t / kAhead & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      float x[32];
-      tmem_ld32(lanes + buf * kTileColumns, x);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t lanes = tmem + (quad << 21) + quarter * kMine, s_empty = dsmem_addr(&sh.s_empty[0], 0);
+    const uint32_t k_full = dsmem_addr(&sh.k_full, 0);
+    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
+      const uint32_t mine = job.p0 + rank * kTile + quad * 32 + lane;
+      // lane l looks up column l of the warp's: its log-sum-exp, and the positions it sees
+      auto column = [&](uint32_t tile, float* lse, int32_t* seen) {
+        *lse = 0.0f;
+        *seen = 0;
+        if (tile >= job.end || deep >= cols.deep) return;
+        const uint32_t half = 2 * tile + quarter / 2, row = half / cols.across * cols.deep + deep;
+        const uint32_t head = half % cols.across * cols.wide + wide;
+        const uint32_t at = cols.flat ? row : row * a.heads + head, token = divide(at, a.by_heads);
+        if (token < run.from || token >= run.tokens || (!cols.flat && head >= a.heads)) return;
+        const float l = __ldg(a.lse + (int64_t)run.first * a.heads + at);
+        if (l == -INFINITY) return;
+        *lse = l * kLog2e;
+        *seen = min(run.before + (int32_t)token, (int32_t)run.len);
+      };
+      float next_lse;
+      int32_t next_seen;
+      column(job.begin, &next_lse, &next_seen);
+
 #pragma unroll
-      for (uint32_t c = 0; c < 32; ++c) {
-        float e = exp2_approx(fmaf(x[c], a.scale, -sh.lse[warp][c]));
-        if (edge && (int32_t)mine >= sh.seen[warp][c]) e = 0.0f;
-        sum[c & 3] += e;
+      for (uint32_t h = 0; h < 2; ++h) {
+        ok = ok && wait(&sh.raw_full[group], h);         // (two halves a job)
+        uint4 lat[4];
+        for (uint32_t k = 0; k < 4; ++k) lat[k] = lds16(from + 128 * k + 16 * piece);
+        const uint4 eight = lds16(from + KVO_LATENT_BYTES), rope = lds16(from + KVO_LATENT_BYTES + 16 + 16 * piece);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
+        if (lane == 0) mbar_arrive(&sh.raw_empty[group]);
+        if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const uint32_t pick = piece >= 4 ? 0x7632u : 0x5410u;
+        const uint32_t scales[2] = {__byte_perm(eight.x, eight.y, pick), __byte_perm(eight.z, eight.w, pick)};
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+          const uint16_t scale = (uint16_t)(scales[k >> 1] >> (k & 1) * 16);
+          const float bias = -1152.0f * __half2float(__ushort_as_half(scale));
+          uint4 x, y;
+          dequant4(lat[k].x, scale, bias, x.x, x.y);
+          dequant4(lat[k].y, scale, bias, x.z, x.w);
+          dequant4(lat[k].z, scale, bias, y.x, y.y);
+          dequant4(lat[k].w, scale, bias, y.z, y.w);
+          sts16(to_lo + 2 * k * kPieceBytes + h * 8192, x);
+          sts16(to_hi + 2 * k * kPieceBytes + h * 8192, y);
+        }
+        sts16(to_rope + h * 8192, rope);
       }
-      const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
-      lost = (now - total) - add;
-      total = now;
+      fence_proxy_async_smem();
       __syncwarp();
-    }
-    sh.sums[quarter][quad * 32 + lane] = total;
-    named_sync(1, kWorkers * 32);
-    if (quarter == 0 && mine < a.rows) {
-      total = (sh.sums[0][mine - p0] + sh.sums[1][mine - p0]) + (sh.sums[2][mine - p0] + sh.sums[3][mine - p0]);
-      if (!there) total = 0.0f;
-      if (a.splits > 1)
-        part[mine] = total;
-      else
-        a.out[s * a.out_ld + mine] =
-            mine < len ? (a.carry ? fmaf(a.keep, a.carry[s * a.carry_ld + mine], total) : total) : 0.0f;
-    }
+      if (lane == 0) cluster_mbar_arrive_own(k_full);
+
+      float total = 0.0f, lost = 0.0f;
+      for (uint32_t tile = job.begin; tile < job.end; ++tile, ++t) {
+        const uint32_t buf = t % kAhead;
+        if (lane < kMine) {
+          sh.lse[warp][lane] = next_lse;
+          sh.seen[warp][lane] = next_seen;
+        }
+        const bool edge = __any_sync(0xffffffffu, next_seen < (int32_t)(job.p0 + rank * kTile + kTile));
+        __syncwarp();
+        column(tile + 1, &next_lse, &next_seen);
+        ok = wait(&sh.s_full[buf], t / kAhead & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        float x[kMine];
+        if constexpr (kMine == 32)
+          tmem_ld32(lanes + buf * (2 * kC), x);
+        else
+          tmem_ld16(lanes + buf * (2 * kC), x);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (uint32_t c = 0; c < kMine; c += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c]);
+          x[c] = exp2_approx(fmaf(x[c], a.scale, -l.x));
+          x[c + 1] = exp2_approx(fmaf(x[c + 1], a.scale, -l.y));
+          x[c + 2] = exp2_approx(fmaf(x[c + 2], a.scale, -l.z));
+          x[c + 3] = exp2_approx(fmaf(x[c + 3], a.scale, -l.w));
+        }
+        if (edge) {
+#pragma unroll
+          for (uint32_t c = 0; c < kMine; c += 4) {
+            const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c]);
+            x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
+            x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
+            x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
+            x[c + 3] = (int32_t)mine < see.w ? x[c + 3] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (uint32_t c = 0; c < kMine; ++c) sum[c & 3] += x[c];
+        const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
+        lost = (now - total) - add;
+        total = now;
+        __syncwarp();
+      }
+      const bool there = sh.there[jobs % 3][quad] >> lane & 1;
+      float* const sums = &sh.sums[jobs & 1][0][quad * 32 + lane];
+      if (quarter) sums[(quarter - 1) * kTile] = total;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.summed);
+      if (quarter == 0) {
+        ok = wait(&sh.summed, jobs & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        total = there ? (total + sums[0]) + (sums[kTile] + sums[2 * kTile]) : 0.0f;
+        if (job.slot != UINT32_MAX)
+          a.part[job.slot * kSpan + rank * kTile + quad * 32 + lane] = total;
+        else if (mine < run.len)
+          a.out[job.seq * a.out_ld + mine] = a.carry ? fmaf(a.keep, a.carry[job.seq * a.carry_ld + mine], total) : total;
+      }
+      ++jobs;
+      return true;
+    });
   }
 
   // Both CTAs end together: the MMAs read the other's memory, and arrivals and
   // copies go to rank 0's barriers.  Where a wait gave up in either, what is in
-  // flight finishes first: the MMAs, then the copies, of which the CTA that has
-  // fewer out issues the missing ones, so that every phase can end.
+  // flight finishes first: the MMAs, then the copies, of which one that a CTA has
+  // not asked for counts as come.
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -309,53 +461,68 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
       }
     }
-    __syncthreads();
-    cluster_sync();
-    if (warp == kLoader && lane == 0) {
-      const uint32_t most = max(sh.issued[0], sh.issued[1]);
-      for (uint32_t n = sh.issued[rank]; n < most; ++n) bring(n);
-      if (rank == 0)
-        for (uint32_t n = most > kSlots ? most - kSlots : 0; n < most; ++n)
-          if (!landed(&sh.full[n % kSlots], n / kSlots & 1)) atomicOr(a.status, kFlagInflight);
+    if (warp == kLoader && lane < 4 && sh.brought[lane] && !landed(&sh.raw_full[lane], (sh.brought[lane] - 1) & 1))
+      atomicOr(a.status, kFlagInflight);
+    if (warp == kQuery && lane == 0 && rank == 0) {
+      const uint32_t most = max(sh.issued[0], sh.issued[1]), least = min(sh.issued[0], sh.issued[1]);
+      for (uint32_t m = least; m < most; ++m) {
+        if (m >= sh.issued[0]) mbar_arrive_expect_tx(&sh.full[m % kSlots], 2 * box);
+        mbar_complete_tx(&sh.full[m % kSlots], box);
+      }
+      for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
+        if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
     }
     __syncthreads();
+  }
+  // Positions that no column sees, or none is held at.
+  const uint32_t per = max(gridDim.x / a.cache.sequences, 1u), groups = gridDim.x / per;   // CTAs a sequence
+  for (uint32_t s = blockIdx.x / per; s < a.cache.sequences && blockIdx.x / per < groups; s += groups) {
+    const Run run(a, s);
+    for (uint32_t p = (run.spans() ? run.len : 0) + blockIdx.x % per * kWeightThreads + tid; p < a.rows; p += per * kWeightThreads)
+      a.out[s * a.out_ld + p] = p < run.len && a.carry ? a.keep * a.carry[s * a.carry_ld + p] : 0.0f;
   }
   cluster_sync();
   if (warp == kMma) pair_tmem_free(tmem, 512);
 }
 
-__global__ void __launch_bounds__(256) add_weights_kernel(const __grid_constant__ WeightArgs a) {
+// Block g - 1: the tile of positions that share g is the first to cut.
+__global__ void __launch_bounds__(kSpan) add_parts_kernel(const __grid_constant__ WeightArgs a) {
+  const uint32_t g = blockIdx.x + 1;
   wait_previous_grid();
   allow_next_grid();
-  const uint32_t p = blockIdx.x * 256 + threadIdx.x, s = blockIdx.y;
-  if (p >= a.rows) return;
+  const Shares shares(a);
+  if (g >= shares.pairs) return;
+  const uint64_t at = shares.from(g);
+  uint32_t seq = 0;
+  uint64_t base = 0;                                     // work before sequence seq
+  for_work(a, [&](uint32_t s0, uint64_t before, uint64_t upto) {
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > at);
+    if (!past) return true;
+    const int i = __ffs((int)past) - 1;
+    seq = s0 + i;
+    const uint64_t prior = __shfl_sync(0xffffffffu, upto, i > 0 ? i - 1 : 0);
+    base = before + (i > 0 ? prior : 0);
+    return false;
+  });
+  const Run run(a, seq);
+  const uint64_t cost = run.tiles() + kTileCost, j = (at - base) / cost, from = base + j * cost, end = from + run.tiles();
+  if (at == from || at >= end || shares.from(g - 1) > from) return;
   float total = 0.0f;
-  if ((int32_t)p < a.lens[s]) {
-    for (uint32_t i = 0; i < a.splits; ++i) total += __ldcg(a.part + ((int64_t)i * a.cache.sequences + s) * a.rows + p);
-    if (a.carry) total = fmaf(a.keep, a.carry[s * a.carry_ld + p], total);
-  }
-  a.out[s * a.out_ld + p] = total;
+  for (uint32_t p = g - 1; p < shares.pairs && shares.from(p) < end; ++p)
+    total += __ldcg(a.part + (2 * p + (p == g - 1)) * kSpan + threadIdx.x);
+  const uint32_t mine = (uint32_t)j * kSpan + threadIdx.x;
+  if (mine < run.len)
+    a.out[seq * a.out_ld + mine] = a.carry ? fmaf(a.keep, a.carry[seq * a.carry_ld + mine], total) : total;
 }
 
-// Pairs that the columns of a sequence's positions are split over: as many as
-// the GPU has room for.
-uint32_t weight_splits(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows, int64_t window) {
-  const int64_t pairs = (rows + kPairGrid - 1) / kPairGrid * sequences, room = device_sms() / 2;
-  int64_t n = tokens / sequences + (tokens % sequences != 0);
-  if (window && window < n) n = window;
-  const int64_t tiles = (n * heads + kTileColumns - 1) / kTileColumns;
-  int64_t splits = pairs < 1 || pairs >= room ? 1 : room / pairs;
-  if (splits > tiles) splits = tiles;
-  return (uint32_t)(splits < 1 ? 1 : splits);
-}
-
+template <uint32_t kC>
 cudaError_t launch_weights(const WeightArgs& a, const CUtensorMap& map, cudaStream_t stream) {
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWeightSmem);
+    e = cudaFuncSetAttribute(weights_kernel<kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWeightSmem);
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
@@ -367,13 +534,15 @@ cudaError_t launch_weights(const WeightArgs& a, const CUtensorMap& map, cudaStre
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3(2 * ((a.rows + kPairGrid - 1) / kPairGrid) * a.splits, a.cache.sequences);
+  lc.gridDim = dim3(2 * a.pairs);
   lc.blockDim = dim3(kWeightThreads);
   lc.dynamicSmemBytes = kWeightSmem;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, weights_kernel, a, map);
+  e = cudaLaunchKernelEx(&lc, weights_kernel<kC>, a, map);
+  if (e != cudaSuccess || a.pairs < 2) return e;
+  return launch_early(add_parts_kernel, dim3(a.pairs - 1), kSpan, 0, stream, a);
 }
 
 }  // namespace
@@ -383,8 +552,7 @@ extern "C" int64_t kvo_attention_weights_work_bytes(int64_t tokens, int32_t sequ
                                                     int64_t window) {
   if (tokens < 0 || tokens > KVO_MAX_QUERIES || sequences < 1 || sequences > KVO_MAX_QUERIES) return -1;
   if (heads < 1 || heads > KVO_MAX_HEADS || rows < 0 || rows > INT32_MAX - 255 || window < 0) return -1;
-  const uint32_t splits = kvo::weight_splits(tokens, sequences, (uint32_t)heads, rows, window);
-  return splits == 1 ? 0 : (int64_t)splits * sequences * rows * 4;
+  return tokens > 0 && rows > 0 ? (int64_t)(kvo::device_sms() / 2) * 2 * kvo::kSpan * 4 : 0;
 }
 
 extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache, const kvo_weight_query* s,
@@ -423,7 +591,7 @@ extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache
   a.tokens = (uint32_t)s->tokens;
   a.heads = (uint32_t)s->heads;
   a.window = s->window > KVO_MAX_QUERIES ? 0 : (uint32_t)s->window;
-  a.splits = weight_splits(s->tokens, cache->sequences, a.heads, s->rows, s->window);
+  a.pairs = (uint32_t)device_sms() / 2;
   a.by_heads = divider(a.heads);
   a.scale = s->scale * kLog2e;
   a.keep = s->keep;
@@ -431,13 +599,13 @@ extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache
   // a dimension of one has no next element: its stride says nothing
   const int64_t head_ld = a.heads > 1 ? s->q_head_ld : KVO_DEQUANT_VALUES;
   const int64_t q_ld = s->tokens > 1 ? s->q_ld : a.heads * head_ld;
-  a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens);
+  int64_t each = (s->tokens + cache->sequences - 1) / cache->sequences;
+  if (a.window && a.window < each) each = a.window;
+  const bool few = each * a.heads <= 64;
+  a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens, few ? 32 : 64);
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   CUtensorMap map = {};
   // without tokens no CTA gets as far as a copy
   if (s->tokens > 0 && !query_map(&map, s->q, a.heads, s->tokens, q_ld * 2, head_ld * 2, a.columns)) return KVO_ECUDA;
-  cudaError_t e = launch_weights(a, map, on);
-  if (e == cudaSuccess && a.splits > 1)
-    e = launch_early(add_weights_kernel, dim3((a.rows + 255) / 256, a.cache.sequences), 256, 0, on, a);
-  return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
+  return (few ? launch_weights<32>(a, map, on) : launch_weights<64>(a, map, on)) == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

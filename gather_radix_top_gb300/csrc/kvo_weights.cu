@@ -32,12 +32,11 @@ constexpr uint32_t kTile = 128;                          // positions of a CTA
 constexpr uint32_t kSpan = 2 * kTile;                    // of a pair
 constexpr uint32_t kHalf = 64;                           // rows that come together
 constexpr uint32_t kWorkers = 16;                        // warps: four for each quarter of the columns
-constexpr uint32_t kMma = kWorkers, kQuery = kWorkers + 1, kLoader = kWorkers + 2, kLoaders = 2;
-constexpr uint32_t kWeightThreads = (kLoader + kLoaders) * 32;
+constexpr uint32_t kMma = kWorkers, kRows = kWorkers + 1, kQuery = kWorkers + 2, kQueries = 2;
+constexpr uint32_t kWeightThreads = (kQuery + kQueries) * 32;
 constexpr uint32_t kPieceBytes = kTile * 128;            // 64 values of every position
 constexpr uint32_t kRingBytes = 32768, kAhead = 4;       // queries; tiles of S
-constexpr uint32_t kPitch = KVO_ROW_BYTES + 16;          // of a raw row
-constexpr uint32_t kWeightSmem = 1024 + 9 * kPieceBytes + kRingBytes + kHalf * kPitch;
+constexpr uint32_t kWeightSmem = 1024 + 9 * kPieceBytes + kRingBytes + kHalf * KVO_ROW_BYTES;
 constexpr uint32_t kTileCost = 3;                        // of a tile of positions, in tiles of columns
 
 struct WeightArgs {
@@ -62,9 +61,9 @@ template <uint32_t kSlots>
 struct WeightShared {
   uint64_t k_full, k_empty, full[kSlots], empty[kSlots], s_full[kAhead], s_empty[kAhead], raw_full[4], raw_empty[4], summed, drained;
   uint32_t tmem, gave_up;
-  uint32_t issued[2];                // queries' pieces that each CTA has asked for
+  uint32_t issued[2][kQueries];      // per CTA and query warp: pieces of its own and before them that it has asked for
   uint32_t brought[4];               // halves that each group's rows have come for
-  uint32_t there[3][4];              // per job in turns: rows that are not masked, row r is bit r % 32 of word r / 32
+  uint32_t there[4][4];              // per job in turns: rows that are not masked, row r is bit r % 32 of word r / 32
   alignas(16) float lse[kWorkers][32];   // per warp and column, base 2
   alignas(16) int32_t seen[kWorkers][32];    // and the positions it sees
   float sums[2][3][kTile];           // per job in turns: of the quarters 1 to 3
@@ -197,7 +196,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     mbar_init(&sh.summed, kWorkers);
     mbar_init(&sh.drained, 1);
     sh.gave_up = a.wait_clocks == 0;
-    sh.issued[0] = sh.issued[1] = 0;
+    for (uint32_t i = 0; i < 2; ++i)
+      for (uint32_t w = 0; w < kQueries; ++w) sh.issued[i][w] = 0;
   }
   if (warp == kMma) pair_tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
@@ -218,64 +218,93 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   uint32_t n = 0, t = 0, jobs = 0;                       // pieces, tiles of S, jobs so far
   bool ok = true;
 
-  if (warp >= kLoader) {
-    // Rows: lane l of warp w brings row 32 w + l of a half; 16 lanes are a group.
-    const uint32_t r = (warp - kLoader) * 32 + lane, group = r / 16, dst = stage + r * kPitch;
-    uint32_t halves = 0;
-    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
-      int64_t row[2];
-#pragma unroll
-      for (uint32_t h = 0; h < 2; ++h) {
-        const uint32_t p = job.p0 + rank * kTile + h * kHalf + r;
-        row[h] = p < run.len ? cache_row(a.cache, job.seq, p) : -1;
-        if (p < run.len && row[h] < 0) atomicOr(a.status, kFlagRange);
-      }
+  if (warp == kRows) {
+    // Lane l looks up rows l and l + 32 of each half, a job ahead.  Sixteen rows
+    // are a group: one copy where they lie one behind the other, as those of a
+    // block do (a copy for every row takes 66 clocks each to issue).
+    uint32_t halves = 0, p0 = 0;
+    int64_t row[2][2];                                   // of the job whose rows come next: [half][l, l + 32]
+    uint32_t held = 0;
+    auto bring = [&]() -> bool {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h, ++halves) {
-        if (halves) ok = ok && wait(&sh.raw_empty[group], (halves - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        const uint32_t there = __ballot_sync(0xffffffffu, row[h] >= 0);
-        if (row[h] < 0) {
-          for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
-          fence_proxy_async_smem();                      // before a later half's copy to the same place
-        }
-        __syncwarp();
-        if (lane == 0) sh.there[jobs % 3][2 * h + r / 32] = there;   // (a slow warp may be two jobs behind)
-        __syncwarp();
-        if (lane % 16 == 0) {
-          mbar_arrive_expect_tx(&sh.raw_full[group], __popc(there >> lane & 0xffffu) * KVO_ROW_BYTES);
-          sh.brought[group] = halves + 1;
-        }
-        __syncwarp();
-        if (row[h] >= 0)
-          bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row[h] * KVO_ROW_BYTES, KVO_ROW_BYTES, &sh.raw_full[group]);
-      }
-      ++jobs;
-      return true;
-    });
-  } else if (warp == kQuery) {
-    // the queries' pieces
-    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
-      if (lane == 0) {
-        for (uint32_t tile = job.begin; tile < job.end && ok; ++tile) {
-          const uint32_t half = 2 * tile + rank, row = half / cols.across, head = half % cols.across * cols.wide;
-          const int32_t z = (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep);
-          for (uint32_t piece = 0; piece < 9; ++piece, ++n) {
-            const uint32_t slot = n % kSlots;
-            if (n >= kSlots) ok = wait(&sh.empty[slot], (n / kSlots - 1) & 1);
-            if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
-            pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)(piece * 64), (int32_t)head, z, dsmem_addr(&sh.full[slot], 0));
+#pragma unroll
+        for (uint32_t u = 0; u < 2; ++u) {
+          const uint32_t there = __ballot_sync(0xffffffffu, row[h][u] >= 0), p = p0 + h * kHalf + u * 32 + lane;
+          if (p < held && row[h][u] < 0) atomicOr(a.status, kFlagRange);
+          if (lane == 0) sh.there[jobs & 3][2 * h + u] = there;   // (a slow warp may be three jobs behind)
+          const int64_t first = __shfl_sync(0xffffffffu, row[h][u], lane & 16);
+          const uint32_t run = __ballot_sync(0xffffffffu, row[h][u] >= 0 && row[h][u] == first + (lane & 15));
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e) {             // lanes 16 e ..
+            const uint32_t group = 2 * u + e, mask = there >> 16 * e & 0xffffu;
+            const bool together = (run >> 16 * e & 0xffffu) == 0xffffu;
+            const uint32_t dst = stage + (u * 32 + lane) * KVO_ROW_BYTES;
+            if (halves) ok = wait(&sh.raw_empty[group], (halves - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            const bool mine = lane / 16 == e;
+            if (mine && row[h][u] < 0) {
+              for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
+              fence_proxy_async_smem();                  // before a later copy to the same place
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sh.raw_full[group], __popc(mask) * KVO_ROW_BYTES);
+              sh.brought[group] = halves + 1;
+            }
+            __syncwarp();
+            if (mine && row[h][u] >= 0 && (!together || lane % 16 == 0))
+              bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row[h][u] * KVO_ROW_BYTES,
+                            (together ? 16 : 1) * KVO_ROW_BYTES, &sh.raw_full[group]);
           }
         }
       }
+      ++jobs;
+      return true;
+    };
+    bool some = false;
+    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
+      int64_t next[2][2];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t p = job.p0 + rank * kTile + i * 32 + lane;
+        next[i / 2][i % 2] = p < run.len ? cache_row(a.cache, job.seq, p) : -1;
+      }
+      if (some && !bring()) return false;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) row[i / 2][i % 2] = next[i / 2][i % 2];
+      p0 = job.p0 + rank * kTile;
+      held = run.len;
+      some = true;
+      return true;
+    });
+    if (some && __all_sync(0xffffffffu, ok)) bring();
+  } else if (warp >= kQuery) {
+    // the queries' pieces: warp w takes every kQueries-th one
+    const uint32_t w = warp - kQuery, full0 = dsmem_addr(&sh.full[0], 0);
+    uint32_t at = 0;                                     // the job's first piece
+    for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
+      const uint32_t tiles = job.end > job.begin ? job.end - job.begin : 0;
+      if (lane == 0) {
+        for (uint32_t k = (w + at) % kQueries; k < 9 * tiles; k += kQueries) {
+          const uint32_t tile = job.begin + k / 9, piece = k % 9, slot = (at + k) % kSlots;
+          const uint32_t half = 2 * tile + rank, row = half / cols.across, head = half % cols.across * cols.wide;
+          if (at + k >= kSlots) ok = wait(&sh.empty[slot], ((at + k) / kSlots - 1) & 1);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
+          pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)(piece * 64), (int32_t)head,
+                        (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep), full0 + slot * 8);
+          n = at + k + 1;
+        }
+      }
+      at += 9 * tiles;
       return (bool)__shfl_sync(0xffffffffu, ok, 0);
     });
     if (lane == 0) {
+      if (ok) n = at;
       // no slot's release may still be on its way when the CTA ends
       for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
-      dsmem_st_u32(dsmem_addr(&sh.issued[rank], 0), n);  // both counts are looked at by rank 0
-      dsmem_st_u32(dsmem_addr(&sh.issued[rank], 1), n);
+      dsmem_st_u32(dsmem_addr(&sh.issued[rank][w], 0), n);
     }
   } else if (warp == kMma) {
     if (rank == 0)
@@ -317,7 +346,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   } else {
     // positions: piece `piece` of each 128 latent bytes of rows slot and slot + 64
     const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3), group = warp / 4;
-    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), from = stage + slot * kPitch;
+    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), from = stage + slot * KVO_ROW_BYTES;
     const uint32_t to_lo = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3));
     const uint32_t to_hi = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + 1);
     const uint32_t to_rope = keys + 8 * kPieceBytes + swizzled(slot, piece);
@@ -327,12 +356,88 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const uint32_t wide = in_half - deep * cols.wide;
     const uint32_t lanes = tmem + (quad << 21) + quarter * kMine, s_empty = dsmem_addr(&sh.s_empty[0], 0);
     const uint32_t k_full = dsmem_addr(&sh.k_full, 0);
+    // A job's last tile is taken after the next job's rows are in place, so that
+    // its MMAs and this overlap.
+    Job last{UINT32_MAX, 0, 0, 0, 0};
+    uint32_t last_len = 0;
+    float total = 0.0f, lost = 0.0f, lse = 0.0f, carried = 0.0f;   // of that job; lane l: column l of its last tile
+    int32_t seen = 0;
+    // one tile's weights to the sum; lane l has looked up column l
+    auto add_tile = [&](uint32_t mine) -> bool {
+      const uint32_t buf = t % kAhead;
+      if (lane < kMine) {
+        sh.lse[warp][lane] = lse;
+        sh.seen[warp][lane] = seen;
+      }
+      const bool edge = __any_sync(0xffffffffu, seen <= (int32_t)(mine | 31));
+      __syncwarp();
+      ok = wait(&sh.s_full[buf], t / kAhead & 1);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      tc_fence_after();
+      float x[kMine];
+      if constexpr (kMine == 32)
+        tmem_ld32(lanes + buf * (2 * kC), x);
+      else
+        tmem_ld16(lanes + buf * (2 * kC), x);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t c = 0; c < kMine; c += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c]);
+        x[c] = exp2_approx(fmaf(x[c], a.scale, -l.x));
+        x[c + 1] = exp2_approx(fmaf(x[c + 1], a.scale, -l.y));
+        x[c + 2] = exp2_approx(fmaf(x[c + 2], a.scale, -l.z));
+        x[c + 3] = exp2_approx(fmaf(x[c + 3], a.scale, -l.w));
+      }
+      if (edge) {
+#pragma unroll
+        for (uint32_t c = 0; c < kMine; c += 4) {
+          const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c]);
+          x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
+          x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
+          x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
+          x[c + 3] = (int32_t)mine < see.w ? x[c + 3] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (uint32_t c = 0; c < kMine; ++c) sum[c & 3] += x[c];
+      const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
+      lost = (now - total) - add;
+      total = now;
+      ++t;
+      __syncwarp();
+      return true;
+    };
+    // the last job's last tile, and its result
+    auto finish = [&]() -> bool {
+      const uint32_t mine = last.p0 + rank * kTile + quad * 32 + lane;
+      if (last.begin < last.end && !add_tile(mine)) return false;
+      const uint32_t job = jobs - 1;
+      const bool there = sh.there[job & 3][quad] >> lane & 1;
+      float* const sums = &sh.sums[job & 1][0][quad * 32 + lane];
+      if (quarter) sums[(quarter - 1) * kTile] = total;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.summed);
+      if (quarter == 0) {
+        ok = wait(&sh.summed, job & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        total = there ? (total + sums[0]) + (sums[kTile] + sums[2 * kTile]) : 0.0f;
+        if (last.slot != UINT32_MAX)
+          a.part[last.slot * kSpan + rank * kTile + quad * 32 + lane] = total;
+        else if (mine < last_len)
+          a.out[last.seq * a.out_ld + mine] = a.carry ? fmaf(a.keep, carried, total) : total;
+      }
+      return true;
+    };
     for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
       const uint32_t mine = job.p0 + rank * kTile + quad * 32 + lane;
       // lane l looks up column l of the warp's: its log-sum-exp, and the positions it sees
-      auto column = [&](uint32_t tile, float* lse, int32_t* seen) {
-        *lse = 0.0f;
-        *seen = 0;
+      auto column = [&](uint32_t tile, float* to_lse, int32_t* to_seen) {
+        *to_lse = 0.0f;
+        *to_seen = 0;
         if (tile >= job.end || deep >= cols.deep) return;
         const uint32_t half = 2 * tile + quarter / 2, row = half / cols.across * cols.deep + deep;
         const uint32_t head = half % cols.across * cols.wide + wide;
@@ -340,12 +445,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if (token < run.from || token >= run.tokens || (!cols.flat && head >= a.heads)) return;
         const float l = __ldg(a.lse + (int64_t)run.first * a.heads + at);
         if (l == -INFINITY) return;
-        *lse = l * kLog2e;
-        *seen = min(run.before + (int32_t)token, (int32_t)run.len);
+        *to_lse = l * kLog2e;
+        *to_seen = min(run.before + (int32_t)token, (int32_t)run.len);
       };
-      float next_lse;
+      float next_lse, next_carried = 0.0f;
       int32_t next_seen;
       column(job.begin, &next_lse, &next_seen);
+      if (quarter == 0 && a.carry && mine < run.len) next_carried = a.carry[job.seq * a.carry_ld + mine];
 
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
@@ -377,72 +483,23 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) cluster_mbar_arrive_own(k_full);
-
-      float total = 0.0f, lost = 0.0f;
-      for (uint32_t tile = job.begin; tile < job.end; ++tile, ++t) {
-        const uint32_t buf = t % kAhead;
-        if (lane < kMine) {
-          sh.lse[warp][lane] = next_lse;
-          sh.seen[warp][lane] = next_seen;
-        }
-        const bool edge = __any_sync(0xffffffffu, next_seen < (int32_t)(job.p0 + rank * kTile + kTile));
-        __syncwarp();
-        column(tile + 1, &next_lse, &next_seen);
-        ok = wait(&sh.s_full[buf], t / kAhead & 1);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        tc_fence_after();
-        float x[kMine];
-        if constexpr (kMine == 32)
-          tmem_ld32(lanes + buf * (2 * kC), x);
-        else
-          tmem_ld16(lanes + buf * (2 * kC), x);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (uint32_t c = 0; c < kMine; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c]);
-          x[c] = exp2_approx(fmaf(x[c], a.scale, -l.x));
-          x[c + 1] = exp2_approx(fmaf(x[c + 1], a.scale, -l.y));
-          x[c + 2] = exp2_approx(fmaf(x[c + 2], a.scale, -l.z));
-          x[c + 3] = exp2_approx(fmaf(x[c + 3], a.scale, -l.w));
-        }
-        if (edge) {
-#pragma unroll
-          for (uint32_t c = 0; c < kMine; c += 4) {
-            const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c]);
-            x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
-            x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
-            x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
-            x[c + 3] = (int32_t)mine < see.w ? x[c + 3] : 0.0f;
-          }
-        }
-#pragma unroll
-        for (uint32_t c = 0; c < kMine; ++c) sum[c & 3] += x[c];
-        const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
-        lost = (now - total) - add;
-        total = now;
-        __syncwarp();
-      }
-      const bool there = sh.there[jobs % 3][quad] >> lane & 1;
-      float* const sums = &sh.sums[jobs & 1][0][quad * 32 + lane];
-      if (quarter) sums[(quarter - 1) * kTile] = total;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.summed);
-      if (quarter == 0) {
-        ok = wait(&sh.summed, jobs & 1);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        total = there ? (total + sums[0]) + (sums[kTile] + sums[2 * kTile]) : 0.0f;
-        if (job.slot != UINT32_MAX)
-          a.part[job.slot * kSpan + rank * kTile + quad * 32 + lane] = total;
-        else if (mine < run.len)
-          a.out[job.seq * a.out_ld + mine] = a.carry ? fmaf(a.keep, a.carry[job.seq * a.carry_ld + mine], total) : total;
-      }
+      if (jobs && !finish()) return false;
       ++jobs;
+      last = job;
+      last_len = run.len;
+      total = lost = 0.0f;
+      lse = next_lse;
+      seen = next_seen;
+      carried = next_carried;
+      for (uint32_t tile = job.begin; tile + 1 < job.end; ++tile) {
+        column(tile + 1, &next_lse, &next_seen);
+        if (!add_tile(mine)) return false;
+        lse = next_lse;
+        seen = next_seen;
+      }
       return true;
     });
+    if (jobs && __all_sync(0xffffffffu, ok)) finish();
   }
 
   // Both CTAs end together: the MMAs read the other's memory, and arrivals and
@@ -461,16 +518,24 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
       }
     }
-    if (warp == kLoader && lane < 4 && sh.brought[lane] && !landed(&sh.raw_full[lane], (sh.brought[lane] - 1) & 1))
+    if (warp == kRows && lane < 4 && sh.brought[lane] && !landed(&sh.raw_full[lane], (sh.brought[lane] - 1) & 1))
       atomicOr(a.status, kFlagInflight);
     if (warp == kQuery && lane == 0 && rank == 0) {
-      const uint32_t most = max(sh.issued[0], sh.issued[1]), least = min(sh.issued[0], sh.issued[1]);
+      uint32_t most = 0, least = UINT32_MAX;
+      for (uint32_t i = 0; i < 2 * kQueries; ++i) {
+        most = max(most, sh.issued[i / kQueries][i % kQueries]);
+        least = min(least, sh.issued[i / kQueries][i % kQueries]);
+      }
       for (uint32_t m = least; m < most; ++m) {
-        if (m >= sh.issued[0]) mbar_arrive_expect_tx(&sh.full[m % kSlots], 2 * box);
+        const bool here = m < sh.issued[0][m % kQueries], there = m < sh.issued[1][m % kQueries];
+        if (here == there) continue;
+        if (!here) mbar_arrive_expect_tx(&sh.full[m % kSlots], 2 * box);
         mbar_complete_tx(&sh.full[m % kSlots], box);
       }
-      for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
+      for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m) {
+        if (m >= sh.issued[0][m % kQueries] && m >= sh.issued[1][m % kQueries]) continue;
         if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
+      }
     }
     __syncthreads();
   }

@@ -158,7 +158,7 @@ __device__ __forceinline__ void for_jobs(const WeightArgs& a, uint32_t pair, uin
         if (x == y) continue;
         Job job{s0 + i, j * kSpan, run.begin + x, run.begin + y, UINT32_MAX};
         if (y - x < tiles) job.slot = 2 * pair + (x == 0);
-        job.begin = max(job.begin, run.tile_of(a, max(run.from, run.sees(job.p0))));   // columns that see none of them
+        if (run.sees(job.p0) > run.from) job.begin = max(job.begin, run.tile_of(a, run.sees(job.p0)));   // others see none of them
         go = f(job, run);
       }
     }
@@ -228,18 +228,37 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     auto bring = [&]() -> bool {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h, ++halves) {
+        uint32_t there[2], run[2];
+        int64_t first[2];
 #pragma unroll
         for (uint32_t u = 0; u < 2; ++u) {
-          const uint32_t there = __ballot_sync(0xffffffffu, row[h][u] >= 0), p = p0 + h * kHalf + u * 32 + lane;
-          if (p < held && row[h][u] < 0) atomicOr(a.status, kFlagRange);
-          if (lane == 0) sh.there[jobs & 3][2 * h + u] = there;   // (a slow warp may be three jobs behind)
-          const int64_t first = __shfl_sync(0xffffffffu, row[h][u], lane & 16);
-          const uint32_t run = __ballot_sync(0xffffffffu, row[h][u] >= 0 && row[h][u] == first + (lane & 15));
+          there[u] = __ballot_sync(0xffffffffu, row[h][u] >= 0);
+          first[u] = __shfl_sync(0xffffffffu, row[h][u], lane & 16);
+          run[u] = __ballot_sync(0xffffffffu, row[h][u] >= 0 && row[h][u] == first[u] + (lane & 15));
+        }
+        if (lane < 2) sh.there[jobs & 3][2 * h + lane] = lane ? there[1] : there[0];   // (a slow warp may be three jobs behind)
+        if ((run[0] & run[1]) == ~0u) {                  // lane 16 e + u: group 2 u + e
+          const uint32_t u = lane & 1, group = 2 * u + (lane >> 4);
+          if ((lane & 14) == 0) {
+            if (halves) ok = wait(&sh.raw_empty[group], (halves - 1) & 1);
+            if (ok) {
+              mbar_arrive_expect_tx(&sh.raw_full[group], 16 * KVO_ROW_BYTES);
+              sh.brought[group] = halves + 1;
+              bulk_copy_g2s(raw + (stage - smem_u32(raw)) + group * 16 * KVO_ROW_BYTES,
+                            a.cache.rows + (u ? first[1] : first[0]) * KVO_ROW_BYTES, 16 * KVO_ROW_BYTES, &sh.raw_full[group]);
+            }
+          }
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          continue;
+        }
 #pragma unroll
+        for (uint32_t u = 0; u < 2; ++u) {
+          const uint32_t p = p0 + h * kHalf + u * 32 + lane, dst = stage + (u * 32 + lane) * KVO_ROW_BYTES;
+          if (p < held && row[h][u] < 0) atomicOr(a.status, kFlagRange);
+#pragma unroll 1
           for (uint32_t e = 0; e < 2; ++e) {             // lanes 16 e ..
-            const uint32_t group = 2 * u + e, mask = there >> 16 * e & 0xffffu;
-            const bool together = (run >> 16 * e & 0xffffu) == 0xffffu;
-            const uint32_t dst = stage + (u * 32 + lane) * KVO_ROW_BYTES;
+            const uint32_t group = 2 * u + e, mask = there[u] >> 16 * e & 0xffffu;
+            const bool together = (run[u] >> 16 * e & 0xffffu) == 0xffffu;
             if (halves) ok = wait(&sh.raw_empty[group], (halves - 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
             const bool mine = lane / 16 == e;

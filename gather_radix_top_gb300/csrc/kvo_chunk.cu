@@ -371,24 +371,6 @@ struct ChunkShared {
   PlanTile upcoming[2];              // the workers' next tile, in turns
 };
 
-// x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
-__device__ __forceinline__ void fma_two(float& x, float& y, float scale, float a, float b) {
-  asm("{\n .reg .b64 v, s, t;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mov.b64 t, {%3, %4};\n"
-      " fma.rn.f32x2 v, v, s, t;\n mov.b64 {%0, %1}, v;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(scale), "f"(a), "f"(b));
-}
-__device__ __forceinline__ void add_two(float& x, float& y, float a, float b) {
-  asm("{\n .reg .b64 v, t;\n mov.b64 v, {%0, %1};\n mov.b64 t, {%2, %3};\n add.rn.f32x2 v, v, t;\n mov.b64 {%0, %1}, v;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-__device__ __forceinline__ float max_three(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 template <uint32_t kN, uint32_t kBit>
 __device__ __forceinline__ void add_lanes(float* v, uint32_t lane) {
   // a step halves the columns that a lane keeps: v[0] is column lane's sum at last

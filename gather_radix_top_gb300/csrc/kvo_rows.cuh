@@ -46,6 +46,24 @@ __device__ __forceinline__ void dequant4(uint32_t bytes, uint16_t scale, float b
   hi = bf16_pair(fma_low(b, scale, bias), fma_high(b, scale, bias));
 }
 
+// x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
+__device__ __forceinline__ void fma_two(float& x, float& y, float scale, float a, float b) {
+  asm("{\n .reg .b64 v, s, t;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mov.b64 t, {%3, %4};\n"
+      " fma.rn.f32x2 v, v, s, t;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(scale), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_two(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 v, t;\n mov.b64 v, {%0, %1};\n mov.b64 t, {%2, %3};\n add.rn.f32x2 v, v, t;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max_three(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Whether any of eight fp16 is infinite or NaN.
 __device__ __forceinline__ bool any_not_finite(uint4 eight) {
   constexpr uint32_t kInf = 0x7c007c00u;

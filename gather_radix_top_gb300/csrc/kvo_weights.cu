@@ -7,11 +7,11 @@
 // over the columns in tiles of 64 or 128: S [256 positions x columns] = K Q^T as
 // pair MMAs, for which each CTA brings half of a tile's queries.  A position is
 // a lane of S, so its sum over the columns stays in one thread's register.
-// Shared memory holds the positions (144 KB), a ring of 32 KB for the queries'
-// pieces (64 values of a CTA's columns), and the next 64 raw rows, which come by
-// bulk copies in four groups of 16, each with its own four warps: they take
-// them to registers, let the next ones come, and store the dequantised ones
-// when the MMAs of the positions before have ended.  Tensor memory holds four
+// Shared memory holds the positions (144 KB), a ring for the queries' pieces (64
+// values of a CTA's columns), and raw rows, which come by bulk copies in groups of
+// 16, each with its own four warps: they take them to registers, let the next
+// ones come, and store the dequantised ones when the MMAs of the positions
+// before have ended.  Tensor memory holds four
 // tiles of S.
 //
 // A thread's sum over a tile is added to its running sum with the rounding
@@ -35,9 +35,20 @@ constexpr uint32_t kWorkers = 16;                        // warps: four for each
 constexpr uint32_t kMma = kWorkers, kRows = kWorkers + 1, kQuery = kWorkers + 2, kQueries = 2;
 constexpr uint32_t kWeightThreads = (kQuery + kQueries) * 32;
 constexpr uint32_t kPieceBytes = kTile * 128;            // 64 values of every position
-constexpr uint32_t kRingBytes = 32768, kAhead = 4;       // queries; tiles of S
-constexpr uint32_t kWeightSmem = 1024 + 9 * kPieceBytes + kRingBytes + kHalf * KVO_ROW_BYTES;
+constexpr uint32_t kAhead = 4;                           // tiles of S
 constexpr uint32_t kTileCost = 3;                        // of a tile of positions, in tiles of columns
+
+// kC: a CTA's columns of a tile.  What the positions leave of shared memory goes
+// to the raw rows where a tile of positions meets few columns (room for four
+// groups of 16, and eight pieces of 32 columns), else to the queries (six pieces
+// of 64 columns, two groups).
+template <uint32_t kC>
+struct WeightShape {
+  static constexpr uint32_t kSlotBytes = kC * 128, kSlots = kC == 32 ? 8 : 6;
+  static constexpr uint32_t kRegions = kC == 32 ? 4 : 2;           // group g's rows go to region g % kRegions
+  static constexpr uint32_t kRegionBytes = 16 * KVO_ROW_BYTES;
+  static constexpr uint32_t kSmem = 1024 + 9 * kPieceBytes + kSlots * kSlotBytes + kRegions * kRegionBytes;
+};
 
 struct WeightArgs {
   CacheView cache;
@@ -57,9 +68,10 @@ struct WeightArgs {
   int64_t wait_clocks;
 };
 
-template <uint32_t kSlots>
+template <uint32_t kSlots, uint32_t kRegions>
 struct WeightShared {
-  uint64_t k_full, k_empty, full[kSlots], empty[kSlots], s_full[kAhead], s_empty[kAhead], raw_full[4], raw_empty[4], summed, drained;
+  uint64_t k_full, k_empty, full[kSlots], empty[kSlots], s_full[kAhead], s_empty[kAhead], raw_full[4], raw_empty[kRegions];
+  uint64_t summed[2], drained;       // summed: per job in turns, as a quarter may be a job ahead of another
   uint32_t tmem, gave_up;
   uint32_t issued[2][kQueries];      // per CTA and query warp: pieces of its own and before them that it has asked for
   uint32_t brought[4];               // halves that each group's rows have come for
@@ -170,12 +182,13 @@ __device__ __forceinline__ void for_jobs(const WeightArgs& a, uint32_t pair, uin
 template <uint32_t kC>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weights_kernel(const __grid_constant__ WeightArgs a, const __grid_constant__ CUtensorMap qmap) {
-  constexpr uint32_t kSlotBytes = kC * 128, kSlots = kRingBytes / kSlotBytes;
+  using S = WeightShape<kC>;
+  constexpr uint32_t kSlotBytes = S::kSlotBytes, kSlots = S::kSlots, kRegions = S::kRegions;
   constexpr uint32_t kMine = kC / 2;                     // columns of a worker warp
   extern __shared__ uint8_t raw[];
-  __shared__ WeightShared<kSlots> sh;
+  __shared__ WeightShared<kSlots, kRegions> sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank(), pair = blockIdx.x >> 1;
-  const uint32_t keys = (smem_u32(raw) + 1023u) & ~1023u, ring = keys + 9 * kPieceBytes, stage = ring + kRingBytes;
+  const uint32_t keys = (smem_u32(raw) + 1023u) & ~1023u, ring = keys + 9 * kPieceBytes, stage = ring + kSlots * kSlotBytes;
 
   if (tid == 0) {
     mbar_init(&sh.k_full, 2 * kWorkers);
@@ -190,10 +203,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     for (uint32_t i = 0; i < 4; ++i) {
       mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], 4);
       sh.brought[i] = 0;
     }
-    mbar_init(&sh.summed, kWorkers);
+    for (uint32_t i = 0; i < kRegions; ++i) mbar_init(&sh.raw_empty[i], 4);
+    for (uint32_t i = 0; i < 2; ++i) mbar_init(&sh.summed[i], kWorkers);
     mbar_init(&sh.drained, 1);
     sh.gave_up = a.wait_clocks == 0;
     for (uint32_t i = 0; i < 2; ++i)
@@ -237,31 +250,40 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           run[u] = __ballot_sync(0xffffffffu, row[h][u] >= 0 && row[h][u] == first[u] + (lane & 15));
         }
         if (lane < 2) sh.there[jobs & 3][2 * h + lane] = lane ? there[1] : there[0];   // (a slow warp may be three jobs behind)
-        if ((run[0] & run[1]) == ~0u) {                  // lane 16 e + u: group 2 u + e
-          const uint32_t u = lane & 1, group = 2 * u + (lane >> 4);
-          if ((lane & 14) == 0) {
-            if (halves) ok = wait(&sh.raw_empty[group], (halves - 1) & 1);
-            if (ok) {
-              mbar_arrive_expect_tx(&sh.raw_full[group], 16 * KVO_ROW_BYTES);
-              sh.brought[group] = halves + 1;
-              bulk_copy_g2s(raw + (stage - smem_u32(raw)) + group * 16 * KVO_ROW_BYTES,
-                            a.cache.rows + (u ? first[1] : first[0]) * KVO_ROW_BYTES, 16 * KVO_ROW_BYTES, &sh.raw_full[group]);
+        // The regions' uses so far: group g of this half is use `uses + g / kRegions` of its region.
+        const uint32_t uses = halves * (4 / kRegions);
+        const bool quick = (run[0] & run[1]) == ~0u;     // all four groups are runs
+        if (quick) {
+#pragma unroll
+          for (uint32_t turn = 0; turn < 4 / kRegions; ++turn) {   // kRegions groups at a time, a lane for each
+            // lane 16 e + u: group 2 u + e
+            const uint32_t u = lane & 1, group = 2 * u + (lane >> 4), region = group % kRegions;
+            if ((lane & 14) == 0 && group / kRegions == turn) {
+              if (uses + turn) ok = wait(&sh.raw_empty[region], (uses + turn - 1) & 1);
+              if (ok) {
+                mbar_arrive_expect_tx(&sh.raw_full[group], 16 * KVO_ROW_BYTES);
+                sh.brought[group] = halves + 1;
+                bulk_copy_g2s(raw + (stage - smem_u32(raw)) + region * S::kRegionBytes,
+                              a.cache.rows + (u ? first[1] : first[0]) * KVO_ROW_BYTES, 16 * KVO_ROW_BYTES,
+                              &sh.raw_full[group]);
+              }
             }
+            if (!__all_sync(0xffffffffu, ok)) return false;
           }
-          if (!__all_sync(0xffffffffu, ok)) return false;
           continue;
         }
 #pragma unroll
         for (uint32_t u = 0; u < 2; ++u) {
-          const uint32_t p = p0 + h * kHalf + u * 32 + lane, dst = stage + (u * 32 + lane) * KVO_ROW_BYTES;
+          const uint32_t p = p0 + h * kHalf + u * 32 + lane;
           if (p < held && row[h][u] < 0) atomicOr(a.status, kFlagRange);
 #pragma unroll 1
           for (uint32_t e = 0; e < 2; ++e) {             // lanes 16 e ..
-            const uint32_t group = 2 * u + e, mask = there[u] >> 16 * e & 0xffffu;
-            const bool together = (run[u] >> 16 * e & 0xffffu) == 0xffffu;
-            if (halves) ok = wait(&sh.raw_empty[group], (halves - 1) & 1);
+            const uint32_t group = 2 * u + e, region = group % kRegions, use = uses + group / kRegions;
+            const uint32_t mask = there[u] >> 16 * e & 0xffffu;
+            const uint32_t dst = stage + region * S::kRegionBytes + lane % 16 * KVO_ROW_BYTES;
+            const bool together = (run[u] >> 16 * e & 0xffffu) == 0xffffu, mine = lane / 16 == e;
+            if (use) ok = wait(&sh.raw_empty[region], (use - 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            const bool mine = lane / 16 == e;
             if (mine && row[h][u] < 0) {
               for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
               fence_proxy_async_smem();                  // before a later copy to the same place
@@ -365,7 +387,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   } else {
     // positions: piece `piece` of each 128 latent bytes of rows slot and slot + 64
     const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3), group = warp / 4;
-    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), from = stage + slot * KVO_ROW_BYTES;
+    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), region = group % kRegions;
+    const uint32_t from = stage + region * S::kRegionBytes + slot % 16 * KVO_ROW_BYTES;
     const uint32_t to_lo = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3));
     const uint32_t to_hi = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + 1);
     const uint32_t to_rope = keys + 8 * kPieceBytes + swizzled(slot, piece);
@@ -393,36 +416,35 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       ok = wait(&sh.s_full[buf], t / kAhead & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
-      float x[kMine];
-      if constexpr (kMine == 32)
-        tmem_ld32(lanes + buf * (2 * kC), x);
-      else
-        tmem_ld16(lanes + buf * (2 * kC), x);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (uint32_t c = 0; c < kMine; c += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c]);
-        x[c] = exp2_approx(fmaf(x[c], a.scale, -l.x));
-        x[c + 1] = exp2_approx(fmaf(x[c + 1], a.scale, -l.y));
-        x[c + 2] = exp2_approx(fmaf(x[c + 2], a.scale, -l.z));
-        x[c + 3] = exp2_approx(fmaf(x[c + 3], a.scale, -l.w));
-      }
-      if (edge) {
+      for (uint32_t c0 = 0; c0 < kMine; c0 += 16) {
+        float x[16];
+        tmem_ld16(lanes + buf * (2 * kC) + c0, x);
+        tmem_ld_wait();
+        if (c0 + 16 == kMine) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_mbar_arrive_relaxed(s_empty + buf * 8);
+        }
 #pragma unroll
-        for (uint32_t c = 0; c < kMine; c += 4) {
-          const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c]);
-          x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
-          x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
-          x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
-          x[c + 3] = (int32_t)mine < see.w ? x[c + 3] : 0.0f;
+        for (uint32_t c = 0; c < 16; c += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c0 + c]);
+          fma_two(x[c], x[c + 1], a.scale, -l.x, -l.y);
+          fma_two(x[c + 2], x[c + 3], a.scale, -l.z, -l.w);
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) x[c + e] = exp2_approx(x[c + e]);
+          if (edge) {
+            const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c0 + c]);
+            x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
+            x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
+            x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
+            x[c + 3] = (int32_t)mine < see.w ? x[c + 3] : 0.0f;
+          }
+          add_two(sum[0], sum[1], x[c], x[c + 1]);
+          add_two(sum[2], sum[3], x[c + 2], x[c + 3]);
         }
       }
-#pragma unroll
-      for (uint32_t c = 0; c < kMine; ++c) sum[c & 3] += x[c];
       const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
       lost = (now - total) - add;
       total = now;
@@ -439,9 +461,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       float* const sums = &sh.sums[job & 1][0][quad * 32 + lane];
       if (quarter) sums[(quarter - 1) * kTile] = total;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.summed);
+      if (lane == 0) mbar_arrive(&sh.summed[job & 1]);
       if (quarter == 0) {
-        ok = wait(&sh.summed, job & 1);
+        ok = wait(&sh.summed[job & 1], job >> 1 & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         total = there ? (total + sums[0]) + (sums[kTile] + sums[2 * kTile]) : 0.0f;
         if (last.slot != UINT32_MAX)
@@ -475,27 +497,37 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
         ok = ok && wait(&sh.raw_full[group], h);         // (two halves a job)
-        uint4 lat[4];
+        uint4 lat[4], lo[4], up[4];
         for (uint32_t k = 0; k < 4; ++k) lat[k] = lds16(from + 128 * k + 16 * piece);
         const uint4 eight = lds16(from + KVO_LATENT_BYTES), rope = lds16(from + KVO_LATENT_BYTES + 16 + 16 * piece);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
-        if (lane == 0) mbar_arrive(&sh.raw_empty[group]);
-        if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) return false;
         const uint32_t pick = piece >= 4 ? 0x7632u : 0x5410u;
         const uint32_t scales[2] = {__byte_perm(eight.x, eight.y, pick), __byte_perm(eight.z, eight.w, pick)};
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k) {
           const uint16_t scale = (uint16_t)(scales[k >> 1] >> (k & 1) * 16);
           const float bias = -1152.0f * __half2float(__ushort_as_half(scale));
-          uint4 x, y;
-          dequant4(lat[k].x, scale, bias, x.x, x.y);
-          dequant4(lat[k].y, scale, bias, x.z, x.w);
-          dequant4(lat[k].z, scale, bias, y.x, y.y);
-          dequant4(lat[k].w, scale, bias, y.z, y.w);
-          sts16(to_lo + 2 * k * kPieceBytes + h * 8192, x);
-          sts16(to_hi + 2 * k * kPieceBytes + h * 8192, y);
+          dequant4(lat[k].x, scale, bias, lo[k].x, lo[k].y);
+          dequant4(lat[k].y, scale, bias, lo[k].z, lo[k].w);
+          dequant4(lat[k].z, scale, bias, up[k].x, up[k].y);
+          dequant4(lat[k].w, scale, bias, up[k].z, up[k].w);
+        }
+        // The rows have to be in registers before the next ones may come: loads
+        // wait behind other warps' stores for longer than a copy takes, and an
+        // arrival does not.  (Every value goes into the vote, whose outcome
+        // changes nothing.)
+        uint32_t all = rope.x ^ rope.y ^ rope.z ^ rope.w;
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          all ^= lo[k].x ^ lo[k].y ^ lo[k].z ^ lo[k].w ^ up[k].x ^ up[k].y ^ up[k].z ^ up[k].w;
+        if (__any_sync(0xffffffffu, all == 0x9e3779b9u)) __nanosleep(0);
+        if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
+        if (lane == 0) mbar_arrive(&sh.raw_empty[region]);
+        if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+          sts16(to_lo + 2 * k * kPieceBytes + h * 8192, lo[k]);
+          sts16(to_hi + 2 * k * kPieceBytes + h * 8192, up[k]);
         }
         sts16(to_rope + h * 8192, rope);
       }
@@ -518,7 +550,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       }
       return true;
     });
-    if (jobs && __all_sync(0xffffffffu, ok)) finish();
+    // The last release too has to come before the CTA ends: what came later
+    // would find another CTA's shared memory there.  And it says that every warp
+    // has ended the job before the last but one, whose barrier and sums are next.
+    if (jobs && __all_sync(0xffffffffu, ok)) {
+      ok = wait(&sh.k_empty, (jobs - 1) & 1);
+      if (__all_sync(0xffffffffu, ok)) finish();
+    }
   }
 
   // Both CTAs end together: the MMAs read the other's memory, and arrivals and
@@ -606,7 +644,7 @@ cudaError_t launch_weights(const WeightArgs& a, const CUtensorMap& map, cudaStre
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev & 63]) {
-    e = cudaFuncSetAttribute(weights_kernel<kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWeightSmem);
+    e = cudaFuncSetAttribute(weights_kernel<kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WeightShape<kC>::kSmem);
     if (e != cudaSuccess) return e;
     ready[dev & 63] = true;
   }
@@ -620,7 +658,7 @@ cudaError_t launch_weights(const WeightArgs& a, const CUtensorMap& map, cudaStre
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.gridDim = dim3(2 * a.pairs);
   lc.blockDim = dim3(kWeightThreads);
-  lc.dynamicSmemBytes = kWeightSmem;
+  lc.dynamicSmemBytes = WeightShape<kC>::kSmem;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 2;

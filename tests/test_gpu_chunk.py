@@ -687,3 +687,203 @@ def test_waits_that_run_out(kvo, counts, lens, heads):
                 assert torch.equal(a, b), clocks
         assert c.sync() == kvo.KVO_OK
     c.close()
+
+
+# ------------------------------------------- attention of many tokens at once
+class Long(Chunk):
+    """The same held positions in a cache with room for many more: enough work for the kernel of many columns."""
+
+    def attend(self, ctx, rows=60_000, **kw):
+        blocks = -(-rows // self.br)
+        table = np.full((self.n, blocks), -1, np.int32)
+        part = np.arange(self.n, dtype=np.int32)[:, None] if self.table is None else self.table[:, :blocks]
+        table[:, :part.shape[1]] = part
+        cache = self.kvo.Cache(rows=dev(self.raw), block_rows=self.br, table=dev(table))
+        return ctx.attend_chunk(cache, self.q, self.dev_starts, self.dev_lens, self.scale, rows, **kw)
+
+
+@pytest.mark.parametrize("counts,lens,heads,block_rows", [
+    ([4], [4], 64, 16), ([4], [300], 64, 16), ([256], [256], 1, 64), ([200], [777], 3, 7), ([13], [1000], 20, 0),
+    ([2, 0, 5, 9], [700, 40, 5, 300], 100, 16), ([90], [400], 128, 64), ([64] * 3, [2000, 777, 513], 64, 16),
+    ([130, 1, 66], [130, 1, 255], 128, 16), ([33] * 9, [256 * i + 33 for i in range(9)], 16, 64), ([40], [5000], 128, 16)])
+def test_long_chunk(kvo, ctx, counts, lens, heads, block_rows):
+    rng = np.random.default_rng([101, sum(counts), max(lens), heads])
+    c = Long(kvo, rng, counts, lens, heads, block_rows)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("heads", [40, 64, 128])
+def test_long_chunk_leaves_other_tokens_alone(kvo, ctx, heads):
+    """Tokens before the first sequence's and behind the last one's, tokens that see nothing, negative lengths."""
+    rng = np.random.default_rng([102, heads])
+    c = Long(kvo, rng, [9, 20, 5, 26, 0], [4, 0, -7, 200, 90], heads, first=2, after=5)
+    out = torch.full((c.tokens, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.tokens, heads), 7.0, device="cuda")
+    c.attend(ctx, out=out, lse=lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    for x in (out, lse):
+        assert (x[:2] == 7).all() and (x[-5:] == 7).all()
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "one", "steps"])
+@pytest.mark.parametrize("n", [200, 1300])
+@pytest.mark.parametrize("tokens,heads", [(14, 20), (90, 64)])
+def test_long_chunk_wide_logits(kvo, ctx, order, n, tokens, heads):
+    """Logits of hundreds along the positions: far above the first tile's for some heads, far below for others."""
+    rng = np.random.default_rng([103, tokens, n, len(order)])
+    raw = random_rows(rng, n)
+    for j in range(n):
+        x = np.zeros(64)
+        x[:8] = {"rising": j / 20, "falling": (n - j) / 20, "one": 60.0 * (j == n * 3 // 5), "steps": 9.0 * (j // 129)}[order]
+        raw[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+    q = rng.standard_normal((tokens, heads, 576))
+    q[..., 512:520] = np.linspace(-1, 4, heads)[None, :, None]
+    c = Long(kvo, rng, [tokens], [n], heads, 0, scale=0.5, q=dev(q, torch.bfloat16), raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("heads,tokens", [(16, 40), (64, 140)])
+def test_long_chunk_values_that_are_not_seen(kvo, ctx, heads, tokens):
+    rng = np.random.default_rng([104, heads, tokens])
+    n, at = 333, 333 - tokens // 2
+    c = Long(kvo, rng, [tokens], [n], heads, rows=400)
+    clean = c.attend(ctx)
+    raw = c.raw.copy()
+    raw[[O.row_of(c.table, c.total, 16, 1, 0, p) for p in range(n, 400)], 512:] = 0xFF
+    nan = O.row_of(c.table, c.total, 16, 1, 0, at)
+    for kind in range(4):
+        spoilt = raw.copy()
+        if kind == 0:
+            spoilt[nan, 518:520] = 0xFF                       # a NaN scale
+        elif kind == 1:
+            spoilt[nan, 512:514] = np.array([0x7C00], np.uint16).view(np.uint8)   # an infinite one
+        elif kind == 2:
+            spoilt[nan, 600:602] = 0xFF                       # a NaN in the position part
+        d = Long(kvo, rng, [tokens], [n], heads, rows=400, q=c.q, raw=spoilt, table=(c.table, c.total))
+        out, lse = d.attend(ctx)
+        assert ctx.sync() == kvo.KVO_OK
+        before = at - (n - tokens) if kind < 3 else tokens    # tokens that do not see it
+        assert torch.equal(out[:before], clean[0][:before]) and torch.equal(lse[:before], clean[1][:before])
+        assert torch.isnan(lse[before:]).all() and torch.isnan(out[before:, :, :64]).all()
+    q = c.q.clone()                                           # a NaN query is its own columns' alone
+    q[5, 3] = float("nan")
+    d = Long(kvo, rng, [tokens], [n], heads, rows=400, q=q, raw=c.raw, table=(c.table, c.total))
+    out, lse = d.attend(ctx)
+    assert torch.isnan(out[5, 3]).all() and torch.isnan(lse[5, 3])
+    out[5, 3], lse[5, 3] = clean[0][5, 3], clean[1][5, 3]
+    # A column whose logits have no maximum sends its 256 columns through another pass, with other references r': their
+    # weights 2^(z - r') are rounded to bf16 afresh, each by 2^-8 at most as before, so that the bits may change and the
+    # bound stays.
+    c.check_attend(out, lse)
+    assert torch.equal(out[16:], clean[0][16:]) and torch.equal(lse[16:], clean[1][16:])
+
+
+def test_long_chunk_infinite_logits(kvo, ctx):
+    rng = np.random.default_rng(105)
+    n, heads, tokens = 700, 20, 60
+    raw = random_rows(rng, n)
+    raw[3::7, 528:530] = np.array([0x7F80], np.uint16).view(np.uint8)             # +inf
+    raw[:300, 528:530] = np.array([0x7F80], np.uint16).view(np.uint8)             # whole tiles of them
+    q = np.abs(rng.standard_normal((tokens, heads, 576)))
+    q[:, :, 512] = -np.abs(q[:, :, 512])
+    c = Long(kvo, rng, [tokens], [n], heads, 0, q=dev(q, torch.bfloat16), raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    keys = C.values(raw)
+    for t in range(tokens):
+        seen = C.seen(c.starts, c.lens, 0, t, n)
+        have = [p for p in range(300, seen) if p % 7 != 3]
+        want, want_lse, spread, size = C.attend(f64(c.q)[t], SCALE, keys[have])
+        tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 4 * U * 576 * size + 100 * U)[:, None]
+        assert (np.abs(f64(out)[t] - want) <= tol).all()
+        assert (np.abs(f64(lse)[t] - want_lse) <= 2 * U * 576 * size + 100 * U + 2 * U * np.abs(want_lse)).all()
+    raw[:, 528:530] = np.array([0x7F80], np.uint16).view(np.uint8)
+    c = Long(kvo, rng, [tokens], [n], heads, 0, q=c.q, raw=raw)
+    out, lse = c.attend(ctx)
+    assert ctx.sync() == kvo.KVO_OK
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("heads,tokens", [(64, 50), (128, 70)])
+def test_long_chunk_bad_pages(kvo, ctx, heads, tokens):
+    rng = np.random.default_rng([106, heads])
+    table = np.array([[-1, 1, -5, 3, 0, 77, 2 ** 31 - 1], [2, 0, 77, 9999, -1, -1, -1]], np.int32)
+    for lens, want in (([112, 60], kvo.KVO_ERANGE), ([80, 20], kvo.KVO_ERANGE), ([0, 32], kvo.KVO_OK)):
+        c = Long(kvo, rng, [tokens, min(tokens, 7)], lens, heads, 16, rows=112, table=(table, 4))
+        out, lse = c.attend(ctx)
+        assert ctx.sync() == want
+        c.check_attend(out, lse)
+
+
+def test_long_chunk_bad_starts(kvo, ctx):
+    rng = np.random.default_rng(107)
+    c = Long(kvo, rng, [40, 40, 40], [100, 90, 80], 20)
+    for starts in ([0, 40, 80, 121], [-1, 40, 80, 120], [0, 90, 40, 120], [0, 40, 2 ** 31 - 1, 120], [0, -2 ** 31, 80, 120]):
+        wide = torch.full((122, 20, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        c.dev_starts = dev(starts, torch.int32)
+        c.attend(ctx, out=wide[1:121], lse=torch.zeros(120, 20, device="cuda"))
+        assert ctx.sync() == kvo.KVO_ERANGE, starts
+        assert (wide[0] == 7).all() and (wide[121] == 7).all()
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([70], [300], 24), ([30, 41], [200, 99], 128), ([40, 41], [99, 200], 7)])
+def test_long_chunk_strides(kvo, ctx, counts, lens, heads):
+    rng = np.random.default_rng([108, heads])
+    c = Long(kvo, rng, counts, lens, heads)
+    want, want_lse = c.attend(ctx)
+    c.check_attend(want, want_lse)
+    wide = torch.full((c.tokens, 2 * heads, 592), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1::2, 8:584] = c.q
+    across = torch.empty(heads, c.tokens, 576, dtype=torch.bfloat16, device="cuda")
+    across.copy_(c.q.transpose(0, 1))
+    for q in (wide[:, 1::2, 8:584], across.transpose(0, 1)):
+        c.q = q
+        out, lse = c.attend(ctx)
+        assert ctx.sync() == kvo.KVO_OK
+        c.check_attend(out, lse)
+        assert ctx.sync() == kvo.KVO_OK
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([64] * 3, [5000, 777, 2000], 64), ([90, 300], [4000, 900], 64), ([600], [600], 16),
+                                               ([1] * 40, [3000] * 40, 64), ([5] * 9, [3100] * 9, 20)])
+def test_the_same_bits_every_time(kvo, ctx, counts, lens, heads):
+    """One call behind the other, on the same inputs."""
+    rng = np.random.default_rng([109, heads])
+    for kind in (Long, Chunk):
+        c = kind(kvo, rng, counts, lens, heads)
+        out, lse = c.attend(ctx)
+        weights = c.weights(ctx, lse)
+        for _ in range(20):
+            got = [c.attend(ctx) for _ in range(3)]
+            sums = [c.weights(ctx, lse) for _ in range(6)]
+            for o, l in got:
+                assert torch.equal(o, out) and torch.equal(l, lse)
+            for w in sums:
+                assert torch.equal(w, weights)
+        assert ctx.sync() == kvo.KVO_OK
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([20, 12], [300, 40], 20), ([64] * 3, [5000, 777, 2000], 64)])
+def test_long_chunk_waits_that_run_out(kvo, counts, lens, heads):
+    rng = np.random.default_rng([110, sum(counts)])
+    c = kvo.Context(1, 64, 64)
+    chunk = Long(kvo, rng, counts, lens, heads)
+    want = [t.clone() for t in chunk.attend(c)]
+    assert c.sync() == kvo.KVO_OK
+    for clocks in WAITS:
+        c.set_wait_clocks(clocks)
+        got = chunk.attend(c)
+        status = c.sync()
+        assert status in ((kvo.KVO_ETIMEDOUT,) if clocks == 0 else (kvo.KVO_OK, kvo.KVO_ETIMEDOUT))
+        assert c.sync() == kvo.KVO_OK
+        c.set_wait_clocks()
+        for again in (got if status == kvo.KVO_OK else None, chunk.attend(c)):
+            for a, b in zip(again or (), want):
+                assert torch.equal(a, b), clocks
+        assert c.sync() == kvo.KVO_OK
+    c.close()

@@ -383,7 +383,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (part) rope[u] = lds16(p - 256 + KVO_LATENT_BYTES + 16);
           }
         if (part) {                                        // after a wait that gave up the next rows must not come
-          __syncwarp();
+          uint32_t all = 0;
+#pragma unroll
+          for (uint32_t u = 0; u < S::kPasses; ++u)
+            if (slot + 64 * u < rows) all ^= mixed(lat[0][u]) ^ mixed(lat[1][u]) ^ mixed(rope[u]);
+          loads_are_in(all);
           if (lane == 0 && come) mbar_arrive(&sh.raw_empty);
         }
         if (i > 0) wait(&sh.pv_done[part], turn ^ 1);

@@ -64,6 +64,15 @@ __device__ __forceinline__ float max_three(float a, float b, float c) {
   return r;
 }
 
+// All lanes' loads of these values have come when this returns: an arrival that
+// lets a copy overwrite what they read is not held up by loads that are still
+// queued (behind other warps' stores, for longer than a copy takes).  The vote
+// needs the values; its outcome changes nothing.
+__device__ __forceinline__ void loads_are_in(uint32_t all) {
+  if (__any_sync(0xffffffffu, all == 0x9e3779b9u)) __nanosleep(0);
+}
+__device__ __forceinline__ uint32_t mixed(uint4 v) { return v.x ^ v.y ^ v.z ^ v.w; }
+
 // Whether any of eight fp16 is infinite or NaN.
 __device__ __forceinline__ bool any_not_finite(uint4 eight) {
   constexpr uint32_t kInf = 0x7c007c00u;

@@ -511,15 +511,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           dequant4(lat[k].z, scale, bias, up[k].x, up[k].y);
           dequant4(lat[k].w, scale, bias, up[k].z, up[k].w);
         }
-        // The rows have to be in registers before the next ones may come: loads
-        // wait behind other warps' stores for longer than a copy takes, and an
-        // arrival does not.  (Every value goes into the vote, whose outcome
-        // changes nothing.)
-        uint32_t all = rope.x ^ rope.y ^ rope.z ^ rope.w;
+        uint32_t all = mixed(rope);                      // the rows are in registers before the next ones may come
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-          all ^= lo[k].x ^ lo[k].y ^ lo[k].z ^ lo[k].w ^ up[k].x ^ up[k].y ^ up[k].z ^ up[k].w;
-        if (__any_sync(0xffffffffu, all == 0x9e3779b9u)) __nanosleep(0);
+        for (uint32_t k = 0; k < 4; ++k) all ^= mixed(lo[k]) ^ mixed(up[k]);
+        loads_are_in(all);
         if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
         if (lane == 0) mbar_arrive(&sh.raw_empty[region]);
         if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);

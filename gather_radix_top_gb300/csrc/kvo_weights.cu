@@ -407,8 +407,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // one tile's weights to the sum; lane l has looked up column l
     auto add_tile = [&](uint32_t mine) -> bool {
       const uint32_t buf = t % kAhead;
+      if (lse == -INFINITY) seen = 0;                      // a column that weighs nothing
       if (lane < kMine) {
-        sh.lse[warp][lane] = lse;
+        sh.lse[warp][lane] = seen ? lse * kLog2e : 0.0f;
         sh.seen[warp][lane] = seen;
       }
       const bool edge = __any_sync(0xffffffffu, seen <= (int32_t)(mine | 31));
@@ -484,9 +485,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         const uint32_t head = half % cols.across * cols.wide + wide;
         const uint32_t at = cols.flat ? row : row * a.heads + head, token = divide(at, a.by_heads);
         if (token < run.from || token >= run.tokens || (!cols.flat && head >= a.heads)) return;
-        const float l = __ldg(a.lse + (int64_t)run.first * a.heads + at);
-        if (l == -INFINITY) return;
-        *to_lse = l * kLog2e;
+        *to_lse = __ldg(a.lse + (int64_t)run.first * a.heads + at);   // (looked at when its tile is)
         *to_seen = min(run.before + (int32_t)token, (int32_t)run.len);
       };
       float next_lse, next_carried = 0.0f;
@@ -500,6 +499,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         uint4 lat[4], lo[4], up[4];
         for (uint32_t k = 0; k < 4; ++k) lat[k] = lds16(from + 128 * k + 16 * piece);
         const uint4 eight = lds16(from + KVO_LATENT_BYTES), rope = lds16(from + KVO_LATENT_BYTES + 16 + 16 * piece);
+        uint32_t all = mixed(eight) ^ mixed(rope);       // the rows are in registers before the next ones may come
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) all ^= mixed(lat[k]);
+        loads_are_in(all);
+        if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
+        if (lane == 0) mbar_arrive(&sh.raw_empty[region]);
         const uint32_t pick = piece >= 4 ? 0x7632u : 0x5410u;
         const uint32_t scales[2] = {__byte_perm(eight.x, eight.y, pick), __byte_perm(eight.z, eight.w, pick)};
 #pragma unroll
@@ -511,12 +516,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           dequant4(lat[k].z, scale, bias, up[k].x, up[k].y);
           dequant4(lat[k].w, scale, bias, up[k].z, up[k].w);
         }
-        uint32_t all = mixed(rope);                      // the rows are in registers before the next ones may come
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) all ^= mixed(lo[k]) ^ mixed(up[k]);
-        loads_are_in(all);
-        if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
-        if (lane == 0) mbar_arrive(&sh.raw_empty[region]);
         if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
 #pragma unroll

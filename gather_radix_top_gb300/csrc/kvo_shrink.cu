@@ -7,6 +7,8 @@
 // have the largest key of all), then an ordered compaction, ties to the lower
 // position.  The second copies rows, keys and factors, a warp for four rows:
 // their 164 pieces of 16 bytes are all asked for before the first is stored.
+#include <algorithm>
+
 #include "kvo_cache.cuh"
 #include "kvo_topk_body.cuh"
 
@@ -14,6 +16,8 @@ namespace kvo {
 namespace {
 
 using namespace topk_detail;
+
+constexpr uint32_t kKeepStatic = 8 * 1024, kKeepSmem = 227 * 1024 - kKeepStatic;
 
 struct ShrinkArgs {
   CacheView from, to;
@@ -26,13 +30,14 @@ struct ShrinkArgs {
   int64_t weights_ld, kept_ld, to_weights_ld;
   uint32_t rows, budget, first, last;
   uint32_t key_pieces;       // 16-byte pieces of a key: 0 (none move), 8 or 16
+  uint32_t held;             // keys that a CTA has room for, in fours
 };
 
-// kResident: a CTA's keys fit in its shared memory; else every pass reads the
-// weights again.
-template <bool kResident>
+// A CTA's keys stay in its shared memory, as far as they fit; the passes read
+// the weights of the others again.
 __global__ void __launch_bounds__(kThreads, 1) keep_kernel(const __grid_constant__ ShrinkArgs a) {
   extern __shared__ __align__(16) uint8_t dyn_smem[];
+  static_assert(sizeof(RadixSmem) + 4 * 2 * (2 * kWarps + 2) + 16 * kMaxCluster <= kKeepStatic);
   __shared__ RadixSmem rsm;
   __shared__ uint32_t scratch[2][2 * kWarps + 2];
   __shared__ uint32_t table[kMaxCluster][4];
@@ -61,7 +66,13 @@ __global__ void __launch_bounds__(kThreads, 1) keep_kernel(const __grid_constant
     const uint32_t p = lo + i;
     return p < a.first || p >= len - a.last ? 0xffffffffu : score_key(__ldg(w + p));
   };
+  const bool wide = (reinterpret_cast<uintptr_t>(w + lo) & 15u) == 0;
   auto four = [&](uint32_t g) -> uint4 {
+    const uint32_t p = lo + 4 * g;
+    if (wide && p >= a.first && p + 4 <= len - a.last && 4 * g + 4 <= count) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(w + p));
+      return make_uint4(score_key(f.x), score_key(f.y), score_key(f.z), score_key(f.w));
+    }
     uint32_t v[4];
 #pragma unroll
     for (uint32_t e = 0; e < 4; ++e) v[e] = 4 * g + e < count ? key(4 * g + e) : 0u;
@@ -72,16 +83,13 @@ __global__ void __launch_bounds__(kThreads, 1) keep_kernel(const __grid_constant
     if (to_w) to_w[out] = __ldg(w + lo + i);
   };
   radix_smem_init(&rsm);
-  if constexpr (kResident) {
-    uint32_t* const keys = reinterpret_cast<uint32_t*>(dyn_smem);
-    for (uint32_t i = tid; i < (count + 3) / 4 * 4; i += kThreads) keys[i] = i < count ? key(i) : 0u;
-    cluster_sync();
-    select_and_emit([&](uint32_t g) { return reinterpret_cast<const uint4*>(keys)[g]; }, count, n, 32, &rsm, scratch,
-                    table, emit);
-  } else {
-    cluster_sync();
-    select_and_emit(four, count, n, 32, &rsm, scratch, table, emit);
-  }
+  uint4* const keys = reinterpret_cast<uint4*>(dyn_smem);
+  const uint32_t held = min((count + 3) / 4, a.held);
+  for_groups(four, held, [&](uint32_t g, uint4 v) {
+    if (g < held) keys[g] = v;
+  });
+  cluster_sync();
+  select_and_emit([&](uint32_t g) { return g < held ? keys[g] : four(g); }, count, n, 32, &rsm, scratch, table, emit);
 }
 
 constexpr uint32_t kMoveThreads = 256, kMoveRows = 4;    // rows of a warp
@@ -132,29 +140,24 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   if (pieces == 8 && dst >= 0) a.to.key_scales[dst] = src >= 0 ? a.from.key_scales[src] : 0.0f;
 }
 
-cudaError_t launch_keep(const ShrinkArgs& a, uint32_t sequences, cudaStream_t stream) {
+cudaError_t launch_keep(ShrinkArgs a, uint32_t sequences, cudaStream_t stream) {
   static int widest[64] = {};                            // clusters of 1,024 threads and all shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   int& most = widest[dev & 63];
   if (!most) {
-    int both = (int)kMaxCluster;
-    for (const void* kern : {(const void*)keep_kernel<true>, (const void*)keep_kernel<false>}) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTopkMaxDynSmem);
-      if (e != cudaSuccess) return e;
-      const int c = best_cluster(kern, kTopkMaxDynSmem, (int)kMaxCluster);
-      if (c < 1) return cudaErrorInvalidConfiguration;
-      both = c < both ? c : both;
-    }
-    most = both;
+    e = cudaFuncSetAttribute(keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeepSmem);
+    if (e != cudaSuccess) return e;
+    const int c = best_cluster((const void*)keep_kernel, kKeepSmem, (int)kMaxCluster);
+    if (c < 1) return cudaErrorInvalidConfiguration;
+    most = c;
   }
   // As many CTAs a sequence as the GPU has room for at once, but not so many
   // that one gets less than a tile of the compaction.
   uint32_t C = 1;
   while ((int)C < most && 2 * C * sequences <= (uint32_t)device_sms() && a.rows > C * 4u * kThreads) C *= 2;
-  const uint32_t chunk = topk_chunk(a.rows, C);
-  const bool resident = (uint64_t)chunk * 4u <= kTopkMaxDynSmem;
+  a.held = std::min(topk_chunk(a.rows, C), kKeepSmem / 4) / 4;
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -165,11 +168,11 @@ cudaError_t launch_keep(const ShrinkArgs& a, uint32_t sequences, cudaStream_t st
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.gridDim = dim3(C * sequences);
   lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = resident ? (size_t)chunk * 4u : 0;
+  lc.dynamicSmemBytes = a.held * 16;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, resident ? keep_kernel<true> : keep_kernel<false>, a);
+  return cudaLaunchKernelEx(&lc, keep_kernel, a);
 }
 
 }  // namespace

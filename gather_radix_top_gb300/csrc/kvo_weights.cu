@@ -40,11 +40,13 @@ constexpr uint32_t kTileCost = 3;                        // of a tile of positio
 
 // kC: a CTA's columns of a tile.  What the positions leave of shared memory goes
 // to the raw rows where a tile of positions meets few columns (room for four
-// groups of 16, and eight pieces of 32 columns), else to the queries (six pieces
-// of 64 columns, two groups).
+// groups of 16, and one tile's nine pieces of 32 columns, which stay for as long
+// as the next tile of positions meets the same ones), else to the queries (six
+// pieces of 64 columns, two groups).
 template <uint32_t kC>
 struct WeightShape {
-  static constexpr uint32_t kSlotBytes = kC * 128, kSlots = kC == 32 ? 8 : 6;
+  static constexpr uint32_t kSlotBytes = kC * 128, kSlots = kC == 32 ? 9 : 6;
+  static constexpr bool kKeep = kSlots == 9;
   static constexpr uint32_t kRegions = kC == 32 ? 4 : 2;           // group g's rows go to region g % kRegions
   static constexpr uint32_t kRegionBytes = 16 * KVO_ROW_BYTES;
   static constexpr uint32_t kSmem = 1024 + 9 * kPieceBytes + kSlots * kSlotBytes + kRegions * kRegionBytes;
@@ -76,10 +78,17 @@ struct WeightShared {
   uint32_t issued[2][kQueries];      // per CTA and query warp: pieces of its own and before them that it has asked for
   uint32_t brought[4];               // halves that each group's rows have come for
   uint32_t there[4][4];              // per job in turns: rows that are not masked, row r is bit r % 32 of word r / 32
-  alignas(16) float lse[kWorkers][32];   // per warp and column, base 2
-  alignas(16) int32_t seen[kWorkers][32];    // and the positions it sees
   float sums[2][3][kTile];           // per job in turns: of the quarters 1 to 3
 };
+
+// A worker warp's columns, where they are too many to pass from lane to lane.
+template <uint32_t kMine>
+struct ColumnShared {
+  alignas(16) float lse[kWorkers][kMine];    // base 2
+  alignas(16) int32_t seen[kWorkers][kMine]; // the positions it sees
+};
+template <>
+struct ColumnShared<16> {};
 
 // A sequence's columns.
 struct Run {
@@ -118,6 +127,17 @@ struct Job {
   uint32_t seq, p0;                  // the pair's first position
   uint32_t begin, end;               // tiles of columns
   uint32_t slot;                     // of part, or UINT32_MAX: all of its columns
+};
+
+// The queries of one tile, as the roles that bring and use them count jobs: a
+// job whose first tile is the last one's before it finds them in place.
+struct Kept {
+  uint32_t seq = UINT32_MAX, tile = 0;
+  __device__ __forceinline__ bool has(const Job& job) const { return seq == job.seq && tile == job.begin; }
+  __device__ __forceinline__ void set(const Job& job) {
+    seq = job.seq;
+    tile = job.end - 1;
+  }
 };
 
 // All sequences' work, 32 of them at a time: f(first sequence, work before it and the lanes' after it).
@@ -187,6 +207,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   constexpr uint32_t kMine = kC / 2;                     // columns of a worker warp
   extern __shared__ uint8_t raw[];
   __shared__ WeightShared<kSlots, kRegions> sh;
+  __shared__ ColumnShared<kMine> sc;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank(), pair = blockIdx.x >> 1;
   const uint32_t keys = (smem_u32(raw) + 1023u) & ~1023u, ring = keys + 9 * kPieceBytes, stage = ring + kSlots * kSlotBytes;
 
@@ -232,22 +253,24 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   bool ok = true;
 
   if (warp == kRows) {
-    // Lane l looks up rows l and l + 32 of each half, a job ahead.  Sixteen rows
+    // Lane l looks up rows l and l + 32 of each half, a job ahead: their blocks are
+    // asked for before the rows of the job before come.  Sixteen rows
     // are a group: one copy where they lie one behind the other, as those of a
     // block do (a copy for every row takes 66 clocks each to issue).
     uint32_t halves = 0, p0 = 0;
-    int64_t row[2][2];                                   // of the job whose rows come next: [half][l, l + 32]
+    int32_t block[2][2];                                 // of the job whose rows come next: [half][l, l + 32]
     uint32_t held = 0;
     auto bring = [&]() -> bool {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h, ++halves) {
         uint32_t there[2], run[2];
-        int64_t first[2];
+        int64_t row[2], first[2];
 #pragma unroll
         for (uint32_t u = 0; u < 2; ++u) {
-          there[u] = __ballot_sync(0xffffffffu, row[h][u] >= 0);
-          first[u] = __shfl_sync(0xffffffffu, row[h][u], lane & 16);
-          run[u] = __ballot_sync(0xffffffffu, row[h][u] >= 0 && row[h][u] == first[u] + (lane & 15));
+          row[u] = cache_row_in(a.cache, block[h][u], p0 + h * kHalf + u * 32 + lane);
+          there[u] = __ballot_sync(0xffffffffu, row[u] >= 0);
+          first[u] = __shfl_sync(0xffffffffu, row[u], lane & 16);
+          run[u] = __ballot_sync(0xffffffffu, row[u] >= 0 && row[u] == first[u] + (lane & 15));
         }
         if (lane < 2) sh.there[jobs & 3][2 * h + lane] = lane ? there[1] : there[0];   // (a slow warp may be three jobs behind)
         // The regions' uses so far: group g of this half is use `uses + g / kRegions` of its region.
@@ -275,7 +298,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll
         for (uint32_t u = 0; u < 2; ++u) {
           const uint32_t p = p0 + h * kHalf + u * 32 + lane;
-          if (p < held && row[h][u] < 0) atomicOr(a.status, kFlagRange);
+          if (p < held && row[u] < 0) atomicOr(a.status, kFlagRange);
 #pragma unroll 1
           for (uint32_t e = 0; e < 2; ++e) {             // lanes 16 e ..
             const uint32_t group = 2 * u + e, region = group % kRegions, use = uses + group / kRegions;
@@ -284,7 +307,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
             const bool together = (run[u] >> 16 * e & 0xffffu) == 0xffffu, mine = lane / 16 == e;
             if (use) ok = wait(&sh.raw_empty[region], (use - 1) & 1);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            if (mine && row[h][u] < 0) {
+            if (mine && row[u] < 0) {
               for (uint32_t c = 0; c < KVO_ROW_BYTES / 16; ++c) sts16(dst + 16 * c, make_uint4(0, 0, 0, 0));
               fence_proxy_async_smem();                  // before a later copy to the same place
             }
@@ -294,8 +317,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
               sh.brought[group] = halves + 1;
             }
             __syncwarp();
-            if (mine && row[h][u] >= 0 && (!together || lane % 16 == 0))
-              bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row[h][u] * KVO_ROW_BYTES,
+            if (mine && row[u] >= 0 && (!together || lane % 16 == 0))
+              bulk_copy_g2s(raw + (dst - smem_u32(raw)), a.cache.rows + row[u] * KVO_ROW_BYTES,
                             (together ? 16 : 1) * KVO_ROW_BYTES, &sh.raw_full[group]);
           }
         }
@@ -305,15 +328,15 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     };
     bool some = false;
     for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
-      int64_t next[2][2];
+      int32_t next[2][2];
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t p = job.p0 + rank * kTile + i * 32 + lane;
-        next[i / 2][i % 2] = p < run.len ? cache_row(a.cache, job.seq, p) : -1;
+        next[i / 2][i % 2] = p < run.len ? cache_block(a.cache, job.seq, p) : -1;
       }
       if (some && !bring()) return false;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) row[i / 2][i % 2] = next[i / 2][i % 2];
+      for (uint32_t i = 0; i < 4; ++i) block[i / 2][i % 2] = next[i / 2][i % 2];
       p0 = job.p0 + rank * kTile;
       held = run.len;
       some = true;
@@ -324,11 +347,14 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // the queries' pieces: warp w takes every kQueries-th one
     const uint32_t w = warp - kQuery, full0 = dsmem_addr(&sh.full[0], 0);
     uint32_t at = 0;                                     // the job's first piece
+    Kept kept;
     for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
-      const uint32_t tiles = job.end > job.begin ? job.end - job.begin : 0;
+      if (job.end <= job.begin) return true;
+      const uint32_t begin = job.begin + (S::kKeep && kept.has(job)), pieces = 9 * (job.end - begin);
+      kept.set(job);
       if (lane == 0) {
-        for (uint32_t k = (w + at) % kQueries; k < 9 * tiles; k += kQueries) {
-          const uint32_t tile = job.begin + k / 9, piece = k % 9, slot = (at + k) % kSlots;
+        for (uint32_t k = (w + at) % kQueries; k < pieces; k += kQueries) {
+          const uint32_t tile = begin + k / 9, piece = k % 9, slot = (at + k) % kSlots;
           const uint32_t half = 2 * tile + rank, row = half / cols.across, head = half % cols.across * cols.wide;
           if (at + k >= kSlots) ok = wait(&sh.empty[slot], ((at + k) / kSlots - 1) & 1);
           if (!ok) break;
@@ -338,7 +364,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           n = at + k + 1;
         }
       }
-      at += 9 * tiles;
+      at += pieces;
       return (bool)__shfl_sync(0xffffffffu, ok, 0);
     });
     if (lane == 0) {
@@ -348,30 +374,36 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       dsmem_st_u32(dsmem_addr(&sh.issued[rank][w], 0), n);
     }
   } else if (warp == kMma) {
-    if (rank == 0)
+    if (rank == 0) {
+      Kept kept;
       for_jobs(a, pair, lo, hi, [&](const Job& job, const Run&) {
         constexpr uint32_t kDesc = pair_desc(1, 2 * kC, false, false);
         const uint64_t k_tile = tile_desc(keys, 16), q_ring = tile_desc(ring, 16);
         const uint32_t tiles = job.end > job.begin ? job.end - job.begin : 0;
+        const bool again = S::kKeep && tiles && kept.has(job), other = S::kKeep && tiles && !again && kept.seq != UINT32_MAX;
+        if (tiles) kept.set(job);
         if (elect_one()) {
+          if (other)                                       // the kept queries are done with
+            for (uint32_t i = 0; i < kSlots; ++i) pair_commit(&sh.empty[i], 3);
           ok = wait(&sh.k_full, jobs & 1);
           uint32_t slot = n % kSlots, turn = n / kSlots & 1;
           for (uint32_t i = 0, at = t; i < tiles && ok; ++i, ++at) {
             const uint32_t buf = at % kAhead;
+            const bool here = again && i == 0, keep = S::kKeep && i + 1 == tiles;
             if (at >= kAhead) ok = wait(&sh.s_empty[buf], (at / kAhead - 1) & 1);
             tc_fence_after();
 #pragma unroll 3
             for (uint32_t piece = 0; piece < 9 && ok; ++piece) {
-              ok = wait(&sh.full[slot], turn);
+              if (!here) ok = wait(&sh.full[slot], turn);
               if (!ok) break;
 #pragma unroll
               for (uint32_t k = 0; k < 4; ++k)
                 pair_mma_bf16(tmem + buf * (2 * kC), k_tile + piece * (kPieceBytes >> 4) + 2 * k,
                               q_ring + slot * (kSlotBytes >> 4) + 2 * k, kDesc, piece + k > 0);
-              pair_commit(&sh.empty[slot], 3);
+              if (!keep) pair_commit(&sh.empty[slot], 3);
               if (++slot == kSlots) {
                 slot = 0;
-                turn ^= 1;
+                turn ^= !here;
               }
             }
             if (ok) pair_commit(&sh.s_full[buf], 3);
@@ -379,18 +411,25 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           if (ok) pair_commit(&sh.k_empty, 3);
         }
         ok = __all_sync(0xffffffffu, ok);
-        n += 9 * tiles;
+        n += 9 * (tiles - again);
         t += tiles;
         ++jobs;
         return ok;
       });
+      if (S::kKeep && kept.seq != UINT32_MAX && ok && elect_one())
+        for (uint32_t i = 0; i < kSlots; ++i) pair_commit(&sh.empty[i], 3);
+    }
   } else {
-    // positions: piece `piece` of each 128 latent bytes of rows slot and slot + 64
-    const uint32_t piece = ((lane >> 3) & 1) * 4 + (lane & 3), group = warp / 4;
-    const uint32_t slot = warp * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1), region = group % kRegions;
+    // positions: piece `piece` of each 128 latent bytes of rows slot and slot + 64.
+    // Eight lanes take a row's eight pieces (all banks once), and the upper four
+    // store their second 16 bytes first: those of the lower four and of the upper
+    // four go to the same banks, whose even 16 bytes then meet odd ones.
+    const uint32_t piece = lane & 7, group = warp / 4;
+    const uint32_t slot = warp * 4 + (lane >> 3), region = group % kRegions;
+    const bool upper = piece >= 4;
     const uint32_t from = stage + region * S::kRegionBytes + slot % 16 * KVO_ROW_BYTES;
-    const uint32_t to_lo = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3));
-    const uint32_t to_hi = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + 1);
+    const uint32_t to_lo = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + upper);
+    const uint32_t to_hi = keys + (piece >> 2) * kPieceBytes + swizzled(slot, 2 * (piece & 3) + !upper);
     const uint32_t to_rope = keys + 8 * kPieceBytes + swizzled(slot, piece);
     // scores: position quad * 32 + lane against the columns quarter * kMine + c of a tile
     const uint32_t quad = warp & 3, quarter = warp >> 2;
@@ -408,10 +447,28 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     auto add_tile = [&](uint32_t mine) -> bool {
       const uint32_t buf = t % kAhead;
       if (lse == -INFINITY) seen = 0;                      // a column that weighs nothing
-      if (lane < kMine) {
-        sh.lse[warp][lane] = seen ? lse * kLog2e : 0.0f;
-        sh.seen[warp][lane] = seen;
+      const float lse2 = seen ? lse * kLog2e : 0.0f;
+      if constexpr (kMine > 16) {
+        if (lane < kMine) {
+          sc.lse[warp][lane] = lse2;
+          sc.seen[warp][lane] = seen;
+        }
       }
+      // four columns' values, from c on
+      auto lses = [&](uint32_t c) -> float4 {
+        if constexpr (kMine > 16)
+          return *reinterpret_cast<const float4*>(&sc.lse[warp][c]);
+        else
+          return make_float4(__shfl_sync(~0u, lse2, c), __shfl_sync(~0u, lse2, c + 1), __shfl_sync(~0u, lse2, c + 2),
+                             __shfl_sync(~0u, lse2, c + 3));
+      };
+      auto sees = [&](uint32_t c) -> int4 {
+        if constexpr (kMine > 16)
+          return *reinterpret_cast<const int4*>(&sc.seen[warp][c]);
+        else
+          return make_int4(__shfl_sync(~0u, seen, c), __shfl_sync(~0u, seen, c + 1), __shfl_sync(~0u, seen, c + 2),
+                           __shfl_sync(~0u, seen, c + 3));
+      };
       const bool edge = __any_sync(0xffffffffu, seen <= (int32_t)(mine | 31));
       __syncwarp();
       ok = wait(&sh.s_full[buf], t / kAhead & 1);
@@ -430,13 +487,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
 #pragma unroll
         for (uint32_t c = 0; c < 16; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(&sh.lse[warp][c0 + c]);
+          const float4 l = lses(c0 + c);
           fma_two(x[c], x[c + 1], a.scale, -l.x, -l.y);
           fma_two(x[c + 2], x[c + 3], a.scale, -l.z, -l.w);
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) x[c + e] = exp2_approx(x[c + e]);
           if (edge) {
-            const int4 see = *reinterpret_cast<const int4*>(&sh.seen[warp][c0 + c]);
+            const int4 see = sees(c0 + c);
             x[c] = (int32_t)mine < see.x ? x[c] : 0.0f;
             x[c + 1] = (int32_t)mine < see.y ? x[c + 1] : 0.0f;
             x[c + 2] = (int32_t)mine < see.z ? x[c + 2] : 0.0f;
@@ -490,7 +547,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       };
       float next_lse, next_carried = 0.0f;
       int32_t next_seen;
-      column(job.begin, &next_lse, &next_seen);
+      if (last.seq == job.seq && last.begin < last.end && last.end - 1 == job.begin) {
+        next_lse = lse;                                    // the same columns again
+        next_seen = seen;
+      } else {
+        column(job.begin, &next_lse, &next_seen);
+      }
       if (quarter == 0 && a.carry && mine < run.len) next_carried = a.carry[job.seq * a.carry_ld + mine];
 
 #pragma unroll
@@ -505,16 +567,16 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         loads_are_in(all);
         if (!__all_sync(0xffffffffu, ok)) return false;  // (then the next rows must not come)
         if (lane == 0) mbar_arrive(&sh.raw_empty[region]);
-        const uint32_t pick = piece >= 4 ? 0x7632u : 0x5410u;
+        const uint32_t pick = upper ? 0x7632u : 0x5410u;
         const uint32_t scales[2] = {__byte_perm(eight.x, eight.y, pick), __byte_perm(eight.z, eight.w, pick)};
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k) {
           const uint16_t scale = (uint16_t)(scales[k >> 1] >> (k & 1) * 16);
           const float bias = -1152.0f * __half2float(__ushort_as_half(scale));
-          dequant4(lat[k].x, scale, bias, lo[k].x, lo[k].y);
-          dequant4(lat[k].y, scale, bias, lo[k].z, lo[k].w);
-          dequant4(lat[k].z, scale, bias, up[k].x, up[k].y);
-          dequant4(lat[k].w, scale, bias, up[k].z, up[k].w);
+          dequant4(upper ? lat[k].z : lat[k].x, scale, bias, lo[k].x, lo[k].y);
+          dequant4(upper ? lat[k].w : lat[k].y, scale, bias, lo[k].z, lo[k].w);
+          dequant4(upper ? lat[k].x : lat[k].z, scale, bias, up[k].x, up[k].y);
+          dequant4(upper ? lat[k].y : lat[k].w, scale, bias, up[k].z, up[k].w);
         }
         if (h == 0 && jobs) ok = wait(&sh.k_empty, (jobs - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;

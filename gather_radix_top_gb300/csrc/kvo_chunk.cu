@@ -103,13 +103,15 @@ struct ChunkArgs {
 // ---------------------------------------------------------------- the shares
 // Cluster g's share of the work: [from(g), from(g + 1)).
 struct Shares {
-  uint64_t units;
-  uint32_t clusters;
+  uint64_t units, each;
+  uint32_t clusters, rest;           // the first `rest` shares have one more than `each`
   __device__ __forceinline__ Shares(const ChunkArgs& a) {
     units = __ldcg(&a.plan[a.most_tiles + 1].units);
     clusters = (uint32_t)min((uint64_t)a.clusters, max(units / 2, (uint64_t)1));
+    each = units / clusters;
+    rest = (uint32_t)(units - each * clusters);
   }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * units / clusters : units; }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * each + min(g, rest) : units; }
 };
 
 // The tile that unit u lies in; a whole warp.

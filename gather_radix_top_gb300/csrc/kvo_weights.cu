@@ -159,13 +159,15 @@ __device__ __forceinline__ uint64_t for_work(const WeightArgs& a, F f) {
 }
 
 struct Shares {
-  uint64_t work;
-  uint32_t pairs;
+  uint64_t work, each;
+  uint32_t pairs, rest;              // the first `rest` shares have one more than `each`
   __device__ __forceinline__ Shares(const WeightArgs& a) {
     work = for_work(a, [](uint32_t, uint64_t, uint64_t) { return true; });
     pairs = (uint32_t)min((uint64_t)a.pairs, max(work / (kTileCost + 1), (uint64_t)1));
+    each = work / pairs;
+    rest = (uint32_t)(work - each * pairs);
   }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * work / pairs : work; }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * each + min(g, rest) : work; }
 };
 
 // f(job, run) for every job of the pair's share [lo, hi), in order, in every warp.

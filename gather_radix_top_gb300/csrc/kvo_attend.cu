@@ -156,6 +156,9 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, float* v) {
 // kChunk: the columns are not the heads of one query but (token, head) pairs
 // of a chunk, the heads of a token next to each other, and see unequal numbers
 // of positions, the last column the most of them.
+// Rows are dequantised once for as many columns as a CTA has, where kvo_attend
+// would do it for every token: 16 sequences of 8,192 rows with 4 tokens of 16
+// heads 52 us (floor 13: the bytes), one token over 61 rows 8 us.
 template <uint32_t kHeads, bool kChunk>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttendShape<kHeads>;

@@ -1,9 +1,13 @@
-// kvo_attend_chunk: causal attention of prompt chunks over a paged cache.
+// kvo_attend_chunk: causal attention of prompt chunks over a paged cache.  With
+// the columns c = (token, head) of a sequence and its positions p:
+//     z_pc = scale * k_p . q_c,   out_c = sum_p exp(z_pc - lse_c) v_p,
+//     lse_c = log sum_p exp(z_pc),  over the positions that c's token sees.
 //
-// Chunks with few columns ((token, head) pairs) go through the kernel of
-// kvo_attend, which dequantises rows for 64 columns at a time.  With many, the
-// rows are first unpacked to bf16 in the caller's scratch, once, and two CTAs
-// of a cluster work on 128 columns and 256 positions at a time:
+// Chunks with few columns go through the kernel of kvo_attend, which
+// dequantises rows for 64 columns at a time.  With many, the rows are first
+// unpacked to bf16 in the caller's scratch, once, and clusters of four CTAs take
+// 256 columns and 256 positions at a time.  Two CTAs are a pair, for 128 of the
+// columns:
 //     S^T [256 positions x 128 columns]      = K [256 x 576] Q^T
 //     O^T [512 values x 128 columns]        += V^T [512 x 256] P^T
 // as pair MMAs with M = 256: a CTA holds 128 of the positions for the first
@@ -12,21 +16,37 @@
 // is halved between them: 64 columns of queries (72 KB) and of weights (32 KB
 // for 256 positions) lie in each CTA's shared memory; the positions' operands
 // stream through a ring of six pieces of 16 KB (128 positions of 64 values
-// for the first product, 64 positions of 128 values for the second).
+// for the first product, 64 positions of 128 values for the second), which
+// both pairs share: each CTA brings half of a piece, for itself and for the CTA
+// of its rank in the other pair (multicast; half the traffic from L2).
 //
 // Sixteen worker warps do the softmax: a lane of S^T is a position.  The
 // weights of the other CTA's 64 columns go to it as one bulk copy (16 KB);
 // stored there directly they took 3,700 clocks a tile, most of them in the
-// fence before the MMAs.
+// fence before the MMAs.  Maxima and sums go the same way.
 // The softmax's reference is the column's maximum in the first tile of
-// positions.  Weights of up to 2^64 lose nothing in fp32 and bf16; where a
-// later logit lies further above, or the first tile shows a column nothing and
-// a later one does, the tile is done again at the end, with the true maximum
-// from a pass over its logits.  So no tile waits for a maximum.
+// positions and 2^32 above it.  Weights within 2^+-64 of it lose nothing in
+// fp32 and bf16; where a later logit lies further above, or the first tile shows
+// a column nothing and a later one does, the tile is done again at the end,
+// with the true maximum from a pass over its logits.  So no tile waits for a
+// maximum.
 //
 // Tiles of columns times tiles of positions, end to end, are shared out evenly
-// over the pairs.  Where a share begins or ends inside a tile of columns, the
-// parts are joined by their log-sum-exps in a second launch.
+// over the clusters.  Where a share begins or ends inside a tile of columns, the
+// parts are joined by their log-sum-exps in a last launch.
+//
+// Measured: 512 tokens of 64 heads over 50,023 positions 2.36-2.42 ms (1.47-1.51
+// PFLOP/s, 0.76-0.78 of cuBLAS's short-run bf16 rate), 2,048 over 16,384
+// 5.73-5.88 ms, a prompt of 4,096 tokens and 16 heads alone 257 us (half of its
+// tiles are masked in part).  A tile of 256 positions takes 4,608 clocks of MMAs
+// and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
+// MMAs' operands, 2,180 of the copies, 900 of the workers.  That is the bound.
+// Steps, ms for the first case: rows dequantised for 64 columns at a time 7.17,
+// pairs 3.80, copies instead of stores to the other CTA 3.27, two pairs a ring
+// 3.08, three loading warps 2.60, no order over the cluster in the workers' loop
+// 2.45; and us for the last: 650, two pairs a ring 401, sixteen columns at a time
+// 362, maxima and sums as copies 320, a loop for each role 298, no rows unpacked
+// where they do not pay and cheaper joins 257.
 #include <algorithm>
 
 #include "kvo_cache.cuh"
@@ -1035,9 +1055,10 @@ __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __
 // Whether unpacking the rows pays.  Per 1,000 rows of a sequence the kernel for
 // few columns takes about 0.29 us for every 64 columns, this one 0.36 us for
 // every 256 and 0.40 us to unpack them, and about 20 us more a call.  Both
-// ways, us: 16 sequences of 8,192 rows with 128 columns each 89 and 131, with
-// 256 165 and 134; one of 50,000 rows with 256 64 and 70, with 512 110 and 86;
-// 1,024 columns over 4,000 rows 31 and 40, over 50,000 216 and 121.
+// ways, us: 16 sequences of 8,192 rows with 128 columns each 91 and 131, with
+// 256 168 and 134; 64 of 4,096 with 256 323 and 239; one of 50,000 rows with 256
+// 66 and 70, with 512 112 and 86; 1,024 columns over 4,000 rows 31 and 41, over
+// 50,000 220 and 121; 4,096 over 2,000 52 and 48.
 bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;

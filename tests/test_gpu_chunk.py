@@ -887,3 +887,119 @@ def test_long_chunk_waits_that_run_out(kvo, counts, lens, heads):
                 assert torch.equal(a, b), clocks
         assert c.sync() == kvo.KVO_OK
     c.close()
+
+
+def test_long_chunk_on_two_streams_and_replayed(kvo, ctx):
+    """The same bits from two calls at once, and from two graphs at once on new inputs."""
+    rng = np.random.default_rng(111)
+    both = [Long(kvo, rng, [90, 40], [700, 300], 64), Long(kvo, rng, [33] * 5, [900, 33, 500, 64, 257], 20)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def run(c):
+        out, lse = c.attend(ctx)
+        return out, lse, c.weights(ctx, lse)
+
+    want = [[t.clone() for t in run(c)] for c in both]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for c, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                got.append(run(c))
+        torch.cuda.synchronize()
+        for a, b in zip(want[0] + want[1], got[0] + got[1]):
+            assert torch.equal(a, b)
+    graphs = []
+    for c in both:
+        cache = c.cache
+        out, lse = c.attend(ctx)                               # (the wide table is made outside the graph)
+        blocks = -(-60_000 // c.br)
+        table = torch.full((c.n, blocks), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = dev(c.table)
+        wide = kvo.Cache(rows=dev(c.raw), block_rows=c.br, table=table)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, l = ctx.attend_chunk(wide, c.q, c.dev_starts, c.dev_lens, c.scale, 60_000)
+            w = ctx.attention_weights(cache, c.q, c.dev_starts, c.dev_lens, l, c.scale, c.rows)
+        graphs.append((g, (o, l, w), wide))
+    for c in both:
+        c.q.copy_(c.q.roll(1, 0))
+    want = [[t.clone() for t in run(c)] for c in both]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, got, _), w in zip(graphs, want):
+            for a, b in zip(got, w):
+                assert torch.equal(a, b)
+    assert ctx.sync() == kvo.KVO_OK
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 1.5])
+@pytest.mark.parametrize("kind", [Chunk, Long])
+def test_chunk_scales(kvo, ctx, kind, scale):
+    rng = np.random.default_rng([112, int(scale * 100) + 10])
+    c = kind(kvo, rng, [40, 12], [300, 150], 20, scale=scale, gain=0.2)
+    out, lse = c.attend(ctx)
+    weights = c.weights(ctx, lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    c.check_weights(weights, lse)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_tokens_of_no_sequence(kvo, ctx, heads):
+    """Every sequence empty, tokens all the same: nothing is written for them, and carried weights stay."""
+    rng = np.random.default_rng([113, heads])
+    for kind in (Chunk, Long):
+        c = kind(kvo, rng, [0, 0, 0], [50, 0, 700], heads, after=40)
+        out = torch.full((40, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((40, heads), 7.0, device="cuda")
+        c.attend(ctx, out=out, lse=lse)
+        assert (out == 7).all() and (lse == 7).all()
+        carry = dev(rng.exponential(1.0, (3, 700)), torch.float32)
+        got = c.weights(ctx, lse, carry=carry, keep=2.0)
+        assert ctx.sync() == kvo.KVO_OK
+        for s, n in enumerate(c.lens):
+            assert torch.equal(got[s, :n], 2 * carry[s, :n]) and not got[s, n:].any()
+
+
+def test_rows_far_into_a_cache(kvo, ctx):
+    """Rows past 2^32 bytes, of both caches, and queries past 2^31 elements."""
+    rng = np.random.default_rng(114)
+    far = 6_600_000 // 16                                       # blocks; times 16 * 656 bytes
+    kinds = [Chunk(kvo, rng, [5, 3], [200, 90], 20), Long(kvo, rng, [50], [700], 64)]
+    store = torch.zeros((far + 200) * 16, 656, dtype=torch.uint8, device="cuda")
+    for c in kinds:
+        want = c.attend(ctx)
+        sums = c.weights(ctx, want[1])
+        store[far * 16:far * 16 + len(c.raw)] = dev(c.raw)
+        table = np.full((c.n, 60_000 // 16), -1, np.int32)
+        table[:, :c.table.shape[1]] = c.table + far
+        cache = kvo.Cache(rows=store, block_rows=16, table=dev(table))
+        rows = 60_000 if isinstance(c, Long) else c.rows
+        wide = torch.empty_strided((c.tokens, c.heads, 576), (2 ** 31 // c.tokens // 8 * 8 + 64, 576, 1),
+                                   dtype=torch.bfloat16, device="cuda")
+        wide.copy_(c.q)
+        for q in (c.q, wide):
+            out, lse = ctx.attend_chunk(cache, q, c.dev_starts, c.dev_lens, c.scale, rows)
+            got = ctx.attention_weights(cache, q, c.dev_starts, c.dev_lens, lse, c.scale, c.rows)
+            if q is c.q:
+                assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(got, sums)
+            c.check_attend(out, lse)
+            c.check_weights(got, lse)
+        budget = 40
+        to_table = dev(np.arange(c.n * 3, dtype=np.int32).reshape(c.n, 3) + far + 150)
+        to = kvo.Cache(rows=store, block_rows=16, table=to_table)
+        kept, lens, _ = ctx.shrink_cache(cache, to, sums, c.dev_lens, budget, first=1, last=2)
+        assert ctx.sync() == kvo.KVO_OK
+        for s in range(c.n):
+            stay = C.keep(sums[s].cpu().numpy(), c.lens[s], budget, 1, 2)
+            assert kept[s].tolist() == stay
+            at = [O.row_of(c.table, c.total, 16, c.n, s, p) for p in stay]
+            base = (far + 150 + 3 * s) * 16
+            assert np.array_equal(store[base:base + budget].cpu().numpy(), c.raw[at])
+        del wide
+        torch.cuda.empty_cache()

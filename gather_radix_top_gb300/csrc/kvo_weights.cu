@@ -360,33 +360,49 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     });
     if (some && __all_sync(0xffffffffu, ok)) bring();
   } else if (warp >= kQuery) {
-    // the queries' pieces: warp w takes every kQueries-th one
+    // the queries' pieces: warp w takes those of slots w, w + kQueries, ..  (A
+    // slot stays with its warp: a wait for a phase is only sound for whoever has
+    // seen the one before it.)
     const uint32_t w = warp - kQuery, full0 = dsmem_addr(&sh.full[0], 0);
-    uint32_t at = 0;                                     // the job's first piece
+    static_assert(kQueries == 2 && (kSlots % kQueries == 0 || kSlots == 9), "warp w has every other slot");
+    uint32_t at = 0;                                     // the tile's first piece
+    uint32_t mine = w, slot = w, lap = 0;                // the warp's next one, its slot, and how often that was used
     Kept kept;
     for_jobs(a, pair, lo, hi, [&](const Job& job, const Run& run) {
       if (job.end <= job.begin) return true;
-      const uint32_t begin = job.begin + (S::kKeep && kept.has(job)), pieces = 9 * (job.end - begin);
+      const uint32_t begin = job.begin + (S::kKeep && kept.has(job));
       kept.set(job);
       if (lane == 0) {
-        for (uint32_t k = (w + at) % kQueries; k < pieces; k += kQueries) {
-          const uint32_t tile = begin + k / 9, piece = k % 9, slot = (at + k) % kSlots;
-          const uint32_t half = 2 * tile + rank, row = half / cols.across, head = half % cols.across * cols.wide;
-          if (at + k >= kSlots) ok = wait(&sh.empty[slot], ((at + k) / kSlots - 1) & 1);
-          if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
-          pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)(piece * 64), (int32_t)head,
-                        (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep), full0 + slot * 8);
-          n = at + k + 1;
+        for (uint32_t tile = begin; tile < job.end && ok; ++tile, at += 9) {
+          const uint32_t half = 2 * tile + rank, row = half / cols.across;
+          const int32_t y = (int32_t)((half - row * cols.across) * cols.wide);
+          const int32_t z = (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep);
+          if (kSlots == 9 && at) {
+            mine = at + w;
+            slot = w;
+            lap = at / 9;
+          }
+          for (; mine < at + 9; mine += kQueries) {
+            if (lap) ok = wait(&sh.empty[slot], (lap - 1) & 1);
+            if (!ok) break;
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
+            pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)((mine - at) * 64), y, z, full0 + slot * 8);
+            n = mine + 1;
+            slot += kQueries;
+            if (slot >= kSlots) {
+              slot -= kSlots;
+              ++lap;
+            }
+          }
         }
       }
-      at += pieces;
       return (bool)__shfl_sync(0xffffffffu, ok, 0);
     });
     if (lane == 0) {
       if (ok) n = at;
       // no slot's release may still be on its way when the CTA ends
-      for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
+      for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m)
+        if (m % kSlots % kQueries == w) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
       dsmem_st_u32(dsmem_addr(&sh.issued[rank][w], 0), n);
     }
   } else if (warp == kMma) {
@@ -656,13 +672,15 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         least = min(least, sh.issued[i / kQueries][i % kQueries]);
       }
       for (uint32_t m = least; m < most; ++m) {
-        const bool here = m < sh.issued[0][m % kQueries], there = m < sh.issued[1][m % kQueries];
+        const uint32_t owner = m % kSlots % kQueries;
+        const bool here = m < sh.issued[0][owner], there = m < sh.issued[1][owner];
         if (here == there) continue;
         if (!here) mbar_arrive_expect_tx(&sh.full[m % kSlots], 2 * box);
         mbar_complete_tx(&sh.full[m % kSlots], box);
       }
       for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m) {
-        if (m >= sh.issued[0][m % kQueries] && m >= sh.issued[1][m % kQueries]) continue;
+        const uint32_t owner = m % kSlots % kQueries;
+        if (m >= sh.issued[0][owner] && m >= sh.issued[1][owner]) continue;
         if (!landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
       }
     }

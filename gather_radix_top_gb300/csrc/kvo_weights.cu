@@ -21,11 +21,12 @@
 // over the pairs.  Where a share begins or ends inside a tile of positions, a
 // second launch adds the parts in their order.
 //
-// Measured: 32 tokens of 64 heads over 50,023 positions 93 us (1.27 PFLOP/s):
-// a tile of 128 columns takes 2,700 to 2,850 clocks, of which its 36 MMAs need
-// 2,304, and between two tiles of positions the tensor core waits 7,500 (the
-// second half of the rows is converted behind the last MMA).  301 uneven tokens
-// of 20 heads in 7 sequences 86 us.
+// Measured: 32 tokens of 64 heads over 50,023 positions 84 us (1.41 PFLOP/s; 90
+// us in a row of eager calls): a tile of 128 columns takes 2,650 clocks, of which
+// its 36 MMAs need 2,304, and between two tiles of positions the tensor core
+// waits 7,500 (the second half of the rows is converted behind the last MMA).
+// The ring of queries matters most: with four slots, and room for four groups
+// of rows, it takes 92 us.  301 uneven tokens of 20 heads in 7 sequences 77 us.
 // A token of 64 heads in each of 64 sequences of 16,384 positions 215 us (3.3
 // TB/s).  There a tile's rows are one chain: 42 KB of raw rows are all that fits
 // beside the dequantised ones, so that memory is idle while they are converted,
@@ -753,7 +754,10 @@ cudaError_t launch_weights(const WeightArgs& a, const CUtensorMap& map, cudaStre
   lc.attrs = attr;
   lc.numAttrs = 2;
   e = cudaLaunchKernelEx(&lc, weights_kernel<kC>, a, map);
-  if (e != cudaSuccess || a.pairs < 2) return e;
+  // no share ends inside a tile of positions that meets one tile of columns
+  const Columns& c = a.columns;
+  const uint32_t units = c.flat ? a.tokens * a.heads : a.tokens, most = ((units + c.deep - 1) / c.deep * c.across + 1) / 2;
+  if (e != cudaSuccess || a.pairs < 2 || most < 2) return e;
   return launch_early(add_parts_kernel, dim3(a.pairs - 1), kSpan, 0, stream, a);
 }
 
@@ -815,9 +819,9 @@ extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache
   if (a.window && a.window < each) each = a.window;
   // Tiles of 64 or of 128 columns, by the columns of a sequence when all have the
   // same.  Both ways, us: 64 columns, 64 sequences of 16,384 positions 212 and
-  // 347, one of 50,000 24 and 29; 16 columns, 64 of 2,048 51 and 66; 128 columns,
-  // 64 of 2,048 62 and 66, 16 of 4,096 37 and 34, one of 50,000 30 and 28; 256
-  // columns, 8 of 8,192 44 and 42.
+  // 347, one of 50,000 24 and 29 (with the second launch); 16 columns, 64 of 2,048
+  // 51 and 66; 128 columns, 64 of 2,048 62 and 66, 16 of 4,096 37 and 34, one of
+  // 50,000 30 and 28; 256 columns, 8 of 8,192 44 and 42.
   const bool few = each * a.heads <= 64;
   a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens, few ? 32 : 64);
   const cudaStream_t on = static_cast<cudaStream_t>(stream);

@@ -35,15 +35,16 @@
 // (720), the raw rows (820) and the queries share.  The softmax (about 1,450
 // from scores to weights) and the hand-overs are the rest: with one tile in
 // shared memory nothing else of the tensor cores' work can run beside it.
-//     1,048,576 rows of one query with 128 heads                480 us, 608 TFLOP/s
-//     64 queries of 64 heads, each with 2,048 listed positions   50.6 us, 1.9 TB/s
-//     2,048 rows of one query with 64 heads                      9.8 us
+//     1,048,576 rows of one query with 128 heads                485 us, 602 TFLOP/s
+//     64 queries of 64 heads, each with 2,048 listed positions   51.3 us, 1.9 TB/s
+//     2,048 rows of one query with 64 heads                      9.9 us
 // Measured on the way, the first of them in us: rows through registers 942
 // (next to this much shared memory the SM keeps about 28 KB of loads in
 // flight), eight worker warps and one loading warp 672, three loading warps
 // 647, references that move seldom and MMAs issued by one elected lane of a
 // converged warp 525 (by a divergent thread 664), two parts instead of five
-// 501, multiply-adds on fp16 operands in the dequantisation 491.
+// 501, multiply-adds on fp16 operands in the dequantisation 491.  (A tile's rows
+// are awaited in registers before the next ones may come: 482 without.)
 #include <type_traits>
 
 #include "kvo_cache.cuh"

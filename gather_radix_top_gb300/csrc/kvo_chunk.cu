@@ -39,8 +39,8 @@
 // 0.82 of cuBLAS's short-run bf16 rate; 2.37-2.42 ms back to back, at the power
 // limit), 2,048 of 128 heads over 16,384 5.5-5.8 ms, a prompt of 4,096 tokens and
 // 16 heads alone 255 us (its tiles of columns meet 8.5 tiles of positions on
-// average, and beginning and ending one takes the time of two).  A tile of 256 positions takes 4,608 clocks of MMAs
-// and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
+// average, and beginning and ending one takes the time of two).  A tile of 256
+// positions takes 4,608 clocks of MMAs and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
 // MMAs' operands, 2,180 of the copies, 900 of the workers.  That is the bound.
 // Steps, ms for the first case: rows dequantised for 64 columns at a time 7.17,
 // pairs 3.80, copies instead of stores to the other CTA 3.27, two pairs a ring

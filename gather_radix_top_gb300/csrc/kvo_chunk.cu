@@ -40,14 +40,15 @@
 // limit), 2,048 of 128 heads over 16,384 5.5-5.8 ms, a prompt of 4,096 tokens and
 // 16 heads alone 255 us (its tiles of columns meet 8.5 tiles of positions on
 // average, and beginning and ending one takes the time of two).  A tile of 256
-// positions takes 4,608 clocks of MMAs and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
-// MMAs' operands, 2,180 of the copies, 900 of the workers.  That is the bound.
+// positions takes 4,608 clocks of MMAs and keeps shared memory busy for 6,300
+// wavefronts of 128 bytes: 3,250 of the MMAs' operands, 2,180 of the copies, 900
+// of the workers.  That is the bound.
 // Steps, ms for the first case: rows dequantised for 64 columns at a time 7.17,
 // pairs 3.80, copies instead of stores to the other CTA 3.27, two pairs a ring
 // 3.08, three loading warps 2.60, no order over the cluster in the workers' loop
 // 2.45; and us for the last: 650, two pairs a ring 401, sixteen columns at a time
-// 362, maxima and sums as copies 320, a loop for each role 298, and
-// unpacking, plan and join in parallel 255.
+// 362, maxima and sums as copies 320, a loop for each role 298, and unpacking,
+// plan and join in parallel 255.
 #include <algorithm>
 
 #include "kvo_cache.cuh"

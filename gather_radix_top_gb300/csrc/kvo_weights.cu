@@ -365,7 +365,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // slot stays with its warp: a wait for a phase is only sound for whoever has
     // seen the one before it.)
     const uint32_t w = warp - kQuery, full0 = dsmem_addr(&sh.full[0], 0);
-    static_assert(kQueries == 2 && (kSlots % kQueries == 0 || kSlots == 9), "warp w has every other slot");
     uint32_t at = 0;                                     // the tile's first piece
     uint32_t mine = w, slot = w, lap = 0;                // the warp's next one, its slot, and how often that was used
     Kept kept;
@@ -378,21 +377,17 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const uint32_t half = 2 * tile + rank, row = half / cols.across;
           const int32_t y = (int32_t)((half - row * cols.across) * cols.wide);
           const int32_t z = (int32_t)((cols.flat ? run.first * a.heads : run.first) + row * cols.deep);
-          if (kSlots == 9 && at) {
-            mine = at + w;
-            slot = w;
-            lap = at / 9;
-          }
-          for (; mine < at + 9; mine += kQueries) {
+          while (mine < at + 9) {
             if (lap) ok = wait(&sh.empty[slot], (lap - 1) & 1);
             if (!ok) break;
             if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * box);
             pair_load_box(ring + slot * kSlotBytes, &qmap, (int32_t)((mine - at) * 64), y, z, full0 + slot * 8);
             n = mine + 1;
+            mine += kQueries;
             slot += kQueries;
             if (slot >= kSlots) {
-              slot -= kSlots;
-              ++lap;
+              slot = w;
+              mine = ++lap * kSlots + w;
             }
           }
         }
@@ -571,10 +566,15 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         *to_lse = 0.0f;
         *to_seen = 0;
         if (tile >= job.end || deep >= cols.deep) return;
-        const uint32_t half = 2 * tile + quarter / 2, row = half / cols.across * cols.deep + deep;
-        const uint32_t head = half % cols.across * cols.wide + wide;
-        const uint32_t at = cols.flat ? row : row * a.heads + head, token = divide(at, a.by_heads);
-        if (token < run.from || token >= run.tokens || (!cols.flat && head >= a.heads)) return;
+        const uint32_t half = 2 * tile + quarter / 2;
+        uint32_t at = half * cols.deep + deep;
+        if (!cols.flat) {
+          const uint32_t row = half / cols.across, head = (half - row * cols.across) * cols.wide + wide;
+          if (head >= a.heads) return;
+          at = (row * cols.deep + deep) * a.heads + head;
+        }
+        const uint32_t token = divide(at, a.by_heads);
+        if (token < run.from || token >= run.tokens) return;
         *to_lse = __ldg(a.lse + (int64_t)run.first * a.heads + at);   // (looked at when its tile is)
         *to_seen = min(run.before + (int32_t)token, (int32_t)run.len);
       };

@@ -10,11 +10,11 @@
 //
 // Measured on the GPU: 50,023 positions to 8,192 rows 13.5 us (the selection's
 // chain of passes and cluster barriers; the copy 4), 33 uneven sequences of up
-// to 20,011 to 1,021 23 us, 1,048,576 to 524,288 235 us: 147 for the copy (826
+// to 20,011 to 1,021 23 us, 1,048,576 to 524,288 229 us: 147 for the copy (826
 // MB at 5.6 TB/s; every second row of 656 bytes leaves parts of DRAM's bursts
-// unused) and 90 for the selection, whose 16 CTAs issue 2.0 instructions a clock
+// unused) and 80 for the selection, whose 16 CTAs issue two instructions a clock
 // in loops over the keys.  With weights read again in every pass, one at a time,
-// it took 270 us.
+// it took 270 us, with another pass for what lies above the cut 239.
 #include <algorithm>
 
 #include "kvo_cache.cuh"
@@ -25,7 +25,7 @@ namespace {
 
 using namespace topk_detail;
 
-constexpr uint32_t kKeepStatic = 8 * 1024, kKeepSmem = 227 * 1024 - kKeepStatic;
+constexpr uint32_t kKeepStatic = 18 * 1024, kKeepSmem = 227 * 1024 - kKeepStatic;
 
 struct ShrinkArgs {
   CacheView from, to;
@@ -41,12 +41,85 @@ struct ShrinkArgs {
   uint32_t held;             // keys that a CTA has room for, in fours
 };
 
+// kDigit: bits of a pass of the radix select.
+template <uint32_t kDigit>
+struct KeepSmem {
+  static constexpr uint32_t kBins = 1u << kDigit, kPasses = (32 + kDigit - 1) / kDigit;
+  static constexpr uint32_t kAll = kBins > (uint32_t)kThreads ? kBins : kThreads;
+  uint32_t hist[kBins];              // this CTA's, of the current digit
+  uint32_t all[kAll];                // the cluster's, and zeros
+  uint32_t warp_sum[kWarps], cut[4];
+  // Every CTA owns an even share of each pass's bins: this many words.
+  __host__ __device__ static constexpr uint32_t owned(uint32_t C) { return kPasses * (kBins / C); }
+};
+
+// The n largest of the cluster's keys, ties to the lower position: a radix
+// select, whose histograms also tell each CTA how many of its own keys lie
+// above the cut and at it, then the ordered compaction.  So the keys are gone
+// over once a digit and once more at most.  owned: the passes' bins, zeroed
+// before a cluster barrier that precedes this call.
+template <uint32_t kDigit, typename Key4, typename Emit>
+__device__ __forceinline__ void keep_largest(Key4 key4, uint32_t count, uint32_t n, KeepSmem<kDigit>* sm, uint32_t* owned,
+                                             uint32_t (*scratch)[2 * kWarps + 2], uint32_t (*table)[4], Emit emit) {
+  const uint32_t tid = threadIdx.x, C = cluster_size(), r = cluster_rank(), per = KeepSmem<kDigit>::kBins / C;
+  const uint32_t ngroups = (count + 3) / 4;
+  uint32_t prefix = 0, mask = 0, remaining = n, shift = 32, mine[2] = {0, 0};
+  for (uint32_t pass = 0;; ++pass) {
+    const uint32_t d = min(shift, kDigit), dmask = (1u << d) - 1;
+    shift -= d;
+    for (uint32_t b = tid; b < KeepSmem<kDigit>::kBins; b += kThreads) sm->hist[b] = 0;
+    __syncthreads();
+    for (uint32_t g0 = 0; g0 < ngroups; g0 += kThreads) {
+      const uint32_t g = g0 + tid;
+      const uint4 k = g < ngroups ? key4(g) : make_uint4(0, 0, 0, 0);
+      const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+      uint32_t bins[4], valid = 0;
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) {
+        bins[e] = v[e] >> shift & dmask;
+        valid |= (uint32_t)(4 * g + e < count && (v[e] & mask) == prefix) << e;
+      }
+      hist_add_warp4(sm->hist, bins, valid);
+    }
+    __syncthreads();
+    for (uint32_t b = tid; b <= dmask; b += kThreads)
+      if (const uint32_t v = sm->hist[b]) dsmem_red_add_u32(dsmem_addr(&owned[pass * per + b % per], b / per), v);
+    cluster_sync();
+    for (uint32_t b = tid; b < KeepSmem<kDigit>::kAll; b += kThreads)
+      sm->all[b] = b <= dmask ? dsmem_ld_u32(dsmem_addr(&owned[pass * per + b % per], b / per)) : 0u;
+    __syncthreads();
+    find_cut<KeepSmem<kDigit>::kAll / kThreads>(sm->all, remaining, sm->warp_sum, sm->cut);
+    const uint32_t bucket = sm->cut[0], inside = sm->cut[2];
+    remaining -= sm->cut[1];
+    prefix |= bucket << shift;
+    mask |= dmask << shift;
+    const bool done = remaining == inside || shift == 0;
+    for (uint32_t b = tid; b <= dmask; b += kThreads) {
+      mine[0] += b > bucket ? sm->hist[b] : 0u;
+      mine[1] += done && b == bucket ? sm->hist[b] : 0u;
+    }
+    if (done) break;
+    __syncthreads();                                     // before hist and cut change
+  }
+  uint32_t sums[2], before, at_before;
+  block_sum2(mine[0], mine[1], scratch[1], &sums[0], &sums[1]);
+  cluster_publish(sums, 2, table, r, C);
+  const RadixCut cut{prefix, shift, remaining};
+  cut_offsets(table, 0, r, cut.need, &before, &at_before);
+  cluster_compact(key4, count, cut, before, at_before, scratch, [&](uint32_t i, uint32_t out) {
+    if (out < n) emit(i, out);
+  });
+}
+
 // A CTA's keys stay in its shared memory, as far as they fit; the passes read
 // the weights of the others again.
+template <uint32_t kDigit>
 __global__ void __launch_bounds__(kThreads, 1) keep_kernel(const __grid_constant__ ShrinkArgs a) {
   extern __shared__ __align__(16) uint8_t dyn_smem[];
-  static_assert(sizeof(RadixSmem) + 4 * 2 * (2 * kWarps + 2) + 16 * kMaxCluster <= kKeepStatic);
-  __shared__ RadixSmem rsm;
+  using Smem = KeepSmem<kDigit>;
+  static_assert(Smem::kBins % kMaxCluster == 0 && Smem::owned(kMaxCluster) % 4 == 0);
+  static_assert(sizeof(Smem) + 4 * 2 * (2 * kWarps + 2) + 16 * kMaxCluster <= kKeepStatic);
+  __shared__ Smem sm;
   __shared__ uint32_t scratch[2][2 * kWarps + 2];
   __shared__ uint32_t table[kMaxCluster][4];
   wait_previous_grid();
@@ -90,14 +163,15 @@ __global__ void __launch_bounds__(kThreads, 1) keep_kernel(const __grid_constant
     kept[out] = (int32_t)(lo + i);
     if (to_w) to_w[out] = __ldg(w + lo + i);
   };
-  radix_smem_init(&rsm);
-  uint4* const keys = reinterpret_cast<uint4*>(dyn_smem);
+  uint32_t* const owned = reinterpret_cast<uint32_t*>(dyn_smem);
+  uint4* const keys = reinterpret_cast<uint4*>(owned + Smem::owned(C));
+  for (uint32_t b = tid; b < Smem::owned(C); b += kThreads) owned[b] = 0;
   const uint32_t held = min((count + 3) / 4, a.held);
   for_groups(four, held, [&](uint32_t g, uint4 v) {
     if (g < held) keys[g] = v;
   });
   cluster_sync();
-  select_and_emit([&](uint32_t g) { return g < held ? keys[g] : four(g); }, count, n, 32, &rsm, scratch, table, emit);
+  keep_largest([&](uint32_t g) { return g < held ? keys[g] : four(g); }, count, n, &sm, owned, scratch, table, emit);
 }
 
 constexpr uint32_t kMoveThreads = 256, kMoveRows = 4;    // rows of a warp
@@ -155,17 +229,28 @@ cudaError_t launch_keep(ShrinkArgs a, uint32_t sequences, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int& most = widest[dev & 63];
   if (!most) {
-    e = cudaFuncSetAttribute(keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeepSmem);
-    if (e != cudaSuccess) return e;
-    const int c = best_cluster((const void*)keep_kernel, kKeepSmem, (int)kMaxCluster);
-    if (c < 1) return cudaErrorInvalidConfiguration;
-    most = c;
+    int both = (int)kMaxCluster;
+    for (const void* kern : {(const void*)keep_kernel<8>, (const void*)keep_kernel<11>}) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeepSmem);
+      if (e != cudaSuccess) return e;
+      const int c = best_cluster(kern, kKeepSmem, (int)kMaxCluster);
+      if (c < 1) return cudaErrorInvalidConfiguration;
+      both = c < both ? c : both;
+    }
+    most = both;
   }
   // As many CTAs a sequence as the GPU has room for at once, but not so many
   // that one gets less than a tile of the compaction.
   uint32_t C = 1;
   while ((int)C < most && 2 * C * sequences <= (uint32_t)device_sms() && a.rows > C * 4u * kThreads) C *= 2;
-  a.held = std::min(topk_chunk(a.rows, C), kKeepSmem / 4) / 4;
+  // Three passes of 11 bits for many keys a CTA, four of 8 for few.  Both ways,
+  // us: one sequence of 50,000 13.9 and 13.3, 262,144 (16,384 a CTA) 21.1 and
+  // 22.2, 500,000 30.0 and 32.9; four of 262,144 24.7 and 23.0; 152 of 30,000 62
+  // and 64, of 200,000 193 and 200.
+  const uint32_t chunk = topk_chunk(a.rows, C);
+  const bool many = chunk > 24 * 1024;
+  const uint32_t bins = many ? KeepSmem<11>::owned(C) : KeepSmem<8>::owned(C);
+  a.held = std::min(chunk, kKeepSmem / 4 - bins) / 4;
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -176,11 +261,11 @@ cudaError_t launch_keep(ShrinkArgs a, uint32_t sequences, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.gridDim = dim3(C * sequences);
   lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = a.held * 16;
+  lc.dynamicSmemBytes = bins * 4 + a.held * 16;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  return cudaLaunchKernelEx(&lc, keep_kernel, a);
+  return cudaLaunchKernelEx(&lc, many ? keep_kernel<11> : keep_kernel<8>, a);
 }
 
 }  // namespace
@@ -224,9 +309,10 @@ extern "C" kvo_status kvo_shrink_cache(kvo_ctx* ctx, const kvo_cache* from, cons
   a.last = (uint32_t)s->last;
   a.key_pieces = !to->keys ? 0 : to->key_type == KVO_E4M3 ? 8 : 16;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_keep(a, (uint32_t)from->sequences, on);
+  const uint32_t sequences = (uint32_t)from->sequences;
+  cudaError_t e = launch_keep(a, sequences, on);
   if (e != cudaSuccess) return KVO_ECUDA;
   const uint32_t most = a.rows < a.budget ? a.rows : a.budget, per = kMoveThreads / 32 * kMoveRows;
-  e = launch_early(move_kernel, dim3((most + per - 1) / per, (unsigned)from->sequences), kMoveThreads, 0, on, a);
+  e = launch_early(move_kernel, dim3((most + per - 1) / per, sequences), kMoveThreads, 0, on, a);
   return e == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -1003,3 +1003,25 @@ def test_rows_far_into_a_cache(kvo, ctx):
             assert np.array_equal(store[base:base + budget].cpu().numpy(), c.raw[at])
         del wide
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["ties", "specials", "falling", "negative", "equal", "close"])
+@pytest.mark.parametrize("budget", [1, 1_000, 225_000, 449_999])
+def test_shrink_orders_of_many(kvo, ctx, kind, budget):
+    """Hundreds of thousands of weights, more than stay in shared memory, over a few blocks named again and again."""
+    rng = np.random.default_rng([115, len(kind), budget])
+    n = 450_000
+    w = {"ties": lambda: rng.integers(0, 5, n) * 0.25, "falling": lambda: -np.arange(n) * 0.5, "equal": lambda: np.full(n, 3.0),
+         "negative": lambda: -rng.exponential(1.0, n), "close": lambda: 1.0 + rng.integers(0, 700, n) * 2.0 ** -23,
+         "specials": lambda: rng.choice([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-42, -1e-42, 7.0, -7.0], n)}[kind]()
+    w = dev(w[None], torch.float32)
+    first, last = (0, 0) if budget < 100 else (3, 9)
+    raw = random_rows(rng, 64 * 16)
+    table = rng.integers(0, 64, (1, n // 16 + 1)).astype(np.int32)
+    cache = kvo.Cache(rows=dev(raw), block_rows=16, table=dev(table))
+    to = kvo.Cache(rows=torch.zeros(budget, 656, dtype=torch.uint8, device="cuda"), block_rows=budget)
+    kept, lens, got = ctx.shrink_cache(cache, to, w, dev([n], torch.int32), budget, first=first, last=last)
+    assert ctx.sync() == kvo.KVO_OK
+    stay = C.keep(w[0].cpu().numpy(), n, budget, first, last)
+    assert lens.tolist() == [budget] and kept[0].tolist() == stay
+    assert torch.equal(got[0].view(torch.int32), w[0, stay].view(torch.int32))

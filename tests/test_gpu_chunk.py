@@ -1025,3 +1025,24 @@ def test_shrink_orders_of_many(kvo, ctx, kind, budget):
     stay = C.keep(w[0].cpu().numpy(), n, budget, first, last)
     assert lens.tolist() == [budget] and kept[0].tolist() == stay
     assert torch.equal(got[0].view(torch.int32), w[0, stay].view(torch.int32))
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([1, 1, 1], [700, 33, 300], 40), ([1] * 5, [900] * 5, 64), ([2, 1], [400, 700], 30),
+                                               ([1, 3], [600, 500], 33), ([9, 1, 1], [300, 2000, 40], 12), ([1, 1], [3000, 9], 128)])
+def test_weights_of_few_columns_strided(kvo, ctx, counts, lens, heads):
+    """Few columns a sequence, heads apart from each other, in tiles that cut a token's heads."""
+    rng = np.random.default_rng([116, heads, len(counts)])
+    c = Chunk(kvo, rng, counts, lens, heads)
+    lse = c.lse()
+    want = c.weights(ctx, lse)
+    c.check_weights(want, lse)
+    wide = torch.full((c.tokens, 2 * heads, 592), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1::2, 8:584] = c.q
+    across = torch.empty(heads, c.tokens, 576, dtype=torch.bfloat16, device="cuda")
+    across.copy_(c.q.transpose(0, 1))
+    for q in (wide[:, 1::2, 8:584], across.transpose(0, 1)):
+        c.q = q
+        for window in (0, 1):
+            got = c.weights(ctx, lse, window=window)
+            assert ctx.sync() == kvo.KVO_OK
+            c.check_weights(got, lse, window)

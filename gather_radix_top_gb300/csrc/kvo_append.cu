@@ -18,6 +18,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "kvo_cache.cuh"
 
 namespace kvo {
@@ -33,6 +35,7 @@ struct AppendArgs {
   const uint8_t* key;
   const int32_t* seq;
   const int32_t* pos;
+  const int32_t* place;                 // or NULL: pos
   uint16_t* out_bf16;
   uint32_t* status;
   int64_t latent_ld, rope_ld, key_ld;   // elements
@@ -109,7 +112,9 @@ __device__ __forceinline__ float quantise(float x, float s, float inv) {
   return t;
 }
 
-template <typename T>
+// kPlaced: rows go to places of their own.  (Asked of every token instead, it
+// takes the 60,000 tokens from 40.0 to 40.4 us.)
+template <typename T, bool kPlaced>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) append_tokens_kernel(const __grid_constant__ AppendArgs a) {
   const uint32_t lane = threadIdx.x & 31;
   const int64_t i = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) appen
   // the token's values are asked for before its place is looked up, so that
   // the two chains of loads overlap
   const int32_t s = a.seq ? a.seq[i] : (int32_t)(i < INT32_MAX ? i : INT32_MAX);
-  const int32_t p = a.pos[i];
+  const int32_t p = a.pos[i], at = kPlaced ? a.place[i] : p;
   float x[16], k[4];
   load_floats<T, 16>(reinterpret_cast<const T*>(a.latent) + i * a.latent_ld + 16 * lane, x);
   const T* rope = reinterpret_cast<const T*>(a.rope) + i * a.rope_ld;
@@ -129,7 +134,8 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 10 : 1) appen
   if (a.key) load_floats<T, 4>(reinterpret_cast<const T*>(a.key) + i * a.key_ld + 4 * lane, k);
 
   if (s < 0) return;
-  const int64_t row = p >= 0 && (uint32_t)s < a.cache.sequences ? cache_row(a.cache, (uint32_t)s, (uint32_t)p) : -1;
+  const int64_t row =
+      p >= 0 && (!kPlaced || at >= 0) && (uint32_t)s < a.cache.sequences ? cache_row(a.cache, (uint32_t)s, (uint32_t)at) : -1;
   uint16_t* values = a.out_bf16 ? a.out_bf16 + i * KVO_DEQUANT_VALUES : nullptr;
   if (row < 0) {
     if (lane == 0) atomicOr(a.status, kFlagRange);
@@ -258,7 +264,8 @@ extern "C" kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, co
   for (int i = 0; i < 32; ++i)
     if (!(std::fabs(t->inv_freq[i]) <= kMaxInvFreq)) return KVO_EINVAL;
   if (t->key && !cache_keys_ok(cache)) return KVO_EINVAL;
-  if (!aligned(t->out_bf16, 16) || !aligned(t->seq, 4) || !aligned(t->pos, 4)) return KVO_EINVAL;
+  if (!aligned(t->out_bf16, 16) || !aligned(t->seq, 4) || !aligned(t->pos, 4) || !aligned(t->place, 4))
+    return KVO_EINVAL;
   if (t->n > 0) {
     if (!t->latent || !t->rope || !t->pos) return KVO_EINVAL;
     const struct {
@@ -283,6 +290,7 @@ extern "C" kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, co
   a.key = static_cast<const uint8_t*>(t->key);
   a.seq = t->seq;
   a.pos = t->pos;
+  a.place = t->place;
   a.out_bf16 = t->out_bf16;
   a.status = status;
   a.latent_ld = t->latent_ld;
@@ -294,8 +302,12 @@ extern "C" kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, co
   a.key_type = (uint32_t)cache->key_type;
   const dim3 grid((unsigned)((t->n + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const auto kernel = t->dtype == KVO_BF16   ? append_tokens_kernel<__nv_bfloat16>
-                      : t->dtype == KVO_FP16 ? append_tokens_kernel<__half>
-                                             : append_tokens_kernel<float>;
+  const auto kernel_for = [&](auto placed) {
+    constexpr bool kPlaced = decltype(placed)::value;
+    return t->dtype == KVO_BF16   ? append_tokens_kernel<__nv_bfloat16, kPlaced>
+           : t->dtype == KVO_FP16 ? append_tokens_kernel<__half, kPlaced>
+                                  : append_tokens_kernel<float, kPlaced>;
+  };
+  const auto kernel = t->place ? kernel_for(std::true_type{}) : kernel_for(std::false_type{});
   return launch_early(kernel, grid, kAppendThreads, 0, s, a) == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

@@ -83,7 +83,7 @@ class kvo_tokens(ctypes.Structure):
                 ("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
                 ("out_bf16", ctypes.c_void_p), ("latent_ld", ctypes.c_int64), ("rope_ld", ctypes.c_int64),
                 ("key_ld", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32)]
+                ("interleaved", ctypes.c_int32), ("place", ctypes.c_void_p)]
 
 
 class kvo_score_query(ctypes.Structure):
@@ -643,11 +643,13 @@ def _flat(t, what: str, dtype, shape) -> int:
 
 
 def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=None, key=None,
-                      interleaved: bool = True, out_bf16=None, stream=None) -> None:
+                      interleaved: bool = True, out_bf16=None, stream=None, place=None) -> None:
     """latent [n, 512], rope [n, 64] and key [n, 128] (optional): bfloat16,
     float16 or float32 CUDA tensors of one type, tokens strided as they are;
     pos and seq (optional): int32 CUDA [n]; inv_freq: 32 floats; out_bf16:
-    bfloat16 (or int16) CUDA [n, 576] (optional)."""
+    bfloat16 (or int16) CUDA [n, 576] (optional); place: int32 CUDA [n], the
+    rows that the tokens become where those are not their positions (behind a
+    shrunk cache)."""
     T = _T()
     n, dt = latent.shape[0], latent.dtype
     kind = T.element.get(dt)
@@ -674,7 +676,7 @@ def kvo_append_tokens(ctx: int, cache: Cache, latent, rope, pos, inv_freq, seq=N
     t = kvo_tokens(_cuda(latent, "latent", dt, (n, LATENT_VALUES)), _cuda(rope, "rope", dt, (n, ROPE_VALUES)), key_ptr,
                    None if seq is None else _cuda(seq, "seq", T.int32, (n,)), _cuda(pos, "pos", T.int32, (n,)), freq_ptr,
                    out_ptr, LATENT_VALUES if lone else latent.stride(0), ROPE_VALUES if lone else rope.stride(0), key_ld,
-                   n, kind, 1 if interleaved else 0)
+                   n, kind, 1 if interleaved else 0, None if place is None else _cuda(place, "place", T.int32, (n,)))
     _check(lib().kvo_append_tokens(ctx, cache.ref, ctypes.addressof(t), _raw_stream(T, latent.device, stream)),
            "kvo_append_tokens")
     del freq
@@ -950,8 +952,8 @@ class Context:
         return (ms[0], ms[1], ms[2]), calls.value
 
     def append_tokens(self, cache, latent, rope, pos, inv_freq, seq=None, key=None, interleaved=True, out_bf16=None,
-                      stream=None):
-        kvo_append_tokens(self.handle, cache, latent, rope, pos, inv_freq, seq, key, interleaved, out_bf16, stream)
+                      stream=None, place=None):
+        kvo_append_tokens(self.handle, cache, latent, rope, pos, inv_freq, seq, key, interleaved, out_bf16, stream, place)
 
     def index_scores(self, cache, q, weights, lens, n, block=1, out=None, stream=None):
         return kvo_index_scores(self.handle, cache, q, weights, lens, n, block, out, stream)

@@ -552,13 +552,17 @@ typedef struct kvo_cache {
  *   seq       device int32[n] or NULL (token i is sequence i); a negative
  *             entry skips its token: nothing is written for it.
  *   pos       device int32[n].
+ *   place     device int32[n] or NULL (pos): which of its sequence's rows the
+ *             token becomes, where that is not its position: behind a cache
+ *             that kvo_shrink_cache has cut, the next place is new_lens while
+ *             the rotation goes on from the positions before the cut.
  *   inv_freq  host double[32], each within [-2^20, 2^20], read before the
  *             call returns.
  *   out_bf16  device uint16[n][576] (16-byte aligned) or NULL: the values
  *             the rows stand for, as kvo_resolve_gather's out_bf16.
- * A sequence outside [0, sequences), a negative position or a position
+ * A sequence outside [0, sequences), a negative position or place, or a place
  * without a row latches KVO_ERANGE; that token's out_bf16 row is zero.  Two
- * tokens of one call must not name the same position.
+ * tokens of one call must not name the same place.
  * KVO_EINVAL: n < 0, a NULL or misaligned argument that n > 0 needs, a
  * stride below a token's values where n > 1 (0 among them), an unknown type, an inv_freq out of range or NaN, cache->rows NULL, or `key` given
  * without cache->keys (or without key_scales for e4m3).
@@ -577,6 +581,7 @@ typedef struct kvo_tokens {
   int64_t n;
   int32_t dtype;
   int32_t interleaved;
+  const int32_t* place;
 } kvo_tokens;
 kvo_status kvo_append_tokens(kvo_ctx* ctx, const kvo_cache* cache, const kvo_tokens* tokens, void* stream);
 
@@ -790,8 +795,9 @@ int64_t kvo_attention_weights_work_bytes(int64_t tokens, int32_t sequences, int3
  * positions 0, 1, .. of sequence s of the cache `to`, each with its row and,
  * if `to` has keys, its key and factor.  A sequence of at most `budget`
  * positions is copied whole.  Rows hold their position's rotation, so
- * attention over the copy needs nothing else; later tokens keep counting
- * their positions for kvo_append_tokens' rotation from the original ones.
+ * attention over the copy needs nothing else.  From then on a sequence's next
+ * row and its next position differ: kvo_append_tokens takes new_lens, counted
+ * on, as the place and the length before the cut, counted on, as the position.
  *   weights     device fp32, sequence s's at weights + s * weights_ld:
  *               kvo_attention_weights' output, or any other measure.
  *   lens        device int32[sequences], at most `rows` of them counted.

@@ -1046,3 +1046,128 @@ def test_weights_of_few_columns_strided(kvo, ctx, counts, lens, heads):
             got = c.weights(ctx, lse, window=window)
             assert ctx.sync() == kvo.KVO_OK
             c.check_weights(got, lse, window)
+
+
+# ------------------------------------------------- decoding on in a shrunk cache
+def row_is(row, kv, pos):
+    """Whether a cache row is what the token kv [576] (64-bit values) at position pos becomes."""
+    for g in range(8):
+        q, bits = O.latent_group(kv[64 * g:64 * g + 64])
+        assert int(row[512 + 2 * g:514 + 2 * g].view(np.uint16)[0]) == bits
+        assert np.array_equal(row[64 * g:64 * g + 64].view(np.int8), q)
+    exact = O.rotate(kv[512:], pos, FREQ, True)
+    pair = np.repeat(np.abs(kv[512::2]) + np.abs(kv[513::2]), 2)
+    # 2^-8 |x| for bf16; the sine, the cosine, two products and a sum in fp32, 8 u of the pair
+    assert (np.abs(O.row_values(row)[1] - exact) <= 2.0 ** -8 * np.abs(exact) + 8 * U * pair).all()
+
+
+@pytest.mark.parametrize("heads,steps,draft", [(20, 3, 1), (64, 2, 3)])
+def test_decoding_on_in_a_shrunk_cache(kvo, ctx, heads, steps, draft):
+    """Behind a cut a token's row is the next place and its rotation goes on from the old length; a second cut later on."""
+    rng = np.random.default_rng([117, heads])
+    budget, br, n = 60, 16, 200
+    st = session(kvo, ctx, [118, heads], sizes=((120, 60), (60, 61)), heads=heads, budget=budget)
+    outs = run_session(ctx, st)
+    assert ctx.sync() == kvo.KVO_OK
+    total, table = outs[7], st["table"]
+    old = st["pieces"][-1]["lens"].clone()
+    small_table, small_total = block_table(rng, 2, -(-(budget + steps * draft) // br))
+    store = torch.full((small_total * br, 656), 0x5A, dtype=torch.uint8, device="cuda")
+    small = kvo.Cache(rows=store, block_rows=br, table=dev(small_table))
+    _, held, _ = ctx.shrink_cache(st["cache"], small, total, old, budget, 2, 8)
+    seq = dev(np.repeat([0, 1], draft), torch.int32)
+    step = dev(np.tile(np.arange(draft), 2), torch.int32)
+    starts = dev(np.array([0, draft, 2 * draft]), torch.int32)
+    for _ in range(steps):
+        kv = dev(rng.standard_normal((2 * draft, 576)), torch.bfloat16)
+        q = dev(rng.standard_normal((2 * draft, heads, 576)), torch.bfloat16)
+        before = store.cpu().numpy()
+        place, pos = held[seq.long()] + step, old[seq.long()] + step
+        values = torch.empty(2 * draft, 576, dtype=torch.bfloat16, device="cuda")
+        ctx.append_tokens(small, kv[:, :512], kv[:, 512:], pos, FREQ, seq=seq, place=place, out_bf16=values)
+        held += draft
+        old += draft
+        out, lse = ctx.attend_chunk(small, q, starts, held, SCALE, budget + steps * draft)
+        assert ctx.sync() == kvo.KVO_OK
+        after = store.cpu().numpy()
+        for i in range(2 * draft):
+            at = O.row_of(small_table, small_total, br, 2, int(seq[i]), int(place[i]))
+            row_is(after[at], f64(kv)[i], int(pos[i]))
+            assert np.array_equal(np.concatenate(O.row_values(after[at])), f64(values)[i])
+            before[at] = after[at]
+        assert np.array_equal(before, after)                  # and nothing else was written
+        c = Chunk(kvo, rng, [draft, draft], held.tolist(), heads, br, rows=budget + steps * draft, q=q, raw=after,
+                  table=(small_table, small_total))
+        c.check_attend(out, lse)
+    # cut once more, into another cache: the rotation still goes on from the old length
+    last = torch.zeros(2 * 48, 656, dtype=torch.uint8, device="cuda")
+    again = kvo.Cache(rows=last, block_rows=48)
+    mass = ctx.attention_weights(small, q, starts, held, lse, SCALE, budget + steps * draft)
+    _, fewer, _ = ctx.shrink_cache(small, again, mass, held, 40, 2, 8)
+    kv = dev(rng.standard_normal((2, 576)), torch.bfloat16)
+    ctx.append_tokens(again, kv[:, :512], kv[:, 512:], old, FREQ, place=fewer)
+    assert ctx.sync() == kvo.KVO_OK
+    for s in range(2):
+        row_is(last[48 * s + int(fewer[s])].cpu().numpy(), f64(kv)[s], int(old[s]))
+
+
+def test_places_of_appended_tokens(kvo, ctx):
+    """Places apart from positions, into keys too; replayed from a graph; the position itself gives the same bytes."""
+    rng = np.random.default_rng(119)
+    table = np.array([[3, 1, -1], [0, 4, 2]], np.int32)
+    n = 6
+    kv = dev(rng.standard_normal((n, 576)), torch.bfloat16)
+    key = dev(rng.standard_normal((n, 128)), torch.bfloat16)
+    rows = torch.zeros(5 * 16, 656, dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(5 * 16, 128, dtype=torch.bfloat16, device="cuda")
+    cache = kvo.Cache(rows=rows, keys=keys, block_rows=16, table=dev(table))
+    seq = dev([0, 1, 0, 1, -1, 1], torch.int32)
+    pos = dev([5, 2 ** 31 - 1, 1_000_000, 0, 3, 77], torch.int32)
+    place = dev([31, 47, 0, 20, 2 ** 31 - 1, 0], torch.int32)
+
+    def run():
+        ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], pos, FREQ, seq=seq, key=key, place=place)
+
+    run()
+    assert ctx.sync() == kvo.KVO_OK
+    got, where = rows.cpu().numpy(), {}
+    for i in (0, 1, 2, 3, 5):
+        at = O.row_of(table, 5, 16, 2, int(seq[i]), int(place[i]))
+        where[i] = at
+        row_is(got[at], f64(kv)[i], int(pos[i]))
+        assert torch.equal(keys[at], key[i])
+    rest = [r for r in range(80) if r not in where.values()]
+    assert not got[rest].any() and not keys[rest].any()
+    want, want_keys = rows.clone(), keys.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    rows.zero_()
+    keys.zero_()
+    g.replay()
+    assert ctx.sync() == kvo.KVO_OK and torch.equal(rows, want) and torch.equal(keys, want_keys)
+    # a place that is the position gives what none gives
+    rows.zero_()
+    at = dev([3, 3], torch.int32)
+    ctx.append_tokens(cache, kv[:2, :512], kv[:2, 512:], at, FREQ)
+    plain = rows.clone()
+    rows.zero_()
+    ctx.append_tokens(cache, kv[:2, :512], kv[:2, 512:], at, FREQ, place=at)
+    assert ctx.sync() == kvo.KVO_OK and torch.equal(rows, plain)
+
+
+@pytest.mark.parametrize("pos,place", [(4, -1), (4, -2 ** 31), (-1, 4), (4, 33), (4, 48), (4, 2 ** 31 - 1)])
+def test_places_without_a_row(kvo, ctx, pos, place):
+    """A place past the table, in a page that is not there, or below zero, and a position below zero: said, not written."""
+    kv = dev(np.random.default_rng(120).standard_normal((1, 576)), torch.bfloat16)
+    rows = torch.full((4 * 16, 656), 0x5A, dtype=torch.uint8, device="cuda")
+    cache = kvo.Cache(rows=rows, block_rows=16, table=dev(np.array([[2, 0, -1]], np.int32)))
+    values = torch.full((1, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], dev([pos], torch.int32), FREQ, out_bf16=values,
+                      place=dev([place], torch.int32))
+    assert ctx.sync() == kvo.KVO_ERANGE
+    assert (rows == 0x5A).all() and not values.any()
+    for bad in (dev([place], torch.int64), dev([place, 0], torch.int32), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], dev([4], torch.int32), FREQ, place=bad)

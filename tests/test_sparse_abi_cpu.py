@@ -97,6 +97,16 @@ def test_append_refusals(kvo, ctx):
     assert good(dict(table=None), dict(seq=None)) == K.KVO_ECUDA
 
 
+def test_append_place_refusals(kvo, ctx):
+    """A place of its own is looked at like the position; none is the position."""
+    K, call = kvo, kvo.lib().kvo_append_tokens
+    good = lambda t={}: run(K, ctx, call, cache(K), tokens(K, **t))
+    assert good(dict(place=A)) == K.KVO_ECUDA and good(dict(place=None)) == K.KVO_ECUDA
+    for bad in (dict(place=A + 1), dict(place=A + 2), dict(place=A, pos=None)):
+        assert good(bad) == K.KVO_EINVAL, bad
+    assert good(dict(n=0, latent=None, rope=None, pos=None, place=None)) == K.KVO_OK
+
+
 def test_score_refusals(kvo, ctx):
     K, call = kvo, kvo.lib().kvo_index_scores
     good = lambda c={}, s={}: run(K, ctx, call, cache(K, **c), score(K, **s))

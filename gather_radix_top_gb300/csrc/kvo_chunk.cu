@@ -5,9 +5,8 @@
 //
 // Chunks with few columns go through the kernel of kvo_attend, which
 // dequantises rows for 64 columns at a time.  With many, the rows are first
-// unpacked to bf16 in the caller's scratch, once, and clusters of four CTAs take
-// 256 columns and 256 positions at a time.  Two CTAs are a pair, for 128 of the
-// columns:
+// unpacked to bf16 in the caller's scratch, once, and pairs of CTAs take 128
+// columns and 256 positions at a time:
 //     S^T [256 positions x 128 columns]      = K [256 x 576] Q^T
 //     O^T [512 values x 128 columns]        += V^T [512 x 256] P^T
 // as pair MMAs with M = 256: a CTA holds 128 of the positions for the first
@@ -16,9 +15,7 @@
 // is halved between them: 64 columns of queries (72 KB) and of weights (32 KB
 // for 256 positions) lie in each CTA's shared memory; the positions' operands
 // stream through a ring of six pieces of 16 KB (128 positions of 64 values
-// for the first product, 64 positions of 128 values for the second), which
-// both pairs share: each CTA brings half of a piece, for itself and for the CTA
-// of its rank in the other pair (multicast; half the traffic from L2).
+// for the first product, 64 positions of 128 values for the second).
 //
 // Sixteen worker warps do the softmax: a lane of S^T is a position.  The
 // weights of the other CTA's 64 columns go to it as one bulk copy (16 KB);
@@ -32,23 +29,22 @@
 // maximum.
 //
 // Tiles of columns times tiles of positions, end to end, are shared out evenly
-// over the clusters.  Where a share begins or ends inside a tile of columns, the
+// over the pairs.  Where a share begins or ends inside a tile of columns, the
 // parts are joined by their log-sum-exps in a last launch.
 //
-// Measured: 512 tokens of 64 heads over 50,023 positions 2.24 ms (1.59 PFLOP/s,
-// 0.82 of cuBLAS's short-run bf16 rate; 2.37-2.42 ms back to back, at the power
-// limit), 2,048 of 128 heads over 16,384 5.5-5.8 ms, a prompt of 4,096 tokens and
-// 16 heads alone 255 us (its tiles of columns meet 8.5 tiles of positions on
-// average, and beginning and ending one takes the time of two).  A tile of 256
-// positions takes 4,608 clocks of MMAs and keeps shared memory busy for 6,300
-// wavefronts of 128 bytes: 3,250 of the MMAs' operands, 2,180 of the copies, 900
-// of the workers.  That is the bound.
+// Measured: 512 tokens of 64 heads over 50,023 positions 2.07-2.13 ms (1.67-1.72
+// PFLOP/s; 2.21 ms back to back, at the power limit), 2,048 of 128 heads over
+// 16,384 5.34 ms, a prompt of 4,096 tokens and 16 heads alone 245 us (its tiles of
+// columns meet 8.5 tiles of positions on average, and beginning and ending one
+// takes the time of two).  A tile of 256 positions is 68 MMAs of 64 clocks, 4,352,
+// and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
+// MMAs' operands, 2,180 of the copies, 900 of the workers.  That is the bound.
 // Steps, ms for the first case: rows dequantised for 64 columns at a time 7.17,
-// pairs 3.80, copies instead of stores to the other CTA 3.27, two pairs a ring
-// 3.08, three loading warps 2.60, no order over the cluster in the workers' loop
-// 2.45; and us for the last: 650, two pairs a ring 401, sixteen columns at a time
-// 362, maxima and sums as copies 320, a loop for each role 298, and unpacking,
-// plan and join in parallel 255.
+// pairs 3.80, copies instead of stores to the other CTA 3.27, three loading warps
+// and no order over the cluster in the workers' loop 2.45, a loop for each role
+// 2.24; the last two with two pairs that shared a ring, each bringing half of
+// every piece for both: a pair by itself takes 2.10, as all 152 SMs have work then
+// (two such pairs leave 8 out) and no pair waits for another.
 #include <algorithm>
 
 #include "kvo_cache.cuh"
@@ -66,8 +62,7 @@ cudaError_t launch_few_columns(const kvo_cache& cache, const kvo_chunk_query& s,
 namespace {
 
 constexpr uint32_t kSpan = 256;                          // positions of a tile
-constexpr uint32_t kPairColumns = 2 * kColumns;
-constexpr uint32_t kTileColumns = 4 * kColumns;          // of a cluster
+constexpr uint32_t kTileColumns = 2 * kColumns;          // of a pair of CTAs
 constexpr uint32_t kTileCost = 2;                        // of a tile of columns, in tiles of positions
 constexpr uint32_t kWorkers = 16;
 constexpr uint32_t kMma = kWorkers, kLoader = kWorkers + 1;
@@ -108,12 +103,12 @@ struct ChunkArgs {
   uint8_t* values;           // [sequences][span][576] bf16
   float* off;                // [sequences][span]: 0, or -inf where there is no row
   PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
-  Cut* cuts;                 // [clusters], from share 1 on
-  uint8_t* again;            // [most_tiles] whole tiles, [2 * clusters] parts that need another pass
-  float* part;               // [2 * clusters][256][512]
-  float* part_lse;           // [2 * clusters][256], base 2
+  Cut* cuts;                 // [pairs], from share 1 on
+  uint8_t* again;            // [most_tiles] whole tiles, [2 * pairs] parts that need another pass
+  float* part;               // [2 * pairs][128][512]
+  float* part_lse;           // [2 * pairs][128], base 2
   uint32_t* status;
-  uint32_t rows, span, tokens, heads, most_tiles, clusters;
+  uint32_t rows, span, tokens, heads, most_tiles, pairs;
   uint32_t unpack_blocks;    // of a sequence
   Divider by_heads;
   Columns columns;
@@ -123,17 +118,17 @@ struct ChunkArgs {
 };
 
 // ---------------------------------------------------------------- the shares
-// Cluster g's share of the work: [from(g), from(g + 1)).
+// Pair g's share of the work: [from(g), from(g + 1)).
 struct Shares {
   uint64_t units, each;
-  uint32_t clusters, rest;           // the first `rest` shares have one more than `each`
+  uint32_t pairs, rest;           // the first `rest` shares have one more than `each`
   __device__ __forceinline__ Shares(const ChunkArgs& a) {
     units = __ldcg(&a.plan[a.most_tiles + 1].units);
-    clusters = (uint32_t)min((uint64_t)a.clusters, max(units / 2, (uint64_t)1));
-    each = units / clusters;
-    rest = (uint32_t)(units - each * clusters);
+    pairs = (uint32_t)min((uint64_t)a.pairs, max(units / 2, (uint64_t)1));
+    each = units / pairs;
+    rest = (uint32_t)(units - each * pairs);
   }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < clusters ? g * each + min(g, rest) : units; }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * each + min(g, rest) : units; }
 };
 
 // The tile that unit u lies in; a whole warp.
@@ -177,7 +172,7 @@ __device__ __forceinline__ uint32_t column_at(const ChunkArgs& a, const PlanTile
 // The last token of a tile.
 __device__ __forceinline__ uint32_t last_token(const ChunkArgs& a, uint32_t index, uint32_t tokens) {
   const Columns& c = a.columns;
-  const uint32_t rows = (4 * index + 3) / c.across * c.deep + c.deep;   // up to the tile's end
+  const uint32_t rows = (2 * index + 1) / c.across * c.deep + c.deep;   // up to the tile's end
   return min(c.flat ? divide(min(rows, tokens * a.heads) - 1, a.by_heads) : rows - 1, tokens - 1);
 }
 
@@ -190,7 +185,7 @@ __device__ void make_plan(const ChunkArgs& a) {
   const Columns& c = a.columns;
   uint32_t tiles = 0;
   uint64_t units = 0;
-  for (uint32_t i = tid; i < a.most_tiles + 2 * a.clusters; i += kUnpackThreads) a.again[i] = 0;
+  for (uint32_t i = tid; i < a.most_tiles + 2 * a.pairs; i += kUnpackThreads) a.again[i] = 0;
   for (uint32_t s0 = 0; s0 < a.cache.sequences; s0 += kUnpackThreads) {
     const uint32_t s = s0 + tid;
     uint32_t mine = 0;
@@ -200,7 +195,7 @@ __device__ void make_plan(const ChunkArgs& a) {
       first[tid] = (uint32_t)min(max(b, 0), T);
       count[tid] = (uint32_t)min(max(e, (int32_t)first[tid]), T) - first[tid];
       const uint32_t rows = c.flat ? count[tid] * a.heads : count[tid];
-      mine = ((rows + c.deep - 1) / c.deep * c.across + 3) / 4;
+      mine = ((rows + c.deep - 1) / c.deep * c.across + 1) / 2;
     }
     uint32_t incl = mine;
 #pragma unroll
@@ -269,7 +264,7 @@ __device__ void make_plan(const ChunkArgs& a) {
   __threadfence_block();
   __syncthreads();
   const Shares shares(a);
-  for (uint32_t g = 1 + warp; g < shares.clusters; g += kUnpackThreads / 32) {
+  for (uint32_t g = 1 + warp; g < shares.pairs; g += kUnpackThreads / 32) {
     const uint64_t at = shares.from(g);
     const uint32_t tile = tile_of(a, at);
     Cut cut;
@@ -278,7 +273,7 @@ __device__ void make_plan(const ChunkArgs& a) {
     cut.last = 0;
     if (at > from && at < end && shares.from(g - 1) <= from) {
       cut.last = g;
-      while (cut.last + 1 < shares.clusters && shares.from(cut.last + 1) < end) ++cut.last;
+      while (cut.last + 1 < shares.pairs && shares.from(cut.last + 1) < end) ++cut.last;
     }
     if (lane == 0) a.cuts[g] = cut;
   }
@@ -345,13 +340,13 @@ struct Segment {
   // where a segment notes that it needs another pass, and its result if it is
   // part of a tile: a share has one that begins inside a tile and one that
   // ends inside one at most
-  __device__ __forceinline__ uint32_t slot(uint32_t cluster) const { return 2 * cluster + (from == 0); }
-  __device__ __forceinline__ uint32_t note(const ChunkArgs& a, uint32_t cluster) const {
-    return whole ? number : a.most_tiles + slot(cluster);
+  __device__ __forceinline__ uint32_t slot(uint32_t pair) const { return 2 * pair + (from == 0); }
+  __device__ __forceinline__ uint32_t note(const ChunkArgs& a, uint32_t pair) const {
+    return whole ? number : a.most_tiles + slot(pair);
   }
 };
 
-// f(segment) for every segment of a cluster's share, in order, in every warp.
+// f(segment) for every segment of a pair's share, in order, in every warp.
 // tile_at(i): tile i of the plan.
 template <typename T, typename F>
 __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, T tile_at, F f) {
@@ -382,7 +377,7 @@ struct ChunkShared {
   uint64_t ready[kLetters], come[kLetters], drained;
   uint32_t tmem, gave_up;
   // per CTA and loading warp: copies of its own and before them that it has started, and queries
-  uint32_t issued[4][kLoaders], q_issued[4][kLoaders];
+  uint32_t issued[2][kLoaders], q_issued[2][kLoaders];
   uint32_t sent[kLetters], armed[kLetters];   // letters that the other CTA has sent, and that this one has been ready for
   uint32_t redo;                     // some segment needs another pass
   alignas(16) float top[2][4][4][32];         // per CTA, quarter of the columns and warp: maxima
@@ -409,21 +404,19 @@ __device__ __forceinline__ void add_lanes(float* v, uint32_t lane) {
 
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
-                 const __grid_constant__ CUtensorMap vmap) {
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ uint8_t raw[];
   __shared__ ChunkShared sh;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // ranks 2 p and 2 p + 1 are pair p: its leader, and the other
-  const uint32_t place = cluster_rank(), rank = place & 1, leader = place & 2, other = place ^ 1;
-  const uint32_t cluster = blockIdx.x >> 2;
-  const uint16_t both = (uint16_t)(3u << leader);
+  const uint32_t rank = cluster_rank(), other = rank ^ 1, pair = blockIdx.x >> 1;
+  constexpr uint16_t kBoth = 3;
   const uint32_t queries = (smem_u32(raw) + 1023u) & ~1023u, probs = queries + kQueryBytes;
   const uint32_t gift = probs + 2 * kHalfBytes, ring = gift + kHalfBytes;
 
   if (tid == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 2);                        // both pairs
+      mbar_init(&sh.empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
@@ -431,7 +424,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 2 * kWorkers);
     }
-    for (uint32_t i = 0; i < 4; ++i)
+    for (uint32_t i = 0; i < 2; ++i)
       for (uint32_t w = 0; w < kLoaders; ++w) sh.issued[i][w] = sh.q_issued[i][w] = 0;
     mbar_init(&sh.p_full, kWorkers + 1);                 // both CTAs' own columns, and that rank 1 has all of its
     for (uint32_t i = 0; i < kLetters; ++i) {
@@ -458,7 +451,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
   const Shares shares(a);
-  const uint64_t begin = shares.from(cluster), end = cluster < shares.clusters ? shares.from(cluster + 1) : begin;
+  const uint64_t begin = shares.from(pair), end = pair < shares.pairs ? shares.from(pair + 1) : begin;
   const uint32_t tile0 = begin < end ? tile_of(a, begin) : 0;
   const uint32_t box = a.columns.wide * a.columns.deep * 128;
 
@@ -474,13 +467,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   //
   // Loading warp w takes every kLoaders-th copy from copy w on, and as many of
   // the queries' nine.
-  const uint32_t load_warp = warp - kLoader, full0 = dsmem_addr(&sh.full[0], leader);
+  const uint32_t load_warp = warp - kLoader, full0 = dsmem_addr(&sh.full[0], 0);
   auto load = [&](const Segment& g, bool max_only) -> bool {
     const uint32_t tiles = g.to - g.from;
     if (lane == 0) {
       if (q_n > 0) ok = ok && wait(&sh.q_empty, (q_n - 1) & 1);
       if (ok) {
-        const uint32_t half = 4 * g.tile.index + place, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, leader);
+        const uint32_t half = 2 * g.tile.index + rank, row = half / a.columns.across, bar = dsmem_addr(&sh.q_full, 0);
         if (rank == 0 && load_warp == 0) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
         for (uint32_t i = load_warp; i < 9; i += kLoaders)
           pair_load_box(queries + i * (kColumns * 128), &qmap, (int32_t)(i * 64),
@@ -488,32 +481,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         (int32_t)((a.columns.flat ? g.tile.first * a.heads : g.tile.first) + row * a.columns.deep), bar);
         ++q_n;
       }
-      // Both pairs take the same pieces: this CTA brings half of each, for itself
-      // and the CTA of its rank in the other pair.
-      const uint32_t half = place >> 1;
-      const uint16_t mask = (uint16_t)(5u << rank);
       uint32_t at = n;                                   // the copy that a run of them begins with
-      // the next `count` copies, the k-th from place_of(k) on
-      auto copies = [&](uint32_t count, auto&& place_of) {
+      // the next `count` copies, the k-th from a map's (0, y(k), z(k)) on
+      auto copies = [&](const CUtensorMap* map, uint32_t count, auto&& y, auto&& z) {
         for (uint32_t k = (load_warp + kLoaders - at % kLoaders) % kLoaders; k < count && ok; k += kLoaders) {
           const uint32_t m = at + k, slot = m % kSlots;
           if (m >= kSlots) ok = wait(&sh.empty[slot], (m / kSlots - 1) & 1);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[slot], 2 * kSlotBytes);
-          const uint2 xy = place_of(k);
-          pair_load_box_multicast(ring + slot * kSlotBytes + half * (kSlotBytes / 2), &vmap, (int32_t)xy.x, (int32_t)xy.y,
-                                  full0 + slot * 8, mask);
+          pair_load_box(ring + slot * kSlotBytes, map, 0, (int32_t)y(k), (int32_t)z(k), full0 + slot * 8);
           n = m + 1;
         }
         at += count;
       };
-      const uint32_t k_row = (uint32_t)g.tile.seq * a.span + rank * 128 + half * 64, v_row = (uint32_t)g.tile.seq * a.span;
-      const uint32_t v_col = rank * 128 + half * 64;
+      const uint32_t first = (uint32_t)g.tile.seq * a.span;
       for (uint32_t i = 0; i <= tiles && ok; ++i) {
-        const uint32_t row = (g.from + i) * kSpan;
-        if (i < tiles) copies(9, [&](uint32_t k) { return make_uint2(64 * k, k_row + row); });
+        const uint32_t row = first + (g.from + i) * kSpan;
+        if (i < tiles)
+          copies(&kmap, 9, [&](uint32_t) { return row + rank * (kSpan / 2); }, [](uint32_t k) { return k; });
         if (i > 0 && !max_only)
-          copies(8, [&](uint32_t k) { return make_uint2((k >> 2) * 256 + v_col, v_row + row - kSpan + (k & 3) * 64); });
+          copies(&vmap, 8, [&](uint32_t k) { return row - kSpan + (k & 3) * 64; },
+                 [&](uint32_t k) { return (k >> 2) * 4 + rank * 2; });
       }
       if (ok) n = at;
     }
@@ -560,7 +548,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // (Waits of the whole warp, with a vote, a fence and an election for every
   // four: 430 clocks.)
   auto multiply = [&](const Segment& g, bool max_only) -> bool {
-    constexpr uint32_t kQk = pair_desc(1, kPairColumns, false, false), kPv = pair_desc(1, kPairColumns, true, true);
+    constexpr uint32_t kQk = pair_desc(1, kTileColumns, false, false), kPv = pair_desc(1, kTileColumns, true, true);
     const uint32_t tiles = g.to - g.from;
     if (ok && elect_one()) {
       const uint64_t q_desc = tile_desc(queries, 16), k_desc = tile_desc(ring, 16);
@@ -575,7 +563,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ok = wait(&sh.q_full, q_n & 1);
       for (uint32_t i = 0, t = it, p = pv; i <= tiles && ok; ++i) {
         if (i < tiles) {
-          const uint32_t buf = t & 1, d = tmem + 256 + buf * kPairColumns;
+          const uint32_t buf = t & 1, d = tmem + 256 + buf * kTileColumns;
           if (t >= 2) ok = wait(&sh.s_empty[buf], ((t >> 1) - 1) & 1);
           tc_fence_after();
 #pragma unroll 3
@@ -586,11 +574,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (uint32_t e = 0; e < 4; ++e)
               pair_mma_bf16(d, k_desc + slot * (kSlotBytes >> 4) + 2 * e, q_desc + k * (kColumns * 128 >> 4) + 2 * e, kQk,
                             k + e > 0);
-            pair_commit(&sh.empty[slot], 15);
+            pair_commit(&sh.empty[slot], kBoth);
           }
           if (!ok) break;
-          pair_commit(&sh.s_full[buf], both);
-          if (i + 1 == tiles) pair_commit(&sh.q_empty, both);
+          pair_commit(&sh.s_full[buf], kBoth);
+          if (i + 1 == tiles) pair_commit(&sh.q_empty, kBoth);
           ++t;
         }
         if (i > 0 && !max_only) {
@@ -603,12 +591,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!ok) break;
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e)
-              pair_mma_bf16(tmem + (k / 4) * kPairColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
+              pair_mma_bf16(tmem + (k / 4) * kTileColumns, v_desc + slot * (kSlotBytes >> 4) + 128 * e,
                             p_desc + (k % 4) * 512 + 128 * e, kPv, i > 1 || k % 4 + e > 0);
-            pair_commit(&sh.empty[slot], 15);
+            pair_commit(&sh.empty[slot], kBoth);
           }
           if (!ok) break;
-          pair_commit(&sh.p_empty, both);
+          pair_commit(&sh.p_empty, kBoth);
           ++p;
         }
       }
@@ -629,7 +617,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (uint32_t i = g.from; i < g.to && !max_only; ++i, ++pv) {
       if (lane == 0) {
         ok = come(pv);
-        if (ok) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, leader));
+        if (ok) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, 0));
       }
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
@@ -639,9 +627,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // A worker's position of a tile: rank * 128 + quad * 32 + lane; its columns: quarter * 32 + c.
   const uint32_t quad = warp & 3, quarter = (warp >> 2) & 3, mine = rank * 128 + quad * 32 + lane;
   const uint32_t lanes = tmem + (quad << 21);
-  auto arrive0 = [&](uint64_t* bar) {                    // at the leader's, for the warp's loads from tensor memory
+  auto arrive0 = [&](uint64_t* bar) {                    // at rank 0's, for the warp's loads from tensor memory
     __syncwarp();
-    if (lane == 0) cluster_mbar_arrive_relaxed(dsmem_addr(bar, leader));
+    if (lane == 0) cluster_mbar_arrive_relaxed(dsmem_addr(bar, 0));
   };
   // the maxima of this warp's columns (lane c: column c's) to both CTAs, and back the whole tile's
   auto meet = [&](float best) -> float {
@@ -657,7 +645,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // first: the references are still to be found
   auto soften = [&](const Segment& g, bool max_only, bool first) -> bool {
     uint32_t at;
-    const uint32_t token = column_at(a, g.tile, 4 * g.tile.index + leader + quarter / 2, quarter % 2 * 32 + lane, &at);
+    const uint32_t token = column_at(a, g.tile, 2 * g.tile.index + quarter / 2, quarter % 2 * 32 + lane, &at);
     const bool real = token < g.tile.tokens;
     const uint32_t sees = real ? visible(a, g.tile.before, token) : UINT32_MAX;   // (others hold nothing up)
     const uint32_t least = __reduce_min_sync(0xffffffffu, sees);
@@ -683,7 +671,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ok = ok && wait(&sh.s_full[it & 1], it >> 1 & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
-      const uint32_t scores = lanes + 256 + (it & 1) * kPairColumns + quarter * 32;
+      const uint32_t scores = lanes + 256 + (it & 1) * kTileColumns + quarter * 32;
       const bool edge = __any_sync(0xffffffffu, gone) || (i + 1) * kSpan > least;
       // sixteen columns at a time, `x` times `scale` their logits
       auto logits = [&](uint32_t h, float* x) -> float {
@@ -776,7 +764,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (own) {
-        if (lane == 0) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, leader));
+        if (lane == 0) cluster_mbar_arrive_own(dsmem_addr(&sh.p_full, 0));
       } else {
         if (lane == 0) mbar_arrive(&sh.ready[kGift]);
         if (warp % 8 == 0) {                             // the first of the eight warps with the other's columns
@@ -816,13 +804,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float total = 0.0f;
     for (uint32_t r = 0; r < 2; ++r)
       for (uint32_t q = 0; q < 4; ++q) total += ((volatile float*)sh.sums[r].of[quarter][q])[lane];
-    const uint32_t slot = g.slot(cluster);
+    const uint32_t slot = g.slot(pair);
     ok = ok && wait(&sh.p_empty, (pv - 1) & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
     tc_fence_after();
     if (again) {
       if (tid == 0) {
-        a.again[g.note(a, cluster)] = 1;                 // (both CTAs write it)
+        a.again[g.note(a, pair)] = 1;                 // (both CTAs write it)
         sh.redo = 1;
       }
     } else {
@@ -831,7 +819,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const float lse2 = total == 0.0f ? -INFINITY : ref - up + log2f(total * (up ? 0x1p32f : 1.0f));
       if (quad == 0 && rank == 0) {
         if (!g.whole)
-          a.part_lse[slot * kTileColumns + leader * kColumns + quarter * 32 + lane] = lse2;
+          a.part_lse[slot * kTileColumns + quarter * 32 + lane] = lse2;
         else if (real && a.lse)
           a.lse[(int64_t)g.tile.first * a.heads + at] = lse2 * 0.6931471805599453f;
       }
@@ -840,14 +828,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t first_at = __shfl_sync(0xffffffffu, at, 0);
       // sixteen columns of 128 values at a time (in one run the columns' results follow each other)
       const int64_t row0 = g.whole ? (int64_t)g.tile.first * a.heads + (a.columns.flat ? first_at : 0)
-                                   : (int64_t)slot * kTileColumns + leader * kColumns + quarter * 32;
+                                   : (int64_t)slot * kTileColumns + quarter * 32;
       sh.ref[quarter][lane] = inv;
       __syncwarp();
 #pragma unroll 1
       for (uint32_t part = 0; part < 4; ++part) {
         const uint32_t c0 = part % 2 * 16, half = part / 2;
         float o[16];
-        tmem_ld16(lanes + half * kPairColumns + quarter * 32 + c0, o);
+        tmem_ld16(lanes + half * kTileColumns + quarter * 32 + c0, o);
         tmem_ld_wait();
 #pragma unroll
         for (uint32_t c = 0; c < 16; c += 4) {
@@ -893,7 +881,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   auto rounds = [&](auto&& tile_at, auto&& work) {
     for (uint32_t round = 0; round < 2; ++round) {
       for_segments(a, begin, end, tile0, tile_at, [&](const Segment& g) -> bool {
-        if (round && !__ldcg(a.again + g.note(a, cluster))) return true;
+        if (round && !__ldcg(a.again + g.note(a, pair))) return true;
         for (uint32_t pass = round ? 0 : 1; pass < 2; ++pass)
           if (!work(g, pass == 0, !round)) return false;
         return true;
@@ -902,9 +890,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __threadfence();
       __syncthreads();
       cluster_sync();
-      // the same answer in all CTAs: nothing changes between the barriers
+      // the same answer in both CTAs: nothing changes between the barriers
       uint32_t redo = 0, gave_up = 0;
-      for (uint32_t r = 0; r < 4; ++r) {
+      for (uint32_t r = 0; r < 2; ++r) {
         redo |= dsmem_ld_u32(dsmem_addr(&sh.redo, r));
         gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
       }
@@ -938,28 +926,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // no slot's release may still be on its way when the CTA ends
       for (uint32_t m = n > kSlots ? n - kSlots : 0; ok && m < n; ++m) ok = wait(&sh.empty[m % kSlots], m / kSlots & 1);
       if (ok && q_n) wait(&sh.q_empty, (q_n - 1) & 1);
-      for (uint32_t r = 0; r < 4; ++r) {
-        dsmem_st_u32(dsmem_addr(&sh.issued[place][load_warp], r), n);
-        dsmem_st_u32(dsmem_addr(&sh.q_issued[place][load_warp], r), q_n);
-      }
+      dsmem_st_u32(dsmem_addr(&sh.issued[rank][load_warp], 0), n);
+      dsmem_st_u32(dsmem_addr(&sh.q_issued[rank][load_warp], 0), q_n);
     }
   } else if (rank == 0) {
     rounds(ahead, [&](const Segment& g, bool max_only, bool) { return multiply(g, max_only); });
   } else {
     rounds(ahead, [&](const Segment& g, bool max_only, bool) { return pass_on(g, max_only); });
   }
-  // All CTAs end together.  Where a wait gave up in any, what is in flight
+  // Both CTAs end together.  Where a wait gave up in either, what is in flight
   // finishes first: the MMAs, then the copies; those that a CTA has not started
   // count as come.
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  uint32_t any_gave_up = 0;
-  for (uint32_t r = 0; r < 4; ++r) any_gave_up |= dsmem_ld_u32(dsmem_addr(&sh.gave_up, r));
-  if (any_gave_up) {
+  const uint32_t other_gave_up = dsmem_ld_u32(dsmem_addr(&sh.gave_up, other));
+  if (sh.gave_up | other_gave_up) {
     if (tid == 0) atomicOr(a.status, kFlagTimeout);
     if (rank == 0 && warp == kMma && elect_one()) {
-      pair_commit(&sh.drained, (uint16_t)(1u << place));
+      pair_commit(&sh.drained, 1);
       if (!landed(&sh.drained, 0)) atomicOr(a.status, kFlagInflight);
     }
     if (tid == 0) {
@@ -971,30 +956,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (rank == 0 && warp == kLoader && lane == 0) {
       uint32_t most = 0, least = UINT32_MAX, queried = 0;
-      for (uint32_t r = 0; r < 4; ++r)
+      for (uint32_t r = 0; r < 2; ++r)
         for (uint32_t w = 0; w < kLoaders; ++w) {
           most = max(most, sh.issued[r][w]);
           least = min(least, sh.issued[r][w]);
-          if ((r & 2) == leader) queried = max(queried, sh.q_issued[r][w]);
+          queried = max(queried, sh.q_issued[r][w]);
         }
       // (whoever starts a copy has seen the one before it in its slot used up)
-      auto started = [&](uint32_t m) {
-        for (uint32_t r = 0; r < 4; ++r)
-          if (m < sh.issued[r][m % kLoaders]) return true;
-        return false;
-      };
+      auto started = [&](uint32_t m) { return m < sh.issued[0][m % kLoaders] || m < sh.issued[1][m % kLoaders]; };
       for (uint32_t m = least; m < most; ++m) {
         uint64_t* const bar = &sh.full[m % kSlots];
         if (!started(m)) continue;
-        if (m >= sh.issued[place][m % kLoaders]) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
-        for (uint32_t r = 0; r < 4; ++r)
-          if (m >= sh.issued[r][m % kLoaders]) mbar_complete_tx(bar, kSlotBytes / 2);
+        if (m >= sh.issued[0][m % kLoaders]) mbar_arrive_expect_tx(bar, 2 * kSlotBytes);
+        for (uint32_t r = 0; r < 2; ++r)
+          if (m >= sh.issued[r][m % kLoaders]) mbar_complete_tx(bar, kSlotBytes);
       }
       for (uint32_t m = most > kSlots ? most - kSlots : 0; m < most; ++m)
         if (started(m) && !landed(&sh.full[m % kSlots], m / kSlots & 1)) atomicOr(a.status, kFlagInflight);
       if (queried) {
-        if (sh.q_issued[place][0] < queried) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
-        for (uint32_t r = leader; r < leader + 2; ++r)
+        if (sh.q_issued[0][0] < queried) mbar_arrive_expect_tx(&sh.q_full, 2 * 9 * box);
+        for (uint32_t r = 0; r < 2; ++r)
           for (uint32_t w = 0; w < kLoaders; ++w)
             if (sh.q_issued[r][w] < queried) mbar_complete_tx(&sh.q_full, 9 / kLoaders * box);
         if (!landed(&sh.q_full, (queried - 1) & 1)) atomicOr(a.status, kFlagInflight);
@@ -1008,37 +989,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
 // Joins the parts of a cut tile by their log-sum-exps: blocks (g - 1, ..) those
 // that share g is the first to cut, four columns of 128 threads each.
-constexpr uint32_t kJoinColumns = 4, kMostParts = 64;
+constexpr uint32_t kJoinColumns = 4, kMostParts = 96;
 
 __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
   const uint32_t g = blockIdx.x + 1, d = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t column = blockIdx.y * kJoinColumns + (threadIdx.x >> 7);
   wait_previous_grid();
-  if (g >= Shares(a).clusters) return;
+  if (g >= Shares(a).pairs) return;
   const uint32_t last = __ldcg(&a.cuts[g].last);
   if (last == 0) return;
   const uint4 *const cut = reinterpret_cast<const uint4*>(a.cuts + g), x = __ldcg(cut), y = __ldcg(cut + 1);
   const PlanTile t{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
   uint32_t where;
-  const uint32_t token = column_at(a, t, 4 * t.index + column / kColumns, column % kColumns, &where);
+  const uint32_t token = column_at(a, t, 2 * t.index + column / kColumns, column % kColumns, &where);
   if (token >= t.tokens) return;                         // (the same for a column's warps)
   const uint32_t parts = last - g + 2;
   auto row_of = [&](uint32_t i) { return (2 * (g - 1 + i) + (i == 0)) * kTileColumns + column; };
-  // lane l has the weights of parts l and l + 32
-  float l0 = lane < parts ? __ldcg(a.part_lse + row_of(lane)) : -INFINITY;
-  float l1 = lane + 32 < parts ? __ldcg(a.part_lse + row_of(lane + 32)) : -INFINITY;
-  float top = fmaxf(l0, l1);
+  // lane l has the weights of parts l, l + 32 and l + 64
+  float l[kMostParts / 32], top = -INFINITY;
+#pragma unroll
+  for (uint32_t k = 0; k < kMostParts / 32; ++k) {
+    l[k] = lane + 32 * k < parts ? __ldcg(a.part_lse + row_of(lane + 32 * k)) : -INFINITY;
+    top = fmaxf(top, l[k]);
+  }
 #pragma unroll
   for (uint32_t e = 16; e; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
   const float base = top == -INFINITY ? 0.0f : top;
-  l0 = exp2f(l0 - base);
-  l1 = exp2f(l1 - base);
+#pragma unroll
+  for (uint32_t k = 0; k < kMostParts / 32; ++k) l[k] = exp2f(l[k] - base);
   float total = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (uint32_t i = 0; i < parts; ++i) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)row_of(i) * KVO_LATENT_BYTES) + d);
-    const float w = __shfl_sync(0xffffffffu, i < 32 ? l0 : l1, i & 31);
+    const float w = __shfl_sync(0xffffffffu, i < 32 ? l[0] : i < 64 ? l[1] : l[2], i & 31);
     if (!(w > 0.0f) && !isnan(w)) continue;
     total += w;
     o.x = fmaf(w, v.x, o.x);
@@ -1055,37 +1039,38 @@ __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __
 
 // ------------------------------------------------------------------ the host
 // Whether unpacking the rows pays.  Per 1,000 rows of a sequence the kernel for
-// few columns takes about 0.29 us for every 64 columns, this one 0.36 us for
-// every 256 and 0.40 us to unpack them, and about 20 us more a call.  Both
-// ways, us: 16 sequences of 8,192 rows with 128 columns each 91 and 131, with
-// 256 168 and 134; 64 of 4,096 with 256 323 and 239; one of 50,000 rows with 256
-// 66 and 70, with 512 112 and 86; 1,024 columns over 4,000 rows 31 and 41, over
-// 50,000 220 and 121; 4,096 over 2,000 52 and 48.
+// few columns takes about 0.29 us for every 64 columns, this one 0.20 us for
+// every 128 and 0.45 us to unpack them, and about 21 us more a call.  Both
+// ways, us: 16 sequences of 8,192 rows with 128 columns each 91 and 114, with
+// 256 168 and 141; 64 of 4,096 with 128 164 and 195, with 256 324 and 255; one of
+// 50,000 rows with 256 66 and 73, with 384 89 and 78, with 1,024 221 and 116; 1,024
+// columns over 4,000 rows 32 and 43; 2,048 over 4,000 51 and 48; 4,096 over 2,000 52
+// and 49, over 1,000 34 and 45; 16,384 over 500 52 and 57.
 bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
   if (sequences * span > INT32_MAX) return false;
   const int64_t columns = (tokens * heads + busy - 1) / busy, each = (tokens + busy - 1) / busy;
   const int64_t seen = rows - std::min(each, rows) / 2;  // of the middle token
-  const int64_t gain = 29 * ((columns + 63) / 64) - 36 * ((columns + 255) / 256) - 40;
-  return gain > 0 && (double)busy * (double)seen * (double)gain > 2e6;
+  const int64_t gain = 29 * ((columns + 63) / 64) - 20 * ((columns + 127) / 128) - 45;
+  return gain > 0 && (double)busy * (double)seen * (double)gain > 2.1e6;
 }
 
 struct Layout {              // of the scratch
-  int64_t span, tiles, clusters;
+  int64_t span, tiles, pairs;
   int64_t values, off, plan, cuts, again, part, part_lse, bytes;
 };
 
 Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   Layout l;
   l.span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
-  l.clusters = std::min(device_sms() / 4, (int)kMostParts);
+  l.pairs = std::min(device_sms() / 2, (int)kMostParts);
   // Tiles of either way to fill them: at worst 33 heads of one token a half.
   const int64_t busy = sequences < tokens ? sequences : tokens;
   const int64_t deep = heads < kColumns ? kColumns / heads : 1, across = heads > kColumns ? 2 : 1;
   const int64_t halves = (tokens + busy * (deep - 1)) / deep * across;
   const int64_t flat = (tokens * heads + busy * (kColumns - 1)) / kColumns;
-  l.tiles = ((halves > flat ? halves : flat) + 3 * busy + 3) / 4;
+  l.tiles = ((halves > flat ? halves : flat) + busy + 1) / 2;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -1095,28 +1080,29 @@ Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows
   l.values = take(sequences * l.span * kValueBytes);
   l.off = take(sequences * l.span * 4);
   l.plan = take((l.tiles + 2) * (int64_t)sizeof(PlanTile));
-  l.cuts = take(l.clusters * (int64_t)sizeof(Cut));
-  l.again = take(l.tiles + 2 * l.clusters);
-  l.part = take(2 * l.clusters * kTileColumns * KVO_LATENT_BYTES * 4);
-  l.part_lse = take(2 * l.clusters * kTileColumns * 4);
+  l.cuts = take(l.pairs * (int64_t)sizeof(Cut));
+  l.again = take(l.tiles + 2 * l.pairs);
+  l.part = take(2 * l.pairs * kTileColumns * KVO_LATENT_BYTES * 4);
+  l.part_lse = take(2 * l.pairs * kTileColumns * 4);
   l.bytes = at;
   return l;
 }
 
-cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap& vmap, cudaStream_t stream) {
-  static int room[64] = {};                              // clusters that run at the same time
+cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         cudaStream_t stream) {
+  static int room[64] = {};                              // pairs that run at the same time
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 4;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3(4);
+  lc.gridDim = dim3(2);
   lc.blockDim = dim3(kChunkThreads);
   lc.dynamicSmemBytes = kChunkSmem;
   lc.stream = stream;
@@ -1131,14 +1117,14 @@ cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap
     if (n < 1) return cudaErrorInvalidConfiguration;
     room[dev & 63] = n;
   }
-  if (a.clusters > (uint32_t)room[dev & 63]) a.clusters = (uint32_t)room[dev & 63];
+  if (a.pairs > (uint32_t)room[dev & 63]) a.pairs = (uint32_t)room[dev & 63];
   e = launch_early(unpack_kernel, dim3(1 + a.unpack_blocks * a.cache.sequences), kUnpackThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
-  lc.gridDim = dim3(4 * a.clusters);
+  lc.gridDim = dim3(2 * a.pairs);
   lc.numAttrs = 2;
-  e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, vmap);
-  if (e != cudaSuccess || a.clusters < 2) return e;
-  return launch_early(join_parts_kernel, dim3(a.clusters - 1, kTileColumns / kJoinColumns), 128 * kJoinColumns, 0,
+  e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, kmap, vmap);
+  if (e != cudaSuccess || a.pairs < 2) return e;
+  return launch_early(join_parts_kernel, dim3(a.pairs - 1, kTileColumns / kJoinColumns), 128 * kJoinColumns, 0,
                       stream, a);
 }
 
@@ -1195,7 +1181,7 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.tokens = (uint32_t)s->tokens;
   a.heads = (uint32_t)s->heads;
   a.most_tiles = (uint32_t)l.tiles;
-  a.clusters = (uint32_t)l.clusters;
+  a.pairs = (uint32_t)l.pairs;
   a.unpack_blocks = (uint32_t)(l.span / kUnpackRows);
   a.by_heads = divider(a.heads);
   a.scale = s->scale * kLog2e;
@@ -1206,9 +1192,10 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   const int64_t head_ld = a.heads > 1 ? s->q_head_ld : KVO_DEQUANT_VALUES;
   const int64_t q_ld = s->tokens > 1 ? s->q_ld : a.heads * head_ld;
   a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens);
-  CUtensorMap qmap, vmap;
+  CUtensorMap qmap, kmap, vmap;
   if (!query_map(&qmap, s->q, a.heads, s->tokens, q_ld * 2, head_ld * 2, a.columns) ||
-      !value_map(&vmap, a.values, cache->sequences * l.span))
+      !value_map(&kmap, a.values, cache->sequences * l.span, kSpan / 2, 1) ||
+      !value_map(&vmap, a.values, cache->sequences * l.span, 64, 2))
     return KVO_ECUDA;
-  return launch_chunk(a, qmap, vmap, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
+  return launch_chunk(a, qmap, kmap, vmap, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
 }

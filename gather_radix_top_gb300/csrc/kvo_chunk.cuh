@@ -109,13 +109,14 @@ inline bool query_map(CUtensorMap* map, const void* q, uint32_t heads, int64_t t
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Unpacked rows as boxes of 64 values of 64 rows.
-inline bool value_map(CUtensorMap* map, const void* values, int64_t rows) {
+// Unpacked rows as groups of 64 values, in boxes of `deep` rows of `groups`
+// groups, the groups one behind the other.
+inline bool value_map(CUtensorMap* map, const void* values, int64_t rows, uint32_t deep, uint32_t groups) {
   const auto encode = map_encoder();
   if (!encode) return false;
-  const cuuint64_t size[2] = {KVO_DEQUANT_VALUES, (cuuint64_t)rows}, pitch[1] = {KVO_DEQUANT_VALUES * 2};
-  const cuuint32_t box[2] = {64, 64}, every[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(values), size, pitch, box, every,
+  const cuuint64_t size[3] = {64, (cuuint64_t)rows, KVO_DEQUANT_VALUES / 64}, pitch[2] = {KVO_DEQUANT_VALUES * 2, 128};
+  const cuuint32_t box[3] = {64, deep, groups}, every[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(values), size, pitch, box, every,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

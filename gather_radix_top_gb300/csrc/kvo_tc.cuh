@@ -195,17 +195,6 @@ __device__ __forceinline__ void pair_load_box(uint32_t dst, const void* map, int
       : "memory");
 }
 
-// A box of a two-dimensional one to that place in the CTAs of `mask`; each completes on the barrier
-// at `bar`'s place in the CTA of its pair that has the parity of `bar`'s.
-__device__ __forceinline__ void pair_load_box_multicast(uint32_t dst, const void* map, int32_t x, int32_t y, uint32_t bar,
-                                                        uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar), "h"(mask)
-      : "memory");
-}
-
 // As if a copy of `bytes` that `bar` expects had come.
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");

@@ -169,3 +169,18 @@ def test_binding_refuses_wrong_tensors(kvo):
     for bad in (torch.zeros(2, 64), torch.zeros(64), torch.zeros(2, 64, dtype=torch.float16)):
         with pytest.raises((ValueError, TypeError)):
             K.kvo_shrink_cache(ctypes.addressof(c), paged, paged, bad, lens, 10)
+
+
+def test_no_copy_is_multicast():
+    """Copies go to one CTA each: what they read may be memory that the caller names, of any kind."""
+    import glob
+    import os
+    import re
+    root = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gather_radix_top_gb300", "csrc")
+    sources = glob.glob(os.path.join(root, "*.cu*"))
+    assert len(sources) > 10
+    for path in sources:
+        text = open(path).read()
+        assert "load_box_multicast" not in text, path
+        for copy in re.findall(r"cp\.async\.bulk[^;]*;", text):
+            assert "multicast" not in copy, (path, copy)

@@ -190,10 +190,10 @@ __device__ void make_plan(const ChunkArgs& a) {
     const uint32_t s = s0 + tid;
     uint32_t mine = 0;
     if (s < a.cache.sequences) {
-      const int32_t b = a.starts[s], e = a.starts[s + 1], T = (int32_t)a.tokens;
-      if (b < 0 || b > T || e < b || e > T) atomicOr(a.status, kFlagRange);
-      first[tid] = (uint32_t)min(max(b, 0), T);
-      count[tid] = (uint32_t)min(max(e, (int32_t)first[tid]), T) - first[tid];
+      const Tokens t = tokens_of(a.starts, s, a.tokens);
+      if (t.bad) atomicOr(a.status, kFlagRange);
+      first[tid] = t.first;
+      count[tid] = t.count;
       const uint32_t rows = c.flat ? count[tid] * a.heads : count[tid];
       mine = ((rows + c.deep - 1) / c.deep * c.across + 1) / 2;
     }
@@ -293,6 +293,8 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
   const uint32_t p0 = ((blockIdx.x - 1) % a.unpack_blocks) * kUnpackRows + warp * 8;
   const uint32_t len = (uint32_t)min(max(a.lens[s], 0), (int32_t)a.rows);
   if (p0 >= (max(len, 1u) + kSpan - 1) / kSpan * kSpan) return;
+  // rows that no token looks at: they may be on pages that are not there
+  if (tokens_of(a.starts, s, a.tokens).count == 0) return;
   int64_t row = -1;
   if (lane < 8) {
     const uint32_t p = p0 + lane;

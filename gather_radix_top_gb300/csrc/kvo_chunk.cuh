@@ -18,6 +18,17 @@ struct ChunkTile {
   uint32_t first, tokens;    // the sequence's tokens
 };
 
+// Sequence s's tokens; starts outside the tokens, or that go back, count as the
+// nearest ones that do not (`bad`).
+struct Tokens {
+  uint32_t first, count;
+  bool bad;
+};
+__device__ __forceinline__ Tokens tokens_of(const int32_t* starts, uint32_t s, uint32_t tokens) {
+  const int32_t b = starts[s], e = starts[s + 1], all = (int32_t)tokens, first = min(max(b, 0), all);
+  return Tokens{(uint32_t)first, (uint32_t)(min(max(e, first), all) - first), b < 0 || b > all || e < b || e > all};
+}
+
 // Tiles that a call's sequences can have at most: their last ones may be part.
 inline uint32_t chunk_tiles(int64_t tokens, int64_t sequences, int64_t heads, int64_t columns) {
   const int64_t busy = sequences < tokens ? sequences : tokens;

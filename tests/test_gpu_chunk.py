@@ -1171,3 +1171,33 @@ def test_places_without_a_row(kvo, ctx, pos, place):
     for bad in (dev([place], torch.int64), dev([place, 0], torch.int32), torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(ValueError):
             ctx.append_tokens(cache, kv[:, :512], kv[:, 512:], dev([4], torch.int32), FREQ, place=bad)
+
+
+# -------------------------------------------------- the kernel of many columns
+class Many(Long):
+    """Chunks that are sure to go through the kernel of many columns: its scratch holds their rows as bf16."""
+
+    def attend(self, ctx, rows=60_000, **kw):
+        need = self.kvo.kvo_attend_chunk_work_bytes(self.tokens, self.n, self.heads, rows)
+        assert need >= self.n * rows * 1152
+        return super().attend(ctx, rows, **kw)
+
+
+@pytest.mark.parametrize("kind", [Chunk, Many])
+@pytest.mark.parametrize("counts", [[90, 0, 40, 0], [0, 0, 64, 70, 0]])
+def test_chunk_idle_sequences(kvo, ctx, kind, counts):
+    """Sequences without tokens are not looked at: their pages may be gone, and they change nothing."""
+    rng = np.random.default_rng([121, len(counts)])
+    heads, lens = 64, [300, 700, 90, 513, 60][:len(counts)]
+    c = kind(kvo, rng, counts, lens, heads)
+    want = c.attend(ctx)
+    weights = c.weights(ctx, want[1])
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(*want)
+    table = c.table.copy()
+    table[[s for s, n in enumerate(counts) if n == 0]] = -1
+    d = kind(kvo, rng, counts, lens, heads, q=c.q, raw=c.raw, table=(table, c.total))
+    out, lse = d.attend(ctx)
+    got = d.weights(ctx, lse)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(got, weights)

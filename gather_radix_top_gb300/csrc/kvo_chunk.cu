@@ -100,7 +100,7 @@ struct ChunkArgs {
   const int32_t* lens;
   uint16_t* out;
   float* lse;
-  uint8_t* values;           // [sequences][span][576] bf16
+  uint8_t* values;           // [sequences][span][576] bf16, of the group in turn
   float* off;                // [sequences][span]: 0, or -inf where there is no row
   PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
   Cut* cuts;                 // [pairs], from share 1 on
@@ -1040,9 +1040,24 @@ __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __
 }
 
 // ------------------------------------------------------------------ the host
+// Sequences are taken in groups whose unpacked rows fit into 4 GiB of scratch,
+// one group after the other, however many there are and however long `rows`
+// says they may be.  No group: a single one's do not fit.
+constexpr int64_t kMostValueBytes = (int64_t)4 << 30;
+
+struct Groups {
+  int64_t span, count, each;         // positions of a sequence; groups; sequences of a group
+  Groups(int64_t sequences, int64_t rows) {
+    span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
+    const int64_t most = kMostValueBytes / (span * kValueBytes);
+    count = most ? (sequences + most - 1) / most : 0;
+    each = count ? (sequences + count - 1) / count : 0;
+  }
+};
+
 // Whether unpacking the rows pays.  Per 1,000 rows of a sequence the kernel for
 // few columns takes about 0.29 us for every 64 columns, this one 0.20 us for
-// every 128 and 0.45 us to unpack them, and about 21 us more a call.  Both
+// every 128 and 0.45 us to unpack them, and about 21 us more a group.  Both
 // ways, us: 16 sequences of 8,192 rows with 128 columns each 91 and 114, with
 // 256 168 and 141; 64 of 4,096 with 128 164 and 195, with 256 324 and 255; one of
 // 50,000 rows with 256 66 and 73, with 384 89 and 78, with 1,024 221 and 116; 1,024
@@ -1050,22 +1065,22 @@ __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __
 // and 49, over 1,000 34 and 45; 16,384 over 500 52 and 57.
 bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   const int64_t busy = sequences < tokens ? sequences : tokens;
-  const int64_t span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
-  if (sequences * span > INT32_MAX) return false;
+  const Groups groups(sequences, rows);
+  if (!groups.count) return false;
   const int64_t columns = (tokens * heads + busy - 1) / busy, each = (tokens + busy - 1) / busy;
   const int64_t seen = rows - std::min(each, rows) / 2;  // of the middle token
   const int64_t gain = 29 * ((columns + 63) / 64) - 20 * ((columns + 127) / 128) - 45;
-  return gain > 0 && (double)busy * (double)seen * (double)gain > 2.1e6;
+  return gain > 0 && (double)busy * (double)seen * (double)gain > 2.1e6 * (double)groups.count;
 }
 
 struct Layout {              // of the scratch
-  int64_t span, tiles, pairs;
+  int64_t tiles, pairs;
   int64_t values, off, plan, cuts, again, part, part_lse, bytes;
 };
 
 Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows) {
   Layout l;
-  l.span = ((rows > 0 ? rows : 1) + kSpan - 1) / kSpan * kSpan;
+  const Groups groups(sequences, rows);
   l.pairs = std::min(device_sms() / 2, (int)kMostParts);
   // Tiles of either way to fill them: at worst 33 heads of one token a half.
   const int64_t busy = sequences < tokens ? sequences : tokens;
@@ -1079,8 +1094,8 @@ Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows
     at += (bytes + 255) / 256 * 256;
     return from;
   };
-  l.values = take(sequences * l.span * kValueBytes);
-  l.off = take(sequences * l.span * 4);
+  l.values = take(groups.each * groups.span * kValueBytes);
+  l.off = take(groups.each * groups.span * 4);
   l.plan = take((l.tiles + 2) * (int64_t)sizeof(PlanTile));
   l.cuts = take(l.pairs * (int64_t)sizeof(Cut));
   l.again = take(l.tiles + 2 * l.pairs);
@@ -1162,12 +1177,10 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   if (!many_columns(s->tokens, cache->sequences, (uint32_t)s->heads, s->rows))
     return launch_few_columns(*cache, *s, status, wait_clocks, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
 
+  const Groups groups(cache->sequences, s->rows);
   const Layout l = layout_of(s->tokens, cache->sequences, (uint32_t)s->heads, s->rows);
   uint8_t* const work = static_cast<uint8_t*>(s->work);
   ChunkArgs a = {};
-  a.cache = cache_view(*cache);
-  a.starts = s->starts;
-  a.lens = s->lens;
   a.out = s->out;
   a.lse = s->lse;
   a.values = work + l.values;
@@ -1179,12 +1192,12 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.part_lse = reinterpret_cast<float*>(work + l.part_lse);
   a.status = status;
   a.rows = (uint32_t)s->rows;
-  a.span = (uint32_t)l.span;
+  a.span = (uint32_t)groups.span;
   a.tokens = (uint32_t)s->tokens;
   a.heads = (uint32_t)s->heads;
   a.most_tiles = (uint32_t)l.tiles;
   a.pairs = (uint32_t)l.pairs;
-  a.unpack_blocks = (uint32_t)(l.span / kUnpackRows);
+  a.unpack_blocks = (uint32_t)(groups.span / kUnpackRows);
   a.by_heads = divider(a.heads);
   a.scale = s->scale * kLog2e;
   // sums of weights up to 2^far over all rows, times latents below 2^23, stay below 2^126
@@ -1196,8 +1209,22 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.columns = columns_of(a.heads, q_ld, head_ld, s->tokens);
   CUtensorMap qmap, kmap, vmap;
   if (!query_map(&qmap, s->q, a.heads, s->tokens, q_ld * 2, head_ld * 2, a.columns) ||
-      !value_map(&kmap, a.values, cache->sequences * l.span, kSpan / 2, 1) ||
-      !value_map(&vmap, a.values, cache->sequences * l.span, 64, 2))
+      !value_map(&kmap, a.values, groups.each * groups.span, kSpan / 2, 1) ||
+      !value_map(&vmap, a.values, groups.each * groups.span, 64, 2))
     return KVO_ECUDA;
-  return launch_chunk(a, qmap, kmap, vmap, on) == cudaSuccess ? KVO_OK : KVO_ECUDA;
+  for (int64_t first = 0; first < cache->sequences; first += groups.each) {
+    kvo_cache part = *cache;
+    part.sequences = (int32_t)std::min(groups.each, cache->sequences - first);
+    if (part.table) {
+      part.table += first * part.table_ld;
+    } else {                                             // sequence s is block s
+      part.rows = static_cast<uint8_t*>(part.rows) + first * part.block_rows * KVO_ROW_BYTES;
+      part.blocks -= first;
+    }
+    a.cache = cache_view(part);
+    a.starts = s->starts + first;
+    a.lens = s->lens + first;
+    if (launch_chunk(a, qmap, kmap, vmap, on) != cudaSuccess) return KVO_ECUDA;
+  }
+  return KVO_OK;
 }

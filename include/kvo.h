@@ -732,8 +732,8 @@ typedef struct kvo_chunk_query {
 kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, const kvo_chunk_query* query, void* stream);
 
 /* kvo_attend_chunk_work_bytes - the scratch bytes a kvo_attend_chunk of
- * `tokens` tokens in all needs on the current device; -1 for arguments it
- * would refuse. */
+ * `tokens` tokens in all needs on the current device, a little over 4 GiB at
+ * most; -1 for arguments it would refuse. */
 int64_t kvo_attend_chunk_work_bytes(int64_t tokens, int32_t sequences, int32_t heads, int64_t rows);
 
 /*

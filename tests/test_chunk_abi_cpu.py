@@ -155,6 +155,20 @@ def test_work_bytes(kvo, ctx):
             assert run(ctx, K.lib().kvo_attend_chunk, cache(K), s) == K.KVO_EINVAL
 
 
+def test_work_bytes_are_bounded(kvo):
+    """However many sequences there are and however long the longest may be."""
+    K = kvo
+    for tokens in (4, 64, 1_024, 4_096, 65_535):
+        for sequences in (1, 3, 64, 256, 512, 65_535):
+            for heads in (1, 16, 128):
+                for rows in (1, 1_000, 131_072, 3_728_270, 10_000_000, 2 ** 31 - 256):
+                    need = K.kvo_attend_chunk_work_bytes(tokens, sequences, heads, rows)
+                    # 4 GiB of values, a factor a row, 76 pairs' parts of 128 columns, the plan
+                    assert 0 <= need <= 2 ** 32 * (1 + 4 / 1152) + 2 ** 26, (tokens, sequences, heads, rows, need)
+    # and no smaller than the rows need where these fit
+    assert K.kvo_attend_chunk_work_bytes(1_024, 64, 16, 16_384) >= 64 * 16_384 * 1152
+
+
 def test_binding_refuses_wrong_tensors(kvo):
     K = kvo
     c = ctypes.create_string_buffer(8192)

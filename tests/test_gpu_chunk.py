@@ -1201,3 +1201,53 @@ def test_chunk_idle_sequences(kvo, ctx, kind, counts):
     got = d.weights(ctx, lse)
     assert ctx.sync() == kvo.KVO_OK
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(got, weights)
+
+
+@pytest.mark.parametrize("table", [True, False])
+@pytest.mark.parametrize("counts", [[4] * 20, [0] * 13 + [70] + [0] * 6, [70] + [0] * 18 + [33], [1, 40, 7, 0, 300] * 4])
+def test_chunk_sequences_in_groups(kvo, ctx, counts, table):
+    """More rows than the scratch takes at once: some sequences after the others, behind a table and without."""
+    rng = np.random.default_rng([122, sum(counts)])
+    rows, heads = 250_000, 128
+    lens = [n + (37 * s) % 500 for s, n in enumerate(counts)]
+    c = Chunk(kvo, rng, counts, lens, heads, 16, first=1, after=2)
+    need = kvo.kvo_attend_chunk_work_bytes(c.tokens, c.n, heads, rows)
+    assert 2 ** 31 < need < 2 ** 32 * 1.01 < c.n * rows * 1152
+    if table:
+        wide = np.full((c.n, rows // 16), -1, np.int32)
+        wide[:, :c.table.shape[1]] = c.table
+        cache = kvo.Cache(rows=dev(c.raw), block_rows=16, table=dev(wide))
+    else:
+        store = torch.zeros(c.n, rows, 656, dtype=torch.uint8, device="cuda")
+        for s, n in enumerate(lens):
+            at = [O.row_of(c.table, c.total, 16, c.n, s, p) for p in range(n)]
+            store[s, :n] = dev(c.raw[at])
+        cache = kvo.Cache(rows=store.view(-1, 656), block_rows=rows)
+    out = torch.full((c.tokens, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.tokens, heads), 7.0, device="cuda")
+    ctx.attend_chunk(cache, c.q, c.dev_starts, c.dev_lens, SCALE, rows, out=out, lse=lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    for x in (out, lse):
+        assert (x[0] == 7).all() and (x[-2:] == 7).all()
+    again = ctx.attend_chunk(cache, c.q, c.dev_starts, c.dev_lens, SCALE, rows)
+    assert torch.equal(again[0][1:-2], out[1:-2]) and torch.equal(again[1][1:-2], lse[1:-2])
+    torch.cuda.empty_cache()
+
+
+def test_chunk_bad_starts_in_groups(kvo, ctx):
+    rng = np.random.default_rng(123)
+    c = Chunk(kvo, rng, [20] * 20, [100 + s for s in range(20)], 128)
+    wide_table = np.full((20, 250_000 // 16), -1, np.int32)
+    wide_table[:, :c.table.shape[1]] = c.table
+    cache = kvo.Cache(rows=dev(c.raw), block_rows=16, table=dev(wide_table))
+    good = c.starts
+    for at, to in ((20, 401), (0, -1), (10, 390), (13, 2 ** 31 - 1), (7, -2 ** 31)):
+        starts = good.copy()
+        starts[at] = to
+        wide = torch.full((402, 128, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((402, 128), 7.0, device="cuda")
+        ctx.attend_chunk(cache, c.q, dev(starts, torch.int32), c.dev_lens, SCALE, 250_000, out=wide[1:401], lse=lse[1:401])
+        assert ctx.sync() == kvo.KVO_ERANGE, starts
+        for x in (wide, lse):
+            assert (x[0] == 7).all() and (x[401] == 7).all()

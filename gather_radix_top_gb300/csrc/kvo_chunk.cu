@@ -29,14 +29,17 @@
 // maximum.
 //
 // Tiles of columns times tiles of positions, end to end, are shared out evenly
-// over the pairs.  Where a share begins or ends inside a tile of columns, the
-// parts are joined by their log-sum-exps in a last launch.
+// over the pairs, or over rows of up to four pairs that take as many tiles of
+// columns and go over the same positions at the same time.  Where a share begins
+// or ends inside a tile of columns, the parts are joined by their log-sum-exps in
+// a last launch.
 //
-// Measured: 512 tokens of 64 heads over 50,023 positions 2.07-2.13 ms (1.67-1.72
-// PFLOP/s; 2.21 ms back to back, at the power limit), 2,048 of 128 heads over
-// 16,384 5.34 ms, a prompt of 4,096 tokens and 16 heads alone 245 us (its tiles of
+// Measured: 512 tokens of 64 heads over 50,023 positions 2.07-2.14 ms (1.66-1.72
+// PFLOP/s; 2.23 ms back to back, at the power limit), 2,048 of 128 heads over
+// 16,384 5.35-5.4 ms, a prompt of 4,096 tokens and 16 heads alone 247 us (its tiles of
 // columns meet 8.5 tiles of positions on average, and beginning and ending one
-// takes the time of two).  A tile of 256 positions is 68 MMAs of 64 clocks, 4,352,
+// takes the time of two), 16 sequences of 8,192 rows with 4,096 columns each 850
+// us (1.37 PFLOP/s).  A tile of 256 positions is 68 MMAs of 64 clocks, 4,352,
 // and keeps shared memory busy for 6,300 wavefronts of 128 bytes: 3,250 of the
 // MMAs' operands, 2,180 of the copies, 900 of the workers.  That is the bound.
 // Steps, ms for the first case: rows dequantised for 64 columns at a time 7.17,
@@ -74,16 +77,18 @@ constexpr uint32_t kSlotBytes = 16384, kSlots = 6;
 constexpr uint32_t kChunkSmem = 1024 + kQueryBytes + 3 * kHalfBytes + kSlots * kSlotBytes;
 constexpr uint32_t kValueBytes = KVO_DEQUANT_VALUES * 2;
 static_assert(9 % kLoaders == 0 && kSlots % kLoaders == 0, "even shares of the queries, and a warp its own slots");
+constexpr uint32_t kMostAbreast = 4;
 constexpr float kRoom = 32.0f;                           // of a reference above the first tile's maximum, in powers of two
 
-// One tile of columns, as the plan lists it.
+// One tile of columns, as the plan lists it.  `abreast` tiles are a row of the
+// plan, one for each of as many pairs next to each other.
 struct __align__(16) PlanTile {
-  uint64_t units;            // work of all tiles before it: their tiles of positions and kTileCost each
+  uint64_t units;            // work of all rows before it: their longest's tiles of positions and kTileCost each
   int32_t seq;
   uint32_t index;            // of its sequence's tiles
   uint32_t first, tokens;    // its sequence's tokens
   int32_t before;            // token i sees the first before + i positions
-  uint32_t spans;            // its tiles of positions
+  uint16_t spans, longest;   // its tiles of positions; the longest of its row
 };
 
 // A tile that ends of shares cut, as the join takes it: of share g - 1 the part
@@ -103,12 +108,13 @@ struct ChunkArgs {
   uint8_t* values;           // [sequences][span][576] bf16, of the group in turn
   float* off;                // [sequences][span]: 0, or -inf where there is no row
   PlanTile* plan;            // [tiles + 1]: the last one's units are all of them
-  Cut* cuts;                 // [pairs], from share 1 on
+  Cut* cuts;                 // [pairs], `abreast` for a share, from share 1 on
   uint8_t* again;            // [most_tiles] whole tiles, [2 * pairs] parts that need another pass
   float* part;               // [2 * pairs][128][512]
   float* part_lse;           // [2 * pairs][128], base 2
   uint32_t* status;
-  uint32_t rows, span, tokens, heads, most_tiles, pairs;
+  uint32_t rows, span, tokens, heads, most_tiles;
+  uint32_t pairs, abreast;   // pairs: a multiple of abreast
   uint32_t unpack_blocks;    // of a sequence
   Divider by_heads;
   Columns columns;
@@ -118,20 +124,20 @@ struct ChunkArgs {
 };
 
 // ---------------------------------------------------------------- the shares
-// Pair g's share of the work: [from(g), from(g + 1)).
+// The share of pairs g * abreast and those behind it: [from(g), from(g + 1)).
 struct Shares {
   uint64_t units, each;
-  uint32_t pairs, rest;           // the first `rest` shares have one more than `each`
+  uint32_t count, rest;              // the first `rest` shares have one more than `each`
   __device__ __forceinline__ Shares(const ChunkArgs& a) {
     units = __ldcg(&a.plan[a.most_tiles + 1].units);
-    pairs = (uint32_t)min((uint64_t)a.pairs, max(units / 2, (uint64_t)1));
-    each = units / pairs;
-    rest = (uint32_t)(units - each * pairs);
+    count = (uint32_t)min((uint64_t)(a.pairs / a.abreast), max(units / 2, (uint64_t)1));
+    each = units / count;
+    rest = (uint32_t)(units - each * count);
   }
-  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < pairs ? g * each + min(g, rest) : units; }
+  __device__ __forceinline__ uint64_t from(uint32_t g) const { return g < count ? g * each + min(g, rest) : units; }
 };
 
-// The tile that unit u lies in; a whole warp.
+// The first tile of the row that unit u lies in; a whole warp.
 __device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
   uint32_t lo = 0, hi = __ldcg(&a.plan[a.most_tiles + 1].index);   // in [lo, hi)
   const uint32_t lane = threadIdx.x & 31;
@@ -142,13 +148,17 @@ __device__ __forceinline__ uint32_t tile_of(const ChunkArgs& a, uint64_t u) {
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
   }
-  return lo;
+  return lo / a.abreast * a.abreast;
 }
 
+__device__ __forceinline__ PlanTile plan_tile(uint4 x, uint4 y) {
+  return PlanTile{(uint64_t)x.y << 32 | x.x, (int32_t)x.z,           x.w, y.x, y.y, (int32_t)y.z,
+                  (uint16_t)(y.w & 0xffffu), (uint16_t)(y.w >> 16)};
+}
 __device__ __forceinline__ PlanTile plan_tile(const ChunkArgs& a, uint32_t i) {
   const uint4* const from = reinterpret_cast<const uint4*>(a.plan + i);
   const uint4 x = __ldcg(from), y = __ldcg(from + 1);
-  return PlanTile{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
+  return plan_tile(x, y);
 }
 
 // ------------------------------------------------------------ rows and plan
@@ -209,12 +219,12 @@ __device__ void make_plan(const ChunkArgs& a) {
     upto[tid] = incl;
     __syncthreads();
     // (starts that go back could list more tiles than there is room for)
-    const uint32_t all = min(upto[kUnpackThreads - 1], a.most_tiles - tiles);
+    const uint32_t real = min(upto[kUnpackThreads - 1], (a.most_tiles - tiles) / a.abreast * a.abreast);
+    const uint32_t all = (real + a.abreast - 1) / a.abreast * a.abreast;   // the last row's rest: tiles of nothing
     for (uint32_t j0 = 0; j0 < all; j0 += kUnpackThreads) {
       const uint32_t j = j0 + tid;
       PlanTile t = {};
-      uint64_t n = 0;
-      if (j < all) {
+      if (j < real) {
         uint32_t lo = 0, hi = kUnpackThreads - 1;        // the first with upto > j
         while (lo < hi) {
           const uint32_t mid = (lo + hi) / 2;
@@ -225,10 +235,13 @@ __device__ void make_plan(const ChunkArgs& a) {
         t.first = first[lo];
         t.tokens = count[lo];
         t.before = min(max(a.lens[t.seq], 0), INT32_MAX - 1) - (int32_t)t.tokens + 1;
-        t.spans = max((visible(a, t.before, last_token(a, t.index, t.tokens)) + kSpan - 1) / kSpan, 1u);
-        n = t.spans + kTileCost;
+        t.spans = (uint16_t)max((visible(a, t.before, last_token(a, t.index, t.tokens)) + kSpan - 1) / kSpan, 1u);
       }
-      uint64_t sum = n;
+      uint32_t longest = t.spans;
+      for (uint32_t d = 1; d < a.abreast; d <<= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+      t.longest = (uint16_t)longest;
+      const uint64_t n = j < all ? longest + kTileCost : 0;
+      uint64_t sum = tid % a.abreast == 0 ? n : 0;
 #pragma unroll
       for (uint32_t d = 1; d < 32; d <<= 1) {
         const uint64_t o = __shfl_up_sync(0xffffffffu, sum, d);
@@ -264,18 +277,18 @@ __device__ void make_plan(const ChunkArgs& a) {
   __threadfence_block();
   __syncthreads();
   const Shares shares(a);
-  for (uint32_t g = 1 + warp; g < shares.pairs; g += kUnpackThreads / 32) {
+  for (uint32_t i = a.abreast + warp; i < shares.count * a.abreast; i += kUnpackThreads / 32) {
+    const uint32_t g = i / a.abreast;
     const uint64_t at = shares.from(g);
-    const uint32_t tile = tile_of(a, at);
     Cut cut;
-    cut.tile = plan_tile(a, tile);
+    cut.tile = plan_tile(a, tile_of(a, at) + i % a.abreast);
     const uint64_t from = cut.tile.units, end = from + cut.tile.spans;
     cut.last = 0;
     if (at > from && at < end && shares.from(g - 1) <= from) {
       cut.last = g;
-      while (cut.last + 1 < shares.pairs && shares.from(cut.last + 1) < end) ++cut.last;
+      while (cut.last + 1 < shares.count && shares.from(cut.last + 1) < end) ++cut.last;
     }
-    if (lane == 0) a.cuts[g] = cut;
+    if (lane == 0) a.cuts[i] = cut;
   }
 }
 
@@ -348,17 +361,17 @@ struct Segment {
   }
 };
 
-// f(segment) for every segment of a pair's share, in order, in every warp.
-// tile_at(i): tile i of the plan.
+// f(segment) for every segment of a pair's share, in order, in every warp, from
+// tile `tile` on.  tile_at(i): tile i of the plan.
 template <typename T, typename F>
 __device__ __forceinline__ void for_segments(const ChunkArgs& a, uint64_t begin, uint64_t end, uint32_t tile, T tile_at, F f) {
-  for (uint64_t u = begin; u < end; ++tile) {
+  for (uint64_t u = begin; u < end; tile += a.abreast) {
     Segment g;
     g.tile = tile_at(tile);
-    const uint64_t past = g.tile.units + g.tile.spans + kTileCost;
+    const uint64_t past = g.tile.units + g.tile.longest + kTileCost;
     g.number = tile;
-    g.from = min((uint32_t)(u - g.tile.units), g.tile.spans);
-    g.to = min((uint32_t)(min(past, end) - g.tile.units), g.tile.spans);
+    g.from = min((uint32_t)(u - g.tile.units), (uint32_t)g.tile.spans);
+    g.to = min((uint32_t)(min(past, end) - g.tile.units), (uint32_t)g.tile.spans);
     g.whole = g.to - g.from == g.tile.spans;
     u = past;
     if (g.from < g.to && !f(g)) return;
@@ -453,8 +466,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return wait_or_give_up(bar, parity, &sh.gave_up, a.wait_clocks);
   };
   const Shares shares(a);
-  const uint64_t begin = shares.from(pair), end = pair < shares.pairs ? shares.from(pair + 1) : begin;
-  const uint32_t tile0 = begin < end ? tile_of(a, begin) : 0;
+  const uint32_t share = pair / a.abreast;
+  const uint64_t begin = shares.from(share), end = share < shares.count ? shares.from(share + 1) : begin;
+  const uint32_t tile0 = begin < end ? tile_of(a, begin) + pair % a.abreast : 0;
   const uint32_t box = a.columns.wide * a.columns.deep * 128;
 
   // The roles' counters run on over segments and passes.
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const float* const off = a.off + (int64_t)g.tile.seq * a.span;
     if (warp == 0 && !max_only) {                        // the next segment's tile, there once the sums have been traded
       if (lane < 2)
-        copy16_async(smem_u32(&sh.upcoming[full_n & 1]) + 16 * lane, reinterpret_cast<const uint4*>(a.plan + g.number + 1) + lane,
+        copy16_async(smem_u32(&sh.upcoming[full_n & 1]) + 16 * lane, reinterpret_cast<const uint4*>(a.plan + g.number + a.abreast) + lane,
                      true);
       copy_async_commit();
     }
@@ -799,7 +813,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const float ref = sh.ref[quarter][lane];
     if (warp == 0) copy_async_wait<0>();
     ok = ok && trade(kSum, full_n, &sh.sums[rank], sizeof(Sums));
-    upcoming_number = g.number + 1;
+    upcoming_number = g.number + a.abreast;
     ++full_n;
     if (!__all_sync(0xffffffffu, ok)) return false;
     const bool again = __any_sync(0xffffffffu, ((volatile uint32_t*)sh.sums[lane >> 4].again)[lane & 15] != 0);
@@ -908,8 +922,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t next_number = UINT32_MAX;
   auto ahead = [&](uint32_t i) {
     const PlanTile t = i == next_number ? next : plan_tile(a, i);
-    next = plan_tile(a, i + 1);
-    next_number = i + 1;
+    next = plan_tile(a, i + a.abreast);
+    next_number = i + a.abreast;
     return t;
   };
   if (warp < kWorkers) {
@@ -989,24 +1003,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == kMma) pair_tmem_free(tmem, 512);
 }
 
-// Joins the parts of a cut tile by their log-sum-exps: blocks (g - 1, ..) those
-// that share g is the first to cut, four columns of 128 threads each.
+// Joins the parts of a cut tile by their log-sum-exps: blocks ((g - 1) * abreast
+// + k, ..) those of the k-th tile that share g is the first to cut, four columns of
+// 128 threads each.
 constexpr uint32_t kJoinColumns = 4, kMostParts = 96;
 
 __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __grid_constant__ ChunkArgs a) {
-  const uint32_t g = blockIdx.x + 1, d = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t g = blockIdx.x / a.abreast + 1, beside = blockIdx.x % a.abreast, d = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t column = blockIdx.y * kJoinColumns + (threadIdx.x >> 7);
   wait_previous_grid();
-  if (g >= Shares(a).pairs) return;
-  const uint32_t last = __ldcg(&a.cuts[g].last);
+  if (g >= Shares(a).count) return;
+  const uint32_t last = __ldcg(&a.cuts[g * a.abreast + beside].last);
   if (last == 0) return;
-  const uint4 *const cut = reinterpret_cast<const uint4*>(a.cuts + g), x = __ldcg(cut), y = __ldcg(cut + 1);
-  const PlanTile t{(uint64_t)x.y << 32 | x.x, (int32_t)x.z, x.w, y.x, y.y, (int32_t)y.z, y.w};
+  const uint4 *const cut = reinterpret_cast<const uint4*>(a.cuts + g * a.abreast + beside), x = __ldcg(cut), y = __ldcg(cut + 1);
+  const PlanTile t = plan_tile(x, y);
   uint32_t where;
   const uint32_t token = column_at(a, t, 2 * t.index + column / kColumns, column % kColumns, &where);
   if (token >= t.tokens) return;                         // (the same for a column's warps)
   const uint32_t parts = last - g + 2;
-  auto row_of = [&](uint32_t i) { return (2 * (g - 1 + i) + (i == 0)) * kTileColumns + column; };
+  auto row_of = [&](uint32_t i) { return (2 * ((g - 1 + i) * a.abreast + beside) + (i == 0)) * kTileColumns + column; };
   // lane l has the weights of parts l, l + 32 and l + 64
   float l[kMostParts / 32], top = -INFINITY;
 #pragma unroll
@@ -1044,6 +1059,7 @@ __global__ void __launch_bounds__(128 * kJoinColumns) join_parts_kernel(const __
 // one group after the other, however many there are and however long `rows`
 // says they may be.  No group: a single one's do not fit.
 constexpr int64_t kMostValueBytes = (int64_t)4 << 30;
+static_assert(kMostValueBytes / kValueBytes / kSpan < 1 << 16, "PlanTile counts tiles of positions in 16 bits");
 
 struct Groups {
   int64_t span, count, each;         // positions of a sequence; groups; sequences of a group
@@ -1073,6 +1089,19 @@ bool many_columns(int64_t tokens, int64_t sequences, uint32_t heads, int64_t row
   return gain > 0 && (double)busy * (double)seen * (double)gain > 2.1e6 * (double)groups.count;
 }
 
+// Pairs that go over the same positions side by side, as the tiles of columns of
+// a sequence allow: the first to take a piece brings it into L2 for all of them.
+// One, two and four, us: 8 sequences of 131,072 rows with 1,024 columns each 2,255,
+// 1,944 and 1,870; 64 of 8,192 with 1,024 1,188, 1,032 and 986; 32 of 65,536 with 256
+// 1,673, 1,510 and 1,514; one of 100,000 with 32,768 4,666, 4,629 and 4,560; a prompt's
+// 4,096 tokens of 16 heads 248, 248 and 247.  A row's pairs wait for the longest of
+// its tiles, so no more than a sequence of average size fills.
+uint32_t abreast_of(int64_t tokens, int64_t sequences, uint32_t heads) {
+  const int64_t busy = sequences < tokens ? sequences : tokens, tiles = tokens * heads / (busy * kTileColumns);
+  return tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
+}
+static_assert(kMostAbreast >= 4 && kUnpackThreads % kMostAbreast == 0);
+
 struct Layout {              // of the scratch
   int64_t tiles, pairs;
   int64_t values, off, plan, cuts, again, part, part_lse, bytes;
@@ -1087,7 +1116,7 @@ Layout layout_of(int64_t tokens, int64_t sequences, uint32_t heads, int64_t rows
   const int64_t deep = heads < kColumns ? kColumns / heads : 1, across = heads > kColumns ? 2 : 1;
   const int64_t halves = (tokens + busy * (deep - 1)) / deep * across;
   const int64_t flat = (tokens * heads + busy * (kColumns - 1)) / kColumns;
-  l.tiles = ((halves > flat ? halves : flat) + busy + 1) / 2;
+  l.tiles = ((halves > flat ? halves : flat) + busy + 1) / 2 + (sequences + kUnpackThreads - 1) / kUnpackThreads * (kMostAbreast - 1);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -1135,13 +1164,15 @@ cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& qmap, const CUtensorMap
     room[dev & 63] = n;
   }
   if (a.pairs > (uint32_t)room[dev & 63]) a.pairs = (uint32_t)room[dev & 63];
+  if (a.pairs < a.abreast) a.abreast = 1;
+  a.pairs -= a.pairs % a.abreast;
   e = launch_early(unpack_kernel, dim3(1 + a.unpack_blocks * a.cache.sequences), kUnpackThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   lc.gridDim = dim3(2 * a.pairs);
   lc.numAttrs = 2;
   e = cudaLaunchKernelEx(&lc, chunk_kernel, a, qmap, kmap, vmap);
-  if (e != cudaSuccess || a.pairs < 2) return e;
-  return launch_early(join_parts_kernel, dim3(a.pairs - 1, kTileColumns / kJoinColumns), 128 * kJoinColumns, 0,
+  if (e != cudaSuccess || a.pairs <= a.abreast) return e;
+  return launch_early(join_parts_kernel, dim3(a.pairs - a.abreast, kTileColumns / kJoinColumns), 128 * kJoinColumns, 0,
                       stream, a);
 }
 
@@ -1197,6 +1228,7 @@ extern "C" kvo_status kvo_attend_chunk(kvo_ctx* ctx, const kvo_cache* cache, con
   a.heads = (uint32_t)s->heads;
   a.most_tiles = (uint32_t)l.tiles;
   a.pairs = (uint32_t)l.pairs;
+  a.abreast = abreast_of(s->tokens, cache->sequences, (uint32_t)s->heads);
   a.unpack_blocks = (uint32_t)(groups.span / kUnpackRows);
   a.by_heads = divider(a.heads);
   a.scale = s->scale * kLog2e;

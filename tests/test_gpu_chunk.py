@@ -1251,3 +1251,67 @@ def test_chunk_bad_starts_in_groups(kvo, ctx):
         assert ctx.sync() == kvo.KVO_ERANGE, starts
         for x in (wide, lse):
             assert (x[0] == 7).all() and (x[401] == 7).all()
+
+
+@pytest.mark.parametrize("counts,heads,rows", [
+    ([10, 10], 20, 60_000), ([17, 12, 9], 20, 60_000),                       # one tile of columns after the other
+    ([5, 4, 3, 6], 64, 60_000), ([4, 0, 8, 4, 1], 64, 60_000),              # two side by side, of one sequence and of two
+    ([40], 128, 60_000), ([9, 31, 0, 17, 2], 64, 60_000),                   # four
+    ([1, 70, 1, 1, 1], 128, 60_000), ([1] * 9 + [200] + [1] * 9, 64, 60_000),
+    ([(3 * s) % 11 for s in range(300)], 64, 12_000), ([130] + [1] * 290, 100, 12_000)])
+def test_chunk_tiles_side_by_side(kvo, ctx, counts, heads, rows):
+    """Sequences of very unequal lengths and numbers of tokens, more of them than are listed at a time."""
+    rng = np.random.default_rng([124, sum(counts), heads])
+    lens = [(1 + 97 * s * s) % 900 if n < 2 else n + (61 * s) % 1100 for s, n in enumerate(counts)]
+    if len(counts) > 20:
+        lens = [n + (5 * s) % 40 for s, n in enumerate(counts)]
+    c = Many(kvo, rng, counts, lens, heads, first=1, after=1)
+    out = torch.full((c.tokens, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.tokens, heads), 7.0, device="cuda")
+    c.attend(ctx, rows, out=out, lse=lse)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    for x in (out, lse):
+        assert (x[0] == 7).all() and (x[-1] == 7).all()
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "one", "steps"])
+@pytest.mark.parametrize("tokens,heads", [(10, 20), (14, 20), (5, 64), (90, 64)])
+def test_many_columns_wide_logits(kvo, ctx, order, tokens, heads):
+    """Logits far above the first tile's: tiles done again, alone and beside others that are not."""
+    rng = np.random.default_rng([125, tokens, len(order)])
+    n = 1300
+    raw = random_rows(rng, n)
+    for j in range(n):
+        x = np.zeros(64)
+        x[:8] = {"rising": j / 20, "falling": (n - j) / 20, "one": 60.0 * (j == n * 3 // 5), "steps": 9.0 * (j // 129)}[order]
+        raw[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+    q = rng.standard_normal((tokens, heads, 576))
+    q[..., 512:520] = np.linspace(-1, 4, heads)[None, :, None]
+    c = Many(kvo, rng, [tokens], [n], heads, 0, scale=0.5, q=dev(q, torch.bfloat16), raw=raw)
+    out, lse = c.attend(ctx, rows=240_000)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("counts,lens,heads", [([10], [1000], 20), ([13, 12], [1000, 300], 20), ([5] * 9, [3100 - 300 * s for s in range(9)], 64),
+                                               ([200], [777], 3), ([40] * 5, [900] * 5, 64)])
+def test_many_columns_same_bits(kvo, ctx, counts, lens, heads):
+    """One call behind the other, and with waits that run out between them."""
+    rng = np.random.default_rng([126, heads, len(counts)])
+    c = Many(kvo, rng, counts, lens, heads)
+    out, lse = c.attend(ctx, rows=240_000)
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    for _ in range(20):
+        o, l = c.attend(ctx, rows=240_000)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    own = kvo.Context(1, 64, 64)
+    for clocks in WAITS:
+        own.set_wait_clocks(clocks)
+        c.attend(own, rows=240_000)
+        assert own.sync() in ((kvo.KVO_ETIMEDOUT,) if clocks == 0 else (kvo.KVO_OK, kvo.KVO_ETIMEDOUT))
+        own.set_wait_clocks()
+        o, l = c.attend(own, rows=240_000)
+        assert own.sync() == kvo.KVO_OK and torch.equal(o, out) and torch.equal(l, lse)
+    own.close()

@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
       }
       const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]) - lost, now = total + add;
-      lost = (now - total) - add;
+      lost = fabsf(now) < INFINITY ? (now - total) - add : 0.0f;   // (an infinite sum stays one)
       total = now;
       ++t;
       __syncwarp();

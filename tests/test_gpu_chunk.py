@@ -1254,7 +1254,7 @@ def test_chunk_bad_starts_in_groups(kvo, ctx):
 
 
 @pytest.mark.parametrize("counts,heads,rows", [
-    ([10, 10], 20, 60_000), ([17, 12, 9], 20, 60_000),                       # one tile of columns after the other
+    ([4], 64, 240_000), ([256], 1, 240_000), ([10, 10], 20, 60_000), ([17, 12, 9], 20, 60_000),   # one tile of columns after the other
     ([5, 4, 3, 6], 64, 60_000), ([4, 0, 8, 4, 1], 64, 60_000),              # two side by side, of one sequence and of two
     ([40], 128, 60_000), ([9, 31, 0, 17, 2], 64, 60_000),                   # four
     ([1, 70, 1, 1, 1], 128, 60_000), ([1] * 9 + [200] + [1] * 9, 64, 60_000),
@@ -1315,3 +1315,23 @@ def test_many_columns_same_bits(kvo, ctx, counts, lens, heads):
         o, l = c.attend(own, rows=240_000)
         assert own.sync() == kvo.KVO_OK and torch.equal(o, out) and torch.equal(l, lse)
     own.close()
+
+
+@pytest.mark.parametrize("tokens,n", [(3, 300), (300, 300), (90, 5000)])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_weights_past_the_largest_number(kvo, ctx, tokens, n, heads):
+    """Log-sum-exps far below the logits: a weight beyond fp32 is infinite, however many tiles come after it; not NaN."""
+    rng = np.random.default_rng([127, tokens, heads])
+    raw = random_rows(rng, n, scale=(1e-4, 1e-3))
+    c = Chunk(kvo, rng, [tokens], [n], heads, 0, raw=raw, scale=0.01)
+    lse = c.lse()
+    lse[: max(1, tokens // 3)] = -500.0                        # one after the other: all of it, and the first tiles' alone
+    carry = dev(rng.exponential(1.0, (1, n)), torch.float32)
+    got = c.weights(ctx, lse, carry=carry)
+    assert ctx.sync() == kvo.KVO_OK
+    assert torch.isinf(got[0, : n - tokens + 1]).all() and (got > 0).all()
+    # token i sees the first n - tokens + 1 + i positions: those that only later tokens see get the later ones' weights
+    few = c.weights(ctx, torch.where(lse == -500.0, -float("inf"), lse), carry=carry)
+    behind = n - tokens + max(1, tokens // 3)
+    assert torch.isinf(got[0, :behind]).all()
+    assert torch.equal(got[0, behind:], few[0, behind:]) and torch.isfinite(few).all()

@@ -46,12 +46,17 @@ __device__ __forceinline__ void dequant4(uint32_t bytes, uint16_t scale, float b
   hi = bf16_pair(fma_low(b, scale, bias), fma_high(b, scale, bias));
 }
 
-// x = x * scale + (a, b), and sums of two, as one instruction each; the largest of three.
+// x = x * scale + (a, b), products and sums of two, as one instruction each; the largest of three.
 __device__ __forceinline__ void fma_two(float& x, float& y, float scale, float a, float b) {
   asm("{\n .reg .b64 v, s, t;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mov.b64 t, {%3, %4};\n"
       " fma.rn.f32x2 v, v, s, t;\n mov.b64 {%0, %1}, v;\n}"
       : "+f"(x), "+f"(y)
       : "f"(scale), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul_two(float& x, float& y, float by) {
+  asm("{\n .reg .b64 v, s;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mul.rn.f32x2 v, v, s;\n mov.b64 {%0, %1}, v;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(by));
 }
 __device__ __forceinline__ void add_two(float& x, float& y, float a, float b) {
   asm("{\n .reg .b64 v, t;\n mov.b64 v, {%0, %1};\n mov.b64 t, {%2, %3};\n add.rn.f32x2 v, v, t;\n mov.b64 {%0, %1}, v;\n}"

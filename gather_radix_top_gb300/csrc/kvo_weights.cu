@@ -80,8 +80,7 @@ struct WeightArgs {
   uint32_t rows, tokens, heads, window, pairs;
   Divider by_heads;
   Columns columns;           // of a CTA's half of a tile
-  float scale;               // times log2(e)
-  float keep;
+  float scale, keep;
   int64_t wait_clocks;
 };
 
@@ -99,7 +98,7 @@ struct WeightShared {
 // A worker warp's columns, where they are too many to pass from lane to lane.
 template <uint32_t kMine>
 struct ColumnShared {
-  alignas(16) float lse[kWorkers][kMine];    // base 2
+  alignas(16) float lse[kWorkers][kMine];
   alignas(16) int32_t seen[kWorkers][kMine]; // the positions it sees
 };
 template <>
@@ -475,10 +474,10 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     auto add_tile = [&](uint32_t mine) -> bool {
       const uint32_t buf = t % kAhead;
       if (lse == -INFINITY) seen = 0;                      // a column that weighs nothing
-      const float lse2 = seen ? lse * kLog2e : 0.0f;
+      const float mine_lse = seen ? lse : 0.0f;
       if constexpr (kMine > 16) {
         if (lane < kMine) {
-          sc.lse[warp][lane] = lse2;
+          sc.lse[warp][lane] = mine_lse;
           sc.seen[warp][lane] = seen;
         }
       }
@@ -487,8 +486,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         if constexpr (kMine > 16)
           return *reinterpret_cast<const float4*>(&sc.lse[warp][c]);
         else
-          return make_float4(__shfl_sync(~0u, lse2, c), __shfl_sync(~0u, lse2, c + 1), __shfl_sync(~0u, lse2, c + 2),
-                             __shfl_sync(~0u, lse2, c + 3));
+          return make_float4(__shfl_sync(~0u, mine_lse, c), __shfl_sync(~0u, mine_lse, c + 1), __shfl_sync(~0u, mine_lse, c + 2),
+                             __shfl_sync(~0u, mine_lse, c + 3));
       };
       auto sees = [&](uint32_t c) -> int4 {
         if constexpr (kMine > 16)
@@ -516,8 +515,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll
         for (uint32_t c = 0; c < 16; c += 4) {
           const float4 l = lses(c0 + c);
+          // The difference first, rounded once, then its power: with logits and
+          // log-sum-exps that come times log2(e) already, each of the two is rounded
+          // at their size, not at the difference's.  (Two more products for four.)
           fma_two(x[c], x[c + 1], a.scale, -l.x, -l.y);
           fma_two(x[c + 2], x[c + 3], a.scale, -l.z, -l.w);
+          mul_two(x[c], x[c + 1], kLog2e);
+          mul_two(x[c + 2], x[c + 3], kLog2e);
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) x[c + e] = exp2_approx(x[c + e]);
           if (edge) {
@@ -809,7 +813,7 @@ extern "C" kvo_status kvo_attention_weights(kvo_ctx* ctx, const kvo_cache* cache
   a.window = s->window > KVO_MAX_QUERIES ? 0 : (uint32_t)s->window;
   a.pairs = (uint32_t)device_sms() / 2;
   a.by_heads = divider(a.heads);
-  a.scale = s->scale * kLog2e;
+  a.scale = s->scale;
   a.keep = s->keep;
   a.wait_clocks = wait_clocks;
   // a dimension of one has no next element: its stride says nothing

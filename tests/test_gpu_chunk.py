@@ -1335,3 +1335,39 @@ def test_weights_past_the_largest_number(kvo, ctx, tokens, n, heads):
     behind = n - tokens + max(1, tokens // 3)
     assert torch.isinf(got[0, :behind]).all()
     assert torch.equal(got[0, behind:], few[0, behind:]) and torch.isfinite(few).all()
+
+
+@pytest.mark.parametrize("counts,heads", [([1], 16), ([1, 1, 1], 64), ([40], 20), ([300], 128)])
+@pytest.mark.parametrize("size", [0.0, 1000.0, -20480.0])
+def test_weights_take_the_difference_first(kvo, ctx, counts, heads, size):
+    """Logits and log-sum-exps that are large and nearly equal: a weight is as exact as their difference."""
+    rng = np.random.default_rng([128, sum(counts), heads])
+    lens = [max(n, 700) for n in counts]
+    c = Chunk(kvo, rng, counts, lens, heads, 16, scale=1.0)
+    # z = size * 1 + 1 * f with f in 32nds: every product and the sum are exact in fp32, and so is z - lse
+    f = rng.integers(0, 32, len(c.raw)) / 32
+    c.raw[:, 512:] = 0
+    for j, v in enumerate(f):
+        x = np.zeros(64)
+        x[:2] = 1.0, v
+        c.raw[j, 528:] = np.ascontiguousarray(O.bf16_bits(x)).view(np.uint8)
+    c.cache = kvo.Cache(rows=dev(c.raw), block_rows=16, table=dev(c.table))
+    q = torch.zeros(c.tokens, heads, 576)
+    q[..., 512], q[..., 513] = size, 1.0
+    c.q = dev(q, torch.bfloat16)
+    assert (c.q[..., 512] == size).all()
+    off = rng.integers(0, 64, (c.tokens, heads)) / 8
+    lse = dev(size + off, torch.float32)
+    assert np.array_equal(f64(lse), size + off)
+    got = f64(c.weights(ctx, lse))
+    assert ctx.sync() == kvo.KVO_OK
+    for s in range(c.n):
+        at = [O.row_of(c.table, c.total, 16, c.n, s, p) for p in range(lens[s])]
+        want = np.zeros(c.rows)
+        for t in C.tokens_of(c.starts, s):
+            n = C.seen(c.starts, c.lens, s, t, c.rows)
+            want[:n] += np.exp(f[at[:n]][:, None] - off[t][None, :]).sum(1)
+        # |z - lse| <= 8: its product with log2 e (rounded, by a rounded constant) is off by 2 u of 11.6, 17 u of the
+        # weight; the exponential 16 u, the sums 64 u
+        tol = (17 + 16 + 64) * U * want
+        assert (np.abs(got[s] - want) <= tol).all(), float((np.abs(got[s] - want) / np.maximum(tol, 1e-300)).max())

@@ -728,6 +728,19 @@ def kvo_attend_work_bytes(nq: int, heads: int, positions: int) -> int:
     return int(lib().kvo_attend_work_bytes(nq, heads, positions))
 
 
+def _work(work, need: int, device, stream) -> tuple:
+    """(tensor, address, bytes) of the caller's scratch, or of some that holds `need` bytes."""
+    if need <= 0:
+        return work, None, 0
+    if work is None:
+        work = _empty(need, _T().uint8, device, stream)
+    elif work.dtype is not _T().uint8 or not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work must be a contiguous uint8 CUDA tensor")
+    elif work.device != device:
+        raise ValueError(f"work must be on {device}, as q is, got {work.device}")
+    return work, work.data_ptr(), work.numel()
+
+
 def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None = None, sel=None, sel_block: int = 1,
                out=None, lse=None, work=None, stream=None):
     """q: bfloat16 CUDA [nq, heads, 576]; lens: int32 [nq]; rows: the largest
@@ -753,18 +766,10 @@ def kvo_attend(ctx: int, cache: Cache, q, lens, scale: float, rows: int | None =
     if lse is None:
         lse = _empty((nq, heads), T.float32, q.device, stream)
     L = lib()
-    work_ptr, need = None, L.kvo_attend_work_bytes(nq, heads, positions)
-    if need > 0:
-        if work is None:
-            work = _empty(need, T.uint8, q.device, stream)
-        elif work.dtype is not T.uint8 or not work.is_cuda or not work.is_contiguous():
-            raise ValueError("work must be a contiguous uint8 CUDA tensor")
-        else:
-            need = work.numel()
-        work_ptr = work.data_ptr()
+    work, work_ptr, size = _work(work, L.kvo_attend_work_bytes(nq, heads, positions), q.device, stream)
     s = kvo_attend_query(q_ptr, _cuda(lens, "lens", T.int32, (nq,)), sel_ptr,
                          _flat(out, "out", T.bfloat16, (nq, heads, LATENT_VALUES)),
-                         _flat(lse, "lse", T.float32, (nq, heads)), work_ptr, max(need, 0), q_ld, q_head_ld, sel_ld, rows,
+                         _flat(lse, "lse", T.float32, (nq, heads)), work_ptr, size, q_ld, q_head_ld, sel_ld, rows,
                          picked, sel_block, per_seq, heads, scale)
     _check(L.kvo_attend(ctx, cache.ref, ctypes.addressof(s), _raw_stream(T, q.device, stream)), "kvo_attend")
     return out, lse
@@ -781,17 +786,6 @@ def _tokens(cache: Cache, q, starts, lens) -> tuple:
     # a dimension of one has no next element: its stride says nothing
     return (ptr, tokens, heads, q_ld if tokens > 1 else heads * DEQUANT_VALUES, head_ld if heads > 1 else DEQUANT_VALUES,
             _flat(starts, "starts", T.int32, (cache.sequences + 1,)), _flat(lens, "lens", T.int32, (cache.sequences,)))
-
-
-def _work(work, need: int, device, stream) -> tuple:
-    """(tensor, address, bytes) of the caller's scratch, or of some that holds `need` bytes."""
-    if need <= 0:
-        return work, None, 0
-    if work is None:
-        work = _empty(need, _T().uint8, device, stream)
-    elif work.dtype is not _T().uint8 or not work.is_cuda or not work.is_contiguous():
-        raise ValueError("work must be a contiguous uint8 CUDA tensor")
-    return work, work.data_ptr(), work.numel()
 
 
 def kvo_attend_chunk_work_bytes(tokens: int, sequences: int, heads: int, rows: int) -> int:

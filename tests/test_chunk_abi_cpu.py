@@ -185,6 +185,30 @@ def test_binding_refuses_wrong_tensors(kvo):
             K.kvo_shrink_cache(ctypes.addressof(c), paged, paged, bad, lens, 10)
 
 
+def test_binding_refuses_scratch_of_another_gpu(kvo):
+    """Scratch has to be on the GPU of the queries; no second GPU is needed to see that."""
+    class Scratch:
+        dtype, is_cuda = torch.uint8, True
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return A
+
+        def numel(self):
+            return 512
+
+    here = torch.device("cuda", 0)
+    assert kvo._work(Scratch(0), 512, here, None)[1:] == (A, 512)
+    assert kvo._work(None, 0, here, None) == (None, None, 0)
+    with pytest.raises(ValueError, match="cuda:0"):
+        kvo._work(Scratch(1), 512, here, None)
+
+
 def test_no_copy_is_multicast():
     """Copies go to one CTA each: what they read may be memory that the caller names, of any kind."""
     import glob

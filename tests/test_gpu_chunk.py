@@ -1371,3 +1371,90 @@ def test_weights_take_the_difference_first(kvo, ctx, counts, heads, size):
         # weight; the exponential 16 u, the sums 64 u
         tol = (17 + 16 + 64) * U * want
         assert (np.abs(got[s] - want) <= tol).all(), float((np.abs(got[s] - want) / np.maximum(tol, 1e-300)).max())
+
+
+# ------------------------------------------------------------- the largest calls
+@pytest.mark.parametrize("sequences", [4_096, 65_535])
+def test_as_many_sequences_as_there_may_be(kvo, ctx, sequences):
+    """One token of two heads in each of them, their weights, and a cut to two positions, against 64 bits as a whole."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(sequences)
+    n, heads, br = sequences, 2, 8
+    lens = torch.randint(0, br + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    raw = torch.randint(0, 256, (n * br, 656), generator=g, device="cuda", dtype=torch.uint8)
+    raw.view(torch.int8)[:, :512].clamp_(-127, 127)
+    raw.view(torch.float16)[:, 256:264] = (torch.rand(n * br, 8, generator=g, device="cuda") * 9e-3 + 1e-3).half()
+    raw.view(torch.bfloat16)[:, 264:] = torch.randn(n * br, 64, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(n, generator=g, device="cuda")[:, None].int()
+    q = torch.randn(n, heads, 576, generator=g, device="cuda").bfloat16()
+    cache = kvo.Cache(rows=raw, block_rows=br, table=table)
+    starts = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out, lse = ctx.attend_chunk(cache, q, starts, lens, SCALE, br)
+    mass = ctx.attention_weights(cache, q, starts, lens, lse, SCALE, br)
+    to_rows = torch.zeros(n * 2, 656, dtype=torch.uint8, device="cuda")
+    kept, left, w = ctx.shrink_cache(cache, kvo.Cache(rows=to_rows, block_rows=2), mass, lens, 2, 1, 0)
+    assert ctx.sync() == kvo.KVO_OK
+    rows = raw.view(n, br, 656)[table[:, 0].long()]
+    lat = (rows.view(torch.int8)[..., :512].float().unflatten(-1, (8, 64)) *
+           rows.view(torch.float16)[..., 256:264].float()[..., None]).flatten(-2).bfloat16().double()
+    keys = torch.cat([lat, rows.view(torch.bfloat16)[..., 264:].double()], -1)
+    hidden = torch.arange(br, device="cuda") >= lens[:, None]
+    z = torch.einsum("nhd,nrd->nhr", q.double(), keys) * SCALE
+    size = float(torch.einsum("nhd,nrd->nhr", q.double().abs(), keys.abs()).max()) * SCALE
+    z = z.masked_fill(hidden[:, None], -float("inf"))
+    want_lse = torch.logsumexp(z, 2)
+    live = lens > 0
+    p = torch.where(live[:, None, None], torch.exp(z - want_lse[..., None]), 0.0)
+    want, spread = torch.einsum("nhr,nrd->nhd", p, lat), torch.einsum("nhr,nrd->nhd", p, lat.abs())
+    logit = 2 * U * 576 * size                                  # as at the top of this file
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + spread * (2.0 ** -8 + 2 * logit + 100 * U) + 2.0 ** -80).all()
+    assert torch.isneginf(lse[~live]).all()
+    assert ((lse.double() - want_lse)[live].abs() <= logit + 100 * U + 2 * U * want_lse[live].abs()).all()
+    assert ((mass.double() - p.sum(1)).abs() <= p.sum(1) * (2 * logit + 100 * U + 8 * U * (size + 3)) + 2.0 ** -120).all()
+    assert torch.equal(left, lens.clamp(max=2))
+    order = mass.clone()
+    order[:, 0] = float("inf")
+    order[hidden] = -float("inf")
+    pick = order.sort(dim=1, descending=True, stable=True).indices[:, :2].sort(1).values.int()
+    pick[torch.arange(2, device="cuda") >= left[:, None]] = -1
+    assert torch.equal(kept, pick)
+    there = (kept >= 0)
+    assert torch.equal(w, torch.where(there, mass.gather(1, kept.clamp(min=0).long()), 0.0))
+    moved = rows.gather(1, kept.clamp(min=0).long()[..., None].expand(-1, -1, 656))
+    assert torch.equal(to_rows.view(n, 2, 656)[there], moved[there])
+
+
+def test_chunk_groups_replayed_with_strided_queries(kvo, ctx):
+    """Groups of sequences from a graph on new inputs, queries with heads before tokens, on another stream."""
+    rng = np.random.default_rng(129)
+    counts, rows, heads = [4, 0, 33, 5] * 5, 250_000, 128
+    c = Chunk(kvo, rng, counts, [n + 50 for n in counts], heads, 16)
+    wide = np.full((c.n, rows // 16), -1, np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    cache = kvo.Cache(rows=dev(c.raw), block_rows=16, table=dev(wide))
+    across = torch.empty(heads, c.tokens, 576, dtype=torch.bfloat16, device="cuda")
+    across.copy_(c.q.transpose(0, 1))
+    c.q = across.transpose(0, 1)
+    work = torch.empty(kvo.kvo_attend_chunk_work_bytes(c.tokens, c.n, heads, rows), dtype=torch.uint8, device="cuda")
+    out = torch.empty(c.tokens, heads, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(c.tokens, heads, device="cuda")
+
+    def run():
+        ctx.attend_chunk(cache, c.q, c.dev_starts, c.dev_lens, SCALE, rows, out=out, lse=lse, work=work)
+
+    run()
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    across.copy_(across.roll(1, 1))
+    out.zero_()
+    work.fill_(255)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    assert ctx.sync() == kvo.KVO_OK
+    c.check_attend(out, lse)

@@ -35,8 +35,8 @@
 // a last launch.
 //
 // Measured: 512 tokens of 64 heads over 50,023 positions 2.07-2.14 ms (1.66-1.72
-// PFLOP/s; 2.23 ms back to back, at the power limit), 2,048 of 128 heads over
-// 16,384 5.35-5.4 ms, a prompt of 4,096 tokens and 16 heads alone 247 us (its tiles of
+// PFLOP/s; 2.26 ms back to back, at the power limit), 2,048 of 128 heads over
+// 16,384 5.35-5.54 ms, a prompt of 4,096 tokens and 16 heads alone 246 us (its tiles of
 // columns meet 8.5 tiles of positions on average, and beginning and ending one
 // takes the time of two), 16 sequences of 8,192 rows with 4,096 columns each 850
 // us (1.37 PFLOP/s).  A tile of 256 positions is 68 MMAs of 64 clocks, 4,352,

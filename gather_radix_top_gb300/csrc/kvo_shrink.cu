@@ -8,9 +8,9 @@
 // position.  The second copies rows, keys and factors, a warp for four rows:
 // their 164 pieces of 16 bytes are all asked for before the first is stored.
 //
-// Measured on the GPU: 50,023 positions to 8,192 rows 13.5 us (the selection's
+// Measured on the GPU: 50,023 positions to 8,192 rows 13.6 us (the selection's
 // chain of passes and cluster barriers; the copy 4), 33 uneven sequences of up
-// to 20,011 to 1,021 23 us, 1,048,576 to 524,288 229 us: 147 for the copy (826
+// to 20,011 to 1,021 23 us, 1,048,576 to 524,288 230 us: 147 for the copy (826
 // MB at 5.6 TB/s; every second row of 656 bytes leaves parts of DRAM's bursts
 // unused) and 80 for the selection, whose 16 CTAs issue two instructions a clock
 // in loops over the keys.  With weights read again in every pass, one at a time,
@@ -244,9 +244,11 @@ cudaError_t launch_keep(ShrinkArgs a, uint32_t sequences, cudaStream_t stream) {
   uint32_t C = 1;
   while ((int)C < most && 2 * C * sequences <= (uint32_t)device_sms() && a.rows > C * 4u * kThreads) C *= 2;
   // Three passes of 11 bits for many keys a CTA, four of 8 for few.  Both ways,
-  // us: one sequence of 50,000 13.9 and 13.3, 262,144 (16,384 a CTA) 21.1 and
-  // 22.2, 500,000 30.0 and 32.9; four of 262,144 24.7 and 23.0; 152 of 30,000 62
-  // and 64, of 200,000 193 and 200.
+  // us, to 1,000 rows, weights even in [0, 1) (and log-normal ones): one sequence of
+  // 50,000 14.3 and 13.6 (13.8 and 13.6), of 262,144, 16,384 a CTA, 24.9 and 22.2
+  // (20.9 and 19.1), of 500,000 35.8 and 36.8 (29.9 and 28.2); four of 262,144 25.9
+  // and 25.5 (21.6 and 22.3); 152 of 200,000 252 and 277 (240 and 241); log-normal,
+  // 1,048,576 to half of them 230 and 236.
   const uint32_t chunk = topk_chunk(a.rows, C);
   const bool many = chunk > 24 * 1024;
   const uint32_t bins = many ? KeepSmem<11>::owned(C) : KeepSmem<8>::owned(C);

@@ -694,7 +694,8 @@ int64_t kvo_attend_work_bytes(int64_t nq, int32_t heads, int64_t positions);
  *           fewer than its tokens, the first tokens see none.
  *   rows    the largest lens value: positions at or past it are not looked at.
  * Tokens that belong to no sequence (before starts[0], or at and past the last
- * entry) are not looked at, and their outputs are left as they are.
+ * entry) are not looked at, and their outputs are left as they are; nor are the
+ * rows of a sequence without tokens.
  * ---------------------------------------------------------------------- */
 
 /*
